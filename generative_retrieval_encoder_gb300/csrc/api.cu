@@ -24,6 +24,7 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Per-launch profiler names of the GEMMs, by Variant: the projection, dx~ and dW GEMMs.
@@ -350,6 +351,86 @@ gbla_status begin(const gbla_shape* s, int op, void* ws, size_t ws_bytes, void* 
   return GBLA_OK;
 }
 
+// ------------------------------------------------------ gated linear recurrence
+// Sizes and workspace of glr_forward / glr_backward (their shape needs no heads).
+struct GlrPlan {
+  bool f32;
+  int T, L, d, n_seq, mode, per_seq, n_chunks;
+};
+
+gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
+  if (!s) return GBLA_ERR_INVALID_ARG;
+  if (s->io_dtype != GBLA_F32 && s->io_dtype != GBLA_BF16) return GBLA_ERR_INVALID_ARG;
+  if (s->B < 1 || s->L < 1 || s->d < 1) return GBLA_ERR_INVALID_ARG;
+  if (s->cu_seqlens && (s->seq_lens || s->B != 1 || s->num_seqs < 1)) return GBLA_ERR_INVALID_ARG;
+  const long long T = s->cu_seqlens ? (long long)s->L : (long long)s->B * s->L;
+  if (T > (1LL << 30) || s->d > (1 << 20)) return GBLA_ERR_UNSUPPORTED;
+  p.f32 = s->io_dtype == GBLA_F32;
+  p.T = (int)T; p.L = s->L; p.d = s->d;
+  p.mode = s->cu_seqlens ? SEQ_VARLEN : (s->seq_lens ? SEQ_PADDED : SEQ_DENSE);
+  p.n_seq = s->cu_seqlens ? s->num_seqs : s->B;
+  if ((long long)p.n_seq * p.d > (1LL << 38)) return GBLA_ERR_UNSUPPORTED;  // one thread each
+  p.per_seq = p.mode != SEQ_VARLEN && p.L >= kGlrChunk ? cdiv(p.L, kGlrChunk) : 0;
+  p.n_chunks = p.per_seq ? p.per_seq * p.n_seq : cdiv(p.T, kGlrChunk);
+  return GBLA_OK;
+}
+
+struct GlrLayout { size_t err, part, total; };
+GlrLayout glr_layout(const GlrPlan& p, int op) {
+  Cursor c;
+  GlrLayout l{};
+  l.err = c.take(16);
+  if (op == GBLA_OP_GLR_BACKWARD) l.part = c.take((size_t)p.n_seq * p.d * 4);
+  l.total = c.off;
+  return l;
+}
+
+struct GlrCtx {
+  GlrPlan p;
+  GlrLayout l;
+  GlrArgs a;
+  int* err;
+  cudaStream_t st;
+};
+
+// The arguments that both directions share; checks them and the sequence data.
+gbla_status glr_begin(const gbla_shape* shape, int op, const void* x, const void* r, const void* i, int64_t ld,
+                      const float* lam, float cc, int reverse, const float* h0, void* ws, size_t ws_bytes, void* stream,
+                      GlrCtx& c) {
+  gbla_status s = make_glr_plan(shape, c.p);
+  if (s != GBLA_OK) return s;
+  const GlrPlan& p = c.p;
+  const size_t es = p.f32 ? 4 : 2;
+  for (const void* q : {x, r, i})
+    if (!q || reinterpret_cast<uintptr_t>(q) % es) return GBLA_ERR_INVALID_ARG;
+  if (!lam || !aligned4(lam) || !aligned4(h0) || ld < p.d || !(cc > 0.f) || cc > 3e38f) return GBLA_ERR_INVALID_ARG;
+  if (reverse != 0 && reverse != 1) return GBLA_ERR_INVALID_ARG;
+  c.l = glr_layout(p, op);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) % kAlign) != 0 || ws_bytes < c.l.total) return GBLA_ERR_WORKSPACE;
+  c.st = static_cast<cudaStream_t>(stream);
+  c.err = at<int>(ws, c.l.err);
+  GlrArgs& a = c.a;
+  a = GlrArgs{};
+  a.x = x; a.r = r; a.i = i; a.ld = ld;
+  a.lam = lam; a.c = cc; a.reverse = reverse; a.h0 = h0;
+  a.d = p.d; a.per_seq = p.per_seq; a.n_chunks = p.n_chunks;
+  a.seq.mode = p.mode; a.seq.n_seq = p.n_seq; a.seq.L = p.mode == SEQ_VARLEN ? p.T : p.L; a.seq.T = p.T;
+  a.seq.lens = shape->seq_lens; a.seq.cu = shape->cu_seqlens;
+  a.err = p.mode == SEQ_DENSE ? nullptr : c.err;
+  return GBLA_OK;
+}
+
+// Clears the error word and checks the sequence data on the device.
+gbla_status glr_check_seqs(GlrCtx& c) {
+  GBLA_CHECK(cudaMemsetAsync(c.err, 0, 16, c.st), "memset");
+  if (c.p.mode != SEQ_DENSE) {
+    const int ts[1] = {kGlrChunk};
+    int32_t* pre[1] = {nullptr};
+    GBLA_CHECK(launch_plan(c.a.seq, 0, ts, pre, c.err, c.st), "plan");
+  }
+  return GBLA_OK;
+}
+
 // State reduction + combine.  The bf16 path centres the state on the
 // k~-weighted mean of v (center); the fp32 path keeps it uncentred.
 // The layer's bf16 readout: the tcgen05 kernel where it applies.
@@ -520,6 +601,10 @@ gbla_status gbla_validate_shape(const gbla_shape* shape) {
 }
 
 size_t gbla_workspace_size(const gbla_shape* shape, int op) {
+  if (op == GBLA_OP_GLR_FORWARD || op == GBLA_OP_GLR_BACKWARD) {
+    GlrPlan g;
+    return make_glr_plan(shape, g) == GBLA_OK ? glr_layout(g, op).total : 0;
+  }
   Plan p;
   if (make_plan(shape, p) != GBLA_OK) return 0;
   if (op < GBLA_OP_FORWARD || op > GBLA_OP_SA_FORWARD) return 0;
@@ -847,6 +932,52 @@ gbla_status sa_core_forward(const gbla_shape* shape, const void* q, const void* 
     GBLA_CHECK(launch_plan(c.seq, 1, ts, pre, c.err, c.st), "plan");
   }
   GBLA_CHECK(launch_sa_fwd_tc(a, sa_blocks(p), c.st), "sa[tc]");
+  return GBLA_OK;
+}
+
+size_t glr_saved_size(const gbla_shape* shape) {
+  GlrPlan p;
+  return make_glr_plan(shape, p) == GBLA_OK ? align_up((size_t)p.n_chunks * p.d * 4) : 0;
+}
+
+gbla_status glr_forward(const gbla_shape* shape, const void* x, const void* r, const void* i, int64_t ld,
+                        const float* lam, float c_decay, int reverse, const float* h0, void* y, float* hT, void* saved,
+                        void* ws, size_t ws_bytes, void* stream) {
+  GlrCtx c;
+  gbla_status s = glr_begin(shape, GBLA_OP_GLR_FORWARD, x, r, i, ld, lam, c_decay, reverse, h0, ws, ws_bytes, stream, c);
+  if (s != GBLA_OK) return s;
+  const size_t es = c.p.f32 ? 4 : 2;
+  if (!y || reinterpret_cast<uintptr_t>(y) % es || !aligned4(hT)) return GBLA_ERR_INVALID_ARG;
+  if (saved && reinterpret_cast<uintptr_t>(saved) % kAlign) return GBLA_ERR_INVALID_ARG;
+  c.a.y = y; c.a.hT = hT; c.a.saved = static_cast<float*>(saved);
+  if ((s = glr_check_seqs(c)) != GBLA_OK) return s;
+  GBLA_CHECK(launch_glr_fwd(c.a, c.p.f32, c.st), "glr fwd");
+  return GBLA_OK;
+}
+
+gbla_status glr_backward(const gbla_shape* shape, const void* x, const void* r, const void* i, int64_t ld,
+                         const float* lam, float c_decay, int reverse, const float* h0, const void* saved,
+                         const void* dy, const float* dhT, void* dx, void* dr, void* di, int64_t ldd, float* dlam,
+                         float* dh0, void* ws, size_t ws_bytes, void* stream) {
+  GlrCtx c;
+  gbla_status s = glr_begin(shape, GBLA_OP_GLR_BACKWARD, x, r, i, ld, lam, c_decay, reverse, h0, ws, ws_bytes, stream, c);
+  if (s != GBLA_OK) return s;
+  const size_t es = c.p.f32 ? 4 : 2;
+  for (const void* q : {dy, (const void*)dx, (const void*)dr, (const void*)di})
+    if (!q || reinterpret_cast<uintptr_t>(q) % es) return GBLA_ERR_INVALID_ARG;
+  if (!saved || reinterpret_cast<uintptr_t>(saved) % kAlign) return GBLA_ERR_INVALID_ARG;
+  if (!aligned4(dhT) || !aligned4(dlam) || !aligned4(dh0) || ldd < c.p.d) return GBLA_ERR_INVALID_ARG;
+  GlrArgs& a = c.a;
+  a.saved = static_cast<float*>(const_cast<void*>(saved));
+  a.dy = dy; a.dhT = dhT; a.dx = dx; a.dr = dr; a.di = di; a.ldd = ldd; a.dh0 = dh0;
+  a.dlam_part = dlam ? at<float>(ws, c.l.part) : nullptr;
+  if ((s = glr_check_seqs(c)) != GBLA_OK) return s;
+  GBLA_CHECK(launch_glr_bwd(a, c.p.f32, c.st), "glr bwd");
+  if (dlam) {
+    ColsumJobs js{};
+    js.j[js.n++] = ColsumJob{a.dlam_part, c.p.n_seq, c.p.d, c.p.d, dlam, nullptr, 0};
+    GBLA_CHECK(launch_colsums(js, c.st), "glr dlam");
+  }
   return GBLA_OK;
 }
 

@@ -168,6 +168,27 @@ struct DecayArgs {
   const int* err;
 };
 
+// The gated linear recurrence (glr.cu).  Its rows are cut into chunks of
+// kGlrChunk: per sequence slot (per_seq chunks each, slots of at least a chunk)
+// or, for packed and short sequences, over all rows (per_seq = 0).
+constexpr int kGlrChunk = 64;
+struct GlrArgs {
+  const void* x; const void* r; const void* i; int64_t ld;  // [T, ld]
+  const float* lam; float c;                                // [d]
+  int reverse;
+  const float* h0;                                          // [n_seq, d] or null
+  void* y; float* hT;                                       // [T, d]; [n_seq, d] or null
+  float* saved;                                             // [chunks][d]: the state on entry to each chunk, or null
+  // backward
+  const void* dy; const float* dhT;                         // [T, d]; [n_seq, d] or null
+  void* dx; void* dr; void* di; int64_t ldd;                // [T, ldd]
+  float* dlam_part; float* dh0;                             // dlam partial rows [..][d]; [n_seq, d] or null
+  int d;
+  SeqDesc seq;
+  int per_seq, n_chunks;
+  const int* err;
+};
+
 // ---------------------------------------------------------------- launchers
 cudaError_t launch_plan(const SeqDesc& s, int ntile, const int* tile_sizes, int32_t* const* prefixes,
                         int* err, cudaStream_t st);
@@ -233,6 +254,9 @@ cudaError_t launch_decay_states(const DecayArgs& a, int n_chunks, cudaStream_t s
 cudaError_t launch_decay_scan(const DecayArgs& a, int n_seq, cudaStream_t st);
 cudaError_t launch_decay_out(const DecayArgs& a, int n_chunks, cudaStream_t st);
 constexpr int kDecayChunk = 128;  // rows per chunk of the decay core
+
+cudaError_t launch_glr_fwd(const GlrArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_glr_bwd(const GlrArgs& a, bool f32, cudaStream_t st);
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, bool f32, cudaStream_t st, int* tiled = nullptr);
 // Writes the parameter-gradient partials to part[0 .. *nparts)[d][5].

@@ -7,6 +7,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -22,13 +23,14 @@ GBLA_POLICY_AUTO, GBLA_POLICY_TC, GBLA_POLICY_MMA = 0, 1, 2
 GBLA_F32, GBLA_BF16 = 0, 1
 GBLA_GATE_SIGMOID, GBLA_GATE_SOFTMAX = 0, 1
 GBLA_OP_FORWARD, GBLA_OP_BACKWARD, GBLA_OP_CORE_FORWARD, GBLA_OP_CORE_BACKWARD, GBLA_OP_DECAY_FORWARD = 0, 1, 2, 3, 4
-GBLA_OP_SA_FORWARD = 5
+GBLA_OP_SA_FORWARD, GBLA_OP_GLR_FORWARD, GBLA_OP_GLR_BACKWARD = 5, 6, 7
 
 EXPORTS = ("gbla_workspace_size", "gbla_saved_size", "gbla_validate_shape", "gbla_forward", "gbla_backward",
            "bla_core_forward", "bla_core_backward", "gbla_check_device_status", "gbla_status_string",
            "gbla_last_error", "gbla_version", "gbla_profiling_enable", "gbla_profiling_read",
            "bla_core_forward_noalloc", "bla_core_noalloc_check_device_status", "gbla_diag_bounded_wait",
-           "gbla_set_kernel_policy", "bla_decay_core_forward", "sa_core_forward")
+           "gbla_set_kernel_policy", "bla_decay_core_forward", "sa_core_forward",
+           "glr_forward", "glr_backward", "glr_saved_size")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -78,6 +80,13 @@ def lib() -> ctypes.CDLL:
         L.bla_decay_core_forward.restype = ctypes.c_int
         L.sa_core_forward.argtypes = [sp] + [vp] * 5 + [sz, vp]
         L.sa_core_forward.restype = ctypes.c_int
+        L.glr_forward.argtypes = [sp, vp, vp, vp, ctypes.c_int64, vp, ctypes.c_float, ctypes.c_int] + [vp] * 5 + [sz, vp]
+        L.glr_forward.restype = ctypes.c_int
+        L.glr_backward.argtypes = [sp, vp, vp, vp, ctypes.c_int64, vp, ctypes.c_float, ctypes.c_int] + [vp] * 7 + \
+            [ctypes.c_int64] + [vp] * 3 + [sz, vp]
+        L.glr_backward.restype = ctypes.c_int
+        L.glr_saved_size.argtypes = [sp]
+        L.glr_saved_size.restype = sz
         L.bla_core_forward_noalloc.argtypes = [sp] + [vp] * 8
         L.bla_core_forward_noalloc.restype = ctypes.c_int
         L.bla_core_noalloc_check_device_status.argtypes = [vp]
@@ -144,6 +153,13 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _on(device):
+    """The device a call's tensors are on, made current for the launch."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
 def _check(status: int, what: str):
     if status != GBLA_OK:
         raise GblaError(status, what)
@@ -163,6 +179,8 @@ def gbla_validate_shape(shape: Shape) -> int:
 
 def workspace(shape: Shape, op: int, device="cuda") -> torch.Tensor:
     n = gbla_workspace_size(shape, op)
+    if n == 0 and op in (GBLA_OP_GLR_FORWARD, GBLA_OP_GLR_BACKWARD):
+        _check(GBLA_ERR_INVALID_ARG, "gbla_workspace_size")
     if n == 0:
         _check(gbla_validate_shape(shape) or GBLA_ERR_INVALID_ARG, "gbla_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -256,6 +274,114 @@ def sa_core_forward(shape: Shape, q, k, v, o=None, ws=None):
                                _stream())
     _check(st, "sa_core_forward")
     return o
+
+
+def glr_shape(B: int, L: int, d: int, dtype: str = "bf16", cu_seqlens: torch.Tensor | None = None,
+              seq_lens: torch.Tensor | None = None) -> Shape:
+    """make_shape for the gated linear recurrence, which has channels but no heads."""
+    for name, t, n in (("cu_seqlens", cu_seqlens, 2), ("seq_lens", seq_lens, B)):
+        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or not t.is_contiguous()
+                              or (t.numel() < n if name == "cu_seqlens" else t.numel() != n)):
+            raise ValueError(f"{name}: want a contiguous int32 CUDA tensor of {n} values{' at least' if n == 2 else ''}, "
+                             f"got {t.dtype} {list(t.shape)} on {t.device}")
+    return make_shape(B, L, d, 1, 1, dtype=dtype, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
+
+
+def glr_saved_size(shape: Shape) -> int:
+    return lib().glr_saved_size(ctypes.byref(shape))
+
+
+def _glr_arg(name, t, shape_, dtype, device, ld=None):
+    """t's row stride.  Raises unless t is a tensor of this shape, dtype and device, its rows contiguous and (ld) of
+    this stride, all else contiguous."""
+    if t.dtype != dtype or tuple(t.shape) != shape_ or t.device != device:
+        raise ValueError(f"{name}: want {dtype} {list(shape_)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    n = t.stride(0) if t.dim() == 2 and t.size(0) > 1 else (ld or t.shape[-1])
+    if t.size(-1) > 1 and t.stride(-1) != 1 or n < t.shape[-1] or (ld is not None and n != ld):
+        raise ValueError(f"{name}: strides {t.stride()}: rows have to be contiguous, and of one stride where tensors share it")
+    return n
+
+
+def _glr_check(shape, x, r, i, lam, h0):
+    dev, d, io = x.device, shape.d, io_dtype(shape)
+    if not x.is_cuda:
+        raise ValueError(f"x: want a CUDA tensor, got {x.device}")
+    T = rows(shape)
+    lds = [t.stride(0) for t in (x, r, i) if t.dim() == 2 and t.size(0) > 1]
+    ld = lds[0] if lds else d
+    for name, t in (("x", x), ("r", r), ("i", i)):
+        _glr_arg(name, t, (T, d), io, dev, ld)
+    _glr_arg("lam", lam, (d,), torch.float32, dev)
+    if h0 is not None:
+        _glr_arg("h0", h0, (n_seq(shape), d), torch.float32, dev, d)
+    return ld
+
+
+def glr_forward(shape: Shape, x, r, i, lam, c: float = 8.0, reverse: bool = False, h0=None, y=None, hT=None,
+                saved: torch.Tensor | bool | None = None, ws=None):
+    """The gated linear recurrence (see gbla.h): returns (y, hT, saved).  x, r and i share their row stride (they may
+    be columns of one tensor).  hT: a tensor to fill (h0 itself to update it in place), or True to allocate it; saved =
+    True allocates what glr_backward needs.  Tensors are on x's device, the call on that device's current stream."""
+    ld = _glr_check(shape, x, r, i, lam, h0)
+    dev, T, d = x.device, rows(shape), shape.d
+    if y is None:
+        y = torch.empty(T, d, dtype=x.dtype, device=dev)
+    _glr_arg("y", y, (T, d), x.dtype, dev, d)
+    if hT is True:
+        hT = torch.empty(n_seq(shape), d, dtype=torch.float32, device=dev)
+    if hT is not None:
+        _glr_arg("hT", hT, (n_seq(shape), d), torch.float32, dev, d)
+    if saved is True:
+        saved = torch.empty(glr_saved_size(shape), dtype=torch.uint8, device=dev)
+    saved = saved if isinstance(saved, torch.Tensor) else None
+    if saved is not None:
+        _glr_saved(shape, saved, dev)
+    if ws is None:
+        ws = workspace(shape, GBLA_OP_GLR_FORWARD, dev)
+    with _on(dev):
+        st = lib().glr_forward(ctypes.byref(shape), _ptr(x), _ptr(r), _ptr(i), ld, _ptr(lam), c, int(reverse), _ptr(h0),
+                               _ptr(y), _ptr(hT), _ptr(saved), _ptr(ws), ws.numel(), _stream())
+    _check(st, "glr_forward")
+    return y, hT, saved
+
+
+def _glr_saved(shape, saved, dev):
+    n = glr_saved_size(shape)
+    if saved.device != dev or not saved.is_contiguous() or saved.numel() * saved.element_size() < n:
+        raise ValueError(f"saved: want {n} bytes on {dev}")
+
+
+def glr_backward(shape: Shape, x, r, i, lam, saved, dy, c: float = 8.0, reverse: bool = False, h0=None, dhT=None,
+                 ws=None, out: dict | None = None) -> dict:
+    """Backward of glr_forward for <dy, y> + <dhT, hT>.  Returns dx, dr, di (io dtype), dlam fp32 and, where h0 or dhT
+    is given, dh0 fp32.  out: tensors to fill (dx, dr and di of one row stride)."""
+    ld = _glr_check(shape, x, r, i, lam, h0)
+    dev, T, d = x.device, rows(shape), shape.d
+    _glr_arg("dy", dy, (T, d), x.dtype, dev, d)
+    if dhT is not None:
+        _glr_arg("dhT", dhT, (n_seq(shape), d), torch.float32, dev, d)
+    _glr_saved(shape, saved, dev)
+    g = out
+    if g is None:
+        g = {n: torch.empty(T, d, dtype=x.dtype, device=dev) for n in ("dx", "dr", "di")}
+        g["dlam"] = torch.empty(d, dtype=torch.float32, device=dev)
+        if h0 is not None or dhT is not None:
+            g["dh0"] = torch.empty(n_seq(shape), d, dtype=torch.float32, device=dev)
+    ldd = g["dx"].stride(0) if T > 1 else d
+    for n in ("dx", "dr", "di"):
+        _glr_arg(n, g[n], (T, d), x.dtype, dev, ldd)
+    if g.get("dlam") is not None:
+        _glr_arg("dlam", g["dlam"], (d,), torch.float32, dev)
+    if g.get("dh0") is not None:
+        _glr_arg("dh0", g["dh0"], (n_seq(shape), d), torch.float32, dev, d)
+    if ws is None:
+        ws = workspace(shape, GBLA_OP_GLR_BACKWARD, dev)
+    with _on(dev):
+        st = lib().glr_backward(ctypes.byref(shape), _ptr(x), _ptr(r), _ptr(i), ld, _ptr(lam), c, int(reverse), _ptr(h0),
+                                _ptr(saved), _ptr(dy), _ptr(dhT), _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["di"]), ldd,
+                                _ptr(g.get("dlam")), _ptr(g.get("dh0")), _ptr(ws), ws.numel(), _stream())
+    _check(st, "glr_backward")
+    return g
 
 
 def bla_core_forward_noalloc(shape: Shape, q, k, v, g, o, den=None, state=None) -> int:

@@ -85,7 +85,9 @@ typedef enum {
   GBLA_OP_CORE_FORWARD = 2,   /* bla_core_forward                            */
   GBLA_OP_CORE_BACKWARD = 3,  /* bla_core_backward                           */
   GBLA_OP_DECAY_FORWARD = 4,  /* bla_decay_core_forward                      */
-  GBLA_OP_SA_FORWARD = 5      /* sa_core_forward                             */
+  GBLA_OP_SA_FORWARD = 5,     /* sa_core_forward                             */
+  GBLA_OP_GLR_FORWARD = 6,    /* glr_forward                                 */
+  GBLA_OP_GLR_BACKWARD = 7    /* glr_backward                                */
 } gbla_op;
 
 typedef struct {
@@ -223,6 +225,58 @@ gbla_status bla_decay_core_forward(const gbla_shape* shape, const void* q,
 gbla_status sa_core_forward(const gbla_shape* shape, const void* q,
                             const void* k, const void* v, void* o, void* ws,
                             size_t ws_bytes, void* stream);
+
+/*
+ * Gated linear recurrence: a state per channel that decays by an amount read
+ * from the token, the token-by-token counterpart of the layer's global sums
+ * (the same operator serves one token at a time: L = 1 with h0 and hT).  Per
+ * sequence and channel, over the tokens t in order (reverse = 0) or from the
+ * last to the first (reverse = 1; a bidirectional encoder runs both):
+ *   s_t = c softplus(lam) sigmoid(r_t),  a_t = exp(-s_t),
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   y_t = h_t,
+ * with h = h0 (or 0) before the sequence's first token.
+ *   x, r, i (io) [rows, d] with row stride ld elements (ld >= d; ld = d when
+ *           contiguous, ld = 3 d when x | r | i are columns of one
+ *           projection): values and the logits of the two gates.  r = -inf
+ *           gives a_t = 1 and leaves the state as it is for finite x and i.
+ *   lam     fp32 [d]; c > 0 (e.g. 8)
+ *   h0      fp32 [n_seq, d] or NULL (zeros); n_seq = B, or num_seqs (varlen)
+ *   y       (io) [rows, d]
+ *   hT      fp32 [n_seq, d] or NULL: the state after the sequence's last token
+ *           in the recurrence's order (h0, or 0, where the sequence is
+ *           empty).  hT may be h0: the state is then updated in place.
+ *   saved   NULL (inference) or glr_saved_size() bytes, 256-byte aligned,
+ *           filled for glr_backward
+ * States, sums and gates are fp32; y is rounded once.  d and ld are free
+ * (any d >= 1); the pointers are aligned to their element; tensors do not
+ * overlap (but hT = h0).  The shape's H, d_h, gate and rms_eps are ignored
+ * (gbla_validate_shape does not apply); rows <= 2^30, d <= 2^20.  Workspace:
+ * gbla_workspace_size(shape, GBLA_OP_GLR_FORWARD).
+ */
+gbla_status glr_forward(const gbla_shape* shape, const void* x, const void* r,
+                        const void* i, int64_t ld, const float* lam, float c,
+                        int reverse, const float* h0, void* y, float* hT,
+                        void* saved, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of the buffer that glr_forward fills for glr_backward (0 on a shape
+ * error).  Caller-owned. */
+size_t glr_saved_size(const gbla_shape* shape);
+
+/*
+ * Backward of glr_forward for the scalar <dy, y> + <dhT, hT>: the forward's
+ * inputs, its `saved`, dy (io) [rows, d] and dhT fp32 [n_seq, d] or NULL
+ * (zeros).  Outputs:
+ *   dx, dr, di (io) [rows, d] with row stride ldd (ldd >= d; e.g. the columns
+ *   of one gradient matrix); dlam fp32 [d] or NULL; dh0 fp32 [n_seq, d] or
+ *   NULL (an empty sequence's is its dhT).  Gradients overwrite.
+ * Workspace: gbla_workspace_size(shape, GBLA_OP_GLR_BACKWARD).
+ */
+gbla_status glr_backward(const gbla_shape* shape, const void* x, const void* r,
+                         const void* i, int64_t ld, const float* lam, float c,
+                         int reverse, const float* h0, const void* saved,
+                         const void* dy, const float* dhT, void* dx, void* dr,
+                         void* di, int64_t ldd, float* dlam, float* dh0,
+                         void* ws, size_t ws_bytes, void* stream);
 
 /*
  * bla_core_forward without a caller workspace (the pages have no counterpart:

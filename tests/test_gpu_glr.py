@@ -1,0 +1,280 @@
+"""The gated linear recurrence (glr_forward, glr_backward) against its formulas
+in 64 bits (glr_cases): dense, padded and packed batches, both directions, with
+and without a start state, odd widths and lengths from one token up, packed
+projections, extreme logits, masked rows, pieces and single steps, streams and
+graphs, bad sequence data."""
+import numpy as np
+import pytest
+import torch
+
+from generative_retrieval_encoder_gb300 import build, gbla
+from glr_cases import Case, check, reference, sigmoid, softplus
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    gbla.lib()
+
+
+CASES = [
+    dict(dtype="bf16", d=64, L=1),
+    dict(dtype="f32", d=1, L=1),
+    dict(dtype="bf16", d=512, L=1, B=5),
+    dict(dtype="f32", d=3, L=7, B=3, reverse=True),
+    dict(dtype="bf16", d=130, L=63, B=2),
+    dict(dtype="f32", d=64, L=64, B=2, packed=True),
+    dict(dtype="bf16", d=72, L=65, B=3, reverse=True, state=False),
+    dict(dtype="bf16", d=33, L=200, B=2, packed=True),
+    dict(dtype="f32", d=66, L=129, B=2, seq_lens=[129, 1]),
+    dict(dtype="bf16", d=64, L=300, B=5, seq_lens=[300, 0, 64, 1, 257], reverse=True),
+    dict(dtype="f32", d=40, L=20, B=7, seq_lens=[20, 0, 1, 19, 2, 20, 5]),
+    dict(dtype="f32", d=48, lengths=[5, 0, 300, 1, 64, 129, 0, 1000]),
+    dict(dtype="bf16", d=64, lengths=[0, 0, 64, 64, 1, 1, 1, 61, 128, 2, 700, 0], reverse=True),
+    dict(dtype="bf16", d=130, lengths=[1] * 150 + [3] * 40, state=False),
+    dict(dtype="f32", d=8, lengths=[1], reverse=True),
+    dict(dtype="bf16", d=64, L=2048, B=3),
+    dict(dtype="f32", d=8, L=20000),                       # chunks of several levels of the scan
+    dict(dtype="f32", d=8, L=20011, reverse=True, packed=True),
+    dict(dtype="bf16", d=5, lengths=[17000, 3, 17500]),
+    dict(dtype="f32", d=6, lengths=[3, 18000, 0, 1, 16400], reverse=True),
+]
+
+
+def _id(c):
+    return "-".join(f"{k}{len(v) if isinstance(v, list) else v}" for k, v in c.items())
+
+
+@pytest.mark.parametrize("kw", CASES, ids=[_id(c) for c in CASES])
+def test_glr_matches_formulas(kw):
+    c = Case(seed=CASES.index(kw), **kw)
+    y, hT, saved = c.forward(hT=True, saved=True)
+    g = c.backward(saved)
+    y2, _, _ = c.forward()  # inference: the same values
+    torch.cuda.synchronize()
+    want = c.reference()
+    check({"y": y, "hT": hT, **g}, want)
+    assert torch.equal(y, y2)
+    pad = np.ones(c.T, bool)
+    for a, n in zip(c.starts, c.lens):
+        pad[a:a + n] = False
+    pad = torch.from_numpy(pad).cuda()
+    for t in (y, g["dx"], g["dr"], g["di"]):
+        assert (t[pad] == 0).all()
+
+
+def test_glr_without_optional_tensors_and_with_strided_outputs():
+    c = Case("bf16", 96, L=150, B=3, state=False, seed=40)
+    y, hT, saved = c.forward(saved=True)
+    assert hT is None
+    buf = torch.full((c.T, 3 * 96 + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = {"dx": buf[:, :96], "dr": buf[:, 96:192], "di": buf[:, 192:288]}
+    c.backward(saved, out=out)
+    torch.cuda.synchronize()
+    want = c.reference()
+    check({"y": y, **out}, want)
+    assert (buf[:, 288:] == 7).all()
+
+
+def test_glr_writes_nothing_around_its_outputs():
+    c = Case("f32", 33, lengths=[70, 0, 5, 129], seed=41)
+    T, d, n = c.T, c.d, c.n
+    guard = lambda r: torch.full((r + 2, d), 5.0, device="cuda")  # noqa: E731
+    y, hT, dx, dr, di, dh0 = guard(T), guard(n), guard(T), guard(T), guard(T), guard(n)
+    dlam = torch.full((3, d), 5.0, device="cuda")
+    saved = torch.full((gbla.glr_saved_size(c.shape) + 512,), 9, dtype=torch.uint8, device="cuda")
+    ws_f = torch.full((gbla.gbla_workspace_size(c.shape, gbla.GBLA_OP_GLR_FORWARD) + 256,), 9, dtype=torch.uint8, device="cuda")
+    ws_b = torch.full((gbla.gbla_workspace_size(c.shape, gbla.GBLA_OP_GLR_BACKWARD) + 256,), 9, dtype=torch.uint8, device="cuda")
+    c.forward(y=y[1:-1], hT=hT[1:-1], saved=saved[:-512], ws=ws_f[:-256])
+    c.backward(saved[:-512], ws=ws_b[:-256], out={"dx": dx[1:-1], "dr": dr[1:-1], "di": di[1:-1], "dh0": dh0[1:-1], "dlam": dlam[1]})
+    torch.cuda.synchronize()
+    check({"y": y[1:-1], "hT": hT[1:-1], "dx": dx[1:-1], "dr": dr[1:-1], "di": di[1:-1], "dh0": dh0[1:-1], "dlam": dlam[1]}, c.reference())
+    for t in (y, hT, dx, dr, di, dh0, dlam):
+        assert (t[0] == 5).all() and (t[-1] == 5).all()
+    assert (saved[-512:] == 9).all() and (ws_f[-256:] == 9).all() and (ws_b[-256:] == 9).all()
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_glr_padded_rows_may_hold_anything(reverse):
+    """Infinities, NaN and the type's lowest value in rows of no sequence reach nothing."""
+    c = Case("bf16", 64, L=100, B=4, seq_lens=[0, 37, 100, 64], reverse=reverse, seed=42)
+    want = c.reference()
+    for b, n in enumerate(c.lens):
+        for t, bad in ((c.x, float("nan")), (c.r, float("inf")), (c.i, torch.finfo(torch.bfloat16).min), (c.dy, float("-inf"))):
+            t[b * 100 + n:(b + 1) * 100] = bad
+    y, hT, saved = c.forward(hT=True, saved=True)
+    g = c.backward(saved)
+    torch.cuda.synchronize()
+    check({"y": y, "hT": hT, **g}, want)
+
+
+def test_glr_a_sequence_with_nan_leaves_the_others_alone():
+    lens = [100, 700, 3, 150]
+    c = Case("f32", 16, lengths=lens, seed=43)
+    want = c.reference()
+    c.x[150] = float("nan")   # in sequence 1
+    c.h0[1] = float("inf")
+    y, hT, saved = c.forward(hT=True, saved=True)
+    g = c.backward(saved)
+    torch.cuda.synchronize()
+    keep = [t for b in (0, 2, 3) for t in range(c.starts[b], c.starts[b] + lens[b])]
+    for n, t in {"y": y, "dx": g["dx"], "dr": g["dr"], "di": g["di"]}.items():
+        check({n: t[keep]}, {n: tuple(w[keep] for w in want[n])})
+    for n, t in {"hT": hT, "dh0": g["dh0"]}.items():
+        check({n: t[[0, 2, 3]]}, {n: tuple(w[[0, 2, 3]] for w in want[n])})
+    assert torch.isnan(y[799]).all() and torch.isnan(hT[1]).all()
+
+
+def test_glr_extreme_logits_and_decays():
+    """r = -inf keeps the state, r = +inf and +-1e4 saturate; lam from -200 (no decay) to 50 (no memory)."""
+    d = 24
+    lam = torch.cat([torch.linspace(-200, 50, 12), torch.linspace(-12, 3, 12)])
+    c = Case("f32", d, L=130, seed=44, lam=lam)
+    big = torch.tensor([-1e4, -80.0, -30.0, 30.0, 1e4, 0.0], device="cuda")
+    c.r[10:16] = big[:, None]
+    c.i[40:46] = big[:, None]
+    c.r[100] = float("-inf")
+    c.r[101] = float("inf")
+    c.i[102] = float("-inf")
+    c.i[103] = float("inf")
+    y, hT, saved = c.forward(hT=True, saved=True)
+    g = c.backward(saved)
+    torch.cuda.synchronize()
+    assert torch.equal(y[100], y[99])
+    want = c.reference()
+    # sigmoids below 2^-126 are 0 in the kernels: absolute, far below any output here
+    check({"y": y, "hT": hT, **g}, want, floor=1e-18)
+
+
+def test_glr_in_pieces_and_in_place_steps():
+    """Prefill in pieces and then token by token, the state updated in place: the whole sequence's outputs."""
+    B, L, d = 3, 210, 40
+    c = Case("f32", d, L=L, B=B, seed=45)
+    want = c.reference(backward=False)
+    h = c.h0.clone()
+    at, out = 0, []
+    cut = lambda t, a, n: t.view(B, L, d)[:, a:a + n].reshape(B * n, d).contiguous()  # noqa: E731
+    for n in [130, 64] + [1] * 16:
+        sh = gbla.glr_shape(B, n, d, dtype="f32")
+        y, hT, _ = gbla.glr_forward(sh, cut(c.x, at, n), cut(c.r, at, n), cut(c.i, at, n), c.lam, h0=h, hT=h)
+        assert hT is h
+        out.append(y.view(B, n, d))
+        at += n
+    torch.cuda.synchronize()
+    check({"y": torch.cat(out, 1).reshape(B * L, d), "hT": h}, want)
+
+
+@pytest.mark.parametrize("lengths", [None, [100, 0, 5000, 1, 63]])
+def test_glr_long_state_in_place(lengths):
+    kw = dict(lengths=lengths) if lengths else dict(L=1500, B=3)
+    c = Case("bf16", 72, seed=46, reverse=True, **kw)
+    want = c.reference(backward=False)
+    y, hT, _ = gbla.glr_forward(c.shape, c.x, c.r, c.i, c.lam, reverse=True, h0=c.h0, hT=c.h0)
+    torch.cuda.synchronize()
+    assert hT is c.h0
+    check({"y": y, "hT": hT}, want)
+
+
+def test_glr_gradients_by_differences():
+    """<dy, y> + <dhT, hT> of the formulas (64 bits) moved by each input, against the kernel's gradients."""
+    c = Case("f32", 4, lengths=[7, 0, 70], seed=47, reverse=True)
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    A = {k: f(getattr(c, k)) for k in ("x", "r", "i", "lam", "h0")}
+
+    def loss(**kw):
+        v = {**A, **kw}
+        o = reference(v["x"], v["r"], v["i"], v["lam"], 8.0, c.starts, c.lens, True, v["h0"], io="f32")
+        return float((o["y"][0] * f(c.dy)).sum() + (o["hT"][0] * f(c.dhT)).sum())
+
+    _, _, saved = c.forward(saved=True)
+    g = c.backward(saved)
+    rng = np.random.default_rng(3)
+    for name, grad in (("x", "dx"), ("r", "dr"), ("i", "di"), ("lam", "dlam"), ("h0", "dh0")):
+        got = f(g[grad])
+        for _ in range(6):
+            at = tuple(rng.integers(0, s) for s in A[name].shape)
+            up, dn = A[name].copy(), A[name].copy()
+            e = 1e-5
+            up[at] += e
+            dn[at] -= e
+            num = (loss(**{name: up}) - loss(**{name: dn})) / (2 * e)
+            # central differences in 64 bits: e^2 of the third derivative and 1e-16 / e of the loss; the kernel fp32
+            assert abs(got[at] - num) <= 1e-4 * max(1.0, abs(num)), (name, at, got[at], num)
+
+
+def test_glr_is_deterministic_on_streams_and_in_graphs():
+    c = Case("bf16", 256, L=4096, B=4, seed=48)
+    y, hT, saved = c.forward(hT=True, saved=True)
+    g = c.backward(saved)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    res = []
+    for s in (s1, s2):  # two calls at once, each with its own workspaces
+        with torch.cuda.stream(s):
+            a = c.forward(hT=True, saved=True)
+            res.append((a, c.backward(a[2])))
+    torch.cuda.synchronize()
+    for a, b in res:
+        assert torch.equal(a[0], y) and torch.equal(a[1], hT)
+        assert all(torch.equal(b[k], g[k]) for k in g)
+    # captured and replayed with new inputs in the same buffers
+    yb, hb, sb = torch.empty_like(y), torch.empty_like(hT), torch.empty_like(saved)
+    gb = {k: torch.empty_like(v) for k, v in g.items()}
+    ws = [gbla.workspace(c.shape, op) for op in (gbla.GBLA_OP_GLR_FORWARD, gbla.GBLA_OP_GLR_BACKWARD)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.forward(y=yb, hT=hb, saved=sb, ws=ws[0])
+        c.backward(sb, out=gb, ws=ws[1])
+    for k in range(3):
+        c.x.add_(0.25)
+        graph.replay()
+        a = c.forward(hT=True, saved=True)
+        b = c.backward(a[2])
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], yb) and torch.equal(a[1], hb) and all(torch.equal(b[n], gb[n]) for n in b)
+
+
+def test_glr_bad_sequence_data_is_reported():
+    """cu_seqlens that decrease or end elsewhere, seq_lens over L: nothing is written, the status says so."""
+    d, T = 16, 100
+    x = torch.randn(T, d, device="cuda")
+    lam = torch.zeros(d, device="cuda")
+    for kw in ({"cu_seqlens": [0, 60, 40, 100]}, {"cu_seqlens": [0, 60, 99]}, {"cu_seqlens": [1, 60, 100]},
+               {"cu_seqlens": [0, 1 << 30, 100]}, {"cu_seqlens": [0, -5, 100]}, {"seq_lens": [51, 3]}, {"seq_lens": [-1, 3]}):
+        t = {k: torch.tensor(v, dtype=torch.int32, device="cuda") for k, v in kw.items()}
+        B, L = (1, T) if "cu_seqlens" in kw else (2, 50)
+        sh = gbla.glr_shape(B, L, d, dtype="f32", **t)
+        ws = gbla.workspace(sh, gbla.GBLA_OP_GLR_FORWARD)
+        y = torch.full((T, d), 3.0, device="cuda")
+        saved = torch.zeros(gbla.glr_saved_size(sh), dtype=torch.uint8, device="cuda")
+        gbla.glr_forward(sh, x, x, x, lam, y=y, ws=ws, saved=saved)
+        assert gbla.gbla_check_device_status(ws) == gbla.GBLA_ERR_DEVICE_CHECK, kw
+        assert (y == 3).all()
+        ws = gbla.workspace(sh, gbla.GBLA_OP_GLR_BACKWARD)
+        out = {n: torch.full((T, d), 3.0, device="cuda") for n in ("dx", "dr", "di")}
+        gbla.glr_backward(sh, x, x, x, lam, saved, x, ws=ws, out=out)
+        assert gbla.gbla_check_device_status(ws) == gbla.GBLA_ERR_DEVICE_CHECK, kw
+        assert all((t == 3).all() for t in out.values())
+
+
+def test_glr_good_call_reports_ok_and_checks_its_arguments():
+    c = Case("f32", 16, L=100, B=2, seed=49)
+    ws = gbla.workspace(c.shape, gbla.GBLA_OP_GLR_FORWARD)
+    c.forward(ws=ws)
+    assert gbla.gbla_check_device_status(ws) == gbla.GBLA_OK
+    call = lambda **kw: gbla.glr_forward(c.shape, **{**dict(x=c.x, r=c.r, i=c.i, lam=c.lam, h0=c.h0), **kw})  # noqa: E731
+    for bad in (dict(x=c.x[:-1]), dict(r=c.r.bfloat16()), dict(i=c.i.cpu()), dict(lam=c.lam[:-1]), dict(lam=c.lam.double()),
+                dict(h0=c.h0[:1]), dict(r=torch.cat([c.r, c.r], 1)[:, :16]), dict(x=c.x.t().contiguous().t()),
+                dict(y=torch.empty(200, 17, device="cuda")[:, :16]), dict(hT=torch.empty(3, 16, device="cuda")),
+                dict(saved=torch.empty(8, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(gbla.GblaError):
+        call(ws=ws[:-1])
+    with pytest.raises(gbla.GblaError):
+        call(c=0.0)
+    with pytest.raises(ValueError):
+        gbla.glr_shape(2, 100, 16, dtype="f32", seq_lens=torch.ones(3, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
