@@ -431,6 +431,106 @@ gbla_status glr_check_seqs(GlrCtx& c) {
   return GBLA_OK;
 }
 
+// ------------------------------------------------------------ AdamW
+// Arguments of one tensor; norm_only: what gbla_grad_norm reads.
+bool adam_tensor_ok(const gbla_adamw_tensor& t, bool norm_only) {
+  if (t.n < 0 || t.n > (1LL << 40)) return false;
+  if (t.grad_dtype != GBLA_F32 && t.grad_dtype != GBLA_BF16) return false;
+  if (t.n == 0) return true;
+  auto ok = [](const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; };
+  if (!ok(t.grad, t.grad_dtype == GBLA_F32 ? 4 : 2)) return false;
+  if (norm_only) return true;
+  if (t.param_dtype != GBLA_F32 && t.param_dtype != GBLA_BF16) return false;
+  if (!ok(t.param, t.param_dtype == GBLA_F32 ? 4 : 2)) return false;
+  if (t.master && (t.param_dtype == GBLA_F32 || !aligned4(t.master))) return false;
+  if (!t.m_scale != !t.v_scale || !aligned4(t.m_scale) || !aligned4(t.v_scale)) return false;
+  const size_t a = t.m_scale ? 1 : 4;
+  return ok(t.m, a) && ok(t.v, a) && t.weight_decay >= 0. && t.weight_decay <= 1e30;
+}
+
+// Units of all tensors, and the launches' tables of at most `cap` tensors with values each.
+int64_t adam_units(const gbla_adamw_tensor* t, int n, int64_t* most = nullptr) {
+  int64_t u = 0;
+  for (int k = 0; k < n; ++k) {
+    const int64_t mine = (t[k].n + kAdamUnit - 1) / kAdamUnit;
+    u += mine;
+    if (most) *most = std::max(*most, mine);
+  }
+  return u;
+}
+int adam_cap(const gbla_adamw_tensor* t, int n) {
+  int live = 0;
+  for (int k = 0; k < n; ++k) live += t[k].n > 0;
+  return live <= kAdamFew ? kAdamFew : kAdamMany;
+}
+
+constexpr size_t kAdamScalarBytes = 256;
+// One fp64 partial for each CTA of each launch.
+size_t adam_parts(const gbla_adamw_tensor* t, int n) {
+  const int cap = adam_cap(t, n);
+  return (size_t)(n / cap + 1) * adamw_ctas(std::max<int64_t>(1, adam_units(t, n)));
+}
+
+gbla_status adam_check(const gbla_adamw_tensor* t, int n, bool norm_only, void* ws, size_t ws_bytes) {
+  if (n < 0 || (n > 0 && !t)) return GBLA_ERR_INVALID_ARG;
+  for (int k = 0; k < n; ++k)
+    if (!adam_tensor_ok(t[k], norm_only)) return GBLA_ERR_INVALID_ARG;
+  if (adam_units(t, n) > (1LL << 30)) return GBLA_ERR_UNSUPPORTED;  // units are counted in 32 bits
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % kAlign || ws_bytes < kAdamScalarBytes + 8 * adam_parts(t, n))
+    return GBLA_ERR_WORKSPACE;
+  return GBLA_OK;
+}
+
+// fn(table) for each launch's table.  The tensors without values are left out.
+template <int N, typename F>
+gbla_status adam_tables(const gbla_adamw_tensor* t, int n, double lr, F&& fn) {
+  AdamTable<N> tab;
+  tab.n = tab.units = 0;
+  int64_t place = 0;
+  for (int k = 0; k < n; ++k) {
+    if (t[k].n > 0) {
+      AdamTensor& o = tab.t[tab.n++];
+      o.param = t[k].param; o.master = t[k].master; o.grad = t[k].grad; o.m = t[k].m; o.v = t[k].v;
+      o.ms = t[k].m_scale; o.vs = t[k].v_scale;
+      o.n = t[k].n; o.place = place; o.first = tab.units;
+      o.keep = (float)(1. - lr * t[k].weight_decay);
+      o.pb = t[k].param_dtype == GBLA_BF16; o.gb = t[k].grad_dtype == GBLA_BF16;
+      o.vec = 0;
+      tab.units += (int)((t[k].n + kAdamUnit - 1) / kAdamUnit);
+      place += (t[k].n + kAdamBlock - 1) / kAdamBlock * kAdamBlock;
+    }
+    if (tab.n == N || (k == n - 1 && tab.n > 0)) {
+      const gbla_status r = fn(tab);
+      if (r != GBLA_OK) return r;
+      tab.n = tab.units = 0;
+    }
+  }
+  return GBLA_OK;
+}
+
+struct AdamCtx { cudaStream_t st; };
+
+template <int N>
+gbla_status run_grad_norm(const gbla_adamw_tensor* t, int n, float* norm, double* part, AdamCtx c) {
+  int parts = 0;
+  const gbla_status r = adam_tables<N>(t, n, 0., [&](const AdamTable<N>& tab) {
+    GBLA_CHECK(launch_sumsq<N>(tab, part + parts, c.st), "grad sumsq");
+    parts += adamw_ctas(tab.units);
+    return GBLA_OK;
+  });
+  if (r != GBLA_OK) return r;
+  GBLA_CHECK(launch_norm(part, parts, norm, c.st), "grad norm");
+  return GBLA_OK;
+}
+
+template <int N>
+gbla_status run_adamw(const gbla_adamw_tensor* t, int n, double lr, const AdamScalars* s, AdamCtx c) {
+  return adam_tables<N>(t, n, lr, [&](const AdamTable<N>& tab) {
+    GBLA_CHECK(launch_adamw<N>(tab, s, c.st), "adamw");
+    return GBLA_OK;
+  });
+}
+
 // State reduction + combine.  The bf16 path centres the state on the
 // k~-weighted mean of v (center); the fp32 path keeps it uncentred.
 // The layer's bf16 readout: the tcgen05 kernel where it applies.
@@ -979,6 +1079,42 @@ gbla_status glr_backward(const gbla_shape* shape, const void* x, const void* r, 
     GBLA_CHECK(launch_colsums(js, c.st), "glr dlam");
   }
   return GBLA_OK;
+}
+
+size_t gbla_adamw_workspace_size(const gbla_adamw_tensor* tensors, int n_tensors) {
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return 0;
+  for (int k = 0; k < n_tensors; ++k)
+    if (tensors[k].n < 0 || tensors[k].n > (1LL << 40)) return 0;
+  return align_up(kAdamScalarBytes + 8 * adam_parts(tensors, n_tensors));
+}
+
+gbla_status gbla_grad_norm(const gbla_adamw_tensor* tensors, int n_tensors, float* norm, void* ws, size_t ws_bytes,
+                           void* stream) {
+  const gbla_status r = adam_check(tensors, n_tensors, true, ws, ws_bytes);
+  if (r != GBLA_OK) return r;
+  if (!norm || !aligned4(norm)) return GBLA_ERR_INVALID_ARG;
+  const AdamCtx c{static_cast<cudaStream_t>(stream)};
+  double* part = at<double>(ws, kAdamScalarBytes);
+  return adam_cap(tensors, n_tensors) == kAdamFew ? run_grad_norm<kAdamFew>(tensors, n_tensors, norm, part, c)
+                                                  : run_grad_norm<kAdamMany>(tensors, n_tensors, norm, part, c);
+}
+
+gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors, const gbla_adamw_config* config,
+                            int64_t* step, const float* norm, void* ws, size_t ws_bytes, void* stream) {
+  const gbla_status r = adam_check(tensors, n_tensors, false, ws, ws_bytes);
+  if (r != GBLA_OK) return r;
+  if (!config || !step || reinterpret_cast<uintptr_t>(step) % 8 || !aligned4(norm)) return GBLA_ERR_INVALID_ARG;
+  const gbla_adamw_config& g = *config;
+  auto in = [](double v, double lo, double hi) { return v >= lo && v <= hi; };  // false for NaN
+  if (!in(g.lr, 0., 1e30) || !in(g.beta1, 0., 0.9999999) || !in(g.beta2, 0., 0.9999999) || !in(g.eps, 1e-30, 1e30) ||
+      !in(g.max_norm, 0., 1e30) || (g.max_norm > 0. && !norm))
+    return GBLA_ERR_INVALID_ARG;
+  const AdamCtx c{static_cast<cudaStream_t>(stream)};
+  AdamScalars* s = at<AdamScalars>(ws, 0);
+  AdamStep a{g.lr, g.beta1, g.beta2, g.eps, g.max_norm, g.seed};
+  GBLA_CHECK(launch_adamw_begin(a, step, norm, s, c.st), "adamw begin");
+  return adam_cap(tensors, n_tensors) == kAdamFew ? run_adamw<kAdamFew>(tensors, n_tensors, g.lr, s, c)
+                                                  : run_adamw<kAdamMany>(tensors, n_tensors, g.lr, s, c);
 }
 
 gbla_status gbla_check_device_status(const void* ws, void* stream) {

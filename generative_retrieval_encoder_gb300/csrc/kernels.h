@@ -189,6 +189,24 @@ struct GlrArgs {
   const int* err;
 };
 
+// AdamW over many tensors (adamw.cu).  A launch takes a table of tensors in its
+// parameters; its CTAs walk equal ranges of the table's units of kAdamUnit values.
+constexpr int kAdamBlock = 256;    // values that share a scale in the 8-bit states
+constexpr int kAdamUnit = 2048;    // values of a CTA's step: a block for each of its 8 warps
+struct AdamTensor {
+  void* param; float* master; const void* grad; void* m; void* v; float* ms; float* vs;
+  int64_t n;
+  int64_t place;                   // of its first value in the (256-padded) row of all tensors: seeds the rounding
+  int first;                       // its first unit in the table
+  float keep;                      // 1 - lr weight_decay
+  int pb, gb, vec;                 // param / grad in bf16; every pointer aligned for wide accesses
+};
+template <int N> struct AdamTable { AdamTensor t[N]; int n, units; };
+constexpr int kAdamFew = 36, kAdamMany = 336;  // table sizes: under 4 KB, and under 32 KB, of parameters
+// What a step's kernels read, formed once by the first of them.
+struct AdamScalars { float clip, b1, c1, b2, c2, step, inv, eps; uint32_t key; int go; };
+struct AdamStep { double lr, b1, b2, eps, max_norm; uint32_t seed; };
+
 // ---------------------------------------------------------------- launchers
 cudaError_t launch_plan(const SeqDesc& s, int ntile, const int* tile_sizes, int32_t* const* prefixes,
                         int* err, cudaStream_t st);
@@ -254,6 +272,14 @@ cudaError_t launch_decay_states(const DecayArgs& a, int n_chunks, cudaStream_t s
 cudaError_t launch_decay_scan(const DecayArgs& a, int n_seq, cudaStream_t st);
 cudaError_t launch_decay_out(const DecayArgs& a, int n_chunks, cudaStream_t st);
 constexpr int kDecayChunk = 128;  // rows per chunk of the decay core
+
+// The step's scalars into *s, the step count moved on.
+cudaError_t launch_adamw_begin(const AdamStep& c, int64_t* step, const float* norm, AdamScalars* s, cudaStream_t st);
+template <int N> cudaError_t launch_adamw(const AdamTable<N>& t, const AdamScalars* s, cudaStream_t st);
+// Sums of squares of the table's gradients: one fp64 partial for each of the launch's adamw_ctas(units) CTAs.
+int adamw_ctas(int64_t units);
+template <int N> cudaError_t launch_sumsq(const AdamTable<N>& t, double* part, cudaStream_t st);
+cudaError_t launch_norm(const double* part, int n, float* norm, cudaStream_t st);
 
 cudaError_t launch_glr_fwd(const GlrArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_glr_bwd(const GlrArgs& a, bool f32, cudaStream_t st);

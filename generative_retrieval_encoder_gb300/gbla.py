@@ -30,8 +30,10 @@ EXPORTS = ("gbla_workspace_size", "gbla_saved_size", "gbla_validate_shape", "gbl
            "gbla_last_error", "gbla_version", "gbla_profiling_enable", "gbla_profiling_read",
            "bla_core_forward_noalloc", "bla_core_noalloc_check_device_status", "gbla_diag_bounded_wait",
            "gbla_set_kernel_policy", "bla_decay_core_forward", "sa_core_forward",
-           "glr_forward", "glr_backward", "glr_saved_size")
+           "glr_forward", "glr_backward", "glr_saved_size", "gbla_adamw_workspace_size", "gbla_grad_norm",
+           "gbla_adamw_step")
 NOALLOC_SCRATCH_BYTES = 64 << 20
+ADAMW_BLOCK = 256
 
 
 class GblaError(RuntimeError):
@@ -48,6 +50,17 @@ class Shape(ctypes.Structure):
                 ("d_h", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
                 ("seq_lens", ctypes.c_void_p), ("io_dtype", ctypes.c_int), ("gate", ctypes.c_int),
                 ("rms_eps", ctypes.c_float)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("param_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("weight_decay", ctypes.c_double)]
+
+
+class AdamWConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("seed", ctypes.c_uint32)]
 
 
 _lib = None
@@ -87,6 +100,13 @@ def lib() -> ctypes.CDLL:
         L.glr_backward.restype = ctypes.c_int
         L.glr_saved_size.argtypes = [sp]
         L.glr_saved_size.restype = sz
+        tp = ctypes.POINTER(AdamWTensor)
+        L.gbla_adamw_workspace_size.argtypes = [tp, ctypes.c_int]
+        L.gbla_adamw_workspace_size.restype = sz
+        L.gbla_grad_norm.argtypes = [tp, ctypes.c_int, vp, vp, sz, vp]
+        L.gbla_grad_norm.restype = ctypes.c_int
+        L.gbla_adamw_step.argtypes = [tp, ctypes.c_int, ctypes.POINTER(AdamWConfig), vp, vp, vp, sz, vp]
+        L.gbla_adamw_step.restype = ctypes.c_int
         L.bla_core_forward_noalloc.argtypes = [sp] + [vp] * 8
         L.bla_core_forward_noalloc.restype = ctypes.c_int
         L.bla_core_noalloc_check_device_status.argtypes = [vp]
@@ -382,6 +402,148 @@ def glr_backward(shape: Shape, x, r, i, lam, saved, dy, c: float = 8.0, reverse:
                                 _ptr(g.get("dlam")), _ptr(g.get("dh0")), _ptr(ws), ws.numel(), _stream())
     _check(st, "glr_backward")
     return g
+
+
+_ADAMW_DTYPE = {torch.float32: GBLA_F32, torch.bfloat16: GBLA_BF16}
+
+
+def _named(tensors):
+    """(names or None, list) of a dict or a sequence of tensors."""
+    return (list(tensors), list(tensors.values())) if isinstance(tensors, dict) else (None, list(tensors))
+
+
+def gbla_adamw_state(params, bits: int = 32, master: bool | None = None) -> dict:
+    """The state of an AdamW run over params (a dict or a sequence), before its first step: step (int64 [1]), m and v per
+    parameter, fp32 (bits = 32) or e4m3 with m_scale and v_scale (bits = 8), and, where a parameter is bf16 (master =
+    False: nowhere), master, the fp32 copy it is rounded from."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits: 8 or 32, got {bits}")
+    P = _named(params)[1]
+    dev = P[0].device if P else torch.device("cuda", torch.cuda.current_device())
+    dt = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    zeros = lambda n, t: torch.zeros(n, dtype=torch.uint8 if t is torch.float8_e4m3fn else t, device=dev).view(t)  # noqa: E731
+    s = {"step": torch.zeros(1, dtype=torch.int64, device=dev), "m": [zeros(p.numel(), dt) for p in P],
+         "v": [zeros(p.numel(), dt) for p in P]}
+    if bits == 8:
+        for k in ("m_scale", "v_scale"):
+            s[k] = [zeros(-(-p.numel() // ADAMW_BLOCK), torch.float32) for p in P]
+    if master is not False:
+        s["master"] = [p.detach().float() if p.dtype == torch.bfloat16 else None for p in P]
+    return s
+
+
+class AdamWPlan:
+    """Which tensors an AdamW step updates, by which gradients and states (gbla_adamw_plan); it keeps them alive."""
+
+    def __init__(self, params, grads, state):
+        names, P = _named(params)
+        self.names, self.n, self.step = names, len(P), state["step"]
+        self.device = self.step.device
+        if self.step.dtype != torch.int64 or self.step.numel() != 1 or not self.step.is_cuda:
+            raise ValueError(f"step: want one int64 on a CUDA device, got {self.step.dtype} on {self.step.device}")
+        self.tensors = (AdamWTensor * self.n)()
+        self._written, self._keep, self._decay = [], [P, state], None
+        lists = {k: state.get(k) or [None] * self.n for k in ("m", "v", "m_scale", "v_scale", "master")}
+        for k, t in lists.items():
+            if len(t) != self.n:
+                raise ValueError(f"{k}: {len(t)} tensors for {self.n} parameters")
+        for j, p in enumerate(P):
+            name = names[j] if names else f"params[{j}]"
+            e, n = self.tensors[j], p.numel()
+            e.n = n
+            e.param, e.param_dtype = self._out(name, p, n, tuple(_ADAMW_DTYPE)), _ADAMW_DTYPE[p.dtype]
+            m, v, ms, vs, ma = (lists[k][j] for k in ("m", "v", "m_scale", "v_scale", "master"))
+            if (ms is None) != (vs is None) or m is None or v is None:
+                raise ValueError(f"{name}: want m and v, and both scales or neither")
+            kind = (torch.float32,) if ms is None else (torch.float8_e4m3fn,)
+            e.m, e.v = self._out(f"m of {name}", m, n, kind), self._out(f"v of {name}", v, n, kind)
+            if ms is not None:
+                e.m_scale = self._out(f"m_scale of {name}", ms, -(-n // ADAMW_BLOCK), (torch.float32,))
+                e.v_scale = self._out(f"v_scale of {name}", vs, -(-n // ADAMW_BLOCK), (torch.float32,))
+            if ma is not None:
+                if p.dtype != torch.bfloat16:
+                    raise ValueError(f"master of {name}: only a bf16 parameter has one")
+                e.master = self._out(f"master of {name}", ma, n, (torch.float32,))
+        self._written.append((self.step.data_ptr(), 8, "step"))
+        self._written.sort()
+        for (a, na, wa), (b, _, wb) in zip(self._written, self._written[1:]):
+            if a + na > b:
+                raise ValueError(f"{wa} and {wb} overlap")
+        self.set_grads(grads)
+        size = lib().gbla_adamw_workspace_size(self.tensors, self.n)
+        if size == 0:
+            _check(GBLA_ERR_INVALID_ARG, "gbla_adamw_workspace_size")
+        self.ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+
+    def _tensor(self, name, t, n, dtypes):
+        if t.dtype not in dtypes or t.numel() != n or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: want {n} contiguous values of {' or '.join(map(str, dtypes))} on {self.device}, got "
+                             f"{list(t.shape)} {t.dtype} on {t.device}")
+        return t.data_ptr()
+
+    def _out(self, name, t, n, dtypes):
+        at = self._tensor(name, t, n, dtypes)
+        if n:
+            self._written.append((at, n * t.element_size(), name))
+        return at
+
+    def set_grads(self, grads):
+        """Other gradient tensors for the same parameters: a sequence in their order, or a dict by their names (with or
+        without the leading d of gbla_backward's)."""
+        if isinstance(grads, dict):
+            if self.names is None:
+                raise ValueError("grads by name need params by name")
+            G = [grads["d" + k] if "d" + k in grads else grads[k] for k in self.names]
+        else:
+            G = list(grads)
+        if len(G) != self.n:
+            raise ValueError(f"{len(G)} gradients for {self.n} parameters")
+        at = [self._tensor(f"gradient {j}", g, self.tensors[j].n, tuple(_ADAMW_DTYPE)) for j, g in enumerate(G)]
+        for j, g in enumerate(G):
+            self.tensors[j].grad, self.tensors[j].grad_dtype = at[j], _ADAMW_DTYPE[g.dtype]
+        self._grads = G
+
+
+def gbla_adamw_plan(params, grads, state: dict) -> AdamWPlan:
+    """The plan of AdamW steps on params (a dict or a sequence of fp32 or bf16 tensors) by grads (fp32 or bf16; a dict
+    may be gbla_backward's) with a state of gbla_adamw_state.  Its workspace orders its calls on one stream."""
+    return AdamWPlan(params, grads, state)
+
+
+def gbla_grad_norm(plan: AdamWPlan, norm: torch.Tensor | None = None) -> torch.Tensor:
+    """The global 2-norm of the plan's gradients (fp32, on the device)."""
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=plan.device)
+    else:
+        plan._tensor("norm", norm, 1, (torch.float32,))
+    with _on(plan.device):
+        st = lib().gbla_grad_norm(plan.tensors, plan.n, _ptr(norm), _ptr(plan.ws), plan.ws.numel(), _stream())
+    _check(st, "gbla_grad_norm")
+    return norm
+
+
+def gbla_adamw_step(plan: AdamWPlan, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
+                    norm: torch.Tensor | None = None, max_norm: float | None = None, seed: int = 0) -> None:
+    """One AdamW step of the plan's tensors, in place (see gbla.h).  weight_decay: one value, or one per parameter; norm:
+    gbla_grad_norm's, which gradients are clipped by (max_norm) and which skips the step where it is not finite; seed: of
+    the 8-bit states' rounding."""
+    if norm is not None:
+        plan._tensor("norm", norm, 1, (torch.float32,))
+    if max_norm is not None and norm is None:
+        raise ValueError("max_norm needs norm (gbla_grad_norm)")
+    wd = tuple(weight_decay) if isinstance(weight_decay, (list, tuple)) else weight_decay
+    if wd != plan._decay:
+        each = wd if isinstance(wd, tuple) else (wd,) * plan.n
+        if len(each) != plan.n:
+            raise ValueError(f"weight_decay: {len(each)} values for {plan.n} parameters")
+        for j, w in enumerate(each):
+            plan.tensors[j].weight_decay = w
+        plan._decay = wd
+    cfg = AdamWConfig(lr, betas[0], betas[1], eps, max_norm or 0.0, seed)
+    with _on(plan.device):
+        st = lib().gbla_adamw_step(plan.tensors, plan.n, ctypes.byref(cfg), _ptr(plan.step), _ptr(norm), _ptr(plan.ws),
+                                   plan.ws.numel(), _stream())
+    _check(st, "gbla_adamw_step")
 
 
 def bla_core_forward_noalloc(shape: Shape, q, k, v, g, o, den=None, state=None) -> int:

@@ -279,6 +279,71 @@ gbla_status glr_backward(const gbla_shape* shape, const void* x, const void* r,
                          void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * AdamW over many tensors at once: the update of the parameters whose
+ * gradients gbla_backward and glr_backward return.  With t the step's number
+ * (from 1), g the gradient times the clip factor, in fp32 whatever the types:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps).
+ * A tensor's m and v are fp32 (m_scale = v_scale = NULL), or 8-bit: m and
+ * sqrt(v) as e4m3 values times an fp32 scale per block of
+ * GBLA_ADAMW_BLOCK consecutive values (the block's largest magnitude / 448;
+ * scale 0 and values 0 below 2^-100).  They are rounded up or down with the
+ * odds of the remainder, by a hash of (seed, t, the value's place), because v
+ * moves by a thousandth of itself a step and rounding to nearest would hold it
+ * still; a sqrt(v) above 0 does not become 0.  The same call with the same
+ * seed gives the same bits.  Zero-filled states (and scales) are the start.
+ */
+#define GBLA_ADAMW_BLOCK 256
+typedef struct {
+  void* param;        /* [n], param_dtype                                     */
+  float* master;      /* [n] or NULL: the fp32 values that a bf16 param is
+                         rounded from; without it bf16 values are updated     */
+  const void* grad;   /* [n], grad_dtype                                      */
+  void* m;            /* [n] fp32 or e4m3                                     */
+  void* v;            /* [n] fp32, or e4m3 sqrt(v)                            */
+  float* m_scale;     /* [ceil(n / GBLA_ADAMW_BLOCK)] or NULL: fp32 states    */
+  float* v_scale;     /* as m_scale                                           */
+  int64_t n;          /* values, >= 0                                         */
+  int param_dtype;    /* gbla_dtype                                           */
+  int grad_dtype;     /* gbla_dtype                                           */
+  double weight_decay;
+} gbla_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps; /* lr >= 0, 0 <= beta <= 0.9999999, eps >= 1e-30      */
+  double max_norm;    /* > 0, with `norm`: gradients are scaled by
+                         min(1, max_norm / (norm + 1e-6)); 0: no clipping     */
+  uint32_t seed;      /* of the 8-bit states' rounding                        */
+} gbla_adamw_config;
+
+/* Bytes of workspace that gbla_grad_norm and gbla_adamw_step need for these
+ * tensors (a host array; 0 on an argument error). */
+size_t gbla_adamw_workspace_size(const gbla_adamw_tensor* tensors, int n_tensors);
+
+/* The global 2-norm of the tensors' gradients into norm (fp32, device; one
+ * value).  Squares are summed in two fp32 words a thread and in fp64 beyond, in
+ * a fixed order; a square over the fp32 range counts as not finite.  Only grad,
+ * grad_dtype and n are read. */
+gbla_status gbla_grad_norm(const gbla_adamw_tensor* tensors, int n_tensors,
+                           float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* One AdamW step.
+ *   tensors  host array of n_tensors >= 0 entries (read during the call), whose
+ *            tensors do not overlap; pointers aligned to their element (16-byte
+ *            aligned ones are read in wider pieces)
+ *   step     int64, device: the steps taken so far; the call adds 1, so that a
+ *            captured and replayed call counts on
+ *   norm     NULL, or the device value of gbla_grad_norm: clips by max_norm; and
+ *            where it is not finite the call leaves everything, the step count
+ *            included, as it was
+ */
+gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors,
+                            const gbla_adamw_config* config, int64_t* step,
+                            const float* norm, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
  * bla_core_forward without a caller workspace (the pages have no counterpart:
  * this is a deployment convenience).  Some callers cannot call cudaMalloc or
  * hand the library a scratch buffer: a plugin running inside a host framework

@@ -1,0 +1,69 @@
+"""Host-side statuses and sizes of gbla_adamw_step and gbla_grad_norm (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from generative_retrieval_encoder_gb300 import build, gbla
+
+FAKE, ODD = 1 << 20, (1 << 20) + 1  # addresses, never dereferenced
+I, W, U, OK = gbla.GBLA_ERR_INVALID_ARG, gbla.GBLA_ERR_WORKSPACE, gbla.GBLA_ERR_UNSUPPORTED, gbla.GBLA_OK
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return gbla.lib()
+
+
+def tensors(count=2, **kw):
+    t = (gbla.AdamWTensor * count)()
+    for e in t:
+        for k, v in {**dict(param=FAKE, grad=FAKE, m=FAKE, v=FAKE, n=100), **kw}.items():
+            setattr(e, k, v)
+    return t
+
+
+def step(L, t, n=None, step=FAKE, norm=None, ws=FAKE, size=1 << 30, **cfg):
+    c = gbla.AdamWConfig(**{**dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, max_norm=0.0, seed=0), **cfg})
+    return L.gbla_adamw_step(t, len(t) if n is None else n, ctypes.byref(c), step, norm, ws, size, None)
+
+
+def test_step_host_errors(L):
+    for bad in (dict(param=None), dict(param=ODD), dict(grad=None), dict(grad=ODD), dict(m=None), dict(v=ODD), dict(param_dtype=2),
+                dict(grad_dtype=-1), dict(n=-1), dict(n=1 << 41), dict(master=FAKE), dict(m_scale=FAKE), dict(v_scale=FAKE),
+                dict(m_scale=ODD, v_scale=FAKE), dict(weight_decay=-1.0), dict(weight_decay=float("nan")),
+                dict(param_dtype=1, master=ODD)):
+        assert step(L, tensors(**bad)) == I, bad
+    for bad in (dict(lr=-1.0), dict(lr=float("nan")), dict(lr=float("inf")), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(eps=0.0),
+                dict(eps=float("nan")), dict(max_norm=-1.0), dict(max_norm=1.0), dict(max_norm=float("nan"), norm=FAKE), dict(step=None),
+                dict(step=FAKE + 4), dict(norm=ODD), dict(n=-1)):
+        assert step(L, tensors(), **bad) == I, bad
+    assert L.gbla_adamw_step(None, 1, None, FAKE, None, FAKE, 1 << 30, None) == I
+    assert L.gbla_adamw_step(tensors(), 2, None, FAKE, None, FAKE, 1 << 30, None) == I
+    size = L.gbla_adamw_workspace_size(tensors(), 2)
+    assert size > 0
+    assert step(L, tensors(), ws=None) == W and step(L, tensors(), ws=FAKE + 16) == W and step(L, tensors(), size=64) == W
+    assert step(L, tensors(300, n=1 << 40)) == U
+
+
+def test_norm_host_errors_and_sizes(L):
+    t = tensors(param=None, m=None, v=None)  # not read
+    assert L.gbla_grad_norm(t, 2, None, FAKE, 1 << 30, None) == I
+    assert L.gbla_grad_norm(t, 2, ODD, FAKE, 1 << 30, None) == I
+    assert L.gbla_grad_norm(t, -2, FAKE, FAKE, 1 << 30, None) == I
+    assert L.gbla_grad_norm(tensors(grad=ODD), 2, FAKE, FAKE, 1 << 30, None) == I
+    assert L.gbla_grad_norm(t, 2, FAKE, None, 1 << 30, None) == W
+    assert L.gbla_adamw_workspace_size(t, -1) == 0 and L.gbla_adamw_workspace_size(None, 3) == 0
+    assert L.gbla_adamw_workspace_size(tensors(n=-1), 2) == 0
+    big = tensors(400, n=1 << 20)
+    assert L.gbla_adamw_workspace_size(big, 400) > L.gbla_adamw_workspace_size(t, 2) > 0
+    assert L.gbla_adamw_workspace_size(None, 0) > 0
+
+
+def test_binding_refuses_host_tensors(L):
+    import torch
+    p = [torch.zeros(4)]
+    with pytest.raises(ValueError):
+        gbla.gbla_adamw_plan(p, p, {"step": torch.zeros(1, dtype=torch.int64), "m": p, "v": p})
+    with pytest.raises(ValueError):
+        gbla.gbla_adamw_state(p, bits=16)
