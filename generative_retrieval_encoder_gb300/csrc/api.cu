@@ -370,16 +370,23 @@ gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
   p.mode = s->cu_seqlens ? SEQ_VARLEN : (s->seq_lens ? SEQ_PADDED : SEQ_DENSE);
   p.n_seq = s->cu_seqlens ? s->num_seqs : s->B;
   if ((long long)p.n_seq * p.d > (1LL << 38)) return GBLA_ERR_UNSUPPORTED;  // one thread each
-  p.per_seq = p.mode != SEQ_VARLEN && p.L >= kGlrChunk ? cdiv(p.L, kGlrChunk) : 0;
+  p.per_seq = p.mode != SEQ_VARLEN && p.L >= kGlrSlot ? cdiv(p.L, kGlrChunk) : 0;
   p.n_chunks = p.per_seq ? p.per_seq * p.n_seq : cdiv(p.T, kGlrChunk);
+  if ((long long)p.n_chunks * cdiv(p.d, 64) > 0x7fffffffLL) return GBLA_ERR_UNSUPPORTED;  // one CTA each
   return GBLA_OK;
 }
 
-struct GlrLayout { size_t err, part, total; };
+size_t glr_dp(const GlrPlan& p) { return (size_t)cdiv(p.d, 64) * 64; }
+struct GlrLayout { size_t err, ticket, marks, words, zero_bytes, part, total; };
 GlrLayout glr_layout(const GlrPlan& p, int op) {
   Cursor c;
   GlrLayout l{};
-  l.err = c.take(16);
+  l.err = c.take(32);  // the error word, then the tile counter
+  l.ticket = l.err + 16;
+  if (p.mode == SEQ_VARLEN) l.marks = c.take((size_t)p.n_chunks * 8);
+  const size_t slots = p.per_seq ? p.n_seq : 1, n = p.per_seq ? p.per_seq : p.n_chunks;
+  l.words = c.take((p.n_chunks + slots * ((n + 15) / 16) + slots * ((n + 255) / 256)) * glr_dp(p) * 8);
+  l.zero_bytes = c.off;
   if (op == GBLA_OP_GLR_BACKWARD) l.part = c.take((size_t)p.n_seq * p.d * 4);
   l.total = c.off;
   return l;
@@ -417,17 +424,18 @@ gbla_status glr_begin(const gbla_shape* shape, int op, const void* x, const void
   a.seq.mode = p.mode; a.seq.n_seq = p.n_seq; a.seq.L = p.mode == SEQ_VARLEN ? p.T : p.L; a.seq.T = p.T;
   a.seq.lens = shape->seq_lens; a.seq.cu = shape->cu_seqlens;
   a.err = p.mode == SEQ_DENSE ? nullptr : c.err;
+  a.err_out = c.err;
+  a.ticket = at<unsigned long long>(ws, c.l.ticket);
+  a.marks = p.mode == SEQ_VARLEN ? at<uint64_t>(ws, c.l.marks) : nullptr;
+  a.words = at<uint64_t>(ws, c.l.words);
+  a.dp = (int64_t)glr_dp(p);
   return GBLA_OK;
 }
 
-// Clears the error word and checks the sequence data on the device.
+// Clears the error word, the tile counter, the marks and the scan's words; checks the sequence data on the device.
 gbla_status glr_check_seqs(GlrCtx& c) {
-  GBLA_CHECK(cudaMemsetAsync(c.err, 0, 16, c.st), "memset");
-  if (c.p.mode != SEQ_DENSE) {
-    const int ts[1] = {kGlrChunk};
-    int32_t* pre[1] = {nullptr};
-    GBLA_CHECK(launch_plan(c.a.seq, 0, ts, pre, c.err, c.st), "plan");
-  }
+  GBLA_CHECK(cudaMemsetAsync(c.err, 0, c.l.zero_bytes, c.st), "memset");
+  if (c.p.mode != SEQ_DENSE) GBLA_CHECK(launch_glr_prep(c.a, c.err, c.st), "plan");
   return GBLA_OK;
 }
 
@@ -1052,6 +1060,7 @@ gbla_status glr_forward(const gbla_shape* shape, const void* x, const void* r, c
   c.a.y = y; c.a.hT = hT; c.a.saved = static_cast<float*>(saved);
   if ((s = glr_check_seqs(c)) != GBLA_OK) return s;
   GBLA_CHECK(launch_glr_fwd(c.a, c.p.f32, c.st), "glr fwd");
+  if (hT && c.p.mode != SEQ_DENSE) GBLA_CHECK(launch_glr_empty(c.a, h0, hT, c.st), "glr empty");
   return GBLA_OK;
 }
 

@@ -169,9 +169,10 @@ struct DecayArgs {
 };
 
 // The gated linear recurrence (glr.cu).  Its rows are cut into chunks of
-// kGlrChunk: per sequence slot (per_seq chunks each, slots of at least a chunk)
-// or, for packed and short sequences, over all rows (per_seq = 0).
-constexpr int kGlrChunk = 64;
+// kGlrChunk: per sequence slot (per_seq chunks each; slots of at least kGlrSlot
+// rows, whose chunks then run side by side with the other slots') or, for packed
+// and short sequences, over all rows (per_seq = 0).
+constexpr int kGlrChunk = 64, kGlrSlot = 512;
 struct GlrArgs {
   const void* x; const void* r; const void* i; int64_t ld;  // [T, ld]
   const float* lam; float c;                                // [d]
@@ -186,7 +187,11 @@ struct GlrArgs {
   int d;
   SeqDesc seq;
   int per_seq, n_chunks;
+  const uint64_t* marks;                                    // packed sequences: bit r % 64 of word r / 64: row r begins one
+  uint64_t* words; int64_t dp;                              // the scan's words [chunks + groups + larger groups][dp], zero on entry
+  unsigned long long* ticket;                               // the next tile, zero on entry
   const int* err;
+  int* err_out;                                             // timeout bit of the workspace error word
 };
 
 // AdamW over many tensors (adamw.cu).  A launch takes a table of tensors in its
@@ -281,6 +286,10 @@ int adamw_ctas(int64_t units);
 template <int N> cudaError_t launch_sumsq(const AdamTable<N>& t, double* part, cudaStream_t st);
 cudaError_t launch_norm(const double* part, int n, float* norm, cudaStream_t st);
 
+// Checks the sequence data (error word *err) and marks the rows that begin a packed sequence.
+cudaError_t launch_glr_prep(const GlrArgs& a, int* err, cudaStream_t st);
+// to = from (or 0) for the sequences without tokens.
+cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st);
 cudaError_t launch_glr_fwd(const GlrArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_glr_bwd(const GlrArgs& a, bool f32, cudaStream_t st);
 
