@@ -377,16 +377,25 @@ gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
 }
 
 size_t glr_dp(const GlrPlan& p) { return (size_t)cdiv(p.d, 64) * 64; }
-struct GlrLayout { size_t err, ticket, marks, words, zero_bytes, part, total; };
+GlrTiles glr_tiles(const GlrPlan& p, int rows) {
+  GlrTiles t;
+  t.per_seq = p.per_seq ? cdiv(p.L, rows) : 0;
+  t.n_chunks = t.per_seq ? t.per_seq * p.n_seq : cdiv(p.T, rows);
+  return t;
+}
+struct GlrLayout { size_t err, ticket, marks, zero_bytes, kd, words, n_words, part, total; };
 GlrLayout glr_layout(const GlrPlan& p, int op) {
   Cursor c;
   GlrLayout l{};
   l.err = c.take(32);  // the error word, then the tile counter
   l.ticket = l.err + 16;
-  if (p.mode == SEQ_VARLEN) l.marks = c.take((size_t)p.n_chunks * 8);
-  const size_t slots = p.per_seq ? p.n_seq : 1, n = p.per_seq ? p.per_seq : p.n_chunks;
-  l.words = c.take((p.n_chunks + slots * ((n + 15) / 16) + slots * ((n + 255) / 256)) * glr_dp(p) * 8);
+  if (p.mode == SEQ_VARLEN) l.marks = c.take((size_t)cdiv(p.T, 64) * 8);
   l.zero_bytes = c.off;
+  l.kd = c.take(glr_dp(p) * 4);
+  const GlrTiles t = glr_tiles(p, kGlrRowsFwd);
+  const size_t slots = t.per_seq ? p.n_seq : 1, n = t.per_seq ? t.per_seq : t.n_chunks;
+  l.n_words = (t.n_chunks + slots * ((n + 15) / 16) + slots * ((n + 255) / 256)) * glr_dp(p);
+  l.words = c.take(l.n_words * 8);
   if (op == GBLA_OP_GLR_BACKWARD) l.part = c.take((size_t)p.n_seq * p.d * 4);
   l.total = c.off;
   return l;
@@ -428,14 +437,15 @@ gbla_status glr_begin(const gbla_shape* shape, int op, const void* x, const void
   a.ticket = at<unsigned long long>(ws, c.l.ticket);
   a.marks = p.mode == SEQ_VARLEN ? at<uint64_t>(ws, c.l.marks) : nullptr;
   a.words = at<uint64_t>(ws, c.l.words);
+  a.kd = at<float>(ws, c.l.kd);
   a.dp = (int64_t)glr_dp(p);
   return GBLA_OK;
 }
 
-// Clears the error word, the tile counter, the marks and the scan's words; checks the sequence data on the device.
+// Clears the error word, the tile counter, the marks and the scan's words, forms c softplus(lam); checks the sequence data on the device.
 gbla_status glr_check_seqs(GlrCtx& c) {
-  GBLA_CHECK(cudaMemsetAsync(c.err, 0, c.l.zero_bytes, c.st), "memset");
-  if (c.p.mode != SEQ_DENSE) GBLA_CHECK(launch_glr_prep(c.a, c.err, c.st), "plan");
+  if (c.p.mode != SEQ_DENSE) GBLA_CHECK(cudaMemsetAsync(c.err, 0, c.l.zero_bytes, c.st), "memset");
+  GBLA_CHECK(launch_glr_prep(c.a, (int64_t)c.l.n_words, c.err, c.st), "glr prep");
   return GBLA_OK;
 }
 
@@ -1059,7 +1069,7 @@ gbla_status glr_forward(const gbla_shape* shape, const void* x, const void* r, c
   if (saved && reinterpret_cast<uintptr_t>(saved) % kAlign) return GBLA_ERR_INVALID_ARG;
   c.a.y = y; c.a.hT = hT; c.a.saved = static_cast<float*>(saved);
   if ((s = glr_check_seqs(c)) != GBLA_OK) return s;
-  GBLA_CHECK(launch_glr_fwd(c.a, c.p.f32, c.st), "glr fwd");
+  GBLA_CHECK(launch_glr_fwd(c.a, glr_tiles(c.p, kGlrRowsFwd), c.p.f32, c.st), "glr fwd");
   if (hT && c.p.mode != SEQ_DENSE) GBLA_CHECK(launch_glr_empty(c.a, h0, hT, c.st), "glr empty");
   return GBLA_OK;
 }

@@ -50,96 +50,107 @@ __device__ __forceinline__ float dsoftplus_ratio(float l) {
   return l < -15.f ? 1.f : 1.f / ((1.f + expf(-l)) * softplus_f(l));
 }
 
-// The gates of one value: decay a, s, m = sqrt(1 - a^2) and s / m.
-struct Gate { float a, s, m, sm, sr; };
-__device__ __forceinline__ Gate gate_of(float r, float k) {
-  Gate g;
-  g.sr = sigmoid_f(r);
-  g.s = k * g.sr;
-  const float s = g.s;
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 e = mul2(x, two(-kLog2e));
+  const float2 d = add2(make_float2(ex2f(e.x), ex2f(e.y)), two(1.f));
+  return make_float2(rcpf(d.x), rcpf(d.y));
+}
+
+// The gates of two values with k = c softplus(lam): a, s, z = 1 - a^2.  SMALL: k < 1/4 for both, so s < 1/4 always.
+struct Gate2 { float2 a, s, z, sr; };
+template <bool SMALL>
+__device__ __forceinline__ Gate2 gate2(float2 r, float2 k) {
+  Gate2 g;
+  g.sr = sigmoid2(r);
+  g.s = mul2(k, g.sr);
+  const float2 s = g.s;
   // q = 1 - e^-s: the series up to s^6 below 1/4 (the next term is below 5e-8 of it)
-  float p = fmaf(s, -1.f / 720.f, 1.f / 120.f);
-  p = fmaf(s, p, -1.f / 24.f);
-  p = fmaf(s, p, 1.f / 6.f);
-  p = fmaf(s, p, -0.5f);
-  p = fmaf(s, p, 1.f);
-  const float e = ex2f(-kLog2e * s);
-  const float q = s < 0.25f ? s * p : 1.f - e;
-  g.a = s < 0.25f ? 1.f - q : e;
-  const float z = q * (2.f - q);
-  const float rs = z >= 1.2e-38f ? rsqf(z) : 0.f;
-  g.m = z * rs;
-  g.sm = s * rs;
+  float2 p = fma2(s, two(-1.f / 720.f), two(1.f / 120.f));
+  p = fma2(s, p, two(-1.f / 24.f));
+  p = fma2(s, p, two(1.f / 6.f));
+  p = fma2(s, p, two(-0.5f));
+  p = fma2(s, p, two(1.f));
+  float2 q = mul2(s, p);
+  g.a = add2(two(1.f), make_float2(-q.x, -q.y));
+  if (!SMALL) {
+    const float2 t = mul2(s, two(-kLog2e));
+    const float2 e = make_float2(ex2f(t.x), ex2f(t.y));
+    if (s.x >= 0.25f) { q.x = 1.f - e.x; g.a.x = e.x; }
+    if (s.y >= 0.25f) { q.y = 1.f - e.y; g.a.y = e.y; }
+  }
+  g.z = mul2(q, add2(two(2.f), make_float2(-q.x, -q.y)));
   return g;
+}
+__device__ __forceinline__ float sqf(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // ------------------------------------------------------------ chunks
-// The rows are cut into chunks of 64 (slots of at least kGlrSlot rows each into their own, everything else as one
-// stream), a chunk and 64 channels are a tile, a tile is one CTA's.  A chunk's rows are numbered in the direction of
-// the recurrence; F, E, V: the rows that are a sequence's first, its last, and in a sequence at all.
-struct Rows {
-  int64_t r0;       // physical first row
-  int nr;           // rows of the chunk
-  uint64_t F, E, V;
+// The rows are cut into chunks (slots of at least kGlrSlot rows each into their own, everything else as one stream); a
+// chunk and 64 channels are a tile, a tile is one CTA's, and a warp has PER neighbouring rows of it.  A chunk's rows
+// are numbered in the direction of the recurrence.
+struct Span {
+  int64_t r0;       // physical first row of the chunk
+  int nr;           // its rows
+  int64_t b;        // its slot (slots of their own)
+  int k;            // its first row in the slot
 };
-__device__ __forceinline__ Rows rows_of(const GlrArgs& a, int64_t chunk, int lane) {
-  Rows c;
-  uint64_t S, Z;
-  if (a.seq.mode == SEQ_VARLEN) {
-    c.r0 = chunk * kGlrChunk;
-    c.nr = (int)min((int64_t)kGlrChunk, a.seq.T - c.r0);
-    S = a.marks[chunk];
-    const uint64_t nxt = c.r0 + kGlrChunk < a.seq.T ? a.marks[chunk + 1] : 1;
-    c.V = c.nr == 64 ? ~0ull : (1ull << c.nr) - 1;
-    Z = (S >> 1) | (nxt << 63);
-    if (c.nr < 64) Z |= 1ull << (c.nr - 1);
+template <int CH>
+__device__ __forceinline__ Span span_of(const GlrArgs& a, int64_t chunk, int per_seq) {
+  Span c;
+  if (per_seq) {
+    c.b = chunk / per_seq;
+    c.k = (int)(chunk - c.b * per_seq) * CH;
+    c.r0 = c.b * a.seq.L + c.k;
+    c.nr = min(CH, a.seq.L - c.k);
   } else {
-    uint32_t v[2], s[2], z[2];
-    if (a.per_seq) {
-      const int64_t b = chunk / a.per_seq;
-      const int k = (int)(chunk - b * a.per_seq) * kGlrChunk;
-      c.r0 = b * a.seq.L + k;
-      c.nr = min(kGlrChunk, a.seq.L - k);
-      const int len = a.seq.mode == SEQ_PADDED ? a.seq.lens[b] : a.seq.L;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int pos = k + lane + 32 * q;
-        const bool in = pos < len;
-        v[q] = __ballot_sync(FULLM, in);
-        s[q] = __ballot_sync(FULLM, in && pos == 0);
-        z[q] = __ballot_sync(FULLM, in && pos == len - 1);
-      }
-    } else {
-      c.r0 = chunk * kGlrChunk;
-      c.nr = (int)min((int64_t)kGlrChunk, a.seq.T - c.r0);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int64_t row = c.r0 + lane + 32 * q;
-        const int b = (int)(row / a.seq.L), pos = (int)(row - (int64_t)b * a.seq.L);
-        const bool there = row < a.seq.T;
-        const int len = a.seq.mode == SEQ_PADDED ? (there ? a.seq.lens[b] : 0) : a.seq.L;
-        const bool in = there && pos < len;
-        v[q] = __ballot_sync(FULLM, in);
-        s[q] = __ballot_sync(FULLM, in && pos == 0);
-        z[q] = __ballot_sync(FULLM, in && pos == len - 1);
-      }
-    }
-    c.V = v[0] | (uint64_t)v[1] << 32;
-    S = s[0] | (uint64_t)s[1] << 32;
-    Z = z[0] | (uint64_t)z[1] << 32;
-  }
-  if (a.reverse) {
-    c.V = __brevll(c.V);
-    c.F = __brevll(Z);
-    c.E = __brevll(S);
-  } else {
-    c.F = S;
-    c.E = Z;
+    c.b = c.k = 0;
+    c.r0 = chunk * CH;
+    c.nr = (int)min((int64_t)CH, a.seq.T - c.r0);
   }
   return c;
 }
-__device__ __forceinline__ int64_t row_at(const GlrArgs& a, const Rows& c, int j) {
-  return a.reverse ? c.r0 + 63 - j : c.r0 + j;
+template <int CH>
+__device__ __forceinline__ int64_t row_at(const GlrArgs& a, const Span& c, int j) {
+  return a.reverse ? c.r0 + CH - 1 - j : c.r0 + j;
+}
+// Bits of the N <= 32 rows from j0 on: in the chunk, in a sequence, a sequence's first, its last (in the direction of the
+// recurrence).  Whole warps call it.
+struct Flags { uint32_t in, V, F, E; };
+template <int CH, int N>
+__device__ __forceinline__ Flags flags_of(const GlrArgs& a, const Span& c, int per_seq, int j0, int lane) {
+  const int j = j0 + min(lane, N - 1), p = a.reverse ? CH - 1 - j : j;  // place in the chunk
+  const bool in = p < c.nr;
+  bool v = in, s, z;
+  const int64_t row = c.r0 + p;
+  if (a.seq.mode == SEQ_VARLEN) {
+    s = in && (a.marks[row >> 6] >> (row & 63) & 1);
+    z = in && (row + 1 == a.seq.T || (a.marks[(row + 1) >> 6] >> ((row + 1) & 63) & 1));
+  } else {
+    int64_t b = c.b;
+    int pos = c.k + p;
+    if (!per_seq) {
+      b = (int)row / a.seq.L;
+      pos = (int)row - (int)b * a.seq.L;
+    }
+    const int len = a.seq.mode == SEQ_PADDED ? (in ? a.seq.lens[b] : 0) : a.seq.L;
+    v = in && pos < len;
+    s = v && pos == 0;
+    z = v && pos == len - 1;
+  }
+  const uint32_t m = N == 32 ? ~0u : (1u << N) - 1;
+  Flags f;
+  f.in = __ballot_sync(FULLM, in) & m;
+  f.V = __ballot_sync(FULLM, v) & m;
+  f.F = __ballot_sync(FULLM, a.reverse ? z : s) & m;
+  f.E = __ballot_sync(FULLM, a.reverse ? s : z) & m;
+  return f;
 }
 // The sequence of a row that is in one.
 __device__ __forceinline__ int seq_of(const GlrArgs& a, int64_t row) {
@@ -204,17 +215,18 @@ __device__ __forceinline__ void await(const uint64_t* p, uint64_t& x, uint64_t& 
 
 // The words of a call: of chunks, groups and larger groups, each [..][dp] with dp the channels rounded up to 64.
 struct Chain {
-  const uint64_t* chunk; const uint64_t* group; const uint64_t* large;
-  int k;            // this chunk's place in its chain
+  uint64_t* chunk; uint64_t* group; uint64_t* large;
+  int k, last;      // this chunk's place in its chain, and the last one
 };
-__device__ __forceinline__ Chain chain_of(const GlrArgs& a, int64_t s, int k, int ch) {
+__device__ __forceinline__ Chain chain_of(const GlrArgs& a, const GlrTiles& t, int64_t s, int k, int ch) {
   // s: the sequence slot (0 for a stream); the arrays hold each slot's words in the order of its chain
-  const int64_t n = a.per_seq ? a.per_seq : a.n_chunks, ng = (n + 15) >> 4, nl = (n + 255) >> 8;
+  const int64_t n = t.per_seq ? t.per_seq : t.n_chunks, ng = (n + 15) >> 4, nl = (n + 255) >> 8;
   Chain c;
   c.chunk = a.words + (s * n) * a.dp + ch;
-  c.group = a.words + ((int64_t)a.n_chunks + s * ng) * a.dp + ch;
-  c.large = a.words + ((int64_t)a.n_chunks + (int64_t)(a.per_seq ? a.seq.n_seq : 1) * ng + s * nl) * a.dp + ch;
+  c.group = a.words + ((int64_t)t.n_chunks + s * ng) * a.dp + ch;
+  c.large = a.words + ((int64_t)t.n_chunks + (int64_t)(t.per_seq ? a.seq.n_seq : 1) * ng + s * nl) * a.dp + ch;
   c.k = k;
+  c.last = (int)n - 1;
   return c;
 }
 // Warp w's share, composed, of the words that chunk k reads: warps 0-3 the larger group's state and the groups before,
@@ -274,154 +286,175 @@ __device__ __forceinline__ void store2(void* base, int64_t o, int n, float2 v) {
   if (n > 1) p[1] = from_f<T>(v.y);
 }
 
-constexpr int kWarps = 8, kPer = kGlrChunk / kWarps;  // a warp's rows; a lane has two channels of each
+constexpr int kWarps = 8;
+constexpr int kPerF = kGlrRowsFwd / kWarps;  // a warp's rows; a lane has two channels of each
 
-// The tile of this CTA: channels from *ch0, chunk (physical) *chunk, slot *s and place *k in its chain.
-__device__ __forceinline__ void tile_of(const GlrArgs& a, unsigned long long t, bool back, int& ch0, int64_t& chunk, int64_t& s, int& k) {
+// Tile t: channels from ch0, chunk (physical), slot s and place k in its chain.
+__device__ __forceinline__ void tile_of(const GlrArgs& a, const GlrTiles& g, unsigned long long t, bool back, int& ch0, int64_t& chunk, int64_t& s, int& k) {
   const unsigned ncg = (unsigned)(a.dp >> 6);
-  ch0 = (int)(t % ncg) * 64;
-  t /= ncg;
-  if (a.per_seq) {
-    s = (int64_t)(t % (unsigned)a.seq.n_seq);
-    k = (int)(t / (unsigned)a.seq.n_seq);
-    chunk = s * a.per_seq + (back ? a.per_seq - 1 - k : k);
+  const unsigned u = (unsigned)t;  // tiles are counted in 31 bits
+  ch0 = (int)(u % ncg) * 64;
+  const unsigned w = u / ncg;
+  if (g.per_seq) {
+    const unsigned q = w / (unsigned)a.seq.n_seq;
+    s = w - q * (unsigned)a.seq.n_seq;
+    k = (int)q;
+    chunk = s * g.per_seq + (back ? g.per_seq - 1 - k : k);
   } else {
     s = 0;
-    k = (int)t;
-    chunk = back ? a.n_chunks - 1 - k : k;
+    k = (int)w;
+    chunk = back ? g.n_chunks - 1 - k : k;
   }
 }
 
+// What a warp's rows do, in shared memory: {A, H} of two channels; A = -1: a sequence starts in them.
+__device__ __forceinline__ float4 pack_map(const Map& x, const Map& y) {
+  return make_float4(x.reset ? -1.f : x.A, x.H, y.reset ? -1.f : y.A, y.H);
+}
+__device__ __forceinline__ void then4(Map& x, Map& y, const float4& g) {
+  x = then(x, Map{g.x, g.y, g.x == -1.f});
+  y = then(y, Map{g.z, g.w, g.z == -1.f});
+}
+
+// The lane's rows of a tile: decays and what they add, and what they do together.
+template <typename T, bool VEC, bool SMALL, int PER, int CH>
+__device__ __forceinline__ void local_rows(const GlrArgs& a, const Span& c, const Flags& f, int j0, int ch, int nch, float2 ka,
+                                           float2 (&da)[PER], float2 (&u)[PER], Map& mx, Map& my) {
+  float2 x[PER], r[PER], i[PER];
+  const int64_t step = a.reverse ? -a.ld : a.ld;
+  int64_t o = row_at<CH>(a, c, j0) * a.ld + ch;
+#pragma unroll
+  for (int q = 0; q < PER; ++q, o += step) {
+    const int n = f.V >> q & 1 ? nch : 0;
+    r[q] = load2<T, VEC>(a.r, o, n);
+    i[q] = load2<T, VEC>(a.i, o, n);
+    x[q] = load2<T, VEC>(a.x, o, n);
+  }
+  float2 A = two(1.f), H = two(0.f);
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const Gate2 g = gate2<SMALL>(r[q], ka);
+    da[q] = g.a;
+    u[q] = mul2(make_float2(sqf(g.z.x), sqf(g.z.y)), mul2(sigmoid2(i[q]), x[q]));
+    if (!(f.V >> q & 1)) {
+      da[q] = two(1.f);
+      u[q] = two(0.f);
+    }
+    if (f.F >> q & 1) {
+      if (a.h0) {
+        const int64_t oh = (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch;
+        if (nch > 0) u[q].x = fmaf(da[q].x, a.h0[oh], u[q].x);
+        if (nch > 1) u[q].y = fmaf(da[q].y, a.h0[oh + 1], u[q].y);
+      }
+      H = u[q];
+    } else {
+      H = fma2(da[q], H, u[q]);
+      A = mul2(A, da[q]);
+    }
+  }
+  mx = Map{A.x, H.x, f.F != 0};
+  my = Map{A.y, H.y, f.F != 0};
+}
+
+// Forward.  Bound by the instructions of the gates (the special function unit has 5 of them a value) and by memory: one
+// pass, x, r and i read once and y written once.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_glr_fwd(const GlrArgs a) {
-  __shared__ float4 agg[kWarps][32];       // {A, H} of each warp's rows, two channels
-  __shared__ float4 back[kWarps][32];      // of each warp's share of the words before
-  __shared__ int back_reset[kWarps];
+__global__ void __launch_bounds__(256, 2) k_glr_fwd(const GlrArgs a, const GlrTiles tl) {
+  constexpr int PER = kPerF, CH = kGlrRowsFwd;
+  __shared__ float4 agg[kWarps][32];
+  __shared__ float4 back[kWarps][32];      // each warp's share of the words before
+  __shared__ float2 enter[kWarps][32];     // the state that enters each warp's rows
   __shared__ unsigned long long tile_s;
+  pdl_enter();
   if (a.err && *a.err) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) tile_s = atomicAdd(a.ticket, 1ull);
   __syncthreads();
   int ch, k;
   int64_t chunk, slot;
-  tile_of(a, tile_s, a.reverse, ch, chunk, slot, k);
+  tile_of(a, tl, tile_s, a.reverse, ch, chunk, slot, k);
   ch += 2 * lane;
-  const int nch = a.d - ch;  // channels of this lane: 2, 1 or none
-  const Rows c = rows_of(a, chunk, lane);
+  const int nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
+  const Span c = span_of<CH>(a, chunk, tl.per_seq);
+  const int j0 = warp * PER;
+  const Flags f = flags_of<CH, PER>(a, c, tl.per_seq, j0, lane);
+  const float2 ka = *(const float2*)(a.kd + ch);
+  float2 da[PER], u[PER];
+  Map mx, my;
+  if (__all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f))
+    local_rows<T, VEC, true, PER, CH>(a, c, f, j0, ch, nch, ka, da, u, mx, my);
+  else
+    local_rows<T, VEC, false, PER, CH>(a, c, f, j0, ch, nch, ka, da, u, mx, my);
+  agg[warp][lane] = pack_map(mx, my);
+  // whether the chunk's first row begins a sequence: then nothing enters
+  const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && k > 0;
 
-  // the lane's rows: a and u
-  float2 ka = make_float2(0.f, 0.f);
-  if (nch > 0) ka.x = a.c * softplus_f(a.lam[ch]);
-  if (nch > 1) ka.y = a.c * softplus_f(a.lam[ch + 1]);
-  const int j0 = warp * kPer;
-  const uint32_t V = (uint32_t)(c.V >> j0) & 0xffu, F = (uint32_t)(c.F >> j0) & 0xffu, E = (uint32_t)(c.E >> j0) & 0xffu;
-  float2 x[kPer], r[kPer], i[kPer];
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int64_t o = row_at(a, c, j0 + q) * a.ld + ch;
-    const int n = V >> q & 1 ? nch : 0;
-    r[q] = load2<T, VEC>(a.r, o, n);
-    i[q] = load2<T, VEC>(a.i, o, n);
-    x[q] = load2<T, VEC>(a.x, o, n);
-  }
-  float2 da[kPer], u[kPer];
-  Map mx{1.f, 0.f, false}, my{1.f, 0.f, false};
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const Gate gx = gate_of(r[q].x, ka.x), gy = gate_of(r[q].y, ka.y);
-    da[q] = make_float2(gx.a, gy.a);
-    u[q] = make_float2(gx.m * sigmoid_f(i[q].x) * x[q].x, gy.m * sigmoid_f(i[q].y) * x[q].y);
-    if (!(V >> q & 1)) {
-      da[q] = make_float2(1.f, 1.f);
-      u[q] = make_float2(0.f, 0.f);
-    }
-    if (F >> q & 1) {
-      if (a.h0) {
-        const int64_t o = (int64_t)seq_of(a, row_at(a, c, j0 + q)) * a.d + ch;
-        if (nch > 0) u[q].x = fmaf(da[q].x, a.h0[o], u[q].x);
-        if (nch > 1) u[q].y = fmaf(da[q].y, a.h0[o + 1], u[q].y);
-      }
-      mx.H = u[q].x;
-      my.H = u[q].y;
-      mx.reset = my.reset = true;
-    } else {
-      mx.H = fmaf(da[q].x, mx.H, u[q].x);
-      my.H = fmaf(da[q].y, my.H, u[q].y);
-      mx.A *= da[q].x;
-      my.A *= da[q].y;
-    }
-  }
-  agg[warp][lane] = make_float4(mx.A, mx.H, my.A, my.H);
-  __syncthreads();
-
-  // what the warps before do together
-  Map px{1.f, 0.f, false}, py{1.f, 0.f, false};
-  for (int w = 0; w < warp; ++w) {
-    const float4 g = agg[w][lane];
-    const bool rs = (c.F >> (w * kPer) & 0xff) != 0;
-    px = then(px, Map{g.x, g.y, rs});
-    py = then(py, Map{g.z, g.w, rs});
-  }
-  const Chain chain = chain_of(a, slot, k, ch);
-  const int64_t last = a.per_seq ? a.per_seq : a.n_chunks;
-  Map tx, ty;
+  const Chain chain = chain_of(a, tl, slot, k, ch);
+  Map tx{1.f, 0.f, false}, ty{1.f, 0.f, false};
   if (warp == kWarps - 1) {
-    tx = then(px, mx);
-    ty = then(py, my);
-    if (k + 1 < last) publish(const_cast<uint64_t*>(chain.chunk) + (int64_t)k * a.dp, tx, ty);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) then4(tx, ty, agg[w][lane]);
+    if (k < chain.last) publish(chain.chunk + (int64_t)k * a.dp, tx, ty);
   }
-  // the state that enters, where the chunk does not begin with a sequence
-  const int first = __ffsll(c.V) - 1;
-  const bool need = first >= 0 && !(c.F >> first & 1);
-  float2 in = make_float2(0.f, 0.f);
   if (need) {
     Map bx, by;
     look_back(chain, a.dp, warp, a.err_out, bx, by);
-    back[warp][lane] = make_float4(bx.A, bx.H, by.A, by.H);
-    if (lane == 0) back_reset[warp] = bx.reset;
+    back[warp][lane] = pack_map(bx, by);
     __syncthreads();
-    Map sx{1.f, 0.f, false}, sy{1.f, 0.f, false};
+  }
+  if (warp == kWarps - 1) {
+    Map sx{1.f, 0.f, false}, sy{1.f, 0.f, false}, gx = sx, gy = sy;
+    if (need) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) then4(sx, sy, back[w][lane]);
+#pragma unroll
+      for (int w = 4; w < 8; ++w) then4(gx, gy, back[w][lane]);
+      sx = then(sx, gx);
+      sy = then(sy, gy);
+    }
+    float2 h = need ? make_float2(sx.H, sy.H) : two(0.f);
+    if ((k & 15) == 15 && k < chain.last) {
+      publish(chain.group + (int64_t)(k >> 4) * a.dp, then(gx, tx), then(gy, ty));
+      if ((k & 255) == 255) {
+        const Map lx{0.f, tx.reset ? tx.H : fmaf(tx.A, h.x, tx.H), true}, ly{0.f, ty.reset ? ty.H : fmaf(ty.A, h.y, ty.H), true};
+        publish(chain.large + (int64_t)(k >> 8) * a.dp, lx, ly);
+      }
+    }
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float4 g = back[w][lane];
-      const bool rs = back_reset[w];
-      sx = then(sx, Map{g.x, g.y, rs});
-      sy = then(sy, Map{g.z, g.w, rs});
-    }
-    in = make_float2(sx.H, sy.H);
-    if (a.saved && warp == 0) store2<float, false>(a.saved, chunk * a.d + ch, nch, in);
-  }
-  if (warp == kWarps - 1 && (k & 15) == 15 && k + 1 < last) {
-    Map gx{1.f, 0.f, false}, gy{1.f, 0.f, false};
-    if (need)
-      for (int w = 4; w < 8; ++w) {
-        const float4 g = back[w][lane];
-        gx = then(gx, Map{g.x, g.y, back_reset[w] != 0});
-        gy = then(gy, Map{g.z, g.w, back_reset[w] != 0});
+      enter[w][lane] = h;
+      // the backward's chunks are of kGlrChunk rows
+      if (a.saved && (w * PER) % kGlrChunk == 0) {
+        const int p = a.reverse ? CH - kGlrChunk - w * PER : w * PER;  // physical place of the piece in the chunk
+        if (p < c.nr) {
+          const int64_t piece = tl.per_seq ? c.b * a.per_seq + (c.k + p) / kGlrChunk : (c.r0 + p) / kGlrChunk;
+          store2<float, false>(a.saved, piece * a.d + ch, nch, h);
+        }
       }
-    publish(const_cast<uint64_t*>(chain.group) + (int64_t)(k >> 4) * a.dp, then(gx, tx), then(gy, ty));
-    if ((k & 255) == 255)
-      publish(const_cast<uint64_t*>(chain.large) + (int64_t)(k >> 8) * a.dp, Map{0.f, tx.reset ? tx.H : fmaf(tx.A, in.x, tx.H), true},
-              Map{0.f, ty.reset ? ty.H : fmaf(ty.A, in.y, ty.H), true});
-  }
-  // the rows again, from the state that enters them
-  float2 h = make_float2(px.reset ? px.H : fmaf(px.A, in.x, px.H), py.reset ? py.H : fmaf(py.A, in.y, py.H));
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int j = j0 + q;
-    const int64_t row = row_at(a, c, j);
-    if (F >> q & 1) {
-      h = u[q];
-    } else {
-      h.x = fmaf(da[q].x, h.x, u[q].x);
-      h.y = fmaf(da[q].y, h.y, u[q].y);
+      const float4 g = agg[w][lane];
+      h = make_float2(g.x == -1.f ? g.y : fmaf(g.x, h.x, g.y), g.z == -1.f ? g.w : fmaf(g.z, h.y, g.w));
     }
-    const bool in_chunk = (a.reverse ? 63 - j : j) < c.nr;
-    store2<T, VEC>(a.y, row * a.d + ch, in_chunk ? nch : 0, V >> q & 1 ? h : make_float2(0.f, 0.f));
-    if (a.hT && (E >> q & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row) * a.d + ch, nch, h);
+  }
+  __syncthreads();
+  // the rows again, from the state that enters them
+  float2 h = enter[warp][lane];
+  const int64_t step = a.reverse ? -a.d : a.d;
+  int64_t o = row_at<CH>(a, c, j0) * a.d + ch;
+#pragma unroll
+  for (int q = 0; q < PER; ++q, o += step) {
+    if (f.F >> q & 1) h = u[q];
+    else h = fma2(da[q], h, u[q]);
+    store2<T, VEC>(a.y, o, f.in >> q & 1 ? nch : 0, f.V >> q & 1 ? h : two(0.f));
+    if (a.hT && (f.E >> q & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch, h);
   }
 }
 
+struct Gate { float a, s, m, sm, sr; };
+__device__ __forceinline__ Gate gate_of(float r, float k) {
+  const Gate2 v = gate2<false>(two(r), two(k));
+  const float rs = v.z.x >= 1.2e-38f ? rsqf(v.z.x) : 0.f;
+  return Gate{v.a.x, v.s.x, v.z.x * rs, v.s.x * rs, v.sr.x};
+}
 // Sequence b's first row and valid rows.
 __device__ __forceinline__ void seq_rows(const SeqDesc& s, int b, int64_t& row0, int& n) {
   if (s.mode == SEQ_VARLEN) {
@@ -496,20 +529,30 @@ __global__ void __launch_bounds__(256) k_glr_bwd(const GlrArgs a) {
     }
 }
 
-// Checks the sequence data and, for packed sequences, marks the rows that begin one.
-__global__ void __launch_bounds__(256) k_glr_prep(const GlrArgs a, int* err) {
-  const int b = blockIdx.x * 256 + threadIdx.x;
-  if (b >= a.seq.n_seq) return;
-  if (a.seq.mode == SEQ_PADDED) {
-    if (a.seq.lens[b] < 0 || a.seq.lens[b] > a.seq.L) atomicOr(err, 1);
-    return;
+// c softplus(lam), the scan's words and the tile counter cleared; checks the sequence data and, for packed sequences,
+// marks the rows that begin one (the error word and the marks are 0 on entry).
+__global__ void __launch_bounds__(256) k_glr_prep(const GlrArgs a, int64_t words, int* err) {
+  pdl_enter();
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)gridDim.x * 256;
+  if (id == 0) {
+    *a.ticket = 0;
+    if (a.seq.mode == SEQ_DENSE) *err = 0;
   }
-  const int lo = a.seq.cu[b], hi = a.seq.cu[b + 1];
-  if (lo < 0 || hi < lo || hi > a.seq.T || (b == 0 && lo != 0) || (b == a.seq.n_seq - 1 && hi != a.seq.T)) {
-    atomicOr(err, 1);
-    return;
+  for (int64_t i = id; i < a.dp; i += n) a.kd[i] = i < a.d ? a.c * softplus_f(a.lam[i]) : 0.f;
+  for (int64_t i = id; i < words / 2; i += n) ((ulonglong2*)a.words)[i] = make_ulonglong2(0, 0);
+  if (a.seq.mode == SEQ_DENSE) return;
+  for (int64_t b = id; b < a.seq.n_seq; b += n) {
+    if (a.seq.mode == SEQ_PADDED) {
+      if (a.seq.lens[b] < 0 || a.seq.lens[b] > a.seq.L) atomicOr(err, 1);
+      continue;
+    }
+    const int lo = a.seq.cu[b], hi = a.seq.cu[b + 1];
+    if (lo < 0 || hi < lo || hi > a.seq.T || (b == 0 && lo != 0) || (b == a.seq.n_seq - 1 && hi != a.seq.T)) {
+      atomicOr(err, 1);
+      continue;
+    }
+    if (lo < hi) atomicOr((unsigned long long*)a.marks + (lo >> 6), 1ull << (lo & 63));
   }
-  if (lo < hi) atomicOr((unsigned long long*)a.marks + lo / kGlrChunk, 1ull << (lo % kGlrChunk));
 }
 
 // A sequence without tokens hands its state on.
@@ -534,25 +577,20 @@ bool pairs_ok(const GlrArgs& a, size_t es) {
 }
 }  // namespace
 
-cudaError_t launch_glr_prep(const GlrArgs& a, int* err, cudaStream_t st) {
-  k_glr_prep<<<(unsigned)((a.seq.n_seq + 255) / 256), 256, 0, st>>>(a, err);
-  return cudaGetLastError();
+cudaError_t launch_glr_prep(const GlrArgs& a, int64_t words, int* err, cudaStream_t st) {
+  const int64_t n = std::max<int64_t>(std::max<int64_t>(words / 2, a.dp), a.seq.mode == SEQ_DENSE ? 1 : a.seq.n_seq);
+  const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sm_count() * 8);
+  return launch_pdl(k_glr_prep, dim3(grid), dim3(256), 0, st, a, words, err);
 }
 cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st) {
   k_glr_empty<<<(unsigned)std::min(a.seq.n_seq, 4096), 256, 0, st>>>(a, from, to);
   return cudaGetLastError();
 }
 
-cudaError_t launch_glr_fwd(const GlrArgs& a, bool f32, cudaStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.n_chunks * (a.dp >> 6));
-  if (f32) {
-    if (pairs_ok(a, 4)) k_glr_fwd<float, true><<<grid, 256, 0, st>>>(a);
-    else k_glr_fwd<float, false><<<grid, 256, 0, st>>>(a);
-  } else {
-    if (pairs_ok(a, 2)) k_glr_fwd<bf16, true><<<grid, 256, 0, st>>>(a);
-    else k_glr_fwd<bf16, false><<<grid, 256, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+cudaError_t launch_glr_fwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st) {
+  const dim3 grid((unsigned)((int64_t)t.n_chunks * (a.dp >> 6)));
+  if (f32) return launch_pdl(pairs_ok(a, 4) ? k_glr_fwd<float, true> : k_glr_fwd<float, false>, grid, dim3(256), 0, st, a, t);
+  return launch_pdl(pairs_ok(a, 2) ? k_glr_fwd<bf16, true> : k_glr_fwd<bf16, false>, grid, dim3(256), 0, st, a, t);
 }
 
 cudaError_t launch_glr_bwd(const GlrArgs& a, bool f32, cudaStream_t st) {

@@ -173,6 +173,9 @@ struct DecayArgs {
 // rows, whose chunks then run side by side with the other slots') or, for packed
 // and short sequences, over all rows (per_seq = 0).
 constexpr int kGlrChunk = 64, kGlrSlot = 512;
+// Rows of a tile of the forward (a state is saved every kGlrChunk of them).
+constexpr int kGlrRowsFwd = 128;
+struct GlrTiles { int per_seq, n_chunks; };  // chunks of a slot (0: one stream), of the call
 struct GlrArgs {
   const void* x; const void* r; const void* i; int64_t ld;  // [T, ld]
   const float* lam; float c;                                // [d]
@@ -190,6 +193,7 @@ struct GlrArgs {
   const uint64_t* marks;                                    // packed sequences: bit r % 64 of word r / 64: row r begins one
   uint64_t* words; int64_t dp;                              // the scan's words [chunks + groups + larger groups][dp], zero on entry
   unsigned long long* ticket;                               // the next tile, zero on entry
+  float* kd;                                                // [dp]: c softplus(lam)
   const int* err;
   int* err_out;                                             // timeout bit of the workspace error word
 };
@@ -287,10 +291,11 @@ template <int N> cudaError_t launch_sumsq(const AdamTable<N>& t, double* part, c
 cudaError_t launch_norm(const double* part, int n, float* norm, cudaStream_t st);
 
 // Checks the sequence data (error word *err) and marks the rows that begin a packed sequence.
-cudaError_t launch_glr_prep(const GlrArgs& a, int* err, cudaStream_t st);
+// Also forms a.kd and clears `words` words and the tile counter.
+cudaError_t launch_glr_prep(const GlrArgs& a, int64_t words, int* err, cudaStream_t st);
 // to = from (or 0) for the sequences without tokens.
 cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st);
-cudaError_t launch_glr_fwd(const GlrArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_glr_fwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st);
 cudaError_t launch_glr_bwd(const GlrArgs& a, bool f32, cudaStream_t st);
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, bool f32, cudaStream_t st, int* tiled = nullptr);
