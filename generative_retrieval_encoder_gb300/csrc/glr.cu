@@ -18,8 +18,8 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "mbarrier.cuh"
 #include "pdl.cuh"
+#include "tcgen05.cuh"
 
 namespace gbla {
 namespace {
@@ -289,22 +289,28 @@ __device__ __forceinline__ void store2(void* base, int64_t o, int n, float2 v) {
 constexpr int kWarps = 8;
 constexpr int kPerF = kGlrRowsFwd / kWarps;  // a warp's rows; a lane has two channels of each
 
-// Tile t: channels from ch0, chunk (physical), slot s and place k in its chain.
-__device__ __forceinline__ void tile_of(const GlrArgs& a, const GlrTiles& g, unsigned long long t, bool back, int& ch0, int64_t& chunk, int64_t& s, int& k) {
+// How a tile's rows are read: copied ahead into shared memory (rows of 16-byte pieces), or straight into registers by
+// pairs of channels or single ones.
+enum GlrLoad { GLR_TMA = 0, GLR_PAIRS = 1, GLR_SINGLE = 2 };
+
+// A tile: channels from ch0, chunk (physical), slot and place k in its chain.
+struct Tile { int ch0, k; int64_t chunk, slot; };
+__device__ __forceinline__ Tile tile_of(const GlrArgs& a, const GlrTiles& g, unsigned t, bool back) {
   const unsigned ncg = (unsigned)(a.dp >> 6);
-  const unsigned u = (unsigned)t;  // tiles are counted in 31 bits
-  ch0 = (int)(u % ncg) * 64;
-  const unsigned w = u / ncg;
+  Tile o;
+  o.ch0 = (int)(t % ncg) * 64;
+  const unsigned w = t / ncg;
   if (g.per_seq) {
     const unsigned q = w / (unsigned)a.seq.n_seq;
-    s = w - q * (unsigned)a.seq.n_seq;
-    k = (int)q;
-    chunk = s * g.per_seq + (back ? g.per_seq - 1 - k : k);
+    o.slot = w - q * (unsigned)a.seq.n_seq;
+    o.k = (int)q;
+    o.chunk = o.slot * g.per_seq + (back ? g.per_seq - 1 - o.k : o.k);
   } else {
-    s = 0;
-    k = (int)w;
-    chunk = back ? g.n_chunks - 1 - k : k;
+    o.slot = 0;
+    o.k = (int)w;
+    o.chunk = back ? g.n_chunks - 1 - o.k : o.k;
   }
+  return o;
 }
 
 // What a warp's rows do, in shared memory: {A, H} of two channels; A = -1: a sequence starts in them.
@@ -316,136 +322,213 @@ __device__ __forceinline__ void then4(Map& x, Map& y, const float4& g) {
   y = then(y, Map{g.z, g.w, g.z == -1.f});
 }
 
-// The lane's rows of a tile: decays and what they add, and what they do together.
-template <typename T, bool VEC, bool SMALL, int PER, int CH>
-__device__ __forceinline__ void local_rows(const GlrArgs& a, const Span& c, const Flags& f, int j0, int ch, int nch, float2 ka,
-                                           float2 (&da)[PER], float2 (&u)[PER], Map& mx, Map& my) {
-  float2 x[PER], r[PER], i[PER];
-  const int64_t step = a.reverse ? -a.ld : a.ld;
-  int64_t o = row_at<CH>(a, c, j0) * a.ld + ch;
-#pragma unroll
-  for (int q = 0; q < PER; ++q, o += step) {
-    const int n = f.V >> q & 1 ? nch : 0;
-    r[q] = load2<T, VEC>(a.r, o, n);
-    i[q] = load2<T, VEC>(a.i, o, n);
-    x[q] = load2<T, VEC>(a.x, o, n);
+// A pair of channels in shared memory.
+template <typename T>
+__device__ __forceinline__ float2 lds2(const T* p) {
+  if (sizeof(T) == 2) {
+    const uint32_t w = *(const uint32_t*)p;
+    return make_float2(bf_lo(w), bf_hi(w));
   }
-  float2 A = two(1.f), H = two(0.f);
+  return *(const float2*)p;
+}
+
+// The lane's rows of a tile: decays and what they add, and what they do together (A, H; a start in them: H alone).
+// PLAIN: every row is inside one sequence.  sm: the lane's first row of x in shared memory, r and i one and two tiles on.
+template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
+__device__ __forceinline__ void local_rows(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch,
+                                           int nch, float2 ka, float2 (&da)[PER], float2 (&u)[PER], float2& A, float2& H) {
+  float2 x[PER], r[PER], i[PER];
+  if (LOAD == GLR_TMA) {
+    const int step = a.reverse ? -64 : 64;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      r[q] = lds2(sm + CH * 64 + q * step);
+      i[q] = lds2(sm + 2 * CH * 64 + q * step);
+      x[q] = lds2(sm + q * step);
+    }
+  } else {
+    const int64_t step = a.reverse ? -a.ld : a.ld;
+    int64_t o = row_at<CH>(a, c, j0) * a.ld + ch;
+#pragma unroll
+    for (int q = 0; q < PER; ++q, o += step) {
+      const int n = f.V >> q & 1 ? nch : 0;
+      r[q] = load2<T, LOAD == GLR_PAIRS>(a.r, o, n);
+      i[q] = load2<T, LOAD == GLR_PAIRS>(a.i, o, n);
+      x[q] = load2<T, LOAD == GLR_PAIRS>(a.x, o, n);
+    }
+  }
+  A = two(1.f);
+  H = two(0.f);
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const Gate2 g = gate2<SMALL>(r[q], ka);
     da[q] = g.a;
     u[q] = mul2(make_float2(sqf(g.z.x), sqf(g.z.y)), mul2(sigmoid2(i[q]), x[q]));
-    if (!(f.V >> q & 1)) {
-      da[q] = two(1.f);
-      u[q] = two(0.f);
-    }
-    if (f.F >> q & 1) {
-      if (a.h0) {
-        const int64_t oh = (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch;
-        if (nch > 0) u[q].x = fmaf(da[q].x, a.h0[oh], u[q].x);
-        if (nch > 1) u[q].y = fmaf(da[q].y, a.h0[oh + 1], u[q].y);
+    if (!PLAIN) {
+      if (!(f.V >> q & 1)) {
+        da[q] = two(1.f);
+        u[q] = two(0.f);
       }
-      H = u[q];
-    } else {
-      H = fma2(da[q], H, u[q]);
-      A = mul2(A, da[q]);
+      if (f.F >> q & 1) {
+        if (a.h0) {
+          const int64_t oh = (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch;
+          if (nch > 0) u[q].x = fmaf(da[q].x, a.h0[oh], u[q].x);
+          if (nch > 1) u[q].y = fmaf(da[q].y, a.h0[oh + 1], u[q].y);
+        }
+        H = u[q];
+        continue;
+      }
     }
+    H = fma2(da[q], H, u[q]);
+    A = mul2(A, da[q]);
   }
-  mx = Map{A.x, H.x, f.F != 0};
-  my = Map{A.y, H.y, f.F != 0};
 }
 
-// Forward.  Bound by the instructions of the gates (the special function unit has 5 of them a value) and by memory: one
-// pass, x, r and i read once and y written once.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, 2) k_glr_fwd(const GlrArgs a, const GlrTiles tl) {
+struct GlrMaps { CUtensorMap m[3]; };  // x, r, i
+
+// Forward: one pass, x, r and i read once and y written once.  Bound by the instructions of the gates (five special
+// functions a value) and by memory.  Two CTAs an SM keep taking tiles; a tile's rows are copied to shared memory
+// while an earlier one is worked on.
+template <typename T, int LOAD>
+__global__ void __launch_bounds__(256, 2) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
   constexpr int PER = kPerF, CH = kGlrRowsFwd;
+  constexpr int ST = sizeof(T) == 2 ? 2 : 1;        // tiles in shared memory
+  constexpr uint32_t BYTES = 3 * CH * 64 * sizeof(T);
+  extern __shared__ __align__(128) uint8_t raw[];
   __shared__ float4 agg[kWarps][32];
-  __shared__ float4 back[kWarps][32];      // each warp's share of the words before
-  __shared__ float2 enter[kWarps][32];     // the state that enters each warp's rows
-  __shared__ unsigned long long tile_s;
+  __shared__ float4 back[kWarps][32];               // each warp's share of the words before
+  __shared__ float2 enter[kWarps][32];              // the state that enters each warp's rows
+  __shared__ Tile tile_s[ST];
+  __shared__ __align__(8) uint64_t bar_s[ST];
   pdl_enter();
   if (a.err && *a.err) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) tile_s = atomicAdd(a.ticket, 1ull);
-  __syncthreads();
-  int ch, k;
-  int64_t chunk, slot;
-  tile_of(a, tl, tile_s, a.reverse, ch, chunk, slot, k);
-  ch += 2 * lane;
-  const int nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
-  const Span c = span_of<CH>(a, chunk, tl.per_seq);
-  const int j0 = warp * PER;
-  const Flags f = flags_of<CH, PER>(a, c, tl.per_seq, j0, lane);
-  const float2 ka = *(const float2*)(a.kd + ch);
-  float2 da[PER], u[PER];
-  Map mx, my;
-  if (__all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f))
-    local_rows<T, VEC, true, PER, CH>(a, c, f, j0, ch, nch, ka, da, u, mx, my);
-  else
-    local_rows<T, VEC, false, PER, CH>(a, c, f, j0, ch, nch, ka, da, u, mx, my);
-  agg[warp][lane] = pack_map(mx, my);
-  // whether the chunk's first row begins a sequence: then nothing enters
-  const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && k > 0;
+  const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
+  const uint32_t base = LOAD == GLR_TMA ? (smem_u32(raw) + 127u) & ~127u : 0u, bar = smem_u32(bar_s);
 
-  const Chain chain = chain_of(a, tl, slot, k, ch);
-  Map tx{1.f, 0.f, false}, ty{1.f, 0.f, false};
-  if (warp == kWarps - 1) {
+  // thread 0: the tile t into stage st
+  auto fetch = [&](unsigned t, int st) {
+    Tile o;
+    o.k = -1;
+    if (t < total) {
+      o = tile_of(a, tl, t, a.reverse);
+      if (LOAD == GLR_TMA) {
+        const Span c = span_of<CH>(a, o.chunk, tl.per_seq);
+        mbar_expect_tx(bar + 8 * st, BYTES);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) then4(tx, ty, agg[w][lane]);
-    if (k < chain.last) publish(chain.chunk + (int64_t)k * a.dp, tx, ty);
-  }
-  if (need) {
-    Map bx, by;
-    look_back(chain, a.dp, warp, a.err_out, bx, by);
-    back[warp][lane] = pack_map(bx, by);
-    __syncthreads();
-  }
-  if (warp == kWarps - 1) {
-    Map sx{1.f, 0.f, false}, sy{1.f, 0.f, false}, gx = sx, gy = sy;
-    if (need) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) then4(sx, sy, back[w][lane]);
-#pragma unroll
-      for (int w = 4; w < 8; ++w) then4(gx, gy, back[w][lane]);
-      sx = then(sx, gx);
-      sy = then(sy, gy);
-    }
-    float2 h = need ? make_float2(sx.H, sy.H) : two(0.f);
-    if ((k & 15) == 15 && k < chain.last) {
-      publish(chain.group + (int64_t)(k >> 4) * a.dp, then(gx, tx), then(gy, ty));
-      if ((k & 255) == 255) {
-        const Map lx{0.f, tx.reset ? tx.H : fmaf(tx.A, h.x, tx.H), true}, ly{0.f, ty.reset ? ty.H : fmaf(ty.A, h.y, ty.H), true};
-        publish(chain.large + (int64_t)(k >> 8) * a.dp, lx, ly);
+        for (int m = 0; m < 3; ++m)
+          tma_load_2d(base + st * BYTES + m * (BYTES / 3), &maps.m[m], bar + 8 * st, o.ch0, (int)c.r0);
       }
     }
+    tile_s[st] = o;
+  };
+  unsigned next = 0;  // thread 0: the tile after those fetched
+  if (threadIdx.x == 0) {
+    if (LOAD == GLR_TMA) {
+      for (int st = 0; st < ST; ++st) mbar_init(bar + 8 * st, 1);
+      mbar_init_fence();
+    }
+    for (int st = 0; st < ST; ++st) fetch((unsigned)atomicAdd(a.ticket, 1ull), st);
+    next = (unsigned)atomicAdd(a.ticket, 1ull);
+  }
+  __syncthreads();
+
+  for (int it = 0;; ++it) {
+    const int st = it % ST;
+    const Tile t = tile_s[st];
+    const int k = t.k;
+    if (k < 0) break;
+    const int ch = t.ch0 + 2 * lane, nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
+    const Span c = span_of<CH>(a, t.chunk, tl.per_seq);
+    const int j0 = warp * PER;
+    const Flags f = flags_of<CH, PER>(a, c, tl.per_seq, j0, lane);
+    const float2 ka = *(const float2*)(a.kd + ch);
+    const T* sm = LOAD == GLR_TMA ? (const T*)(raw + (base - smem_u32(raw)) + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane : nullptr;
+    if (LOAD == GLR_TMA && !mbar_wait_bounded(bar + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
+    constexpr uint32_t ALL = (1u << PER) - 1;
+    const bool plain = LOAD == GLR_TMA && f.V == ALL && f.F == 0;
+    const bool small = __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
+    float2 da[PER], u[PER], A, H;
+    if (plain && small) local_rows<T, LOAD, true, true, PER, CH>(a, sm, c, f, j0, ch, nch, ka, da, u, A, H);
+    else if (plain) local_rows<T, LOAD, false, true, PER, CH>(a, sm, c, f, j0, ch, nch, ka, da, u, A, H);
+    else local_rows<T, LOAD, false, false, PER, CH>(a, sm, c, f, j0, ch, nch, ka, da, u, A, H);
+    agg[warp][lane] = f.F ? make_float4(-1.f, H.x, -1.f, H.y) : make_float4(A.x, H.x, A.y, H.y);
+    // whether the chunk's first row begins a sequence: then nothing enters
+    const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && k > 0;
+    if (threadIdx.x == 0) {
+      fetch(next, st);
+      if (next < total) next = (unsigned)atomicAdd(a.ticket, 1ull);
+    }
+
+    const Chain chain = chain_of(a, tl, t.slot, k, ch);
+    Map tx{1.f, 0.f, false}, ty{1.f, 0.f, false};
+    if (warp == kWarps - 1) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      enter[w][lane] = h;
-      // the backward's chunks are of kGlrChunk rows
-      if (a.saved && (w * PER) % kGlrChunk == 0) {
-        const int p = a.reverse ? CH - kGlrChunk - w * PER : w * PER;  // physical place of the piece in the chunk
-        if (p < c.nr) {
-          const int64_t piece = tl.per_seq ? c.b * a.per_seq + (c.k + p) / kGlrChunk : (c.r0 + p) / kGlrChunk;
-          store2<float, false>(a.saved, piece * a.d + ch, nch, h);
+      for (int w = 0; w < kWarps; ++w) then4(tx, ty, agg[w][lane]);
+      if (k < chain.last) publish(chain.chunk + (int64_t)k * a.dp, tx, ty);
+    }
+    if (need) {
+      Map bx, by;
+      look_back(chain, a.dp, warp, a.err_out, bx, by);
+      back[warp][lane] = pack_map(bx, by);
+      __syncthreads();
+    }
+    if (warp == kWarps - 1) {
+      Map sx{1.f, 0.f, false}, sy{1.f, 0.f, false}, gx = sx, gy = sy;
+      if (need) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) then4(sx, sy, back[w][lane]);
+#pragma unroll
+        for (int w = 4; w < 8; ++w) then4(gx, gy, back[w][lane]);
+        sx = then(sx, gx);
+        sy = then(sy, gy);
+      }
+      float2 h = need ? make_float2(sx.H, sy.H) : two(0.f);
+      if ((k & 15) == 15 && k < chain.last) {
+        publish(chain.group + (int64_t)(k >> 4) * a.dp, then(gx, tx), then(gy, ty));
+        if ((k & 255) == 255) {
+          const Map lx{0.f, tx.reset ? tx.H : fmaf(tx.A, h.x, tx.H), true}, ly{0.f, ty.reset ? ty.H : fmaf(ty.A, h.y, ty.H), true};
+          publish(chain.large + (int64_t)(k >> 8) * a.dp, lx, ly);
         }
       }
-      const float4 g = agg[w][lane];
-      h = make_float2(g.x == -1.f ? g.y : fmaf(g.x, h.x, g.y), g.z == -1.f ? g.w : fmaf(g.z, h.y, g.w));
-    }
-  }
-  __syncthreads();
-  // the rows again, from the state that enters them
-  float2 h = enter[warp][lane];
-  const int64_t step = a.reverse ? -a.d : a.d;
-  int64_t o = row_at<CH>(a, c, j0) * a.d + ch;
 #pragma unroll
-  for (int q = 0; q < PER; ++q, o += step) {
-    if (f.F >> q & 1) h = u[q];
-    else h = fma2(da[q], h, u[q]);
-    store2<T, VEC>(a.y, o, f.in >> q & 1 ? nch : 0, f.V >> q & 1 ? h : two(0.f));
-    if (a.hT && (f.E >> q & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch, h);
+      for (int w = 0; w < kWarps; ++w) {
+        enter[w][lane] = h;
+        // the backward's chunks are of kGlrChunk rows
+        if (a.saved && (w * PER) % kGlrChunk == 0) {
+          const int p = a.reverse ? CH - kGlrChunk - w * PER : w * PER;  // physical place of the piece in the chunk
+          if (p < c.nr) {
+            const int64_t piece = tl.per_seq ? c.b * a.per_seq + (c.k + p) / kGlrChunk : (c.r0 + p) / kGlrChunk;
+            store2<float, false>(a.saved, piece * a.d + ch, nch, h);
+          }
+        }
+        const float4 g = agg[w][lane];
+        h = make_float2(g.x == -1.f ? g.y : fmaf(g.x, h.x, g.y), g.z == -1.f ? g.w : fmaf(g.z, h.y, g.w));
+      }
+    }
+    __syncthreads();
+    // the rows again, from the state that enters them
+    float2 h = enter[warp][lane];
+    const int64_t step = a.reverse ? -a.d : a.d;
+    int64_t o = row_at<CH>(a, c, j0) * a.d + ch;
+    if (plain && (!a.hT || f.E == 0)) {
+      if (nch > 0) {
+        T* y = (T*)a.y + o;
+#pragma unroll
+        for (int q = 0; q < PER; ++q, y += step) {
+          h = fma2(da[q], h, u[q]);
+          store2<T, true>(y, 0, 2, h);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < PER; ++q, o += step) {
+        if (f.F >> q & 1) h = u[q];
+        else h = fma2(da[q], h, u[q]);
+        store2<T, LOAD != GLR_SINGLE>(a.y, o, f.in >> q & 1 ? nch : 0, f.V >> q & 1 ? h : two(0.f));
+        if (a.hT && (f.E >> q & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch, h);
+      }
+    }
   }
 }
 
@@ -587,10 +670,40 @@ cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cud
   return cudaGetLastError();
 }
 
+namespace {
+// A map of [rows][d] with row stride ld, its box 64 channels of `box` rows; false where TMA does not take it.
+bool rows_map(CUtensorMap* m, const void* p, bool f32, int d, int64_t T, int64_t ld, int box) {
+  const size_t es = f32 ? 4 : 2;
+  auto enc = encoder();
+  if (!enc || reinterpret_cast<uintptr_t>(p) % 16 || ld * es % 16 || (size_t)d * es % 16 || ld * es >= (1ull << 40)) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)T}, strides[1] = {(cuuint64_t)(ld * es)};
+  cuuint32_t boxes[2] = {64, (cuuint32_t)box}, es1[2] = {1, 1};
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides,
+             boxes, es1, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+cudaError_t run_glr_fwd(const GlrArgs& a, const GlrTiles& t, cudaStream_t st) {
+  constexpr bool f32 = sizeof(T) == 4;
+  GlrMaps maps{};
+  const bool tma = reinterpret_cast<uintptr_t>(a.y) % (2 * sizeof(T)) == 0 &&
+                   rows_map(&maps.m[0], a.x, f32, a.d, a.seq.T, a.ld, kGlrRowsFwd) &&
+                   rows_map(&maps.m[1], a.r, f32, a.d, a.seq.T, a.ld, kGlrRowsFwd) &&
+                   rows_map(&maps.m[2], a.i, f32, a.d, a.seq.T, a.ld, kGlrRowsFwd);
+  const size_t smem = tma ? (size_t)3 * kGlrRowsFwd * 64 * 4 + 128 : 0;
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)t.n_chunks * (a.dp >> 6), (int64_t)sm_count() * 2));
+  if (tma) {
+    const cudaError_t e = cudaFuncSetAttribute(k_glr_fwd<T, GLR_TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_glr_fwd<T, GLR_TMA>, grid, dim3(256), smem, st, a, t, maps);
+  }
+  return launch_pdl(pairs_ok(a, sizeof(T)) ? k_glr_fwd<T, GLR_PAIRS> : k_glr_fwd<T, GLR_SINGLE>, grid, dim3(256), 0, st, a, t, maps);
+}
+}  // namespace
+
 cudaError_t launch_glr_fwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st) {
-  const dim3 grid((unsigned)((int64_t)t.n_chunks * (a.dp >> 6)));
-  if (f32) return launch_pdl(pairs_ok(a, 4) ? k_glr_fwd<float, true> : k_glr_fwd<float, false>, grid, dim3(256), 0, st, a, t);
-  return launch_pdl(pairs_ok(a, 2) ? k_glr_fwd<bf16, true> : k_glr_fwd<bf16, false>, grid, dim3(256), 0, st, a, t);
+  return f32 ? run_glr_fwd<float>(a, t, st) : run_glr_fwd<bf16>(a, t, st);
 }
 
 cudaError_t launch_glr_bwd(const GlrArgs& a, bool f32, cudaStream_t st) {

@@ -3,6 +3,7 @@
 // descriptors, MMA issue and commit, TMEM loads and stores, tiled TMA loads.
 #pragma once
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cstdint>
 
 #include "mbarrier.cuh"
@@ -218,6 +219,8 @@ __device__ __forceinline__ void named_bar(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// Host: the driver's tensor map encoder, null if it cannot be found.
+PFN_cuTensorMapEncodeTiled_v12000 encoder();
 // Host: 2-D bf16 tensor map over a row-major [outer][inner] array (row pitch
 // ld elements), box {box_inner, box_outer}, 128-byte swizzle, zero fill out of
 // bounds, L2 promotion of 256 bytes (wide) or 128 bytes.  False if the driver
