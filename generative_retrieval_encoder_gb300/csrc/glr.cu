@@ -98,24 +98,9 @@ __device__ __forceinline__ float sqf(float x) {
 struct Span {
   int64_t r0;       // physical first row of the chunk
   int nr;           // its rows
-  int64_t b;        // its slot (slots of their own)
+  int b;            // its slot (slots of their own)
   int k;            // its first row in the slot
 };
-template <int CH>
-__device__ __forceinline__ Span span_of(const GlrArgs& a, int64_t chunk, int per_seq) {
-  Span c;
-  if (per_seq) {
-    c.b = chunk / per_seq;
-    c.k = (int)(chunk - c.b * per_seq) * CH;
-    c.r0 = c.b * a.seq.L + c.k;
-    c.nr = min(CH, a.seq.L - c.k);
-  } else {
-    c.b = c.k = 0;
-    c.r0 = chunk * CH;
-    c.nr = (int)min((int64_t)CH, a.seq.T - c.r0);
-  }
-  return c;
-}
 template <int CH>
 __device__ __forceinline__ int64_t row_at(const GlrArgs& a, const Span& c, int j) {
   return a.reverse ? c.r0 + CH - 1 - j : c.r0 + j;
@@ -133,11 +118,10 @@ __device__ __forceinline__ Flags flags_of(const GlrArgs& a, const Span& c, int p
     s = in && (a.marks[row >> 6] >> (row & 63) & 1);
     z = in && (row + 1 == a.seq.T || (a.marks[(row + 1) >> 6] >> ((row + 1) & 63) & 1));
   } else {
-    int64_t b = c.b;
-    int pos = c.k + p;
+    int b = c.b, pos = c.k + p;
     if (!per_seq) {
       b = (int)row / a.seq.L;
-      pos = (int)row - (int)b * a.seq.L;
+      pos = (int)row - b * a.seq.L;
     }
     const int len = a.seq.mode == SEQ_PADDED ? (in ? a.seq.lens[b] : 0) : a.seq.L;
     v = in && pos < len;
@@ -194,68 +178,92 @@ __device__ __forceinline__ Map then(const Map& m, const Map& n) {
 }
 __device__ __forceinline__ uint64_t word_of(const Map& m) { return m.reset ? reset_word(m.H) : word(m.A, m.H); }
 
-__device__ __forceinline__ void publish(uint64_t* p, const Map& x, const Map& y) {
-  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(word_of(x)), "l"(word_of(y)) : "memory");
+__device__ __forceinline__ void publish(uint64_t* p, const Map& x) {
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(word_of(x)) : "memory");
 }
-__device__ __forceinline__ void peek(const uint64_t* p, uint64_t& x, uint64_t& y) {
-  asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "l"(p) : "memory");
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+  uint64_t x;
+  asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(x) : "l"(p) : "memory");
+  return x;
 }
-// Waits for a pair of words: bounded, and given up at once where another wait has been.
-__device__ __forceinline__ void await(const uint64_t* p, uint64_t& x, uint64_t& y, int* err) {
-  for (int n = 0; !(x >> 63 & y >> 63); ++n) {
-    if (n > 64) __nanosleep(100);
-    if ((n & 1023) == 1023 && (*(volatile int*)err & kErrTimeout)) break;
-    if (n > (1 << 22)) {
-      atomicOr(err, kErrTimeout);
-      break;
-    }
-    peek(p, x, y);
-  }
-}
-
 // The words of a call: of chunks, groups and larger groups, each [..][dp] with dp the channels rounded up to 64.
 struct Chain {
   uint64_t* chunk; uint64_t* group; uint64_t* large;
   int k, last;      // this chunk's place in its chain, and the last one
 };
-__device__ __forceinline__ Chain chain_of(const GlrArgs& a, const GlrTiles& t, int64_t s, int k, int ch) {
+__device__ __forceinline__ Chain chain_of(const GlrArgs& a, const GlrTiles& t, int s, int k, int ch) {
   // s: the sequence slot (0 for a stream); the arrays hold each slot's words in the order of its chain
   const int64_t n = t.per_seq ? t.per_seq : t.n_chunks, ng = (n + 15) >> 4, nl = (n + 255) >> 8;
   Chain c;
-  c.chunk = a.words + (s * n) * a.dp + ch;
+  c.chunk = a.words + s * n * a.dp + ch;
   c.group = a.words + ((int64_t)t.n_chunks + s * ng) * a.dp + ch;
   c.large = a.words + ((int64_t)t.n_chunks + (int64_t)(t.per_seq ? a.seq.n_seq : 1) * ng + s * nl) * a.dp + ch;
   c.k = k;
   c.last = (int)n - 1;
   return c;
 }
-// Warp w's share, composed, of the words that chunk k reads: warps 0-3 the larger group's state and the groups before,
-// warps 4-7 the chunks before.
-__device__ __forceinline__ void look_back(const Chain& c, int64_t dp, int warp, int* err, Map& x, Map& y) {
-  x.A = y.A = 1.f;
-  x.H = y.H = 0.f;
-  x.reset = y.reset = false;
-  const int g = c.k >> 4, l = c.k >> 8, q = warp & 3;
-  const int n = warp < 4 ? (g & 15) + (l > 0) : c.k & 15;
-  const int lo = q * n >> 2, m = ((q + 1) * n >> 2) - lo;
-  const uint64_t* p[4];
-  uint64_t wx[4], wy[4];
+// The words that chunk c.k reads: those of the chunks before it in its group, of the groups before its own in the larger
+// group, and the state after the last larger group.  ask() asks for all of them at once, before they are needed; near()
+// and far() wait for those that were not there yet and compose them: the chunks of the group, and the state that the
+// group begins with.  What a group does is published between the two, so no group waits for another's.
+constexpr uint32_t kPolls = 1u << 20;  // of a wait inside a CTA: a second or so at the least
+constexpr uint64_t kIdentity = 0xBF80000000000000ull;  // h -> 1 h + 0
+struct Words { uint64_t chunk[15], group[15], large; };
+__device__ __forceinline__ void ask(const Chain& c, int64_t dp, Words& w) {
+  const int l = c.k >> 8, n1 = c.k & 15, n2 = c.k >> 4 & 15;
+  const uint64_t* p = c.chunk + (int64_t)(c.k - n1) * dp;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j >= m) break;
-    const int i = lo + j;
-    p[j] = warp >= 4 ? c.chunk + (int64_t)((g << 4) + i) * dp
-           : l > 0   ? (i == 0 ? c.large + (int64_t)(l - 1) * dp : c.group + (int64_t)((l << 4) + i - 1) * dp)
-                     : c.group + (int64_t)i * dp;
-    peek(p[j], wx[j], wy[j]);
-  }
+  for (int j = 0; j < 15; ++j, p += dp) w.chunk[j] = j < n1 ? peek(p) : kIdentity;
+  p = c.group + (int64_t)(l << 4) * dp;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j >= m) break;
-    await(p[j], wx[j], wy[j], err);
-    x = then(x, map_of(wx[j]));
-    y = then(y, map_of(wy[j]));
+  for (int j = 0; j < 15; ++j, p += dp) w.group[j] = j < n2 ? peek(p) : kIdentity;
+  w.large = l > 0 ? peek(c.large + (int64_t)(l - 1) * dp) : kIdentity;
+}
+// Whether to go on asking after n vain tries: bounded, and given up at once where another wait has been.
+__device__ __forceinline__ bool patient(int n, int* err) {
+  if ((n & 255) != 255) return true;
+  if (*(volatile int*)err & kErrTimeout) return false;
+  if (n < (1 << 22)) return true;
+  atomicOr(err, kErrTimeout);
+  return false;
+}
+__device__ __forceinline__ Map near(const Chain& c, int64_t dp, Words& w, int* err) {
+  for (int n = 0;; ++n) {
+    uint64_t there = w.chunk[0];
+#pragma unroll
+    for (int j = 1; j < 15; ++j) there &= w.chunk[j];
+    if (there >> 63 || !patient(n, err)) break;
+    const uint64_t* p = c.chunk + (int64_t)(c.k & ~15) * dp;
+#pragma unroll
+    for (int j = 0; j < 15; ++j, p += dp)
+      if (!(w.chunk[j] >> 63)) w.chunk[j] = peek(p);
   }
+  Map m{1.f, 0.f, false};
+#pragma unroll
+  for (int j = 0; j < 15; ++j) m = then(m, map_of(w.chunk[j]));
+  return m;
+}
+__device__ __forceinline__ float far(const Chain& c, int64_t dp, Words& w, int* err) {
+  const int l = c.k >> 8;
+  if (c.k < 16) return 0.f;
+  for (int n = 0;; ++n) {
+    uint64_t there = w.large;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) there &= w.group[j];
+    if (there >> 63 || !patient(n, err)) break;
+    const uint64_t* p = c.group + (int64_t)(l << 4) * dp;
+#pragma unroll
+    for (int j = 0; j < 15; ++j, p += dp)
+      if (!(w.group[j] >> 63)) w.group[j] = peek(p);
+    if (!(w.large >> 63)) w.large = peek(c.large + (int64_t)(l - 1) * dp);
+  }
+  float h = __uint_as_float((uint32_t)w.large);
+#pragma unroll
+  for (int j = 0; j < 15; ++j) {
+    const Map m = map_of(w.group[j]);
+    h = m.reset ? m.H : fmaf(m.A, h, m.H);
+  }
+  return h;
 }
 
 // ------------------------------------------------------------ tiles
@@ -286,15 +294,22 @@ __device__ __forceinline__ void store2(void* base, int64_t o, int n, float2 v) {
   if (n > 1) p[1] = from_f<T>(v.y);
 }
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;                   // that work on rows
+constexpr int kScan = 2;                     // that work on the states between tiles, a lane a channel
+constexpr int kThreads = (kWarps + kScan + 1) * 32;  // and one that takes tiles
 constexpr int kPerF = kGlrRowsFwd / kWarps;  // a warp's rows; a lane has two channels of each
 
 // How a tile's rows are read: copied ahead into shared memory (rows of 16-byte pieces), or straight into registers by
 // pairs of channels or single ones.
 enum GlrLoad { GLR_TMA = 0, GLR_PAIRS = 1, GLR_SINGLE = 2 };
 
-// A tile: channels from ch0, chunk (physical), slot and place k in its chain.
-struct Tile { int ch0, k; int64_t chunk, slot; };
+// A tile: channels from ch0, the chunk's rows, and its place k in its slot's chain (-1: no tile).
+struct Tile {
+  int ch0, k;
+  Span c;
+  int inner;        // every row is inside one sequence and neither its first nor its last
+};
+template <int CH>
 __device__ __forceinline__ Tile tile_of(const GlrArgs& a, const GlrTiles& g, unsigned t, bool back) {
   const unsigned ncg = (unsigned)(a.dp >> 6);
   Tile o;
@@ -302,24 +317,27 @@ __device__ __forceinline__ Tile tile_of(const GlrArgs& a, const GlrTiles& g, uns
   const unsigned w = t / ncg;
   if (g.per_seq) {
     const unsigned q = w / (unsigned)a.seq.n_seq;
-    o.slot = w - q * (unsigned)a.seq.n_seq;
+    o.c.b = (int)(w - q * (unsigned)a.seq.n_seq);
     o.k = (int)q;
-    o.chunk = o.slot * g.per_seq + (back ? g.per_seq - 1 - o.k : o.k);
+    o.c.k = (back ? g.per_seq - 1 - o.k : o.k) * CH;
+    o.c.r0 = (int64_t)o.c.b * a.seq.L + o.c.k;
+    o.c.nr = min(CH, a.seq.L - o.c.k);
+    const int len = a.seq.mode == SEQ_PADDED ? a.seq.lens[o.c.b] : a.seq.L;
+    o.inner = o.c.k > 0 && o.c.k + CH < len;
   } else {
-    o.slot = 0;
+    o.c.b = o.c.k = 0;
     o.k = (int)w;
-    o.chunk = back ? g.n_chunks - 1 - o.k : o.k;
+    o.c.r0 = (int64_t)(back ? g.n_chunks - 1 - o.k : o.k) * CH;
+    o.c.nr = (int)min((int64_t)CH, a.seq.T - o.c.r0);
+    o.inner = 0;
+    if (a.seq.mode == SEQ_VARLEN && o.c.r0 + CH < a.seq.T) {
+      uint64_t m = a.marks[(o.c.r0 + CH) >> 6] & 1;
+#pragma unroll
+      for (int j = 0; j < CH / 64; ++j) m |= a.marks[(o.c.r0 >> 6) + j];
+      o.inner = m == 0;
+    }
   }
   return o;
-}
-
-// What a warp's rows do, in shared memory: {A, H} of two channels; A = -1: a sequence starts in them.
-__device__ __forceinline__ float4 pack_map(const Map& x, const Map& y) {
-  return make_float4(x.reset ? -1.f : x.A, x.H, y.reset ? -1.f : y.A, y.H);
-}
-__device__ __forceinline__ void then4(Map& x, Map& y, const float4& g) {
-  x = then(x, Map{g.x, g.y, g.x == -1.f});
-  y = then(y, Map{g.z, g.w, g.z == -1.f});
 }
 
 // A pair of channels in shared memory.
@@ -337,33 +355,28 @@ __device__ __forceinline__ float2 lds2(const T* p) {
 template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
 __device__ __forceinline__ void local_rows(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch,
                                            int nch, float2 ka, float2 (&da)[PER], float2 (&u)[PER], float2& A, float2& H) {
-  float2 x[PER], r[PER], i[PER];
-  if (LOAD == GLR_TMA) {
-    const int step = a.reverse ? -64 : 64;
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      r[q] = lds2(sm + CH * 64 + q * step);
-      i[q] = lds2(sm + 2 * CH * 64 + q * step);
-      x[q] = lds2(sm + q * step);
-    }
-  } else {
-    const int64_t step = a.reverse ? -a.ld : a.ld;
-    int64_t o = row_at<CH>(a, c, j0) * a.ld + ch;
-#pragma unroll
-    for (int q = 0; q < PER; ++q, o += step) {
-      const int n = f.V >> q & 1 ? nch : 0;
-      r[q] = load2<T, LOAD == GLR_PAIRS>(a.r, o, n);
-      i[q] = load2<T, LOAD == GLR_PAIRS>(a.i, o, n);
-      x[q] = load2<T, LOAD == GLR_PAIRS>(a.x, o, n);
-    }
-  }
+  const int64_t step = a.reverse ? -a.ld : a.ld;
+  int64_t o = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.ld + ch;
   A = two(1.f);
   H = two(0.f);
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
-    const Gate2 g = gate2<SMALL>(r[q], ka);
+    float2 x, r, i;
+    if (LOAD == GLR_TMA) {
+      r = lds2(sm + CH * 64);
+      i = lds2(sm + 2 * CH * 64);
+      x = lds2(sm);
+      sm += a.reverse ? -64 : 64;
+    } else {
+      const int n = f.V >> q & 1 ? nch : 0;
+      r = load2<T, LOAD == GLR_PAIRS>(a.r, o, n);
+      i = load2<T, LOAD == GLR_PAIRS>(a.i, o, n);
+      x = load2<T, LOAD == GLR_PAIRS>(a.x, o, n);
+      o += step;
+    }
+    const Gate2 g = gate2<SMALL>(r, ka);
     da[q] = g.a;
-    u[q] = mul2(make_float2(sqf(g.z.x), sqf(g.z.y)), mul2(sigmoid2(i[q]), x[q]));
+    u[q] = mul2(make_float2(sqf(g.z.x), sqf(g.z.y)), mul2(sigmoid2(i), x));
     if (!PLAIN) {
       if (!(f.V >> q & 1)) {
         da[q] = two(1.f);
@@ -386,149 +399,206 @@ __device__ __forceinline__ void local_rows(const GlrArgs& a, const T* sm, const 
 
 struct GlrMaps { CUtensorMap m[3]; };  // x, r, i
 
+template <typename T> constexpr int stages_fwd() { return sizeof(T) == 2 ? 3 : 2; }
+
+// Shared memory of a CTA of the forward, after its tiles of x, r and i.
+struct GlrShared {
+  float2 agg[2][kWarps][64];      // {A, H} of each warp's rows; A = -1: a sequence starts in them
+  float enter[2][kWarps][64];     // the state that enters each warp's rows
+  Tile tile[8];
+  int first[2];                   // the tile's first row begins a sequence
+  uint64_t full[3], empty[3], agg_bar[2], enter_bar[2], tile_bar[8];
+  int fail;
+};
+
 // Forward: one pass, x, r and i read once and y written once.  Bound by the instructions of the gates (five special
-// functions a value) and by memory.  Two CTAs an SM keep taking tiles; a tile's rows are copied to shared memory
-// while an earlier one is worked on.
+// functions a value) and by memory.  One CTA an SM keeps taking tiles: 16 warps form the gates of tile n (copied ahead
+// into shared memory) and then, with the state that enters tile n - 1, its outputs; its decays wait in registers in
+// between, the time in which two more warps, a lane a channel, compose the states across tiles (they alone wait for
+// other CTAs); one more takes tiles and copies them.
+// Every barrier's phase is seen by all who wait for it before it can pass again: agg of tile n + 2 takes the outputs of
+// tile n, those take enter of tile n, and that takes both scan warps past agg of tile n; empty and full alternate;
+// tile n + 8 is taken after the outputs of tile n.
 template <typename T, int LOAD>
-__global__ void __launch_bounds__(256, 2) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
-  constexpr int PER = kPerF, CH = kGlrRowsFwd;
-  constexpr int ST = sizeof(T) == 2 ? 2 : 1;        // tiles in shared memory
-  constexpr uint32_t BYTES = 3 * CH * 64 * sizeof(T);
+__global__ void __launch_bounds__(kThreads, 1) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
+  constexpr int PER = kPerF, CH = kGlrRowsFwd, ST = stages_fwd<T>();
+  constexpr uint32_t BYTES = 3 * CH * 64 * sizeof(T), ALL = (1u << PER) - 1;
   extern __shared__ __align__(128) uint8_t raw[];
-  __shared__ float4 agg[kWarps][32];
-  __shared__ float4 back[kWarps][32];               // each warp's share of the words before
-  __shared__ float2 enter[kWarps][32];              // the state that enters each warp's rows
-  __shared__ Tile tile_s[ST];
-  __shared__ __align__(8) uint64_t bar_s[ST];
   pdl_enter();
   if (a.err && *a.err) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
-  const uint32_t base = LOAD == GLR_TMA ? (smem_u32(raw) + 127u) & ~127u : 0u, bar = smem_u32(bar_s);
-
-  // thread 0: the tile t into stage st
-  auto fetch = [&](unsigned t, int st) {
-    Tile o;
-    o.k = -1;
-    if (t < total) {
-      o = tile_of(a, tl, t, a.reverse);
-      if (LOAD == GLR_TMA) {
-        const Span c = span_of<CH>(a, o.chunk, tl.per_seq);
-        mbar_expect_tx(bar + 8 * st, BYTES);
-#pragma unroll
-        for (int m = 0; m < 3; ++m)
-          tma_load_2d(base + st * BYTES + m * (BYTES / 3), &maps.m[m], bar + 8 * st, o.ch0, (int)c.r0);
-      }
-    }
-    tile_s[st] = o;
-  };
-  unsigned next = 0;  // thread 0: the tile after those fetched
+  uint8_t* tiles = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
+  GlrShared& sh = *reinterpret_cast<GlrShared*>(tiles + (LOAD == GLR_TMA ? ST * BYTES : 0));
+  const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty), agg_bar = smem_u32(sh.agg_bar),
+                 enter_bar = smem_u32(sh.enter_bar), tile_bar = smem_u32(sh.tile_bar);
   if (threadIdx.x == 0) {
-    if (LOAD == GLR_TMA) {
-      for (int st = 0; st < ST; ++st) mbar_init(bar + 8 * st, 1);
-      mbar_init_fence();
+    for (int st = 0; st < ST; ++st) {
+      mbar_init(full + 8 * st, 1);
+      mbar_init(empty + 8 * st, kWarps);
     }
-    for (int st = 0; st < ST; ++st) fetch((unsigned)atomicAdd(a.ticket, 1ull), st);
-    next = (unsigned)atomicAdd(a.ticket, 1ull);
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(agg_bar + 8 * q, kWarps);
+      mbar_init(enter_bar + 8 * q, kScan);
+    }
+    for (int q = 0; q < 8; ++q) mbar_init(tile_bar + 8 * q, 1);
+    mbar_init_fence();
+    sh.fail = 0;
   }
   __syncthreads();
 
-  for (int it = 0;; ++it) {
-    const int st = it % ST;
-    const Tile t = tile_s[st];
-    const int k = t.k;
-    if (k < 0) break;
-    const int ch = t.ch0 + 2 * lane, nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
-    const Span c = span_of<CH>(a, t.chunk, tl.per_seq);
-    const int j0 = warp * PER;
-    const Flags f = flags_of<CH, PER>(a, c, tl.per_seq, j0, lane);
-    const float2 ka = *(const float2*)(a.kd + ch);
-    const T* sm = LOAD == GLR_TMA ? (const T*)(raw + (base - smem_u32(raw)) + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane : nullptr;
-    if (LOAD == GLR_TMA && !mbar_wait_bounded(bar + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
-    constexpr uint32_t ALL = (1u << PER) - 1;
-    const bool plain = LOAD == GLR_TMA && f.V == ALL && f.F == 0;
-    const bool small = __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
-    float2 da[PER], u[PER], A, H;
-    if (plain && small) local_rows<T, LOAD, true, true, PER, CH>(a, sm, c, f, j0, ch, nch, ka, da, u, A, H);
-    else if (plain) local_rows<T, LOAD, false, true, PER, CH>(a, sm, c, f, j0, ch, nch, ka, da, u, A, H);
-    else local_rows<T, LOAD, false, false, PER, CH>(a, sm, c, f, j0, ch, nch, ka, da, u, A, H);
-    agg[warp][lane] = f.F ? make_float4(-1.f, H.x, -1.f, H.y) : make_float4(A.x, H.x, A.y, H.y);
-    // whether the chunk's first row begins a sequence: then nothing enters
-    const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && k > 0;
-    if (threadIdx.x == 0) {
-      fetch(next, st);
-      if (next < total) next = (unsigned)atomicAdd(a.ticket, 1ull);
+  if (warp == kWarps + kScan) {
+    // ---- tiles
+    if (lane != 0) return;
+    const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
+    unsigned t = (unsigned)atomicAdd(a.ticket, 1ull);
+    int n = 0, held = 0;  // held: the first tile that may still be on its way at the end
+    for (;; ++n) {
+      const int st = n % ST;
+      Tile o;
+      o.k = -1;
+      if (t < total) o = tile_of<CH>(a, tl, t, a.reverse);
+      if (n >= ST && !mbar_wait(empty + 8 * st, (n / ST - 1) & 1, &sh.fail, kPolls)) break;
+      held = max(0, n - ST + 1);
+      sh.tile[n & 7] = o;
+      mbar_arrive(tile_bar + 8 * (n & 7));
+      if (LOAD == GLR_TMA && t < total) {
+        mbar_expect_tx(full + 8 * st, BYTES);
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+          tma_load_2d(smem_u32(tiles) + st * BYTES + m * (BYTES / 3), &maps.m[m], full + 8 * st, o.ch0, (int)o.c.r0);
+      } else {
+        mbar_arrive(full + 8 * st);
+      }
+      if (t >= total) break;
+      t = (unsigned)atomicAdd(a.ticket, 1ull);
     }
+    // the copies end before the CTA does, whatever became of the other warps
+    for (int m = held; m < n; ++m) mbar_wait(full + 8 * (m % ST), (m / ST) & 1, &sh.fail, kPolls);
+    if (sh.fail) atomicOr(a.err_out, kErrTimeout);
+    return;
+  }
 
-    const Chain chain = chain_of(a, tl, t.slot, k, ch);
-    Map tx{1.f, 0.f, false}, ty{1.f, 0.f, false};
-    if (warp == kWarps - 1) {
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) then4(tx, ty, agg[w][lane]);
-      if (k < chain.last) publish(chain.chunk + (int64_t)k * a.dp, tx, ty);
-    }
-    if (need) {
-      Map bx, by;
-      look_back(chain, a.dp, warp, a.err_out, bx, by);
-      back[warp][lane] = pack_map(bx, by);
-      __syncthreads();
-    }
-    if (warp == kWarps - 1) {
-      Map sx{1.f, 0.f, false}, sy{1.f, 0.f, false}, gx = sx, gy = sy;
-      if (need) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) then4(sx, sy, back[w][lane]);
-#pragma unroll
-        for (int w = 4; w < 8; ++w) then4(gx, gy, back[w][lane]);
-        sx = then(sx, gx);
-        sy = then(sy, gy);
-      }
-      float2 h = need ? make_float2(sx.H, sy.H) : two(0.f);
-      if ((k & 15) == 15 && k < chain.last) {
-        publish(chain.group + (int64_t)(k >> 4) * a.dp, then(gx, tx), then(gy, ty));
-        if ((k & 255) == 255) {
-          const Map lx{0.f, tx.reset ? tx.H : fmaf(tx.A, h.x, tx.H), true}, ly{0.f, ty.reset ? ty.H : fmaf(ty.A, h.y, ty.H), true};
-          publish(chain.large + (int64_t)(k >> 8) * a.dp, lx, ly);
-        }
-      }
+  if (warp >= kWarps) {
+    // ---- the states between tiles
+    const int cc = (warp - kWarps) * 32 + lane;
+    for (int n = 0;; ++n) {
+      const int q = n & 1;
+      if (!mbar_wait(tile_bar + 8 * (n & 7), (n >> 3) & 1, &sh.fail, kPolls)) break;
+      const Tile& t = sh.tile[n & 7];
+      const int k = t.k, ch = t.ch0 + cc;
+      if (k < 0) break;
+      const Chain chain = chain_of(a, tl, t.c.b, k, ch);
+      Words words;
+      ask(chain, a.dp, words);
+      if (!mbar_wait(agg_bar + 8 * q, (n >> 1) & 1, &sh.fail, kPolls)) break;
+      Map tot{1.f, 0.f, false};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        enter[w][lane] = h;
-        // the backward's chunks are of kGlrChunk rows
-        if (a.saved && (w * PER) % kGlrChunk == 0) {
+        const float2 g = sh.agg[q][w][cc];
+        tot = then(tot, Map{g.x, g.y, g.x == -1.f});
+      }
+      if (k < chain.last) publish(chain.chunk + (int64_t)k * a.dp, tot);
+      const bool need = !sh.first[q] && k > 0;
+      Map grp{1.f, 0.f, false};
+      if (need) grp = near(chain, a.dp, words, a.err_out);
+      if ((k & 15) == 15 && k < chain.last) publish(chain.group + (int64_t)(k >> 4) * a.dp, then(grp, tot));
+      float h = 0.f;
+      if (need) {
+        h = far(chain, a.dp, words, a.err_out);
+        h = grp.reset ? grp.H : fmaf(grp.A, h, grp.H);
+      }
+      if ((k & 255) == 255 && k < chain.last)
+        publish(chain.large + (int64_t)(k >> 8) * a.dp, Map{0.f, tot.reset ? tot.H : fmaf(tot.A, h, tot.H), true});
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        sh.enter[q][w][cc] = h;
+        if ((w * PER) % kGlrChunk == 0 && a.saved && ch < a.d) {  // the backward's chunks are of kGlrChunk rows
           const int p = a.reverse ? CH - kGlrChunk - w * PER : w * PER;  // physical place of the piece in the chunk
-          if (p < c.nr) {
-            const int64_t piece = tl.per_seq ? c.b * a.per_seq + (c.k + p) / kGlrChunk : (c.r0 + p) / kGlrChunk;
-            store2<float, false>(a.saved, piece * a.d + ch, nch, h);
+          if (p < t.c.nr) {
+            const int64_t piece = tl.per_seq ? (int64_t)t.c.b * a.per_seq + (t.c.k + p) / kGlrChunk : (t.c.r0 + p) / kGlrChunk;
+            a.saved[piece * a.d + ch] = h;
           }
         }
-        const float4 g = agg[w][lane];
-        h = make_float2(g.x == -1.f ? g.y : fmaf(g.x, h.x, g.y), g.z == -1.f ? g.w : fmaf(g.z, h.y, g.w));
+        const float2 g = sh.agg[q][w][cc];
+        h = g.x == -1.f ? g.y : fmaf(g.x, h, g.y);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(enter_bar + 8 * q);
     }
-    __syncthreads();
-    // the rows again, from the state that enters them
-    float2 h = enter[warp][lane];
+    return;
+  }
+
+  // ---- rows
+  struct Held { uint32_t f; };  // in, V, F, E: eight bits each
+  constexpr uint32_t INNER = ALL | ALL << 8;
+  const int j0 = warp * PER;
+  // tile n: gates, decays held in da and u
+  auto begin = [&](int n, float2 (&da)[PER], float2 (&u)[PER], Held& hd) -> bool {
+    const int st = n % ST, q = n & 1;
+    if (!mbar_wait(full + 8 * st, (n / ST) & 1, &sh.fail, kPolls)) return false;
+    const Tile& t = sh.tile[n & 7];
+    if (t.k < 0) return false;
+    const int ch = t.ch0 + 2 * lane;
+    const float2 ka = *(const float2*)(a.kd + ch);
+    const bool small = __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
+    const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
+    Flags f{ALL, ALL, 0, 0};
+    if (!t.inner) f = flags_of<CH, PER>(a, t.c, tl.per_seq, j0, lane);
+    hd.f = f.in | f.V << 8 | f.F << 16 | f.E << 24;
+    float2 A, H;
+    if (LOAD == GLR_TMA && (hd.f & 0xffffffu) == INNER) {
+      if (small) local_rows<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, a.d - ch, ka, da, u, A, H);
+      else local_rows<T, LOAD, false, true, PER, CH>(a, sm, t.c, f, j0, ch, a.d - ch, ka, da, u, A, H);
+    } else {
+      local_rows<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, a.d - ch, ka, da, u, A, H);
+    }
+    *(float4*)&sh.agg[q][warp][2 * lane] = f.F ? make_float4(-1.f, H.x, -1.f, H.y) : make_float4(A.x, H.x, A.y, H.y);
+    if (threadIdx.x == 0) sh.first[q] = f.F & 1;
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(agg_bar + 8 * q);
+      mbar_arrive(empty + 8 * st);
+    }
+    return true;
+  };
+  // tile n: the rows again, from the state that enters them
+  auto finish = [&](int n, const float2 (&da)[PER], const float2 (&u)[PER], const Held& hd) -> bool {
+    const int q = n & 1;
+    if (!mbar_wait(enter_bar + 8 * q, (n >> 1) & 1, &sh.fail, kPolls)) return false;
+    float2 h = *(const float2*)&sh.enter[q][warp][2 * lane];
+    const Tile& t = sh.tile[n & 7];
+    const int ch = t.ch0 + 2 * lane, nch = a.d - ch;
     const int64_t step = a.reverse ? -a.d : a.d;
-    int64_t o = row_at<CH>(a, c, j0) * a.d + ch;
-    if (plain && (!a.hT || f.E == 0)) {
+    int64_t o = row_at<CH>(a, t.c, j0) * a.d + ch;
+    if (LOAD == GLR_TMA && hd.f == INNER) {
       if (nch > 0) {
         T* y = (T*)a.y + o;
 #pragma unroll
-        for (int q = 0; q < PER; ++q, y += step) {
-          h = fma2(da[q], h, u[q]);
+        for (int p = 0; p < PER; ++p, y += step) {
+          h = fma2(da[p], h, u[p]);
           store2<T, true>(y, 0, 2, h);
         }
       }
     } else {
+      const Flags f{hd.f & 255u, hd.f >> 8 & 255u, hd.f >> 16 & 255u, hd.f >> 24};
 #pragma unroll
-      for (int q = 0; q < PER; ++q, o += step) {
-        if (f.F >> q & 1) h = u[q];
-        else h = fma2(da[q], h, u[q]);
-        store2<T, LOAD != GLR_SINGLE>(a.y, o, f.in >> q & 1 ? nch : 0, f.V >> q & 1 ? h : two(0.f));
-        if (a.hT && (f.E >> q & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch, h);
+      for (int p = 0; p < PER; ++p, o += step) {
+        if (f.F >> p & 1) h = u[p];
+        else h = fma2(da[p], h, u[p]);
+        store2<T, LOAD != GLR_SINGLE>(a.y, o, f.in >> p & 1 ? nch : 0, f.V >> p & 1 ? h : two(0.f));
+        if (a.hT && (f.E >> p & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + p)) * a.d + ch, nch, h);
       }
     }
+    return true;
+  };
+  float2 da0[PER], u0[PER], da1[PER], u1[PER];
+  Held h0, h1;
+  if (!begin(0, da0, u0, h0)) return;
+  for (int n = 1;; n += 2) {
+    const bool b1 = begin(n, da1, u1, h1);
+    if (!finish(n - 1, da0, u0, h0) || !b1) break;
+    const bool b2 = begin(n + 1, da0, u0, h0);
+    if (!finish(n, da1, u1, h1) || !b2) break;
   }
 }
 
@@ -691,14 +761,12 @@ cudaError_t run_glr_fwd(const GlrArgs& a, const GlrTiles& t, cudaStream_t st) {
                    rows_map(&maps.m[0], a.x, f32, a.d, a.seq.T, a.ld, kGlrRowsFwd) &&
                    rows_map(&maps.m[1], a.r, f32, a.d, a.seq.T, a.ld, kGlrRowsFwd) &&
                    rows_map(&maps.m[2], a.i, f32, a.d, a.seq.T, a.ld, kGlrRowsFwd);
-  const size_t smem = tma ? (size_t)3 * kGlrRowsFwd * 64 * 4 + 128 : 0;
-  const dim3 grid((unsigned)std::min<int64_t>((int64_t)t.n_chunks * (a.dp >> 6), (int64_t)sm_count() * 2));
-  if (tma) {
-    const cudaError_t e = cudaFuncSetAttribute(k_glr_fwd<T, GLR_TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(k_glr_fwd<T, GLR_TMA>, grid, dim3(256), smem, st, a, t, maps);
-  }
-  return launch_pdl(pairs_ok(a, sizeof(T)) ? k_glr_fwd<T, GLR_PAIRS> : k_glr_fwd<T, GLR_SINGLE>, grid, dim3(256), 0, st, a, t, maps);
+  const size_t smem = 128 + sizeof(GlrShared) + (tma ? stages_fwd<T>() * (size_t)3 * kGlrRowsFwd * 64 * sizeof(T) : 0);
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)t.n_chunks * (a.dp >> 6), sm_count()));
+  auto kernel = tma ? k_glr_fwd<T, GLR_TMA> : pairs_ok(a, sizeof(T)) ? k_glr_fwd<T, GLR_PAIRS> : k_glr_fwd<T, GLR_SINGLE>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, grid, dim3(kThreads), smem, st, a, t, maps);
 }
 }  // namespace
 
