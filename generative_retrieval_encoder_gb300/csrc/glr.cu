@@ -60,30 +60,49 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
   return make_float2(rcpf(d.x), rcpf(d.y));
 }
 
-// The gates of two values with k = c softplus(lam): a, s, z = 1 - a^2.  SMALL: k < 1/4 for both, so s < 1/4 always.
-struct Gate2 { float2 a, s, z, sr; };
-template <bool SMALL>
-__device__ __forceinline__ Gate2 gate2(float2 r, float2 k) {
-  Gate2 g;
-  g.sr = sigmoid2(r);
-  g.s = mul2(k, g.sr);
-  const float2 s = g.s;
-  // q = 1 - e^-s: the series up to s^6 below 1/4 (the next term is below 5e-8 of it)
-  float2 p = fma2(s, two(-1.f / 720.f), two(1.f / 120.f));
-  p = fma2(s, p, two(-1.f / 24.f));
-  p = fma2(s, p, two(1.f / 6.f));
-  p = fma2(s, p, two(-0.5f));
+// The gates of two values with k = c softplus(lam): a, s and m = sqrt(1 - a^2).
+struct Gate2 { float2 a, s, m, sr; };
+// k < 1/4 for both channels, so s < 1/4: with g = sqrt(sigmoid(r)) = rsqrt(1 + e^-r), two special functions a value, and
+// polynomials (Chebyshev interpolation on [0, 1/4]) for (1 - e^-s) / s and sqrt((1 - e^-2s) / 2s), both within 1e-8.
+__device__ __forceinline__ Gate2 gate2_small(float2 r, float2 k, float2 root2k) {
+  Gate2 v;
+  const float2 e = mul2(r, two(-kLog2e));
+  const float2 d = add2(make_float2(ex2f(e.x), ex2f(e.y)), two(1.f));
+  const float2 g = make_float2(rsqf(d.x), rsqf(d.y));
+  v.sr = mul2(g, g);
+  v.s = mul2(k, v.sr);
+  const float2 s = v.s;
+  float2 p = fma2(s, two(0.0075136060f), two(-0.0414906554f));
+  p = fma2(s, p, two(0.1666510850f));
+  p = fma2(s, p, two(-0.4999995232f));
+  p = fma2(s, p, two(1.f));
+  v.a = fma2(make_float2(-s.x, -s.y), p, two(1.f));
+  float2 w = fma2(s, two(0.0123387622f), two(-0.0622048900f));
+  w = fma2(s, w, two(0.2083072215f));
+  w = fma2(s, w, two(-0.4999991953f));
+  w = fma2(s, w, two(1.f));
+  v.m = mul2(mul2(g, root2k), w);
+  return v;
+}
+// Any k: q = 1 - e^-s from the polynomial below 1/4, m = sqrt(q (2 - q)).
+__device__ __forceinline__ float sqf(float x);
+__device__ __forceinline__ Gate2 gate2_any(float2 r, float2 k) {
+  Gate2 v;
+  v.sr = sigmoid2(r);
+  v.s = mul2(k, v.sr);
+  const float2 s = v.s, t = mul2(s, two(-kLog2e));
+  float2 p = fma2(s, two(0.0075136060f), two(-0.0414906554f));
+  p = fma2(s, p, two(0.1666510850f));
+  p = fma2(s, p, two(-0.4999995232f));
   p = fma2(s, p, two(1.f));
   float2 q = mul2(s, p);
-  g.a = add2(two(1.f), make_float2(-q.x, -q.y));
-  if (!SMALL) {
-    const float2 t = mul2(s, two(-kLog2e));
-    const float2 e = make_float2(ex2f(t.x), ex2f(t.y));
-    if (s.x >= 0.25f) { q.x = 1.f - e.x; g.a.x = e.x; }
-    if (s.y >= 0.25f) { q.y = 1.f - e.y; g.a.y = e.y; }
-  }
-  g.z = mul2(q, add2(two(2.f), make_float2(-q.x, -q.y)));
-  return g;
+  v.a = add2(two(1.f), make_float2(-q.x, -q.y));
+  const float2 e = make_float2(ex2f(t.x), ex2f(t.y));
+  if (s.x >= 0.25f) { q.x = 1.f - e.x; v.a.x = e.x; }
+  if (s.y >= 0.25f) { q.y = 1.f - e.y; v.a.y = e.y; }
+  const float2 z = mul2(q, add2(two(2.f), make_float2(-q.x, -q.y)));
+  v.m = make_float2(sqf(z.x), sqf(z.y));
+  return v;
 }
 __device__ __forceinline__ float sqf(float x) {
   float y;
@@ -202,22 +221,32 @@ __device__ __forceinline__ Chain chain_of(const GlrArgs& a, const GlrTiles& t, i
   c.last = (int)n - 1;
   return c;
 }
-// The words that chunk c.k reads: those of the chunks before it in its group, of the groups before its own in the larger
-// group, and the state after the last larger group.  ask() asks for all of them at once, before they are needed; near()
-// and far() wait for those that were not there yet and compose them: the chunks of the group, and the state that the
-// group begins with.  What a group does is published between the two, so no group waits for another's.
-constexpr uint32_t kPolls = 1u << 20;  // of a wait inside a CTA: a second or so at the least
+// The 31 words that chunk c.k reads, from the oldest on: the state after the last larger group, what the groups before its
+// own in the larger group do, what the chunks before it in its group do.  Four parts of 8 (the last of 7), a thread of
+// each for every channel: ask() asks for a thread's at once, before they are needed; answer() waits for those that were
+// not there yet, again together, and composes them.
 constexpr uint64_t kIdentity = 0xBF80000000000000ull;  // h -> 1 h + 0
-struct Words { uint64_t chunk[15], group[15], large; };
-__device__ __forceinline__ void ask(const Chain& c, int64_t dp, Words& w) {
-  const int l = c.k >> 8, n1 = c.k & 15, n2 = c.k >> 4 & 15;
-  const uint64_t* p = c.chunk + (int64_t)(c.k - n1) * dp;
+struct Words { uint64_t w[8]; };
+__device__ __forceinline__ const uint64_t* words_at(const Chain& c, int64_t dp, int part) {
+  const int l = c.k >> 8;
+  return part >= 2 ? c.chunk + (int64_t)((c.k & ~15) + (part - 2) * 8) * dp : c.group + (int64_t)((l << 4) + part * 8 - 1) * dp;
+}
+// The word j of a part exists (the rest count as identities).
+__device__ __forceinline__ bool word_is(const Chain& c, int part, int j) {
+  if (part >= 2) return (part - 2) * 8 + j < (c.k & 15);
+  if (part == 0 && j == 0) return c.k >= 256;
+  return part * 8 + j - 1 < (c.k >> 4 & 15);
+}
+__device__ __forceinline__ uint64_t peek_word(const Chain& c, const uint64_t* p, int64_t dp, int part, int j) {
+  return peek(part == 0 && j == 0 ? c.large + (int64_t)((c.k >> 8) - 1) * dp : p + j * dp);
+}
+__device__ __forceinline__ void ask(const Chain& c, int64_t dp, int part, Words& v) {
+  const uint64_t* p = words_at(c, dp, part);
 #pragma unroll
-  for (int j = 0; j < 15; ++j, p += dp) w.chunk[j] = j < n1 ? peek(p) : kIdentity;
-  p = c.group + (int64_t)(l << 4) * dp;
-#pragma unroll
-  for (int j = 0; j < 15; ++j, p += dp) w.group[j] = j < n2 ? peek(p) : kIdentity;
-  w.large = l > 0 ? peek(c.large + (int64_t)(l - 1) * dp) : kIdentity;
+  for (int j = 0; j < 8; ++j) {
+    v.w[j] = kIdentity;
+    if (word_is(c, part, j)) v.w[j] = peek_word(c, p, dp, part, j);
+  }
 }
 // Whether to go on asking after n vain tries: bounded, and given up at once where another wait has been.
 __device__ __forceinline__ bool patient(int n, int* err) {
@@ -227,43 +256,21 @@ __device__ __forceinline__ bool patient(int n, int* err) {
   atomicOr(err, kErrTimeout);
   return false;
 }
-__device__ __forceinline__ Map near(const Chain& c, int64_t dp, Words& w, int* err) {
+__device__ __forceinline__ Map answer(const Chain& c, int64_t dp, int part, Words& v, int* err) {
   for (int n = 0;; ++n) {
-    uint64_t there = w.chunk[0];
+    uint64_t there = v.w[0];
 #pragma unroll
-    for (int j = 1; j < 15; ++j) there &= w.chunk[j];
+    for (int j = 1; j < 8; ++j) there &= v.w[j];
     if (there >> 63 || !patient(n, err)) break;
-    const uint64_t* p = c.chunk + (int64_t)(c.k & ~15) * dp;
+    const uint64_t* p = words_at(c, dp, part);
 #pragma unroll
-    for (int j = 0; j < 15; ++j, p += dp)
-      if (!(w.chunk[j] >> 63)) w.chunk[j] = peek(p);
+    for (int j = 0; j < 8; ++j)
+      if (!(v.w[j] >> 63)) v.w[j] = peek_word(c, p, dp, part, j);
   }
   Map m{1.f, 0.f, false};
 #pragma unroll
-  for (int j = 0; j < 15; ++j) m = then(m, map_of(w.chunk[j]));
+  for (int j = 0; j < 8; ++j) m = then(m, map_of(v.w[j]));
   return m;
-}
-__device__ __forceinline__ float far(const Chain& c, int64_t dp, Words& w, int* err) {
-  const int l = c.k >> 8;
-  if (c.k < 16) return 0.f;
-  for (int n = 0;; ++n) {
-    uint64_t there = w.large;
-#pragma unroll
-    for (int j = 0; j < 15; ++j) there &= w.group[j];
-    if (there >> 63 || !patient(n, err)) break;
-    const uint64_t* p = c.group + (int64_t)(l << 4) * dp;
-#pragma unroll
-    for (int j = 0; j < 15; ++j, p += dp)
-      if (!(w.group[j] >> 63)) w.group[j] = peek(p);
-    if (!(w.large >> 63)) w.large = peek(c.large + (int64_t)(l - 1) * dp);
-  }
-  float h = __uint_as_float((uint32_t)w.large);
-#pragma unroll
-  for (int j = 0; j < 15; ++j) {
-    const Map m = map_of(w.group[j]);
-    h = m.reset ? m.H : fmaf(m.A, h, m.H);
-  }
-  return h;
 }
 
 // ------------------------------------------------------------ tiles
@@ -294,9 +301,8 @@ __device__ __forceinline__ void store2(void* base, int64_t o, int n, float2 v) {
   if (n > 1) p[1] = from_f<T>(v.y);
 }
 
-constexpr int kWarps = 16;                   // that work on rows
-constexpr int kScan = 2;                     // that work on the states between tiles, a lane a channel
-constexpr int kThreads = (kWarps + kScan + 1) * 32;  // and one that takes tiles
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kCtasFwd = 2;                  // an SM's
 constexpr int kPerF = kGlrRowsFwd / kWarps;  // a warp's rows; a lane has two channels of each
 
 // How a tile's rows are read: copied ahead into shared memory (rows of 16-byte pieces), or straight into registers by
@@ -354,7 +360,7 @@ __device__ __forceinline__ float2 lds2(const T* p) {
 // PLAIN: every row is inside one sequence.  sm: the lane's first row of x in shared memory, r and i one and two tiles on.
 template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
 __device__ __forceinline__ void local_rows(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch,
-                                           int nch, float2 ka, float2 (&da)[PER], float2 (&u)[PER], float2& A, float2& H) {
+                                           int nch, float2 ka, float2 root2k, float2 (&da)[PER], float2 (&u)[PER], float2& A, float2& H) {
   const int64_t step = a.reverse ? -a.ld : a.ld;
   int64_t o = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.ld + ch;
   A = two(1.f);
@@ -374,9 +380,9 @@ __device__ __forceinline__ void local_rows(const GlrArgs& a, const T* sm, const 
       x = load2<T, LOAD == GLR_PAIRS>(a.x, o, n);
       o += step;
     }
-    const Gate2 g = gate2<SMALL>(r, ka);
+    const Gate2 g = SMALL ? gate2_small(r, ka, root2k) : gate2_any(r, ka);
     da[q] = g.a;
-    u[q] = mul2(make_float2(sqf(g.z.x), sqf(g.z.y)), mul2(sigmoid2(i), x));
+    u[q] = mul2(g.m, mul2(sigmoid2(i), x));
     if (!PLAIN) {
       if (!(f.V >> q & 1)) {
         da[q] = two(1.f);
@@ -399,178 +405,137 @@ __device__ __forceinline__ void local_rows(const GlrArgs& a, const T* sm, const 
 
 struct GlrMaps { CUtensorMap m[3]; };  // x, r, i
 
-template <typename T> constexpr int stages_fwd() { return sizeof(T) == 2 ? 3 : 2; }
+// Tiles in shared memory at once.
+template <typename T> constexpr int stages_fwd() { return sizeof(T) == 2 ? 2 : 1; }
 
 // Shared memory of a CTA of the forward, after its tiles of x, r and i.
 struct GlrShared {
-  float2 agg[2][kWarps][64];      // {A, H} of each warp's rows; A = -1: a sequence starts in them
-  float enter[2][kWarps][64];     // the state that enters each warp's rows
-  Tile tile[8];
-  int first[2];                   // the tile's first row begins a sequence
-  uint64_t full[3], empty[3], agg_bar[2], enter_bar[2], tile_bar[8];
-  int fail;
+  float2 agg[kWarps][64];     // {A, H} of each warp's rows (A = -1: a sequence starts in them), then the state that enters them
+  float2 before[4][64];       // each part of the words before, composed; A = -1 as above
+  Tile tile[2];
+  uint64_t full[2];
 };
+__device__ __forceinline__ float2 pack_map(const Map& m) { return make_float2(m.reset ? -1.f : m.A, m.H); }
+__device__ __forceinline__ Map map_at(float2 g) { return Map{g.x, g.y, g.x == -1.f}; }
 
-// Forward: one pass, x, r and i read once and y written once.  Bound by the instructions of the gates (five special
-// functions a value) and by memory.  One CTA an SM keeps taking tiles: 16 warps form the gates of tile n (copied ahead
-// into shared memory) and then, with the state that enters tile n - 1, its outputs; its decays wait in registers in
-// between, the time in which two more warps, a lane a channel, compose the states across tiles (they alone wait for
-// other CTAs); one more takes tiles and copies them.
-// Every barrier's phase is seen by all who wait for it before it can pass again: agg of tile n + 2 takes the outputs of
-// tile n, those take enter of tile n, and that takes both scan warps past agg of tile n; empty and full alternate;
-// tile n + 8 is taken after the outputs of tile n.
+// Forward: one pass, x, r and i read once and y written once.  Bound by the instructions of the gates (four special
+// functions a value) and by memory.  Two CTAs an SM keep taking tiles, so that one's wait for the state between tiles
+// is another's arithmetic; a tile's rows are copied to shared memory while an earlier one is worked on.
 template <typename T, int LOAD>
-__global__ void __launch_bounds__(kThreads, 1) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
+__global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
   constexpr int PER = kPerF, CH = kGlrRowsFwd, ST = stages_fwd<T>();
   constexpr uint32_t BYTES = 3 * CH * 64 * sizeof(T), ALL = (1u << PER) - 1;
   extern __shared__ __align__(128) uint8_t raw[];
   pdl_enter();
   if (a.err && *a.err) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cc = tid & 63, part = tid >> 6;
   uint8_t* tiles = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
   GlrShared& sh = *reinterpret_cast<GlrShared*>(tiles + (LOAD == GLR_TMA ? ST * BYTES : 0));
-  const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty), agg_bar = smem_u32(sh.agg_bar),
-                 enter_bar = smem_u32(sh.enter_bar), tile_bar = smem_u32(sh.tile_bar);
-  if (threadIdx.x == 0) {
-    for (int st = 0; st < ST; ++st) {
-      mbar_init(full + 8 * st, 1);
-      mbar_init(empty + 8 * st, kWarps);
+  const uint32_t full = smem_u32(sh.full);
+  const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
+
+  // thread 0: tile o into stage st
+  auto fetch = [&](const Tile& o, int st) {
+    sh.tile[st] = o;
+    if (LOAD == GLR_TMA && o.k >= 0) {
+      mbar_expect_tx(full + 8 * st, BYTES);
+#pragma unroll
+      for (int m = 0; m < 3; ++m)
+        tma_load_2d(smem_u32(tiles) + st * BYTES + m * (BYTES / 3), &maps.m[m], full + 8 * st, o.ch0, (int)o.c.r0);
     }
-    for (int q = 0; q < 2; ++q) {
-      mbar_init(agg_bar + 8 * q, kWarps);
-      mbar_init(enter_bar + 8 * q, kScan);
+  };
+  auto take = [&]() {
+    const unsigned t = (unsigned)atomicAdd(a.ticket, 1ull);
+    Tile o;
+    o.k = -1;
+    if (t < total) o = tile_of<CH>(a, tl, t, a.reverse);
+    return o;
+  };
+  Tile next;  // thread 0: the tile after those fetched
+  if (tid == 0) {
+    if (LOAD == GLR_TMA) {
+      for (int st = 0; st < ST; ++st) mbar_init(full + 8 * st, 1);
+      mbar_init_fence();
     }
-    for (int q = 0; q < 8; ++q) mbar_init(tile_bar + 8 * q, 1);
-    mbar_init_fence();
-    sh.fail = 0;
+    for (int st = 0; st < ST; ++st) fetch(take(), st);
+    next = take();
   }
   __syncthreads();
 
-  if (warp == kWarps + kScan) {
-    // ---- tiles
-    if (lane != 0) return;
-    const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
-    unsigned t = (unsigned)atomicAdd(a.ticket, 1ull);
-    int n = 0, held = 0;  // held: the first tile that may still be on its way at the end
-    for (;; ++n) {
-      const int st = n % ST;
-      Tile o;
-      o.k = -1;
-      if (t < total) o = tile_of<CH>(a, tl, t, a.reverse);
-      if (n >= ST && !mbar_wait(empty + 8 * st, (n / ST - 1) & 1, &sh.fail, kPolls)) break;
-      held = max(0, n - ST + 1);
-      sh.tile[n & 7] = o;
-      mbar_arrive(tile_bar + 8 * (n & 7));
-      if (LOAD == GLR_TMA && t < total) {
-        mbar_expect_tx(full + 8 * st, BYTES);
-#pragma unroll
-        for (int m = 0; m < 3; ++m)
-          tma_load_2d(smem_u32(tiles) + st * BYTES + m * (BYTES / 3), &maps.m[m], full + 8 * st, o.ch0, (int)o.c.r0);
-      } else {
-        mbar_arrive(full + 8 * st);
-      }
-      if (t >= total) break;
-      t = (unsigned)atomicAdd(a.ticket, 1ull);
+  for (int it = 0;; ++it) {
+    const int st = it % ST;
+    const Tile t = sh.tile[st];
+    const int k = t.k;
+    if (k < 0) break;
+    const Chain chain = chain_of(a, tl, t.c.b, k, t.ch0 + cc);
+    Words words;
+    ask(chain, a.dp, part, words);
+    // the lane's rows
+    const int ch = t.ch0 + 2 * lane, nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
+    const int j0 = warp * PER;
+    const float2 ka = *(const float2*)(a.kd + ch);
+    Flags f{ALL, ALL, 0, 0};
+    if (!t.inner) f = flags_of<CH, PER>(a, t.c, tl.per_seq, j0, lane);
+    const bool inner = LOAD == GLR_TMA && f.V == ALL && f.F == 0;
+    const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
+    if (LOAD == GLR_TMA && !mbar_wait_bounded(full + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
+    float2 da[PER], u[PER], A, H;
+    if (inner && __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f)) {
+      const float2 root2k = make_float2(sqf(2.f * ka.x), sqf(2.f * ka.y));
+      local_rows<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, root2k, da, u, A, H);
+    } else if (inner) {
+      local_rows<T, LOAD, false, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, u, A, H);
+    } else {
+      local_rows<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, u, A, H);
     }
-    // the copies end before the CTA does, whatever became of the other warps
-    for (int m = held; m < n; ++m) mbar_wait(full + 8 * (m % ST), (m / ST) & 1, &sh.fail, kPolls);
-    if (sh.fail) atomicOr(a.err_out, kErrTimeout);
-    return;
-  }
-
-  if (warp >= kWarps) {
-    // ---- the states between tiles
-    const int cc = (warp - kWarps) * 32 + lane;
-    for (int n = 0;; ++n) {
-      const int q = n & 1;
-      if (!mbar_wait(tile_bar + 8 * (n & 7), (n >> 3) & 1, &sh.fail, kPolls)) break;
-      const Tile& t = sh.tile[n & 7];
-      const int k = t.k, ch = t.ch0 + cc;
-      if (k < 0) break;
-      const Chain chain = chain_of(a, tl, t.c.b, k, ch);
-      Words words;
-      ask(chain, a.dp, words);
-      if (!mbar_wait(agg_bar + 8 * q, (n >> 1) & 1, &sh.fail, kPolls)) break;
-      Map tot{1.f, 0.f, false};
+    *(float4*)&sh.agg[warp][2 * lane] = f.F ? make_float4(-1.f, H.x, -1.f, H.y) : make_float4(A.x, H.x, A.y, H.y);
+    // whether the chunk's first row begins a sequence: then nothing enters
+    const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && k > 0;
+    if (tid == 0) fetch(next, st);
+    Map tot{1.f, 0.f, false};
+    if (part == 3) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 g = sh.agg[q][w][cc];
-        tot = then(tot, Map{g.x, g.y, g.x == -1.f});
-      }
+      for (int w = 0; w < kWarps; ++w) tot = then(tot, map_at(sh.agg[w][cc]));
       if (k < chain.last) publish(chain.chunk + (int64_t)k * a.dp, tot);
-      const bool need = !sh.first[q] && k > 0;
-      Map grp{1.f, 0.f, false};
-      if (need) grp = near(chain, a.dp, words, a.err_out);
-      if ((k & 15) == 15 && k < chain.last) publish(chain.group + (int64_t)(k >> 4) * a.dp, then(grp, tot));
+    }
+    if (need && (part >= 2 || k >= 16)) sh.before[part][cc] = pack_map(answer(chain, a.dp, part, words, a.err_out));
+    if ((k & 15) == 15 && k < chain.last && part >= 2) {  // what the group does takes no other group: it does not wait for parts 0 and 1
+      named_bar(1, 128);
+      if (part == 3) publish(chain.group + (int64_t)(k >> 4) * a.dp, need ? then(then(map_at(sh.before[2][cc]), map_at(sh.before[3][cc])), tot) : tot);
+    }
+    if (need) __syncthreads();
+    if (part == 3) {
       float h = 0.f;
       if (need) {
-        h = far(chain, a.dp, words, a.err_out);
-        h = grp.reset ? grp.H : fmaf(grp.A, h, grp.H);
+        Map o{1.f, 0.f, false};
+        if (k >= 16) o = then(map_at(sh.before[0][cc]), map_at(sh.before[1][cc]));
+        h = then(o, then(map_at(sh.before[2][cc]), map_at(sh.before[3][cc]))).H;
       }
       if ((k & 255) == 255 && k < chain.last)
         publish(chain.large + (int64_t)(k >> 8) * a.dp, Map{0.f, tot.reset ? tot.H : fmaf(tot.A, h, tot.H), true});
+      float2 g[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) g[w] = sh.agg[w][cc];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        sh.enter[q][w][cc] = h;
-        if ((w * PER) % kGlrChunk == 0 && a.saved && ch < a.d) {  // the backward's chunks are of kGlrChunk rows
-          const int p = a.reverse ? CH - kGlrChunk - w * PER : w * PER;  // physical place of the piece in the chunk
+        sh.agg[w][cc].x = h;
+        if ((w * PER) % kGlrChunk == 0 && a.saved && t.ch0 + cc < a.d) {  // the backward's chunks are of kGlrChunk rows
+          const int p = a.reverse ? CH - kGlrChunk - w * PER : w * PER;   // physical place of the piece in the chunk
           if (p < t.c.nr) {
             const int64_t piece = tl.per_seq ? (int64_t)t.c.b * a.per_seq + (t.c.k + p) / kGlrChunk : (t.c.r0 + p) / kGlrChunk;
-            a.saved[piece * a.d + ch] = h;
+            a.saved[piece * a.d + t.ch0 + cc] = h;
           }
         }
-        const float2 g = sh.agg[q][w][cc];
-        h = g.x == -1.f ? g.y : fmaf(g.x, h, g.y);
+        h = g[w].x == -1.f ? g[w].y : fmaf(g[w].x, h, g[w].y);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(enter_bar + 8 * q);
     }
-    return;
-  }
-
-  // ---- rows
-  struct Held { uint32_t f; };  // in, V, F, E: eight bits each
-  constexpr uint32_t INNER = ALL | ALL << 8;
-  const int j0 = warp * PER;
-  // tile n: gates, decays held in da and u
-  auto begin = [&](int n, float2 (&da)[PER], float2 (&u)[PER], Held& hd) -> bool {
-    const int st = n % ST, q = n & 1;
-    if (!mbar_wait(full + 8 * st, (n / ST) & 1, &sh.fail, kPolls)) return false;
-    const Tile& t = sh.tile[n & 7];
-    if (t.k < 0) return false;
-    const int ch = t.ch0 + 2 * lane;
-    const float2 ka = *(const float2*)(a.kd + ch);
-    const bool small = __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
-    const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
-    Flags f{ALL, ALL, 0, 0};
-    if (!t.inner) f = flags_of<CH, PER>(a, t.c, tl.per_seq, j0, lane);
-    hd.f = f.in | f.V << 8 | f.F << 16 | f.E << 24;
-    float2 A, H;
-    if (LOAD == GLR_TMA && (hd.f & 0xffffffu) == INNER) {
-      if (small) local_rows<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, a.d - ch, ka, da, u, A, H);
-      else local_rows<T, LOAD, false, true, PER, CH>(a, sm, t.c, f, j0, ch, a.d - ch, ka, da, u, A, H);
-    } else {
-      local_rows<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, a.d - ch, ka, da, u, A, H);
-    }
-    *(float4*)&sh.agg[q][warp][2 * lane] = f.F ? make_float4(-1.f, H.x, -1.f, H.y) : make_float4(A.x, H.x, A.y, H.y);
-    if (threadIdx.x == 0) sh.first[q] = f.F & 1;
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(agg_bar + 8 * q);
-      mbar_arrive(empty + 8 * st);
-    }
-    return true;
-  };
-  // tile n: the rows again, from the state that enters them
-  auto finish = [&](int n, const float2 (&da)[PER], const float2 (&u)[PER], const Held& hd) -> bool {
-    const int q = n & 1;
-    if (!mbar_wait(enter_bar + 8 * q, (n >> 1) & 1, &sh.fail, kPolls)) return false;
-    float2 h = *(const float2*)&sh.enter[q][warp][2 * lane];
-    const Tile& t = sh.tile[n & 7];
-    const int ch = t.ch0 + 2 * lane, nch = a.d - ch;
+    __syncthreads();
+    // the rows again, from the state that enters them
+    const float4 e = *(const float4*)&sh.agg[warp][2 * lane];
+    float2 h = make_float2(e.x, e.z);
     const int64_t step = a.reverse ? -a.d : a.d;
     int64_t o = row_at<CH>(a, t.c, j0) * a.d + ch;
-    if (LOAD == GLR_TMA && hd.f == INNER) {
+    if (inner && (!a.hT || f.E == 0)) {
       if (nch > 0) {
         T* y = (T*)a.y + o;
 #pragma unroll
@@ -580,7 +545,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_glr_fwd(const GlrArgs a, const 
         }
       }
     } else {
-      const Flags f{hd.f & 255u, hd.f >> 8 & 255u, hd.f >> 16 & 255u, hd.f >> 24};
 #pragma unroll
       for (int p = 0; p < PER; ++p, o += step) {
         if (f.F >> p & 1) h = u[p];
@@ -589,24 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_glr_fwd(const GlrArgs a, const 
         if (a.hT && (f.E >> p & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + p)) * a.d + ch, nch, h);
       }
     }
-    return true;
-  };
-  float2 da0[PER], u0[PER], da1[PER], u1[PER];
-  Held h0, h1;
-  if (!begin(0, da0, u0, h0)) return;
-  for (int n = 1;; n += 2) {
-    const bool b1 = begin(n, da1, u1, h1);
-    if (!finish(n - 1, da0, u0, h0) || !b1) break;
-    const bool b2 = begin(n + 1, da0, u0, h0);
-    if (!finish(n, da1, u1, h1) || !b2) break;
+    if (tid == 0 && next.k >= 0) next = take();
   }
 }
 
 struct Gate { float a, s, m, sm, sr; };
 __device__ __forceinline__ Gate gate_of(float r, float k) {
-  const Gate2 v = gate2<false>(two(r), two(k));
-  const float rs = v.z.x >= 1.2e-38f ? rsqf(v.z.x) : 0.f;
-  return Gate{v.a.x, v.s.x, v.z.x * rs, v.s.x * rs, v.sr.x};
+  const Gate2 v = gate2_any(two(r), two(k));
+  return Gate{v.a.x, v.s.x, v.m.x, v.m.x > 0.f ? v.s.x / v.m.x : 0.f, v.sr.x};
 }
 // Sequence b's first row and valid rows.
 __device__ __forceinline__ void seq_rows(const SeqDesc& s, int b, int64_t& row0, int& n) {
@@ -762,7 +716,7 @@ cudaError_t run_glr_fwd(const GlrArgs& a, const GlrTiles& t, cudaStream_t st) {
                    rows_map(&maps.m[1], a.r, f32, a.d, a.seq.T, a.ld, kGlrRowsFwd) &&
                    rows_map(&maps.m[2], a.i, f32, a.d, a.seq.T, a.ld, kGlrRowsFwd);
   const size_t smem = 128 + sizeof(GlrShared) + (tma ? stages_fwd<T>() * (size_t)3 * kGlrRowsFwd * 64 * sizeof(T) : 0);
-  const dim3 grid((unsigned)std::min<int64_t>((int64_t)t.n_chunks * (a.dp >> 6), sm_count()));
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)t.n_chunks * (a.dp >> 6), (int64_t)sm_count() * kCtasFwd));
   auto kernel = tma ? k_glr_fwd<T, GLR_TMA> : pairs_ok(a, sizeof(T)) ? k_glr_fwd<T, GLR_PAIRS> : k_glr_fwd<T, GLR_SINGLE>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

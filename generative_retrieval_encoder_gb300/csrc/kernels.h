@@ -173,8 +173,7 @@ struct DecayArgs {
 // rows, whose chunks then run side by side with the other slots') or, for packed
 // and short sequences, over all rows (per_seq = 0).
 constexpr int kGlrChunk = 64, kGlrSlot = 512;
-// Rows of a tile of the forward (a state is saved every kGlrChunk of them).
-constexpr int kGlrRowsFwd = 128;
+constexpr int kGlrRowsFwd = 128;  // rows of a tile of the forward (a state is saved every kGlrChunk of them)
 struct GlrTiles { int per_seq, n_chunks; };  // chunks of a slot (0: one stream), of the call
 struct GlrArgs {
   const void* x; const void* r; const void* i; int64_t ld;  // [T, ld]
