@@ -408,15 +408,28 @@ struct GlrMaps { CUtensorMap m[3]; };  // x, r, i
 // Tiles in shared memory at once.
 template <typename T> constexpr int stages_fwd() { return sizeof(T) == 2 ? 2 : 1; }
 
-// Shared memory of a CTA of the forward, after its tiles of x, r and i.
+// Shared memory of a CTA of the forward, after its tiles of x, r and i.  A lane's two channels are {A, A, H, H}, and A = -1
+// where a sequence starts.
 struct GlrShared {
-  float2 agg[kWarps][64];     // {A, H} of each warp's rows (A = -1: a sequence starts in them), then the state that enters them
-  float2 before[4][64];       // each part of the words before, composed; A = -1 as above
+  float4 agg[2][kWarps][32];  // of each warp's rows; tiles take turns
+  float4 before[4][32];       // of each part of the words before
   Tile tile[2];
   uint64_t full[2];
 };
-__device__ __forceinline__ float2 pack_map(const Map& m) { return make_float2(m.reset ? -1.f : m.A, m.H); }
-__device__ __forceinline__ Map map_at(float2 g) { return Map{g.x, g.y, g.x == -1.f}; }
+__device__ __forceinline__ void put_map(float4* row, int cc, const Map& m) {
+  float* p = (float*)(row + (cc >> 1)) + (cc & 1);
+  p[0] = m.reset ? -1.f : m.A;
+  p[2] = m.H;
+}
+__device__ __forceinline__ Map get_map(const float4* row, int cc) {
+  const float* p = (const float*)(row + (cc >> 1)) + (cc & 1);
+  return Map{p[0], p[2], p[0] == -1.f};
+}
+// The state after what g does to h.
+__device__ __forceinline__ float2 after(float4 g, float2 h) {
+  const float2 o = fma2(make_float2(g.x, g.y), h, make_float2(g.z, g.w));
+  return g.x == -1.f ? make_float2(g.z, g.w) : o;
+}
 
 // Forward: one pass, x, r and i read once and y written once.  Bound by the instructions of the gates (four special
 // functions a value) and by memory.  Two CTAs an SM keep taking tiles, so that one's wait for the state between tiles
@@ -488,51 +501,44 @@ __global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a,
     } else {
       local_rows<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, u, A, H);
     }
-    *(float4*)&sh.agg[warp][2 * lane] = f.F ? make_float4(-1.f, H.x, -1.f, H.y) : make_float4(A.x, H.x, A.y, H.y);
+    float4(*agg)[32] = sh.agg[it & 1];
+    agg[warp][lane] = f.F ? make_float4(-1.f, -1.f, H.x, H.y) : make_float4(A.x, A.y, H.x, H.y);
     // whether the chunk's first row begins a sequence: then nothing enters
     const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && k > 0;
     if (tid == 0) fetch(next, st);
     Map tot{1.f, 0.f, false};
-    if (part == 3) {
+    if (part == 3 && k < chain.last) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) tot = then(tot, map_at(sh.agg[w][cc]));
-      if (k < chain.last) publish(chain.chunk + (int64_t)k * a.dp, tot);
+      for (int w = 0; w < kWarps; ++w) tot = then(tot, get_map(agg[w], cc));
+      publish(chain.chunk + (int64_t)k * a.dp, tot);
     }
-    if (need && (part >= 2 || k >= 16)) sh.before[part][cc] = pack_map(answer(chain, a.dp, part, words, a.err_out));
+    if (need && (part >= 2 || k >= 16)) put_map(sh.before[part], cc, answer(chain, a.dp, part, words, a.err_out));
     if ((k & 15) == 15 && k < chain.last && part >= 2) {  // what the group does takes no other group: it does not wait for parts 0 and 1
       named_bar(1, 128);
-      if (part == 3) publish(chain.group + (int64_t)(k >> 4) * a.dp, need ? then(then(map_at(sh.before[2][cc]), map_at(sh.before[3][cc])), tot) : tot);
+      if (part == 3)
+        publish(chain.group + (int64_t)(k >> 4) * a.dp, need ? then(then(get_map(sh.before[2], cc), get_map(sh.before[3], cc)), tot) : tot);
     }
-    if (need) __syncthreads();
-    if (part == 3) {
-      float h = 0.f;
-      if (need) {
-        Map o{1.f, 0.f, false};
-        if (k >= 16) o = then(map_at(sh.before[0][cc]), map_at(sh.before[1][cc]));
-        h = then(o, then(map_at(sh.before[2][cc]), map_at(sh.before[3][cc]))).H;
-      }
-      if ((k & 255) == 255 && k < chain.last)
-        publish(chain.large + (int64_t)(k >> 8) * a.dp, Map{0.f, tot.reset ? tot.H : fmaf(tot.A, h, tot.H), true});
-      float2 g[kWarps];
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) g[w] = sh.agg[w][cc];
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        sh.agg[w][cc].x = h;
-        if ((w * PER) % kGlrChunk == 0 && a.saved && t.ch0 + cc < a.d) {  // the backward's chunks are of kGlrChunk rows
-          const int p = a.reverse ? CH - kGlrChunk - w * PER : w * PER;   // physical place of the piece in the chunk
-          if (p < t.c.nr) {
-            const int64_t piece = tl.per_seq ? (int64_t)t.c.b * a.per_seq + (t.c.k + p) / kGlrChunk : (t.c.r0 + p) / kGlrChunk;
-            a.saved[piece * a.d + t.ch0 + cc] = h;
-          }
-        }
-        h = g[w].x == -1.f ? g[w].y : fmaf(g[w].x, h, g[w].y);
+    // the state that enters the warp's rows
+    float2 h = two(0.f);
+    if (need) {
+      __syncthreads();
+      if (k >= 16) h = after(sh.before[1][lane], after(sh.before[0][lane], h));
+      h = after(sh.before[3][lane], after(sh.before[2][lane], h));
+    }
+    if ((k & 255) == 255 && k < chain.last && part == 3) {
+      const float2 c2 = make_float2(__shfl_sync(FULLM, h.x, cc >> 1), __shfl_sync(FULLM, h.y, cc >> 1));
+      const float in = cc & 1 ? c2.y : c2.x;
+      publish(chain.large + (int64_t)(k >> 8) * a.dp, Map{0.f, tot.reset ? tot.H : fmaf(tot.A, in, tot.H), true});
+    }
+    for (int w = 0; w < warp; ++w) h = after(agg[w][lane], h);
+    if (j0 % kGlrChunk == 0 && a.saved) {  // the backward's chunks are of kGlrChunk rows
+      const int p = a.reverse ? CH - kGlrChunk - j0 : j0;  // physical place of the piece in the chunk
+      if (p < t.c.nr) {
+        const int64_t piece = tl.per_seq ? (int64_t)t.c.b * a.per_seq + (t.c.k + p) / kGlrChunk : (t.c.r0 + p) / kGlrChunk;
+        store2<float, false>(a.saved, piece * a.d + ch, nch, h);
       }
     }
-    __syncthreads();
     // the rows again, from the state that enters them
-    const float4 e = *(const float4*)&sh.agg[warp][2 * lane];
-    float2 h = make_float2(e.x, e.z);
     const int64_t step = a.reverse ? -a.d : a.d;
     int64_t o = row_at<CH>(a, t.c, j0) * a.d + ch;
     if (inner && (!a.hT || f.E == 0)) {
