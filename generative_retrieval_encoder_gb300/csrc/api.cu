@@ -383,7 +383,8 @@ GlrTiles glr_tiles(const GlrPlan& p, int rows) {
   t.n_chunks = t.per_seq ? t.per_seq * p.n_seq : cdiv(p.T, rows);
   return t;
 }
-struct GlrLayout { size_t err, ticket, marks, zero_bytes, kd, words, n_words, part, total; };
+constexpr int kDlamRows = 16;  // partial sums of dlam between its two kernels
+struct GlrLayout { size_t err, ticket, marks, zero_bytes, kd, words, n_words, part, part2, total; };
 GlrLayout glr_layout(const GlrPlan& p, int op) {
   Cursor c;
   GlrLayout l{};
@@ -392,11 +393,14 @@ GlrLayout glr_layout(const GlrPlan& p, int op) {
   if (p.mode == SEQ_VARLEN) l.marks = c.take((size_t)cdiv(p.T, 64) * 8);
   l.zero_bytes = c.off;
   l.kd = c.take(glr_dp(p) * 4);
-  const GlrTiles t = glr_tiles(p, kGlrRowsFwd);
+  const GlrTiles t = glr_tiles(p, op == GBLA_OP_GLR_FORWARD ? kGlrRowsFwd : kGlrChunk);
   const size_t slots = t.per_seq ? p.n_seq : 1, n = t.per_seq ? t.per_seq : t.n_chunks;
   l.n_words = (t.n_chunks + slots * ((n + 15) / 16) + slots * ((n + 255) / 256)) * glr_dp(p);
   l.words = c.take(l.n_words * 8);
-  if (op == GBLA_OP_GLR_BACKWARD) l.part = c.take((size_t)p.n_seq * p.d * 4);
+  if (op == GBLA_OP_GLR_BACKWARD) {
+    l.part = c.take((size_t)t.n_chunks * p.d * 4);
+    l.part2 = c.take((size_t)kDlamRows * p.d * 4);
+  }
   l.total = c.off;
   return l;
 }
@@ -1091,12 +1095,18 @@ gbla_status glr_backward(const gbla_shape* shape, const void* x, const void* r, 
   a.dy = dy; a.dhT = dhT; a.dx = dx; a.dr = dr; a.di = di; a.ldd = ldd; a.dh0 = dh0;
   a.dlam_part = dlam ? at<float>(ws, c.l.part) : nullptr;
   if ((s = glr_check_seqs(c)) != GBLA_OK) return s;
-  GBLA_CHECK(launch_glr_bwd(a, c.p.f32, c.st), "glr bwd");
+  GBLA_CHECK(launch_glr_bwd(a, glr_tiles(c.p, kGlrChunk), c.p.f32, c.st), "glr bwd");
   if (dlam) {
-    ColsumJobs js{};
-    js.j[js.n++] = ColsumJob{a.dlam_part, c.p.n_seq, c.p.d, c.p.d, dlam, nullptr, 0};
-    GBLA_CHECK(launch_colsums(js, c.st), "glr dlam");
+    const int rows = std::min(kDlamRows, c.p.n_chunks);
+    float* sums = at<float>(ws, c.l.part2);
+    GBLA_CHECK(launch_glr_dlam(a, c.p.n_chunks, rows, rows > 1 ? sums : dlam, c.st), "glr dlam");
+    if (rows > 1) {
+      ColsumJobs js{};
+      js.j[js.n++] = ColsumJob{sums, rows, c.p.d, c.p.d, dlam, nullptr, 0};
+      GBLA_CHECK(launch_colsums(js, c.st), "glr dlam");
+    }
   }
+  if (dh0 && c.p.mode != SEQ_DENSE) GBLA_CHECK(launch_glr_empty(a, dhT, dh0, c.st), "glr empty");
   return GBLA_OK;
 }
 

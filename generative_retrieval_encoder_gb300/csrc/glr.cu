@@ -42,7 +42,6 @@ __device__ __forceinline__ float rsqf(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sigmoid_f(float x) { return rcpf(1.f + ex2f(-kLog2e * x)); }
 
 // softplus(lam), and sigmoid(lam) / softplus(lam) (1 - e^lam / 2 + .. for small e^lam).
 __device__ __forceinline__ float softplus_f(float l) { return fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))); }
@@ -563,83 +562,301 @@ __global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a,
   }
 }
 
-struct Gate { float a, s, m, sm, sr; };
-__device__ __forceinline__ Gate gate_of(float r, float k) {
-  const Gate2 v = gate2_any(two(r), two(k));
-  return Gate{v.a.x, v.s.x, v.m.x, v.m.x > 0.f ? v.s.x / v.m.x : 0.f, v.sr.x};
-}
-// Sequence b's first row and valid rows.
-__device__ __forceinline__ void seq_rows(const SeqDesc& s, int b, int64_t& row0, int& n) {
-  if (s.mode == SEQ_VARLEN) {
-    row0 = s.cu[b];
-    n = s.cu[b + 1] - s.cu[b];
-  } else {
-    row0 = (int64_t)b * s.L;
-    n = s.mode == SEQ_PADDED ? s.lens[b] : s.L;
+// s / (2 sinh s) = a s / (1 - a^2), the even factor of the decay's gradient: a polynomial in s^2 below s = 1/4 (Chebyshev
+// interpolation, within 4e-8).
+template <bool SMALL>
+__device__ __forceinline__ float2 half_s_over_sinh(const Gate2& g) {
+  const float2 w = mul2(g.s, g.s);
+  float2 p = fma2(w, two(0.5f * 0.0192536078f), two(0.5f * -0.1666622013f));
+  p = fma2(w, p, two(0.5f));
+  if (!SMALL) {
+    if (g.s.x >= 0.25f) p.x = g.a.x * g.s.x * rcpf(g.m.x * g.m.x);
+    if (g.s.y >= 0.25f) p.y = g.a.y * g.s.y * rcpf(g.m.y * g.m.y);
   }
-}
-// The chunk of a row (the tiles of GlrArgs), and whether the row is its first in the direction of the recurrence.
-__device__ __forceinline__ int64_t chunk_of(const GlrArgs& a, int b, int64_t row, int64_t row0, bool& first, bool& last) {
-  const int64_t p = a.per_seq ? row - row0 : row;
-  const int64_t c = p / kGlrChunk + (a.per_seq ? (int64_t)b * a.per_seq : 0);
-  const bool lo = p % kGlrChunk == 0, hi = p % kGlrChunk == kGlrChunk - 1;
-  first = a.reverse ? hi : lo;
-  last = a.reverse ? lo : hi;
-  return c;
+  return p;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_glr_bwd(const GlrArgs a) {
-  if (a.err && *a.err) return;
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (id >= (int64_t)a.seq.n_seq * a.d) return;
-  const int b = (int)(id / a.d), ch = (int)(id % a.d);
-  int64_t row0;
-  int n;
-  seq_rows(a.seq, b, row0, n);
-  const float k = a.c * softplus_f(a.lam[ch]);
-  float w = a.dhT ? a.dhT[id] : 0.f, dl = 0.f;  // w: a_{t+1} w_{t+1}
-  int hi = n;                                   // rows [lo, hi) of the recurrence: one chunk's
-  while (hi > 0) {
-    int lo = hi - 1;
-    float before[kGlrChunk];
-    float h = 0.f;
-    for (;; --lo) {  // back to the first row of the chunk, or of the sequence
-      const int64_t row = a.reverse ? row0 + n - 1 - lo : row0 + lo;
-      bool first, last;
-      const int64_t c = chunk_of(a, b, row, row0, first, last);
-      if (lo == 0) { h = a.h0 ? a.h0[id] : 0.f; break; }
-      if (first) { h = a.saved[c * a.d + ch]; break; }
+// What the backward holds of a row: a; p = m sig(i) (dx = w p); sig(i); s; then G = -a (s h_{t-1} - u s / (2 sinh s)) in the
+// place of s (e = w G) and x (1 - sig(i)) in that of sig(i) (di = dx times it); x and dy as they came.
+template <typename T> struct RowPair;
+template <> struct RowPair<bf16> {
+  uint32_t w;
+  __device__ __forceinline__ float2 get() const { return make_float2(bf_lo(w), bf_hi(w)); }
+  __device__ __forceinline__ void set(float2 v) { w = pack_bf16(v.x, v.y); }  // exact: it was bf16
+};
+template <> struct RowPair<float> {
+  float2 v;
+  __device__ __forceinline__ float2 get() const { return v; }
+  __device__ __forceinline__ void set(float2 o) { v = o; }
+};
+
+constexpr int kPerB = kGlrChunk / kWarps;
+constexpr int kCtasBwd = 2;  // an SM's
+template <typename T> constexpr int stages_bwd() { return sizeof(T) == 2 ? 2 : 1; }
+
+template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
+__device__ __forceinline__ void local_rows_bwd(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch, int nch,
+                                               float2 ka, float2 root2k, float2 (&da)[PER], float2 (&pp)[PER], float2 (&gi)[PER],
+                                               float2 (&s)[PER], RowPair<T> (&x)[PER], RowPair<T> (&dy)[PER], float2& A, float2& H, float2& D) {
+  const int64_t step = a.reverse ? -a.ld : a.ld, stepy = a.reverse ? -a.d : a.d;
+  int64_t o = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.ld + ch, oy = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.d + ch;
+  A = two(1.f);
+  H = D = two(0.f);
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    float2 r, i;
+    if (LOAD == GLR_TMA) {
+      r = lds2(sm + CH * 64);
+      i = lds2(sm + 2 * CH * 64);
+      x[q] = *(const RowPair<T>*)sm;
+      dy[q] = *(const RowPair<T>*)(sm + 3 * CH * 64);
+      sm += a.reverse ? -64 : 64;
+    } else {
+      const int n = f.V >> q & 1 ? nch : 0;
+      r = load2<T, LOAD == GLR_PAIRS>(a.r, o, n);
+      i = load2<T, LOAD == GLR_PAIRS>(a.i, o, n);
+      x[q].set(load2<T, LOAD == GLR_PAIRS>(a.x, o, n));
+      dy[q].set(load2<T, LOAD == GLR_PAIRS>(a.dy, oy, n));
+      o += step;
+      oy += stepy;
     }
-    for (int t = lo; t < hi; ++t) {
-      const int64_t row = a.reverse ? row0 + n - 1 - t : row0 + t;
-      const int64_t o = row * a.ld + ch;
-      before[t - lo] = h;
-      const Gate g = gate_of(to_f(((const T*)a.r)[o]), k);
-      h = fmaf(g.a, h, g.m * sigmoid_f(to_f(((const T*)a.i)[o])) * to_f(((const T*)a.x)[o]));
+    const Gate2 g = SMALL ? gate2_small(r, ka, root2k) : gate2_any(r, ka);
+    da[q] = g.a;
+    s[q] = g.s;
+    gi[q] = sigmoid2(i);
+    pp[q] = mul2(g.m, gi[q]);
+    if (!PLAIN) {
+      if (!(f.V >> q & 1)) {
+        da[q] = two(1.f);
+        pp[q] = s[q] = gi[q] = two(0.f);
+        x[q].set(two(0.f));
+        dy[q].set(two(0.f));
+      }
+      if (f.F >> q & 1) {
+        float2 h = two(0.f);
+        if (a.h0) h = load2<float, false>(a.h0, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch);
+        H = fma2(da[q], h, mul2(pp[q], x[q].get()));
+        continue;
+      }
     }
-    for (int t = hi - 1; t >= lo; --t) {
-      const int64_t row = a.reverse ? row0 + n - 1 - t : row0 + t;
-      const int64_t o = row * a.ld + ch, od = row * a.ldd + ch;
-      const Gate g = gate_of(to_f(((const T*)a.r)[o]), k);
-      const float gi = sigmoid_f(to_f(((const T*)a.i)[o])), x = to_f(((const T*)a.x)[o]);
-      w += to_f(((const T*)a.dy)[row * a.d + ch]);
-      const float e = -w * (g.a * g.s * before[t - lo] - gi * x * g.a * g.a * g.sm);
-      ((T*)a.dx)[od] = from_f<T>(w * g.m * gi);
-      ((T*)a.di)[od] = from_f<T>(w * g.m * x * gi * (1.f - gi));
-      ((T*)a.dr)[od] = from_f<T>(e * (1.f - g.sr));
-      dl += e;
-      w *= g.a;
-    }
-    hi = lo;
+    H = fma2(da[q], H, mul2(pp[q], x[q].get()));
+    A = mul2(A, da[q]);
   }
-  if (a.dh0) a.dh0[id] = w;
-  if (a.dlam_part) a.dlam_part[id] = dl * dsoftplus_ratio(a.lam[ch]);
-  if (a.seq.mode == SEQ_PADDED)
-    for (int t = n; t < a.seq.L; ++t) {
-      const int64_t od = (row0 + t) * a.ldd + ch;
-      ((T*)a.dx)[od] = ((T*)a.dr)[od] = ((T*)a.di)[od] = from_f<T>(0.f);
+  if (!PLAIN && (f.F | f.E)) {  // A is the product of all decays where it counts: rows behind a start or before an end
+    A = two(1.f);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) A = mul2(A, da[q]);
+  }
+#pragma unroll
+  for (int q = PER - 1; q >= 0; --q) {
+    if (!PLAIN && (f.E >> q & 1)) D = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
+    D = mul2(da[q], add2(D, dy[q].get()));
+  }
+}
+
+struct GlrMaps4 { CUtensorMap m[4]; };  // x, r, i, dy
+
+struct GlrSharedBwd {
+  float4 agg[2][kWarps][32];   // forward: what each warp's rows do to the state; tiles take turns
+  float4 gga[2][kWarps][32];   // backward: what they do to a w
+  float4 before[4][32];        // of each part of the words of the chunks behind
+  float2 sum[2][kWarps][32];   // dlam of each warp's rows
+  Tile tile[2];
+  uint64_t full[2];
+};
+
+// Backward: one pass from each sequence's end, x, r, i and dy read once, dx, dr and di written once; the states before the
+// rows come from the chunk's saved one, the w behind them as the forward's states do.  As the forward, with tiles of
+// kGlrChunk rows: a row's held values take eleven registers a pair of channels.
+template <typename T, int LOAD>
+__global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps4 maps) {
+  constexpr int PER = kPerB, CH = kGlrChunk, ST = stages_bwd<T>();
+  constexpr uint32_t BYTES = 4 * CH * 64 * sizeof(T), ALL = (1u << PER) - 1;
+  extern __shared__ __align__(128) uint8_t raw[];
+  pdl_enter();
+  if (a.err && *a.err) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cc = tid & 63, part = tid >> 6;
+  uint8_t* tiles = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
+  GlrSharedBwd& sh = *reinterpret_cast<GlrSharedBwd*>(tiles + (LOAD == GLR_TMA ? ST * BYTES : 0));
+  const uint32_t full = smem_u32(sh.full);
+  const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
+
+  auto fetch = [&](const Tile& o, int st) {  // thread 0: tile o into stage st
+    sh.tile[st] = o;
+    if (LOAD == GLR_TMA && o.k >= 0) {
+      mbar_expect_tx(full + 8 * st, BYTES);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        tma_load_2d(smem_u32(tiles) + st * BYTES + m * (BYTES / 4), &maps.m[m], full + 8 * st, o.ch0, (int)o.c.r0);
     }
+  };
+  auto take = [&]() {
+    const unsigned t = (unsigned)atomicAdd(a.ticket, 1ull);
+    Tile o;
+    o.k = -1;
+    if (t < total) o = tile_of<CH>(a, tl, t, !a.reverse);  // the chains run against the recurrence
+    return o;
+  };
+  // dlam of a tile: its warps' sums in order
+  auto put_sum = [&](int q, int64_t piece, int ch0) {
+    if (warp != 0 || !a.dlam_part) return;
+    float2 v = two(0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v = add2(v, sh.sum[q][w][lane]);
+    store2<float, false>(a.dlam_part, piece * a.d + ch0 + 2 * lane, a.d - ch0 - 2 * lane, v);
+  };
+  Tile next;  // thread 0: the tile after those fetched
+  if (tid == 0) {
+    if (LOAD == GLR_TMA) {
+      for (int st = 0; st < ST; ++st) mbar_init(full + 8 * st, 1);
+      mbar_init_fence();
+    }
+    for (int st = 0; st < ST; ++st) fetch(take(), st);
+    next = take();
+  }
+  __syncthreads();
+
+  int64_t last_piece = 0;
+  int last_ch0 = 0;
+  int it = 0;
+  for (;; ++it) {
+    const int st = it % ST;
+    const Tile t = sh.tile[st];
+    const int k = t.k;
+    if (k < 0) break;
+    const Chain chain = chain_of(a, tl, t.c.b, k, t.ch0 + cc);
+    Words words;
+    ask(chain, a.dp, part, words);
+    const int ch = t.ch0 + 2 * lane, nch = a.d - ch;
+    const int64_t piece = tl.per_seq ? (int64_t)t.c.b * tl.per_seq + t.c.k / CH : t.c.r0 / CH;
+    float2 h = load2<float, false>(a.saved, piece * a.d + ch, nch);  // the state before the chunk's rows
+    const int j0 = warp * PER;
+    const float2 ka = *(const float2*)(a.kd + ch);
+    Flags f{ALL, ALL, 0, 0};
+    if (!t.inner) f = flags_of<CH, PER>(a, t.c, tl.per_seq, j0, lane);
+    const bool inner = LOAD == GLR_TMA && f.V == ALL && (f.F | f.E) == 0;
+    const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
+    if (LOAD == GLR_TMA && !mbar_wait_bounded(full + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
+    float2 da[PER], pp[PER], gi[PER], s[PER], A, H, D;
+    RowPair<T> x[PER], dy[PER];
+    const bool small = __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
+    if (inner && small) {
+      const float2 root2k = make_float2(sqf(2.f * ka.x), sqf(2.f * ka.y));
+      local_rows_bwd<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, root2k, da, pp, gi, s, x, dy, A, H, D);
+    } else if (inner) {
+      local_rows_bwd<T, LOAD, false, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, pp, gi, s, x, dy, A, H, D);
+    } else {
+      local_rows_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, pp, gi, s, x, dy, A, H, D);
+    }
+    const int tq = it & 1;
+    sh.agg[tq][warp][lane] = f.F ? make_float4(-1.f, -1.f, H.x, H.y) : make_float4(A.x, A.y, H.x, H.y);
+    sh.gga[tq][warp][lane] = f.E ? make_float4(-1.f, -1.f, D.x, D.y) : make_float4(A.x, A.y, D.x, D.y);
+    // whether a sequence ends with the chunk's last row: then nothing comes from behind
+    const bool need = !__syncthreads_or(warp == kWarps - 1 && (f.E >> (PER - 1) & 1)) && k > 0;
+    if (tid == 0) fetch(next, st);
+    if (it > 0) put_sum(tq ^ 1, last_piece, last_ch0);
+    last_piece = piece;
+    last_ch0 = t.ch0;
+    Map tot{1.f, 0.f, false};
+    if (part == 3 && k < chain.last) {
+#pragma unroll
+      for (int w = kWarps - 1; w >= 0; --w) tot = then(tot, get_map(sh.gga[tq][w], cc));
+      publish(chain.chunk + (int64_t)k * a.dp, tot);
+    }
+    // the states before the warp's rows, and with them what e is of w
+    for (int w = 0; w < warp; ++w) h = after(sh.agg[tq][w][lane], h);
+    const float2 rk = make_float2(ka.x > 0.f ? 1.f / ka.x : 0.f, ka.y > 0.f ? 1.f / ka.y : 0.f);
+    float2 osr[PER];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const float2 xv = x[q].get(), u = mul2(pp[q], xv);
+      if (!inner && (f.F >> q & 1)) h = a.h0 ? load2<float, false>(a.h0, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + q)) * a.d + ch, nch) : two(0.f);
+      Gate2 g;
+      g.a = da[q];
+      g.s = s[q];
+      float2 sg;
+      if (small) {
+        sg = half_s_over_sinh<true>(g);
+      } else {
+        const float2 z = fma2(make_float2(-da[q].x, -da[q].y), da[q], two(1.f));  // 1 - a^2, read where s >= 1/4
+        g.m = make_float2(sqf(z.x), sqf(z.y));
+        sg = half_s_over_sinh<false>(g);
+      }
+      const float2 su = mul2(sg, u), sh_ = mul2(s[q], h);
+      osr[q] = fma2(make_float2(-s[q].x, -s[q].y), rk, two(1.f));
+      s[q] = mul2(da[q], add2(su, make_float2(-sh_.x, -sh_.y)));  // G
+      gi[q] = fma2(make_float2(-xv.x, -xv.y), gi[q], xv);         // x (1 - sig(i))
+      h = fma2(da[q], h, u);
+    }
+    if (need && (part >= 2 || k >= 16)) put_map(sh.before[part], cc, answer(chain, a.dp, part, words, a.err_out));
+    if ((k & 15) == 15 && k < chain.last && part >= 2) {
+      named_bar(1, 128);
+      if (part == 3)
+        publish(chain.group + (int64_t)(k >> 4) * a.dp, need ? then(then(get_map(sh.before[2], cc), get_map(sh.before[3], cc)), tot) : tot);
+    }
+    // a w from behind the warp's rows
+    float2 v = two(0.f);
+    if (need) {
+      __syncthreads();
+      if (k >= 16) v = after(sh.before[1][lane], after(sh.before[0][lane], v));
+      v = after(sh.before[3][lane], after(sh.before[2][lane], v));
+    }
+    if ((k & 255) == 255 && k < chain.last && part == 3) {
+      const float2 c2 = make_float2(__shfl_sync(FULLM, v.x, cc >> 1), __shfl_sync(FULLM, v.y, cc >> 1));
+      const float in = cc & 1 ? c2.y : c2.x;
+      publish(chain.large + (int64_t)(k >> 8) * a.dp, Map{0.f, tot.reset ? tot.H : fmaf(tot.A, in, tot.H), true});
+    }
+    for (int w = kWarps - 1; w > warp; --w) v = after(sh.gga[tq][w][lane], v);
+    // the gradients, from the last row on
+    float2 dl = two(0.f);
+    const int64_t step = a.reverse ? a.ldd : -a.ldd;
+    int64_t o = row_at<CH>(a, t.c, j0 + PER - 1) * a.ldd + ch;
+#pragma unroll
+    for (int q = PER - 1; q >= 0; --q, o += step) {
+      if (!inner && (f.E >> q & 1)) v = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + q)) * a.d + ch, nch) : two(0.f);
+      const float2 w = add2(dy[q].get(), v);
+      v = mul2(da[q], w);
+      float2 dx = mul2(w, pp[q]), di = mul2(dx, gi[q]), e = mul2(w, s[q]), dr = mul2(e, osr[q]);
+      if (inner) {
+        dl = add2(dl, e);
+        if (nch > 0) {
+          store2<T, true>(a.dx, o, 2, dx);
+          store2<T, true>(a.dr, o, 2, dr);
+          store2<T, true>(a.di, o, 2, di);
+        }
+      } else {
+        const bool ok = f.V >> q & 1;
+        const int n = f.in >> q & 1 ? nch : 0;
+        if (ok) dl = add2(dl, e);
+        store2<T, LOAD != GLR_SINGLE>(a.dx, o, n, ok ? dx : two(0.f));
+        store2<T, LOAD != GLR_SINGLE>(a.dr, o, n, ok ? dr : two(0.f));
+        store2<T, LOAD != GLR_SINGLE>(a.di, o, n, ok ? di : two(0.f));
+        if (a.dh0 && (f.F >> q & 1)) store2<float, false>(a.dh0, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + q)) * a.d + ch, nch, v);
+        if (!ok) v = dy[q].get();  // (0: a row of no sequence hands nothing on, whatever entered)
+      }
+    }
+    sh.sum[tq][warp][lane] = dl;
+    if (tid == 0 && next.k >= 0) next = take();
+  }
+  __syncthreads();
+  if (it > 0) put_sum((it - 1) & 1, last_piece, last_ch0);
+}
+
+// dlam's partial rows n0 = blockIdx.y, n0 + gridDim.y, .. of 64 channels, summed in order, times the derivative of softplus over it.
+__global__ void __launch_bounds__(256) k_glr_dlam(const float* part, int64_t n, int d, const float* lam, float* out) {
+  pdl_enter();
+  __shared__ float red[4][64];
+  const int ch = blockIdx.x * 64 + (threadIdx.x & 63), p = threadIdx.x >> 6;
+  float v = 0.f;
+  if (ch < d) {
+    const int64_t step = (int64_t)gridDim.y * 4;
+#pragma unroll 8
+    for (int64_t i = blockIdx.y * 4 + p; i < n; i += step) v += part[i * d + ch];
+  }
+  red[p][threadIdx.x & 63] = v;
+  __syncthreads();
+  if (p == 0 && ch < d)
+    out[(int64_t)blockIdx.y * d + ch] = (((red[0][threadIdx.x] + red[1][threadIdx.x]) + red[2][threadIdx.x]) + red[3][threadIdx.x]) * dsoftplus_ratio(lam[ch]);
 }
 
 // c softplus(lam), the scan's words and the tile counter cleared; checks the sequence data and, for packed sequences,
@@ -734,12 +951,30 @@ cudaError_t launch_glr_fwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaSt
   return f32 ? run_glr_fwd<float>(a, t, st) : run_glr_fwd<bf16>(a, t, st);
 }
 
-cudaError_t launch_glr_bwd(const GlrArgs& a, bool f32, cudaStream_t st) {
-  const int64_t n = (int64_t)a.seq.n_seq * a.d;
-  const unsigned grid = (unsigned)((n + 255) / 256);
-  if (f32) k_glr_bwd<float><<<grid, 256, 0, st>>>(a);
-  else k_glr_bwd<bf16><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+namespace {
+template <typename T>
+cudaError_t run_glr_bwd(const GlrArgs& a, const GlrTiles& t, cudaStream_t st) {
+  constexpr bool f32 = sizeof(T) == 4;
+  GlrMaps4 maps{};
+  const bool tma = pairs_ok(a, sizeof(T)) && rows_map(&maps.m[0], a.x, f32, a.d, a.seq.T, a.ld, kGlrChunk) &&
+                   rows_map(&maps.m[1], a.r, f32, a.d, a.seq.T, a.ld, kGlrChunk) &&
+                   rows_map(&maps.m[2], a.i, f32, a.d, a.seq.T, a.ld, kGlrChunk) &&
+                   rows_map(&maps.m[3], a.dy, f32, a.d, a.seq.T, a.d, kGlrChunk);
+  const size_t smem = 128 + sizeof(GlrSharedBwd) + (tma ? stages_bwd<T>() * (size_t)4 * kGlrChunk * 64 * sizeof(T) : 0);
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)t.n_chunks * (a.dp >> 6), (int64_t)sm_count() * kCtasBwd));
+  auto kernel = tma ? k_glr_bwd<T, GLR_TMA> : pairs_ok(a, sizeof(T)) ? k_glr_bwd<T, GLR_PAIRS> : k_glr_bwd<T, GLR_SINGLE>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, grid, dim3(kThreads), smem, st, a, t, maps);
+}
+}  // namespace
+
+cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st) {
+  return f32 ? run_glr_bwd<float>(a, t, st) : run_glr_bwd<bf16>(a, t, st);
+}
+
+cudaError_t launch_glr_dlam(const GlrArgs& a, int64_t n, int rows, float* out, cudaStream_t st) {
+  return launch_pdl(k_glr_dlam, dim3((unsigned)(a.dp >> 6), (unsigned)rows), dim3(256), 0, st, (const float*)a.dlam_part, n, a.d, a.lam, out);
 }
 
 }  // namespace gbla

@@ -185,7 +185,7 @@ struct GlrArgs {
   // backward
   const void* dy; const float* dhT;                         // [T, d]; [n_seq, d] or null
   void* dx; void* dr; void* di; int64_t ldd;                // [T, ldd]
-  float* dlam_part; float* dh0;                             // dlam partial rows [..][d]; [n_seq, d] or null
+  float* dlam_part; float* dh0;                             // [chunks][d] or null; [n_seq, d] or null
   int d;
   SeqDesc seq;
   int per_seq, n_chunks;
@@ -295,7 +295,9 @@ cudaError_t launch_glr_prep(const GlrArgs& a, int64_t words, int* err, cudaStrea
 // to = from (or 0) for the sequences without tokens.
 cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st);
 cudaError_t launch_glr_fwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st);
-cudaError_t launch_glr_bwd(const GlrArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st);
+// The n partial rows of a.dlam_part in `rows` sums [rows][d] (to be summed), times sigmoid(lam) / softplus(lam).
+cudaError_t launch_glr_dlam(const GlrArgs& a, int64_t n, int rows, float* out, cudaStream_t st);
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, bool f32, cudaStream_t st, int* tiled = nullptr);
 // Writes the parameter-gradient partials to part[0 .. *nparts)[d][5].
