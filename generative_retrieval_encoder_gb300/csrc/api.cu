@@ -377,8 +377,16 @@ gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
 }
 
 size_t glr_dp(const GlrPlan& p) { return (size_t)cdiv(p.d, 64) * 64; }
+// n / d as (t + (n - t) / 2) >> s with t = the high word of n m (Granlund and Montgomery); s = -1: d = 1.
+GlrDiv glr_div(uint32_t d) {
+  int l = 0;
+  while ((1ull << l) < d) ++l;
+  return GlrDiv{(uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l - 1};
+}
 GlrTiles glr_tiles(const GlrPlan& p, int rows) {
   GlrTiles t;
+  t.by_cg = glr_div((uint32_t)cdiv(p.d, 64));
+  t.by_seq = glr_div((uint32_t)p.n_seq);
   t.per_seq = p.per_seq ? cdiv(p.L, rows) : 0;
   t.n_chunks = t.per_seq ? t.per_seq * p.n_seq : cdiv(p.T, rows);
   return t;

@@ -165,87 +165,123 @@ __device__ __forceinline__ int seq_of(const GlrArgs& a, int64_t row) {
   return lo;
 }
 
-// ------------------------------------------------------------ the scan between chunks
-// A tile publishes, per channel, what its rows do to a state that enters: h -> A h + H, as one 64-bit word {H, A}
-// (present when the top bit, A's sign, is set; A = infinity stands for "a sequence starts here: h -> H").  Chunks
-// form groups of 16 and groups of groups; a chunk that needs the state before it composes the words of the chunks
-// before it in its group, of the groups before its own in the larger group, and the state after the last larger
-// group: at most 31 words, read together.  The order of composition is fixed, so results do not depend on timing.
-// Tiles are handed out by a counter in an order in which everything a tile waits for has been handed out before:
-// the earliest unfinished tile waits for nothing unfinished, so every wait ends (and is bounded all the same).
-constexpr uint64_t kReset = 0xFF80000000000000ull;
-__device__ __forceinline__ uint64_t word(float A, float H) {
-  return (uint64_t)(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(H);
+// ------------------------------------------------------------ tiles
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kPerF = kGlrRowsFwd / kWarps;  // a warp's rows; a lane has two channels of each
+constexpr int kPerB = kGlrChunk / kWarps;
+constexpr int kCtasFwd = 2, kCtasBwd = 2;    // an SM's
+
+// How a tile's rows are read: copied ahead into shared memory (rows of 16-byte pieces), or straight into registers by
+// pairs of channels or single ones.
+enum GlrLoad { GLR_TMA = 0, GLR_PAIRS = 1, GLR_SINGLE = 2 };
+
+// A tile: channels from ch0, the chunk's rows, its place k in its slot's chain (-1: no tile) of last + 1, and where the
+// chain's words for it are.
+struct Tile {
+  int ch0, k, last;
+  int inner;        // every row is inside one sequence and neither its first nor its last
+  Span c;
+  int64_t own, near, far, large;  // the chunk's word; its group's first; the one before its larger group's first; the larger group before
+};
+__device__ __forceinline__ unsigned quotient(unsigned n, GlrDiv d) {  // n / divisor (Granlund and Montgomery's method)
+  const unsigned t = __umulhi(n, d.m);
+  return d.s < 0 ? n : (t + ((n - t) >> 1)) >> d.s;
 }
-__device__ __forceinline__ uint64_t reset_word(float H) { return kReset | __float_as_uint(H); }
-struct Map { float A, H; bool reset; };  // reset: h -> H
-__device__ __forceinline__ Map map_of(uint64_t w) {
-  Map m;
-  m.H = __uint_as_float((uint32_t)w);
-  m.A = __uint_as_float((uint32_t)(w >> 32) & 0x7fffffffu);
-  m.reset = (w >> 32) == (kReset >> 32);
-  return m;
-}
-// first m, then n
-__device__ __forceinline__ Map then(const Map& m, const Map& n) {
-  Map o;
-  o.reset = m.reset || n.reset;
-  o.H = n.reset ? n.H : fmaf(n.A, m.H, n.H);
-  o.A = m.A * n.A;  // of no use where reset
+// Tile t of the call's; back: the chain runs from the last chunk.  `word` is what tells inner (inner_of), asked for here.
+template <int CH>
+__device__ __forceinline__ Tile tile_of(const GlrArgs& a, const GlrTiles& g, unsigned t, bool back, uint64_t& word) {
+  Tile o;
+  const unsigned w = quotient(t, g.by_cg);
+  o.ch0 = (int)(t - w * (unsigned)(a.dp >> 6)) * 64;
+  const int n = g.per_seq ? g.per_seq : g.n_chunks;
+  o.last = n - 1;
+  word = 0;
+  if (g.per_seq) {
+    const unsigned q = quotient(w, g.by_seq);
+    o.c.b = (int)(w - q * (unsigned)a.seq.n_seq);
+    o.k = (int)q;
+    o.c.k = (back ? n - 1 - o.k : o.k) * CH;
+    o.c.r0 = (int64_t)o.c.b * a.seq.L + o.c.k;
+    o.c.nr = min(CH, a.seq.L - o.c.k);
+    word = a.seq.mode == SEQ_PADDED ? (uint64_t)a.seq.lens[o.c.b] : (uint64_t)a.seq.L;
+  } else {
+    o.c.b = o.c.k = 0;
+    o.k = (int)w;
+    o.c.r0 = (int64_t)(back ? n - 1 - o.k : o.k) * CH;
+    o.c.nr = (int)min((int64_t)CH, a.seq.T - o.c.r0);
+    if (a.seq.mode == SEQ_VARLEN && o.c.r0 + CH < a.seq.T) {
+      word = a.marks[(o.c.r0 + CH) >> 6] & 1;
+#pragma unroll
+      for (int j = 0; j < CH / 64; ++j) word |= a.marks[(o.c.r0 >> 6) + j];
+    }
+  }
+  // the arrays hold each slot's words in the order of its chain: of chunks, of groups of 16, of 16 groups
+  const int64_t ng = (n + 15) >> 4, nl = (n + 255) >> 8, slots = g.per_seq ? a.seq.n_seq : 1, l = o.k >> 8;
+  const int64_t chunk = (int64_t)o.c.b * n, group = (int64_t)g.n_chunks + o.c.b * ng, large = (int64_t)g.n_chunks + slots * ng + o.c.b * nl;
+  o.own = (chunk + o.k) * a.dp + o.ch0;
+  o.near = (chunk + (o.k & ~15)) * a.dp + o.ch0;
+  o.far = (group + (l << 4) - 1) * a.dp + o.ch0;
+  o.large = (large + l - 1) * a.dp + o.ch0;
   return o;
 }
-__device__ __forceinline__ uint64_t word_of(const Map& m) { return m.reset ? reset_word(m.H) : word(m.A, m.H); }
-
-__device__ __forceinline__ void publish(uint64_t* p, const Map& x) {
-  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(word_of(x)) : "memory");
+template <int CH>
+__device__ __forceinline__ int inner_of(const GlrArgs& a, const GlrTiles& g, const Tile& o, uint64_t word) {
+  if (g.per_seq) return o.c.k > 0 && o.c.k + CH < (int)word;
+  return a.seq.mode == SEQ_VARLEN && o.c.r0 + CH < a.seq.T && word == 0;
 }
-__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
-  uint64_t x;
-  asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(x) : "l"(p) : "memory");
+
+// ------------------------------------------------------------ the scan between chunks
+// A tile publishes, per channel, what its rows do to a state that enters: h -> A h + H, as one 64-bit word {H, A}
+// (present when the top bit, A's sign, is set).  A = 0: a sequence starts here, h -> H whatever h was.  Chunks form
+// groups of 16 and groups of groups; a chunk that needs the state before it composes the words of the chunks before it in
+// its group, of the groups before its own in the larger group, and the state after the last larger group: at most 31
+// words, read together.  The order of composition is fixed, so results do not depend on timing.
+// Tiles are handed out by a counter in an order in which everything a tile waits for has been handed out before:
+// the earliest unfinished tile waits for nothing unfinished, so every wait ends (and is bounded all the same).
+struct Map { float A, H; };
+struct Map2 { float2 A, H; };  // of a lane's two channels
+constexpr uint64_t kIdentity = 0xBF80000000000000ull;  // h -> 1 h + 0
+__device__ __forceinline__ uint64_t word_of(float A, float H) {
+  return (uint64_t)(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(H);
+}
+__device__ __forceinline__ Map then(Map m, Map n) {  // first m, then n
+  return Map{m.A * n.A, n.A == 0.f ? n.H : fmaf(n.A, m.H, n.H)};
+}
+__device__ __forceinline__ float2 after(const Map2& n, float2 h) {
+  const float2 o = fma2(n.A, h, n.H);
+  return make_float2(n.A.x == 0.f ? n.H.x : o.x, n.A.y == 0.f ? n.H.y : o.y);
+}
+__device__ __forceinline__ Map2 then(const Map2& m, const Map2& n) { return Map2{mul2(m.A, n.A), after(n, m.H)}; }
+// In shared memory: {A, A, H, H} of a lane's two channels.
+__device__ __forceinline__ Map2 map_at(const float4& g) { return Map2{make_float2(g.x, g.y), make_float2(g.z, g.w)}; }
+__device__ __forceinline__ float4 packed(const Map2& m) { return make_float4(m.A.x, m.A.y, m.H.x, m.H.y); }
+__device__ __forceinline__ void publish(uint64_t* p, const Map2& m) {
+  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(word_of(m.A.x, m.H.x)), "l"(word_of(m.A.y, m.H.y)) : "memory");
+}
+// x, or where `is` the word at p (a predicated load: no branch).
+__device__ __forceinline__ uint64_t peek(const uint64_t* p, bool is, uint64_t x) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %2, 0;\n @q ld.relaxed.gpu.global.b64 %0, [%1];\n}" : "+l"(x) : "l"(p), "r"((uint32_t)is) : "memory");
   return x;
 }
-// The words of a call: of chunks, groups and larger groups, each [..][dp] with dp the channels rounded up to 64.
-struct Chain {
-  uint64_t* chunk; uint64_t* group; uint64_t* large;
-  int k, last;      // this chunk's place in its chain, and the last one
-};
-__device__ __forceinline__ Chain chain_of(const GlrArgs& a, const GlrTiles& t, int s, int k, int ch) {
-  // s: the sequence slot (0 for a stream); the arrays hold each slot's words in the order of its chain
-  const int64_t n = t.per_seq ? t.per_seq : t.n_chunks, ng = (n + 15) >> 4, nl = (n + 255) >> 8;
-  Chain c;
-  c.chunk = a.words + s * n * a.dp + ch;
-  c.group = a.words + ((int64_t)t.n_chunks + s * ng) * a.dp + ch;
-  c.large = a.words + ((int64_t)t.n_chunks + (int64_t)(t.per_seq ? a.seq.n_seq : 1) * ng + s * nl) * a.dp + ch;
-  c.k = k;
-  c.last = (int)n - 1;
-  return c;
-}
-// The 31 words that chunk c.k reads, from the oldest on: the state after the last larger group, what the groups before its
-// own in the larger group do, what the chunks before it in its group do.  Four parts of 8 (the last of 7), a thread of
-// each for every channel: ask() asks for a thread's at once, before they are needed; answer() waits for those that were
-// not there yet, again together, and composes them.
-constexpr uint64_t kIdentity = 0xBF80000000000000ull;  // h -> 1 h + 0
+
+// The 31 words that a chunk reads, from the oldest on (the larger group's, 15 groups', 15 chunks'), in four parts of 8 (the
+// last of 7), a thread of each for every channel: ask() asks for a thread's at once, before they are needed; answer() waits
+// for those that were not there yet, again together, and composes them.  Words that do not exist are identities: they are
+// read from one that is.
 struct Words { uint64_t w[8]; };
-__device__ __forceinline__ const uint64_t* words_at(const Chain& c, int64_t dp, int part) {
-  const int l = c.k >> 8;
-  return part >= 2 ? c.chunk + (int64_t)((c.k & ~15) + (part - 2) * 8) * dp : c.group + (int64_t)((l << 4) + part * 8 - 1) * dp;
-}
-// The word j of a part exists (the rest count as identities).
-__device__ __forceinline__ bool word_is(const Chain& c, int part, int j) {
-  if (part >= 2) return (part - 2) * 8 + j < (c.k & 15);
-  if (part == 0 && j == 0) return c.k >= 256;
-  return part * 8 + j - 1 < (c.k >> 4 & 15);
-}
-__device__ __forceinline__ uint64_t peek_word(const Chain& c, const uint64_t* p, int64_t dp, int part, int j) {
-  return peek(part == 0 && j == 0 ? c.large + (int64_t)((c.k >> 8) - 1) * dp : p + j * dp);
-}
-__device__ __forceinline__ void ask(const Chain& c, int64_t dp, int part, Words& v) {
-  const uint64_t* p = words_at(c, dp, part);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v.w[j] = kIdentity;
-    if (word_is(c, part, j)) v.w[j] = peek_word(c, p, dp, part, j);
+__device__ __forceinline__ uint64_t peek_word(const GlrArgs& a, const Tile& t, int part, int cc, int j, bool want, uint64_t x) {
+  const int lim = part >= 2 ? (t.k & 15) - (part - 2) * 8 : (t.k >> 4 & 15) + 1 - part * 8;
+  int64_t at = (part >= 2 ? t.near + (part - 2) * 8 * a.dp : t.far + part * 8 * a.dp) + j * a.dp;
+  bool is = j < lim;
+  if (j == 0 && part == 0) {
+    at = t.large;
+    is = t.k >= 256;
   }
+  return peek(a.words + at + cc, is && want, x);
+}
+__device__ __forceinline__ void ask(const GlrArgs& a, const Tile& t, int part, int cc, Words& v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v.w[j] = peek_word(a, t, part, cc, j, true, kIdentity);
 }
 // Whether to go on asking after n vain tries: bounded, and given up at once where another wait has been.
 __device__ __forceinline__ bool patient(int n, int* err) {
@@ -255,24 +291,79 @@ __device__ __forceinline__ bool patient(int n, int* err) {
   atomicOr(err, kErrTimeout);
   return false;
 }
-__device__ __forceinline__ Map answer(const Chain& c, int64_t dp, int part, Words& v, int* err) {
+__device__ __forceinline__ Map answer(const GlrArgs& a, const Tile& t, int part, int cc, Words& v) {
   for (int n = 0;; ++n) {
     uint64_t there = v.w[0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) there &= v.w[j];
-    if (there >> 63 || !patient(n, err)) break;
-    const uint64_t* p = words_at(c, dp, part);
+    if (there >> 63 || !patient(n, a.err_out)) break;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (!(v.w[j] >> 63)) v.w[j] = peek_word(c, p, dp, part, j);
+    for (int j = 0; j < 8; ++j) v.w[j] = peek_word(a, t, part, cc, j, !(v.w[j] >> 63), v.w[j]);
   }
-  Map m{1.f, 0.f, false};
+  Map m{1.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = then(m, map_of(v.w[j]));
+  for (int j = 0; j < 8; ++j)
+    m = then(m, Map{__uint_as_float((uint32_t)(v.w[j] >> 32) & 0x7fffffffu), __uint_as_float((uint32_t)v.w[j])});
   return m;
 }
 
-// ------------------------------------------------------------ tiles
+// Shared memory of the scan: what the rows of each warp (in the chain's order) do, tiles taking turns; the parts of the words.
+struct ScanShared {
+  float4 agg[2][kWarps][32];
+  float4 before[4][32];
+};
+// After the warps' maps are in sc.agg[q]: what those before warp vw do, composed; the last warp publishes the tile's word.
+__device__ __forceinline__ Map2 scan_local(const GlrArgs& a, const Tile& t, const ScanShared& sc, int q, int vw, int lane, Map2& total) {
+  Map2 m{two(1.f), two(0.f)};
+  for (int w = 0; w < vw; ++w) m = then(m, map_at(sc.agg[q][w][lane]));
+  if (vw == kWarps - 1) {
+    total = then(m, map_at(sc.agg[q][vw][lane]));
+    if (t.k < t.last) publish(a.words + t.own + 2 * lane, total);
+  }
+  return m;
+}
+// This thread's part of the words into sc.before; a full group's word published (it takes no other group's: it does not wait
+// for parts 0 and 1).
+__device__ __forceinline__ void scan_words(const GlrArgs& a, const Tile& t, ScanShared& sc, int vw, int lane, bool need, Words& words, const Map2& total) {
+  const int part = vw >> 1, cc = (vw & 1) * 32 + lane;
+  if (need && (part >= 2 || t.k >= 16)) {
+    const Map m = answer(a, t, part, cc, words);
+    float* p = (float*)&sc.before[part][cc >> 1] + (cc & 1);
+    p[0] = m.A;
+    p[2] = m.H;
+  }
+  if ((t.k & 15) == 15 && t.k < t.last && part >= 2) {
+    named_bar(1, 128);
+    if (vw == kWarps - 1) {
+      Map2 m = total;
+      if (need) m = then(then(map_at(sc.before[2][lane]), map_at(sc.before[3][lane])), total);
+      publish(a.words + t.far + (int64_t)((t.k >> 4 & 15) + 1) * a.dp + 2 * lane, m);
+    }
+  }
+}
+// The state that enters the tile.  Whole CTAs call it (need is the same for all).
+__device__ __forceinline__ float2 scan_state(const GlrArgs& a, const Tile& t, const ScanShared& sc, int vw, int lane, bool need, const Map2& total) {
+  float2 h = two(0.f);
+  if (need) {
+    __syncthreads();
+    if (t.k >= 16) h = after(map_at(sc.before[1][lane]), after(map_at(sc.before[0][lane]), h));
+    h = after(map_at(sc.before[3][lane]), after(map_at(sc.before[2][lane]), h));
+  }
+  if ((t.k & 255) == 255 && t.k < t.last && vw == kWarps - 1)
+    publish(a.words + t.large + a.dp + 2 * lane, Map2{two(0.f), after(total, h)});
+  return h;
+}
+
+// Thread 0's side of a CTA's tiles: the ticket of a tile is drawn as soon as the one before is fetched, decoded a good while
+// later (into the ring of tiles in shared memory), and what its rows are is looked at later still, so that no step waits
+// for memory.
+struct Drawn { unsigned t; uint64_t word; };
+template <int CH>
+__device__ __forceinline__ void decode(const GlrArgs& a, const GlrTiles& tl, unsigned total, bool back, Drawn& d, Tile& o) {
+  if (d.t < total) o = tile_of<CH>(a, tl, d.t, back, d.word);
+  else o.k = -1;
+}
+
 // A pair of neighbouring channels of a row.  VEC: pairs are aligned and whole.
 template <typename T, bool VEC>
 __device__ __forceinline__ float2 load2(const void* base, int64_t o, int n) {
@@ -298,51 +389,6 @@ __device__ __forceinline__ void store2(void* base, int64_t o, int n, float2 v) {
   }
   if (n > 0) p[0] = from_f<T>(v.x);
   if (n > 1) p[1] = from_f<T>(v.y);
-}
-
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kCtasFwd = 2;                  // an SM's
-constexpr int kPerF = kGlrRowsFwd / kWarps;  // a warp's rows; a lane has two channels of each
-
-// How a tile's rows are read: copied ahead into shared memory (rows of 16-byte pieces), or straight into registers by
-// pairs of channels or single ones.
-enum GlrLoad { GLR_TMA = 0, GLR_PAIRS = 1, GLR_SINGLE = 2 };
-
-// A tile: channels from ch0, the chunk's rows, and its place k in its slot's chain (-1: no tile).
-struct Tile {
-  int ch0, k;
-  Span c;
-  int inner;        // every row is inside one sequence and neither its first nor its last
-};
-template <int CH>
-__device__ __forceinline__ Tile tile_of(const GlrArgs& a, const GlrTiles& g, unsigned t, bool back) {
-  const unsigned ncg = (unsigned)(a.dp >> 6);
-  Tile o;
-  o.ch0 = (int)(t % ncg) * 64;
-  const unsigned w = t / ncg;
-  if (g.per_seq) {
-    const unsigned q = w / (unsigned)a.seq.n_seq;
-    o.c.b = (int)(w - q * (unsigned)a.seq.n_seq);
-    o.k = (int)q;
-    o.c.k = (back ? g.per_seq - 1 - o.k : o.k) * CH;
-    o.c.r0 = (int64_t)o.c.b * a.seq.L + o.c.k;
-    o.c.nr = min(CH, a.seq.L - o.c.k);
-    const int len = a.seq.mode == SEQ_PADDED ? a.seq.lens[o.c.b] : a.seq.L;
-    o.inner = o.c.k > 0 && o.c.k + CH < len;
-  } else {
-    o.c.b = o.c.k = 0;
-    o.k = (int)w;
-    o.c.r0 = (int64_t)(back ? g.n_chunks - 1 - o.k : o.k) * CH;
-    o.c.nr = (int)min((int64_t)CH, a.seq.T - o.c.r0);
-    o.inner = 0;
-    if (a.seq.mode == SEQ_VARLEN && o.c.r0 + CH < a.seq.T) {
-      uint64_t m = a.marks[(o.c.r0 + CH) >> 6] & 1;
-#pragma unroll
-      for (int j = 0; j < CH / 64; ++j) m |= a.marks[(o.c.r0 >> 6) + j];
-      o.inner = m == 0;
-    }
-  }
-  return o;
 }
 
 // A pair of channels in shared memory.
@@ -407,32 +453,16 @@ struct GlrMaps { CUtensorMap m[3]; };  // x, r, i
 // Tiles in shared memory at once.
 template <typename T> constexpr int stages_fwd() { return sizeof(T) == 2 ? 2 : 1; }
 
-// Shared memory of a CTA of the forward, after its tiles of x, r and i.  A lane's two channels are {A, A, H, H}, and A = -1
-// where a sequence starts.
+// Shared memory of a CTA of the forward, after its tiles of x, r and i.
 struct GlrShared {
-  float4 agg[2][kWarps][32];  // of each warp's rows; tiles take turns
-  float4 before[4][32];       // of each part of the words before
-  Tile tile[2];
+  ScanShared sc;
+  Tile tile[4];                // the CTA's n-th at n & 3
   uint64_t full[2];
 };
-__device__ __forceinline__ void put_map(float4* row, int cc, const Map& m) {
-  float* p = (float*)(row + (cc >> 1)) + (cc & 1);
-  p[0] = m.reset ? -1.f : m.A;
-  p[2] = m.H;
-}
-__device__ __forceinline__ Map get_map(const float4* row, int cc) {
-  const float* p = (const float*)(row + (cc >> 1)) + (cc & 1);
-  return Map{p[0], p[2], p[0] == -1.f};
-}
-// The state after what g does to h.
-__device__ __forceinline__ float2 after(float4 g, float2 h) {
-  const float2 o = fma2(make_float2(g.x, g.y), h, make_float2(g.z, g.w));
-  return g.x == -1.f ? make_float2(g.z, g.w) : o;
-}
 
 // Forward: one pass, x, r and i read once and y written once.  Bound by the instructions of the gates (four special
-// functions a value) and by memory.  Two CTAs an SM keep taking tiles, so that one's wait for the state between tiles
-// is another's arithmetic; a tile's rows are copied to shared memory while an earlier one is worked on.
+// functions a value), by the waits between tiles and by memory.  Two CTAs an SM keep taking tiles, so that one's wait for
+// the state between tiles is another's arithmetic; a tile's rows are copied to shared memory while an earlier one is worked on.
 template <typename T, int LOAD>
 __global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
   constexpr int PER = kPerF, CH = kGlrRowsFwd, ST = stages_fwd<T>();
@@ -440,106 +470,84 @@ __global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a,
   extern __shared__ __align__(128) uint8_t raw[];
   pdl_enter();
   if (a.err && *a.err) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cc = tid & 63, part = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* tiles = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
   GlrShared& sh = *reinterpret_cast<GlrShared*>(tiles + (LOAD == GLR_TMA ? ST * BYTES : 0));
   const uint32_t full = smem_u32(sh.full);
   const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
 
-  // thread 0: tile o into stage st
-  auto fetch = [&](const Tile& o, int st) {
-    sh.tile[st] = o;
-    if (LOAD == GLR_TMA && o.k >= 0) {
+  // thread 0: the CTA's n-th tile, decoded
+  auto fetch = [&](const Drawn& d, int n) {
+    Tile& o = sh.tile[n & 3];
+    if (o.k < 0) return;
+    o.inner = inner_of<CH>(a, tl, o, d.word);
+    if (LOAD == GLR_TMA) {
+      const int st = n % ST;
       mbar_expect_tx(full + 8 * st, BYTES);
 #pragma unroll
       for (int m = 0; m < 3; ++m)
         tma_load_2d(smem_u32(tiles) + st * BYTES + m * (BYTES / 3), &maps.m[m], full + 8 * st, o.ch0, (int)o.c.r0);
     }
   };
-  auto take = [&]() {
-    const unsigned t = (unsigned)atomicAdd(a.ticket, 1ull);
-    Tile o;
-    o.k = -1;
-    if (t < total) o = tile_of<CH>(a, tl, t, a.reverse);
-    return o;
-  };
-  Tile next;  // thread 0: the tile after those fetched
+  Drawn next;
   if (tid == 0) {
     if (LOAD == GLR_TMA) {
       for (int st = 0; st < ST; ++st) mbar_init(full + 8 * st, 1);
       mbar_init_fence();
     }
-    for (int st = 0; st < ST; ++st) fetch(take(), st);
-    next = take();
+    for (int n = 0; n <= ST; ++n) {
+      next.t = (unsigned)atomicAdd(a.ticket, 1ull);
+      decode<CH>(a, tl, total, a.reverse, next, sh.tile[n & 3]);
+      if (n < ST) fetch(next, n);
+    }
   }
   __syncthreads();
 
   for (int it = 0;; ++it) {
     const int st = it % ST;
-    const Tile t = sh.tile[st];
-    const int k = t.k;
-    if (k < 0) break;
-    const Chain chain = chain_of(a, tl, t.c.b, k, t.ch0 + cc);
+    const Tile& me = sh.tile[it & 3];
+    if (me.k < 0) break;
     Words words;
-    ask(chain, a.dp, part, words);
+    ask(a, me, warp >> 1, (warp & 1) * 32 + lane, words);
     // the lane's rows
-    const int ch = t.ch0 + 2 * lane, nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
+    const int ch = me.ch0 + 2 * lane, nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
     const int j0 = warp * PER;
     const float2 ka = *(const float2*)(a.kd + ch);
     Flags f{ALL, ALL, 0, 0};
-    if (!t.inner) f = flags_of<CH, PER>(a, t.c, tl.per_seq, j0, lane);
+    if (!me.inner) f = flags_of<CH, PER>(a, me.c, tl.per_seq, j0, lane);
     const bool inner = LOAD == GLR_TMA && f.V == ALL && f.F == 0;
     const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
     if (LOAD == GLR_TMA && !mbar_wait_bounded(full + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
     float2 da[PER], u[PER], A, H;
     if (inner && __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f)) {
       const float2 root2k = make_float2(sqf(2.f * ka.x), sqf(2.f * ka.y));
-      local_rows<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, root2k, da, u, A, H);
+      local_rows<T, LOAD, true, true, PER, CH>(a, sm, me.c, f, j0, ch, nch, ka, root2k, da, u, A, H);
     } else if (inner) {
-      local_rows<T, LOAD, false, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, u, A, H);
+      local_rows<T, LOAD, false, true, PER, CH>(a, sm, me.c, f, j0, ch, nch, ka, ka, da, u, A, H);
     } else {
-      local_rows<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, u, A, H);
+      local_rows<T, LOAD, false, false, PER, CH>(a, sm, me.c, f, j0, ch, nch, ka, ka, da, u, A, H);
     }
-    float4(*agg)[32] = sh.agg[it & 1];
-    agg[warp][lane] = f.F ? make_float4(-1.f, -1.f, H.x, H.y) : make_float4(A.x, A.y, H.x, H.y);
+    sh.sc.agg[it & 1][warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
     // whether the chunk's first row begins a sequence: then nothing enters
-    const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && k > 0;
-    if (tid == 0) fetch(next, st);
-    Map tot{1.f, 0.f, false};
-    if (part == 3 && k < chain.last) {
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) tot = then(tot, get_map(agg[w], cc));
-      publish(chain.chunk + (int64_t)k * a.dp, tot);
+    const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && me.k > 0;
+    if (tid == 0) {
+      fetch(next, it + ST);
+      if (next.t < total) next.t = (unsigned)atomicAdd(a.ticket, 1ull);
     }
-    if (need && (part >= 2 || k >= 16)) put_map(sh.before[part], cc, answer(chain, a.dp, part, words, a.err_out));
-    if ((k & 15) == 15 && k < chain.last && part >= 2) {  // what the group does takes no other group: it does not wait for parts 0 and 1
-      named_bar(1, 128);
-      if (part == 3)
-        publish(chain.group + (int64_t)(k >> 4) * a.dp, need ? then(then(get_map(sh.before[2], cc), get_map(sh.before[3], cc)), tot) : tot);
-    }
-    // the state that enters the warp's rows
-    float2 h = two(0.f);
-    if (need) {
-      __syncthreads();
-      if (k >= 16) h = after(sh.before[1][lane], after(sh.before[0][lane], h));
-      h = after(sh.before[3][lane], after(sh.before[2][lane], h));
-    }
-    if ((k & 255) == 255 && k < chain.last && part == 3) {
-      const float2 c2 = make_float2(__shfl_sync(FULLM, h.x, cc >> 1), __shfl_sync(FULLM, h.y, cc >> 1));
-      const float in = cc & 1 ? c2.y : c2.x;
-      publish(chain.large + (int64_t)(k >> 8) * a.dp, Map{0.f, tot.reset ? tot.H : fmaf(tot.A, in, tot.H), true});
-    }
-    for (int w = 0; w < warp; ++w) h = after(agg[w][lane], h);
+    Map2 tot;
+    const Map2 pre = scan_local(a, me, sh.sc, it & 1, warp, lane, tot);
+    scan_words(a, me, sh.sc, warp, lane, need, words, tot);
+    float2 h = after(pre, scan_state(a, me, sh.sc, warp, lane, need, tot));
     if (j0 % kGlrChunk == 0 && a.saved) {  // the backward's chunks are of kGlrChunk rows
       const int p = a.reverse ? CH - kGlrChunk - j0 : j0;  // physical place of the piece in the chunk
-      if (p < t.c.nr) {
-        const int64_t piece = tl.per_seq ? (int64_t)t.c.b * a.per_seq + (t.c.k + p) / kGlrChunk : (t.c.r0 + p) / kGlrChunk;
+      if (p < me.c.nr) {
+        const int64_t piece = tl.per_seq ? (int64_t)me.c.b * a.per_seq + (me.c.k + p) / kGlrChunk : (me.c.r0 + p) / kGlrChunk;
         store2<float, false>(a.saved, piece * a.d + ch, nch, h);
       }
     }
     // the rows again, from the state that enters them
     const int64_t step = a.reverse ? -a.d : a.d;
-    int64_t o = row_at<CH>(a, t.c, j0) * a.d + ch;
+    int64_t o = row_at<CH>(a, me.c, j0) * a.d + ch;
     if (inner && (!a.hT || f.E == 0)) {
       if (nch > 0) {
         T* y = (T*)a.y + o;
@@ -555,10 +563,10 @@ __global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a,
         if (f.F >> p & 1) h = u[p];
         else h = fma2(da[p], h, u[p]);
         store2<T, LOAD != GLR_SINGLE>(a.y, o, f.in >> p & 1 ? nch : 0, f.V >> p & 1 ? h : two(0.f));
-        if (a.hT && (f.E >> p & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + p)) * a.d + ch, nch, h);
+        if (a.hT && (f.E >> p & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, me.c, j0 + p)) * a.d + ch, nch, h);
       }
     }
-    if (tid == 0 && next.k >= 0) next = take();
+    if (tid == 0) decode<CH>(a, tl, total, a.reverse, next, sh.tile[(it + ST + 1) & 3]);
   }
 }
 
@@ -590,8 +598,6 @@ template <> struct RowPair<float> {
   __device__ __forceinline__ void set(float2 o) { v = o; }
 };
 
-constexpr int kPerB = kGlrChunk / kWarps;
-constexpr int kCtasBwd = 2;  // an SM's
 template <typename T> constexpr int stages_bwd() { return sizeof(T) == 2 ? 2 : 1; }
 
 template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
@@ -657,11 +663,10 @@ __device__ __forceinline__ void local_rows_bwd(const GlrArgs& a, const T* sm, co
 struct GlrMaps4 { CUtensorMap m[4]; };  // x, r, i, dy
 
 struct GlrSharedBwd {
-  float4 agg[2][kWarps][32];   // forward: what each warp's rows do to the state; tiles take turns
-  float4 gga[2][kWarps][32];   // backward: what they do to a w
-  float4 before[4][32];        // of each part of the words of the chunks behind
+  ScanShared sc;               // what the rows do to a w
+  float4 fwd[2][kWarps][32];   // what they do to a state
   float2 sum[2][kWarps][32];   // dlam of each warp's rows
-  Tile tile[2];
+  Tile tile[4];                // the CTA's n-th at n & 3
   uint64_t full[2];
 };
 
@@ -675,27 +680,23 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
   extern __shared__ __align__(128) uint8_t raw[];
   pdl_enter();
   if (a.err && *a.err) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cc = tid & 63, part = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, vw = kWarps - 1 - warp;  // vw: in the order of the chain
   uint8_t* tiles = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
   GlrSharedBwd& sh = *reinterpret_cast<GlrSharedBwd*>(tiles + (LOAD == GLR_TMA ? ST * BYTES : 0));
   const uint32_t full = smem_u32(sh.full);
   const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
 
-  auto fetch = [&](const Tile& o, int st) {  // thread 0: tile o into stage st
-    sh.tile[st] = o;
-    if (LOAD == GLR_TMA && o.k >= 0) {
+  auto fetch = [&](const Drawn& d, int n) {  // thread 0: the CTA's n-th tile, decoded
+    Tile& o = sh.tile[n & 3];
+    if (o.k < 0) return;
+    o.inner = inner_of<CH>(a, tl, o, d.word);
+    if (LOAD == GLR_TMA) {
+      const int st = n % ST;
       mbar_expect_tx(full + 8 * st, BYTES);
 #pragma unroll
       for (int m = 0; m < 4; ++m)
         tma_load_2d(smem_u32(tiles) + st * BYTES + m * (BYTES / 4), &maps.m[m], full + 8 * st, o.ch0, (int)o.c.r0);
     }
-  };
-  auto take = [&]() {
-    const unsigned t = (unsigned)atomicAdd(a.ticket, 1ull);
-    Tile o;
-    o.k = -1;
-    if (t < total) o = tile_of<CH>(a, tl, t, !a.reverse);  // the chains run against the recurrence
-    return o;
   };
   // dlam of a tile: its warps' sums in order
   auto put_sum = [&](int q, int64_t piece, int ch0) {
@@ -705,14 +706,17 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
     for (int w = 0; w < kWarps; ++w) v = add2(v, sh.sum[q][w][lane]);
     store2<float, false>(a.dlam_part, piece * a.d + ch0 + 2 * lane, a.d - ch0 - 2 * lane, v);
   };
-  Tile next;  // thread 0: the tile after those fetched
+  Drawn next;
   if (tid == 0) {
     if (LOAD == GLR_TMA) {
       for (int st = 0; st < ST; ++st) mbar_init(full + 8 * st, 1);
       mbar_init_fence();
     }
-    for (int st = 0; st < ST; ++st) fetch(take(), st);
-    next = take();
+    for (int n = 0; n <= ST; ++n) {
+      next.t = (unsigned)atomicAdd(a.ticket, 1ull);
+      decode<CH>(a, tl, total, !a.reverse, next, sh.tile[n & 3]);  // the chains run against the recurrence
+      if (n < ST) fetch(next, n);
+    }
   }
   __syncthreads();
 
@@ -721,12 +725,10 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
   int it = 0;
   for (;; ++it) {
     const int st = it % ST;
-    const Tile t = sh.tile[st];
-    const int k = t.k;
-    if (k < 0) break;
-    const Chain chain = chain_of(a, tl, t.c.b, k, t.ch0 + cc);
+    const Tile& t = sh.tile[it & 3];
+    if (t.k < 0) break;
     Words words;
-    ask(chain, a.dp, part, words);
+    ask(a, t, vw >> 1, (vw & 1) * 32 + lane, words);
     const int ch = t.ch0 + 2 * lane, nch = a.d - ch;
     const int64_t piece = tl.per_seq ? (int64_t)t.c.b * tl.per_seq + t.c.k / CH : t.c.r0 / CH;
     float2 h = load2<float, false>(a.saved, piece * a.d + ch, nch);  // the state before the chunk's rows
@@ -749,22 +751,21 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
       local_rows_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, pp, gi, s, x, dy, A, H, D);
     }
     const int tq = it & 1;
-    sh.agg[tq][warp][lane] = f.F ? make_float4(-1.f, -1.f, H.x, H.y) : make_float4(A.x, A.y, H.x, H.y);
-    sh.gga[tq][warp][lane] = f.E ? make_float4(-1.f, -1.f, D.x, D.y) : make_float4(A.x, A.y, D.x, D.y);
+    sh.fwd[tq][warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
+    sh.sc.agg[tq][vw][lane] = packed(Map2{f.E ? two(0.f) : A, D});
     // whether a sequence ends with the chunk's last row: then nothing comes from behind
-    const bool need = !__syncthreads_or(warp == kWarps - 1 && (f.E >> (PER - 1) & 1)) && k > 0;
-    if (tid == 0) fetch(next, st);
+    const bool need = !__syncthreads_or(warp == kWarps - 1 && (f.E >> (PER - 1) & 1)) && t.k > 0;
+    if (tid == 0) {
+      fetch(next, it + ST);
+      if (next.t < total) next.t = (unsigned)atomicAdd(a.ticket, 1ull);
+    }
     if (it > 0) put_sum(tq ^ 1, last_piece, last_ch0);
     last_piece = piece;
     last_ch0 = t.ch0;
-    Map tot{1.f, 0.f, false};
-    if (part == 3 && k < chain.last) {
-#pragma unroll
-      for (int w = kWarps - 1; w >= 0; --w) tot = then(tot, get_map(sh.gga[tq][w], cc));
-      publish(chain.chunk + (int64_t)k * a.dp, tot);
-    }
+    Map2 tot;
+    const Map2 pre = scan_local(a, t, sh.sc, tq, vw, lane, tot);
     // the states before the warp's rows, and with them what e is of w
-    for (int w = 0; w < warp; ++w) h = after(sh.agg[tq][w][lane], h);
+    for (int w = 0; w < warp; ++w) h = after(map_at(sh.fwd[tq][w][lane]), h);
     const float2 rk = make_float2(ka.x > 0.f ? 1.f / ka.x : 0.f, ka.y > 0.f ? 1.f / ka.y : 0.f);
     float2 osr[PER];
 #pragma unroll
@@ -788,25 +789,9 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
       gi[q] = fma2(make_float2(-xv.x, -xv.y), gi[q], xv);         // x (1 - sig(i))
       h = fma2(da[q], h, u);
     }
-    if (need && (part >= 2 || k >= 16)) put_map(sh.before[part], cc, answer(chain, a.dp, part, words, a.err_out));
-    if ((k & 15) == 15 && k < chain.last && part >= 2) {
-      named_bar(1, 128);
-      if (part == 3)
-        publish(chain.group + (int64_t)(k >> 4) * a.dp, need ? then(then(get_map(sh.before[2], cc), get_map(sh.before[3], cc)), tot) : tot);
-    }
     // a w from behind the warp's rows
-    float2 v = two(0.f);
-    if (need) {
-      __syncthreads();
-      if (k >= 16) v = after(sh.before[1][lane], after(sh.before[0][lane], v));
-      v = after(sh.before[3][lane], after(sh.before[2][lane], v));
-    }
-    if ((k & 255) == 255 && k < chain.last && part == 3) {
-      const float2 c2 = make_float2(__shfl_sync(FULLM, v.x, cc >> 1), __shfl_sync(FULLM, v.y, cc >> 1));
-      const float in = cc & 1 ? c2.y : c2.x;
-      publish(chain.large + (int64_t)(k >> 8) * a.dp, Map{0.f, tot.reset ? tot.H : fmaf(tot.A, in, tot.H), true});
-    }
-    for (int w = kWarps - 1; w > warp; --w) v = after(sh.gga[tq][w][lane], v);
+    scan_words(a, t, sh.sc, vw, lane, need, words, tot);
+    float2 v = after(pre, scan_state(a, t, sh.sc, vw, lane, need, tot));
     // the gradients, from the last row on
     float2 dl = two(0.f);
     const int64_t step = a.reverse ? a.ldd : -a.ldd;
@@ -836,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
       }
     }
     sh.sum[tq][warp][lane] = dl;
-    if (tid == 0 && next.k >= 0) next = take();
+    if (tid == 0) decode<CH>(a, tl, total, !a.reverse, next, sh.tile[(it + ST + 1) & 3]);
   }
   __syncthreads();
   if (it > 0) put_sum((it - 1) & 1, last_piece, last_ch0);

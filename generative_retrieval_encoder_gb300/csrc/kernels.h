@@ -174,7 +174,11 @@ struct DecayArgs {
 // and short sequences, over all rows (per_seq = 0).
 constexpr int kGlrChunk = 64, kGlrSlot = 512;
 constexpr int kGlrRowsFwd = 128;  // rows of a tile of the forward (a state is saved every kGlrChunk of them)
-struct GlrTiles { int per_seq, n_chunks; };  // chunks of a slot (0: one stream), of the call
+struct GlrDiv { uint32_t m; int s; };  // division by an invariant (quotient() in glr.cu)
+struct GlrTiles {
+  int per_seq, n_chunks;               // chunks of a slot (0: one stream), of the call
+  GlrDiv by_cg, by_seq;                // by the groups of 64 channels, by the slots
+};
 struct GlrArgs {
   const void* x; const void* r; const void* i; int64_t ld;  // [T, ld]
   const float* lam; float c;                                // [d]
