@@ -166,10 +166,9 @@ __device__ __forceinline__ int seq_of(const GlrArgs& a, int64_t row) {
 }
 
 // ------------------------------------------------------------ tiles
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kPerF = kGlrRowsFwd / kWarps;  // a warp's rows; a lane has two channels of each
-constexpr int kPerB = kGlrChunk / kWarps;
-constexpr int kCtasFwd = 2, kCtasBwd = 2;    // an SM's
+constexpr int kWarpsF = 8, kWarpsB = 8;                                       // of a CTA, forward and backward
+constexpr int kPerF = kGlrRowsFwd / kWarpsF, kPerB = kGlrChunk / kWarpsB;     // a warp's rows; a lane has two channels of each
+constexpr int kCtasFwd = 2, kCtasBwd = 2;                                     // an SM's
 
 // How a tile's rows are read: copied ahead into shared memory (rows of 16-byte pieces), or straight into registers by
 // pairs of channels or single ones.
@@ -264,14 +263,16 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p, bool is, uint64_t x)
   return x;
 }
 
-// The 31 words that a chunk reads, from the oldest on (the larger group's, 15 groups', 15 chunks'), in four parts of 8 (the
-// last of 7), a thread of each for every channel: ask() asks for a thread's at once, before they are needed; answer() waits
-// for those that were not there yet, again together, and composes them.  Words that do not exist are identities: they are
-// read from one that is.
-struct Words { uint64_t w[8]; };
+// The 31 words that a chunk reads, from the oldest on (the larger group's, 15 groups', 15 chunks'), in W / 2 parts for the W
+// warps of a CTA, a thread of each part for every channel: ask() asks for a thread's at once, before they are needed;
+// answer() waits for those that were not there yet, again together, and composes them.  Words that do not exist are
+// identities.
+template <int W> struct Words { uint64_t w[64 / W]; };
+template <int W>
 __device__ __forceinline__ uint64_t peek_word(const GlrArgs& a, const Tile& t, int part, int cc, int j, bool want, uint64_t x) {
-  const int lim = part >= 2 ? (t.k & 15) - (part - 2) * 8 : (t.k >> 4 & 15) + 1 - part * 8;
-  int64_t at = (part >= 2 ? t.near + (part - 2) * 8 * a.dp : t.far + part * 8 * a.dp) + j * a.dp;
+  constexpr int N = 64 / W, FAR = W / 4;  // words of a part; the parts of groups
+  const int lim = part >= FAR ? (t.k & 15) - (part - FAR) * N : (t.k >> 4 & 15) + 1 - part * N;
+  int64_t at = (part >= FAR ? t.near + (part - FAR) * N * a.dp : t.far + part * N * a.dp) + j * a.dp;
   bool is = j < lim;
   if (j == 0 && part == 0) {
     at = t.large;
@@ -279,9 +280,10 @@ __device__ __forceinline__ uint64_t peek_word(const GlrArgs& a, const Tile& t, i
   }
   return peek(a.words + at + cc, is && want, x);
 }
-__device__ __forceinline__ void ask(const GlrArgs& a, const Tile& t, int part, int cc, Words& v) {
+template <int W>
+__device__ __forceinline__ void ask(const GlrArgs& a, const Tile& t, int part, int cc, Words<W>& v) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v.w[j] = peek_word(a, t, part, cc, j, true, kIdentity);
+  for (int j = 0; j < 64 / W; ++j) v.w[j] = peek_word<W>(a, t, part, cc, j, true, kIdentity);
 }
 // Whether to go on asking after n vain tries: bounded, and given up at once where another wait has been.
 __device__ __forceinline__ bool patient(int n, int* err) {
@@ -291,65 +293,74 @@ __device__ __forceinline__ bool patient(int n, int* err) {
   atomicOr(err, kErrTimeout);
   return false;
 }
-__device__ __forceinline__ Map answer(const GlrArgs& a, const Tile& t, int part, int cc, Words& v) {
+template <int W>
+__device__ __forceinline__ Map answer(const GlrArgs& a, const Tile& t, int part, int cc, Words<W>& v) {
   for (int n = 0;; ++n) {
     uint64_t there = v.w[0];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) there &= v.w[j];
+    for (int j = 1; j < 64 / W; ++j) there &= v.w[j];
     if (there >> 63 || !patient(n, a.err_out)) break;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v.w[j] = peek_word(a, t, part, cc, j, !(v.w[j] >> 63), v.w[j]);
+    for (int j = 0; j < 64 / W; ++j) v.w[j] = peek_word<W>(a, t, part, cc, j, !(v.w[j] >> 63), v.w[j]);
   }
   Map m{1.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 64 / W; ++j)
     m = then(m, Map{__uint_as_float((uint32_t)(v.w[j] >> 32) & 0x7fffffffu), __uint_as_float((uint32_t)v.w[j])});
   return m;
 }
 
 // Shared memory of the scan: what the rows of each warp (in the chain's order) do, tiles taking turns; the parts of the words.
-struct ScanShared {
-  float4 agg[2][kWarps][32];
-  float4 before[4][32];
+template <int W> struct ScanShared {
+  float4 agg[2][W][32];
+  float4 before[W / 2][32];
 };
 // After the warps' maps are in sc.agg[q]: what those before warp vw do, composed; the last warp publishes the tile's word.
-__device__ __forceinline__ Map2 scan_local(const GlrArgs& a, const Tile& t, const ScanShared& sc, int q, int vw, int lane, Map2& total) {
+template <int W>
+__device__ __forceinline__ Map2 scan_local(const GlrArgs& a, const Tile& t, const ScanShared<W>& sc, int q, int vw, int lane, Map2& total) {
   Map2 m{two(1.f), two(0.f)};
   for (int w = 0; w < vw; ++w) m = then(m, map_at(sc.agg[q][w][lane]));
-  if (vw == kWarps - 1) {
+  if (vw == W - 1) {
     total = then(m, map_at(sc.agg[q][vw][lane]));
     if (t.k < t.last) publish(a.words + t.own + 2 * lane, total);
   }
   return m;
 }
 // This thread's part of the words into sc.before; a full group's word published (it takes no other group's: it does not wait
-// for parts 0 and 1).
-__device__ __forceinline__ void scan_words(const GlrArgs& a, const Tile& t, ScanShared& sc, int vw, int lane, bool need, Words& words, const Map2& total) {
+// for the parts of those).
+template <int W>
+__device__ __forceinline__ void scan_words(const GlrArgs& a, const Tile& t, ScanShared<W>& sc, int vw, int lane, bool need, Words<W>& words, const Map2& total) {
+  constexpr int P = W / 2, FAR = W / 4;
   const int part = vw >> 1, cc = (vw & 1) * 32 + lane;
-  if (need && (part >= 2 || t.k >= 16)) {
-    const Map m = answer(a, t, part, cc, words);
+  if (need && (part >= FAR || t.k >= 16)) {
+    const Map m = answer<W>(a, t, part, cc, words);
     float* p = (float*)&sc.before[part][cc >> 1] + (cc & 1);
     p[0] = m.A;
     p[2] = m.H;
   }
-  if ((t.k & 15) == 15 && t.k < t.last && part >= 2) {
-    named_bar(1, 128);
-    if (vw == kWarps - 1) {
+  if ((t.k & 15) == 15 && t.k < t.last && part >= FAR) {
+    named_bar(1, W * 16);
+    if (vw == W - 1) {
       Map2 m = total;
-      if (need) m = then(then(map_at(sc.before[2][lane]), map_at(sc.before[3][lane])), total);
+      if (need) {
+#pragma unroll
+        for (int q = P - 1; q >= FAR; --q) m = then(map_at(sc.before[q][lane]), m);
+      }
       publish(a.words + t.far + (int64_t)((t.k >> 4 & 15) + 1) * a.dp + 2 * lane, m);
     }
   }
 }
 // The state that enters the tile.  Whole CTAs call it (need is the same for all).
-__device__ __forceinline__ float2 scan_state(const GlrArgs& a, const Tile& t, const ScanShared& sc, int vw, int lane, bool need, const Map2& total) {
+template <int W>
+__device__ __forceinline__ float2 scan_state(const GlrArgs& a, const Tile& t, const ScanShared<W>& sc, int vw, int lane, bool need, const Map2& total) {
   float2 h = two(0.f);
   if (need) {
     __syncthreads();
-    if (t.k >= 16) h = after(map_at(sc.before[1][lane]), after(map_at(sc.before[0][lane]), h));
-    h = after(map_at(sc.before[3][lane]), after(map_at(sc.before[2][lane]), h));
+#pragma unroll
+    for (int q = 0; q < W / 2; ++q)
+      if (q >= W / 4 || t.k >= 16) h = after(map_at(sc.before[q][lane]), h);
   }
-  if ((t.k & 255) == 255 && t.k < t.last && vw == kWarps - 1)
+  if ((t.k & 255) == 255 && t.k < t.last && vw == W - 1)
     publish(a.words + t.large + a.dp + 2 * lane, Map2{two(0.f), after(total, h)});
   return h;
 }
@@ -455,7 +466,7 @@ template <typename T> constexpr int stages_fwd() { return sizeof(T) == 2 ? 2 : 1
 
 // Shared memory of a CTA of the forward, after its tiles of x, r and i.
 struct GlrShared {
-  ScanShared sc;
+  ScanShared<kWarpsF> sc;
   Tile tile[4];                // the CTA's n-th at n & 3
   uint64_t full[2];
 };
@@ -464,7 +475,7 @@ struct GlrShared {
 // functions a value), by the waits between tiles and by memory.  Two CTAs an SM keep taking tiles, so that one's wait for
 // the state between tiles is another's arithmetic; a tile's rows are copied to shared memory while an earlier one is worked on.
 template <typename T, int LOAD>
-__global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
+__global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
   constexpr int PER = kPerF, CH = kGlrRowsFwd, ST = stages_fwd<T>();
   constexpr uint32_t BYTES = 3 * CH * 64 * sizeof(T), ALL = (1u << PER) - 1;
   extern __shared__ __align__(128) uint8_t raw[];
@@ -507,8 +518,6 @@ __global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a,
     const int st = it % ST;
     const Tile& me = sh.tile[it & 3];
     if (me.k < 0) break;
-    Words words;
-    ask(a, me, warp >> 1, (warp & 1) * 32 + lane, words);
     // the lane's rows
     const int ch = me.ch0 + 2 * lane, nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
     const int j0 = warp * PER;
@@ -527,6 +536,8 @@ __global__ void __launch_bounds__(kThreads, kCtasFwd) k_glr_fwd(const GlrArgs a,
     } else {
       local_rows<T, LOAD, false, false, PER, CH>(a, sm, me.c, f, j0, ch, nch, ka, ka, da, u, A, H);
     }
+    Words<kWarpsF> words;
+    ask(a, me, warp >> 1, (warp & 1) * 32 + lane, words);
     sh.sc.agg[it & 1][warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
     // whether the chunk's first row begins a sequence: then nothing enters
     const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && me.k > 0;
@@ -663,9 +674,9 @@ __device__ __forceinline__ void local_rows_bwd(const GlrArgs& a, const T* sm, co
 struct GlrMaps4 { CUtensorMap m[4]; };  // x, r, i, dy
 
 struct GlrSharedBwd {
-  ScanShared sc;               // what the rows do to a w
-  float4 fwd[2][kWarps][32];   // what they do to a state
-  float2 sum[2][kWarps][32];   // dlam of each warp's rows
+  ScanShared<kWarpsB> sc;      // what the rows do to a w
+  float4 fwd[2][kWarpsB][32];  // what they do to a state
+  float2 sum[2][kWarpsB][32];   // dlam of each warp's rows
   Tile tile[4];                // the CTA's n-th at n & 3
   uint64_t full[2];
 };
@@ -674,13 +685,13 @@ struct GlrSharedBwd {
 // rows come from the chunk's saved one, the w behind them as the forward's states do.  As the forward, with tiles of
 // kGlrChunk rows: a row's held values take eleven registers a pair of channels.
 template <typename T, int LOAD>
-__global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps4 maps) {
+__global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps4 maps) {
   constexpr int PER = kPerB, CH = kGlrChunk, ST = stages_bwd<T>();
   constexpr uint32_t BYTES = 4 * CH * 64 * sizeof(T), ALL = (1u << PER) - 1;
   extern __shared__ __align__(128) uint8_t raw[];
   pdl_enter();
   if (a.err && *a.err) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, vw = kWarps - 1 - warp;  // vw: in the order of the chain
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, vw = kWarpsB - 1 - warp;  // vw: in the order of the chain
   uint8_t* tiles = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
   GlrSharedBwd& sh = *reinterpret_cast<GlrSharedBwd*>(tiles + (LOAD == GLR_TMA ? ST * BYTES : 0));
   const uint32_t full = smem_u32(sh.full);
@@ -703,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
     if (warp != 0 || !a.dlam_part) return;
     float2 v = two(0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v = add2(v, sh.sum[q][w][lane]);
+    for (int w = 0; w < kWarpsB; ++w) v = add2(v, sh.sum[q][w][lane]);
     store2<float, false>(a.dlam_part, piece * a.d + ch0 + 2 * lane, a.d - ch0 - 2 * lane, v);
   };
   Drawn next;
@@ -727,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
     const int st = it % ST;
     const Tile& t = sh.tile[it & 3];
     if (t.k < 0) break;
-    Words words;
+    Words<kWarpsB> words;
     ask(a, t, vw >> 1, (vw & 1) * 32 + lane, words);
     const int ch = t.ch0 + 2 * lane, nch = a.d - ch;
     const int64_t piece = tl.per_seq ? (int64_t)t.c.b * tl.per_seq + t.c.k / CH : t.c.r0 / CH;
@@ -754,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, kCtasBwd) k_glr_bwd(const GlrArgs a,
     sh.fwd[tq][warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
     sh.sc.agg[tq][vw][lane] = packed(Map2{f.E ? two(0.f) : A, D});
     // whether a sequence ends with the chunk's last row: then nothing comes from behind
-    const bool need = !__syncthreads_or(warp == kWarps - 1 && (f.E >> (PER - 1) & 1)) && t.k > 0;
+    const bool need = !__syncthreads_or(warp == kWarpsB - 1 && (f.E >> (PER - 1) & 1)) && t.k > 0;
     if (tid == 0) {
       fetch(next, it + ST);
       if (next.t < total) next.t = (unsigned)atomicAdd(a.ticket, 1ull);
@@ -928,7 +939,7 @@ cudaError_t run_glr_fwd(const GlrArgs& a, const GlrTiles& t, cudaStream_t st) {
   auto kernel = tma ? k_glr_fwd<T, GLR_TMA> : pairs_ok(a, sizeof(T)) ? k_glr_fwd<T, GLR_PAIRS> : k_glr_fwd<T, GLR_SINGLE>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, grid, dim3(kThreads), smem, st, a, t, maps);
+  return launch_pdl(kernel, grid, dim3(kWarpsF * 32), smem, st, a, t, maps);
 }
 }  // namespace
 
@@ -950,7 +961,7 @@ cudaError_t run_glr_bwd(const GlrArgs& a, const GlrTiles& t, cudaStream_t st) {
   auto kernel = tma ? k_glr_bwd<T, GLR_TMA> : pairs_ok(a, sizeof(T)) ? k_glr_bwd<T, GLR_PAIRS> : k_glr_bwd<T, GLR_SINGLE>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, grid, dim3(kThreads), smem, st, a, t, maps);
+  return launch_pdl(kernel, grid, dim3(kWarpsB * 32), smem, st, a, t, maps);
 }
 }  // namespace
 
