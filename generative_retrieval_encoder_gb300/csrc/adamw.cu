@@ -28,21 +28,24 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x *= 0xBB67AE85u;
   return x ^ (x >> 16);
 }
-// The 32 random bits of a place (the fraction bits of the golden ratio spread neighbours).
-__device__ __forceinline__ uint32_t bits_of(uint64_t place, uint32_t key) {
-  return mix32((uint32_t)place * 0x9E3779B9u + (uint32_t)(place >> 32) * 0xBB67AE85u + key);
-}
+// The 32 random bits of a place are mix32(low word of the place * 0x9E3779B9 (the fraction bits of the golden ratio spread
+// neighbours) + high word * 0xBB67AE85 + the step's key).
 
-// t in [0, 448] to an e4m3 magnitude, 16 random bits d: at the normal values (t >= 2^-6) the fraction's
-// lower 20 bits, below them the fixed step 2^-9.
+// t in [0, 448] to an e4m3 magnitude, 16 random bits d: at the normal values (t >= 2^-6) the fraction's lower 20 bits,
+// below them the fixed step 2^-9, floor(512 t + d 2^-16) (512 t is exact; floor by an addition rounded down at 2^23).
 __device__ __forceinline__ uint32_t e4m3_up(float t, uint32_t d) {
   const uint32_t n = ((__float_as_uint(t) + (d << 4)) >> 20) - (120u << 3);
-  const uint32_t s = (uint32_t)floorf(__fadd_rn(t * 512.f, (float)d * 0x1p-16f));
+  const float u = __uint_as_float(0x3F800000u | d << 7) - 1.f;  // d 2^-16
+  const uint32_t s = __float_as_uint(__fadd_rd(__fmaf_rn(t, 512.f, u), 8388608.f)) & 15u;
   return t >= 0x1p-6f ? n : s;
 }
-__device__ __forceinline__ float e4m3_value(uint32_t code) {  // of the low 7 bits
-  const uint32_t k = code & 127u;
-  return k >= 8u ? __uint_as_float((k << 20) + (120u << 23)) : (float)k * 0x1p-9f;
+// Two e4m3 values (exact in fp16 and fp32).
+__device__ __forceinline__ float2 e4m3x2(uint32_t w) {
+  uint32_t h;
+  float2 o;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  asm("{\n .reg .f16 l, g;\n mov.b32 {l, g}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, g;\n}" : "=f"(o.x), "=f"(o.y) : "r"(h));
+  return o;
 }
 
 __global__ void k_adamw_begin(const AdamStep c, int64_t* step, const float* norm, AdamScalars* s) {
@@ -82,9 +85,56 @@ __device__ __forceinline__ void move(float g, float& m, float& v, float& root, f
   p = p * keep - s.step * __fdividef(m, fmaf(root, s.inv, s.eps));
 }
 
-// A warp takes 256 values, lane l those at l, l + 32, ..
+// Four values at p from element e on: in one access where the tensor is aligned and all are there, else the nv there are.
+__device__ __forceinline__ void load4(float (&o)[4], const void* p, int64_t e, bool b16, bool wide, int nv) {
+  if (wide) {
+    if (b16) {
+      const uint2 w = __ldcs((const uint2*)((const bf16*)p + e));
+      o[0] = bf_lo(w.x); o[1] = bf_hi(w.x); o[2] = bf_lo(w.y); o[3] = bf_hi(w.y);
+    } else {
+      const float4 w = __ldcs((const float4*)((const float*)p + e));
+      o[0] = w.x; o[1] = w.y; o[2] = w.z; o[3] = w.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = j >= nv ? 0.f : b16 ? to_f(((const bf16*)p)[e + j]) : ((const float*)p)[e + j];
+}
+__device__ __forceinline__ void store4(const float (&v)[4], void* p, int64_t e, bool b16, bool wide, int nv) {
+  if (wide) {
+    if (b16) __stcs((uint2*)((bf16*)p + e), make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])));
+    else __stcs((float4*)((float*)p + e), make_float4(v[0], v[1], v[2], v[3]));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < nv) {
+      if (b16) ((bf16*)p)[e + j] = from_f<bf16>(v[j]);
+      else ((float*)p)[e + j] = v[j];
+    }
+}
+__device__ __forceinline__ uint32_t load4b(const void* p, int64_t e, bool wide, int nv) {
+  if (wide) return __ldcs((const uint32_t*)((const uint8_t*)p + e));
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < nv) w |= (uint32_t)((const uint8_t*)p)[e + j] << 8 * j;
+  return w;
+}
+__device__ __forceinline__ void store4b(uint32_t w, void* p, int64_t e, bool wide, int nv) {
+  if (wide) {
+    __stcs((uint32_t*)((uint8_t*)p + e), w);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < nv) ((uint8_t*)p)[e + j] = (uint8_t)(w >> 8 * j);
+}
+
+// One pass over every tensor: bound by memory.  A warp takes a block of 256 values at a time, lane l those at 4 l .. 4 l + 3
+// of either half: 16-byte accesses of fp32, and the block's largest magnitudes by one warp reduction each.
 template <int N>
-__global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ AdamTable<N> tab, const AdamScalars* sc) {
+__global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdamTable<N> tab, const AdamScalars* sc) {
   pdl_enter();
   const AdamScalars s = *sc;
   if (!s.go) return;
@@ -97,46 +147,70 @@ __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ AdamTable
     const AdamTensor& t = tab.t[k];
     const int64_t e0 = (int64_t)(u - t.first) * kAdamUnit + warp * kAdamBlock;
     if (e0 >= t.n) continue;
-    const bool q8 = t.ms != nullptr;
+    const bool q8 = t.ms != nullptr, pb = t.pb && !t.master;  // pb: updated in bf16
     const int64_t blk = e0 / kAdamBlock;
-    float m[8], root[8];
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = e0 + lane + 32 * j;
-      m[j] = root[j] = 0.f;
-      if (e >= t.n) continue;
-      float v;
+    void* src = t.master ? (void*)t.master : t.param;
+    float g[2][4], p[2][4], m[2][4], r[2][4];
+    uint32_t wm[2], wv[2];
+    int64_t e[2];
+    int nv[2];
+    bool wide[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      e[h] = e0 + 128 * h + 4 * lane;
+      nv[h] = (int)max((int64_t)0, min((int64_t)4, t.n - e[h]));
+      wide[h] = t.vec && nv[h] == 4;
+      load4(g[h], t.grad, e[h], t.gb, wide[h], nv[h]);
+      load4(p[h], src, e[h], pb, wide[h], nv[h]);
       if (q8) {
-        const uint32_t cm = ((const uint8_t*)t.m)[e], cv = ((const uint8_t*)t.v)[e];
-        const float a = __fmul_rn(e4m3_value(cm), t.ms[blk]);
-        m[j] = cm & 128u ? -a : a;
-        v = __fmul_rn(e4m3_value(cv), t.vs[blk]);
-        v = __fmul_rn(v, v);
+        wm[h] = load4b(t.m, e[h], wide[h], nv[h]);
+        wv[h] = load4b(t.v, e[h], wide[h], nv[h]);
       } else {
-        m[j] = ((const float*)t.m)[e];
-        v = ((const float*)t.v)[e];
+        load4(m[h], t.m, e[h], false, wide[h], nv[h]);
+        load4(r[h], t.v, e[h], false, wide[h], nv[h]);
       }
-      const float g = t.gb ? to_f(((const bf16*)t.grad)[e]) : ((const float*)t.grad)[e];
-      float p = t.master ? t.master[e] : t.pb ? to_f(((const bf16*)t.param)[e]) : ((const float*)t.param)[e];
-      move(g, m[j], v, root[j], p, s, t.keep);
-      if (t.master) t.master[e] = p;
-      if (t.pb) ((bf16*)t.param)[e] = from_f<bf16>(p);
-      else ((float*)t.param)[e] = p;
+    }
+    if (q8) {
+      const float sm = t.ms[blk], sv = t.vs[blk];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 a = e4m3x2(wm[h]), b = e4m3x2(wm[h] >> 16), c = e4m3x2(wv[h]), d = e4m3x2(wv[h] >> 16);
+        m[h][0] = __fmul_rn(a.x, sm); m[h][1] = __fmul_rn(a.y, sm); m[h][2] = __fmul_rn(b.x, sm); m[h][3] = __fmul_rn(b.y, sm);
+        r[h][0] = __fmul_rn(c.x, sv); r[h][1] = __fmul_rn(c.y, sv); r[h][2] = __fmul_rn(d.x, sv); r[h][3] = __fmul_rn(d.y, sv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[h][j] = __fmul_rn(r[h][j], r[h][j]);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float root;
+        move(g[h][j], m[h][j], r[h][j], root, p[h][j], s, t.keep);
+        if (q8) r[h][j] = root;
+      }
+      store4(p[h], src, e[h], pb, wide[h], nv[h]);
+      if (t.master) store4(p[h], t.param, e[h], true, wide[h], nv[h]);
       if (!q8) {
-        ((float*)t.m)[e] = m[j];
-        ((float*)t.v)[e] = v;
+        store4(m[h], t.m, e[h], false, wide[h], nv[h]);
+        store4(r[h], t.v, e[h], false, wide[h], nv[h]);
       }
     }
     if (!q8) continue;
-    // the largest magnitudes as bit patterns: a NaN or infinity is the largest of all
+    // the largest magnitudes as bit patterns: a NaN or infinity is the largest of all (values past the end do not count)
     uint32_t tm = 0, tv = 0;
-    for (int j = 0; j < 8; ++j) {
-      tm = max(tm, __float_as_uint(m[j]) & 0x7fffffffu);
-      tv = max(tv, __float_as_uint(root[j]) & 0x7fffffffu);
-    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < nv[h]) {
+          tm = max(tm, __float_as_uint(m[h][j]) & 0x7fffffffu);
+          tv = max(tv, __float_as_uint(r[h][j]) & 0x7fffffffu);
+        }
     tm = __reduce_max_sync(FULL, tm);
     tv = __reduce_max_sync(FULL, tv);
     const float fm = __uint_as_float(tm), fv = __uint_as_float(tv);
-    const bool badm = !isfinite(fm), badv = !isfinite(fv);
+    const bool badm = tm >= 0x7f800000u, badv = tv >= 0x7f800000u;
     const float im = fm >= 0x1p-100f ? __fmul_rn(__frcp_rn(fm), 448.f) : 0.f;
     const float iv = fv >= 0x1p-100f ? __fmul_rn(__frcp_rn(fv), 448.f) : 0.f;
     __syncwarp();  // every lane has read the block's scales
@@ -144,16 +218,23 @@ __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ AdamTable
       t.ms[blk] = badm ? __uint_as_float(0x7fc00000u) : fm >= 0x1p-100f ? __fmul_rn(fm, 1.f / 448.f) : 0.f;
       t.vs[blk] = badv ? __uint_as_float(0x7fc00000u) : fv >= 0x1p-100f ? __fmul_rn(fv, 1.f / 448.f) : 0.f;
     }
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = e0 + lane + 32 * j;
-      if (e >= t.n) continue;
-      const uint32_t z = bits_of((uint64_t)(t.place + e), s.key);
-      const float xm = fminf(__fmul_rn(fabsf(m[j]), im), 448.f), xv = fminf(__fmul_rn(root[j], iv), 448.f);
-      uint32_t cm = e4m3_up(xm, z & 0xffffu) | (__float_as_uint(m[j]) >> 31 << 7);
-      uint32_t cv = e4m3_up(xv, z >> 16);
-      if (xv > 0.f) cv = max(cv, 1u);
-      ((uint8_t*)t.m)[e] = (uint8_t)(badm ? 0x7fu : cm);
-      ((uint8_t*)t.v)[e] = (uint8_t)(badv ? 0x7fu : cv);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t cm = 0, cv = 0;
+      const uint64_t place = (uint64_t)(t.place + e[h]);
+      const uint32_t base = (uint32_t)place * 0x9E3779B9u + (uint32_t)(place >> 32) * 0xBB67AE85u + s.key;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // (four neighbours share the place's upper word: places of blocks are multiples of 256)
+        const uint32_t z = mix32(base + j * 0x9E3779B9u);
+        const float xm = fminf(__fmul_rn(fabsf(m[h][j]), im), 448.f), xv = fminf(__fmul_rn(r[h][j], iv), 448.f);
+        const uint32_t a = e4m3_up(xm, z & 0xffffu) | (__float_as_uint(m[h][j]) >> 31 << 7);
+        uint32_t b = e4m3_up(xv, z >> 16);
+        if (xv > 0.f) b = max(b, 1u);
+        cm |= a << 8 * j;
+        cv |= b << 8 * j;
+      }
+      store4b(badm ? 0x7f7f7f7fu : cm, t.m, e[h], wide[h], nv[h]);
+      store4b(badv ? 0x7f7f7f7fu : cv, t.v, e[h], wide[h], nv[h]);
     }
   }
 }
@@ -170,15 +251,22 @@ __global__ void __launch_bounds__(256) k_sumsq(const __grid_constant__ AdamTable
   for (int u = u0; u < u1; ++u) {
     while (k + 1 < tab.n && tab.t[k + 1].first <= u) ++k;
     const AdamTensor& t = tab.t[k];
-    for (int j = 0; j < kAdamUnit / 256; ++j) {
-      const int64_t e = (int64_t)(u - t.first) * kAdamUnit + threadIdx.x + 256 * j;
-      if (e >= t.n) break;
-      const float g = t.gb ? to_f(((const bf16*)t.grad)[e]) : ((const float*)t.grad)[e];
-      const float q = __fmul_rn(g, g), w = __fmaf_rn(g, g, -q);
-      const float sum = __fadd_rn(hi, q), b = __fadd_rn(sum, -hi);
-      lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fadd_rn(hi, -__fadd_rn(sum, -b)), __fadd_rn(q, -b)), w));
-      hi = sum;
+    float g[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t e = (int64_t)(u - t.first) * kAdamUnit + 1024 * h + 4 * threadIdx.x;
+      const int nv = (int)max((int64_t)0, min((int64_t)4, t.n - e));
+      load4(g[h], t.grad, e, t.gb, t.vec && nv == 4, nv);
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = g[h][j], q = __fmul_rn(v, v), w = __fmaf_rn(v, v, -q);
+        const float sum = __fadd_rn(hi, q), b = __fadd_rn(sum, -hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fadd_rn(hi, -__fadd_rn(sum, -b)), __fadd_rn(q, -b)), w));
+        hi = sum;
+      }
   }
   double d = (double)hi + (double)lo;
   for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(FULL, d, o);

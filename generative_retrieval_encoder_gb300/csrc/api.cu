@@ -525,7 +525,10 @@ gbla_status adam_tables(const gbla_adamw_tensor* t, int n, double lr, F&& fn) {
       o.n = t[k].n; o.place = place; o.first = tab.units;
       o.keep = (float)(1. - lr * t[k].weight_decay);
       o.pb = t[k].param_dtype == GBLA_BF16; o.gb = t[k].grad_dtype == GBLA_BF16;
-      o.vec = 0;
+      uintptr_t bits = 0;
+      for (const void* q : {(const void*)t[k].param, (const void*)t[k].master, t[k].grad, (const void*)t[k].m, (const void*)t[k].v})
+        bits |= reinterpret_cast<uintptr_t>(q);
+      o.vec = bits % 16 == 0;
       tab.units += (int)((t[k].n + kAdamUnit - 1) / kAdamUnit);
       place += (t[k].n + kAdamBlock - 1) / kAdamBlock * kAdamBlock;
     }
