@@ -58,8 +58,9 @@ __global__ void k_adamw_begin(const AdamStep c, int64_t* step, const float* norm
   o.clip = norm && c.max_norm > 0. ? fminf(__fmul_rn(__frcp_rn(__fadd_rn(nm, 1e-6f)), (float)c.max_norm), 1.f) : 1.f;
   o.b1 = (float)c.b1; o.c1 = (float)(1. - c.b1);
   o.b2 = (float)c.b2; o.c2 = (float)(1. - c.b2);
-  o.step = (float)(c.lr / (1. - pow(c.b1, (double)t)));
-  o.inv = (float)(1. / sqrt(1. - pow(c.b2, (double)t)));
+  // 1 - b^t = -expm1(t ln b): relative errors of 2^-23, in fp32 (a power in fp64 takes this one thread 9 us)
+  o.step = __fdiv_rn((float)c.lr, -expm1f((float)((double)t * c.ln1)));
+  o.inv = __frcp_rn(__fsqrt_rn(-expm1f((float)((double)t * c.ln2))));
   o.eps = (float)c.eps;
   o.key = mix32(mix32((uint32_t)t ^ 0x9E3779B9u) + c.seed);
   *s = o;

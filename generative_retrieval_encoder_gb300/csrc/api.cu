@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <string>
@@ -1151,7 +1152,7 @@ gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors, con
     return GBLA_ERR_INVALID_ARG;
   const AdamCtx c{static_cast<cudaStream_t>(stream)};
   AdamScalars* s = at<AdamScalars>(ws, 0);
-  AdamStep a{g.lr, g.beta1, g.beta2, g.eps, g.max_norm, g.seed};
+  AdamStep a{g.lr, g.beta1, g.beta2, g.eps, g.max_norm, std::log(g.beta1), std::log(g.beta2), g.seed};  // beta = 0: -inf
   GBLA_CHECK(launch_adamw_begin(a, step, norm, s, c.st), "adamw begin");
   return adam_cap(tensors, n_tensors) == kAdamFew ? run_adamw<kAdamFew>(tensors, n_tensors, g.lr, s, c)
                                                   : run_adamw<kAdamMany>(tensors, n_tensors, g.lr, s, c);

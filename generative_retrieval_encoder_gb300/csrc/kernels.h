@@ -217,7 +217,7 @@ template <int N> struct AdamTable { AdamTensor t[N]; int n, units; };
 constexpr int kAdamFew = 36, kAdamMany = 336;  // table sizes: under 4 KB, and under 32 KB, of parameters
 // What a step's kernels read, formed once by the first of them.
 struct AdamScalars { float clip, b1, c1, b2, c2, step, inv, eps; uint32_t key; int go; };
-struct AdamStep { double lr, b1, b2, eps, max_norm; uint32_t seed; };
+struct AdamStep { double lr, b1, b2, eps, max_norm, ln1, ln2; uint32_t seed; };  // ln: of b1, b2
 
 // ---------------------------------------------------------------- launchers
 cudaError_t launch_plan(const SeqDesc& s, int ntile, const int* tile_sizes, int32_t* const* prefixes,
