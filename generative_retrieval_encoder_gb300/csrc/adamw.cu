@@ -31,13 +31,19 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 // The 32 random bits of a place are mix32(low word of the place * 0x9E3779B9 (the fraction bits of the golden ratio spread
 // neighbours) + high word * 0xBB67AE85 + the step's key).
 
-// t in [0, 448] to an e4m3 magnitude, 16 random bits d: at the normal values (t >= 2^-6) the fraction's lower 20 bits,
-// below them the fixed step 2^-9, floor(512 t + d 2^-16) (512 t is exact; floor by an addition rounded down at 2^23).
-__device__ __forceinline__ uint32_t e4m3_up(float t, uint32_t d) {
-  const uint32_t n = ((__float_as_uint(t) + (d << 4)) >> 20) - (120u << 3);
-  const float u = __uint_as_float(0x3F800000u | d << 7) - 1.f;  // d 2^-16
-  const uint32_t s = __float_as_uint(__fadd_rd(__fmaf_rn(t, 512.f, u), 8388608.f)) & 15u;
+// t in [0, 448] (or two units in the last place above: the sum below does not reach the next code) to an e4m3 magnitude, 16
+// random bits d: at the normal values (t >= 2^-6) the fraction's lower 20 bits, below them the fixed step 2^-9,
+// floor(512 t + d 2^-16) (both products exact; floor by an addition rounded down at 2^23).
+__device__ __forceinline__ uint32_t e4m3_up(float t, uint16_t d) {
+  const uint32_t n = ((__float_as_uint(t) + ((uint32_t)d << 4)) >> 20) - (120u << 3);
+  const uint32_t s = __float_as_uint(__fadd_rd(__fmaf_rn((float)d, 0x1p-16f, t * 512.f), 8388608.f)) & 15u;
   return t >= 0x1p-6f ? n : s;
+}
+// The larger of c and |a|, |b|; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float o;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(o) : "f"(a), "f"(b), "f"(c));
+  return o;
 }
 // Two e4m3 values (exact in fp16 and fp32).
 __device__ __forceinline__ float2 e4m3x2(uint32_t w) {
@@ -77,18 +83,26 @@ __device__ __forceinline__ int tensor_of(const AdamTable<N>& t, int unit) {
   return lo;
 }
 
-// One value: m, root = sqrt(v) and p moved by g.
-__device__ __forceinline__ void move(float g, float& m, float& v, float& root, float& p, const AdamScalars& s, float keep) {
-  g = __fmul_rn(g, s.clip);
-  m = __fadd_rn(__fmul_rn(s.b1, m), __fmul_rn(s.c1, g));
-  v = __fadd_rn(__fmul_rn(s.b2, v), __fmul_rn(__fmul_rn(s.c2, g), g));
-  root = __fsqrt_rn(v);
-  p = p * keep - s.step * __fdividef(m, fmaf(root, s.inv, s.eps));
+// Two products, each rounded once.  (Scalar instructions: a packed product and a packed sum that take one another come out
+// of the assembler as one fused operation, whatever rounding they ask for: an ulp off in one value of six, measured.)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+// Two values: m, v, root = sqrt(v) and p moved by g; every operation of m, v and root rounded once.
+__device__ __forceinline__ void move(float2 g, float2& m, float2& v, float2& root, float2& p, const AdamScalars& s, float keep) {
+  auto all = [](float x) { return make_float2(x, x); };
+  g = mul2(g, all(s.clip));
+  m = add2(mul2(all(s.b1), m), mul2(all(s.c1), g));
+  v = add2(mul2(all(s.b2), v), mul2(mul2(all(s.c2), g), g));
+  root = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+  const float2 den = __ffma2_rn(root, all(s.inv), all(s.eps));
+  const float2 q = make_float2(__fdividef(m.x, den.x), __fdividef(m.y, den.y));
+  p = __ffma2_rn(all(-s.step), q, mul2(p, all(keep)));
 }
 
-// Four values at p from element e on: in one access where the tensor is aligned and all are there, else the nv there are.
-__device__ __forceinline__ void load4(float (&o)[4], const void* p, int64_t e, bool b16, bool wide, int nv) {
-  if (wide) {
+// Four values at p from element e on: WIDE in one access, else the nv there are.
+template <bool WIDE>
+__device__ __forceinline__ void load4(float (&o)[4], const void* p, int64_t e, bool b16, int nv) {
+  if (WIDE) {
     if (b16) {
       const uint2 w = __ldcs((const uint2*)((const bf16*)p + e));
       o[0] = bf_lo(w.x); o[1] = bf_hi(w.x); o[2] = bf_lo(w.y); o[3] = bf_hi(w.y);
@@ -101,8 +115,9 @@ __device__ __forceinline__ void load4(float (&o)[4], const void* p, int64_t e, b
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = j >= nv ? 0.f : b16 ? to_f(((const bf16*)p)[e + j]) : ((const float*)p)[e + j];
 }
-__device__ __forceinline__ void store4(const float (&v)[4], void* p, int64_t e, bool b16, bool wide, int nv) {
-  if (wide) {
+template <bool WIDE>
+__device__ __forceinline__ void store4(const float (&v)[4], void* p, int64_t e, bool b16, int nv) {
+  if (WIDE) {
     if (b16) __stcs((uint2*)((bf16*)p + e), make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])));
     else __stcs((float4*)((float*)p + e), make_float4(v[0], v[1], v[2], v[3]));
     return;
@@ -114,16 +129,18 @@ __device__ __forceinline__ void store4(const float (&v)[4], void* p, int64_t e, 
       else ((float*)p)[e + j] = v[j];
     }
 }
-__device__ __forceinline__ uint32_t load4b(const void* p, int64_t e, bool wide, int nv) {
-  if (wide) return __ldcs((const uint32_t*)((const uint8_t*)p + e));
+template <bool WIDE>
+__device__ __forceinline__ uint32_t load4b(const void* p, int64_t e, int nv) {
+  if (WIDE) return __ldcs((const uint32_t*)((const uint8_t*)p + e));
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (j < nv) w |= (uint32_t)((const uint8_t*)p)[e + j] << 8 * j;
   return w;
 }
-__device__ __forceinline__ void store4b(uint32_t w, void* p, int64_t e, bool wide, int nv) {
-  if (wide) {
+template <bool WIDE>
+__device__ __forceinline__ void store4b(uint32_t w, void* p, int64_t e, int nv) {
+  if (WIDE) {
     __stcs((uint32_t*)((uint8_t*)p + e), w);
     return;
   }
@@ -132,8 +149,110 @@ __device__ __forceinline__ void store4b(uint32_t w, void* p, int64_t e, bool wid
     if (j < nv) ((uint8_t*)p)[e + j] = (uint8_t)(w >> 8 * j);
 }
 
-// One pass over every tensor: bound by memory.  A warp takes a block of 256 values at a time, lane l those at 4 l .. 4 l + 3
-// of either half: 16-byte accesses of fp32, and the block's largest magnitudes by one warp reduction each.
+// A warp's block of 256 values from e0 on, lane l those at 4 l .. 4 l + 3 of either half: 16-byte accesses of fp32, and the
+// block's largest magnitudes by one warp reduction each.  WIDE: the block is whole and aligned.
+template <bool Q8, bool WIDE>
+__device__ __forceinline__ void block_step(const AdamTensor& t, int64_t e0, const AdamScalars& s, int lane) {
+  const bool pb = t.pb && !t.master;  // updated in bf16
+  const int64_t blk = e0 / kAdamBlock;
+  void* src = t.master ? (void*)t.master : t.param;
+  float g[2][4], p[2][4], m[2][4], r[2][4];
+  uint32_t wm[2], wv[2];
+  int nv[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t e = e0 + 128 * h + 4 * lane;
+    nv[h] = WIDE ? 4 : (int)max((int64_t)0, min((int64_t)4, t.n - e));
+    load4<WIDE>(g[h], t.grad, e, t.gb, nv[h]);
+    load4<WIDE>(p[h], src, e, pb, nv[h]);
+    if (Q8) {
+      wm[h] = load4b<WIDE>(t.m, e, nv[h]);
+      wv[h] = load4b<WIDE>(t.v, e, nv[h]);
+    } else {
+      load4<WIDE>(m[h], t.m, e, false, nv[h]);
+      load4<WIDE>(r[h], t.v, e, false, nv[h]);
+    }
+  }
+  if (Q8) {
+    const float2 sm = make_float2(t.ms[blk], t.ms[blk]), sv = make_float2(t.vs[blk], t.vs[blk]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const float2 a = mul2(e4m3x2(wm[h] >> 8 * j), sm);
+        float2 b = mul2(e4m3x2(wv[h] >> 8 * j), sv);
+        b = mul2(b, b);
+        m[h][j] = a.x; m[h][j + 1] = a.y;
+        r[h][j] = b.x; r[h][j + 1] = b.y;
+      }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      float2 a = make_float2(m[h][j], m[h][j + 1]), v = make_float2(r[h][j], r[h][j + 1]), q = make_float2(p[h][j], p[h][j + 1]), root;
+      move(make_float2(g[h][j], g[h][j + 1]), a, v, root, q, s, t.keep);
+      m[h][j] = a.x; m[h][j + 1] = a.y;
+      if (Q8) v = root;
+      r[h][j] = v.x; r[h][j + 1] = v.y;
+      p[h][j] = q.x; p[h][j + 1] = q.y;
+    }
+    const int64_t e = e0 + 128 * h + 4 * lane;
+    store4<WIDE>(p[h], src, e, pb, nv[h]);
+    if (t.master) store4<WIDE>(p[h], t.param, e, true, nv[h]);
+    if (!Q8) {
+      store4<WIDE>(m[h], t.m, e, false, nv[h]);
+      store4<WIDE>(r[h], t.v, e, false, nv[h]);
+    }
+  }
+  if (!Q8) return;
+  float fm = 0.f, fv = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (!WIDE) {  // values past the end do not count
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j >= nv[h]) m[h][j] = r[h][j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      fm = max_abs(m[h][j], m[h][j + 1], fm);
+      fv = max_abs(r[h][j], r[h][j + 1], fv);
+    }
+  }
+  // as bit patterns: a NaN or infinity is the largest of all
+  fm = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(fm)));
+  fv = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(fv)));
+  const bool badm = __float_as_uint(fm) >= 0x7f800000u, badv = __float_as_uint(fv) >= 0x7f800000u;
+  const float im = fm >= 0x1p-100f ? __fmul_rn(__frcp_rn(fm), 448.f) : 0.f;
+  const float iv = fv >= 0x1p-100f ? __fmul_rn(__frcp_rn(fv), 448.f) : 0.f;
+  __syncwarp();  // every lane has read the block's scales
+  if (lane == 0) {
+    t.ms[blk] = badm ? __uint_as_float(0x7fc00000u) : fm >= 0x1p-100f ? __fmul_rn(fm, 1.f / 448.f) : 0.f;
+    t.vs[blk] = badv ? __uint_as_float(0x7fc00000u) : fv >= 0x1p-100f ? __fmul_rn(fv, 1.f / 448.f) : 0.f;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t cm = 0, cv = 0;
+    const int64_t e = e0 + 128 * h + 4 * lane;
+    const uint64_t place = (uint64_t)(t.place + e);
+    const uint32_t base = (uint32_t)place * 0x9E3779B9u + (uint32_t)(place >> 32) * 0xBB67AE85u + s.key;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // (four neighbours share the place's upper word: places of blocks are multiples of 256)
+      const uint32_t z = mix32(base + j * 0x9E3779B9u);
+      const float xv = __fmul_rn(r[h][j], iv);
+      const uint32_t a = e4m3_up(__fmul_rn(fabsf(m[h][j]), im), (uint16_t)z) | (__float_as_uint(m[h][j]) >> 24 & 128u);
+      uint32_t b = e4m3_up(xv, (uint16_t)(z >> 16));
+      if (xv > 0.f) b = max(b, 1u);
+      cm |= a << 8 * j;
+      cv |= b << 8 * j;
+    }
+    store4b<WIDE>(badm ? 0x7f7f7f7fu : cm, t.m, e, nv[h]);
+    store4b<WIDE>(badv ? 0x7f7f7f7fu : cv, t.v, e, nv[h]);
+  }
+}
+
+// One pass over every tensor: bound by memory, with 8-bit states as much by their rounding's instructions.
 template <int N>
 __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdamTable<N> tab, const AdamScalars* sc) {
   pdl_enter();
@@ -148,94 +267,13 @@ __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdamTa
     const AdamTensor& t = tab.t[k];
     const int64_t e0 = (int64_t)(u - t.first) * kAdamUnit + warp * kAdamBlock;
     if (e0 >= t.n) continue;
-    const bool q8 = t.ms != nullptr, pb = t.pb && !t.master;  // pb: updated in bf16
-    const int64_t blk = e0 / kAdamBlock;
-    void* src = t.master ? (void*)t.master : t.param;
-    float g[2][4], p[2][4], m[2][4], r[2][4];
-    uint32_t wm[2], wv[2];
-    int64_t e[2];
-    int nv[2];
-    bool wide[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      e[h] = e0 + 128 * h + 4 * lane;
-      nv[h] = (int)max((int64_t)0, min((int64_t)4, t.n - e[h]));
-      wide[h] = t.vec && nv[h] == 4;
-      load4(g[h], t.grad, e[h], t.gb, wide[h], nv[h]);
-      load4(p[h], src, e[h], pb, wide[h], nv[h]);
-      if (q8) {
-        wm[h] = load4b(t.m, e[h], wide[h], nv[h]);
-        wv[h] = load4b(t.v, e[h], wide[h], nv[h]);
-      } else {
-        load4(m[h], t.m, e[h], false, wide[h], nv[h]);
-        load4(r[h], t.v, e[h], false, wide[h], nv[h]);
-      }
-    }
-    if (q8) {
-      const float sm = t.ms[blk], sv = t.vs[blk];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float2 a = e4m3x2(wm[h]), b = e4m3x2(wm[h] >> 16), c = e4m3x2(wv[h]), d = e4m3x2(wv[h] >> 16);
-        m[h][0] = __fmul_rn(a.x, sm); m[h][1] = __fmul_rn(a.y, sm); m[h][2] = __fmul_rn(b.x, sm); m[h][3] = __fmul_rn(b.y, sm);
-        r[h][0] = __fmul_rn(c.x, sv); r[h][1] = __fmul_rn(c.y, sv); r[h][2] = __fmul_rn(d.x, sv); r[h][3] = __fmul_rn(d.y, sv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r[h][j] = __fmul_rn(r[h][j], r[h][j]);
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float root;
-        move(g[h][j], m[h][j], r[h][j], root, p[h][j], s, t.keep);
-        if (q8) r[h][j] = root;
-      }
-      store4(p[h], src, e[h], pb, wide[h], nv[h]);
-      if (t.master) store4(p[h], t.param, e[h], true, wide[h], nv[h]);
-      if (!q8) {
-        store4(m[h], t.m, e[h], false, wide[h], nv[h]);
-        store4(r[h], t.v, e[h], false, wide[h], nv[h]);
-      }
-    }
-    if (!q8) continue;
-    // the largest magnitudes as bit patterns: a NaN or infinity is the largest of all (values past the end do not count)
-    uint32_t tm = 0, tv = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < nv[h]) {
-          tm = max(tm, __float_as_uint(m[h][j]) & 0x7fffffffu);
-          tv = max(tv, __float_as_uint(r[h][j]) & 0x7fffffffu);
-        }
-    tm = __reduce_max_sync(FULL, tm);
-    tv = __reduce_max_sync(FULL, tv);
-    const float fm = __uint_as_float(tm), fv = __uint_as_float(tv);
-    const bool badm = tm >= 0x7f800000u, badv = tv >= 0x7f800000u;
-    const float im = fm >= 0x1p-100f ? __fmul_rn(__frcp_rn(fm), 448.f) : 0.f;
-    const float iv = fv >= 0x1p-100f ? __fmul_rn(__frcp_rn(fv), 448.f) : 0.f;
-    __syncwarp();  // every lane has read the block's scales
-    if (lane == 0) {
-      t.ms[blk] = badm ? __uint_as_float(0x7fc00000u) : fm >= 0x1p-100f ? __fmul_rn(fm, 1.f / 448.f) : 0.f;
-      t.vs[blk] = badv ? __uint_as_float(0x7fc00000u) : fv >= 0x1p-100f ? __fmul_rn(fv, 1.f / 448.f) : 0.f;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t cm = 0, cv = 0;
-      const uint64_t place = (uint64_t)(t.place + e[h]);
-      const uint32_t base = (uint32_t)place * 0x9E3779B9u + (uint32_t)(place >> 32) * 0xBB67AE85u + s.key;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // (four neighbours share the place's upper word: places of blocks are multiples of 256)
-        const uint32_t z = mix32(base + j * 0x9E3779B9u);
-        const float xm = fminf(__fmul_rn(fabsf(m[h][j]), im), 448.f), xv = fminf(__fmul_rn(r[h][j], iv), 448.f);
-        const uint32_t a = e4m3_up(xm, z & 0xffffu) | (__float_as_uint(m[h][j]) >> 31 << 7);
-        uint32_t b = e4m3_up(xv, z >> 16);
-        if (xv > 0.f) b = max(b, 1u);
-        cm |= a << 8 * j;
-        cv |= b << 8 * j;
-      }
-      store4b(badm ? 0x7f7f7f7fu : cm, t.m, e[h], wide[h], nv[h]);
-      store4b(badv ? 0x7f7f7f7fu : cv, t.v, e[h], wide[h], nv[h]);
+    const bool wide = t.vec && e0 + kAdamBlock <= t.n;
+    if (t.ms) {
+      if (wide) block_step<true, true>(t, e0, s, lane);
+      else block_step<true, false>(t, e0, s, lane);
+    } else {
+      if (wide) block_step<false, true>(t, e0, s, lane);
+      else block_step<false, false>(t, e0, s, lane);
     }
   }
 }
@@ -257,7 +295,8 @@ __global__ void __launch_bounds__(256) k_sumsq(const __grid_constant__ AdamTable
     for (int h = 0; h < 2; ++h) {
       const int64_t e = (int64_t)(u - t.first) * kAdamUnit + 1024 * h + 4 * threadIdx.x;
       const int nv = (int)max((int64_t)0, min((int64_t)4, t.n - e));
-      load4(g[h], t.grad, e, t.gb, t.vec && nv == 4, nv);
+      if (t.vec && nv == 4) load4<true>(g[h], t.grad, e, t.gb, nv);
+      else load4<false>(g[h], t.grad, e, t.gb, nv);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
