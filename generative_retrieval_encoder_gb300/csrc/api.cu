@@ -356,7 +356,9 @@ gbla_status begin(const gbla_shape* s, int op, void* ws, size_t ws_bytes, void* 
 // Sizes and workspace of glr_forward / glr_backward (their shape needs no heads).
 struct GlrPlan {
   bool f32;
-  int T, L, d, n_seq, mode, per_seq, n_chunks;
+  int T, L, d, n_seq, mode;
+  bool slots;     // chunks per slot
+  int64_t pieces; // saved states
 };
 
 gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
@@ -371,9 +373,10 @@ gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
   p.mode = s->cu_seqlens ? SEQ_VARLEN : (s->seq_lens ? SEQ_PADDED : SEQ_DENSE);
   p.n_seq = s->cu_seqlens ? s->num_seqs : s->B;
   if ((long long)p.n_seq * p.d > (1LL << 38)) return GBLA_ERR_UNSUPPORTED;  // one thread each
-  p.per_seq = p.mode != SEQ_VARLEN && p.L >= kGlrSlot ? cdiv(p.L, kGlrChunk) : 0;
-  p.n_chunks = p.per_seq ? p.per_seq * p.n_seq : cdiv(p.T, kGlrChunk);
-  if ((long long)p.n_chunks * cdiv(p.d, 64) > 0x7fffffffLL) return GBLA_ERR_UNSUPPORTED;  // one CTA each
+  p.slots = p.mode != SEQ_VARLEN && p.L >= kGlrSlot;
+  p.pieces = p.slots ? (int64_t)p.n_seq * cdiv(p.L, kGlrPiece) : cdiv(p.T, kGlrPiece);
+  if ((p.slots ? (long long)p.n_seq * cdiv(p.L, kGlrRowsBwd) : cdiv(p.T, kGlrRowsBwd)) * cdiv(p.d, 64) > 0x7fffffffLL)
+    return GBLA_ERR_UNSUPPORTED;  // tiles are counted in 31 bits
   return GBLA_OK;
 }
 
@@ -388,7 +391,7 @@ GlrTiles glr_tiles(const GlrPlan& p, int rows) {
   GlrTiles t;
   t.by_cg = glr_div((uint32_t)cdiv(p.d, 64));
   t.by_seq = glr_div((uint32_t)p.n_seq);
-  t.per_seq = p.per_seq ? cdiv(p.L, rows) : 0;
+  t.per_seq = p.slots ? cdiv(p.L, rows) : 0;
   t.n_chunks = t.per_seq ? t.per_seq * p.n_seq : cdiv(p.T, rows);
   return t;
 }
@@ -402,7 +405,7 @@ GlrLayout glr_layout(const GlrPlan& p, int op) {
   if (p.mode == SEQ_VARLEN) l.marks = c.take((size_t)cdiv(p.T, 64) * 8);
   l.zero_bytes = c.off;
   l.kd = c.take(glr_dp(p) * 4);
-  const GlrTiles t = glr_tiles(p, op == GBLA_OP_GLR_FORWARD ? kGlrRowsFwd : kGlrChunk);
+  const GlrTiles t = glr_tiles(p, op == GBLA_OP_GLR_FORWARD ? kGlrRowsFwd : kGlrRowsBwd);
   const size_t slots = t.per_seq ? p.n_seq : 1, n = t.per_seq ? t.per_seq : t.n_chunks;
   l.n_words = (t.n_chunks + slots * ((n + 15) / 16) + slots * ((n + 255) / 256)) * glr_dp(p);
   l.words = c.take(l.n_words * 8);
@@ -442,7 +445,7 @@ gbla_status glr_begin(const gbla_shape* shape, int op, const void* x, const void
   a = GlrArgs{};
   a.x = x; a.r = r; a.i = i; a.ld = ld;
   a.lam = lam; a.c = cc; a.reverse = reverse; a.h0 = h0;
-  a.d = p.d; a.per_seq = p.per_seq; a.n_chunks = p.n_chunks;
+  a.d = p.d; a.pieces = p.slots ? cdiv(p.L, kGlrPiece) : 0;
   a.seq.mode = p.mode; a.seq.n_seq = p.n_seq; a.seq.L = p.mode == SEQ_VARLEN ? p.T : p.L; a.seq.T = p.T;
   a.seq.lens = shape->seq_lens; a.seq.cu = shape->cu_seqlens;
   a.err = p.mode == SEQ_DENSE ? nullptr : c.err;
@@ -1071,7 +1074,7 @@ gbla_status sa_core_forward(const gbla_shape* shape, const void* q, const void* 
 
 size_t glr_saved_size(const gbla_shape* shape) {
   GlrPlan p;
-  return make_glr_plan(shape, p) == GBLA_OK ? align_up((size_t)p.n_chunks * p.d * 4) : 0;
+  return make_glr_plan(shape, p) == GBLA_OK ? align_up((size_t)p.pieces * p.d * 4) : 0;
 }
 
 gbla_status glr_forward(const gbla_shape* shape, const void* x, const void* r, const void* i, int64_t ld,
@@ -1107,11 +1110,12 @@ gbla_status glr_backward(const gbla_shape* shape, const void* x, const void* r, 
   a.dy = dy; a.dhT = dhT; a.dx = dx; a.dr = dr; a.di = di; a.ldd = ldd; a.dh0 = dh0;
   a.dlam_part = dlam ? at<float>(ws, c.l.part) : nullptr;
   if ((s = glr_check_seqs(c)) != GBLA_OK) return s;
-  GBLA_CHECK(launch_glr_bwd(a, glr_tiles(c.p, kGlrChunk), c.p.f32, c.st), "glr bwd");
+  const GlrTiles t = glr_tiles(c.p, kGlrRowsBwd);
+  GBLA_CHECK(launch_glr_bwd(a, t, c.p.f32, c.st), "glr bwd");
   if (dlam) {
-    const int rows = std::min(kDlamRows, c.p.n_chunks);
+    const int rows = std::min(kDlamRows, t.n_chunks);
     float* sums = at<float>(ws, c.l.part2);
-    GBLA_CHECK(launch_glr_dlam(a, c.p.n_chunks, rows, rows > 1 ? sums : dlam, c.st), "glr dlam");
+    GBLA_CHECK(launch_glr_dlam(a, t.n_chunks, rows, rows > 1 ? sums : dlam, c.st), "glr dlam");
     if (rows > 1) {
       ColsumJobs js{};
       js.j[js.n++] = ColsumJob{sums, rows, c.p.d, c.p.d, dlam, nullptr, 0};

@@ -12,7 +12,7 @@
 // stay finite where a = 1.
 //
 // A thread walks one channel of one sequence.  The state on entry to every
-// kGlrChunk-row chunk is saved for the backward, which recomputes the states
+// piece of rows is saved for the backward, which recomputes the states
 // of a chunk from it.
 #include <algorithm>
 
@@ -167,7 +167,7 @@ __device__ __forceinline__ int seq_of(const GlrArgs& a, int64_t row) {
 
 // ------------------------------------------------------------ tiles
 constexpr int kWarpsF = 8, kWarpsB = 8;                                       // of a CTA, forward and backward
-constexpr int kPerF = kGlrRowsFwd / kWarpsF, kPerB = kGlrChunk / kWarpsB;     // a warp's rows; a lane has two channels of each
+constexpr int kPerF = kGlrRowsFwd / kWarpsF, kPerB = kGlrRowsBwd / kWarpsB;     // a warp's rows; a lane has two channels of each
 constexpr int kCtasFwd = 2, kCtasBwd = 2;                                     // an SM's
 
 // How a tile's rows are read: copied ahead into shared memory (rows of 16-byte pieces), or straight into registers by
@@ -549,14 +549,13 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     const Map2 pre = scan_local(a, me, sh.sc, it & 1, warp, lane, tot);
     scan_words(a, me, sh.sc, warp, lane, need, words, tot);
     float2 h = after(pre, scan_state(a, me, sh.sc, warp, lane, need, tot));
-    if (j0 % kGlrChunk == 0 && a.saved) {  // the backward's chunks are of kGlrChunk rows
-      const int p = a.reverse ? CH - kGlrChunk - j0 : j0;  // physical place of the piece in the chunk
-      if (p < me.c.nr) {
-        const int64_t piece = tl.per_seq ? (int64_t)me.c.b * a.per_seq + (me.c.k + p) / kGlrChunk : (me.c.r0 + p) / kGlrChunk;
-        store2<float, false>(a.saved, piece * a.d + ch, nch, h);
-      }
-    }
-    // the rows again, from the state that enters them
+    // the rows again, from the state that enters them; every kGlrPiece rows it is saved
+    static_assert(PER % kGlrPiece == 0, "a warp's rows are whole pieces");
+    const int64_t piece0 = a.pieces ? (int64_t)me.c.b * a.pieces + me.c.k / kGlrPiece : me.c.r0 / kGlrPiece;
+    auto save = [&](int p) {  // before the warp's row p
+      const int at = a.reverse ? CH - kGlrPiece - j0 - p : j0 + p;  // physical place of the piece in the chunk
+      if (at < me.c.nr) store2<float, false>(a.saved, (piece0 + at / kGlrPiece) * a.d + ch, nch, h);
+    };
     const int64_t step = a.reverse ? -a.d : a.d;
     int64_t o = row_at<CH>(a, me.c, j0) * a.d + ch;
     if (inner && (!a.hT || f.E == 0)) {
@@ -564,6 +563,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
         T* y = (T*)a.y + o;
 #pragma unroll
         for (int p = 0; p < PER; ++p, y += step) {
+          if (p % kGlrPiece == 0 && a.saved) save(p);
           h = fma2(da[p], h, u[p]);
           store2<T, true>(y, 0, 2, h);
         }
@@ -571,6 +571,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     } else {
 #pragma unroll
       for (int p = 0; p < PER; ++p, o += step) {
+        if (p % kGlrPiece == 0 && a.saved) save(p);
         if (f.F >> p & 1) h = u[p];
         else h = fma2(da[p], h, u[p]);
         store2<T, LOAD != GLR_SINGLE>(a.y, o, f.in >> p & 1 ? nch : 0, f.V >> p & 1 ? h : two(0.f));
@@ -595,8 +596,6 @@ __device__ __forceinline__ float2 half_s_over_sinh(const Gate2& g) {
   return p;
 }
 
-// What the backward holds of a row: a; p = m sig(i) (dx = w p); sig(i); s; then G = -a (s h_{t-1} - u s / (2 sinh s)) in the
-// place of s (e = w G) and x (1 - sig(i)) in that of sig(i) (di = dx times it); x and dy as they came.
 template <typename T> struct RowPair;
 template <> struct RowPair<bf16> {
   uint32_t w;
@@ -611,63 +610,95 @@ template <> struct RowPair<float> {
 
 template <typename T> constexpr int stages_bwd() { return sizeof(T) == 2 ? 2 : 1; }
 
+// What the backward holds of a row: a, p = m sig(i) (dx = w p), x (1 - sig(i)) (di is dx times it), G = -a (s h_{t-1} -
+// u s / (2 sinh s)) (e = w G), 1 - sig(r) (dr is e times it), dy as it came.
+template <typename T, int PER> struct Held { float2 a[PER], p[PER], x[PER], g[PER], o[PER]; RowPair<T> dy[PER]; };
+
+// The lane's rows: from the state h before them; A and D: what they do together to a w from behind, w -> A w + D.
 template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
 __device__ __forceinline__ void local_rows_bwd(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch, int nch,
-                                               float2 ka, float2 root2k, float2 (&da)[PER], float2 (&pp)[PER], float2 (&gi)[PER],
-                                               float2 (&s)[PER], RowPair<T> (&x)[PER], RowPair<T> (&dy)[PER], float2& A, float2& H, float2& D) {
+                                               float2 ka, float2 root2k, float2 h, Held<T, PER>& v, float2& A, float2& D) {
   const int64_t step = a.reverse ? -a.ld : a.ld, stepy = a.reverse ? -a.d : a.d;
   int64_t o = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.ld + ch, oy = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.d + ch;
   A = two(1.f);
-  H = D = two(0.f);
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
-    float2 r, i;
+    float2 r, i, x;
     if (LOAD == GLR_TMA) {
       r = lds2(sm + CH * 64);
       i = lds2(sm + 2 * CH * 64);
-      x[q] = *(const RowPair<T>*)sm;
-      dy[q] = *(const RowPair<T>*)(sm + 3 * CH * 64);
+      x = lds2(sm);
+      v.dy[q] = *(const RowPair<T>*)(sm + 3 * CH * 64);
       sm += a.reverse ? -64 : 64;
     } else {
       const int n = f.V >> q & 1 ? nch : 0;
       r = load2<T, LOAD == GLR_PAIRS>(a.r, o, n);
       i = load2<T, LOAD == GLR_PAIRS>(a.i, o, n);
-      x[q].set(load2<T, LOAD == GLR_PAIRS>(a.x, o, n));
-      dy[q].set(load2<T, LOAD == GLR_PAIRS>(a.dy, oy, n));
+      x = load2<T, LOAD == GLR_PAIRS>(a.x, o, n);
+      v.dy[q].set(load2<T, LOAD == GLR_PAIRS>(a.dy, oy, n));
       o += step;
       oy += stepy;
     }
     const Gate2 g = SMALL ? gate2_small(r, ka, root2k) : gate2_any(r, ka);
-    da[q] = g.a;
-    s[q] = g.s;
-    gi[q] = sigmoid2(i);
-    pp[q] = mul2(g.m, gi[q]);
-    if (!PLAIN) {
-      if (!(f.V >> q & 1)) {
-        da[q] = two(1.f);
-        pp[q] = s[q] = gi[q] = two(0.f);
-        x[q].set(two(0.f));
-        dy[q].set(two(0.f));
-      }
-      if (f.F >> q & 1) {
-        float2 h = two(0.f);
-        if (a.h0) h = load2<float, false>(a.h0, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch);
-        H = fma2(da[q], h, mul2(pp[q], x[q].get()));
-        continue;
-      }
+    const float2 gi = sigmoid2(i);
+    v.a[q] = g.a;
+    v.p[q] = mul2(g.m, gi);
+    v.x[q] = fma2(make_float2(-x.x, -x.y), gi, x);
+    v.o[q] = add2(two(1.f), make_float2(-g.sr.x, -g.sr.y));
+    const float2 u = mul2(v.p[q], x);
+    if (!PLAIN && (f.F >> q & 1))
+      h = a.h0 ? load2<float, false>(a.h0, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
+    const float2 sh = mul2(g.s, h);
+    v.g[q] = mul2(g.a, fma2(half_s_over_sinh<SMALL>(g), u, make_float2(-sh.x, -sh.y)));
+    h = fma2(g.a, h, u);
+    if (!PLAIN && !(f.V >> q & 1)) {
+      v.a[q] = two(1.f);
+      v.p[q] = v.x[q] = v.g[q] = v.o[q] = h = two(0.f);
+      v.dy[q].set(two(0.f));
     }
-    H = fma2(da[q], H, mul2(pp[q], x[q].get()));
-    A = mul2(A, da[q]);
+    A = mul2(A, v.a[q]);
   }
-  if (!PLAIN && (f.F | f.E)) {  // A is the product of all decays where it counts: rows behind a start or before an end
-    A = two(1.f);
-#pragma unroll
-    for (int q = 0; q < PER; ++q) A = mul2(A, da[q]);
-  }
+  D = two(0.f);
 #pragma unroll
   for (int q = PER - 1; q >= 0; --q) {
-    if (!PLAIN && (f.E >> q & 1)) D = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
-    D = mul2(da[q], add2(D, dy[q].get()));
+    if (!PLAIN && (f.E >> q & 1)) {
+      D = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
+      A = two(0.f);  // nothing from behind an end gets here
+    }
+    D = mul2(v.a[q], add2(D, v.dy[q].get()));
+  }
+}
+
+// The gradients, from the last row on, w what comes from behind it; dl: the rows' share of dlam.
+template <typename T, int LOAD, bool PLAIN, int PER, int CH>
+__device__ __forceinline__ void finish_rows_bwd(const GlrArgs& a, const Span& c, const Flags& f, int j0, int ch, int nch,
+                                                const Held<T, PER>& v, float2 w, float2& dl) {
+  dl = two(0.f);
+  const int64_t step = a.reverse ? a.ldd : -a.ldd;
+  const int64_t o0 = row_at<CH>(a, c, j0 + PER - 1) * a.ldd + ch;
+  T *px = (T*)a.dx + o0, *pr = (T*)a.dr + o0, *pi = (T*)a.di + o0;
+#pragma unroll
+  for (int q = PER - 1; q >= 0; --q, px += step, pr += step, pi += step) {
+    if (!PLAIN && (f.E >> q & 1)) w = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
+    w = add2(v.dy[q].get(), w);
+    const float2 dx = mul2(w, v.p[q]), di = mul2(dx, v.x[q]), e = mul2(w, v.g[q]), dr = mul2(e, v.o[q]);
+    w = mul2(v.a[q], w);
+    if (PLAIN) {
+      dl = add2(dl, e);
+      if (nch > 0) {
+        store2<T, true>(px, 0, 2, dx);
+        store2<T, true>(pr, 0, 2, dr);
+        store2<T, true>(pi, 0, 2, di);
+      }
+    } else {
+      const bool ok = f.V >> q & 1;
+      const int n = f.in >> q & 1 ? nch : 0;
+      if (ok) dl = add2(dl, e);
+      store2<T, LOAD != GLR_SINGLE>(px, 0, n, ok ? dx : two(0.f));
+      store2<T, LOAD != GLR_SINGLE>(pr, 0, n, ok ? dr : two(0.f));
+      store2<T, LOAD != GLR_SINGLE>(pi, 0, n, ok ? di : two(0.f));
+      if (a.dh0 && (f.F >> q & 1)) store2<float, false>(a.dh0, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch, w);
+    }
   }
 }
 
@@ -675,18 +706,17 @@ struct GlrMaps4 { CUtensorMap m[4]; };  // x, r, i, dy
 
 struct GlrSharedBwd {
   ScanShared<kWarpsB> sc;      // what the rows do to a w
-  float4 fwd[2][kWarpsB][32];  // what they do to a state
   float2 sum[2][kWarpsB][32];   // dlam of each warp's rows
   Tile tile[4];                // the CTA's n-th at n & 3
   uint64_t full[2];
 };
 
-// Backward: one pass from each sequence's end, x, r, i and dy read once, dx, dr and di written once; the states before the
-// rows come from the chunk's saved one, the w behind them as the forward's states do.  As the forward, with tiles of
-// kGlrChunk rows: a row's held values take eleven registers a pair of channels.
+// Backward: one pass from each sequence's end, x, r, i and dy read once, dx, dr and di written once; the states before a
+// warp's rows come from the saved one, the w behind them as the forward's states do.  As the forward, with half the rows:
+// what is held of a row takes eleven registers for a pair of channels.
 template <typename T, int LOAD>
 __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps4 maps) {
-  constexpr int PER = kPerB, CH = kGlrChunk, ST = stages_bwd<T>();
+  constexpr int PER = kPerB, CH = kGlrRowsBwd, ST = stages_bwd<T>();
   constexpr uint32_t BYTES = 4 * CH * 64 * sizeof(T), ALL = (1u << PER) - 1;
   extern __shared__ __align__(128) uint8_t raw[];
   pdl_enter();
@@ -710,12 +740,12 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     }
   };
   // dlam of a tile: its warps' sums in order
-  auto put_sum = [&](int q, int64_t piece, int ch0) {
+  auto put_sum = [&](int q, int64_t row, int ch0) {
     if (warp != 0 || !a.dlam_part) return;
     float2 v = two(0.f);
 #pragma unroll
     for (int w = 0; w < kWarpsB; ++w) v = add2(v, sh.sum[q][w][lane]);
-    store2<float, false>(a.dlam_part, piece * a.d + ch0 + 2 * lane, a.d - ch0 - 2 * lane, v);
+    store2<float, false>(a.dlam_part, row * a.d + ch0 + 2 * lane, a.d - ch0 - 2 * lane, v);
   };
   Drawn next;
   if (tid == 0) {
@@ -731,111 +761,55 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
   }
   __syncthreads();
 
-  int64_t last_piece = 0;
+  int64_t last_row = 0;
   int last_ch0 = 0;
   int it = 0;
   for (;; ++it) {
     const int st = it % ST;
     const Tile& t = sh.tile[it & 3];
     if (t.k < 0) break;
-    Words<kWarpsB> words;
-    ask(a, t, vw >> 1, (vw & 1) * 32 + lane, words);
     const int ch = t.ch0 + 2 * lane, nch = a.d - ch;
-    const int64_t piece = tl.per_seq ? (int64_t)t.c.b * tl.per_seq + t.c.k / CH : t.c.r0 / CH;
-    float2 h = load2<float, false>(a.saved, piece * a.d + ch, nch);  // the state before the chunk's rows
+    const int64_t row = tl.per_seq ? (int64_t)t.c.b * tl.per_seq + t.c.k / CH : t.c.r0 / CH;  // dlam's partial row
     const int j0 = warp * PER;
+    static_assert(PER == kGlrPiece, "a warp's rows are a piece");
+    const int at = a.reverse ? CH - PER - j0 : j0;  // physical place of the warp's piece in the chunk
+    const int64_t piece = (a.pieces ? (int64_t)t.c.b * a.pieces + t.c.k / PER : t.c.r0 / PER) + at / PER;
+    const float2 h = load2<float, false>(a.saved, piece * a.d + ch, at < t.c.nr ? nch : 0);
     const float2 ka = *(const float2*)(a.kd + ch);
     Flags f{ALL, ALL, 0, 0};
     if (!t.inner) f = flags_of<CH, PER>(a, t.c, tl.per_seq, j0, lane);
-    const bool inner = LOAD == GLR_TMA && f.V == ALL && (f.F | f.E) == 0;
+    const bool plain = LOAD == GLR_TMA && f.V == ALL && (f.F | f.E) == 0 && __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
     const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
     if (LOAD == GLR_TMA && !mbar_wait_bounded(full + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
-    float2 da[PER], pp[PER], gi[PER], s[PER], A, H, D;
-    RowPair<T> x[PER], dy[PER];
-    const bool small = __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
-    if (inner && small) {
-      const float2 root2k = make_float2(sqf(2.f * ka.x), sqf(2.f * ka.y));
-      local_rows_bwd<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, root2k, da, pp, gi, s, x, dy, A, H, D);
-    } else if (inner) {
-      local_rows_bwd<T, LOAD, false, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, pp, gi, s, x, dy, A, H, D);
-    } else {
-      local_rows_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, pp, gi, s, x, dy, A, H, D);
-    }
+    Held<T, PER> v;
+    float2 A, D;
+    if (plain) local_rows_bwd<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, make_float2(sqf(2.f * ka.x), sqf(2.f * ka.y)), h, v, A, D);
+    else local_rows_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, h, v, A, D);
+    Words<kWarpsB> words;
+    ask(a, t, vw >> 1, (vw & 1) * 32 + lane, words);
     const int tq = it & 1;
-    sh.fwd[tq][warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
-    sh.sc.agg[tq][vw][lane] = packed(Map2{f.E ? two(0.f) : A, D});
+    sh.sc.agg[tq][vw][lane] = packed(Map2{A, D});
     // whether a sequence ends with the chunk's last row: then nothing comes from behind
     const bool need = !__syncthreads_or(warp == kWarpsB - 1 && (f.E >> (PER - 1) & 1)) && t.k > 0;
     if (tid == 0) {
       fetch(next, it + ST);
       if (next.t < total) next.t = (unsigned)atomicAdd(a.ticket, 1ull);
     }
-    if (it > 0) put_sum(tq ^ 1, last_piece, last_ch0);
-    last_piece = piece;
+    if (it > 0) put_sum(tq ^ 1, last_row, last_ch0);
+    last_row = row;
     last_ch0 = t.ch0;
     Map2 tot;
     const Map2 pre = scan_local(a, t, sh.sc, tq, vw, lane, tot);
-    // the states before the warp's rows, and with them what e is of w
-    for (int w = 0; w < warp; ++w) h = after(map_at(sh.fwd[tq][w][lane]), h);
-    const float2 rk = make_float2(ka.x > 0.f ? 1.f / ka.x : 0.f, ka.y > 0.f ? 1.f / ka.y : 0.f);
-    float2 osr[PER];
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const float2 xv = x[q].get(), u = mul2(pp[q], xv);
-      if (!inner && (f.F >> q & 1)) h = a.h0 ? load2<float, false>(a.h0, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + q)) * a.d + ch, nch) : two(0.f);
-      Gate2 g;
-      g.a = da[q];
-      g.s = s[q];
-      float2 sg;
-      if (small) {
-        sg = half_s_over_sinh<true>(g);
-      } else {
-        const float2 z = fma2(make_float2(-da[q].x, -da[q].y), da[q], two(1.f));  // 1 - a^2, read where s >= 1/4
-        g.m = make_float2(sqf(z.x), sqf(z.y));
-        sg = half_s_over_sinh<false>(g);
-      }
-      const float2 su = mul2(sg, u), sh_ = mul2(s[q], h);
-      osr[q] = fma2(make_float2(-s[q].x, -s[q].y), rk, two(1.f));
-      s[q] = mul2(da[q], add2(su, make_float2(-sh_.x, -sh_.y)));  // G
-      gi[q] = fma2(make_float2(-xv.x, -xv.y), gi[q], xv);         // x (1 - sig(i))
-      h = fma2(da[q], h, u);
-    }
-    // a w from behind the warp's rows
     scan_words(a, t, sh.sc, vw, lane, need, words, tot);
-    float2 v = after(pre, scan_state(a, t, sh.sc, vw, lane, need, tot));
-    // the gradients, from the last row on
-    float2 dl = two(0.f);
-    const int64_t step = a.reverse ? a.ldd : -a.ldd;
-    int64_t o = row_at<CH>(a, t.c, j0 + PER - 1) * a.ldd + ch;
-#pragma unroll
-    for (int q = PER - 1; q >= 0; --q, o += step) {
-      if (!inner && (f.E >> q & 1)) v = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + q)) * a.d + ch, nch) : two(0.f);
-      const float2 w = add2(dy[q].get(), v);
-      v = mul2(da[q], w);
-      float2 dx = mul2(w, pp[q]), di = mul2(dx, gi[q]), e = mul2(w, s[q]), dr = mul2(e, osr[q]);
-      if (inner) {
-        dl = add2(dl, e);
-        if (nch > 0) {
-          store2<T, true>(a.dx, o, 2, dx);
-          store2<T, true>(a.dr, o, 2, dr);
-          store2<T, true>(a.di, o, 2, di);
-        }
-      } else {
-        const bool ok = f.V >> q & 1;
-        const int n = f.in >> q & 1 ? nch : 0;
-        if (ok) dl = add2(dl, e);
-        store2<T, LOAD != GLR_SINGLE>(a.dx, o, n, ok ? dx : two(0.f));
-        store2<T, LOAD != GLR_SINGLE>(a.dr, o, n, ok ? dr : two(0.f));
-        store2<T, LOAD != GLR_SINGLE>(a.di, o, n, ok ? di : two(0.f));
-        if (a.dh0 && (f.F >> q & 1)) store2<float, false>(a.dh0, (int64_t)seq_of(a, row_at<CH>(a, t.c, j0 + q)) * a.d + ch, nch, v);
-        if (!ok) v = dy[q].get();  // (0: a row of no sequence hands nothing on, whatever entered)
-      }
-    }
+    const float2 w = after(pre, scan_state(a, t, sh.sc, vw, lane, need, tot));
+    float2 dl;
+    if (plain) finish_rows_bwd<T, LOAD, true, PER, CH>(a, t.c, f, j0, ch, nch, v, w, dl);
+    else finish_rows_bwd<T, LOAD, false, PER, CH>(a, t.c, f, j0, ch, nch, v, w, dl);
     sh.sum[tq][warp][lane] = dl;
     if (tid == 0) decode<CH>(a, tl, total, !a.reverse, next, sh.tile[(it + ST + 1) & 3]);
   }
   __syncthreads();
-  if (it > 0) put_sum((it - 1) & 1, last_piece, last_ch0);
+  if (it > 0) put_sum((it - 1) & 1, last_row, last_ch0);
 }
 
 // dlam's partial rows n0 = blockIdx.y, n0 + gridDim.y, .. of 64 channels, summed in order, times the derivative of softplus over it.
@@ -952,11 +926,11 @@ template <typename T>
 cudaError_t run_glr_bwd(const GlrArgs& a, const GlrTiles& t, cudaStream_t st) {
   constexpr bool f32 = sizeof(T) == 4;
   GlrMaps4 maps{};
-  const bool tma = pairs_ok(a, sizeof(T)) && rows_map(&maps.m[0], a.x, f32, a.d, a.seq.T, a.ld, kGlrChunk) &&
-                   rows_map(&maps.m[1], a.r, f32, a.d, a.seq.T, a.ld, kGlrChunk) &&
-                   rows_map(&maps.m[2], a.i, f32, a.d, a.seq.T, a.ld, kGlrChunk) &&
-                   rows_map(&maps.m[3], a.dy, f32, a.d, a.seq.T, a.d, kGlrChunk);
-  const size_t smem = 128 + sizeof(GlrSharedBwd) + (tma ? stages_bwd<T>() * (size_t)4 * kGlrChunk * 64 * sizeof(T) : 0);
+  const bool tma = pairs_ok(a, sizeof(T)) && rows_map(&maps.m[0], a.x, f32, a.d, a.seq.T, a.ld, kGlrRowsBwd) &&
+                   rows_map(&maps.m[1], a.r, f32, a.d, a.seq.T, a.ld, kGlrRowsBwd) &&
+                   rows_map(&maps.m[2], a.i, f32, a.d, a.seq.T, a.ld, kGlrRowsBwd) &&
+                   rows_map(&maps.m[3], a.dy, f32, a.d, a.seq.T, a.d, kGlrRowsBwd);
+  const size_t smem = 128 + sizeof(GlrSharedBwd) + (tma ? stages_bwd<T>() * (size_t)4 * kGlrRowsBwd * 64 * sizeof(T) : 0);
   const dim3 grid((unsigned)std::min<int64_t>((int64_t)t.n_chunks * (a.dp >> 6), (int64_t)sm_count() * kCtasBwd));
   auto kernel = tma ? k_glr_bwd<T, GLR_TMA> : pairs_ok(a, sizeof(T)) ? k_glr_bwd<T, GLR_PAIRS> : k_glr_bwd<T, GLR_SINGLE>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -168,12 +168,13 @@ struct DecayArgs {
   const int* err;
 };
 
-// The gated linear recurrence (glr.cu).  Its rows are cut into chunks of
-// kGlrChunk: per sequence slot (per_seq chunks each; slots of at least kGlrSlot
-// rows, whose chunks then run side by side with the other slots') or, for packed
-// and short sequences, over all rows (per_seq = 0).
-constexpr int kGlrChunk = 64, kGlrSlot = 512;
-constexpr int kGlrRowsFwd = 128;  // rows of a tile of the forward (a state is saved every kGlrChunk of them)
+// The gated linear recurrence (glr.cu).  Its rows are cut into chunks of a tile's
+// rows: per sequence slot (slots of at least kGlrSlot rows, whose chunks then run
+// side by side with the other slots') or, for packed and short sequences, over
+// all rows (per_seq = 0).  The state on entry to every kGlrPiece rows (of a slot,
+// or of all rows) is saved for the backward.
+constexpr int kGlrSlot = 512, kGlrPiece = 8;
+constexpr int kGlrRowsFwd = 128, kGlrRowsBwd = 64;  // rows of a tile
 struct GlrDiv { uint32_t m; int s; };  // division by an invariant (quotient() in glr.cu)
 struct GlrTiles {
   int per_seq, n_chunks;               // chunks of a slot (0: one stream), of the call
@@ -185,14 +186,14 @@ struct GlrArgs {
   int reverse;
   const float* h0;                                          // [n_seq, d] or null
   void* y; float* hT;                                       // [T, d]; [n_seq, d] or null
-  float* saved;                                             // [chunks][d]: the state on entry to each chunk, or null
+  float* saved;                                             // [pieces][d]: the state on entry to each piece, or null
   // backward
   const void* dy; const float* dhT;                         // [T, d]; [n_seq, d] or null
   void* dx; void* dr; void* di; int64_t ldd;                // [T, ldd]
   float* dlam_part; float* dh0;                             // [chunks][d] or null; [n_seq, d] or null
   int d;
   SeqDesc seq;
-  int per_seq, n_chunks;
+  int pieces;                                               // of a slot (0: one stream)
   const uint64_t* marks;                                    // packed sequences: bit r % 64 of word r / 64: row r begins one
   uint64_t* words; int64_t dp;                              // the scan's words [chunks + groups + larger groups][dp], zero on entry
   unsigned long long* ticket;                               // the next tile, zero on entry

@@ -46,7 +46,7 @@ def test_shapes_and_sizes(L):
     small, big = gbla.glr_shape(2, 100, 48), gbla.glr_shape(32, 4096, 512)
     for op in (gbla.GBLA_OP_GLR_FORWARD, gbla.GBLA_OP_GLR_BACKWARD):
         assert 0 < gbla.gbla_workspace_size(small, op) <= gbla.gbla_workspace_size(big, op)
-    assert gbla.glr_saved_size(big) == 32 * 64 * 512 * 4  # a state per 64 rows
+    assert gbla.glr_saved_size(big) == 32 * 512 * 512 * 4  # a state per 8 rows
     assert 0 < gbla.glr_saved_size(small) < gbla.glr_saved_size(big)
     bad = gbla.glr_shape(2, 100, 48)
     bad.io_dtype = 9
