@@ -356,9 +356,8 @@ gbla_status begin(const gbla_shape* s, int op, void* ws, size_t ws_bytes, void* 
 // Sizes and workspace of glr_forward / glr_backward (their shape needs no heads).
 struct GlrPlan {
   bool f32;
-  int T, L, d, n_seq, mode;
-  bool slots;     // chunks per slot
-  int64_t pieces; // saved states
+  int T, L, d, n_seq, mode, cut;
+  int64_t pieces;  // saved states
 };
 
 gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
@@ -372,11 +371,15 @@ gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
   p.T = (int)T; p.L = s->L; p.d = s->d;
   p.mode = s->cu_seqlens ? SEQ_VARLEN : (s->seq_lens ? SEQ_PADDED : SEQ_DENSE);
   p.n_seq = s->cu_seqlens ? s->num_seqs : s->B;
-  if ((long long)p.n_seq * p.d > (1LL << 38)) return GBLA_ERR_UNSUPPORTED;  // one thread each
-  p.slots = p.mode != SEQ_VARLEN && p.L >= kGlrSlot;
-  p.pieces = p.slots ? (int64_t)p.n_seq * cdiv(p.L, kGlrPiece) : cdiv(p.T, kGlrPiece);
-  if ((p.slots ? (long long)p.n_seq * cdiv(p.L, kGlrRowsBwd) : cdiv(p.T, kGlrRowsBwd)) * cdiv(p.d, 64) > 0x7fffffffLL)
-    return GBLA_ERR_UNSUPPORTED;  // tiles are counted in 31 bits
+  if ((long long)p.n_seq * p.d > (1LL << 38) || p.n_seq > (1 << 30)) return GBLA_ERR_UNSUPPORTED;
+  // Packed sequences are cut one by one where they are long on the mean and the call is several rounds of tiles (the
+  // order's two kernels take 8 us; a 64 k-row, d = 1024 batch of long ones: 1.8 times as fast as in one stream).
+  const long long rounds = T / kGlrRowsFwd * cdiv(p.d, 64) / (2LL * sm_count());
+  p.cut = p.mode != SEQ_VARLEN ? (p.L >= kGlrSlot ? GLR_SLOTS : GLR_STREAM)
+          : T / p.n_seq >= kGlrSlot && rounds >= 3 && p.n_seq > 1 && T <= (8LL << 20) ? GLR_SEQS : GLR_STREAM;
+  p.pieces = p.cut == GLR_SLOTS ? (int64_t)p.n_seq * cdiv(p.L, kGlrPiece)
+             : p.cut == GLR_SEQS ? p.T / kGlrPiece + p.n_seq : cdiv(p.T, kGlrPiece);
+  if (((long long)p.T / kGlrRowsBwd + p.n_seq + 1) * cdiv(p.d, 64) > 0x7fffffffLL) return GBLA_ERR_UNSUPPORTED;  // tiles are counted in 31 bits
   return GBLA_OK;
 }
 
@@ -388,29 +391,39 @@ GlrDiv glr_div(uint32_t d) {
   return GlrDiv{(uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l - 1};
 }
 GlrTiles glr_tiles(const GlrPlan& p, int rows) {
-  GlrTiles t;
+  GlrTiles t{};
+  t.cut = p.cut;
+  t.rows = rows;
   t.by_cg = glr_div((uint32_t)cdiv(p.d, 64));
   t.by_seq = glr_div((uint32_t)p.n_seq);
-  t.per_seq = p.slots ? cdiv(p.L, rows) : 0;
-  t.n_chunks = t.per_seq ? t.per_seq * p.n_seq : cdiv(p.T, rows);
+  t.per_seq = p.cut == GLR_SLOTS ? cdiv(p.L, rows) : 0;
+  t.n_chunks = p.cut == GLR_SLOTS ? t.per_seq * p.n_seq : p.cut == GLR_SEQS ? p.T / rows + p.n_seq : cdiv(p.T, rows);
+  // word c of a slot or sequence whose rows begin at r, the s-th: r / rows + s + c; groups and larger groups alike
+  const int s = p.cut == GLR_STREAM ? 1 : p.n_seq;
+  t.n_words = p.T / rows + s;
+  t.n_groups = p.T / (16 * rows) + s;
+  t.levels = p.cut == GLR_SEQS ? cdiv(p.T, rows) : 0;
   return t;
 }
 constexpr int kDlamRows = 16;  // partial sums of dlam between its two kernels
-struct GlrLayout { size_t err, ticket, marks, zero_bytes, kd, words, n_words, part, part2, total; };
+struct GlrLayout { size_t err, ticket, count, level, marks, zero_bytes, kd, order, words, n_words, part, n_part, part2, total; };
 GlrLayout glr_layout(const GlrPlan& p, int op) {
   Cursor c;
   GlrLayout l{};
-  l.err = c.take(32);  // the error word, then the tile counter
+  const GlrTiles t = glr_tiles(p, op == GBLA_OP_GLR_FORWARD ? kGlrRowsFwd : kGlrRowsBwd);
+  l.err = c.take(32);  // the error word, then the tile counter, then the number of ordered chunks
   l.ticket = l.err + 16;
-  if (p.mode == SEQ_VARLEN) l.marks = c.take((size_t)cdiv(p.T, 64) * 8);
+  l.count = l.err + 24;
+  if (p.cut == GLR_SEQS) l.level = c.take((size_t)t.levels * 4);
+  else if (p.mode == SEQ_VARLEN) l.marks = c.take((size_t)cdiv(p.T, 64) * 8);
   l.zero_bytes = c.off;
   l.kd = c.take(glr_dp(p) * 4);
-  const GlrTiles t = glr_tiles(p, op == GBLA_OP_GLR_FORWARD ? kGlrRowsFwd : kGlrRowsBwd);
-  const size_t slots = t.per_seq ? p.n_seq : 1, n = t.per_seq ? t.per_seq : t.n_chunks;
-  l.n_words = (t.n_chunks + slots * ((n + 15) / 16) + slots * ((n + 255) / 256)) * glr_dp(p);
+  if (p.cut == GLR_SEQS) l.order = c.take((size_t)t.n_chunks * 16);
+  l.n_words = ((size_t)t.n_words + t.n_groups + p.T / (256 * t.rows) + (p.cut == GLR_STREAM ? 1 : p.n_seq)) * glr_dp(p);
   l.words = c.take(l.n_words * 8);
   if (op == GBLA_OP_GLR_BACKWARD) {
-    l.part = c.take((size_t)t.n_chunks * p.d * 4);
+    l.n_part = (size_t)t.n_chunks * p.d;
+    l.part = c.take(l.n_part * 4);
     l.part2 = c.take((size_t)kDlamRows * p.d * 4);
   }
   l.total = c.off;
@@ -420,6 +433,8 @@ GlrLayout glr_layout(const GlrPlan& p, int op) {
 struct GlrCtx {
   GlrPlan p;
   GlrLayout l;
+  GlrTiles t;
+  int* level;
   GlrArgs a;
   int* err;
   cudaStream_t st;
@@ -445,23 +460,32 @@ gbla_status glr_begin(const gbla_shape* shape, int op, const void* x, const void
   a = GlrArgs{};
   a.x = x; a.r = r; a.i = i; a.ld = ld;
   a.lam = lam; a.c = cc; a.reverse = reverse; a.h0 = h0;
-  a.d = p.d; a.pieces = p.slots ? cdiv(p.L, kGlrPiece) : 0;
+  a.d = p.d; a.pieces = p.cut == GLR_SLOTS ? cdiv(p.L, kGlrPiece) : 0;
   a.seq.mode = p.mode; a.seq.n_seq = p.n_seq; a.seq.L = p.mode == SEQ_VARLEN ? p.T : p.L; a.seq.T = p.T;
   a.seq.lens = shape->seq_lens; a.seq.cu = shape->cu_seqlens;
   a.err = p.mode == SEQ_DENSE ? nullptr : c.err;
   a.err_out = c.err;
   a.ticket = at<unsigned long long>(ws, c.l.ticket);
-  a.marks = p.mode == SEQ_VARLEN ? at<uint64_t>(ws, c.l.marks) : nullptr;
+  a.marks = p.mode == SEQ_VARLEN && p.cut == GLR_STREAM ? at<uint64_t>(ws, c.l.marks) : nullptr;
+  c.t = glr_tiles(p, op == GBLA_OP_GLR_FORWARD ? kGlrRowsFwd : kGlrRowsBwd);
+  c.level = nullptr;
+  if (p.cut == GLR_SEQS) {
+    c.t.order = at<int4>(ws, c.l.order);
+    c.t.n_order = at<int>(ws, c.l.count);
+    c.level = at<int>(ws, c.l.level);
+  }
   a.words = at<uint64_t>(ws, c.l.words);
   a.kd = at<float>(ws, c.l.kd);
   a.dp = (int64_t)glr_dp(p);
   return GBLA_OK;
 }
 
-// Clears the error word, the tile counter, the marks and the scan's words, forms c softplus(lam); checks the sequence data on the device.
-gbla_status glr_check_seqs(GlrCtx& c) {
+// Clears the error word, the tile counter, the marks and the scan's words, forms c softplus(lam), checks the sequence data on
+// the device, and orders the chunks of packed sequences.
+gbla_status glr_prepare(GlrCtx& c) {
   if (c.p.mode != SEQ_DENSE) GBLA_CHECK(cudaMemsetAsync(c.err, 0, c.l.zero_bytes, c.st), "memset");
-  GBLA_CHECK(launch_glr_prep(c.a, (int64_t)c.l.n_words, c.err, c.st), "glr prep");
+  GBLA_CHECK(launch_glr_prep(c.a, c.t, (int64_t)c.l.n_words, c.a.dlam_part ? (int64_t)c.l.n_part : 0, c.level, c.err, c.st), "glr prep");
+  if (c.p.cut == GLR_SEQS) GBLA_CHECK(launch_glr_order(c.a, c.t, c.level, c.st), "glr order");
   return GBLA_OK;
 }
 
@@ -1087,8 +1111,8 @@ gbla_status glr_forward(const gbla_shape* shape, const void* x, const void* r, c
   if (!y || reinterpret_cast<uintptr_t>(y) % es || !aligned4(hT)) return GBLA_ERR_INVALID_ARG;
   if (saved && reinterpret_cast<uintptr_t>(saved) % kAlign) return GBLA_ERR_INVALID_ARG;
   c.a.y = y; c.a.hT = hT; c.a.saved = static_cast<float*>(saved);
-  if ((s = glr_check_seqs(c)) != GBLA_OK) return s;
-  GBLA_CHECK(launch_glr_fwd(c.a, glr_tiles(c.p, kGlrRowsFwd), c.p.f32, c.st), "glr fwd");
+  if ((s = glr_prepare(c)) != GBLA_OK) return s;
+  GBLA_CHECK(launch_glr_fwd(c.a, c.t, c.p.f32, c.st), "glr fwd");
   if (hT && c.p.mode != SEQ_DENSE) GBLA_CHECK(launch_glr_empty(c.a, h0, hT, c.st), "glr empty");
   return GBLA_OK;
 }
@@ -1109,8 +1133,8 @@ gbla_status glr_backward(const gbla_shape* shape, const void* x, const void* r, 
   a.saved = static_cast<float*>(const_cast<void*>(saved));
   a.dy = dy; a.dhT = dhT; a.dx = dx; a.dr = dr; a.di = di; a.ldd = ldd; a.dh0 = dh0;
   a.dlam_part = dlam ? at<float>(ws, c.l.part) : nullptr;
-  if ((s = glr_check_seqs(c)) != GBLA_OK) return s;
-  const GlrTiles t = glr_tiles(c.p, kGlrRowsBwd);
+  if ((s = glr_prepare(c)) != GBLA_OK) return s;
+  const GlrTiles& t = c.t;
   GBLA_CHECK(launch_glr_bwd(a, t, c.p.f32, c.st), "glr bwd");
   if (dlam) {
     const int rows = std::min(kDlamRows, t.n_chunks);

@@ -110,14 +110,14 @@ __device__ __forceinline__ float sqf(float x) {
 }
 
 // ------------------------------------------------------------ chunks
-// The rows are cut into chunks (slots of at least kGlrSlot rows each into their own, everything else as one stream); a
-// chunk and 64 channels are a tile, a tile is one CTA's, and a warp has PER neighbouring rows of it.  A chunk's rows
+// The rows are cut into chunks (GlrCut); a chunk and 64 channels are a tile, a tile is one CTA's, and a warp has PER neighbouring rows of it.  A chunk's rows
 // are numbered in the direction of the recurrence.
 struct Span {
   int64_t r0;       // physical first row of the chunk
   int nr;           // its rows
-  int b;            // its slot (slots of their own)
-  int k;            // its first row in the slot
+  int b;            // its slot or sequence (where those are cut by themselves)
+  int k;            // its first row in that
+  int len;          // that one's valid rows
 };
 template <int CH>
 __device__ __forceinline__ int64_t row_at(const GlrArgs& a, const Span& c, int j) {
@@ -127,21 +127,21 @@ __device__ __forceinline__ int64_t row_at(const GlrArgs& a, const Span& c, int j
 // recurrence).  Whole warps call it.
 struct Flags { uint32_t in, V, F, E; };
 template <int CH, int N>
-__device__ __forceinline__ Flags flags_of(const GlrArgs& a, const Span& c, int per_seq, int j0, int lane) {
+__device__ __forceinline__ Flags flags_of(const GlrArgs& a, const Span& c, int cut, int j0, int lane) {
   const int j = j0 + min(lane, N - 1), p = a.reverse ? CH - 1 - j : j;  // place in the chunk
   const bool in = p < c.nr;
   bool v = in, s, z;
   const int64_t row = c.r0 + p;
-  if (a.seq.mode == SEQ_VARLEN) {
+  if (cut == GLR_STREAM && a.seq.mode == SEQ_VARLEN) {
     s = in && (a.marks[row >> 6] >> (row & 63) & 1);
     z = in && (row + 1 == a.seq.T || (a.marks[(row + 1) >> 6] >> ((row + 1) & 63) & 1));
   } else {
-    int b = c.b, pos = c.k + p;
-    if (!per_seq) {
-      b = (int)row / a.seq.L;
+    int pos = c.k + p, len = c.len;
+    if (cut == GLR_STREAM) {
+      const int b = (int)row / a.seq.L;
       pos = (int)row - b * a.seq.L;
+      len = a.seq.mode == SEQ_PADDED ? (in ? a.seq.lens[b] : 0) : a.seq.L;
     }
-    const int len = a.seq.mode == SEQ_PADDED ? (in ? a.seq.lens[b] : 0) : a.seq.L;
     v = in && pos < len;
     s = v && pos == 0;
     z = v && pos == len - 1;
@@ -155,7 +155,7 @@ __device__ __forceinline__ Flags flags_of(const GlrArgs& a, const Span& c, int p
   return f;
 }
 // The sequence of a row that is in one.
-__device__ __forceinline__ int seq_of(const GlrArgs& a, int64_t row) {
+__device__ __forceinline__ int seq_of(const GlrArgs& a, int64_t row) {  // (rows that begin or end one only: few)
   if (a.seq.mode != SEQ_VARLEN) return (int)(row / a.seq.L);
   int lo = 0, hi = a.seq.n_seq - 1;  // the last b with cu[b] <= row: it is not empty
   while (lo < hi) {
@@ -174,59 +174,76 @@ constexpr int kCtasFwd = 2, kCtasBwd = 2;                                     //
 // pairs of channels or single ones.
 enum GlrLoad { GLR_TMA = 0, GLR_PAIRS = 1, GLR_SINGLE = 2 };
 
-// A tile: channels from ch0, the chunk's rows, its place k in its slot's chain (-1: no tile) of last + 1, and where the
-// chain's words for it are.
+// A tile: channels from ch0, the chunk's rows, its place k in its chain (-1: no tile) of last + 1, and where the chain's words
+// for it, its saved states and its partial row of dlam are.
 struct Tile {
   int ch0, k, last;
   int inner;        // every row is inside one sequence and neither its first nor its last
   Span c;
   int64_t own, near, far, large;  // the chunk's word; its group's first; the one before its larger group's first; the larger group before
+  int64_t piece, row;
 };
 __device__ __forceinline__ unsigned quotient(unsigned n, GlrDiv d) {  // n / divisor (Granlund and Montgomery's method)
   const unsigned t = __umulhi(n, d.m);
   return d.s < 0 ? n : (t + ((n - t) >> 1)) >> d.s;
 }
-// Tile t of the call's; back: the chain runs from the last chunk.  `word` is what tells inner (inner_of), asked for here.
+// What of tile t has to be asked of memory.
 template <int CH>
-__device__ __forceinline__ Tile tile_of(const GlrArgs& a, const GlrTiles& g, unsigned t, bool back, uint64_t& word) {
-  Tile o;
+__device__ __forceinline__ int4 asked_of(const GlrArgs& a, const GlrTiles& g, unsigned t, bool back) {
+  const unsigned w = quotient(t, g.by_cg);
+  int4 e = make_int4(0, a.seq.L, 0, 0);
+  if (g.cut == GLR_SEQS) e = g.order[w];
+  if (g.cut == GLR_SLOTS && a.seq.mode == SEQ_PADDED) e.y = a.seq.lens[w - quotient(w, g.by_seq) * (unsigned)a.seq.n_seq];
+  if (g.cut == GLR_STREAM && a.seq.mode == SEQ_VARLEN) {  // whether rows of the chunk, or the one behind, begin a sequence
+    const int64_t r0 = (int64_t)(back ? g.n_chunks - 1 - (int)w : (int)w) * CH;
+    uint64_t m = 1;
+    if (r0 + CH < a.seq.T) {
+      m = a.marks[(r0 + CH) >> 6] & 1;
+#pragma unroll
+      for (int j = 0; j < CH / 64; ++j) m |= a.marks[(r0 >> 6) + j];
+    }
+    e.x = (int)(uint32_t)m;
+    e.y = (int)(uint32_t)(m >> 32);
+  }
+  return e;
+}
+// Tile t of the call's with that; back: the chain runs from the last chunk.
+template <int CH>
+__device__ __forceinline__ void tile_of(const GlrArgs& a, const GlrTiles& g, unsigned t, bool back, const int4& e, Tile& o) {
   const unsigned w = quotient(t, g.by_cg);
   o.ch0 = (int)(t - w * (unsigned)(a.dp >> 6)) * 64;
-  const int n = g.per_seq ? g.per_seq : g.n_chunks;
-  o.last = n - 1;
-  word = 0;
-  if (g.per_seq) {
+  int row0 = 0, s = 0, n = g.n_chunks, k = (int)w, rows = a.seq.T;
+  if (g.cut == GLR_SLOTS) {
     const unsigned q = quotient(w, g.by_seq);
-    o.c.b = (int)(w - q * (unsigned)a.seq.n_seq);
-    o.k = (int)q;
-    o.c.k = (back ? n - 1 - o.k : o.k) * CH;
-    o.c.r0 = (int64_t)o.c.b * a.seq.L + o.c.k;
-    o.c.nr = min(CH, a.seq.L - o.c.k);
-    word = a.seq.mode == SEQ_PADDED ? (uint64_t)a.seq.lens[o.c.b] : (uint64_t)a.seq.L;
-  } else {
-    o.c.b = o.c.k = 0;
-    o.k = (int)w;
-    o.c.r0 = (int64_t)(back ? n - 1 - o.k : o.k) * CH;
-    o.c.nr = (int)min((int64_t)CH, a.seq.T - o.c.r0);
-    if (a.seq.mode == SEQ_VARLEN && o.c.r0 + CH < a.seq.T) {
-      word = a.marks[(o.c.r0 + CH) >> 6] & 1;
-#pragma unroll
-      for (int j = 0; j < CH / 64; ++j) word |= a.marks[(o.c.r0 >> 6) + j];
-    }
+    s = (int)(w - q * (unsigned)a.seq.n_seq);
+    k = (int)q;
+    n = g.per_seq;
+    row0 = s * a.seq.L;
+    rows = a.seq.L;
+  } else if (g.cut == GLR_SEQS) {
+    row0 = e.x;
+    s = e.z;
+    k = e.w;
+    rows = e.y;
+    n = (rows + CH - 1) / CH;
   }
-  // the arrays hold each slot's words in the order of its chain: of chunks, of groups of 16, of 16 groups
-  const int64_t ng = (n + 15) >> 4, nl = (n + 255) >> 8, slots = g.per_seq ? a.seq.n_seq : 1, l = o.k >> 8;
-  const int64_t chunk = (int64_t)o.c.b * n, group = (int64_t)g.n_chunks + o.c.b * ng, large = (int64_t)g.n_chunks + slots * ng + o.c.b * nl;
-  o.own = (chunk + o.k) * a.dp + o.ch0;
-  o.near = (chunk + (o.k & ~15)) * a.dp + o.ch0;
-  o.far = (group + (l << 4) - 1) * a.dp + o.ch0;
-  o.large = (large + l - 1) * a.dp + o.ch0;
-  return o;
-}
-template <int CH>
-__device__ __forceinline__ int inner_of(const GlrArgs& a, const GlrTiles& g, const Tile& o, uint64_t word) {
-  if (g.per_seq) return o.c.k > 0 && o.c.k + CH < (int)word;
-  return a.seq.mode == SEQ_VARLEN && o.c.r0 + CH < a.seq.T && word == 0;
+  const int c = back ? n - 1 - k : k;
+  o.k = k;
+  o.last = n - 1;
+  o.c.b = s;
+  o.c.k = c * CH;
+  o.c.r0 = (int64_t)row0 + o.c.k;
+  o.c.nr = min(CH, rows - o.c.k);
+  o.c.len = e.y;
+  o.inner = g.cut == GLR_STREAM ? a.seq.mode == SEQ_VARLEN && (e.x | e.y) == 0 : o.c.k > 0 && o.c.k + CH < e.y;
+  // words of chunks, of groups of 16, of 16 groups: those of a chain in a row, in its order
+  const int64_t chunk = row0 / CH + s, group = (int64_t)g.n_words + row0 / (16 * CH) + s, large = (int64_t)g.n_words + g.n_groups + row0 / (256 * CH) + s;
+  o.own = (chunk + k) * a.dp + o.ch0;
+  o.near = (chunk + (k & ~15)) * a.dp + o.ch0;
+  o.far = (group + (k >> 8 << 4) - 1) * a.dp + o.ch0;
+  o.large = (large + (k >> 8) - 1) * a.dp + o.ch0;
+  o.piece = (g.cut == GLR_SLOTS ? (int64_t)s * a.pieces : row0 / kGlrPiece + s) + o.c.k / kGlrPiece;
+  o.row = g.cut == GLR_SLOTS ? (int64_t)s * n + c : row0 / CH + s + c;
 }
 
 // ------------------------------------------------------------ the scan between chunks
@@ -365,15 +382,9 @@ __device__ __forceinline__ float2 scan_state(const GlrArgs& a, const Tile& t, co
   return h;
 }
 
-// Thread 0's side of a CTA's tiles: the ticket of a tile is drawn as soon as the one before is fetched, decoded a good while
-// later (into the ring of tiles in shared memory), and what its rows are is looked at later still, so that no step waits
-// for memory.
-struct Drawn { unsigned t; uint64_t word; };
-template <int CH>
-__device__ __forceinline__ void decode(const GlrArgs& a, const GlrTiles& tl, unsigned total, bool back, Drawn& d, Tile& o) {
-  if (d.t < total) o = tile_of<CH>(a, tl, d.t, back, d.word);
-  else o.k = -1;
-}
+// Thread 0's side of a CTA's tiles: the ticket of a tile is drawn as soon as the one before is fetched, what it needs from
+// memory asked for a good while later, and looked at later still, so that no step waits.
+struct Drawn { unsigned t; int4 e; };
 
 // A pair of neighbouring channels of a row.  VEC: pairs are aligned and whole.
 template <typename T, bool VEC>
@@ -485,13 +496,14 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
   uint8_t* tiles = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
   GlrShared& sh = *reinterpret_cast<GlrShared*>(tiles + (LOAD == GLR_TMA ? ST * BYTES : 0));
   const uint32_t full = smem_u32(sh.full);
-  const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
+  const unsigned total = (unsigned)(tl.cut == GLR_SEQS ? *tl.n_order : tl.n_chunks) * (unsigned)(a.dp >> 6);
 
-  // thread 0: the CTA's n-th tile, decoded
+  // thread 0: the CTA's n-th tile
   auto fetch = [&](const Drawn& d, int n) {
     Tile& o = sh.tile[n & 3];
-    if (o.k < 0) return;
-    o.inner = inner_of<CH>(a, tl, o, d.word);
+    o.k = -1;
+    if (d.t >= total) return;
+    tile_of<CH>(a, tl, d.t, a.reverse, d.e, o);
     if (LOAD == GLR_TMA) {
       const int st = n % ST;
       mbar_expect_tx(full + 8 * st, BYTES);
@@ -508,7 +520,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     }
     for (int n = 0; n <= ST; ++n) {
       next.t = (unsigned)atomicAdd(a.ticket, 1ull);
-      decode<CH>(a, tl, total, a.reverse, next, sh.tile[n & 3]);
+      if (next.t < total) next.e = asked_of<CH>(a, tl, next.t, a.reverse);
       if (n < ST) fetch(next, n);
     }
   }
@@ -523,7 +535,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     const int j0 = warp * PER;
     const float2 ka = *(const float2*)(a.kd + ch);
     Flags f{ALL, ALL, 0, 0};
-    if (!me.inner) f = flags_of<CH, PER>(a, me.c, tl.per_seq, j0, lane);
+    if (!me.inner) f = flags_of<CH, PER>(a, me.c, tl.cut, j0, lane);
     const bool inner = LOAD == GLR_TMA && f.V == ALL && f.F == 0;
     const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
     if (LOAD == GLR_TMA && !mbar_wait_bounded(full + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
@@ -551,10 +563,9 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     float2 h = after(pre, scan_state(a, me, sh.sc, warp, lane, need, tot));
     // the rows again, from the state that enters them; every kGlrPiece rows it is saved
     static_assert(PER % kGlrPiece == 0, "a warp's rows are whole pieces");
-    const int64_t piece0 = a.pieces ? (int64_t)me.c.b * a.pieces + me.c.k / kGlrPiece : me.c.r0 / kGlrPiece;
     auto save = [&](int p) {  // before the warp's row p
       const int at = a.reverse ? CH - kGlrPiece - j0 - p : j0 + p;  // physical place of the piece in the chunk
-      if (at < me.c.nr) store2<float, false>(a.saved, (piece0 + at / kGlrPiece) * a.d + ch, nch, h);
+      if (at < me.c.nr) store2<float, false>(a.saved, (me.piece + at / kGlrPiece) * a.d + ch, nch, h);
     };
     const int64_t step = a.reverse ? -a.d : a.d;
     int64_t o = row_at<CH>(a, me.c, j0) * a.d + ch;
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
         if (a.hT && (f.E >> p & 1)) store2<float, false>(a.hT, (int64_t)seq_of(a, row_at<CH>(a, me.c, j0 + p)) * a.d + ch, nch, h);
       }
     }
-    if (tid == 0) decode<CH>(a, tl, total, a.reverse, next, sh.tile[(it + ST + 1) & 3]);
+    if (tid == 0 && next.t < total) next.e = asked_of<CH>(a, tl, next.t, a.reverse);
   }
 }
 
@@ -725,12 +736,13 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
   uint8_t* tiles = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
   GlrSharedBwd& sh = *reinterpret_cast<GlrSharedBwd*>(tiles + (LOAD == GLR_TMA ? ST * BYTES : 0));
   const uint32_t full = smem_u32(sh.full);
-  const unsigned total = (unsigned)tl.n_chunks * (unsigned)(a.dp >> 6);
+  const unsigned total = (unsigned)(tl.cut == GLR_SEQS ? *tl.n_order : tl.n_chunks) * (unsigned)(a.dp >> 6);
 
-  auto fetch = [&](const Drawn& d, int n) {  // thread 0: the CTA's n-th tile, decoded
+  auto fetch = [&](const Drawn& d, int n) {  // thread 0: the CTA's n-th tile (the chains run against the recurrence)
     Tile& o = sh.tile[n & 3];
-    if (o.k < 0) return;
-    o.inner = inner_of<CH>(a, tl, o, d.word);
+    o.k = -1;
+    if (d.t >= total) return;
+    tile_of<CH>(a, tl, d.t, !a.reverse, d.e, o);
     if (LOAD == GLR_TMA) {
       const int st = n % ST;
       mbar_expect_tx(full + 8 * st, BYTES);
@@ -755,7 +767,7 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     }
     for (int n = 0; n <= ST; ++n) {
       next.t = (unsigned)atomicAdd(a.ticket, 1ull);
-      decode<CH>(a, tl, total, !a.reverse, next, sh.tile[n & 3]);  // the chains run against the recurrence
+      if (next.t < total) next.e = asked_of<CH>(a, tl, next.t, !a.reverse);
       if (n < ST) fetch(next, n);
     }
   }
@@ -769,15 +781,15 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     const Tile& t = sh.tile[it & 3];
     if (t.k < 0) break;
     const int ch = t.ch0 + 2 * lane, nch = a.d - ch;
-    const int64_t row = tl.per_seq ? (int64_t)t.c.b * tl.per_seq + t.c.k / CH : t.c.r0 / CH;  // dlam's partial row
+    const int64_t row = t.row;
     const int j0 = warp * PER;
     static_assert(PER == kGlrPiece, "a warp's rows are a piece");
     const int at = a.reverse ? CH - PER - j0 : j0;  // physical place of the warp's piece in the chunk
-    const int64_t piece = (a.pieces ? (int64_t)t.c.b * a.pieces + t.c.k / PER : t.c.r0 / PER) + at / PER;
+    const int64_t piece = t.piece + at / PER;
     const float2 h = load2<float, false>(a.saved, piece * a.d + ch, at < t.c.nr ? nch : 0);
     const float2 ka = *(const float2*)(a.kd + ch);
     Flags f{ALL, ALL, 0, 0};
-    if (!t.inner) f = flags_of<CH, PER>(a, t.c, tl.per_seq, j0, lane);
+    if (!t.inner) f = flags_of<CH, PER>(a, t.c, tl.cut, j0, lane);
     const bool plain = LOAD == GLR_TMA && f.V == ALL && (f.F | f.E) == 0 && __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
     const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
     if (LOAD == GLR_TMA && !mbar_wait_bounded(full + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
@@ -806,7 +818,7 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     if (plain) finish_rows_bwd<T, LOAD, true, PER, CH>(a, t.c, f, j0, ch, nch, v, w, dl);
     else finish_rows_bwd<T, LOAD, false, PER, CH>(a, t.c, f, j0, ch, nch, v, w, dl);
     sh.sum[tq][warp][lane] = dl;
-    if (tid == 0) decode<CH>(a, tl, total, !a.reverse, next, sh.tile[(it + ST + 1) & 3]);
+    if (tid == 0 && next.t < total) next.e = asked_of<CH>(a, tl, next.t, !a.reverse);
   }
   __syncthreads();
   if (it > 0) put_sum((it - 1) & 1, last_row, last_ch0);
@@ -829,9 +841,10 @@ __global__ void __launch_bounds__(256) k_glr_dlam(const float* part, int64_t n, 
     out[(int64_t)blockIdx.y * d + ch] = (((red[0][threadIdx.x] + red[1][threadIdx.x]) + red[2][threadIdx.x]) + red[3][threadIdx.x]) * dsoftplus_ratio(lam[ch]);
 }
 
-// c softplus(lam), the scan's words and the tile counter cleared; checks the sequence data and, for packed sequences,
-// marks the rows that begin one (the error word and the marks are 0 on entry).
-__global__ void __launch_bounds__(256) k_glr_prep(const GlrArgs a, int64_t words, int* err) {
+// c softplus(lam), the scan's words and the tile counter cleared; checks the sequence data; marks the rows that begin a packed
+// sequence (STREAM), or counts the chunks of every level (SEQS: chunk k of n at level k levels / n, rounded down, so a
+// sequence's chunks are at different ones, in order).  The error word, marks and counts are 0 on entry.
+__global__ void __launch_bounds__(256) k_glr_prep(const GlrArgs a, const GlrTiles tl, int64_t words, int64_t parts, int* level, int* err) {
   pdl_enter();
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)gridDim.x * 256;
   if (id == 0) {
@@ -841,17 +854,69 @@ __global__ void __launch_bounds__(256) k_glr_prep(const GlrArgs a, int64_t words
   for (int64_t i = id; i < a.dp; i += n) a.kd[i] = i < a.d ? a.c * softplus_f(a.lam[i]) : 0.f;
   for (int64_t i = id; i < words / 2; i += n) ((ulonglong2*)a.words)[i] = make_ulonglong2(0, 0);
   if (a.seq.mode == SEQ_DENSE) return;
-  for (int64_t b = id; b < a.seq.n_seq; b += n) {
+  if (tl.cut == GLR_SEQS)  // rows of dlam's partial sums that no chunk has
+    for (int64_t i = id; i < parts; i += n) a.dlam_part[i] = 0.f;
+  const int lane = threadIdx.x & 31;
+  for (int64_t b = id >> 5; b < a.seq.n_seq; b += n >> 5) {  // a warp each
     if (a.seq.mode == SEQ_PADDED) {
-      if (a.seq.lens[b] < 0 || a.seq.lens[b] > a.seq.L) atomicOr(err, 1);
+      if (lane == 0 && (a.seq.lens[b] < 0 || a.seq.lens[b] > a.seq.L)) atomicOr(err, 1);
       continue;
     }
     const int lo = a.seq.cu[b], hi = a.seq.cu[b + 1];
     if (lo < 0 || hi < lo || hi > a.seq.T || (b == 0 && lo != 0) || (b == a.seq.n_seq - 1 && hi != a.seq.T)) {
-      atomicOr(err, 1);
+      if (lane == 0) atomicOr(err, 1);
       continue;
     }
-    if (lo < hi) atomicOr((unsigned long long*)a.marks + (lo >> 6), 1ull << (lo & 63));
+    if (tl.cut == GLR_SEQS) {
+      const int c = (hi - lo + tl.rows - 1) / tl.rows;
+      for (int k = lane; k < c; k += 32) atomicAdd(level + (int64_t)k * tl.levels / c, 1);
+    } else if (lane == 0 && lo < hi) {
+      atomicOr((unsigned long long*)a.marks + (lo >> 6), 1ull << (lo & 63));
+    }
+  }
+}
+
+// Counts to first places: their sums before, in place; the sum of all to *total.  One CTA.
+__global__ void __launch_bounds__(1024) k_glr_levels(int* level, int n, int* total, const int* err) {
+  pdl_enter();
+  __shared__ int wsum[32];
+  __shared__ int carry;
+  if (threadIdx.x == 0) carry = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int base = 0; base < n; base += 4096) {
+    const int i = base + threadIdx.x * 4;
+    int v[4], s = 0;
+    for (int j = 0; j < 4; ++j) s += v[j] = i + j < n ? level[i + j] : 0;
+    int x = s;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(FULLM, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    int at = before + x - s;
+    for (int j = 0; j < 4; ++j) {
+      if (i + j < n) level[i + j] = at;
+      at += v[j];
+    }
+    __syncthreads();
+    if (threadIdx.x == 1023) carry = before + x;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *total = *err ? 0 : carry;
+}
+
+// The chunks in the order of their levels (within one in any order: results do not depend on it).
+__global__ void __launch_bounds__(256) k_glr_place(const GlrArgs a, const GlrTiles tl, int* level) {
+  pdl_enter();
+  if (*a.err) return;
+  const int lane = threadIdx.x & 31;
+  for (int64_t b = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5; b < a.seq.n_seq; b += (int64_t)gridDim.x * 8) {
+    const int lo = a.seq.cu[b], hi = a.seq.cu[b + 1], c = (hi - lo + tl.rows - 1) / tl.rows;
+    for (int k = lane; k < c; k += 32)
+      const_cast<int4*>(tl.order)[atomicAdd(level + (int64_t)k * tl.levels / c, 1)] = make_int4(lo, hi - lo, (int)b, k);
   }
 }
 
@@ -877,10 +942,16 @@ bool pairs_ok(const GlrArgs& a, size_t es) {
 }
 }  // namespace
 
-cudaError_t launch_glr_prep(const GlrArgs& a, int64_t words, int* err, cudaStream_t st) {
-  const int64_t n = std::max<int64_t>(std::max<int64_t>(words / 2, a.dp), a.seq.mode == SEQ_DENSE ? 1 : a.seq.n_seq);
+cudaError_t launch_glr_prep(const GlrArgs& a, const GlrTiles& t, int64_t words, int64_t parts, int* level, int* err, cudaStream_t st) {
+  const int64_t n = std::max<int64_t>(std::max<int64_t>(words / 2, a.dp), a.seq.mode == SEQ_DENSE ? 1 : (int64_t)a.seq.n_seq * 32);
   const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sm_count() * 8);
-  return launch_pdl(k_glr_prep, dim3(grid), dim3(256), 0, st, a, words, err);
+  return launch_pdl(k_glr_prep, dim3(grid), dim3(256), 0, st, a, t, words, parts, level, err);
+}
+cudaError_t launch_glr_order(const GlrArgs& a, const GlrTiles& t, int* level, cudaStream_t st) {
+  const cudaError_t e = launch_pdl(k_glr_levels, dim3(1), dim3(1024), 0, st, level, t.levels, const_cast<int*>(t.n_order), a.err);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)a.seq.n_seq + 7) / 8, (int64_t)sm_count() * 4);
+  return launch_pdl(k_glr_place, dim3(grid), dim3(256), 0, st, a, t, level);
 }
 cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st) {
   k_glr_empty<<<(unsigned)std::min(a.seq.n_seq, 4096), 256, 0, st>>>(a, from, to);

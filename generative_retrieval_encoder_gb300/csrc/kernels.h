@@ -169,16 +169,29 @@ struct DecayArgs {
 };
 
 // The gated linear recurrence (glr.cu).  Its rows are cut into chunks of a tile's
-// rows: per sequence slot (slots of at least kGlrSlot rows, whose chunks then run
-// side by side with the other slots') or, for packed and short sequences, over
-// all rows (per_seq = 0).  The state on entry to every kGlrPiece rows (of a slot,
-// or of all rows) is saved for the backward.
-constexpr int kGlrSlot = 512, kGlrPiece = 8;
+// rows, in one of three ways (GlrCut):
+//   STREAM   all rows as one (many short sequences, or little work at all);
+//   SLOTS    each slot of a dense or padded batch by itself, chunk k of every
+//            slot before chunk k + 1 of any;
+//   SEQS     each packed sequence by itself, its chunks spread evenly over the
+//            call in an order made on the device (k_glr_place).
+// The state on entry to every kGlrPiece rows (of a slot or sequence, or of all
+// rows) is saved for the backward.
+enum GlrCut { GLR_STREAM = 0, GLR_SLOTS = 1, GLR_SEQS = 2 };
+constexpr int kGlrSlot = 512;                       // rows of a slot, and of a sequence on the mean, from which it is cut by itself
+constexpr int kGlrPiece = 8;
 constexpr int kGlrRowsFwd = 128, kGlrRowsBwd = 64;  // rows of a tile
-struct GlrDiv { uint32_t m; int s; };  // division by an invariant (quotient() in glr.cu)
+struct GlrDiv { uint32_t m; int s; };               // division by an invariant (quotient() in glr.cu)
 struct GlrTiles {
-  int per_seq, n_chunks;               // chunks of a slot (0: one stream), of the call
-  GlrDiv by_cg, by_seq;                // by the groups of 64 channels, by the slots
+  int cut;
+  int rows;                  // of a chunk
+  int per_seq;               // SLOTS: chunks of a slot
+  int n_chunks;              // chunks of the call; SEQS: at most
+  int n_words, n_groups;     // words of chunks, and of groups, before those of larger groups
+  int levels;                // SEQS: places in the order that a sequence's chunks are spread over
+  GlrDiv by_cg, by_seq;      // by the groups of 64 channels, by the slots
+  const int4* order;         // SEQS: {first row, rows, sequence, chunk} of each chunk in turn
+  const int* n_order;        // SEQS: how many
 };
 struct GlrArgs {
   const void* x; const void* r; const void* i; int64_t ld;  // [T, ld]
@@ -193,7 +206,7 @@ struct GlrArgs {
   float* dlam_part; float* dh0;                             // [chunks][d] or null; [n_seq, d] or null
   int d;
   SeqDesc seq;
-  int pieces;                                               // of a slot (0: one stream)
+  int pieces;                                               // SLOTS: of a slot
   const uint64_t* marks;                                    // packed sequences: bit r % 64 of word r / 64: row r begins one
   uint64_t* words; int64_t dp;                              // the scan's words [chunks + groups + larger groups][dp], zero on entry
   unsigned long long* ticket;                               // the next tile, zero on entry
@@ -296,7 +309,10 @@ cudaError_t launch_norm(const double* part, int n, float* norm, cudaStream_t st)
 
 // Checks the sequence data (error word *err) and marks the rows that begin a packed sequence.
 // Also forms a.kd and clears `words` words and the tile counter.
-cudaError_t launch_glr_prep(const GlrArgs& a, int64_t words, int* err, cudaStream_t st);
+// SEQS: counts the chunks of each place of the order (level[.] is 0 on entry) and clears `parts` values of a.dlam_part.
+cudaError_t launch_glr_prep(const GlrArgs& a, const GlrTiles& t, int64_t words, int64_t parts, int* level, int* err, cudaStream_t st);
+// SEQS: the order of the chunks into t.order, *t.n_order.
+cudaError_t launch_glr_order(const GlrArgs& a, const GlrTiles& t, int* level, cudaStream_t st);
 // to = from (or 0) for the sequences without tokens.
 cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st);
 cudaError_t launch_glr_fwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st);

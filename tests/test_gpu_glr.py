@@ -40,6 +40,8 @@ CASES = [
     dict(dtype="f32", d=8, L=20011, reverse=True, packed=True),
     dict(dtype="bf16", d=5, lengths=[17000, 3, 17500]),
     dict(dtype="f32", d=6, lengths=[3, 18000, 0, 1, 16400], reverse=True),
+    dict(dtype="bf16", d=2040, lengths=[700, 0, 2500, 1, 128, 1300, 0, 3003]),  # packed sequences cut one by one
+    dict(dtype="f32", d=1030, lengths=[129, 5000, 1, 0, 64, 3900, 2048], reverse=True),
 ]
 
 
@@ -166,10 +168,10 @@ def test_glr_in_pieces_and_in_place_steps():
     check({"y": torch.cat(out, 1).reshape(B * L, d), "hT": h}, want)
 
 
-@pytest.mark.parametrize("lengths", [None, [100, 0, 5000, 1, 63]])
-def test_glr_long_state_in_place(lengths):
+@pytest.mark.parametrize("d,lengths", [(72, None), (72, [100, 0, 5000, 1, 63]), (1024, [0, 3000, 100, 6000, 1])])
+def test_glr_long_state_in_place(d, lengths):
     kw = dict(lengths=lengths) if lengths else dict(L=1500, B=3)
-    c = Case("bf16", 72, seed=46, reverse=True, **kw)
+    c = Case("bf16", d, seed=46, reverse=True, **kw)
     want = c.reference(backward=False)
     y, hT, _ = gbla.glr_forward(c.shape, c.x, c.r, c.i, c.lam, reverse=True, h0=c.h0, hT=c.h0)
     torch.cuda.synchronize()
@@ -257,6 +259,25 @@ def test_glr_bad_sequence_data_is_reported():
         gbla.glr_backward(sh, x, x, x, lam, saved, x, ws=ws, out=out)
         assert gbla.gbla_check_device_status(ws) == gbla.GBLA_ERR_DEVICE_CHECK, kw
         assert all((t == 3).all() for t in out.values())
+
+
+def test_glr_bad_sequence_data_of_long_sequences_is_reported():
+    """The same where packed sequences are cut one by one."""
+    d, T = 1024, 8192
+    x = torch.randn(T, d, device="cuda").bfloat16()
+    lam = torch.zeros(d, device="cuda")
+    for cu in ([0, 5000, 4000, T], [0, 5000, T - 1], [0, 1 << 30, T], [0, -5, T], [2, 5000, T]):
+        sh = gbla.glr_shape(1, T, d, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        ws = gbla.workspace(sh, gbla.GBLA_OP_GLR_FORWARD)
+        y = torch.full_like(x, 3.0)
+        saved = torch.zeros(gbla.glr_saved_size(sh), dtype=torch.uint8, device="cuda")
+        gbla.glr_forward(sh, x, x, x, lam, y=y, ws=ws, saved=saved)
+        assert gbla.gbla_check_device_status(ws) == gbla.GBLA_ERR_DEVICE_CHECK, cu
+        ws = gbla.workspace(sh, gbla.GBLA_OP_GLR_BACKWARD)
+        out = {n: torch.full_like(x, 3.0) for n in ("dx", "dr", "di")}
+        gbla.glr_backward(sh, x, x, x, lam, saved, x, ws=ws, out=out)
+        assert gbla.gbla_check_device_status(ws) == gbla.GBLA_ERR_DEVICE_CHECK, cu
+        assert (y == 3).all() and all((t == 3).all() for t in out.values())
 
 
 def test_glr_good_call_reports_ok_and_checks_its_arguments():
