@@ -168,7 +168,7 @@ __device__ __forceinline__ int seq_of(const GlrArgs& a, int64_t row) {  // (rows
 // ------------------------------------------------------------ tiles
 constexpr int kWarpsF = 8, kWarpsB = 8;                                       // of a CTA, forward and backward
 constexpr int kPerF = kGlrRowsFwd / kWarpsF, kPerB = kGlrRowsBwd / kWarpsB;     // a warp's rows; a lane has two channels of each
-constexpr int kCtasFwd = 2, kCtasBwd = 2;                                     // an SM's
+constexpr int kCtasFwd = 2, kCtasBwd = 3;                                     // an SM's
 
 // How a tile's rows are read: copied ahead into shared memory (rows of 16-byte pieces), or straight into registers by
 // pairs of channels or single ones.
@@ -327,18 +327,18 @@ __device__ __forceinline__ Map answer(const GlrArgs& a, const Tile& t, int part,
   return m;
 }
 
-// Shared memory of the scan: what the rows of each warp (in the chain's order) do, tiles taking turns; the parts of the words.
+// Shared memory of the scan: what the rows of each warp (in the chain's order) do; the parts of the words.
 template <int W> struct ScanShared {
-  float4 agg[2][W][32];
+  float4 agg[W][32];
   float4 before[W / 2][32];
 };
-// After the warps' maps are in sc.agg[q]: what those before warp vw do, composed; the last warp publishes the tile's word.
+// After the warps' maps are in sc.agg: what those before warp vw do, composed; the last warp publishes the tile's word.
 template <int W>
-__device__ __forceinline__ Map2 scan_local(const GlrArgs& a, const Tile& t, const ScanShared<W>& sc, int q, int vw, int lane, Map2& total) {
+__device__ __forceinline__ Map2 scan_local(const GlrArgs& a, const Tile& t, const ScanShared<W>& sc, int vw, int lane, Map2& total) {
   Map2 m{two(1.f), two(0.f)};
-  for (int w = 0; w < vw; ++w) m = then(m, map_at(sc.agg[q][w][lane]));
+  for (int w = 0; w < vw; ++w) m = then(m, map_at(sc.agg[w][lane]));
   if (vw == W - 1) {
-    total = then(m, map_at(sc.agg[q][vw][lane]));
+    total = then(m, map_at(sc.agg[vw][lane]));
     if (t.k < t.last) publish(a.words + t.own + 2 * lane, total);
   }
   return m;
@@ -371,8 +371,8 @@ __device__ __forceinline__ void scan_words(const GlrArgs& a, const Tile& t, Scan
 template <int W>
 __device__ __forceinline__ float2 scan_state(const GlrArgs& a, const Tile& t, const ScanShared<W>& sc, int vw, int lane, bool need, const Map2& total) {
   float2 h = two(0.f);
+  __syncthreads();
   if (need) {
-    __syncthreads();
 #pragma unroll
     for (int q = 0; q < W / 2; ++q)
       if (q >= W / 4 || t.k >= 16) h = after(map_at(sc.before[q][lane]), h);
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     }
     Words<kWarpsF> words;
     ask(a, me, warp >> 1, (warp & 1) * 32 + lane, words);
-    sh.sc.agg[it & 1][warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
+    sh.sc.agg[warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
     // whether the chunk's first row begins a sequence: then nothing enters
     const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && me.k > 0;
     if (tid == 0) {
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
       if (next.t < total) next.t = (unsigned)atomicAdd(a.ticket, 1ull);
     }
     Map2 tot;
-    const Map2 pre = scan_local(a, me, sh.sc, it & 1, warp, lane, tot);
+    const Map2 pre = scan_local(a, me, sh.sc, warp, lane, tot);
     scan_words(a, me, sh.sc, warp, lane, need, words, tot);
     float2 h = after(pre, scan_state(a, me, sh.sc, warp, lane, need, tot));
     // the rows again, from the state that enters them; every kGlrPiece rows it is saved
@@ -619,55 +619,39 @@ template <> struct RowPair<float> {
   __device__ __forceinline__ void set(float2 o) { v = o; }
 };
 
-template <typename T> constexpr int stages_bwd() { return sizeof(T) == 2 ? 2 : 1; }
+constexpr int kStagesBwd = 2;
 
-// What the backward holds of a row: a, p = m sig(i) (dx = w p), x (1 - sig(i)) (di is dx times it), G = -a (s h_{t-1} -
-// u s / (2 sinh s)) (e = w G), 1 - sig(r) (dr is e times it), dy as it came.
-template <typename T, int PER> struct Held { float2 a[PER], p[PER], x[PER], g[PER], o[PER]; RowPair<T> dy[PER]; };
+// The backward goes over a tile's rows twice (they stay in shared memory): first for the decays, which with dy are all that
+// the scan of w takes, then, with w known, for everything else.  Held in between: a, and dy, whose place w takes.
 
-// The lane's rows: from the state h before them; A and D: what they do together to a w from behind, w -> A w + D.
+// The lane's rows, what they do together to a w from behind: w -> A w + D.  sm: the lane's first row of x in shared memory, r, i
+// and dy one, two and three tiles on.
 template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
-__device__ __forceinline__ void local_rows_bwd(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch, int nch,
-                                               float2 ka, float2 root2k, float2 h, Held<T, PER>& v, float2& A, float2& D) {
+__device__ __forceinline__ void decays_bwd(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch, int nch, float2 ka,
+                                           float2 (&da)[PER], RowPair<T> (&dy)[PER], float2& A, float2& D) {
   const int64_t step = a.reverse ? -a.ld : a.ld, stepy = a.reverse ? -a.d : a.d;
   int64_t o = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.ld + ch, oy = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.d + ch;
   A = two(1.f);
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
-    float2 r, i, x;
+    float2 r;
     if (LOAD == GLR_TMA) {
       r = lds2(sm + CH * 64);
-      i = lds2(sm + 2 * CH * 64);
-      x = lds2(sm);
-      v.dy[q] = *(const RowPair<T>*)(sm + 3 * CH * 64);
+      dy[q] = *(const RowPair<T>*)(sm + 3 * CH * 64);
       sm += a.reverse ? -64 : 64;
     } else {
       const int n = f.V >> q & 1 ? nch : 0;
       r = load2<T, LOAD == GLR_PAIRS>(a.r, o, n);
-      i = load2<T, LOAD == GLR_PAIRS>(a.i, o, n);
-      x = load2<T, LOAD == GLR_PAIRS>(a.x, o, n);
-      v.dy[q].set(load2<T, LOAD == GLR_PAIRS>(a.dy, oy, n));
+      dy[q].set(load2<T, LOAD == GLR_PAIRS>(a.dy, oy, n));
       o += step;
       oy += stepy;
     }
-    const Gate2 g = SMALL ? gate2_small(r, ka, root2k) : gate2_any(r, ka);
-    const float2 gi = sigmoid2(i);
-    v.a[q] = g.a;
-    v.p[q] = mul2(g.m, gi);
-    v.x[q] = fma2(make_float2(-x.x, -x.y), gi, x);
-    v.o[q] = add2(two(1.f), make_float2(-g.sr.x, -g.sr.y));
-    const float2 u = mul2(v.p[q], x);
-    if (!PLAIN && (f.F >> q & 1))
-      h = a.h0 ? load2<float, false>(a.h0, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
-    const float2 sh = mul2(g.s, h);
-    v.g[q] = mul2(g.a, fma2(half_s_over_sinh<SMALL>(g), u, make_float2(-sh.x, -sh.y)));
-    h = fma2(g.a, h, u);
+    da[q] = SMALL ? gate2_small(r, ka, ka).a : gate2_any(r, ka).a;
     if (!PLAIN && !(f.V >> q & 1)) {
-      v.a[q] = two(1.f);
-      v.p[q] = v.x[q] = v.g[q] = v.o[q] = h = two(0.f);
-      v.dy[q].set(two(0.f));
+      da[q] = two(1.f);
+      dy[q].set(two(0.f));
     }
-    A = mul2(A, v.a[q]);
+    A = mul2(A, da[q]);
   }
   D = two(0.f);
 #pragma unroll
@@ -676,24 +660,53 @@ __device__ __forceinline__ void local_rows_bwd(const GlrArgs& a, const T* sm, co
       D = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
       A = two(0.f);  // nothing from behind an end gets here
     }
-    D = mul2(v.a[q], add2(D, v.dy[q].get()));
+    D = mul2(da[q], add2(D, dy[q].get()));
   }
 }
 
-// The gradients, from the last row on, w what comes from behind it; dl: the rows' share of dlam.
-template <typename T, int LOAD, bool PLAIN, int PER, int CH>
-__device__ __forceinline__ void finish_rows_bwd(const GlrArgs& a, const Span& c, const Flags& f, int j0, int ch, int nch,
-                                                const Held<T, PER>& v, float2 w, float2& dl) {
-  dl = two(0.f);
-  const int64_t step = a.reverse ? a.ldd : -a.ldd;
-  const int64_t o0 = row_at<CH>(a, c, j0 + PER - 1) * a.ldd + ch;
-  T *px = (T*)a.dx + o0, *pr = (T*)a.dr + o0, *pi = (T*)a.di + o0;
+// The gradients: w of every row from the last on, v what comes from behind it; then from the first row on, from the state h
+// before it.  dl: the rows' share of dlam.
+template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
+__device__ __forceinline__ void gradients(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch, int nch, float2 ka,
+                                          float2 root2k, const float2 (&da)[PER], const RowPair<T> (&dy)[PER], float2 v, float2 h, float2& dl) {
+  float2 w[PER];
 #pragma unroll
-  for (int q = PER - 1; q >= 0; --q, px += step, pr += step, pi += step) {
-    if (!PLAIN && (f.E >> q & 1)) w = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
-    w = add2(v.dy[q].get(), w);
-    const float2 dx = mul2(w, v.p[q]), di = mul2(dx, v.x[q]), e = mul2(w, v.g[q]), dr = mul2(e, v.o[q]);
-    w = mul2(v.a[q], w);
+  for (int q = PER - 1; q >= 0; --q) {
+    if (!PLAIN && (f.E >> q & 1)) v = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
+    w[q] = add2(dy[q].get(), v);
+    v = mul2(da[q], w[q]);
+    if (!PLAIN && a.dh0 && (f.F >> q & 1)) store2<float, false>(a.dh0, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch, v);
+  }
+  dl = two(0.f);
+  const int64_t step = a.reverse ? -a.ld : a.ld, stepd = a.reverse ? -a.ldd : a.ldd;
+  int64_t o = LOAD == GLR_TMA ? 0 : row_at<CH>(a, c, j0) * a.ld + ch;
+  const int64_t od = row_at<CH>(a, c, j0) * a.ldd + ch;
+  T *px = (T*)a.dx + od, *pr = (T*)a.dr + od, *pi = (T*)a.di + od;
+#pragma unroll
+  for (int q = 0; q < PER; ++q, px += stepd, pr += stepd, pi += stepd) {
+    float2 r, i, x;
+    const bool ok = PLAIN || (f.V >> q & 1);
+    if (LOAD == GLR_TMA) {
+      r = lds2(sm + CH * 64);
+      i = lds2(sm + 2 * CH * 64);
+      x = lds2(sm);
+      sm += a.reverse ? -64 : 64;
+    } else {
+      const int n = ok ? nch : 0;
+      r = load2<T, LOAD == GLR_PAIRS>(a.r, o, n);
+      i = load2<T, LOAD == GLR_PAIRS>(a.i, o, n);
+      x = load2<T, LOAD == GLR_PAIRS>(a.x, o, n);
+      o += step;
+    }
+    if (!PLAIN && (f.F >> q & 1))
+      h = a.h0 ? load2<float, false>(a.h0, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
+    Gate2 g = SMALL ? gate2_small(r, ka, root2k) : gate2_any(r, ka);
+    const float2 gi = sigmoid2(i), p = mul2(g.m, gi), u = mul2(p, x), sh = mul2(g.s, h);
+    g.a = ok ? da[q] : g.a;
+    const float2 G = mul2(g.a, fma2(half_s_over_sinh<SMALL>(g), u, make_float2(-sh.x, -sh.y)));  // e = w G
+    h = fma2(g.a, h, u);
+    const float2 dx = mul2(w[q], p), di = mul2(dx, fma2(make_float2(-x.x, -x.y), gi, x)), e = mul2(w[q], G);
+    const float2 dr = mul2(e, add2(two(1.f), make_float2(-g.sr.x, -g.sr.y)));
     if (PLAIN) {
       dl = add2(dl, e);
       if (nch > 0) {
@@ -702,13 +715,12 @@ __device__ __forceinline__ void finish_rows_bwd(const GlrArgs& a, const Span& c,
         store2<T, true>(pi, 0, 2, di);
       }
     } else {
-      const bool ok = f.V >> q & 1;
       const int n = f.in >> q & 1 ? nch : 0;
       if (ok) dl = add2(dl, e);
+      else h = two(0.f);
       store2<T, LOAD != GLR_SINGLE>(px, 0, n, ok ? dx : two(0.f));
       store2<T, LOAD != GLR_SINGLE>(pr, 0, n, ok ? dr : two(0.f));
       store2<T, LOAD != GLR_SINGLE>(pi, 0, n, ok ? di : two(0.f));
-      if (a.dh0 && (f.F >> q & 1)) store2<float, false>(a.dh0, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch, w);
     }
   }
 }
@@ -717,17 +729,18 @@ struct GlrMaps4 { CUtensorMap m[4]; };  // x, r, i, dy
 
 struct GlrSharedBwd {
   ScanShared<kWarpsB> sc;      // what the rows do to a w
-  float2 sum[2][kWarpsB][32];   // dlam of each warp's rows
+  float2 sum[kWarpsB][32];      // dlam of each warp's rows
   Tile tile[4];                // the CTA's n-th at n & 3
   uint64_t full[2];
 };
 
 // Backward: one pass from each sequence's end, x, r, i and dy read once, dx, dr and di written once; the states before a
-// warp's rows come from the saved one, the w behind them as the forward's states do.  As the forward, with half the rows:
-// what is held of a row takes eleven registers for a pair of channels.
+// warp's rows come from the saved one, the w behind them as the forward's states do.  As the forward, with half the rows in a
+// tile and three CTAs an SM.  Every tile has two barriers between the first and the second pass, so what one tile leaves in
+// shared memory for them is read before the next one's is written.
 template <typename T, int LOAD>
 __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps4 maps) {
-  constexpr int PER = kPerB, CH = kGlrRowsBwd, ST = stages_bwd<T>();
+  constexpr int PER = kPerB, CH = kGlrRowsBwd, ST = kStagesBwd;
   constexpr uint32_t BYTES = 4 * CH * 64 * sizeof(T), ALL = (1u << PER) - 1;
   extern __shared__ __align__(128) uint8_t raw[];
   pdl_enter();
@@ -752,11 +765,11 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     }
   };
   // dlam of a tile: its warps' sums in order
-  auto put_sum = [&](int q, int64_t row, int ch0) {
+  auto put_sum = [&](int64_t row, int ch0) {
     if (warp != 0 || !a.dlam_part) return;
     float2 v = two(0.f);
 #pragma unroll
-    for (int w = 0; w < kWarpsB; ++w) v = add2(v, sh.sum[q][w][lane]);
+    for (int w = 0; w < kWarpsB; ++w) v = add2(v, sh.sum[w][lane]);
     store2<float, false>(a.dlam_part, row * a.d + ch0 + 2 * lane, a.d - ch0 - 2 * lane, v);
   };
   Drawn next;
@@ -793,35 +806,34 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     const bool plain = LOAD == GLR_TMA && f.V == ALL && (f.F | f.E) == 0 && __all_sync(FULLM, ka.x < 0.25f && ka.y < 0.25f);
     const T* sm = (const T*)(tiles + st * BYTES) + (a.reverse ? CH - 1 - j0 : j0) * 64 + 2 * lane;
     if (LOAD == GLR_TMA && !mbar_wait_bounded(full + 8 * st, (it / ST) & 1)) atomicOr(a.err_out, kErrTimeout);
-    Held<T, PER> v;
-    float2 A, D;
-    if (plain) local_rows_bwd<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, make_float2(sqf(2.f * ka.x), sqf(2.f * ka.y)), h, v, A, D);
-    else local_rows_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, h, v, A, D);
+    float2 da[PER], A, D;
+    RowPair<T> dy[PER];
+    if (plain) decays_bwd<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, da, dy, A, D);
+    else decays_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, da, dy, A, D);
     Words<kWarpsB> words;
     ask(a, t, vw >> 1, (vw & 1) * 32 + lane, words);
-    const int tq = it & 1;
-    sh.sc.agg[tq][vw][lane] = packed(Map2{A, D});
+    sh.sc.agg[vw][lane] = packed(Map2{A, D});
     // whether a sequence ends with the chunk's last row: then nothing comes from behind
     const bool need = !__syncthreads_or(warp == kWarpsB - 1 && (f.E >> (PER - 1) & 1)) && t.k > 0;
-    if (tid == 0) {
-      fetch(next, it + ST);
+    if (tid == 0 && it > 0) {  // the tile before has been gone over: its place is free
+      fetch(next, it + 1);
       if (next.t < total) next.t = (unsigned)atomicAdd(a.ticket, 1ull);
     }
-    if (it > 0) put_sum(tq ^ 1, last_row, last_ch0);
+    if (it > 0) put_sum(last_row, last_ch0);
     last_row = row;
     last_ch0 = t.ch0;
     Map2 tot;
-    const Map2 pre = scan_local(a, t, sh.sc, tq, vw, lane, tot);
+    const Map2 pre = scan_local(a, t, sh.sc, vw, lane, tot);
     scan_words(a, t, sh.sc, vw, lane, need, words, tot);
-    const float2 w = after(pre, scan_state(a, t, sh.sc, vw, lane, need, tot));
+    const float2 v = after(pre, scan_state(a, t, sh.sc, vw, lane, need, tot));
     float2 dl;
-    if (plain) finish_rows_bwd<T, LOAD, true, PER, CH>(a, t.c, f, j0, ch, nch, v, w, dl);
-    else finish_rows_bwd<T, LOAD, false, PER, CH>(a, t.c, f, j0, ch, nch, v, w, dl);
-    sh.sum[tq][warp][lane] = dl;
+    if (plain) gradients<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, make_float2(sqf(2.f * ka.x), sqf(2.f * ka.y)), da, dy, v, h, dl);
+    else gradients<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, ka, da, dy, v, h, dl);
+    sh.sum[warp][lane] = dl;
     if (tid == 0 && next.t < total) next.e = asked_of<CH>(a, tl, next.t, !a.reverse);
   }
   __syncthreads();
-  if (it > 0) put_sum((it - 1) & 1, last_row, last_ch0);
+  if (it > 0) put_sum(last_row, last_ch0);
 }
 
 // dlam's partial rows n0 = blockIdx.y, n0 + gridDim.y, .. of 64 channels, summed in order, times the derivative of softplus over it.
@@ -920,6 +932,35 @@ __global__ void __launch_bounds__(256) k_glr_place(const GlrArgs a, const GlrTil
   }
 }
 
+// A few tokens of many sequences (one of each: serving): a thread for two channels of a sequence, no scan and no other launch.
+// Bound by the latency of one load and the launch.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(128) k_glr_step(const GlrArgs a, int* err) {
+  pdl_enter();
+  const int pairs = (a.d + 1) / 2;
+  const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
+  if (id == 0) *err = 0;
+  if (id >= (int64_t)a.seq.n_seq * pairs) return;
+  const int64_t b = id / pairs;
+  const int ch = 2 * (int)(id - b * pairs), nch = a.d - ch;
+  const int64_t row0 = b * a.seq.L + (a.reverse ? a.seq.L - 1 : 0), step = a.reverse ? -1 : 1;
+  float2 r = load2<T, VEC>(a.r, row0 * a.ld + ch, nch), i = load2<T, VEC>(a.i, row0 * a.ld + ch, nch), x = load2<T, VEC>(a.x, row0 * a.ld + ch, nch);
+  float2 h = a.h0 ? load2<float, false>(a.h0, b * a.d + ch, nch) : two(0.f), ka = two(0.f);
+  ka.x = a.c * softplus_f(a.lam[ch]);
+  if (nch > 1) ka.y = a.c * softplus_f(a.lam[ch + 1]);
+  for (int t = 0; t < a.seq.L; ++t) {
+    const Gate2 g = gate2_any(r, ka);
+    h = fma2(g.a, h, mul2(g.m, mul2(sigmoid2(i), x)));
+    store2<T, VEC>(a.y, (row0 + t * step) * a.d + ch, nch, h);
+    if (t + 1 == a.seq.L) break;
+    const int64_t o = (row0 + (t + 1) * step) * a.ld + ch;
+    r = load2<T, VEC>(a.r, o, nch);
+    i = load2<T, VEC>(a.i, o, nch);
+    x = load2<T, VEC>(a.x, o, nch);
+  }
+  if (a.hT) store2<float, false>(a.hT, b * a.d + ch, nch, h);
+}
+
 // A sequence without tokens hands its state on.
 __global__ void __launch_bounds__(256) k_glr_empty(const GlrArgs a, const float* from, float* to) {
   if (a.err && *a.err) return;
@@ -952,6 +993,11 @@ cudaError_t launch_glr_order(const GlrArgs& a, const GlrTiles& t, int* level, cu
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)a.seq.n_seq + 7) / 8, (int64_t)sm_count() * 4);
   return launch_pdl(k_glr_place, dim3(grid), dim3(256), 0, st, a, t, level);
+}
+cudaError_t launch_glr_step(const GlrArgs& a, bool f32, int* err, cudaStream_t st) {
+  const dim3 grid((unsigned)(((int64_t)a.seq.n_seq * ((a.d + 1) / 2) + 127) / 128));
+  if (f32) return launch_pdl(pairs_ok(a, 4) ? k_glr_step<float, true> : k_glr_step<float, false>, grid, dim3(128), 0, st, a, err);
+  return launch_pdl(pairs_ok(a, 2) ? k_glr_step<bf16, true> : k_glr_step<bf16, false>, grid, dim3(128), 0, st, a, err);
 }
 cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st) {
   k_glr_empty<<<(unsigned)std::min(a.seq.n_seq, 4096), 256, 0, st>>>(a, from, to);
@@ -1001,7 +1047,7 @@ cudaError_t run_glr_bwd(const GlrArgs& a, const GlrTiles& t, cudaStream_t st) {
                    rows_map(&maps.m[1], a.r, f32, a.d, a.seq.T, a.ld, kGlrRowsBwd) &&
                    rows_map(&maps.m[2], a.i, f32, a.d, a.seq.T, a.ld, kGlrRowsBwd) &&
                    rows_map(&maps.m[3], a.dy, f32, a.d, a.seq.T, a.d, kGlrRowsBwd);
-  const size_t smem = 128 + sizeof(GlrSharedBwd) + (tma ? stages_bwd<T>() * (size_t)4 * kGlrRowsBwd * 64 * sizeof(T) : 0);
+  const size_t smem = 128 + sizeof(GlrSharedBwd) + (tma ? kStagesBwd * (size_t)4 * kGlrRowsBwd * 64 * sizeof(T) : 0);
   const dim3 grid((unsigned)std::min<int64_t>((int64_t)t.n_chunks * (a.dp >> 6), (int64_t)sm_count() * kCtasBwd));
   auto kernel = tma ? k_glr_bwd<T, GLR_TMA> : pairs_ok(a, sizeof(T)) ? k_glr_bwd<T, GLR_PAIRS> : k_glr_bwd<T, GLR_SINGLE>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -313,6 +313,8 @@ cudaError_t launch_norm(const double* part, int n, float* norm, cudaStream_t st)
 cudaError_t launch_glr_prep(const GlrArgs& a, const GlrTiles& t, int64_t words, int64_t parts, int* level, int* err, cudaStream_t st);
 // SEQS: the order of the chunks into t.order, *t.n_order.
 cudaError_t launch_glr_order(const GlrArgs& a, const GlrTiles& t, int* level, cudaStream_t st);
+// The forward of dense slots of few rows, nothing saved; clears *err.
+cudaError_t launch_glr_step(const GlrArgs& a, bool f32, int* err, cudaStream_t st);
 // to = from (or 0) for the sequences without tokens.
 cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st);
 cudaError_t launch_glr_fwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st);

@@ -7,7 +7,6 @@ raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -173,13 +172,6 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _on(device):
-    """The device a call's tensors are on, made current for the launch."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
 def _check(status: int, what: str):
     if status != GBLA_OK:
         raise GblaError(status, what)
@@ -311,30 +303,43 @@ def glr_saved_size(shape: Shape) -> int:
     return lib().glr_saved_size(ctypes.byref(shape))
 
 
-def _glr_arg(name, t, shape_, dtype, device, ld=None):
-    """t's row stride.  Raises unless t is a tensor of this shape, dtype and device, its rows contiguous and (ld) of
-    this stride, all else contiguous."""
-    if t.dtype != dtype or tuple(t.shape) != shape_ or t.device != device:
-        raise ValueError(f"{name}: want {dtype} {list(shape_)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
-    n = t.stride(0) if t.dim() == 2 and t.size(0) > 1 else (ld or t.shape[-1])
-    if t.size(-1) > 1 and t.stride(-1) != 1 or n < t.shape[-1] or (ld is not None and n != ld):
-        raise ValueError(f"{name}: strides {t.stride()}: rows have to be contiguous, and of one stride where tensors share it")
-    return n
+def _glr_arg(name, t, n, d, dtype, device, ld):
+    """t's address.  Raises unless t is an [n, d] tensor of this dtype and device with contiguous rows of stride ld."""
+    if t.dtype is not dtype or t.device != device or t.shape != (n, d):
+        raise ValueError(f"{name}: want {dtype} {[n, d]} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if t.stride() != (ld, 1) and (n > 1 and t.stride(0) != ld or d > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: strides {t.stride()}, want {(ld, 1)}: rows are contiguous, and of one stride in x, r and i, "
+                         "in dx, dr and di, and d in all else")
+    return t.data_ptr()
 
 
-def _glr_check(shape, x, r, i, lam, h0):
-    dev, d, io = x.device, shape.d, io_dtype(shape)
+def _glr_vec(name, t, d, device):
+    if t.dtype is not torch.float32 or t.device != device or t.shape != (d,) or (d > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: want contiguous fp32 [{d}] on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _glr_bytes(name, t, n, device):
+    if t.device != device or not t.is_contiguous() or t.numel() * t.element_size() < n:
+        raise ValueError(f"{name}: want {n} contiguous bytes on {device}, got {t.numel() * t.element_size()} on {t.device}")
+    return t.data_ptr()
+
+
+def _glr_inputs(shape, x, r, i, lam, h0):
+    dev, d, io, T = x.device, shape.d, io_dtype(shape), rows(shape)
     if not x.is_cuda:
         raise ValueError(f"x: want a CUDA tensor, got {x.device}")
-    T = rows(shape)
-    lds = [t.stride(0) for t in (x, r, i) if t.dim() == 2 and t.size(0) > 1]
-    ld = lds[0] if lds else d
-    for name, t in (("x", x), ("r", r), ("i", i)):
-        _glr_arg(name, t, (T, d), io, dev, ld)
-    _glr_arg("lam", lam, (d,), torch.float32, dev)
-    if h0 is not None:
-        _glr_arg("h0", h0, (n_seq(shape), d), torch.float32, dev, d)
-    return ld
+    ld = x.stride(0) if T > 1 and x.dim() == 2 else d
+    return (ld, *[_glr_arg(n, t, T, d, io, dev, ld) for n, t in (("x", x), ("r", r), ("i", i))], _glr_vec("lam", lam, d, dev),
+            None if h0 is None else _glr_arg("h0", h0, n_seq(shape), d, torch.float32, dev, d))
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args, torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, torch.cuda.current_stream().cuda_stream)
 
 
 def glr_forward(shape: Shape, x, r, i, lam, c: float = 8.0, reverse: bool = False, h0=None, y=None, hT=None,
@@ -342,65 +347,51 @@ def glr_forward(shape: Shape, x, r, i, lam, c: float = 8.0, reverse: bool = Fals
     """The gated linear recurrence (see gbla.h): returns (y, hT, saved).  x, r and i share their row stride (they may
     be columns of one tensor).  hT: a tensor to fill (h0 itself to update it in place), or True to allocate it; saved =
     True allocates what glr_backward needs.  Tensors are on x's device, the call on that device's current stream."""
-    ld = _glr_check(shape, x, r, i, lam, h0)
+    ld, px, pr, pi, pl, ph = _glr_inputs(shape, x, r, i, lam, h0)
     dev, T, d = x.device, rows(shape), shape.d
     if y is None:
-        y = torch.empty(T, d, dtype=x.dtype, device=dev)
-    _glr_arg("y", y, (T, d), x.dtype, dev, d)
+        y = torch.empty((T, d), dtype=x.dtype, device=dev)
+    py = _glr_arg("y", y, T, d, x.dtype, dev, d)
     if hT is True:
-        hT = torch.empty(n_seq(shape), d, dtype=torch.float32, device=dev)
-    if hT is not None:
-        _glr_arg("hT", hT, (n_seq(shape), d), torch.float32, dev, d)
+        hT = torch.empty((n_seq(shape), d), dtype=torch.float32, device=dev)
+    pT = None if hT is None else ph if hT is h0 else _glr_arg("hT", hT, n_seq(shape), d, torch.float32, dev, d)
     if saved is True:
         saved = torch.empty(glr_saved_size(shape), dtype=torch.uint8, device=dev)
     saved = saved if isinstance(saved, torch.Tensor) else None
-    if saved is not None:
-        _glr_saved(shape, saved, dev)
+    ps = None if saved is None else _glr_bytes("saved", saved, glr_saved_size(shape), dev)
     if ws is None:
         ws = workspace(shape, GBLA_OP_GLR_FORWARD, dev)
-    with _on(dev):
-        st = lib().glr_forward(ctypes.byref(shape), _ptr(x), _ptr(r), _ptr(i), ld, _ptr(lam), c, int(reverse), _ptr(h0),
-                               _ptr(y), _ptr(hT), _ptr(saved), _ptr(ws), ws.numel(), _stream())
-    _check(st, "glr_forward")
+    st = _call(dev, lib().glr_forward, ctypes.byref(shape), px, pr, pi, ld, pl, c, int(reverse), ph, py, pT, ps,
+               _glr_bytes("ws", ws, 0, dev), ws.numel() * ws.element_size())
+    if st != GBLA_OK:
+        raise GblaError(st, "glr_forward")
     return y, hT, saved
-
-
-def _glr_saved(shape, saved, dev):
-    n = glr_saved_size(shape)
-    if saved.device != dev or not saved.is_contiguous() or saved.numel() * saved.element_size() < n:
-        raise ValueError(f"saved: want {n} bytes on {dev}")
 
 
 def glr_backward(shape: Shape, x, r, i, lam, saved, dy, c: float = 8.0, reverse: bool = False, h0=None, dhT=None,
                  ws=None, out: dict | None = None) -> dict:
     """Backward of glr_forward for <dy, y> + <dhT, hT>.  Returns dx, dr, di (io dtype), dlam fp32 and, where h0 or dhT
     is given, dh0 fp32.  out: tensors to fill (dx, dr and di of one row stride)."""
-    ld = _glr_check(shape, x, r, i, lam, h0)
-    dev, T, d = x.device, rows(shape), shape.d
-    _glr_arg("dy", dy, (T, d), x.dtype, dev, d)
-    if dhT is not None:
-        _glr_arg("dhT", dhT, (n_seq(shape), d), torch.float32, dev, d)
-    _glr_saved(shape, saved, dev)
+    ld, px, pr, pi, pl, ph = _glr_inputs(shape, x, r, i, lam, h0)
+    dev, T, d, N, f32 = x.device, rows(shape), shape.d, n_seq(shape), torch.float32
     g = out
     if g is None:
-        g = {n: torch.empty(T, d, dtype=x.dtype, device=dev) for n in ("dx", "dr", "di")}
-        g["dlam"] = torch.empty(d, dtype=torch.float32, device=dev)
+        g = {n: torch.empty((T, d), dtype=x.dtype, device=dev) for n in ("dx", "dr", "di")}
+        g["dlam"] = torch.empty(d, dtype=f32, device=dev)
         if h0 is not None or dhT is not None:
-            g["dh0"] = torch.empty(n_seq(shape), d, dtype=torch.float32, device=dev)
-    ldd = g["dx"].stride(0) if T > 1 else d
-    for n in ("dx", "dr", "di"):
-        _glr_arg(n, g[n], (T, d), x.dtype, dev, ldd)
-    if g.get("dlam") is not None:
-        _glr_arg("dlam", g["dlam"], (d,), torch.float32, dev)
-    if g.get("dh0") is not None:
-        _glr_arg("dh0", g["dh0"], (n_seq(shape), d), torch.float32, dev, d)
+            g["dh0"] = torch.empty((N, d), dtype=f32, device=dev)
+    ldd = g["dx"].stride(0) if T > 1 and g["dx"].dim() == 2 else d
+    pg = [_glr_arg(n, g[n], T, d, x.dtype, dev, ldd) for n in ("dx", "dr", "di")]
+    dl, dh = g.get("dlam"), g.get("dh0")
     if ws is None:
         ws = workspace(shape, GBLA_OP_GLR_BACKWARD, dev)
-    with _on(dev):
-        st = lib().glr_backward(ctypes.byref(shape), _ptr(x), _ptr(r), _ptr(i), ld, _ptr(lam), c, int(reverse), _ptr(h0),
-                                _ptr(saved), _ptr(dy), _ptr(dhT), _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["di"]), ldd,
-                                _ptr(g.get("dlam")), _ptr(g.get("dh0")), _ptr(ws), ws.numel(), _stream())
-    _check(st, "glr_backward")
+    st = _call(dev, lib().glr_backward, ctypes.byref(shape), px, pr, pi, ld, pl, c, int(reverse), ph,
+               _glr_bytes("saved", saved, glr_saved_size(shape), dev), _glr_arg("dy", dy, T, d, x.dtype, dev, d),
+               None if dhT is None else _glr_arg("dhT", dhT, N, d, f32, dev, d), *pg, ldd,
+               None if dl is None else _glr_vec("dlam", dl, d, dev), None if dh is None else _glr_arg("dh0", dh, N, d, f32, dev, d),
+               _glr_bytes("ws", ws, 0, dev), ws.numel() * ws.element_size())
+    if st != GBLA_OK:
+        raise GblaError(st, "glr_backward")
     return g
 
 
@@ -516,9 +507,8 @@ def gbla_grad_norm(plan: AdamWPlan, norm: torch.Tensor | None = None) -> torch.T
         norm = torch.empty((), dtype=torch.float32, device=plan.device)
     else:
         plan._tensor("norm", norm, 1, (torch.float32,))
-    with _on(plan.device):
-        st = lib().gbla_grad_norm(plan.tensors, plan.n, _ptr(norm), _ptr(plan.ws), plan.ws.numel(), _stream())
-    _check(st, "gbla_grad_norm")
+    _check(_call(plan.device, lib().gbla_grad_norm, plan.tensors, plan.n, norm.data_ptr(), plan.ws.data_ptr(), plan.ws.numel()),
+           "gbla_grad_norm")
     return norm
 
 
@@ -540,10 +530,8 @@ def gbla_adamw_step(plan: AdamWPlan, lr: float, betas=(0.9, 0.999), eps: float =
             plan.tensors[j].weight_decay = w
         plan._decay = wd
     cfg = AdamWConfig(lr, betas[0], betas[1], eps, max_norm or 0.0, seed)
-    with _on(plan.device):
-        st = lib().gbla_adamw_step(plan.tensors, plan.n, ctypes.byref(cfg), _ptr(plan.step), _ptr(norm), _ptr(plan.ws),
-                                   plan.ws.numel(), _stream())
-    _check(st, "gbla_adamw_step")
+    _check(_call(plan.device, lib().gbla_adamw_step, plan.tensors, plan.n, ctypes.byref(cfg), plan.step.data_ptr(),
+                 None if norm is None else norm.data_ptr(), plan.ws.data_ptr(), plan.ws.numel()), "gbla_adamw_step")
 
 
 def bla_core_forward_noalloc(shape: Shape, q, k, v, g, o, den=None, state=None) -> int:
