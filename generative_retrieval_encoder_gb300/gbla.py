@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -396,6 +397,8 @@ def glr_backward(shape: Shape, x, r, i, lam, saved, dy, c: float = 8.0, reverse:
 
 
 _ADAMW_DTYPE = {torch.float32: GBLA_F32, torch.bfloat16: GBLA_BF16}
+_ADAMW_ROW = np.dtype([(n, {ctypes.c_void_p: np.uint64, ctypes.c_int64: np.int64, ctypes.c_int: np.int32, ctypes.c_double: np.float64}[t])
+                       for n, t in AdamWTensor._fields_], align=True)
 
 
 def _named(tensors):
@@ -432,51 +435,60 @@ class AdamWPlan:
         self.device = self.step.device
         if self.step.dtype != torch.int64 or self.step.numel() != 1 or not self.step.is_cuda:
             raise ValueError(f"step: want one int64 on a CUDA device, got {self.step.dtype} on {self.step.device}")
-        self.tensors = (AdamWTensor * self.n)()
-        self._written, self._keep, self._decay = [], [P, state], None
-        lists = {k: state.get(k) or [None] * self.n for k in ("m", "v", "m_scale", "v_scale", "master")}
-        for k, t in lists.items():
+        self.sizes = [p.numel() for p in P]
+        self._keep, self._decay = [P, state], None
+        none = [None] * self.n
+        M, V, MS, VS, MA = (list(state.get(k) or none) for k in ("m", "v", "m_scale", "v_scale", "master"))
+        for k, t in (("m", M), ("v", V), ("m_scale", MS), ("v_scale", VS), ("master", MA)):
             if len(t) != self.n:
                 raise ValueError(f"{k}: {len(t)} tensors for {self.n} parameters")
-        for j, p in enumerate(P):
-            name = names[j] if names else f"params[{j}]"
-            e, n = self.tensors[j], p.numel()
-            e.n = n
-            e.param, e.param_dtype = self._out(name, p, n, tuple(_ADAMW_DTYPE)), _ADAMW_DTYPE[p.dtype]
-            m, v, ms, vs, ma = (lists[k][j] for k in ("m", "v", "m_scale", "v_scale", "master"))
-            if (ms is None) != (vs is None) or m is None or v is None:
-                raise ValueError(f"{name}: want m and v, and both scales or neither")
-            kind = (torch.float32,) if ms is None else (torch.float8_e4m3fn,)
-            e.m, e.v = self._out(f"m of {name}", m, n, kind), self._out(f"v of {name}", v, n, kind)
-            if ms is not None:
-                e.m_scale = self._out(f"m_scale of {name}", ms, -(-n // ADAMW_BLOCK), (torch.float32,))
-                e.v_scale = self._out(f"v_scale of {name}", vs, -(-n // ADAMW_BLOCK), (torch.float32,))
-            if ma is not None:
-                if p.dtype != torch.bfloat16:
-                    raise ValueError(f"master of {name}: only a bf16 parameter has one")
-                e.master = self._out(f"master of {name}", ma, n, (torch.float32,))
-        self._written.append((self.step.data_ptr(), 8, "step"))
-        self._written.sort()
-        for (a, na, wa), (b, _, wb) in zip(self._written, self._written[1:]):
-            if a + na > b:
-                raise ValueError(f"{wa} and {wb} overlap")
+        written = [(self.step.data_ptr(), 8, "step")]
+        blocks = [-(-n // ADAMW_BLOCK) for n in self.sizes]
+        kind = [torch.float32 if s is None else torch.float8_e4m3fn for s in MS]
+        cols = {"param": self._column("parameter", P, self.sizes, None, written),
+                "m": self._column("m", M, self.sizes, kind, written), "v": self._column("v", V, self.sizes, kind, written),
+                "m_scale": self._column("m_scale", MS, blocks, [torch.float32] * self.n, written, VS),
+                "v_scale": self._column("v_scale", VS, blocks, [torch.float32] * self.n, written, MS),
+                "master": self._column("master", MA, self.sizes, [torch.float32] * self.n, written, MA)}
+        for p, t in zip(P, MA):
+            if t is not None and p.dtype is not torch.bfloat16:
+                raise ValueError("master: only a bf16 parameter has one")
+        written.sort()
+        end, who = 0, None
+        for at, size, name in written:
+            if at < end:
+                raise ValueError(f"{who} and {name} overlap")
+            end, who = at + size, name
+        self.tensors = (AdamWTensor * self.n)()
+        self._rows = np.frombuffer(self.tensors, dtype=_ADAMW_ROW) if self.n else np.empty(0, _ADAMW_ROW)
+        for k, col in cols.items():
+            self._rows[k] = col
+        self._rows["n"] = self.sizes
+        self._rows["param_dtype"] = [_ADAMW_DTYPE[p.dtype] for p in P]
         self.set_grads(grads)
         size = lib().gbla_adamw_workspace_size(self.tensors, self.n)
         if size == 0:
             _check(GBLA_ERR_INVALID_ARG, "gbla_adamw_workspace_size")
         self.ws = torch.empty(size, dtype=torch.uint8, device=self.device)
 
-    def _tensor(self, name, t, n, dtypes):
-        if t.dtype not in dtypes or t.numel() != n or t.device != self.device or not t.is_contiguous():
-            raise ValueError(f"{name}: want {n} contiguous values of {' or '.join(map(str, dtypes))} on {self.device}, got "
-                             f"{list(t.shape)} {t.dtype} on {t.device}")
-        return t.data_ptr()
-
-    def _out(self, name, t, n, dtypes):
-        at = self._tensor(name, t, n, dtypes)
-        if n:
-            self._written.append((at, n * t.element_size(), name))
-        return at
+    def _column(self, what, tensors, sizes, dtypes, written=None, like=None):
+        """The addresses of one tensor for every parameter; dtypes: what each has to be (None: fp32 or bf16); where `like` is
+        given a parameter may have none, if it has none of `like` either."""
+        dev, col = self.device, []
+        for j, (t, n) in enumerate(zip(tensors, sizes)):
+            if t is None and like is not None and like[j] is None:
+                col.append(0)
+                continue
+            if (t is None or t.numel() != n or t.device != dev or not t.is_contiguous()
+                    or (t.dtype not in _ADAMW_DTYPE if dtypes is None else t.dtype is not dtypes[j])):
+                want = "fp32 or bf16" if dtypes is None else dtypes[j]
+                got = "none" if t is None else f"{list(t.shape)} {t.dtype} on {t.device}"
+                raise ValueError(f"{what} of {self.names[j] if self.names else j}: want {n} contiguous values of {want} on {dev}, got {got}")
+            at = t.data_ptr() if n else 0
+            col.append(at)
+            if n and written is not None:
+                written.append((at, n * t.element_size(), what))
+        return col
 
     def set_grads(self, grads):
         """Other gradient tensors for the same parameters: a sequence in their order, or a dict by their names (with or
@@ -489,9 +501,8 @@ class AdamWPlan:
             G = list(grads)
         if len(G) != self.n:
             raise ValueError(f"{len(G)} gradients for {self.n} parameters")
-        at = [self._tensor(f"gradient {j}", g, self.tensors[j].n, tuple(_ADAMW_DTYPE)) for j, g in enumerate(G)]
-        for j, g in enumerate(G):
-            self.tensors[j].grad, self.tensors[j].grad_dtype = at[j], _ADAMW_DTYPE[g.dtype]
+        self._rows["grad"] = self._column("gradient", G, self.sizes, None)
+        self._rows["grad_dtype"] = [_ADAMW_DTYPE[g.dtype] for g in G]
         self._grads = G
 
 
@@ -506,7 +517,7 @@ def gbla_grad_norm(plan: AdamWPlan, norm: torch.Tensor | None = None) -> torch.T
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=plan.device)
     else:
-        plan._tensor("norm", norm, 1, (torch.float32,))
+        plan._column("norm", [norm], [1], [torch.float32])
     _check(_call(plan.device, lib().gbla_grad_norm, plan.tensors, plan.n, norm.data_ptr(), plan.ws.data_ptr(), plan.ws.numel()),
            "gbla_grad_norm")
     return norm
@@ -518,7 +529,7 @@ def gbla_adamw_step(plan: AdamWPlan, lr: float, betas=(0.9, 0.999), eps: float =
     gbla_grad_norm's, which gradients are clipped by (max_norm) and which skips the step where it is not finite; seed: of
     the 8-bit states' rounding."""
     if norm is not None:
-        plan._tensor("norm", norm, 1, (torch.float32,))
+        plan._column("norm", [norm], [1], [torch.float32])
     if max_norm is not None and norm is None:
         raise ValueError("max_norm needs norm (gbla_grad_norm)")
     wd = tuple(weight_decay) if isinstance(weight_decay, (list, tuple)) else weight_decay
@@ -526,8 +537,7 @@ def gbla_adamw_step(plan: AdamWPlan, lr: float, betas=(0.9, 0.999), eps: float =
         each = wd if isinstance(wd, tuple) else (wd,) * plan.n
         if len(each) != plan.n:
             raise ValueError(f"weight_decay: {len(each)} values for {plan.n} parameters")
-        for j, w in enumerate(each):
-            plan.tensors[j].weight_decay = w
+        plan._rows["weight_decay"] = each
         plan._decay = wd
     cfg = AdamWConfig(lr, betas[0], betas[1], eps, max_norm or 0.0, seed)
     _check(_call(plan.device, lib().gbla_adamw_step, plan.tensors, plan.n, ctypes.byref(cfg), plan.step.data_ptr(),
