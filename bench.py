@@ -11,6 +11,8 @@ Prints one JSON line (rank 0).  --impl reference times the fp64 CPU oracle on
 a bounded sample of the same workload instead.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME] [--impl ours|reference]
+                  [--update [--state-bits 8|32]]
+--update adds the parameters' AdamW step (gbla_grad_norm, gbla_adamw_step) to every step.
 """
 from __future__ import annotations
 
@@ -369,8 +371,10 @@ def core_lines(wl, dev, timed, flush, peaks, steps: int = 10):
     tokens and heads: tokens/s and HBM rate on their algorithmic bytes per
     token-head (core forward 8 d_h + 4: q, k, v, g in, o out; backward
     14 d_h + 8: q, k, v, g, do in, dq, dk, dv, dg out; decay forward
-    8 d_h + 8: q, k, v, g, lambda in, o out); and the SA blocks' softmax
-    attention (sa_core_forward) with its tensor rate."""
+    8 d_h + 8: q, k, v, g, lambda in, o out); the SA blocks' softmax
+    attention (sa_core_forward) with its tensor rate; and the gated linear
+    recurrence on the same tokens and channels (per value: forward 8 bytes, x,
+    r, i in, y out; backward 14, x, r, i, dy in, dx, dr, di out)."""
     import torch
     from generative_retrieval_encoder_gb300 import gbla
     B, L, H, dh = wl.B, wl.L, wl.H, wl.dh
@@ -409,7 +413,23 @@ def core_lines(wl, dev, timed, flush, peaks, steps: int = 10):
     out["sa_forward"] = {"ms": round(ms, 4), "tokens_per_s": T / (ms * 1e-3), "tflops": round(fl / (ms * 1e-3) / 1e12, 1),
                          "frac": round(fl / (ms * 1e-3) / 1e12 / peaks["bf16_tflops_sustained"], 3),
                          "peak": "measured (cuBLAS bf16, sustained)"}
-    del q, k, v, d_o, g, lam, o, ws_f, ws_b, ws_d, ws_s
+    d = H * dh
+    rec = gbla.glr_shape(B, L, d)
+    decay = torch.log(torch.expm1(-torch.log(0.9 + 0.099 * torch.rand(d, generator=r)) / 8)).to(dev)
+    ws_f, ws_b = gbla.workspace(rec, gbla.GBLA_OP_GLR_FORWARD, dev), gbla.workspace(rec, gbla.GBLA_OP_GLR_BACKWARD, dev)
+    saved = torch.empty(gbla.glr_saved_size(rec), dtype=torch.uint8, device=dev)
+    dout = {n: torch.empty_like(q) for n in ("dx", "dr", "di")}
+    dout["dlam"] = torch.empty(d, dtype=torch.float32, device=dev)
+    gbla.glr_forward(rec, v, q, k, decay, y=o, saved=saved, ws=ws_f)
+    for name, fn, per in (("recurrence_forward", lambda: gbla.glr_forward(rec, v, q, k, decay, y=o, ws=ws_f), 8),
+                          ("recurrence_backward", lambda: gbla.glr_backward(rec, v, q, k, decay, saved, d_o, ws=ws_b, out=dout), 14)):
+        for _ in range(3):
+            fn()
+        ms = timed(fn, steps)
+        out[name] = {"ms": round(ms, 4), "tokens_per_s": T / (ms * 1e-3), "algorithmic_bytes": T * d * per,
+                     "achieved_GBps": round(T * d * per / (ms * 1e-3) / 1e9, 1),
+                     "frac": round(T * d * per / (ms * 1e-3) / 1e9 / peaks["hbm_gbs"], 3)}
+    del q, k, v, d_o, g, lam, o, ws_f, ws_b, ws_d, ws_s, saved, dout
     torch.cuda.empty_cache()
     return out
 
@@ -456,13 +476,21 @@ def run_ours(args, wl, rank: int, world: int, local_rank: int):
              "dW_v": torch.empty(d, H * dh, **f32), "dW_r": torch.empty(d, H * dh, **f32),
              "dw_g": torch.empty(d, H, **f32), "db_g": torch.empty(H, **f32), "drms_w": torch.empty(dh, **f32)}
     flush = torch.empty(2 * L2_BYTES // 4, dtype=torch.float32, device=dev)
+    # --update: AdamW on the layer's parameters with the step's gradients, clipped by their global norm
+    plan = gbla.gbla_adamw_plan(P, grads, gbla.gbla_adamw_state(P, bits=args.state_bits)) if args.update else None
+    norm = torch.empty((), **f32)
 
     def fwd():
         gbla.gbla_forward(shape, x, P, y=y, saved=saved, ws=ws_f)
 
+    def update():
+        gbla.gbla_adamw_step(plan, lr=1e-3, norm=gbla.gbla_grad_norm(plan, norm), max_norm=1.0)
+
     def step():
         fwd()
         gbla.gbla_backward(shape, x, P, saved, dy, ws=ws_b, out=grads)
+        if plan is not None:
+            update()
 
     def timed(fn, k):
         total = 0.0
@@ -562,6 +590,9 @@ def run_ours(args, wl, rank: int, world: int, local_rank: int):
             o = outs[c]
             gbla.gbla_forward(shape, xb[c], P, y=o["y"], saved=saved, ws=ws_f)
             gbla.gbla_backward(shape, xb[c], P, saved, dyb[c], ws=ws_b, out=o)
+            if plan is not None:
+                plan.set_grads(o)
+                update()
             freed[c].record(main)
             done[c].record(main)
             d2h_stream.wait_event(done[c])
@@ -624,7 +655,7 @@ def run_ours(args, wl, rank: int, world: int, local_rank: int):
     line = {"metric": METRIC, "value": job_rate(tokens, world, ms_step), "unit": "tokens/s", "n_gpus": world,
             "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms_step, "higher_is_better": True,
             "scaling": "weak", "vs_baseline": None, "dtype": wl.dtype, "data": "synthetic",
-            "config": {"workload": wl.name, "step": "forward+backward", "tokens_per_gpu": tokens,
+            "config": {"workload": wl.name, "step": "forward+backward" + ("+adamw" if args.update else ""), "tokens_per_gpu": tokens,
                        "l2": "flushed between timed steps (write of 2x L2 outside the events)",
                        "parallelism": f"replicas x{world}" if world > 1 else "single GPU"},
             "fwd_tokens_per_s": job_rate(tokens, world, ms_fwd), "ms_fwd": ms_fwd,
@@ -648,6 +679,9 @@ def main():
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--impl", choices=("ours", "reference"), default="ours")
     ap.add_argument("--workload", default="train2k", choices=sorted(workloads()))
+    ap.add_argument("--update", action="store_true",
+                    help="the step also updates the parameters (AdamW, clipped by the gradients' global norm)")
+    ap.add_argument("--state-bits", type=int, choices=(8, 32), default=32, help="AdamW states of --update")
     ap.add_argument("--no-scaling", dest="scaling", action="store_false",
                     help="skip the L = 2k .. 32k linearity sweep")
     args = ap.parse_args()
