@@ -285,6 +285,12 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p, bool is, uint64_t x)
 // answer() waits for those that were not there yet, again together, and composes them.  Words that do not exist are
 // identities.
 template <int W> struct Words { uint64_t w[64 / W]; };
+// Whether chunk k has words of this part at all.
+template <int W>
+__device__ __forceinline__ bool part_is(int k, int part) {
+  constexpr int N = 64 / W, FAR = W / 4;
+  return part >= FAR ? (k & 15) > (part - FAR) * N : k >= 16 && (part == 0 || (k >> 4 & 15) >= part * N);
+}
 template <int W>
 __device__ __forceinline__ uint64_t peek_word(const GlrArgs& a, const Tile& t, int part, int cc, int j, bool want, uint64_t x) {
   constexpr int N = 64 / W, FAR = W / 4;  // words of a part; the parts of groups
@@ -299,6 +305,7 @@ __device__ __forceinline__ uint64_t peek_word(const GlrArgs& a, const Tile& t, i
 }
 template <int W>
 __device__ __forceinline__ void ask(const GlrArgs& a, const Tile& t, int part, int cc, Words<W>& v) {
+  if (!part_is<W>(t.k, part)) return;
 #pragma unroll
   for (int j = 0; j < 64 / W; ++j) v.w[j] = peek_word<W>(a, t, part, cc, j, true, kIdentity);
 }
@@ -349,7 +356,7 @@ template <int W>
 __device__ __forceinline__ void scan_words(const GlrArgs& a, const Tile& t, ScanShared<W>& sc, int vw, int lane, bool need, Words<W>& words, const Map2& total) {
   constexpr int P = W / 2, FAR = W / 4;
   const int part = vw >> 1, cc = (vw & 1) * 32 + lane;
-  if (need && (part >= FAR || t.k >= 16)) {
+  if (need && part_is<W>(t.k, part)) {
     const Map m = answer<W>(a, t, part, cc, words);
     float* p = (float*)&sc.before[part][cc >> 1] + (cc & 1);
     p[0] = m.A;
@@ -361,7 +368,8 @@ __device__ __forceinline__ void scan_words(const GlrArgs& a, const Tile& t, Scan
       Map2 m = total;
       if (need) {
 #pragma unroll
-        for (int q = P - 1; q >= FAR; --q) m = then(map_at(sc.before[q][lane]), m);
+        for (int q = P - 1; q >= FAR; --q)
+          if (part_is<W>(t.k, q)) m = then(map_at(sc.before[q][lane]), m);
       }
       publish(a.words + t.far + (int64_t)((t.k >> 4 & 15) + 1) * a.dp + 2 * lane, m);
     }
@@ -375,7 +383,7 @@ __device__ __forceinline__ float2 scan_state(const GlrArgs& a, const Tile& t, co
   if (need) {
 #pragma unroll
     for (int q = 0; q < W / 2; ++q)
-      if (q >= W / 4 || t.k >= 16) h = after(map_at(sc.before[q][lane]), h);
+      if (part_is<W>(t.k, q)) h = after(map_at(sc.before[q][lane]), h);
   }
   if ((t.k & 255) == 255 && t.k < t.last && vw == W - 1)
     publish(a.words + t.large + a.dp + 2 * lane, Map2{two(0.f), after(total, h)});
