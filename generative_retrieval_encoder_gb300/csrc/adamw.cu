@@ -99,15 +99,17 @@ __device__ __forceinline__ void move(float2 g, float2& m, float2& v, float2& roo
   p = __ffma2_rn(all(-s.step), q, mul2(p, all(keep)));
 }
 
-// Four values at p from element e on: WIDE in one access, else the nv there are.
-template <bool WIDE>
+// Four values at p from element e on: WIDE in one access, else the nv there are.  KEEP: they will be read again.
+template <bool WIDE, bool KEEP = false>
 __device__ __forceinline__ void load4(float (&o)[4], const void* p, int64_t e, bool b16, int nv) {
   if (WIDE) {
     if (b16) {
-      const uint2 w = __ldcs((const uint2*)((const bf16*)p + e));
+      const uint2* at = (const uint2*)((const bf16*)p + e);
+      const uint2 w = KEEP ? __ldg(at) : __ldcs(at);
       o[0] = bf_lo(w.x); o[1] = bf_hi(w.x); o[2] = bf_lo(w.y); o[3] = bf_hi(w.y);
     } else {
-      const float4 w = __ldcs((const float4*)((const float*)p + e));
+      const float4* at = (const float4*)((const float*)p + e);
+      const float4 w = KEEP ? __ldg(at) : __ldcs(at);
       o[0] = w.x; o[1] = w.y; o[2] = w.z; o[3] = w.w;
     }
     return;
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(256) k_sumsq(const __grid_constant__ AdamTable
     for (int h = 0; h < 2; ++h) {
       const int64_t e = (int64_t)(u - t.first) * kAdamUnit + 1024 * h + 4 * threadIdx.x;
       const int nv = (int)max((int64_t)0, min((int64_t)4, t.n - e));
-      if (t.vec && nv == 4) load4<true>(g[h], t.grad, e, t.gb, nv);
+      if (t.vec && nv == 4) load4<true, true>(g[h], t.grad, e, t.gb, nv);
       else load4<false>(g[h], t.grad, e, t.gb, nv);
     }
 #pragma unroll
