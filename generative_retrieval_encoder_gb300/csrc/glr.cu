@@ -5,15 +5,22 @@
 // per sequence and channel in either direction, and its backward
 //   w_t = dy_t + a_{t+1} w_{t+1}          (w = dL/dh, + dhT at the last token)
 //   dx = w m sig(i),  di = w m x sig(i) (1 - sig(i)),
-//   e_t = s_t dL/ds_t = -w (a s h_{t-1} - sig(i) x a^2 (s / m)),
+//   e_t = s_t dL/ds_t = -w a (s h_{t-1} - u s / (2 sinh s)),  u = m sig(i) x,
 //   dr = e (1 - sig(r)),  dlam = sum_t e_t sig(lam) / softplus(lam),  dh0 = a w at the first token.
-// q is formed without cancellation (a polynomial for small s), so m keeps its
-// relative accuracy for decays near 1; s / m tends to 0 with s, so dr and dlam
-// stay finite where a = 1.
+// (dL/ds = -a w (h_{t-1} - (a / m) sig(i) x), and a^2 s / m^2 = a s / (2 sinh s).)  q is formed without cancellation (a
+// polynomial for small s), so m keeps its relative accuracy for decays near 1; s / (2 sinh s) is 1/2 at s = 0, so dr
+// and dlam stay finite where a = 1.  States, decays and sums are fp32; y and the gradients are rounded once.
 //
-// A thread walks one channel of one sequence.  The state on entry to every
-// piece of rows is saved for the backward, which recomputes the states
-// of a chunk from it.
+// What a call cannot do without (bf16): forward 8 bytes a value, backward 14; and four special functions a value and
+// direction, which at 6.8 TB/s take half the special function units' time.  The scan runs along the rows, so the rows are
+// cut: tiles of 128 (forward) or 64 rows x 64 channels, whose effects on a state are composed across tiles while the rows'
+// values stay on the chip (scan_* below): every input is read once.  Measured (perf of the whole call, launches included):
+//   forward  B = 32, L = 2048, d = 512 (268 MB)   65 us, 4.2 TB/s;  B = 8, L = 32768 (1.07 GB)  255 us, 4.2 TB/s
+//            one sequence of 65536 rows (268 MB)  100 us, 2.7 TB/s; packed, d = 1024 (1.35 GB)  344 us, 3.9 TB/s
+//   forward and backward  B = 16, L = 8192 (1.48 GB)  424 us, 3.5 TB/s; packed, d = 1024 (2.67 GB)  735 us, 3.6 TB/s
+// Without the waits between tiles (a copy that left them out) the forward takes 61, 200, 59 and 284 us, and without the
+// gates too 47, 162, 46 and 218: what is left above the copy is first the gates' instructions, then the tiles of one chain
+// that are worked on at the same time and so wait for one another, most where one sequence has few channels.
 #include <algorithm>
 
 #include "common.cuh"
@@ -248,7 +255,7 @@ __device__ __forceinline__ void tile_of(const GlrArgs& a, const GlrTiles& g, uns
 
 // ------------------------------------------------------------ the scan between chunks
 // A tile publishes, per channel, what its rows do to a state that enters: h -> A h + H, as one 64-bit word {H, A}
-// (present when the top bit, A's sign, is set).  A = 0: a sequence starts here, h -> H whatever h was.  Chunks form
+// (present when the top bit, A's sign, is set: one word, so nothing else has to be ordered).  A = 0: a sequence starts here, h -> H whatever h was.  Chunks form
 // groups of 16 and groups of groups; a chunk that needs the state before it composes the words of the chunks before it in
 // its group, of the groups before its own in the larger group, and the state after the last larger group: at most 31
 // words, read together.  The order of composition is fixed, so results do not depend on timing.
@@ -491,8 +498,12 @@ struct GlrShared {
 };
 
 // Forward: one pass, x, r and i read once and y written once.  Bound by the instructions of the gates (four special
-// functions a value), by the waits between tiles and by memory.  Two CTAs an SM keep taking tiles, so that one's wait for
-// the state between tiles is another's arithmetic; a tile's rows are copied to shared memory while an earlier one is worked on.
+// functions and 36 instructions a value in all; 42 % of the issue slots), by the waits between tiles and by memory.  Two CTAs
+// an SM keep taking tiles, so that one's wait for the state between tiles is another's arithmetic; a tile's rows are copied
+// to shared memory while an earlier one is worked on.  A lane holds a and u of its 16 rows between the two halves of a tile: 64
+// registers, hence two CTAs.  Other shapes (B = 8, L = 32768): 64-row tiles 365 us with three CTAs of 8 x 8 rows, 466 with four
+// of 4 x 16 (the composition costs the same for half the rows); one CTA of 16 x 16 rows 250, but 71 against 65 us at L = 2048;
+// forming the decays twice to hold u alone, three CTAs, 324.
 template <typename T, int LOAD>
 __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps maps) {
   constexpr int PER = kPerF, CH = kGlrRowsFwd, ST = stages_fwd<T>();
@@ -538,6 +549,8 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     const int st = it % ST;
     const Tile& me = sh.tile[it & 3];
     if (me.k < 0) break;
+    Words<kWarpsF> words;
+    ask(a, me, warp >> 1, (warp & 1) * 32 + lane, words);
     // the lane's rows
     const int ch = me.ch0 + 2 * lane, nch = a.d - ch;  // channels of this lane: 2 (or more), 1 or none
     const int j0 = warp * PER;
@@ -556,8 +569,6 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     } else {
       local_rows<T, LOAD, false, false, PER, CH>(a, sm, me.c, f, j0, ch, nch, ka, ka, da, u, A, H);
     }
-    Words<kWarpsF> words;
-    ask(a, me, warp >> 1, (warp & 1) * 32 + lane, words);
     sh.sc.agg[warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
     // whether the chunk's first row begins a sequence: then nothing enters
     const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && me.k > 0;
@@ -744,7 +755,9 @@ struct GlrSharedBwd {
 
 // Backward: one pass from each sequence's end, x, r, i and dy read once, dx, dr and di written once; the states before a
 // warp's rows come from the saved one, the w behind them as the forward's states do.  As the forward, with half the rows in a
-// tile and three CTAs an SM.  Every tile has two barriers between the first and the second pass, so what one tile leaves in
+// tile and three CTAs an SM (80 registers; holding everything from the first pass took 128, two CTAs and spills: 541 against 426
+// us for both directions at B = 16, L = 8192).  Bound by instructions (81 a value, 50 % of the issue slots) and the waits
+// between tiles.  Every tile has two barriers between the first and the second pass, so what one tile leaves in
 // shared memory for them is read before the next one's is written.
 template <typename T, int LOAD>
 __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArgs a, const GlrTiles tl, const __grid_constant__ GlrMaps4 maps) {
@@ -802,6 +815,8 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     const Tile& t = sh.tile[it & 3];
     if (t.k < 0) break;
     const int ch = t.ch0 + 2 * lane, nch = a.d - ch;
+    Words<kWarpsB> words;
+    ask(a, t, vw >> 1, (vw & 1) * 32 + lane, words);
     const int64_t row = t.row;
     const int j0 = warp * PER;
     static_assert(PER == kGlrPiece, "a warp's rows are a piece");
@@ -818,8 +833,6 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     RowPair<T> dy[PER];
     if (plain) decays_bwd<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, da, dy, A, D);
     else decays_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, da, dy, A, D);
-    Words<kWarpsB> words;
-    ask(a, t, vw >> 1, (vw & 1) * 32 + lane, words);
     sh.sc.agg[vw][lane] = packed(Map2{A, D});
     // whether a sequence ends with the chunk's last row: then nothing comes from behind
     const bool need = !__syncthreads_or(warp == kWarpsB - 1 && (f.E >> (PER - 1) & 1)) && t.k > 0;
@@ -928,7 +941,9 @@ __global__ void __launch_bounds__(1024) k_glr_levels(int* level, int n, int* tot
   if (threadIdx.x == 0) *total = *err ? 0 : carry;
 }
 
-// The chunks in the order of their levels (within one in any order: results do not depend on it).
+// The chunks in the order of their levels (within one in any order: results do not depend on it).  In this order the next chunk
+// of a sequence comes many tiles later, when its predecessor's words are long there: packed sequences of d = 1024 take
+// 361 us forward against 625 in one stream, where all tiles at work are neighbours, and 899 against 1825 trained.
 __global__ void __launch_bounds__(256) k_glr_place(const GlrArgs a, const GlrTiles tl, int* level) {
   pdl_enter();
   if (*a.err) return;
@@ -941,7 +956,8 @@ __global__ void __launch_bounds__(256) k_glr_place(const GlrArgs a, const GlrTil
 }
 
 // A few tokens of many sequences (one of each: serving): a thread for two channels of a sequence, no scan and no other launch.
-// Bound by the latency of one load and the launch.
+// Bound by the latency of a load a row where there are few threads (B = 16, L = 1, d = 512: 1.8 us on the device, against 16 of
+// the tiles with their preparation), by memory where there are many (B = 4096, L = 64: 4.7 TB/s).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(128) k_glr_step(const GlrArgs a, int* err) {
   pdl_enter();

@@ -44,7 +44,9 @@
  *   that only the device can see (cu_seqlens not starting at 0, decreasing,
  *   or not ending at T; seq_lens outside [0, L]) sets an error word in the
  *   workspace, every kernel then skips its work, and gbla_check_device_status()
- *   reports GBLA_ERR_DEVICE_CHECK.  No kernel traps or waits on another CTA.
+ *   reports GBLA_ERR_DEVICE_CHECK.  No kernel traps, and none waits on another
+ *   CTA but those of glr_forward and glr_backward, whose tiles wait for the
+ *   states of tiles handed out before them (a bounded wait, as below).
  *   The tensor-core kernels wait on their own copies and MMAs through
  *   mbarriers; every such wait is bounded, and one that gives up (a device
  *   that stopped making progress) sets a timeout bit in the error word instead

@@ -293,6 +293,34 @@ def test_norm_of_many_small_squares_and_wide_ranges():
         assert abs(float(n) - w) <= 1.01 * E * w
 
 
+def test_a_tensor_beyond_32_bits():
+    """2^31 + 1000 values with 8-bit states, bf16 values and gradients: its last blocks bit for bit, the norm of all."""
+    n, tail = 2 ** 31 + 1000, 1000
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    g[n - tail:] = torch.linspace(-1, 1, tail, device="cuda").bfloat16()
+    w = np.sqrt(2.0 ** 31 * 0.25 + (f64(g[n - tail:]) ** 2).sum())
+    st = gbla.gbla_adamw_state([p], bits=8, master=False)
+    plan = gbla.gbla_adamw_plan([p], [g], st)
+    assert abs(float(gbla.gbla_grad_norm(plan)) - w) <= 1.01 * E * w
+    gbla.gbla_adamw_step(plan, LR, seed=9)
+    at = (n - tail) // 256 * 256  # 2^31: a block's first value
+    gt = g[at:].float().cpu().numpy()
+    c = [np.float32(v) for v in (1 - BETAS[0], 1 - BETAS[1])]
+    m, root = c[0] * gt, np.sqrt((c[1] * gt) * gt)
+    with np.errstate(over="ignore"):
+        key = mix(mix(np.array([1 ^ 0x9E3779B9])) + np.uint32(9))
+        z = mix((np.uint32(at) + np.arange(gt.size, dtype=np.uint32)) * np.uint32(0x9E3779B9) + key)
+    for name, v, dither in (("m", m, z & np.uint32(0xFFFF)), ("v", root, z >> np.uint32(16))):
+        code, scale = encode(v.astype(np.float32), dither, name == "v")
+        assert np.array_equal(st[name][0][at:].view(torch.uint8).cpu().numpy(), code), name
+        assert np.array_equal(st[name + "_scale"][0][at // 256:].cpu().numpy(), scale), name
+    # the first step moves every value by lr against its gradient's sign
+    assert (p[:2 ** 31:1 << 20].float() + LR).abs().max() <= LR * (2.0 ** -8 + 1e-5)
+    del p, g, st, plan
+    torch.cuda.empty_cache()
+
+
 def test_writes_nothing_around_its_tensors():
     for bits in (8, 32):
         bufs = {k: torch.full((4, 600), 1, dtype=torch.uint8, device="cuda") for k in ("m", "v")} if bits == 8 else \

@@ -238,6 +238,31 @@ def test_glr_is_deterministic_on_streams_and_in_graphs():
         assert torch.equal(a[0], yb) and torch.equal(a[1], hb) and all(torch.equal(b[n], gb[n]) for n in b)
 
 
+@pytest.mark.parametrize("form", ["dense", "varlen", "steps"])
+def test_glr_offsets_beyond_32_bits(form):
+    """2.2e9 values (offsets in elements and bytes pass 2^31 and 2^32): the last sequence against the formulas, one tensor
+    serving as x, r and i."""
+    d, L = 2048, 1024 if form != "steps" else 4
+    B = (2 ** 31 + 2 ** 27) // (d * L)
+    T = B * L
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator("cuda").manual_seed(70))
+    lam = torch.log(torch.expm1(-torch.log(torch.linspace(0.9, 0.999, d)) / 8)).cuda()
+    cu = torch.arange(0, T + 1, L, dtype=torch.int32, device="cuda")
+    sh = gbla.glr_shape(1, T, d, cu_seqlens=cu) if form == "varlen" else gbla.glr_shape(B, L, d)
+    y, hT, saved = gbla.glr_forward(sh, x, x, x, lam, hT=True, saved=True if form != "steps" else None)
+    v = x[T - L:].double().cpu().numpy()
+    want = reference(v, v, v, lam.double().cpu().numpy(), 8.0, [0], [L], dy=v)
+    check({"y": y[T - L:], "hT": hT[B - 1:]}, want)
+    del y
+    if form == "steps":
+        return
+    g = gbla.glr_backward(sh, x, x, x, lam, saved, x)
+    check({n: g[n][T - L:] for n in ("dx", "dr", "di")}, want)
+    del g, saved, x
+    torch.cuda.empty_cache()
+
+
 def test_glr_bad_sequence_data_is_reported():
     """cu_seqlens that decrease or end elsewhere, seq_lens over L: nothing is written, the status says so."""
     d, T = 16, 100
