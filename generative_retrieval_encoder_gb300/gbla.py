@@ -297,7 +297,9 @@ def glr_shape(B: int, L: int, d: int, dtype: str = "bf16", cu_seqlens: torch.Ten
                               or (t.numel() < n if name == "cu_seqlens" else t.numel() != n)):
             raise ValueError(f"{name}: want a contiguous int32 CUDA tensor of {n} values{' at least' if n == 2 else ''}, "
                              f"got {t.dtype} {list(t.shape)} on {t.device}")
-    return make_shape(B, L, d, 1, 1, dtype=dtype, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
+    s = make_shape(B, L, d, 1, 1, dtype=dtype, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
+    s._sizes = rows(s), n_seq(s), d, io_dtype(s)
+    return s
 
 
 def glr_saved_size(shape: Shape) -> int:
@@ -326,21 +328,32 @@ def _glr_bytes(name, t, n, device):
     return t.data_ptr()
 
 
+def _glr_sizes(shape):
+    """(rows, sequences, d, io dtype), once for a shape of glr_shape."""
+    s = getattr(shape, "_sizes", None)
+    return s if s is not None else (rows(shape), n_seq(shape), shape.d, io_dtype(shape))
+
+
 def _glr_inputs(shape, x, r, i, lam, h0):
-    dev, d, io, T = x.device, shape.d, io_dtype(shape), rows(shape)
+    T, N, d, io = _glr_sizes(shape)
+    dev = x.device
     if not x.is_cuda:
         raise ValueError(f"x: want a CUDA tensor, got {x.device}")
     ld = x.stride(0) if T > 1 and x.dim() == 2 else d
-    return (ld, *[_glr_arg(n, t, T, d, io, dev, ld) for n, t in (("x", x), ("r", r), ("i", i))], _glr_vec("lam", lam, d, dev),
-            None if h0 is None else _glr_arg("h0", h0, n_seq(shape), d, torch.float32, dev, d))
+    return (dev, T, N, d, ld, _glr_arg("x", x, T, d, io, dev, ld), _glr_arg("r", r, T, d, io, dev, ld), _glr_arg("i", i, T, d, io, dev, ld),
+            _glr_vec("lam", lam, d, dev), None if h0 is None else _glr_arg("h0", h0, N, d, torch.float32, dev, d))
+
+
+# The current stream's handle of a device (by index): torch's own short way where it has one, 2 us less a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _call(device, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
     if device.index == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream().cuda_stream)
+        return fn(*args, _raw_stream(device.index))
     with torch.cuda.device(device):
-        return fn(*args, torch.cuda.current_stream().cuda_stream)
+        return fn(*args, _raw_stream(device.index))
 
 
 def glr_forward(shape: Shape, x, r, i, lam, c: float = 8.0, reverse: bool = False, h0=None, y=None, hT=None,
@@ -348,14 +361,13 @@ def glr_forward(shape: Shape, x, r, i, lam, c: float = 8.0, reverse: bool = Fals
     """The gated linear recurrence (see gbla.h): returns (y, hT, saved).  x, r and i share their row stride (they may
     be columns of one tensor).  hT: a tensor to fill (h0 itself to update it in place), or True to allocate it; saved =
     True allocates what glr_backward needs.  Tensors are on x's device, the call on that device's current stream."""
-    ld, px, pr, pi, pl, ph = _glr_inputs(shape, x, r, i, lam, h0)
-    dev, T, d = x.device, rows(shape), shape.d
+    dev, T, N, d, ld, px, pr, pi, pl, ph = _glr_inputs(shape, x, r, i, lam, h0)
     if y is None:
         y = torch.empty((T, d), dtype=x.dtype, device=dev)
     py = _glr_arg("y", y, T, d, x.dtype, dev, d)
     if hT is True:
-        hT = torch.empty((n_seq(shape), d), dtype=torch.float32, device=dev)
-    pT = None if hT is None else ph if hT is h0 else _glr_arg("hT", hT, n_seq(shape), d, torch.float32, dev, d)
+        hT = torch.empty((N, d), dtype=torch.float32, device=dev)
+    pT = None if hT is None else ph if hT is h0 else _glr_arg("hT", hT, N, d, torch.float32, dev, d)
     if saved is True:
         saved = torch.empty(glr_saved_size(shape), dtype=torch.uint8, device=dev)
     saved = saved if isinstance(saved, torch.Tensor) else None
@@ -373,8 +385,8 @@ def glr_backward(shape: Shape, x, r, i, lam, saved, dy, c: float = 8.0, reverse:
                  ws=None, out: dict | None = None) -> dict:
     """Backward of glr_forward for <dy, y> + <dhT, hT>.  Returns dx, dr, di (io dtype), dlam fp32 and, where h0 or dhT
     is given, dh0 fp32.  out: tensors to fill (dx, dr and di of one row stride)."""
-    ld, px, pr, pi, pl, ph = _glr_inputs(shape, x, r, i, lam, h0)
-    dev, T, d, N, f32 = x.device, rows(shape), shape.d, n_seq(shape), torch.float32
+    dev, T, N, d, ld, px, pr, pi, pl, ph = _glr_inputs(shape, x, r, i, lam, h0)
+    f32 = torch.float32
     g = out
     if g is None:
         g = {n: torch.empty((T, d), dtype=x.dtype, device=dev) for n in ("dx", "dr", "di")}
