@@ -297,9 +297,7 @@ def glr_shape(B: int, L: int, d: int, dtype: str = "bf16", cu_seqlens: torch.Ten
                               or (t.numel() < n if name == "cu_seqlens" else t.numel() != n)):
             raise ValueError(f"{name}: want a contiguous int32 CUDA tensor of {n} values{' at least' if n == 2 else ''}, "
                              f"got {t.dtype} {list(t.shape)} on {t.device}")
-    s = make_shape(B, L, d, 1, 1, dtype=dtype, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
-    s._sizes = rows(s), n_seq(s), d, io_dtype(s)
-    return s
+    return make_shape(B, L, d, 1, 1, dtype=dtype, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
 
 
 def glr_saved_size(shape: Shape) -> int:
@@ -328,14 +326,8 @@ def _glr_bytes(name, t, n, device):
     return t.data_ptr()
 
 
-def _glr_sizes(shape):
-    """(rows, sequences, d, io dtype), once for a shape of glr_shape."""
-    s = getattr(shape, "_sizes", None)
-    return s if s is not None else (rows(shape), n_seq(shape), shape.d, io_dtype(shape))
-
-
 def _glr_inputs(shape, x, r, i, lam, h0):
-    T, N, d, io = _glr_sizes(shape)
+    T, N, d, io = rows(shape), n_seq(shape), shape.d, io_dtype(shape)
     dev = x.device
     if not x.is_cuda:
         raise ValueError(f"x: want a CUDA tensor, got {x.device}")

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from generative_retrieval_encoder_gb300 import build, gbla
 
@@ -68,3 +69,30 @@ def test_binding_refuses_host_tensors(L):
         gbla.glr_forward(gbla.glr_shape(2, 100, 48, dtype="f32"), t, t, t, torch.zeros(48))
     with pytest.raises(ValueError):
         gbla.glr_shape(1, 100, 48, cu_seqlens=torch.zeros(2, dtype=torch.int32))
+
+
+def test_checks_follow_a_changed_shape(L):
+    """A shape's fields are plain values: after a change the binding's checks are those of the new sizes."""
+    sh = gbla.glr_shape(2, 16, 8)
+    seen = []
+
+    class Fake:  # what the binding asks of a tensor
+        is_cuda, dtype, device = True, torch.bfloat16, torch.device("cuda", 0)
+
+        def __init__(self, *shape):
+            self.shape = shape
+
+        def dim(self):
+            return 2
+
+        def stride(self, k=None):
+            return (8, 1) if k is None else (8, 1)[k]
+
+        def data_ptr(self):
+            seen.append(self.shape)
+            return 256
+
+    sh.L = 32
+    with pytest.raises(ValueError, match="64, 8"):
+        gbla._glr_inputs(sh, Fake(32, 8), Fake(32, 8), Fake(32, 8), None, None)
+    assert not seen
