@@ -284,8 +284,9 @@ __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdamTa
   }
 }
 
-// Bound by memory (0.8 GB in 130 us).  Sums of squares, a CTA's in one partial: a thread adds g g exactly rounded into two fp32 words (the product's own
-// error and that of each addition go to the lower word), the CTA adds those in fp64 in a fixed order.
+// Sums of squares, a CTA's in one partial: a thread adds g g into two fp32 words (the product's own error and that of each
+// addition go to the lower word), the CTA adds those in fp64 in a fixed order.  Bound by memory: 0.8 GB of fp32 gradients in two
+// tables in 106 + 37 us, 5.7 TB/s.
 template <int N>
 __global__ void __launch_bounds__(256) k_sumsq(const __grid_constant__ AdamTable<N> tab, double* part) {
   pdl_enter();

@@ -372,8 +372,8 @@ gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
   p.mode = s->cu_seqlens ? SEQ_VARLEN : (s->seq_lens ? SEQ_PADDED : SEQ_DENSE);
   p.n_seq = s->cu_seqlens ? s->num_seqs : s->B;
   if ((long long)p.n_seq * p.d > (1LL << 38) || p.n_seq > (1 << 30)) return GBLA_ERR_UNSUPPORTED;
-  // Packed sequences are cut one by one where they are long on the mean and the call is several rounds of tiles (the
-  // order's two kernels take 8 us; a 64 k-row, d = 1024 batch of long ones: 1.8 times as fast as in one stream).
+  // Packed sequences are cut one by one where they are long on the mean and the call is several rounds of tiles (64 of
+  // 64 .. 16384 rows, d = 1024: 361 us against 625 in one stream).
   const long long rounds = T / kGlrRowsFwd * cdiv(p.d, 64) / (2LL * sm_count());
   p.cut = p.mode != SEQ_VARLEN ? (p.L >= kGlrSlot ? GLR_SLOTS : GLR_STREAM)
           : T / p.n_seq >= kGlrSlot && rounds >= 3 && p.n_seq > 1 && T <= (8LL << 20) ? GLR_SEQS : GLR_STREAM;
@@ -405,7 +405,6 @@ GlrTiles glr_tiles(const GlrPlan& p, int rows) {
   t.levels = p.cut == GLR_SEQS ? cdiv(p.T, rows) : 0;
   return t;
 }
-constexpr int kDlamRows = 16;  // partial sums of dlam between its two kernels
 struct GlrLayout { size_t err, ticket, count, level, marks, zero_bytes, kd, order, words, n_words, part, n_part, part2, total; };
 GlrLayout glr_layout(const GlrPlan& p, int op) {
   Cursor c;
@@ -1144,16 +1143,7 @@ gbla_status glr_backward(const gbla_shape* shape, const void* x, const void* r, 
   if ((s = glr_prepare(c)) != GBLA_OK) return s;
   const GlrTiles& t = c.t;
   GBLA_CHECK(launch_glr_bwd(a, t, c.p.f32, c.st), "glr bwd");
-  if (dlam) {
-    const int rows = std::min(kDlamRows, t.n_chunks);
-    float* sums = at<float>(ws, c.l.part2);
-    GBLA_CHECK(launch_glr_dlam(a, t.n_chunks, rows, rows > 1 ? sums : dlam, c.st), "glr dlam");
-    if (rows > 1) {
-      ColsumJobs js{};
-      js.j[js.n++] = ColsumJob{sums, rows, c.p.d, c.p.d, dlam, nullptr, 0};
-      GBLA_CHECK(launch_colsums(js, c.st), "glr dlam");
-    }
-  }
+  if (dlam) GBLA_CHECK(launch_glr_dlam(a, t.n_chunks, at<float>(ws, c.l.part2), dlam, c.st), "glr dlam");
   if (dh0 && c.p.mode != SEQ_DENSE) GBLA_CHECK(launch_glr_empty(a, dhT, dh0, c.st), "glr empty");
   return GBLA_OK;
 }

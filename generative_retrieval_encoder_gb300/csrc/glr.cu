@@ -857,9 +857,10 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
   if (it > 0) put_sum(last_row, last_ch0);
 }
 
-// dlam's partial rows n0 = blockIdx.y, n0 + gridDim.y, .. of 64 channels, summed in order, times the derivative of softplus over it.
-__global__ void __launch_bounds__(256) k_glr_dlam(const float* part, int64_t n, int d, const float* lam, float* out) {
+// Rows n0 = blockIdx.y, n0 + gridDim.y, .. of [n][d] for 64 channels, summed in order; lam: times the derivative of softplus over it.
+__global__ void __launch_bounds__(256) k_glr_dlam(const float* part, int64_t n, int d, const float* lam, const int* err, float* out) {
   pdl_enter();
+  if (err && *err) return;
   __shared__ float red[4][64];
   const int ch = blockIdx.x * 64 + (threadIdx.x & 63), p = threadIdx.x >> 6;
   float v = 0.f;
@@ -870,8 +871,10 @@ __global__ void __launch_bounds__(256) k_glr_dlam(const float* part, int64_t n, 
   }
   red[p][threadIdx.x & 63] = v;
   __syncthreads();
-  if (p == 0 && ch < d)
-    out[(int64_t)blockIdx.y * d + ch] = (((red[0][threadIdx.x] + red[1][threadIdx.x]) + red[2][threadIdx.x]) + red[3][threadIdx.x]) * dsoftplus_ratio(lam[ch]);
+  if (p == 0 && ch < d) {
+    const float s = ((red[0][threadIdx.x] + red[1][threadIdx.x]) + red[2][threadIdx.x]) + red[3][threadIdx.x];
+    out[(int64_t)blockIdx.y * d + ch] = lam ? s * dsoftplus_ratio(lam[ch]) : s;
+  }
 }
 
 // c softplus(lam), the scan's words and the tile counter cleared; checks the sequence data; marks the rows that begin a packed
@@ -1084,8 +1087,16 @@ cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaSt
   return f32 ? run_glr_bwd<float>(a, t, st) : run_glr_bwd<bf16>(a, t, st);
 }
 
-cudaError_t launch_glr_dlam(const GlrArgs& a, int64_t n, int rows, float* out, cudaStream_t st) {
-  return launch_pdl(k_glr_dlam, dim3((unsigned)(a.dp >> 6), (unsigned)rows), dim3(256), 0, st, (const float*)a.dlam_part, n, a.d, a.lam, out);
+cudaError_t launch_glr_dlam(const GlrArgs& a, int64_t n, float* sums, float* out, cudaStream_t st) {
+  const dim3 cols((unsigned)(a.dp >> 6));
+  const float* part = a.dlam_part;
+  if (n > kDlamRows) {
+    const cudaError_t e = launch_pdl(k_glr_dlam, dim3(cols.x, kDlamRows), dim3(256), 0, st, part, n, a.d, (const float*)nullptr, (const int*)a.err, sums);
+    if (e != cudaSuccess) return e;
+    part = sums;
+    n = kDlamRows;
+  }
+  return launch_pdl(k_glr_dlam, cols, dim3(256), 0, st, part, n, a.d, a.lam, (const int*)a.err, out);
 }
 
 }  // namespace gbla

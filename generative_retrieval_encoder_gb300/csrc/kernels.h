@@ -319,8 +319,9 @@ cudaError_t launch_glr_step(const GlrArgs& a, bool f32, int* err, cudaStream_t s
 cudaError_t launch_glr_empty(const GlrArgs& a, const float* from, float* to, cudaStream_t st);
 cudaError_t launch_glr_fwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st);
 cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrTiles& t, bool f32, cudaStream_t st);
-// The n partial rows of a.dlam_part in `rows` sums [rows][d] (to be summed), times sigmoid(lam) / softplus(lam).
-cudaError_t launch_glr_dlam(const GlrArgs& a, int64_t n, int rows, float* out, cudaStream_t st);
+// The sum of the n partial rows of a.dlam_part times sigmoid(lam) / softplus(lam); many of them by way of sums [kDlamRows][d].
+constexpr int kDlamRows = 16;
+cudaError_t launch_glr_dlam(const GlrArgs& a, int64_t n, float* sums, float* out, cudaStream_t st);
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, bool f32, cudaStream_t st, int* tiled = nullptr);
 // Writes the parameter-gradient partials to part[0 .. *nparts)[d][5].

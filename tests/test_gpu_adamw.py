@@ -447,3 +447,43 @@ def test_training_step_of_layer_and_recurrence(bits):
             got = f64(st["master"][j] if st["master"][j] is not None else p).ravel()
             assert (np.abs(got - want[j][0][0]) <= want[j][1][0] + E * np.abs(want[j][0][0])).all(), (t, k)
     assert int(st["step"]) == 3
+
+
+def test_states_and_types_mixed_in_one_plan():
+    """Every tensor its own types, states and alignment: each the bits it gets in a plan of its kind, at the same place."""
+    kinds = [("f32", "f32", 32, 0), ("bf16", "bf16", 8, 0), ("f32", "bf16", 8, 1), ("bf16", "f32", 32, 3)]
+    sizes = [300, 2500, 256, 1]
+    alone = [make(sizes, p, g, bits=b, offset=o, seed=90 + k) for k, (p, g, b, o) in enumerate(kinds)]
+    mixed = [make(sizes, p, g, bits=b, offset=o, seed=90 + k) for k, (p, g, b, o) in enumerate(kinds)]
+    state = {"step": torch.full((1,), 20, dtype=torch.int64, device="cuda")}
+    for name in ("m", "v", "m_scale", "v_scale", "master"):
+        state[name] = [(mixed[j % 4][2].get(name) or [None] * 4)[j] for j in range(4)]
+    plan = gbla.gbla_adamw_plan([mixed[j][0][j] for j in range(4)], [mixed[j][1][j] for j in range(4)], state)
+    gbla.gbla_adamw_step(plan, LR, BETAS, EPS, WD, seed=3)
+    places = np.concatenate([[0], np.cumsum([-(-n // 256) * 256 for n in sizes])])
+    for j, (P, G, st) in enumerate(alone):
+        st["step"].fill_(20)
+        # tensors of other kinds before it take its blocks' places
+        lead = torch.zeros(int(places[j]), device="cuda")
+        one = {"step": st["step"]}
+        pad = gbla.gbla_adamw_state([lead], bits=32)
+        for name in ("m", "v", "m_scale", "v_scale", "master"):
+            one[name] = [(pad.get(name) or [None])[0], (st.get(name) or [None] * 4)[j]]
+        gbla.gbla_adamw_step(gbla.gbla_adamw_plan([lead, P[j]], [torch.zeros_like(lead), G[j]], one), LR, BETAS, EPS, WD, seed=3)
+        assert torch.equal(plan._keep[0][j], P[j]), j
+        for name in ("m", "v", "m_scale", "v_scale", "master"):
+            a, b = state[name][j], one[name][1]
+            assert (a is None) == (b is None) and (a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))), (j, name)
+    assert int(state["step"]) == 21
+
+
+def test_norm_reads_the_gradients_alone():
+    g = torch.randn(5000, device="cuda")
+    t = (gbla.AdamWTensor * 2)()
+    for k, (at, n) in enumerate(((g, 3001), (g[3001:], 1999))):
+        t[k].grad, t[k].n, t[k].grad_dtype = at.data_ptr(), n, gbla.GBLA_F32
+    ws = torch.empty(gbla.lib().gbla_adamw_workspace_size(t, 2), dtype=torch.uint8, device="cuda")
+    norm = torch.zeros(1, device="cuda")
+    assert gbla.lib().gbla_grad_norm(t, 2, norm.data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+    want = float(g.double().norm())
+    assert abs(float(norm) - want) <= 2 * E * want  # the sum is good to 2^-40; one rounding of the root

@@ -324,3 +324,59 @@ def test_glr_good_call_reports_ok_and_checks_its_arguments():
     with pytest.raises(ValueError):
         gbla.glr_shape(2, 100, 16, dtype="f32", seq_lens=torch.ones(3, dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("form", ["padded", "stream", "seqs"])
+def test_glr_bad_sequence_data_leaves_every_output(form):
+    """The outputs that are sums or states too (dlam, hT, dh0) keep what they held."""
+    d, T = (1024, 8192) if form == "seqs" else (16, 2400)
+    bad = torch.tensor([T // 2 + 1, 3] if form == "padded" else [0, T // 2, T - 1], dtype=torch.int32, device="cuda")
+    sh = gbla.glr_shape(2, T // 2, d, seq_lens=bad) if form == "padded" else gbla.glr_shape(1, T, d, cu_seqlens=bad)
+    x = torch.randn(T, d, device="cuda").bfloat16()
+    lam, h0, kept = torch.zeros(d, device="cuda"), torch.ones(2, d, device="cuda"), torch.full((2, d), 3.0, device="cuda")
+    ws, y, saved = gbla.workspace(sh, gbla.GBLA_OP_GLR_FORWARD), torch.full_like(x, 3.0), torch.full((gbla.glr_saved_size(sh),), 3, dtype=torch.uint8, device="cuda")
+    gbla.glr_forward(sh, x, x, x, lam, h0=h0, y=y, hT=kept, saved=saved, ws=ws)
+    assert gbla.gbla_check_device_status(ws) == gbla.GBLA_ERR_DEVICE_CHECK
+    assert (kept == 3).all() and (y == 3).all() and (saved == 3).all()
+    ws = gbla.workspace(sh, gbla.GBLA_OP_GLR_BACKWARD)
+    out = {n: torch.full((T, d), 3.0, device="cuda", dtype=torch.bfloat16) for n in ("dx", "dr", "di")}
+    out["dlam"], out["dh0"] = torch.full((d,), 3.0, device="cuda"), kept
+    gbla.glr_backward(sh, x, x, x, lam, saved, x, h0=h0, dhT=h0, out=out, ws=ws)
+    assert gbla.gbla_check_device_status(ws) == gbla.GBLA_ERR_DEVICE_CHECK
+    for n, t in out.items():
+        assert (t == 3).all(), n
+
+
+@pytest.mark.parametrize("form", ["padded", "stream", "seqs"])
+def test_glr_captured_call_follows_its_sequence_data(form):
+    """Lengths are read on the device: a replay with others in the same tensor gives what a call with those gives."""
+    d, T = (1024, 8192) if form == "seqs" else (48, 2400)
+    n = 3
+    sets = [[800, 0, 17], [1, 799, 800], [0, 0, 64]] if form == "padded" else \
+        [[0, T // 3, T // 2, T], [0, 0, 1, T], [0, T, T, T], [0, 100, 164, T]]
+    at = torch.tensor(sets[0], dtype=torch.int32, device="cuda")
+    sh = gbla.glr_shape(n, T // n, d, seq_lens=at) if form == "padded" else gbla.glr_shape(1, T, d, cu_seqlens=at)
+    gen = torch.Generator("cuda").manual_seed(71)
+    x, r, i, dy = (torch.randn(T, d, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    lam = torch.full((d,), -4.0, device="cuda")
+    h0, dhT = (torch.randn(n, d, generator=gen, device="cuda") for _ in range(2))
+
+    def run():
+        y, hT, saved = gbla.glr_forward(sh, x, r, i, lam, h0=h0, hT=True, saved=True)
+        return {"y": y, "hT": hT, **gbla.glr_backward(sh, x, r, i, lam, saved, dy, h0=h0, dhT=dhT)}
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for s in sets + sets[:1]:
+        at.copy_(torch.tensor(s, dtype=torch.int32))
+        graph.replay()
+        want = run()
+        torch.cuda.synchronize()
+        for k, t in want.items():
+            assert torch.equal(got[k], t), (s, k)
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    starts, lens = ([0, 800, 1600], sets[0]) if form == "padded" else (sets[0][:-1], [b - a for a, b in zip(sets[0], sets[0][1:])])
+    cols = slice(0, 48)  # (columns are independent)
+    check({k: t[..., cols] for k, t in got.items()},
+          reference(f(x)[:, cols], f(r)[:, cols], f(i)[:, cols], f(lam)[cols], 8.0, starts, lens, False, f(h0)[:, cols], f(dy)[:, cols], f(dhT)[:, cols]))
