@@ -31,13 +31,19 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 // The 32 random bits of a place are mix32(low word of the place * 0x9E3779B9 (the fraction bits of the golden ratio spread
 // neighbours) + high word * 0xBB67AE85 + the step's key).
 
-// t in [0, 448] (or two units in the last place above: the sum below does not reach the next code) to an e4m3 magnitude, 16
-// random bits d: at the normal values (t >= 2^-6) the fraction's lower 20 bits, below them the fixed step 2^-9,
-// floor(512 t + d 2^-16) (both products exact; floor by an addition rounded down at 2^23).
-__device__ __forceinline__ uint32_t e4m3_up(float t, uint16_t d) {
-  const uint32_t n = ((__float_as_uint(t) + ((uint32_t)d << 4)) >> 20) - (120u << 3);
-  const uint32_t s = __float_as_uint(__fadd_rd(__fmaf_rn((float)d, 0x1p-16f, t * 512.f), 8388608.f)) & 15u;
-  return t >= 0x1p-6f ? n : s;
+// t 2^-120 with |t| in [0, 448] (or two units in the last place above: the sum below does not reach the next code) and 16 random
+// bits, at bits 8 .. 23 of d, to an e4m3 magnitude in the top byte.  At 2^-120 the values of e4m3 are the fp32 ones of 3 fraction
+// bits, those below 2^-6 among the subnormal ones (a fixed step of 2^-9 for both), so the bits below are added to and cut off
+// alike (there are 20 of them: a subnormal t 2^-120 is rounded 2^-21 of a step at most from its value).
+__device__ __forceinline__ uint32_t e4m3_up(float t, uint32_t d) { return (__float_as_uint(t) << 4) + d; }
+// The top bytes of four words.
+__device__ __forceinline__ uint32_t top4(const uint32_t (&w)[4]) {
+  return __byte_perm(__byte_perm(w[0], w[1], 0x0073), __byte_perm(w[2], w[3], 0x0073), 0x5410);
+}
+__device__ __forceinline__ float rcpf(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // The larger of c and |a|, |b|; NaN if one is.
 __device__ __forceinline__ float max_abs(float a, float b, float c) {
@@ -87,15 +93,17 @@ __device__ __forceinline__ int tensor_of(const AdamTable<N>& t, int unit) {
 // of the assembler as one fused operation, whatever rounding they ask for: an ulp off in one value of six, measured.)
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y)); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+// Two products that no sum takes.
+__device__ __forceinline__ float2 times(float2 a, float2 b) { return __fmul2_rn(a, b); }
 // Two values: m, v, root = sqrt(v) and p moved by g; every operation of m, v and root rounded once.
 __device__ __forceinline__ void move(float2 g, float2& m, float2& v, float2& root, float2& p, const AdamScalars& s, float keep) {
   auto all = [](float x) { return make_float2(x, x); };
-  g = mul2(g, all(s.clip));
+  g = times(g, all(s.clip));
   m = add2(mul2(all(s.b1), m), mul2(all(s.c1), g));
-  v = add2(mul2(all(s.b2), v), mul2(mul2(all(s.c2), g), g));
+  v = add2(mul2(all(s.b2), v), mul2(times(all(s.c2), g), g));
   root = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
   const float2 den = __ffma2_rn(root, all(s.inv), all(s.eps));
-  const float2 q = make_float2(__fdividef(m.x, den.x), __fdividef(m.y, den.y));
+  const float2 q = times(m, make_float2(rcpf(den.x), rcpf(den.y)));  // a reciprocal of 1 ulp, and its product
   p = __ffma2_rn(all(-s.step), q, mul2(p, all(keep)));
 }
 
@@ -181,9 +189,9 @@ __device__ __forceinline__ void block_step(const AdamTensor& t, int64_t e0, cons
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
-        const float2 a = mul2(e4m3x2(wm[h] >> 8 * j), sm);
-        float2 b = mul2(e4m3x2(wv[h] >> 8 * j), sv);
-        b = mul2(b, b);
+        const float2 a = times(e4m3x2(wm[h] >> 8 * j), sm);
+        float2 b = times(e4m3x2(wv[h] >> 8 * j), sv);
+        b = times(b, b);
         m[h][j] = a.x; m[h][j + 1] = a.y;
         r[h][j] = b.x; r[h][j + 1] = b.y;
       }
@@ -235,22 +243,24 @@ __device__ __forceinline__ void block_step(const AdamTensor& t, int64_t e0, cons
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t cm = 0, cv = 0;
+    uint32_t cm[4], cv[4], sign[4];
     const int64_t e = e0 + 128 * h + 4 * lane;
     const uint64_t place = (uint64_t)(t.place + e);
     const uint32_t base = (uint32_t)place * 0x9E3779B9u + (uint32_t)(place >> 32) * 0xBB67AE85u + s.key;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // (four neighbours share the place's upper word: places of blocks are multiples of 256)
-      const uint32_t z = mix32(base + j * 0x9E3779B9u);
-      const float xv = __fmul_rn(r[h][j], iv);
-      const uint32_t a = e4m3_up(__fmul_rn(fabsf(m[h][j]), im), (uint16_t)z) | (__float_as_uint(m[h][j]) >> 24 & 128u);
-      uint32_t b = e4m3_up(xv, (uint16_t)(z >> 16));
-      if (xv > 0.f) b = max(b, 1u);
-      cm |= a << 8 * j;
-      cv |= b << 8 * j;
+    for (int j = 0; j < 4; j += 2) {  // (four neighbours share the place's upper word: places of blocks are multiples of 256)
+      const float2 xv = times(make_float2(r[h][j], r[h][j + 1]), make_float2(iv, iv)), down = make_float2(0x1p-120f, 0x1p-120f);
+      const float2 tm = times(times(make_float2(m[h][j], m[h][j + 1]), make_float2(im, im)), down), tv = times(xv, down);
+      const uint32_t z0 = mix32(base + j * 0x9E3779B9u), z1 = mix32(base + (j + 1) * 0x9E3779B9u);
+      sign[j] = __float_as_uint(tm.x);
+      sign[j + 1] = __float_as_uint(tm.y);
+      cm[j] = e4m3_up(tm.x, __byte_perm(z0, 0, 0x4104));
+      cm[j + 1] = e4m3_up(tm.y, __byte_perm(z1, 0, 0x4104));
+      cv[j] = max(e4m3_up(tv.x, __byte_perm(z0, 0, 0x4324)), xv.x > 0.f ? 1u << 24 : 0u);
+      cv[j + 1] = max(e4m3_up(tv.y, __byte_perm(z1, 0, 0x4324)), xv.y > 0.f ? 1u << 24 : 0u);
     }
-    store4b<WIDE>(badm ? 0x7f7f7f7fu : cm, t.m, e, nv[h]);
-    store4b<WIDE>(badv ? 0x7f7f7f7fu : cv, t.v, e, nv[h]);
+    store4b<WIDE>(badm ? 0x7f7f7f7fu : top4(cm) | (top4(sign) & 0x80808080u), t.m, e, nv[h]);
+    store4b<WIDE>(badv ? 0x7f7f7f7fu : top4(cv), t.v, e, nv[h]);
   }
 }
 
