@@ -264,11 +264,17 @@ __device__ __forceinline__ void block_step(const AdamTensor& t, int64_t e0, cons
   }
 }
 
+// n bytes at p will be read: 16-byte aligned, a multiple of 16.
+__device__ __forceinline__ void to_l2(const void* p, int n) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
+}
+
 // One pass over every tensor, tables of tensors in the launch's parameters (one launch for up to 336).  Bound by memory with
 // fp32 states (12.6 M values of bf16 parameters with masters, 30 bytes each: 77 us with the norm and both small launches, 5.0
-// TB/s; 57 us of it here), with 8-bit states as much by instructions (98 a value: 70 % of the issue slots at 64 % of the copy
-// rate; 201 M values, 18 bytes each: 876 us with the norm, which reads 0.8 GB again).  64 registers and 4 CTAs an SM: 5 or 6 take
-// 902 and 947 us, 3 942.
+// TB/s; 57 us of it here), with 8-bit states by instructions as well (201 M values, 18 bytes each: 774 us with the norm, which
+// reads 0.8 GB again).  A warp's loads of one block cover half of the time it takes at 64 registers and 4 CTAs an SM, so with
+// 8-bit states its next block is brought into L2 meanwhile: 860 us without, 783 two and 849 four blocks ahead; with fp32 states
+// 80 us with, 77 without.  5 CTAs an SM: 793; one wave of CTAs (4 an SM in all) rather than two: 833.
 template <int N>
 __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdamTable<N> tab, const AdamScalars* sc) {
   pdl_enter();
@@ -284,6 +290,14 @@ __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdamTa
     const int64_t e0 = (int64_t)(u - t.first) * kAdamUnit + warp * kAdamBlock;
     if (e0 >= t.n) continue;
     const bool wide = t.vec && e0 + kAdamBlock <= t.n;
+    const int64_t e1 = e0 + kAdamUnit;
+    if (t.ms && lane == 0 && t.vec && e1 + kAdamBlock <= t.n && u + 1 < u1) {
+      const bool pb = t.pb && !t.master;
+      to_l2((const uint8_t*)t.grad + (e1 << (t.gb ? 1 : 2)), kAdamBlock << (t.gb ? 1 : 2));
+      to_l2((const uint8_t*)(t.master ? (void*)t.master : t.param) + (e1 << (pb ? 1 : 2)), kAdamBlock << (pb ? 1 : 2));
+      to_l2((const uint8_t*)t.m + e1, kAdamBlock);
+      to_l2((const uint8_t*)t.v + e1, kAdamBlock);
+    }
     if (t.ms) {
       if (wide) block_step<true, true>(t, e0, s, lane);
       else block_step<true, false>(t, e0, s, lane);
