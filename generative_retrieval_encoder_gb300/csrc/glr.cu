@@ -265,7 +265,9 @@ struct Map { float A, H; };
 struct Map2 { float2 A, H; };  // of a lane's two channels
 constexpr uint64_t kIdentity = 0xBF80000000000000ull;  // h -> 1 h + 0
 __device__ __forceinline__ uint64_t word_of(float A, float H) {
-  return (uint64_t)(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(H);
+  uint32_t a;  // (written as C++ this comes out as the float -|A|, which loses a NaN's sign: the word would never be there)
+  asm("or.b32 %0, %1, 0x80000000;" : "=r"(a) : "r"(__float_as_uint(A)));
+  return (uint64_t)a << 32 | __float_as_uint(H);
 }
 __device__ __forceinline__ Map then(Map m, Map n) {  // first m, then n
   return Map{m.A * n.A, n.A == 0.f ? n.H : fmaf(n.A, m.H, n.H)};
@@ -275,6 +277,9 @@ __device__ __forceinline__ float2 after(const Map2& n, float2 h) {
   return make_float2(n.A.x == 0.f ? n.H.x : o.x, n.A.y == 0.f ? n.H.y : o.y);
 }
 __device__ __forceinline__ Map2 then(const Map2& m, const Map2& n) { return Map2{mul2(m.A, n.A), after(n, m.H)}; }
+// What a warp's rows do.  A NaN decay (it has made H NaN) counts as A = 0, h -> H: no A is NaN then, so a start ends what is
+// before it.  (fmaxf takes the number of a NaN and a number.)
+__device__ __forceinline__ Map2 map_of(float2 A, float2 H) { return Map2{make_float2(fmaxf(A.x, 0.f), fmaxf(A.y, 0.f)), H}; }
 // In shared memory: {A, A, H, H} of a lane's two channels.
 __device__ __forceinline__ Map2 map_at(const float4& g) { return Map2{make_float2(g.x, g.y), make_float2(g.z, g.w)}; }
 __device__ __forceinline__ float4 packed(const Map2& m) { return make_float4(m.A.x, m.A.y, m.H.x, m.H.y); }
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     } else {
       local_rows<T, LOAD, false, false, PER, CH>(a, sm, me.c, f, j0, ch, nch, ka, ka, da, u, A, H);
     }
-    sh.sc.agg[warp][lane] = packed(Map2{f.F ? two(0.f) : A, H});
+    sh.sc.agg[warp][lane] = packed(map_of(f.F ? two(0.f) : A, H));
     // whether the chunk's first row begins a sequence: then nothing enters
     const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && me.k > 0;
     if (tid == 0) {
@@ -833,7 +838,7 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     RowPair<T> dy[PER];
     if (plain) decays_bwd<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, da, dy, A, D);
     else decays_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, da, dy, A, D);
-    sh.sc.agg[vw][lane] = packed(Map2{A, D});
+    sh.sc.agg[vw][lane] = packed(map_of(A, D));
     // whether a sequence ends with the chunk's last row: then nothing comes from behind
     const bool need = !__syncthreads_or(warp == kWarpsB - 1 && (f.E >> (PER - 1) & 1)) && t.k > 0;
     if (tid == 0 && it > 0) {  // the tile before has been gone over: its place is free

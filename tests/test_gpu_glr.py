@@ -380,3 +380,47 @@ def test_glr_captured_call_follows_its_sequence_data(form):
     cols = slice(0, 48)  # (columns are independent)
     check({k: t[..., cols] for k, t in got.items()},
           reference(f(x)[:, cols], f(r)[:, cols], f(i)[:, cols], f(lam)[cols], 8.0, starts, lens, False, f(h0)[:, cols], f(dy)[:, cols], f(dhT)[:, cols]))
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("lengths", [[100, 300, 200, 1, 1000, 7, 3000, 500], [3, 2, 1] * 700])
+def test_glr_a_nan_decay_stays_in_its_sequence(lengths, reverse):
+    """A gate that is NaN makes its sequence's decay NaN; what the tiles compose across a sequence's border is not."""
+    c, clean = (Case("f32", 40, lengths=lengths, reverse=reverse, seed=80) for _ in range(2))
+    bad = [1, 4, len(lengths) - 2]
+    for b in bad:
+        c.r[c.starts[b] + lengths[b] // 2] = float("nan")
+    y, hT, saved = c.forward(hT=True, saved=True)
+    g = c.backward(saved)
+    y0, hT0, saved0 = clean.forward(hT=True, saved=True)
+    g0 = clean.backward(saved0)
+    torch.cuda.synchronize()
+    rows = torch.ones(c.T, dtype=torch.bool, device="cuda")
+    seqs = torch.ones(c.n, dtype=torch.bool, device="cuda")
+    for b in bad:
+        rows[c.starts[b]:c.starts[b] + lengths[b]] = False
+        seqs[b] = False
+    assert torch.isnan(hT[bad]).all() and torch.isnan(g["dlam"]).all()
+    assert torch.equal(y[rows], y0[rows]) and torch.equal(hT[seqs], hT0[seqs]) and torch.equal(g["dh0"][seqs], g0["dh0"][seqs])
+    for n in ("dx", "dr", "di"):
+        assert torch.equal(g[n][rows], g0[n][rows]), n
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_glr_a_nan_decay_of_long_slots_stays_in_its_channel(reverse):
+    """A NaN gate and a NaN lam in chains of many tiles: the calls end, their channels alone are NaN."""
+    c = Case("bf16", 72, L=3000, B=3, reverse=reverse, seed=81)
+    want = c.reference()
+    c.r[3000 + 1500, 5] = float("nan")  # sequence 1
+    c.lam[8] = float("nan")
+    ws = [gbla.workspace(c.shape, op) for op in (gbla.GBLA_OP_GLR_FORWARD, gbla.GBLA_OP_GLR_BACKWARD)]
+    y, hT, saved = c.forward(hT=True, saved=True, ws=ws[0])
+    g = c.backward(saved, ws=ws[1])
+    assert all(gbla.gbla_check_device_status(w) == gbla.GBLA_OK for w in ws)
+    ok = [ch for ch in range(72) if ch not in (5, 8)]
+    check({n: t[..., ok] for n, t in {"y": y, "hT": hT, **g}.items()}, {n: tuple(w[..., ok] for w in v) for n, v in want.items()})
+    for b in (0, 2):  # the other sequences' channel 5
+        rows = slice(3000 * b, 3000 * b + 3000)
+        check({n: t[rows, 5] for n, t in {"y": y, "dx": g["dx"], "dr": g["dr"], "di": g["di"]}.items()},
+              {n: tuple(w[rows, 5] for w in want[n]) for n in ("y", "dx", "dr", "di")})
+    assert torch.isnan(hT[1, 5]) and torch.isnan(hT[:, 8]).all() and torch.isnan(g["dlam"][[5, 8]]).all()
