@@ -31,11 +31,17 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 // The 32 random bits of a place are mix32(low word of the place * 0x9E3779B9 (the fraction bits of the golden ratio spread
 // neighbours) + high word * 0xBB67AE85 + the step's key).
 
-// t 2^-120 with |t| in [0, 448] (or two units in the last place above: the sum below does not reach the next code) and 16 random
-// bits, at bits 8 .. 23 of d, to an e4m3 magnitude in the top byte.  At 2^-120 the values of e4m3 are the fp32 ones of 3 fraction
-// bits, those below 2^-6 among the subnormal ones (a fixed step of 2^-9 for both), so the bits below are added to and cut off
-// alike (there are 20 of them: a subnormal t 2^-120 is rounded 2^-21 of a step at most from its value).
+// |t| in [0, 448] (or two units in the last place above: the sum below does not reach the next code) to an e4m3 magnitude in the
+// top byte, with 16 random bits.  From t 2^-120, where the normal values of e4m3 (t >= 2^-6) are the fp32 ones of 3 fraction
+// bits, the random bits at bits 8 .. 23 of d; 0 stays 0.
 __device__ __forceinline__ uint32_t e4m3_up(float t, uint32_t d) { return (__float_as_uint(t) << 4) + d; }
+// Below 2^-6 the fixed step 2^-9: floor(512 t + d 2^-16) (both products exact; floor by an addition rounded down at 2^23), of
+// two values; d the low or the high half of z.
+__device__ __forceinline__ uint2 e4m3_low(float2 t, uint32_t z0, uint32_t z1) {
+  const float2 d = make_float2((float)(uint16_t)z0, (float)(uint16_t)z1);
+  const float2 s = __fadd2_rd(__ffma2_rn(d, make_float2(0x1p-16f, 0x1p-16f), __fmul2_rn(t, make_float2(512.f, 512.f))), make_float2(8388608.f, 8388608.f));
+  return make_uint2(__float_as_uint(s.x) << 24, __float_as_uint(s.y) << 24);
+}
 // The top bytes of four words.
 __device__ __forceinline__ uint32_t top4(const uint32_t (&w)[4]) {
   return __byte_perm(__byte_perm(w[0], w[1], 0x0073), __byte_perm(w[2], w[3], 0x0073), 0x5410);
@@ -247,17 +253,22 @@ __device__ __forceinline__ void block_step(const AdamTensor& t, int64_t e0, cons
     const int64_t e = e0 + 128 * h + 4 * lane;
     const uint64_t place = (uint64_t)(t.place + e);
     const uint32_t base = (uint32_t)place * 0x9E3779B9u + (uint32_t)(place >> 32) * 0xBB67AE85u + s.key;
+    const float2 down = make_float2(0x1p-120f, 0x1p-120f);
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {  // (four neighbours share the place's upper word: places of blocks are multiples of 256)
-      const float2 xv = times(make_float2(r[h][j], r[h][j + 1]), make_float2(iv, iv)), down = make_float2(0x1p-120f, 0x1p-120f);
-      const float2 tm = times(times(make_float2(m[h][j], m[h][j + 1]), make_float2(im, im)), down), tv = times(xv, down);
+      const float2 xm = times(make_float2(fabsf(m[h][j]), fabsf(m[h][j + 1])), make_float2(im, im));
+      const float2 xv = times(make_float2(r[h][j], r[h][j + 1]), make_float2(iv, iv));
+      const float2 tm = times(xm, down), tv = times(xv, down);
       const uint32_t z0 = mix32(base + j * 0x9E3779B9u), z1 = mix32(base + (j + 1) * 0x9E3779B9u);
-      sign[j] = __float_as_uint(tm.x);
-      sign[j + 1] = __float_as_uint(tm.y);
-      cm[j] = e4m3_up(tm.x, __byte_perm(z0, 0, 0x4104));
-      cm[j + 1] = e4m3_up(tm.y, __byte_perm(z1, 0, 0x4104));
-      cv[j] = max(e4m3_up(tv.x, __byte_perm(z0, 0, 0x4324)), xv.x > 0.f ? 1u << 24 : 0u);
-      cv[j + 1] = max(e4m3_up(tv.y, __byte_perm(z1, 0, 0x4324)), xv.y > 0.f ? 1u << 24 : 0u);
+      const uint2 lm = e4m3_low(xm, z0, z1), lv = e4m3_low(xv, z0 >> 16, z1 >> 16);
+      cm[j] = xm.x < 0x1p-6f ? lm.x : e4m3_up(tm.x, __byte_perm(z0, 0, 0x4104));
+      cm[j + 1] = xm.y < 0x1p-6f ? lm.y : e4m3_up(tm.y, __byte_perm(z1, 0, 0x4104));
+      cv[j] = xv.x < 0x1p-6f ? lv.x : e4m3_up(tv.x, __byte_perm(z0, 0, 0x4324));
+      cv[j + 1] = xv.y < 0x1p-6f ? lv.y : e4m3_up(tv.y, __byte_perm(z1, 0, 0x4324));
+      if (xv.x > 0.f) cv[j] = max(cv[j], 1u << 24);
+      if (xv.y > 0.f) cv[j + 1] = max(cv[j + 1], 1u << 24);
+      sign[j] = __float_as_uint(m[h][j]);
+      sign[j + 1] = __float_as_uint(m[h][j + 1]);
     }
     store4b<WIDE>(badm ? 0x7f7f7f7fu : top4(cm) | (top4(sign) & 0x80808080u), t.m, e, nv[h]);
     store4b<WIDE>(badv ? 0x7f7f7f7fu : top4(cv), t.v, e, nv[h]);
@@ -271,10 +282,11 @@ __device__ __forceinline__ void to_l2(const void* p, int n) {
 
 // One pass over every tensor, tables of tensors in the launch's parameters (one launch for up to 336).  Bound by memory with
 // fp32 states (12.6 M values of bf16 parameters with masters, 30 bytes each: 77 us with the norm and both small launches, 5.0
-// TB/s; 57 us of it here), with 8-bit states by instructions as well (201 M values, 18 bytes each: 774 us with the norm, which
-// reads 0.8 GB again).  A warp's loads of one block cover half of the time it takes at 64 registers and 4 CTAs an SM, so with
-// 8-bit states its next block is brought into L2 meanwhile: 860 us without, 783 two and 849 four blocks ahead; with fp32 states
-// 80 us with, 77 without.  5 CTAs an SM: 793; one wave of CTAs (4 an SM in all) rather than two: 833.
+// TB/s; 57 us of it here), with 8-bit states by instructions (99 a value, 78 % of the issue slots at 5.6 TB/s; 201 M values, 18
+// bytes each: 800 us with the norm, which reads 0.8 GB again).  At 64 registers and 4 CTAs an SM a warp's loads of one block do
+// not cover the time it takes, so with 8-bit states its next block is brought into L2 meanwhile (860 us before; two and four
+// blocks ahead are 10 and 75 us slower than one); with fp32 states 80 us with, 77 without.  5 CTAs an SM, or one wave of CTAs
+// rather than two: 20 and 60 us slower.
 template <int N>
 __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdamTable<N> tab, const AdamScalars* sc) {
   pdl_enter();

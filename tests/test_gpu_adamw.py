@@ -487,3 +487,22 @@ def test_norm_reads_the_gradients_alone():
     assert gbla.lib().gbla_grad_norm(t, 2, norm.data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
     want = float(g.double().norm())
     assert abs(float(norm) - want) <= 2 * E * want  # the sum is good to 2^-40; one rounding of the root
+
+
+def test_8bit_codes_of_small_values_bit_for_bit():
+    """Blocks whose values spread over many powers of two: half of them are below the smallest normal code, where a last bit of
+    the quotient decides once in some million values."""
+    n = 1 << 24
+    gen = torch.Generator().manual_seed(95)
+    g = (torch.randn(n, generator=gen) * torch.exp(4 * torch.randn(n, generator=gen)) * 1e-4).cuda()
+    P = [torch.zeros(n, device="cuda")]
+    st = gbla.gbla_adamw_state(P, bits=8)
+    zero, scale = np.zeros(n, np.uint8), np.zeros(n // 256, np.float32)
+    codes, scales, (m, root) = step8((zero, zero), (scale, scale), g.cpu().numpy(), 1, 0, 77)
+    for x, s in ((np.abs(m), scales[0]), (root, scales[1])):
+        assert ((x < np.repeat(s, 256) * np.float32(2.0 ** -6)).mean() > 0.3)
+    gbla.gbla_adamw_step(gbla.gbla_adamw_plan(P, [g], st), LR, BETAS, EPS, WD, seed=77)
+    for k, name in enumerate(("m", "v")):
+        assert np.array_equal(st[name + "_scale"][0].cpu().numpy(), scales[k]), name
+        off = np.count_nonzero(st[name][0].view(torch.uint8).cpu().numpy() != codes[k])
+        assert off == 0, f"{name}: {off} codes"
