@@ -266,8 +266,9 @@ size_t glr_saved_size(const gbla_shape* shape);
 
 /*
  * Backward of glr_forward for the scalar <dy, y> + <dhT, hT>: the forward's
- * inputs, its `saved`, dy (io) [rows, d] and dhT fp32 [n_seq, d] or NULL
- * (zeros).  Outputs:
+ * inputs (h0 as it was then: not one that the call updated in place), its
+ * `saved` (of the same shape and direction), dy (io) [rows, d] and dhT fp32
+ * [n_seq, d] or NULL (zeros).  Outputs:
  *   dx, dr, di (io) [rows, d] with row stride ldd (ldd >= d; e.g. the columns
  *   of one gradient matrix); dlam fp32 [d] or NULL; dh0 fp32 [n_seq, d] or
  *   NULL (an empty sequence's is its dhT).  Gradients overwrite.
