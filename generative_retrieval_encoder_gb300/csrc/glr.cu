@@ -255,7 +255,9 @@ __device__ __forceinline__ void tile_of(const GlrArgs& a, const GlrTiles& g, uns
 
 // ------------------------------------------------------------ the scan between chunks
 // A tile publishes, per channel, what its rows do to a state that enters: h -> A h + H, as one 64-bit word {H, A}
-// (present when the top bit, A's sign, is set: one word, so nothing else has to be ordered).  A = 0: a sequence starts here, h -> H whatever h was.  Chunks form
+// (present when the top bit, A's sign, is set: one word, so nothing else has to be ordered).  A = 0: a sequence starts here, h -> H
+// whatever h was.  A product of decays is never 0: one below the fp32 range counts as its smallest value, 2^-149, so that a state
+// that is NaN or infinite stays so to its sequence's end (and a finite one adds 2^-149 of itself at most).  Chunks form
 // groups of 16 and groups of groups; a chunk that needs the state before it composes the words of the chunks before it in
 // its group, of the groups before its own in the larger group, and the state after the last larger group: at most 31
 // words, read together.  The order of composition is fixed, so results do not depend on timing.
@@ -269,17 +271,22 @@ __device__ __forceinline__ uint64_t word_of(float A, float H) {
   asm("or.b32 %0, %1, 0x80000000;" : "=r"(a) : "r"(__float_as_uint(A)));
   return (uint64_t)a << 32 | __float_as_uint(H);
 }
-__device__ __forceinline__ Map then(Map m, Map n) {  // first m, then n
-  return Map{m.A * n.A, n.A == 0.f ? n.H : fmaf(n.A, m.H, n.H)};
-}
+constexpr float kTiny = 0x1p-149f;
+// The product p of decays, the least of them low: 0 where one of them is, and only there.
+__device__ __forceinline__ float product(float p, float low) { return fmaxf(p, fminf(low, kTiny)); }
+__device__ __forceinline__ float2 product(float2 p, float2 low) { return make_float2(product(p.x, low.x), product(p.y, low.y)); }
+__device__ __forceinline__ float2 least(float2 a, float2 b) { return make_float2(fminf(a.x, b.x), fminf(a.y, b.y)); }
 __device__ __forceinline__ float2 after(const Map2& n, float2 h) {
   const float2 o = fma2(n.A, h, n.H);
   return make_float2(n.A.x == 0.f ? n.H.x : o.x, n.A.y == 0.f ? n.H.y : o.y);
 }
-__device__ __forceinline__ Map2 then(const Map2& m, const Map2& n) { return Map2{mul2(m.A, n.A), after(n, m.H)}; }
-// What a warp's rows do.  A NaN decay (it has made H NaN) counts as A = 0, h -> H: no A is NaN then, so a start ends what is
-// before it.  (fmaxf takes the number of a NaN and a number.)
-__device__ __forceinline__ Map2 map_of(float2 A, float2 H) { return Map2{make_float2(fmaxf(A.x, 0.f), fmaxf(A.y, 0.f)), H}; }
+// First m, then n.
+__device__ __forceinline__ Map2 then(const Map2& m, const Map2& n) { return Map2{product(mul2(m.A, n.A), least(m.A, n.A)), after(n, m.H)}; }
+// What a warp's rows do, A the product of their decays; start: nothing from before them gets through.  A NaN decay (it has made H
+// NaN) counts as 2^-149 too: no A is NaN then, so a start ends what is before it.  (fmaxf takes the number of a NaN and a number.)
+__device__ __forceinline__ Map2 map_of(float2 A, float2 H, bool start) {
+  return Map2{start ? two(0.f) : make_float2(fmaxf(A.x, kTiny), fmaxf(A.y, kTiny)), H};
+}
 // In shared memory: {A, A, H, H} of a lane's two channels.
 __device__ __forceinline__ Map2 map_at(const float4& g) { return Map2{make_float2(g.x, g.y), make_float2(g.z, g.w)}; }
 __device__ __forceinline__ float4 packed(const Map2& m) { return make_float4(m.A.x, m.A.y, m.H.x, m.H.y); }
@@ -340,10 +347,14 @@ __device__ __forceinline__ Map answer(const GlrArgs& a, const Tile& t, int part,
     for (int j = 0; j < 64 / W; ++j) v.w[j] = peek_word<W>(a, t, part, cc, j, !(v.w[j] >> 63), v.w[j]);
   }
   Map m{1.f, 0.f};
+  float low = 1.f;
 #pragma unroll
-  for (int j = 0; j < 64 / W; ++j)
-    m = then(m, Map{__uint_as_float((uint32_t)(v.w[j] >> 32) & 0x7fffffffu), __uint_as_float((uint32_t)v.w[j])});
-  return m;
+  for (int j = 0; j < 64 / W; ++j) {  // one after the other
+    const float A = __uint_as_float((uint32_t)(v.w[j] >> 32) & 0x7fffffffu), H = __uint_as_float((uint32_t)v.w[j]);
+    m = Map{m.A * A, A == 0.f ? H : fmaf(A, m.H, H)};
+    low = fminf(low, A);
+  }
+  return Map{product(m.A, low), m.H};
 }
 
 // Shared memory of the scan: what the rows of each warp (in the chain's order) do; the parts of the words.
@@ -355,7 +366,20 @@ template <int W> struct ScanShared {
 template <int W>
 __device__ __forceinline__ Map2 scan_local(const GlrArgs& a, const Tile& t, const ScanShared<W>& sc, int vw, int lane, Map2& total) {
   Map2 m{two(1.f), two(0.f)};
-  for (int w = 0; w < vw; ++w) m = then(m, map_at(sc.agg[w][lane]));
+  float2 low = two(1.f);
+  if (t.inner) {  // no start among the rows
+    for (int w = 0; w < vw; ++w) {
+      const Map2 n = map_at(sc.agg[w][lane]);
+      m = Map2{mul2(m.A, n.A), fma2(n.A, m.H, n.H)};
+    }
+  } else {
+    for (int w = 0; w < vw; ++w) {
+      const Map2 n = map_at(sc.agg[w][lane]);
+      m = Map2{mul2(m.A, n.A), after(n, m.H)};
+      low = least(low, n.A);
+    }
+  }
+  m.A = product(m.A, low);
   if (vw == W - 1) {
     total = then(m, map_at(sc.agg[vw][lane]));
     if (t.k < t.last) publish(a.words + t.own + 2 * lane, total);
@@ -574,7 +598,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, kCtasFwd) k_glr_fwd(const GlrArg
     } else {
       local_rows<T, LOAD, false, false, PER, CH>(a, sm, me.c, f, j0, ch, nch, ka, ka, da, u, A, H);
     }
-    sh.sc.agg[warp][lane] = packed(map_of(f.F ? two(0.f) : A, H));
+    sh.sc.agg[warp][lane] = packed(map_of(A, H, f.F != 0));
     // whether the chunk's first row begins a sequence: then nothing enters
     const bool need = !__syncthreads_or(warp == 0 && (f.F & 1)) && me.k > 0;
     if (tid == 0) {
@@ -648,8 +672,8 @@ constexpr int kStagesBwd = 2;
 // The backward goes over a tile's rows twice (they stay in shared memory): first for the decays, which with dy are all that
 // the scan of w takes, then, with w known, for everything else.  Held in between: a, and dy, whose place w takes.
 
-// The lane's rows, what they do together to a w from behind: w -> A w + D.  sm: the lane's first row of x in shared memory, r, i
-// and dy one, two and three tiles on.
+// The lane's rows, what they do together to a w from behind: w -> A w + D (an end in them: D alone).  sm: the lane's first row of
+// x in shared memory, r, i and dy one, two and three tiles on.
 template <typename T, int LOAD, bool SMALL, bool PLAIN, int PER, int CH>
 __device__ __forceinline__ void decays_bwd(const GlrArgs& a, const T* sm, const Span& c, const Flags& f, int j0, int ch, int nch, float2 ka,
                                            float2 (&da)[PER], RowPair<T> (&dy)[PER], float2& A, float2& D) {
@@ -680,10 +704,8 @@ __device__ __forceinline__ void decays_bwd(const GlrArgs& a, const T* sm, const 
   D = two(0.f);
 #pragma unroll
   for (int q = PER - 1; q >= 0; --q) {
-    if (!PLAIN && (f.E >> q & 1)) {
+    if (!PLAIN && (f.E >> q & 1))
       D = a.dhT ? load2<float, false>(a.dhT, (int64_t)seq_of(a, row_at<CH>(a, c, j0 + q)) * a.d + ch, nch) : two(0.f);
-      A = two(0.f);  // nothing from behind an end gets here
-    }
     D = mul2(da[q], add2(D, dy[q].get()));
   }
 }
@@ -838,7 +860,7 @@ __global__ void __launch_bounds__(kWarpsB * 32, kCtasBwd) k_glr_bwd(const GlrArg
     RowPair<T> dy[PER];
     if (plain) decays_bwd<T, LOAD, true, true, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, da, dy, A, D);
     else decays_bwd<T, LOAD, false, false, PER, CH>(a, sm, t.c, f, j0, ch, nch, ka, da, dy, A, D);
-    sh.sc.agg[vw][lane] = packed(map_of(A, D));
+    sh.sc.agg[vw][lane] = packed(map_of(A, D, f.E != 0));
     // whether a sequence ends with the chunk's last row: then nothing comes from behind
     const bool need = !__syncthreads_or(warp == kWarpsB - 1 && (f.E >> (PER - 1) & 1)) && t.k > 0;
     if (tid == 0 && it > 0) {  // the tile before has been gone over: its place is free

@@ -424,3 +424,54 @@ def test_glr_a_nan_decay_of_long_slots_stays_in_its_channel(reverse):
         check({n: t[rows, 5] for n, t in {"y": y, "dx": g["dx"], "dr": g["dr"], "di": g["di"]}.items()},
               {n: tuple(w[rows, 5] for w in want[n]) for n in ("y", "dx", "dr", "di")})
     assert torch.isnan(hT[1, 5]) and torch.isnan(hT[:, 8]).all() and torch.isnan(g["dlam"][[5, 8]]).all()
+
+
+def _nonfinite(t):
+    return (~torch.isfinite(t)).all()
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("lam", [None, 0.0, 30.0], ids=["slow", "fast", "instant"])
+@pytest.mark.parametrize("kw", [dict(dtype="f32", d=40, L=9001, B=2), dict(dtype="bf16", d=40, L=9001, B=2, seq_lens=[9001, 8700]),
+                                dict(dtype="bf16", d=1032, lengths=[700, 9001, 600]), dict(dtype="f32", d=40, lengths=[9001] + [1, 5, 300] * 9)],
+                         ids=["dense", "padded", "seqs", "stream"])
+def test_glr_a_nonfinite_state_lasts_to_its_sequence_end(kw, lam, reverse):
+    """A NaN or an infinity in h0, x or a gate, in dhT or dy, reaches every later row of its channel, however small the product of
+    the decays in between is (it is 0 in fp32 over a tile, over some tiles, and in each row), and nothing else."""
+    make = lambda: Case(seed=90, reverse=reverse, lam=None if lam is None else torch.full((kw["d"],), lam), **kw)  # noqa: E731
+    c, clean = make(), make()
+    b = 1 if "lengths" in kw and kw["d"] > 100 else 0  # the long sequence
+    n, r0 = c.lens[b], c.starts[b]
+    order = list(range(r0 + n - 1, r0 - 1, -1)) if reverse else list(range(r0, r0 + n))
+    inf, nan = float("inf"), float("nan")
+    c.h0[b, 3], c.h0[b, 5] = inf, nan
+    c.x[order[3], 7], c.x[order[130], 9], c.r[order[3], 11] = nan, inf, nan
+    first = {3: 0, 5: 0, 7: 3, 9: 130, 11: 3}
+    y, hT, saved = c.forward(hT=True, saved=True)
+    y0, hT0, saved0 = clean.forward(hT=True, saved=True)
+    for ch, k in first.items():
+        assert _nonfinite(y[order[k:], ch]) and _nonfinite(hT[b, ch]), ch
+    ok = torch.ones_like(y, dtype=torch.bool)
+    for ch, k in first.items():
+        ok[order[k:], ch] = False
+    okT = torch.ones_like(hT, dtype=torch.bool)
+    okT[b, list(first)] = False
+    assert torch.equal(y[ok], y0[ok]) and torch.equal(hT[okT], hT0[okT])
+    # what comes from behind, on clean states
+    g0 = clean.backward(saved0)
+    clean.dhT[b, 13], clean.dhT[b, 15] = inf, nan
+    clean.dy[order[-4], 17], clean.dy[order[-131], 19] = nan, inf
+    last = {13: n, 15: n, 17: n - 3, 19: n - 130}
+    g = clean.backward(saved0)
+    ok = torch.ones_like(y, dtype=torch.bool)
+    for ch, k in last.items():
+        assert _nonfinite(g["dx"][order[:k], ch]) and _nonfinite(g["dr"][order[:k], ch]) and _nonfinite(g["dh0"][b, ch]), ch
+        assert _nonfinite(g["dlam"][ch]), ch
+        ok[order[:k], ch] = False
+    okT = torch.ones_like(hT, dtype=torch.bool)
+    okT[b, list(last)] = False
+    for name in ("dx", "dr", "di"):
+        assert torch.equal(g[name][ok], g0[name][ok]), name
+    assert torch.equal(g["dh0"][okT], g0["dh0"][okT])
+    rest = [ch for ch in range(c.d) if ch not in last]
+    assert torch.equal(g["dlam"][rest], g0["dlam"][rest])
