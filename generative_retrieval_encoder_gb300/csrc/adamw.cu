@@ -321,37 +321,44 @@ __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdamTa
 }
 
 // Sums of squares, a CTA's in one partial: a thread adds g g into two fp32 words (the product's own error and that of each
-// addition go to the lower word), the CTA adds those in fp64 in a fixed order.  Bound by memory: 0.8 GB of fp32 gradients in two
-// tables in 106 + 37 us, 5.7 TB/s.
+// addition go to the lower word), the CTA adds those in fp64 in a fixed order.  A thread whose sum passes the fp32 range goes
+// over its values again in fp64.  Bound by memory: 0.8 GB of fp32 gradients in two tables in 106 + 37 us, 5.7 TB/s.
 template <int N>
 __global__ void __launch_bounds__(256) k_sumsq(const __grid_constant__ AdamTable<N> tab, double* part) {
   pdl_enter();
   __shared__ double red[8];
   const int u0 = (int)((int64_t)tab.units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)tab.units * (blockIdx.x + 1) / gridDim.x);
-  float hi = 0.f, lo = 0.f;
-  int k = u0 < u1 ? tensor_of(tab, u0) : 0;
-  for (int u = u0; u < u1; ++u) {
-    while (k + 1 < tab.n && tab.t[k + 1].first <= u) ++k;
-    const AdamTensor& t = tab.t[k];
-    float g[2][4];
+  auto walk = [&](auto&& add) {  // the thread's values
+    int k = u0 < u1 ? tensor_of(tab, u0) : 0;
+    for (int u = u0; u < u1; ++u) {
+      while (k + 1 < tab.n && tab.t[k + 1].first <= u) ++k;
+      const AdamTensor& t = tab.t[k];
+      float g[2][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t e = (int64_t)(u - t.first) * kAdamUnit + 1024 * h + 4 * threadIdx.x;
-      const int nv = (int)max((int64_t)0, min((int64_t)4, t.n - e));
-      if (t.vec && nv == 4) load4<true, true>(g[h], t.grad, e, t.gb, nv);
-      else load4<false>(g[h], t.grad, e, t.gb, nv);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v = g[h][j], q = __fmul_rn(v, v), w = __fmaf_rn(v, v, -q);
-        const float sum = __fadd_rn(hi, q), b = __fadd_rn(sum, -hi);
-        lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fadd_rn(hi, -__fadd_rn(sum, -b)), __fadd_rn(q, -b)), w));
-        hi = sum;
+      for (int h = 0; h < 2; ++h) {
+        const int64_t e = (int64_t)(u - t.first) * kAdamUnit + 1024 * h + 4 * threadIdx.x;
+        const int nv = (int)max((int64_t)0, min((int64_t)4, t.n - e));
+        if (t.vec && nv == 4) load4<true, true>(g[h], t.grad, e, t.gb, nv);
+        else load4<false>(g[h], t.grad, e, t.gb, nv);
       }
-  }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) add(g[h][j]);
+    }
+  };
+  float hi = 0.f, lo = 0.f;
+  walk([&](float v) {
+    const float q = __fmul_rn(v, v), w = __fmaf_rn(v, v, -q);
+    const float sum = __fadd_rn(hi, q), b = __fadd_rn(sum, -hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fadd_rn(hi, -__fadd_rn(sum, -b)), __fadd_rn(q, -b)), w));
+    hi = sum;
+  });
   double d = (double)hi + (double)lo;
+  if (!isfinite(hi)) {
+    d = 0.;
+    walk([&](float v) { d += isfinite(__fmul_rn(v, v)) ? (double)v * (double)v : (double)__fmul_rn(v, v); });
+  }
   for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(FULL, d, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = d;
   __syncthreads();

@@ -325,8 +325,9 @@ typedef struct {
 size_t gbla_adamw_workspace_size(const gbla_adamw_tensor* tensors, int n_tensors);
 
 /* The global 2-norm of the tensors' gradients into norm (fp32, device; one
- * value).  Squares are summed in two fp32 words a thread and in fp64 beyond, in
- * a fixed order; a square over the fp32 range counts as not finite.  Only grad,
+ * value).  Squares are summed in two fp32 words a thread (in fp64 where their
+ * sum passes the fp32 range) and in fp64 beyond, in a fixed order; a single
+ * square over the fp32 range counts as not finite, one under it as 0.  Only grad,
  * grad_dtype and n are read. */
 gbla_status gbla_grad_norm(const gbla_adamw_tensor* tensors, int n_tensors,
                            float* norm, void* ws, size_t ws_bytes, void* stream);

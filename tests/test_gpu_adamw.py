@@ -506,3 +506,17 @@ def test_8bit_codes_of_small_values_bit_for_bit():
         assert np.array_equal(st[name + "_scale"][0].cpu().numpy(), scales[k]), name
         off = np.count_nonzero(st[name][0].view(torch.uint8).cpu().numpy() != codes[k])
         assert off == 0, f"{name}: {off} codes"
+
+
+def test_norm_of_large_gradients_whose_squares_are_finite():
+    """2048 squares of 1e38 each: a thread has eight of them, and four are over the fp32 range; the norm, 4.5e20, is not."""
+    for g in (torch.full((2048,), 1e19, device="cuda"), torch.full((5000,), 1e19, device="cuda").bfloat16(),
+              torch.cat([torch.full((3,), 1.8e19, device="cuda"), torch.randn(300000, device="cuda")])):
+        P = [torch.zeros(g.numel(), device="cuda")]
+        st = gbla.gbla_adamw_state(P)
+        plan = gbla.gbla_adamw_plan(P, [g], st)
+        norm = gbla.gbla_grad_norm(plan)
+        w = np.sqrt((f64(g) ** 2).sum())
+        assert abs(float(norm) - w) <= 1.01 * E * w  # one rounding
+        gbla.gbla_adamw_step(plan, LR, norm=norm, max_norm=1.0)
+        assert int(st["step"]) == 1
