@@ -66,8 +66,9 @@ __device__ __forceinline__ float2 e4m3x2(uint32_t w) {
   return o;
 }
 
-__global__ void k_adamw_begin(const AdamStep c, int64_t* step, const float* norm, AdamScalars* s) {
+__global__ void k_adamw_begin(const AdamStep c, int64_t* step, const float* norm, AdamScalars* s, int* err) {
   pdl_enter();
+  *err = 0;
   const float nm = norm ? *norm : 0.f;
   AdamScalars o;
   o.go = isfinite(nm);
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(256) k_sumsq(const __grid_constant__ AdamTable
   }
 }
 
-__global__ void __launch_bounds__(256) k_norm(const double* part, int n, float* norm) {
+__global__ void __launch_bounds__(256) k_norm(const double* part, int n, float* norm, int* err) {
   pdl_enter();
   __shared__ double red[256];
   double d = 0.;
@@ -379,15 +380,18 @@ __global__ void __launch_bounds__(256) k_norm(const double* part, int n, float* 
     if ((int)threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
     __syncthreads();
   }
-  if (threadIdx.x == 0) *norm = (float)sqrt(red[0]);
+  if (threadIdx.x == 0) {
+    *norm = (float)sqrt(red[0]);
+    *err = 0;
+  }
 }
 
 }  // namespace
 
 int adamw_ctas(int64_t units) { return (int)std::min<int64_t>(units, (int64_t)sm_count() * 8); }
 
-cudaError_t launch_adamw_begin(const AdamStep& c, int64_t* step, const float* norm, AdamScalars* s, cudaStream_t st) {
-  return launch_pdl(k_adamw_begin, dim3(1), dim3(1), 0, st, c, step, norm, s);
+cudaError_t launch_adamw_begin(const AdamStep& c, int64_t* step, const float* norm, AdamScalars* s, int* err, cudaStream_t st) {
+  return launch_pdl(k_adamw_begin, dim3(1), dim3(1), 0, st, c, step, norm, s, err);
 }
 
 template <int N>
@@ -398,8 +402,8 @@ template <int N>
 cudaError_t launch_sumsq(const AdamTable<N>& t, double* part, cudaStream_t st) {
   return launch_pdl(k_sumsq<N>, dim3((unsigned)adamw_ctas(t.units)), dim3(256), 0, st, t, part);
 }
-cudaError_t launch_norm(const double* part, int n, float* norm, cudaStream_t st) {
-  return launch_pdl(k_norm, dim3(1), dim3(256), 0, st, part, n, norm);
+cudaError_t launch_norm(const double* part, int n, float* norm, int* err, cudaStream_t st) {
+  return launch_pdl(k_norm, dim3(1), dim3(256), 0, st, part, n, norm, err);
 }
 template cudaError_t launch_adamw<kAdamFew>(const AdamTable<kAdamFew>&, const AdamScalars*, cudaStream_t);
 template cudaError_t launch_adamw<kAdamMany>(const AdamTable<kAdamMany>&, const AdamScalars*, cudaStream_t);

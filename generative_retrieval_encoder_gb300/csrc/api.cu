@@ -521,7 +521,9 @@ int adam_cap(const gbla_adamw_tensor* t, int n) {
   return live <= kAdamFew ? kAdamFew : kAdamMany;
 }
 
-constexpr size_t kAdamScalarBytes = 256;
+// The workspace: the error word (0: these calls find no error on the device), the step's scalars, the norm's partials.
+constexpr size_t kAdamScalars = 64, kAdamParts = 256;
+static_assert(kAdamScalars + sizeof(AdamScalars) <= kAdamParts, "");
 // One fp64 partial for each CTA of each launch.
 size_t adam_parts(const gbla_adamw_tensor* t, int n) {
   const int cap = adam_cap(t, n);
@@ -533,7 +535,7 @@ gbla_status adam_check(const gbla_adamw_tensor* t, int n, bool norm_only, void* 
   for (int k = 0; k < n; ++k)
     if (!adam_tensor_ok(t[k], norm_only)) return GBLA_ERR_INVALID_ARG;
   if (adam_units(t, n) > (1LL << 30)) return GBLA_ERR_UNSUPPORTED;  // units are counted in 32 bits
-  if (!ws || reinterpret_cast<uintptr_t>(ws) % kAlign || ws_bytes < kAdamScalarBytes + 8 * adam_parts(t, n))
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % kAlign || ws_bytes < kAdamParts + 8 * adam_parts(t, n))
     return GBLA_ERR_WORKSPACE;
   return GBLA_OK;
 }
@@ -571,7 +573,8 @@ gbla_status adam_tables(const gbla_adamw_tensor* t, int n, double lr, F&& fn) {
 struct AdamCtx { cudaStream_t st; };
 
 template <int N>
-gbla_status run_grad_norm(const gbla_adamw_tensor* t, int n, float* norm, double* part, AdamCtx c) {
+gbla_status run_grad_norm(const gbla_adamw_tensor* t, int n, float* norm, void* ws, AdamCtx c) {
+  double* part = at<double>(ws, kAdamParts);
   int parts = 0;
   const gbla_status r = adam_tables<N>(t, n, 0., [&](const AdamTable<N>& tab) {
     GBLA_CHECK(launch_sumsq<N>(tab, part + parts, c.st), "grad sumsq");
@@ -579,7 +582,7 @@ gbla_status run_grad_norm(const gbla_adamw_tensor* t, int n, float* norm, double
     return GBLA_OK;
   });
   if (r != GBLA_OK) return r;
-  GBLA_CHECK(launch_norm(part, parts, norm, c.st), "grad norm");
+  GBLA_CHECK(launch_norm(part, parts, norm, at<int>(ws, 0), c.st), "grad norm");
   return GBLA_OK;
 }
 
@@ -1152,7 +1155,7 @@ size_t gbla_adamw_workspace_size(const gbla_adamw_tensor* tensors, int n_tensors
   if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return 0;
   for (int k = 0; k < n_tensors; ++k)
     if (tensors[k].n < 0 || tensors[k].n > (1LL << 40)) return 0;
-  return align_up(kAdamScalarBytes + 8 * adam_parts(tensors, n_tensors));
+  return align_up(kAdamParts + 8 * adam_parts(tensors, n_tensors));
 }
 
 gbla_status gbla_grad_norm(const gbla_adamw_tensor* tensors, int n_tensors, float* norm, void* ws, size_t ws_bytes,
@@ -1161,9 +1164,8 @@ gbla_status gbla_grad_norm(const gbla_adamw_tensor* tensors, int n_tensors, floa
   if (r != GBLA_OK) return r;
   if (!norm || !aligned4(norm)) return GBLA_ERR_INVALID_ARG;
   const AdamCtx c{static_cast<cudaStream_t>(stream)};
-  double* part = at<double>(ws, kAdamScalarBytes);
-  return adam_cap(tensors, n_tensors) == kAdamFew ? run_grad_norm<kAdamFew>(tensors, n_tensors, norm, part, c)
-                                                  : run_grad_norm<kAdamMany>(tensors, n_tensors, norm, part, c);
+  return adam_cap(tensors, n_tensors) == kAdamFew ? run_grad_norm<kAdamFew>(tensors, n_tensors, norm, ws, c)
+                                                  : run_grad_norm<kAdamMany>(tensors, n_tensors, norm, ws, c);
 }
 
 gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors, const gbla_adamw_config* config,
@@ -1177,9 +1179,9 @@ gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors, con
       !in(g.max_norm, 0., 1e30) || (g.max_norm > 0. && !norm))
     return GBLA_ERR_INVALID_ARG;
   const AdamCtx c{static_cast<cudaStream_t>(stream)};
-  AdamScalars* s = at<AdamScalars>(ws, 0);
+  AdamScalars* s = at<AdamScalars>(ws, kAdamScalars);
   AdamStep a{g.lr, g.beta1, g.beta2, g.eps, g.max_norm, std::log(g.beta1), std::log(g.beta2), g.seed};  // beta = 0: -inf
-  GBLA_CHECK(launch_adamw_begin(a, step, norm, s, c.st), "adamw begin");
+  GBLA_CHECK(launch_adamw_begin(a, step, norm, s, at<int>(ws, 0), c.st), "adamw begin");
   return adam_cap(tensors, n_tensors) == kAdamFew ? run_adamw<kAdamFew>(tensors, n_tensors, g.lr, s, c)
                                                   : run_adamw<kAdamMany>(tensors, n_tensors, g.lr, s, c);
 }

@@ -299,13 +299,14 @@ cudaError_t launch_decay_scan(const DecayArgs& a, int n_seq, cudaStream_t st);
 cudaError_t launch_decay_out(const DecayArgs& a, int n_chunks, cudaStream_t st);
 constexpr int kDecayChunk = 128;  // rows per chunk of the decay core
 
-// The step's scalars into *s, the step count moved on.
-cudaError_t launch_adamw_begin(const AdamStep& c, int64_t* step, const float* norm, AdamScalars* s, cudaStream_t st);
+// The step's scalars into *s, the step count moved on; clears *err.
+cudaError_t launch_adamw_begin(const AdamStep& c, int64_t* step, const float* norm, AdamScalars* s, int* err, cudaStream_t st);
 template <int N> cudaError_t launch_adamw(const AdamTable<N>& t, const AdamScalars* s, cudaStream_t st);
 // Sums of squares of the table's gradients: one fp64 partial for each of the launch's adamw_ctas(units) CTAs.
 int adamw_ctas(int64_t units);
 template <int N> cudaError_t launch_sumsq(const AdamTable<N>& t, double* part, cudaStream_t st);
-cudaError_t launch_norm(const double* part, int n, float* norm, cudaStream_t st);
+// The root of the sum of n partials into *norm; clears *err.
+cudaError_t launch_norm(const double* part, int n, float* norm, int* err, cudaStream_t st);
 
 // Checks the sequence data (error word *err) and marks the rows that begin a packed sequence.
 // Also forms a.kd and clears `words` words and the tile counter.

@@ -321,7 +321,8 @@ typedef struct {
 } gbla_adamw_config;
 
 /* Bytes of workspace that gbla_grad_norm and gbla_adamw_step need for these
- * tensors (a host array; 0 on an argument error). */
+ * tensors (a host array; 0 on an argument error).  Both leave its error word
+ * at 0: gbla_check_device_status() reports GBLA_OK. */
 size_t gbla_adamw_workspace_size(const gbla_adamw_tensor* tensors, int n_tensors);
 
 /* The global 2-norm of the tensors' gradients into norm (fp32, device; one

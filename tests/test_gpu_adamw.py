@@ -520,3 +520,18 @@ def test_norm_of_large_gradients_whose_squares_are_finite():
         assert abs(float(norm) - w) <= 1.01 * E * w  # one rounding
         gbla.gbla_adamw_step(plan, LR, norm=norm, max_norm=1.0)
         assert int(st["step"]) == 1
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_good_call_reports_ok(bits):
+    P, G, st = make([300, 5000], bits=bits, seed=56)
+    plan = gbla.gbla_adamw_plan(P, G, st)
+    plan.ws.fill_(255)
+    norm = gbla.gbla_grad_norm(plan)
+    assert gbla.gbla_check_device_status(plan.ws) == gbla.GBLA_OK
+    plan.ws.fill_(255)
+    gbla.gbla_adamw_step(plan, LR, norm=norm, max_norm=0.5)
+    assert gbla.gbla_check_device_status(plan.ws) == gbla.GBLA_OK
+    G[0][7] = float("nan")
+    gbla.gbla_adamw_step(plan, LR, norm=gbla.gbla_grad_norm(plan))  # skipped: no error either
+    assert gbla.gbla_check_device_status(plan.ws) == gbla.GBLA_OK
