@@ -540,23 +540,28 @@ gbla_status adam_check(const gbla_adamw_tensor* t, int n, bool norm_only, void* 
   return GBLA_OK;
 }
 
-// fn(table) for each launch's table.  The tensors without values are left out.
+// fn(table) for each launch's table of at most N tensors.  The tensors without values are left out; norm_only: of each grad,
+// grad_dtype and n alone.
 template <int N, typename F>
-gbla_status adam_tables(const gbla_adamw_tensor* t, int n, double lr, F&& fn) {
+gbla_status adam_tables(const gbla_adamw_tensor* t, int n, bool norm_only, double lr, F&& fn) {
   AdamTable<N> tab;
   tab.n = tab.units = 0;
   int64_t place = 0;
   for (int k = 0; k < n; ++k) {
     if (t[k].n > 0) {
       AdamTensor& o = tab.t[tab.n++];
-      o.param = t[k].param; o.master = t[k].master; o.grad = t[k].grad; o.m = t[k].m; o.v = t[k].v;
-      o.ms = t[k].m_scale; o.vs = t[k].v_scale;
+      o = AdamTensor{};
+      o.grad = t[k].grad; o.gb = t[k].grad_dtype == GBLA_BF16;
       o.n = t[k].n; o.place = place; o.first = tab.units;
-      o.keep = (float)(1. - lr * t[k].weight_decay);
-      o.pb = t[k].param_dtype == GBLA_BF16; o.gb = t[k].grad_dtype == GBLA_BF16;
-      uintptr_t bits = 0;
-      for (const void* q : {(const void*)t[k].param, (const void*)t[k].master, t[k].grad, (const void*)t[k].m, (const void*)t[k].v})
-        bits |= reinterpret_cast<uintptr_t>(q);
+      uintptr_t bits = reinterpret_cast<uintptr_t>(o.grad);
+      if (!norm_only) {
+        o.param = t[k].param; o.master = t[k].master; o.m = t[k].m; o.v = t[k].v;
+        o.ms = t[k].m_scale; o.vs = t[k].v_scale;
+        o.keep = (float)(1. - lr * t[k].weight_decay);
+        o.pb = t[k].param_dtype == GBLA_BF16;
+        for (const void* q : {(const void*)o.param, (const void*)o.master, (const void*)o.m, (const void*)o.v})
+          bits |= reinterpret_cast<uintptr_t>(q);
+      }
       o.vec = bits % 16 == 0;
       tab.units += (int)((t[k].n + kAdamUnit - 1) / kAdamUnit);
       place += (t[k].n + kAdamBlock - 1) / kAdamBlock * kAdamBlock;
@@ -576,7 +581,7 @@ template <int N>
 gbla_status run_grad_norm(const gbla_adamw_tensor* t, int n, float* norm, void* ws, AdamCtx c) {
   double* part = at<double>(ws, kAdamParts);
   int parts = 0;
-  const gbla_status r = adam_tables<N>(t, n, 0., [&](const AdamTable<N>& tab) {
+  const gbla_status r = adam_tables<N>(t, n, true, 0., [&](const AdamTable<N>& tab) {
     GBLA_CHECK(launch_sumsq<N>(tab, part + parts, c.st), "grad sumsq");
     parts += adamw_ctas(tab.units);
     return GBLA_OK;
@@ -588,7 +593,7 @@ gbla_status run_grad_norm(const gbla_adamw_tensor* t, int n, float* norm, void* 
 
 template <int N>
 gbla_status run_adamw(const gbla_adamw_tensor* t, int n, double lr, const AdamScalars* s, AdamCtx c) {
-  return adam_tables<N>(t, n, lr, [&](const AdamTable<N>& tab) {
+  return adam_tables<N>(t, n, false, lr, [&](const AdamTable<N>& tab) {
     GBLA_CHECK(launch_adamw<N>(tab, s, c.st), "adamw");
     return GBLA_OK;
   });

@@ -535,3 +535,20 @@ def test_a_good_call_reports_ok(bits):
     G[0][7] = float("nan")
     gbla.gbla_adamw_step(plan, LR, norm=gbla.gbla_grad_norm(plan))  # skipped: no error either
     assert gbla.gbla_check_device_status(plan.ws) == gbla.GBLA_OK
+
+
+def test_norm_takes_no_other_field():
+    """Whatever the other fields hold (addresses that are not even aligned, a NaN, no type): the same bits."""
+    g = torch.randn(100003, device="cuda")
+    norms = torch.zeros(2, device="cuda")
+    for other in (0, 1):
+        t = (gbla.AdamWTensor * 1)()
+        t[0].grad, t[0].n, t[0].grad_dtype = g.data_ptr(), g.numel(), gbla.GBLA_F32
+        if other:
+            t[0].param, t[0].master, t[0].m, t[0].v, t[0].m_scale, t[0].v_scale = range(1, 13, 2)
+            t[0].param_dtype, t[0].weight_decay = 9, float("nan")
+        ws = torch.empty(gbla.lib().gbla_adamw_workspace_size(t, 1), dtype=torch.uint8, device="cuda")
+        assert gbla.lib().gbla_grad_norm(t, 1, norms[other:].data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+    assert norms[0] == norms[1]
+    w = float(g.double().norm())
+    assert abs(float(norms[0]) - w) <= 1.01 * E * w
