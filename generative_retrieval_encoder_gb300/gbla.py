@@ -431,7 +431,8 @@ def gbla_adamw_state(params, bits: int = 32, master: bool | None = None) -> dict
 
 
 class AdamWPlan:
-    """Which tensors an AdamW step updates, by which gradients and states (gbla_adamw_plan); it keeps them alive."""
+    """Which tensors an AdamW step updates, by which gradients and states (gbla_adamw_plan); it keeps them alive, also where
+    the caller puts others in their place (which another plan is needed for)."""
 
     def __init__(self, params, grads, state):
         names, P = _named(params)
@@ -440,9 +441,9 @@ class AdamWPlan:
         if self.step.dtype != torch.int64 or self.step.numel() != 1 or not self.step.is_cuda:
             raise ValueError(f"step: want one int64 on a CUDA device, got {self.step.dtype} on {self.step.device}")
         self.sizes = [p.numel() for p in P]
-        self._keep, self._decay = [P, state], None
         none = [None] * self.n
         M, V, MS, VS, MA = (list(state.get(k) or none) for k in ("m", "v", "m_scale", "v_scale", "master"))
+        self._keep, self._decay = [P, M, V, MS, VS, MA], None  # the lists' own copies: the caller's may change
         for k, t in (("m", M), ("v", V), ("m_scale", MS), ("v_scale", VS), ("master", MA)):
             if len(t) != self.n:
                 raise ValueError(f"{k}: {len(t)} tensors for {self.n} parameters")

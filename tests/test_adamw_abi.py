@@ -67,3 +67,52 @@ def test_binding_refuses_host_tensors(L):
         gbla.gbla_adamw_plan(p, p, {"step": torch.zeros(1, dtype=torch.int64), "m": p, "v": p})
     with pytest.raises(ValueError):
         gbla.gbla_adamw_state(p, bits=16)
+
+
+class Fake:
+    """What the binding asks of a tensor, with an address that nothing reads."""
+    is_cuda, made = True, 0
+
+    def __init__(self, n, dtype):
+        import torch
+        Fake.made += 1
+        self.n, self.dtype, self.device, self.shape, self.at = n, dtype, torch.device("cpu"), (n,), FAKE + (Fake.made << 16)
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+
+def fakes(sizes, dtype):
+    return [Fake(n, dtype) for n in sizes]
+
+
+def test_plan_keeps_its_tensors_alive(L):
+    """Also where the caller puts others in the state's lists afterwards."""
+    import gc
+    import torch
+    import weakref
+    sizes, f32 = [100, 300], torch.float32
+    P, G = fakes(sizes, torch.bfloat16), fakes(sizes, f32)
+    st = {"step": Fake(1, torch.int64), "m": fakes(sizes, torch.float8_e4m3fn), "v": fakes(sizes, torch.float8_e4m3fn),
+          "m_scale": fakes([1, 2], f32), "v_scale": fakes([1, 2], f32), "master": fakes(sizes, f32)}
+    refs = [weakref.ref(t) for t in P + G + [st["step"]] + st["m"] + st["v"] + st["m_scale"] + st["v_scale"] + st["master"]]
+    plan = gbla.gbla_adamw_plan(P, G, st)
+    for k in ("m", "v", "m_scale", "v_scale", "master"):
+        st[k][0] = None
+    st.clear()
+    P.clear()
+    G.clear()
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del plan
+    gc.collect()
+    assert not any(r() is not None for r in refs)
