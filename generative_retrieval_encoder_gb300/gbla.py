@@ -497,11 +497,17 @@ class AdamWPlan:
 
     def set_grads(self, grads):
         """Other gradient tensors for the same parameters: a sequence in their order, or a dict by their names (with or
-        without the leading d of gbla_backward's)."""
+        without the leading d of gbla_backward's: d<name> first, unless another parameter has that name).  A captured call
+        keeps to those of its capture, which are the caller's to keep."""
         if isinstance(grads, dict):
             if self.names is None:
                 raise ValueError("grads by name need params by name")
-            G = [grads["d" + k] if "d" + k in grads else grads[k] for k in self.names]
+            G, taken = [], set(self.names)
+            for k in self.names:
+                at = "d" + k if "d" + k in grads and "d" + k not in taken else k
+                if at not in grads:
+                    raise ValueError(f"no gradient of {k}")
+                G.append(grads[at])
         else:
             G = list(grads)
         if len(G) != self.n:

@@ -116,3 +116,18 @@ def test_plan_keeps_its_tensors_alive(L):
     del plan
     gc.collect()
     assert not any(r() is not None for r in refs)
+
+
+def test_gradients_by_name(L):
+    """The name d<name> is a parameter's gradient unless another parameter has that name."""
+    import torch
+    f32 = torch.float32
+    P = {"w": Fake(10, f32), "dw": Fake(10, f32), "lam": Fake(10, f32)}
+    state = {"step": Fake(1, torch.int64), "m": fakes([10] * 3, f32), "v": fakes([10] * 3, f32)}
+    G = {k: Fake(10, f32) for k in ("w", "dw", "dlam")}
+    plan = gbla.gbla_adamw_plan(P, G, state)
+    assert [t.grad for t in plan.tensors] == [G[k].at for k in ("w", "dw", "dlam")]
+    for bad in ({k: G["w"] for k in ("dw", "ddw", "dlam")}, {k: G["w"] for k in ("w", "dw")}):
+        with pytest.raises(ValueError, match="gradient of"):
+            plan.set_grads(bad)
+    assert [t.grad for t in plan.tensors] == [G[k].at for k in ("w", "dw", "dlam")]
