@@ -488,6 +488,28 @@ gbla_status glr_prepare(GlrCtx& c) {
   return GBLA_OK;
 }
 
+// Dense rows without saved states: a thread for two channels of a sequence, row by row (true), or tiles.  The first takes a
+// row's latency (0.28 us where the inputs are still in L2, 0.69 from memory: 0.55 for calls that read 8 MB at most, which may be
+// either) or its bytes at 4.7 TB/s, the tiles 10 us and their values (padded to 64 channels) at a rate that goes by the cut, a million
+// a us: 0.56 for slots (at most 6.6 TB/s), as one stream 0.33 where slots begin at tiles' borders and 0.22 elsewhere, 0.1 where rows
+// are not copied by TMA.  Measured on the device, us of this one against the tiles', d = 512, bf16: B = 16, L = 16 (in L2) 5.6 / 10.2,
+// L = 40 26 / 10; B = 128, L = 32 23 / 12; B = 300, L = 40 31 / 34, L = 128 93 / 66, L = 2048 1414 / 556; B = 512, L = 64 50 / 60,
+// L = 300 226 / 442, L = 1024 756 / 470; B = 4096, L = 64 228 / 370; fp32: B = 150, L = 1024 679 / 198, B = 1024, L = 100 178 / 389;
+// d = 33: B = 300, L = 200 135 / 39, B = 4800 159 / 463.  Of 518 shapes nine lose more than 1.3 times by it, 1.6 at most, all but
+// one by less than 6 us.
+bool glr_step_is_faster(const GlrCtx& c) {
+  const GlrPlan& p = c.p;
+  const GlrArgs& a = c.a;
+  const size_t es = p.f32 ? 4 : 2;
+  uintptr_t bits = (uintptr_t)(a.ld * es) | (uintptr_t)(p.d * es);
+  for (const void* q : {a.x, a.r, a.i}) bits |= reinterpret_cast<uintptr_t>(q);
+  const double row = 4. * es * p.n_seq * p.d, latency = 0.75 * row * p.L <= 8e6 ? 0.55 : 0.69;
+  const double rate = bits % 16 ? 0.1e6
+                      : p.cut == GLR_SLOTS ? std::min(0.56e6, 6.6e6 / (4. * es))
+                      : kGlrRowsFwd % p.L == 0 ? 0.33e6 : 0.22e6;
+  return 1.2 + p.L * std::max(latency, row / 4.7e6) <= 10. + (double)p.n_seq * p.L * glr_dp(p) / rate;
+}
+
 // ------------------------------------------------------------ AdamW
 // Arguments of one tensor; norm_only: what gbla_grad_norm reads.
 bool adam_tensor_ok(const gbla_adamw_tensor& t, bool norm_only) {
@@ -1118,11 +1140,7 @@ gbla_status glr_forward(const gbla_shape* shape, const void* x, const void* r, c
   if (!y || reinterpret_cast<uintptr_t>(y) % es || !aligned4(hT)) return GBLA_ERR_INVALID_ARG;
   if (saved && reinterpret_cast<uintptr_t>(saved) % kAlign) return GBLA_ERR_INVALID_ARG;
   c.a.y = y; c.a.hT = hT; c.a.saved = static_cast<float*>(saved);
-  // A thread for two channels of a sequence, or tiles: a row takes the first 0.28 us of latency or its bytes at 4.1 TB/s, the
-  // tiles 10 us and their bytes at the same rate (measured at d = 512: B = 16, L = 16 / 32 / 64 rows 5.7 / 9.9 / 18.2 us against
-  // 10.7; B = 512, L = 32 15.9 against 31.2; B = 4096, L = 64 227 against 378).
-  const double row_us = 4. * es * c.p.n_seq * c.p.d / 4.1e6;
-  if (c.p.mode == SEQ_DENSE && !saved && c.p.L * (0.28 - row_us) <= 10.) {
+  if (c.p.mode == SEQ_DENSE && !saved && glr_step_is_faster(c)) {
     GBLA_CHECK(launch_glr_step(c.a, c.p.f32, c.err, c.st), "glr step");
     return GBLA_OK;
   }

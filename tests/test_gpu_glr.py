@@ -475,3 +475,33 @@ def test_glr_a_nonfinite_state_lasts_to_its_sequence_end(kw, lam, reverse):
     assert torch.equal(g["dh0"][okT], g0["dh0"][okT])
     rest = [ch for ch in range(c.d) if ch not in last]
     assert torch.equal(g["dlam"][rest], g0["dlam"][rest])
+
+
+@pytest.mark.parametrize("dtype,B,L,d,step", [("bf16", 16, 1, 512, True), ("bf16", 16, 8, 512, True), ("f32", 16, 64, 512, False),
+                                              ("bf16", 300, 2048, 512, False), ("f32", 150, 1024, 512, False), ("bf16", 512, 600, 512, False),
+                                              ("bf16", 1024, 40, 512, True), ("f32", 600, 37, 500, True), ("f32", 4800, 20, 33, True)])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_glr_dense_inference_by_the_faster_kernel(dtype, B, L, d, step, reverse):
+    """Rows one after the other where those are few or the sequences many, tiles elsewhere (each of these sides is at least 1.3
+    times the other's time away from the choice); the first, middle and last sequences against the formulas."""
+    gen = torch.Generator("cuda").manual_seed(91)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    x, r, i = (torch.randn(B * L, d, generator=gen, device="cuda").to(dt) for _ in range(3))
+    h0 = torch.randn(B, d, generator=gen, device="cuda")
+    lam = torch.linspace(-5, 0, d, device="cuda")
+    sh = gbla.glr_shape(B, L, d, dtype=dtype)
+    gbla.gbla_profiling_read()
+    gbla.gbla_profiling_enable(True)
+    try:
+        y, hT, _ = gbla.glr_forward(sh, x, r, i, lam, reverse=reverse, h0=h0, hT=True)
+        names = [n for n, _ in gbla.gbla_profiling_read()]
+    finally:
+        gbla.gbla_profiling_enable(False)
+    assert ("glr step" in names) == step and ("glr fwd" in names) != step, names
+    assert torch.isfinite(y).all() and torch.isfinite(hT).all()
+    cols = slice(0, min(d, 64))
+    f = lambda t: t[..., cols].double().cpu().numpy()  # noqa: E731
+    for b in sorted({0, B // 2, B - 1}):
+        at = slice(b * L, b * L + L)
+        check({"y": y[at, cols], "hT": hT[b:b + 1, cols]},
+              reference(f(x[at]), f(r[at]), f(i[at]), f(lam), 8.0, [0], [L], reverse, f(h0[b:b + 1]), io=dtype))
