@@ -372,11 +372,20 @@ gbla_status make_glr_plan(const gbla_shape* s, GlrPlan& p) {
   p.mode = s->cu_seqlens ? SEQ_VARLEN : (s->seq_lens ? SEQ_PADDED : SEQ_DENSE);
   p.n_seq = s->cu_seqlens ? s->num_seqs : s->B;
   if ((long long)p.n_seq * p.d > (1LL << 38) || p.n_seq > (1 << 30)) return GBLA_ERR_UNSUPPORTED;
-  // Packed sequences are cut one by one where they are long on the mean and the call is several rounds of tiles (64 of
-  // 64 .. 16384 rows, d = 1024: 361 us against 625 in one stream).
-  const long long rounds = T / kGlrRowsFwd * cdiv(p.d, 64) / (2LL * sm_count());
-  p.cut = p.mode != SEQ_VARLEN ? (p.L >= kGlrSlot ? GLR_SLOTS : GLR_STREAM)
-          : T / p.n_seq >= kGlrSlot && rounds >= 3 && p.n_seq > 1 && T <= (8LL << 20) ? GLR_SEQS : GLR_STREAM;
+  // Slots, or packed sequences, one by one, or all rows as one stream, whose tiles of one round are neighbours and wait for one
+  // another.  The stream is the faster one in few rounds, and where sequences fill too little of their tiles.  Measured, us
+  // forward / backward as a stream against one by one, d = 512, bf16, rounds of tiles in brackets:
+  //   dense   L = 64 [6] 65 / 106, 95 / 99;  L = 65 [6] 97 / 194, 95 / 179;  L = 100 [0] 22 / 34, 24 / 36, [6] 95 / 179, 69 / 122,
+  //           [53] 1054 / 2228, 413 / 763;  L = 256 [6] 83 / 175, 52 / 99, [53] 908 / 2928, 280 / 544;  L = 512 [0] 19 / 35, 19 / 35
+  //   padded  L = 200 [13] 176 / 371, 124 / 239
+  //   packed  of 16 .. 128 rows (53 on the mean) [6] 104 / 192, 122 / 157, [13, d = 1024] 235 / 398, 214 / 274, [107] 2426 / 4755, 1541 / 1992;
+  //           of 1 .. 64 (15) [107] 2691 / 6239, 5293 / 5508;  of 64 .. 256 (137) [1] 32 / 54, 42 / 61, [6] 87 / 176, 89 / 141,
+  //           [26] 421 / 808, 257 / 421;  of 512 .. 2048 [3, d = 1024] 42 / 77, 48 / 77, [6] 69 / 132, 65 / 106, [27] 254 / 568, 171 / 289
+  const long long rounds = T / kGlrRowsFwd * cdiv(p.d, 64) / (2LL * sm_count()), mean = T / p.n_seq;
+  if (p.mode != SEQ_VARLEN)
+    p.cut = p.L >= kGlrSlot || (p.L > kGlrRowsBwd && rounds >= 3) ? GLR_SLOTS : GLR_STREAM;
+  else  // (the order of the chunks is made for calls of up to 8 M rows)
+    p.cut = p.n_seq > 1 && T <= (8LL << 20) && ((mean >= 128 && rounds >= 6) || (mean >= 48 && rounds >= 13)) ? GLR_SEQS : GLR_STREAM;
   p.pieces = p.cut == GLR_SLOTS ? (int64_t)p.n_seq * cdiv(p.L, kGlrPiece)
              : p.cut == GLR_SEQS ? p.T / kGlrPiece + p.n_seq : cdiv(p.T, kGlrPiece);
   if (((long long)p.T / kGlrRowsBwd + p.n_seq + 1) * cdiv(p.d, 64) > 0x7fffffffLL) return GBLA_ERR_UNSUPPORTED;  // tiles are counted in 31 bits
@@ -490,13 +499,13 @@ gbla_status glr_prepare(GlrCtx& c) {
 
 // Dense rows without saved states: a thread for two channels of a sequence, row by row (true), or tiles.  The first takes a
 // row's latency (0.28 us where the inputs are still in L2, 0.69 from memory: 0.55 for calls that read 8 MB at most, which may be
-// either) or its bytes at 4.7 TB/s, the tiles 10 us and their values (padded to 64 channels) at a rate that goes by the cut, a million
-// a us: 0.56 for slots (at most 6.6 TB/s), as one stream 0.33 where slots begin at tiles' borders and 0.22 elsewhere, 0.1 where rows
-// are not copied by TMA.  Measured on the device, us of this one against the tiles', d = 512, bf16: B = 16, L = 16 (in L2) 5.6 / 10.2,
-// L = 40 26 / 10; B = 128, L = 32 23 / 12; B = 300, L = 40 31 / 34, L = 128 93 / 66, L = 2048 1414 / 556; B = 512, L = 64 50 / 60,
-// L = 300 226 / 442, L = 1024 756 / 470; B = 4096, L = 64 228 / 370; fp32: B = 150, L = 1024 679 / 198, B = 1024, L = 100 178 / 389;
-// d = 33: B = 300, L = 200 135 / 39, B = 4800 159 / 463.  Of 518 shapes nine lose more than 1.3 times by it, 1.6 at most, all but
-// one by less than 6 us.
+// either) or its bytes at 4.7 TB/s, the tiles 10 us and their values (slots padded to tiles, channels to 64) at a rate that goes by
+// the cut, a million a us: 0.53 for slots (at most 6.6 TB/s), as one stream 0.33 where slots begin at tiles' borders and 0.3
+// elsewhere, 0.1 where rows are not copied by TMA.  Measured on the device, us of this one against the tiles', d = 512, bf16:
+// B = 16, L = 16 (in L2) 5.6 / 10.2, L = 40 26 / 10; B = 128, L = 32 23 / 12; B = 300, L = 40 32 / 34, L = 128 95 / 64, L = 2048
+// 1453 / 555; B = 512, L = 64 52 / 60, L = 256 198 / 154; B = 1024, L = 300 283 / 463; B = 4096, L = 64 231 / 373, L = 256 899 / 1131;
+// fp32: B = 150, L = 1024 679 / 198, B = 1024, L = 64 117 / 124, L = 256 455 / 362; d = 33: B = 300, L = 200 137 / 39, B = 4800
+// 159 / 463.  Of 518 shapes five lose more than 1.3 times by it, 1.6 at most, none of them more than 6 us.
 bool glr_step_is_faster(const GlrCtx& c) {
   const GlrPlan& p = c.p;
   const GlrArgs& a = c.a;
@@ -505,9 +514,10 @@ bool glr_step_is_faster(const GlrCtx& c) {
   for (const void* q : {a.x, a.r, a.i}) bits |= reinterpret_cast<uintptr_t>(q);
   const double row = 4. * es * p.n_seq * p.d, latency = 0.75 * row * p.L <= 8e6 ? 0.55 : 0.69;
   const double rate = bits % 16 ? 0.1e6
-                      : p.cut == GLR_SLOTS ? std::min(0.56e6, 6.6e6 / (4. * es))
-                      : kGlrRowsFwd % p.L == 0 ? 0.33e6 : 0.22e6;
-  return 1.2 + p.L * std::max(latency, row / 4.7e6) <= 10. + (double)p.n_seq * p.L * glr_dp(p) / rate;
+                      : p.cut == GLR_SLOTS ? std::min(0.53e6, 6.6e6 / (4. * es))
+                      : kGlrRowsFwd % p.L == 0 ? 0.33e6 : 0.3e6;
+  const double rows = (double)p.n_seq * (p.cut == GLR_SLOTS ? (double)c.t.per_seq * kGlrRowsFwd : p.L);
+  return 1.2 + p.L * std::max(latency, row / 4.7e6) <= 10. + rows * glr_dp(p) / rate;
 }
 
 // ------------------------------------------------------------ AdamW

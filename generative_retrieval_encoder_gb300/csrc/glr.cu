@@ -972,8 +972,9 @@ __global__ void __launch_bounds__(1024) k_glr_levels(int* level, int n, int* tot
 }
 
 // The chunks in the order of their levels (within one in any order: results do not depend on it).  In this order the next chunk
-// of a sequence comes many tiles later, when its predecessor's words are long there: packed sequences of d = 1024 take
-// 361 us forward against 625 in one stream, where all tiles at work are neighbours, and 899 against 1825 trained.
+// of a sequence comes many tiles later, when its predecessor's words are long there: 64 packed sequences of d = 1024 take 341
+// us forward (64 .. 16384 rows) against 505 in one stream, where all tiles at work are neighbours, and 471 backward (64 .. 8192)
+// against 923.
 __global__ void __launch_bounds__(256) k_glr_place(const GlrArgs a, const GlrTiles tl, int* level) {
   pdl_enter();
   if (*a.err) return;

@@ -178,7 +178,7 @@ struct DecayArgs {
 // The state on entry to every kGlrPiece rows (of a slot or sequence, or of all
 // rows) is saved for the backward.
 enum GlrCut { GLR_STREAM = 0, GLR_SLOTS = 1, GLR_SEQS = 2 };
-constexpr int kGlrSlot = 512;                       // rows of a slot, and of a sequence on the mean, from which it is cut by itself
+constexpr int kGlrSlot = 512;                       // rows of a slot from which it is cut by itself in calls of any size
 constexpr int kGlrPiece = 8;
 constexpr int kGlrRowsFwd = 128, kGlrRowsBwd = 64;  // rows of a tile
 struct GlrDiv { uint32_t m; int s; };               // division by an invariant (quotient() in glr.cu)

@@ -96,3 +96,17 @@ def test_checks_follow_a_changed_shape(L):
     with pytest.raises(ValueError, match="64, 8"):
         gbla._glr_inputs(sh, Fake(32, 8), Fake(32, 8), Fake(32, 8), None, None)
     assert not seen
+
+
+def test_which_calls_are_cut_one_by_one(L):
+    """By the size of what a forward saves: a state per 8 rows of each slot (or sequence), or of all rows as one stream."""
+    def pieces(d, B, rows, n=0):
+        s = gbla.glr_shape(B, rows, d)
+        if n:
+            s.cu_seqlens, s.num_seqs = 256, n
+        return gbla.glr_saved_size(s) // (4 * d)
+    for B, rows, one in ((2621, 100, True), (504, 65, True), (40, 100, False), (4096, 63, False), (2, 513, True), (8, 511, False), (64, 511, True)):
+        assert pieces(512, B, rows) == (B * -(-rows // 8) if one else -(-B * rows // 8)), (B, rows)
+    for d, T, n, one in ((512, 131076, 929, True), (512, 524311, 9714, True), (512, 524291, 35195, False), (512, 8266, 56, False),
+                         (512, 32771, 600, False), (1024, 32770, 600, True), (512, 33158, 27, True), (1024, 8653, 8, False), (1024, 262144, 1, False)):
+        assert pieces(d, 1, T, n) == (T // 8 + n if one else -(-T // 8)), (d, T, n)

@@ -433,7 +433,7 @@ def _nonfinite(t):
 @pytest.mark.parametrize("reverse", [False, True])
 @pytest.mark.parametrize("lam", [None, 0.0, 30.0], ids=["slow", "fast", "instant"])
 @pytest.mark.parametrize("kw", [dict(dtype="f32", d=40, L=9001, B=2), dict(dtype="bf16", d=40, L=9001, B=2, seq_lens=[9001, 8700]),
-                                dict(dtype="bf16", d=1032, lengths=[700, 9001, 600]), dict(dtype="f32", d=40, lengths=[9001] + [1, 5, 300] * 9)],
+                                dict(dtype="bf16", d=2056, lengths=[700, 9001, 600]), dict(dtype="f32", d=40, lengths=[9001] + [1, 5, 300] * 9)],
                          ids=["dense", "padded", "seqs", "stream"])
 def test_glr_a_nonfinite_state_lasts_to_its_sequence_end(kw, lam, reverse):
     """A NaN or an infinity in h0, x or a gate, in dhT or dy, reaches every later row of its channel, however small the product of
@@ -505,3 +505,81 @@ def test_glr_dense_inference_by_the_faster_kernel(dtype, B, L, d, step, reverse)
         at = slice(b * L, b * L + L)
         check({"y": y[at, cols], "hT": hT[b:b + 1, cols]},
               reference(f(x[at]), f(r[at]), f(i[at]), f(lam), 8.0, [0], [L], reverse, f(h0[b:b + 1]), io=dtype))
+
+
+def _spread(n, lo, hi, seed):
+    """n lengths from lo to hi, odd ones among them, and an empty sequence at either end and in the middle."""
+    v = np.random.default_rng(seed).integers(lo, hi + 1, n).tolist()
+    v[0] = v[n // 2] = v[-1] = 0
+    return v
+
+
+@pytest.mark.parametrize("kw", [dict(dtype="bf16", d=1030, L=100, B=71), dict(dtype="f32", d=1028, L=65, B=110, reverse=True, packed=True),
+                                dict(dtype="bf16", d=1032, L=257, B=30, reverse=True), dict(dtype="f32", d=1032, L=511, B=15),
+                                dict(dtype="bf16", d=1032, L=200, B=40, seq_lens=_spread(40, 1, 200, 1)),
+                                dict(dtype="f32", d=1032, L=129, B=60, seq_lens=_spread(60, 0, 129, 2), reverse=True),
+                                dict(dtype="bf16", d=2040, lengths=_spread(60, 40, 300, 3)),
+                                dict(dtype="f32", d=2040, lengths=_spread(20, 100, 900, 4), reverse=True),
+                                dict(dtype="bf16", d=4104, lengths=_spread(140, 1, 128, 5), reverse=True)], ids=_id)
+def test_glr_short_sequences_one_by_one(kw):
+    """Calls of several rounds of tiles: slots and packed sequences from some 50 rows on are cut by themselves."""
+    c = Case(seed=92, **kw)
+    h = c.h0.clone()
+    y, hT, saved = c.forward(hT=True, saved=True)
+    g = c.backward(saved)
+    names = {"y": y, "hT": hT, **g}
+    y2, h2, _ = gbla.glr_forward(c.shape, c.x, c.r, c.i, c.lam, reverse=c.reverse, h0=h, hT=h)  # in place, nothing saved
+    if "B" not in kw or "seq_lens" in kw:  # (dense: perhaps by the row-by-row kernel)
+        assert torch.equal(y2, y) and torch.equal(h2, hT)
+    cols = [0, 1, 63, 64, 65, c.d // 2, c.d - 3, c.d - 2, c.d - 1]  # (columns are independent)
+    f = lambda t: t[..., cols].double().cpu().numpy()  # noqa: E731
+    want = reference(f(c.x), f(c.r), f(c.i), f(c.lam), c.c, c.starts, c.lens, c.reverse, f(c.h0), f(c.dy), f(c.dhT), c.dtype)
+    check({n: t[..., cols] for n, t in names.items()}, want)
+    check({"y": y2[:, cols], "hT": h2[:, cols]}, want)
+    pad = torch.ones(c.T, dtype=torch.bool)
+    for a, n in zip(c.starts, c.lens):
+        pad[a:a + n] = False
+    for n in ("y", "dx", "dr", "di"):
+        assert torch.isfinite(names[n]).all() and (names[n][pad.cuda()] == 0).all(), n
+
+
+def test_glr_short_packed_sequences_follow_their_data():
+    """A captured call of packed sequences cut one by one, replayed with other lengths, bad ones in between: those write nothing."""
+    d, T, n = 2048, 8192, 24
+    gen = torch.Generator("cuda").manual_seed(93)
+    x, r, i, dy = (torch.randn(T, d, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    lam = torch.full((d,), -4.0, device="cuda")
+    h0 = torch.randn(n, d, generator=gen, device="cuda")
+    even = [T * k // n for k in range(n + 1)]
+    good = [even, [0] * n + [T], [0] + [T] * n, sorted([0, T] + np.random.default_rng(6).integers(0, T, n - 1).tolist())]
+    bad = [even[:5] + [even[7], even[6]] + even[7:], even[:-1] + [T - 1], [1] + even[1:], even[:3] + [1 << 30] + even[4:], even[:3] + [-7] + even[4:]]
+    cu = torch.tensor(even, dtype=torch.int32, device="cuda")
+    sh = gbla.glr_shape(1, T, d, cu_seqlens=cu)
+    ws = [gbla.workspace(sh, op) for op in (gbla.GBLA_OP_GLR_FORWARD, gbla.GBLA_OP_GLR_BACKWARD)]
+
+    def run(ws):
+        y, hT, saved = gbla.glr_forward(sh, x, r, i, lam, h0=h0, hT=True, saved=True, ws=ws[0])
+        return {"y": y, "hT": hT, **gbla.glr_backward(sh, x, r, i, lam, saved, dy, h0=h0, dhT=h0, ws=ws[1])}
+
+    gbla.gbla_profiling_read()
+    gbla.gbla_profiling_enable(True)
+    try:
+        run(ws)
+        assert [k for k, _ in gbla.gbla_profiling_read()].count("glr order") == 2
+    finally:
+        gbla.gbla_profiling_enable(False)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(ws)
+    for k in range(5):
+        cu.copy_(torch.tensor(bad[k], dtype=torch.int32))
+        for t in got.values():
+            t.fill_(3.0)
+        graph.replay()
+        assert all(gbla.gbla_check_device_status(w) == gbla.GBLA_ERR_DEVICE_CHECK for w in ws), k
+        assert all((t == 3).all() for t in got.values()), k
+        cu.copy_(torch.tensor(good[k % 4], dtype=torch.int32))
+        graph.replay()
+        assert all(gbla.gbla_check_device_status(w) == gbla.GBLA_OK for w in ws), k
+        want = run([None, None])
+        assert all(torch.equal(got[name], want[name]) for name in want), k
