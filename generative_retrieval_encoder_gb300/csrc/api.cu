@@ -408,9 +408,12 @@ GlrTiles glr_tiles(const GlrPlan& p, int rows) {
   t.per_seq = p.cut == GLR_SLOTS ? cdiv(p.L, rows) : 0;
   t.n_chunks = p.cut == GLR_SLOTS ? t.per_seq * p.n_seq : p.cut == GLR_SEQS ? p.T / rows + p.n_seq : cdiv(p.T, rows);
   // word c of a slot or sequence whose rows begin at r, the s-th: r / rows + s + c; groups and larger groups alike
+  // (none where no slot has a chunk behind one, a group, a larger group)
   const int s = p.cut == GLR_STREAM ? 1 : p.n_seq;
-  t.n_words = p.T / rows + s;
-  t.n_groups = p.T / (16 * rows) + s;
+  auto words = [&](int chunks) { return p.cut == GLR_SLOTS && t.per_seq <= chunks ? 0 : p.T / (chunks * rows) + s; };
+  t.n_words = words(1);
+  t.n_groups = words(16);
+  t.n_large = words(256);
   t.levels = p.cut == GLR_SEQS ? cdiv(p.T, rows) : 0;
   return t;
 }
@@ -427,7 +430,7 @@ GlrLayout glr_layout(const GlrPlan& p, int op) {
   l.zero_bytes = c.off;
   l.kd = c.take(glr_dp(p) * 4);
   if (p.cut == GLR_SEQS) l.order = c.take((size_t)t.n_chunks * 16);
-  l.n_words = ((size_t)t.n_words + t.n_groups + p.T / (256 * t.rows) + (p.cut == GLR_STREAM ? 1 : p.n_seq)) * glr_dp(p);
+  l.n_words = ((size_t)t.n_words + t.n_groups + t.n_large) * glr_dp(p);
   l.words = c.take(l.n_words * 8);
   if (op == GBLA_OP_GLR_BACKWARD) {
     l.n_part = (size_t)t.n_chunks * p.d;

@@ -187,7 +187,7 @@ struct GlrTiles {
   int rows;                  // of a chunk
   int per_seq;               // SLOTS: chunks of a slot
   int n_chunks;              // chunks of the call; SEQS: at most
-  int n_words, n_groups;     // words of chunks, and of groups, before those of larger groups
+  int n_words, n_groups, n_large;  // words of chunks, then of groups, then of larger groups
   int levels;                // SEQS: places in the order that a sequence's chunks are spread over
   GlrDiv by_cg, by_seq;      // by the groups of 64 channels, by the slots
   const int4* order;         // SEQS: {first row, rows, sequence, chunk} of each chunk in turn

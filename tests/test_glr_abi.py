@@ -110,3 +110,12 @@ def test_which_calls_are_cut_one_by_one(L):
     for d, T, n, one in ((512, 131076, 929, True), (512, 524311, 9714, True), (512, 524291, 35195, False), (512, 8266, 56, False),
                          (512, 32771, 600, False), (1024, 32770, 600, True), (512, 33158, 27, True), (1024, 8653, 8, False), (1024, 262144, 1, False)):
         assert pieces(d, 1, T, n) == (T // 8 + n if one else -(-T // 8)), (d, T, n)
+
+
+def test_workspace_of_short_slots(L):
+    """Slots of one tile exchange no words: the forward's workspace holds none, the backward's (smaller tiles) little."""
+    rows, d = 4096 * 100, 512
+    s = gbla.glr_shape(4096, 100, d)
+    assert gbla.gbla_workspace_size(s, gbla.GBLA_OP_GLR_FORWARD) < 1 << 16
+    # two chunks of 64 rows a slot: a word of 8 bytes and a partial sum of 4 for each and channel, one slot more in either
+    assert gbla.gbla_workspace_size(s, gbla.GBLA_OP_GLR_BACKWARD) < (rows // 64 + 2 * 4096) * d * 8 + 2 * 4097 * d * 4 + (1 << 16)
