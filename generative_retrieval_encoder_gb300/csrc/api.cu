@@ -540,16 +540,13 @@ bool adam_tensor_ok(const gbla_adamw_tensor& t, bool norm_only) {
   return ok(t.m, a) && ok(t.v, a) && t.weight_decay >= 0. && t.weight_decay <= 1e30;
 }
 
-// Units of all tensors, and the launches' tables of at most `cap` tensors with values each.
-int64_t adam_units(const gbla_adamw_tensor* t, int n, int64_t* most = nullptr) {
+// Units of all tensors.
+int64_t adam_units(const gbla_adamw_tensor* t, int n) {
   int64_t u = 0;
-  for (int k = 0; k < n; ++k) {
-    const int64_t mine = (t[k].n + kAdamUnit - 1) / kAdamUnit;
-    u += mine;
-    if (most) *most = std::max(*most, mine);
-  }
+  for (int k = 0; k < n; ++k) u += (t[k].n + kAdamUnit - 1) / kAdamUnit;
   return u;
 }
+// The size of the launches' tables of tensors with values.
 int adam_cap(const gbla_adamw_tensor* t, int n) {
   int live = 0;
   for (int k = 0; k < n; ++k) live += t[k].n > 0;

@@ -14,10 +14,11 @@
 // What a call cannot do without (bf16): forward 8 bytes a value, backward 14; and four special functions a value and
 // direction, which at 6.8 TB/s take half the special function units' time.  The scan runs along the rows, so the rows are
 // cut: tiles of 128 (forward) or 64 rows x 64 channels, whose effects on a state are composed across tiles while the rows'
-// values stay on the chip (scan_* below): every input is read once.  Measured (perf of the whole call, launches included):
-//   forward  B = 32, L = 2048, d = 512 (268 MB)   65 us, 4.2 TB/s;  B = 8, L = 32768 (1.07 GB)  255 us, 4.2 TB/s
-//            one sequence of 65536 rows (268 MB)  100 us, 2.7 TB/s; packed, d = 1024 (1.35 GB)  344 us, 3.9 TB/s
-//   forward and backward  B = 16, L = 8192 (1.48 GB)  424 us, 3.5 TB/s; packed, d = 1024 (2.67 GB)  735 us, 3.6 TB/s
+// values stay on the chip (scan_* below): every input is read once.  Measured (whole calls back to back, launches included):
+//   forward  B = 32, L = 2048, d = 512 (268 MB)   65 us, 4.1 TB/s (72 with L2 flushed before each);
+//            B = 8, L = 32768 (1.07 GB)  257 us, 4.2 TB/s
+//            one sequence of 65536 rows (268 MB)  98 us, 2.7 TB/s; packed, d = 1024 (1.35 GB)  350 us, 3.9 TB/s
+//   forward and backward  B = 16, L = 8192 (1.48 GB)  424 us, 3.5 TB/s; packed, d = 1024 (2.67 GB)  741 us, 3.6 TB/s
 // Without the waits between tiles (a copy that left them out) the forward takes 61, 200, 59 and 284 us, and without the
 // gates too 47, 162, 46 and 218: what is left above the copy is first the gates' instructions, then the tiles of one chain
 // that are worked on at the same time and so wait for one another, most where one sequence has few channels.
@@ -782,8 +783,9 @@ struct GlrSharedBwd {
 
 // Backward: one pass from each sequence's end, x, r, i and dy read once, dx, dr and di written once; the states before a
 // warp's rows come from the saved one, the w behind them as the forward's states do.  As the forward, with half the rows in a
-// tile and three CTAs an SM (80 registers; holding everything from the first pass took 128, two CTAs and spills: 541 against 426
-// us for both directions at B = 16, L = 8192).  Bound by instructions (81 a value, 50 % of the issue slots) and the waits
+// tile and three CTAs an SM: 80 registers, for which a thread spills 56 bytes (bf16 rows copied by TMA) to 148; holding everything
+// from the first pass took 128, two CTAs and spilled too: 541 against 426 us for both directions at B = 16, L = 8192.  In fp32 the
+// two stages of one CTA take an SM's shared memory.  Bound by instructions (81 a value, 50 % of the issue slots) and the waits
 // between tiles.  Every tile has two barriers between the first and the second pass, so what one tile leaves in
 // shared memory for them is read before the next one's is written.
 template <typename T, int LOAD>
