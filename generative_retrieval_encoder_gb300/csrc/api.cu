@@ -631,6 +631,113 @@ gbla_status run_adamw(const gbla_adamw_tensor* t, int n, double lr, const AdamSc
   });
 }
 
+// ------------------------------------------ token embedding, layer norm
+// The rows of a shape whose operator works token by token: padded slots matter, packed sequences do not.
+struct RowPlan { bool f32; int64_t rows; int d, L; const int32_t* lens; };
+gbla_status make_row_plan(const gbla_shape* s, RowPlan& p) {
+  if (!s) return GBLA_ERR_INVALID_ARG;
+  if (s->io_dtype != GBLA_F32 && s->io_dtype != GBLA_BF16) return GBLA_ERR_INVALID_ARG;
+  if (s->B < 1 || s->L < 1 || s->d < 1) return GBLA_ERR_INVALID_ARG;
+  if (s->cu_seqlens && (s->seq_lens || s->B != 1 || s->num_seqs < 1)) return GBLA_ERR_INVALID_ARG;
+  p.f32 = s->io_dtype == GBLA_F32;
+  p.rows = s->cu_seqlens ? (int64_t)s->L : (int64_t)s->B * s->L;
+  p.d = s->d;
+  p.L = s->L;
+  p.lens = s->seq_lens;
+  return p.rows > (1LL << 30) || p.d > (1 << 20) ? GBLA_ERR_UNSUPPORTED : GBLA_OK;
+}
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+gbla_status ws_status(const void* ws, size_t have, size_t need) {
+  return !ws || !aligned(ws, kAlign) || have < need ? GBLA_ERR_WORKSPACE : GBLA_OK;
+}
+
+struct EmbedLayout { size_t sums, range, zero_bytes, keys[2], slots[2], count, part, total; int passes, bits; };
+gbla_status embed_plan(const gbla_shape* s, int64_t vocab, int k, RowPlan& p) {
+  const gbla_status r = make_row_plan(s, p);
+  if (r != GBLA_OK) return r;
+  if (vocab < 1 || k < 1) return GBLA_ERR_INVALID_ARG;
+  if (vocab > (1LL << 30) || vocab * p.d > (1LL << 38) || k > (1 << 20) || p.rows * k > (1LL << 30)) return GBLA_ERR_UNSUPPORTED;
+  return GBLA_OK;
+}
+// The workspace: the error word; of the backward also the sort's counts, two sets of keys and slots, the ids' ranges, partial sums.
+EmbedLayout embed_layout(const RowPlan& p, int64_t vocab, int k, bool backward) {
+  EmbedLayout l{};
+  Cursor c;
+  c.take(16);
+  if (backward) {
+    const size_t n = (size_t)p.rows * k, tiles = (n + kEmbedTile - 1) / kEmbedTile;
+    int bits = 1;
+    while ((vocab >> bits) > 0) ++bits;  // of the keys 0 .. vocab
+    l.passes = cdiv(bits, kEmbedDigit);
+    l.bits = cdiv(bits, l.passes);
+    l.sums = c.take(tiles > 1 ? l.passes * ((tiles + kEmbedTiles - 1) / kEmbedTiles) * (4u << kEmbedDigit) : 0);
+    l.range = c.take((size_t)vocab * 8);
+    l.zero_bytes = c.off;
+    for (int i = 0; i < 2; ++i) {
+      l.keys[i] = c.take(n * 4);
+      l.slots[i] = c.take(n * 4);
+    }
+    l.count = c.take(tiles > 1 ? tiles * (4u << kEmbedDigit) : 0);
+    l.part = c.take(2 * ((n + kEmbedCap - 1) / kEmbedCap) * p.d * 4);
+  }
+  l.total = c.off;
+  return l;
+}
+EmbedArgs embed_args(const RowPlan& p, const void* ids, int wide_ids, int k, int64_t vocab, float scale, void* ws) {
+  EmbedArgs a{};
+  a.ids = ids; a.wide_ids = wide_ids;
+  a.n = p.rows * k; a.k = k;
+  a.d = p.d; a.V = (int)vocab; a.scale = scale;
+  a.lens = p.lens; a.L = p.L;
+  a.err = at<int>(ws, 0);
+  return a;
+}
+
+struct RowCtx { cudaStream_t st; };
+
+size_t ln_bytes(const RowPlan& p, bool backward) {
+  return align_up(kAlign + (backward ? (size_t)ln_parts(p.rows, p.d) * 2 * p.d * 4 : 0));
+}
+LnArgs ln_args(const RowPlan& p, const void* x, int64_t ldx, const void* w, void* ws) {
+  LnArgs a{};
+  a.x = x; a.ldx = ldx; a.w = w;
+  a.rows = p.rows; a.d = p.d;
+  a.lens = p.lens; a.L = p.L;
+  a.err = at<int>(ws, 0);
+  return a;
+}
+
+// ------------------------------------------------------------ beam search
+gbla_status beam_ok(const gbla_beam* g) {
+  if (!g || g->B < 1 || g->K < 1 || g->V < 1 || g->n_out < 1) return GBLA_ERR_INVALID_ARG;
+  if (g->io_dtype != GBLA_F32 && g->io_dtype != GBLA_BF16) return GBLA_ERR_INVALID_ARG;
+  if (g->eos < -1 || g->eos >= g->V || (g->over_allowed != 0 && g->over_allowed != 1)) return GBLA_ERR_INVALID_ARG;
+  if (g->K > kBeamMost || g->n_out > kBeamMost || (int64_t)g->K * g->V > (1LL << 32)) return GBLA_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)g->B * g->K;
+  if (rows > (1LL << 30) || rows * (g->V / 1024 + 1) > (1LL << 31) || (int64_t)g->B * g->n_out > (1LL << 30)) return GBLA_ERR_UNSUPPORTED;
+  return GBLA_OK;
+}
+// Sizes of beam_select: the rows' tasks, and runs of about sqrt(K V / n_out) tokens, so that the two selections (of K V / run and of
+// n_out * run) are alike.
+struct BeamLayout { int tasks, runs, lg; size_t part, top, total; };
+BeamLayout beam_layout(const gbla_beam& g) {
+  BeamLayout l{};
+  const int E = g.io_dtype == GBLA_F32 ? 4 : 8;
+  const int64_t places = (int64_t)g.V + E - 1;  // a row may begin behind a 16-byte boundary
+  l.tasks = (int)((places + kBeamPieces * 32 * E - 1) / (kBeamPieces * 32 * E));
+  const double want = std::sqrt((double)g.K * g.V / g.n_out);
+  while (l.lg < 5 && E * (1.5 * (1 << l.lg)) < want) ++l.lg;
+  const int run = E << l.lg;
+  l.runs = (int)((places + run - 1) / run);
+  Cursor c;
+  c.take(16);
+  const size_t rows = (size_t)g.B * g.K;
+  l.part = c.take(rows * l.tasks * sizeof(BeamPart));
+  l.top = c.take(rows * l.runs * 4);
+  l.total = c.off;
+  return l;
+}
+
 // State reduction + combine.  The bf16 path centres the state on the
 // k~-weighted mean of v (center); the fp32 path keeps it uncentred.
 // The layer's bf16 readout: the tcgen05 kernel where it applies.
@@ -1217,6 +1324,192 @@ gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors, con
   GBLA_CHECK(launch_adamw_begin(a, step, norm, s, at<int>(ws, 0), c.st), "adamw begin");
   return adam_cap(tensors, n_tensors) == kAdamFew ? run_adamw<kAdamFew>(tensors, n_tensors, g.lr, s, c)
                                                   : run_adamw<kAdamMany>(tensors, n_tensors, g.lr, s, c);
+}
+
+size_t embed_workspace_size(const gbla_shape* shape, int64_t vocab, int k, int backward) {
+  RowPlan p;
+  if (backward < 0 || backward > 1 || embed_plan(shape, vocab, k, p) != GBLA_OK) return 0;
+  return embed_layout(p, vocab, k, backward != 0).total;
+}
+
+gbla_status embed_forward(const gbla_shape* shape, const void* ids, int wide_ids, int k, const void* table, int64_t vocab,
+                          float scale, void* y, void* ws, size_t ws_bytes, void* stream) {
+  RowPlan p;
+  gbla_status r = embed_plan(shape, vocab, k, p);
+  if (r != GBLA_OK) return r;
+  const size_t es = p.f32 ? 4 : 2;
+  if (!ids || !table || !y || (wide_ids != 0 && wide_ids != 1) || !aligned(ids, wide_ids ? 8 : 4) || !aligned(table, es) || !aligned(y, es))
+    return GBLA_ERR_INVALID_ARG;
+  if ((r = ws_status(ws, ws_bytes, embed_layout(p, vocab, k, false).total)) != GBLA_OK) return r;
+  const RowCtx c{static_cast<cudaStream_t>(stream)};
+  EmbedArgs a = embed_args(p, ids, wide_ids, k, vocab, scale, ws);
+  a.table = table; a.y = y;
+  if (embed_fwd_ctas(a, p.f32) > 1) GBLA_CHECK(cudaMemsetAsync(a.err, 0, sizeof(int), c.st), "memset");
+  GBLA_CHECK(launch_embed_fwd(a, p.f32, c.st), "embed fwd");
+  return GBLA_OK;
+}
+
+gbla_status embed_backward(const gbla_shape* shape, const void* ids, int wide_ids, int k, const void* dy, int64_t vocab,
+                           float scale, float* dtable, void* ws, size_t ws_bytes, void* stream) {
+  RowPlan p;
+  gbla_status r = embed_plan(shape, vocab, k, p);
+  if (r != GBLA_OK) return r;
+  if (!ids || !dy || !dtable || (wide_ids != 0 && wide_ids != 1) || !aligned(ids, wide_ids ? 8 : 4) || !aligned(dy, p.f32 ? 4 : 2) ||
+      !aligned4(dtable))
+    return GBLA_ERR_INVALID_ARG;
+  const EmbedLayout l = embed_layout(p, vocab, k, true);
+  if ((r = ws_status(ws, ws_bytes, l.total)) != GBLA_OK) return r;
+  const RowCtx c{static_cast<cudaStream_t>(stream)};
+  EmbedArgs a = embed_args(p, ids, wide_ids, k, vocab, scale, ws);
+  a.dy = dy; a.dtable = dtable;
+  EmbedSort s{};
+  s.tiles = (int)((a.n + kEmbedTile - 1) / kEmbedTile);
+  s.key_bits = l.passes * l.bits;
+  for (int i = 0; i < 2; ++i) {
+    s.keys[i] = at<int>(ws, l.keys[i]);
+    s.slots[i] = at<int>(ws, l.slots[i]);
+  }
+  s.count = at<int>(ws, l.count);
+  s.range = at<int2>(ws, l.range);
+  s.part = at<float>(ws, l.part);
+  GBLA_CHECK(cudaMemsetAsync(ws, 0, l.zero_bytes, c.st), "memset");
+  const int groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
+  for (int i = 0; i < (s.tiles == 1 ? 1 : l.passes); ++i) {
+    s.key_in = s.keys[(i + 1) & 1]; s.slot_in = s.slots[(i + 1) & 1];
+    s.key_out = s.keys[i & 1]; s.slot_out = s.slots[i & 1];
+    s.sums = at<int>(ws, l.sums) + ((size_t)i * groups << kEmbedDigit);
+    if (s.tiles > 1) GBLA_CHECK(launch_embed_count(a, s, l.bits, i * l.bits, c.st), "embed count");
+    GBLA_CHECK(launch_embed_place(a, s, l.bits, i * l.bits, c.st), "embed place");
+  }
+  if (s.tiles > 1) {
+    GBLA_CHECK(launch_embed_mark(a, s, c.st), "embed mark");
+  } else {  // the one CTA went through every pass
+    s.key_out = s.keys[(l.passes - 1) & 1];
+    s.slot_out = s.slots[(l.passes - 1) & 1];
+  }
+  GBLA_CHECK(launch_embed_rows(a, s, p.f32, c.st), "embed rows");
+  if (a.n > kEmbedCap) GBLA_CHECK(launch_embed_join(a, s, c.st), "embed join");
+  return GBLA_OK;
+}
+
+size_t layer_norm_workspace_size(const gbla_shape* shape, int backward) {
+  RowPlan p;
+  if (backward < 0 || backward > 1 || make_row_plan(shape, p) != GBLA_OK) return 0;
+  return ln_bytes(p, backward != 0);
+}
+
+gbla_status layer_norm_forward(const gbla_shape* shape, const void* x, int64_t ldx, const void* res, const void* w, const void* b,
+                               float eps, void* sum, void* y, float* stats, void* ws, size_t ws_bytes, void* stream) {
+  RowPlan p;
+  gbla_status r = make_row_plan(shape, p);
+  if (r != GBLA_OK) return r;
+  const size_t es = p.f32 ? 4 : 2;
+  for (const void* q : {x, res, w, b, (const void*)sum, (const void*)y})
+    if (!aligned(q, es)) return GBLA_ERR_INVALID_ARG;
+  if (!x || !y || ldx < p.d || !aligned(stats, 8) || !(eps >= 0.f) || eps > 3e38f) return GBLA_ERR_INVALID_ARG;
+  if (sum && (!res || (sum == x && ldx != p.d)) || y == x || y == res || (const void*)y == sum) return GBLA_ERR_INVALID_ARG;
+  if ((r = ws_status(ws, ws_bytes, ln_bytes(p, false))) != GBLA_OK) return r;
+  const RowCtx c{static_cast<cudaStream_t>(stream)};
+  LnArgs a = ln_args(p, x, ldx, w, ws);
+  a.res = res; a.b = b; a.eps = eps; a.sum = sum; a.y = y; a.stats = stats;
+  if (a.lens) GBLA_CHECK(cudaMemsetAsync(a.err, 0, sizeof(int), c.st), "memset");
+  GBLA_CHECK(launch_ln(a, p.f32, false, c.st), "layer norm fwd");
+  return GBLA_OK;
+}
+
+gbla_status layer_norm_backward(const gbla_shape* shape, const void* x, int64_t ldx, const void* w, const float* stats, const void* dy,
+                                const void* ds, void* dx, float* dw, float* db, void* ws, size_t ws_bytes, void* stream) {
+  RowPlan p;
+  gbla_status r = make_row_plan(shape, p);
+  if (r != GBLA_OK) return r;
+  const size_t es = p.f32 ? 4 : 2;
+  for (const void* q : {x, w, dy, ds, (const void*)dx})
+    if (!aligned(q, es)) return GBLA_ERR_INVALID_ARG;
+  if (!x || !stats || !dy || !dx || ldx < p.d || !aligned(stats, 8) || !aligned4(dw) || !aligned4(db)) return GBLA_ERR_INVALID_ARG;
+  if (dx == x || dx == dy) return GBLA_ERR_INVALID_ARG;
+  if ((r = ws_status(ws, ws_bytes, ln_bytes(p, true))) != GBLA_OK) return r;
+  const RowCtx c{static_cast<cudaStream_t>(stream)};
+  LnArgs a = ln_args(p, x, ldx, w, ws);
+  a.stats = const_cast<float*>(stats); a.dy = dy; a.ds = ds; a.dx = dx;
+  a.part = dw || db ? at<float>(ws, kAlign) : nullptr;
+  if (a.lens) GBLA_CHECK(cudaMemsetAsync(a.err, 0, sizeof(int), c.st), "memset");
+  GBLA_CHECK(launch_ln(a, p.f32, true, c.st), "layer norm bwd");
+  if (!a.part) return GBLA_OK;
+  if (!ln_group(p.d)) GBLA_CHECK(launch_ln_cols_long(a, p.f32, c.st), "layer norm cols");
+  GBLA_CHECK(launch_ln_cols(a, dw, db, c.st), "layer norm dw");
+  return GBLA_OK;
+}
+
+size_t beam_workspace_size(const gbla_beam* beam) { return beam_ok(beam) == GBLA_OK ? beam_layout(*beam).total : 0; }
+
+gbla_status beam_select(const gbla_beam* beam, const void* logits, int64_t ld, const float* scores, const uint32_t* allowed,
+                        const uint8_t* done, float* new_scores, int32_t* tokens, int32_t* parents, uint8_t* new_done, void* ws,
+                        size_t ws_bytes, void* stream) {
+  gbla_status r = beam_ok(beam);
+  if (r != GBLA_OK) return r;
+  const gbla_beam& g = *beam;
+  const bool f32 = g.io_dtype == GBLA_F32;
+  for (const void* q : {(const void*)scores, (const void*)new_scores, (const void*)tokens, (const void*)parents})
+    if (!q || !aligned4(q)) return GBLA_ERR_INVALID_ARG;
+  if (!logits || !aligned(logits, f32 ? 4 : 2) || ld < g.V || ld > (1LL << 40) || !aligned4(allowed) || (done && g.eos < 0))
+    return GBLA_ERR_INVALID_ARG;
+  const BeamLayout l = beam_layout(g);
+  if ((r = ws_status(ws, ws_bytes, l.total)) != GBLA_OK) return r;
+  const RowCtx c{static_cast<cudaStream_t>(stream)};
+  BeamArgs a{};
+  a.logits = logits; a.ld = ld; a.scores = scores;
+  a.allowed = allowed; a.words = (g.V + 31) / 32; a.done = done;
+  a.B = g.B; a.K = g.K; a.V = g.V; a.n = g.n_out; a.eos = g.eos; a.over_allowed = allowed && g.over_allowed;
+  a.out_scores = new_scores; a.out_tokens = tokens; a.out_parents = parents; a.out_done = new_done;
+  a.part = at<BeamPart>(ws, l.part); a.tasks = l.tasks;
+  a.top = at<float>(ws, l.top); a.runs = l.runs; a.lg = l.lg;
+  a.err = at<int>(ws, 0);
+  GBLA_CHECK(launch_beam_rows(a, f32, c.st), "beam rows");
+  GBLA_CHECK(launch_beam_pick(a, f32, c.st), "beam pick");
+  return GBLA_OK;
+}
+
+gbla_status beam_reorder(const gbla_beam* beam, const gbla_beam_state* states, int n_states, const int32_t* parents, void* ws,
+                         size_t ws_bytes, void* stream) {
+  gbla_status r = beam_ok(beam);
+  if (r != GBLA_OK) return r;
+  const gbla_beam& g = *beam;
+  if (n_states < 0 || (n_states > 0 && !states) || !parents || !aligned4(parents)) return GBLA_ERR_INVALID_ARG;
+  BeamMove m{parents, g.B, g.K, g.n_out, std::max(1, kBeamMoveUnits / g.n_out), at<int>(ws, 0)};
+  for (int k = 0; k < n_states; ++k) {
+    const gbla_beam_state& t = states[k];
+    if (t.row_bytes < 0 || (t.row_bytes > 0 && (!t.dst || !t.src)) || (t.dst == t.src && g.n_out != g.K && t.row_bytes > 0))
+      return GBLA_ERR_INVALID_ARG;
+    if (t.row_bytes > (1LL << 30) || (double)t.row_bytes * g.B / m.cols > 1e9) return GBLA_ERR_UNSUPPORTED;  // tasks are counted in 31 bits
+  }
+  if ((r = ws_status(ws, ws_bytes, kAlign)) != GBLA_OK) return r;
+  const RowCtx c{static_cast<cudaStream_t>(stream)};
+  BeamTable tab;
+  tab.n = 0;
+  int64_t ctas = 0;
+  for (int k = 0; k <= n_states; ++k) {
+    BeamState t{};
+    int64_t more = 0;
+    if (k < n_states && states[k].row_bytes > 0) {
+      t.dst = states[k].dst; t.src = states[k].src; t.row_bytes = states[k].row_bytes;
+      const uintptr_t bits = (uintptr_t)t.row_bytes | reinterpret_cast<uintptr_t>(t.dst) | reinterpret_cast<uintptr_t>(t.src);
+      t.unit = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+      t.chunks = (int)((t.row_bytes / t.unit + m.cols - 1) / m.cols);
+      more = (int64_t)t.chunks * g.B;
+    }
+    const bool full = tab.n == 64 || ctas + more > 0x7fffff00LL;
+    if (full || k == n_states) {
+      GBLA_CHECK(launch_beam_move(tab, m, (int)ctas, c.st), "beam reorder");
+      tab.n = 0;
+      ctas = 0;
+    }
+    if (more) {
+      t.first = (int)ctas;
+      tab.t[tab.n++] = t;
+      ctas += more;
+    }
+  }
+  return GBLA_OK;
 }
 
 gbla_status gbla_check_device_status(const void* ws, void* stream) {

@@ -308,6 +308,85 @@ template <int N> cudaError_t launch_sumsq(const AdamTable<N>& t, double* part, c
 // The root of the sum of n partials into *norm; clears *err.
 cudaError_t launch_norm(const double* part, int n, float* norm, int* err, cudaStream_t st);
 
+// ------------------------------------------------------------ layer norm
+struct LnArgs {
+  const void* x; int64_t ldx;         // [rows, ldx]; backward: what was normed
+  const void* res;                    // [rows, d] or null
+  const void* w; const void* b;       // [d] or null
+  float eps;
+  void* sum; void* y; float* stats;   // [rows, d] or null; [rows, d]; [rows, 2] (mean, 1 / deviation), forward: or null
+  const void* dy; const void* ds;     // [rows, d]; or null
+  void* dx; float* part;              // [rows, d]; [ln_parts][2][d] or null
+  int64_t rows; int d;
+  const int32_t* lens; int L;         // padded slots: valid rows of each, or null
+  int* err;                           // the error word: 0 on entry with lens, cleared by the kernel without
+};
+int ln_group(int d);
+int ln_ctas(int64_t rows, int d);
+int ln_parts(int64_t rows, int d);    // partial rows of the gradients of w and b
+cudaError_t launch_ln(const LnArgs& a, bool f32, bool bwd, cudaStream_t st);
+// Rows that no group of threads holds (ln_group = 0): their partial column sums, by a kernel of their own.
+cudaError_t launch_ln_cols_long(const LnArgs& a, bool f32, cudaStream_t st);
+// dw, db (either may be null) from the partial rows.
+cudaError_t launch_ln_cols(const LnArgs& a, float* dw, float* db, cudaStream_t st);
+
+// ------------------------------------------------------------ token embedding
+constexpr int kEmbedTile = 2048;   // keys of a CTA of the sort
+constexpr int kEmbedTiles = 32;    // tiles whose counts are also kept summed
+constexpr int kEmbedDigit = 11;    // bits of a digit, at most
+constexpr int kEmbedCap = 64;      // slots of an id that one group of threads sums; more go in pieces
+struct EmbedArgs {
+  const void* ids; int wide_ids;      // [n] int32 or int64
+  int64_t n; int k;                   // slots = tokens * k
+  int d, V;
+  float scale;
+  const void* table; void* y;         // [V, d]; [n, d]
+  const void* dy; float* dtable;      // [n, d]; [V, d]
+  const int32_t* lens; int L;         // padded slots: valid tokens of each, or null
+  int* err;                           // the error word, 0 on entry (the forward of one CTA clears it itself)
+};
+struct EmbedSort {
+  int tiles, key_bits;
+  const int* key_in; int* key_out; const int* slot_in; int* slot_out;  // of the pass; at last key_out, slot_out are the sorted ones
+  int* keys[2]; int* slots[2];        // [n] each
+  int* count; int* sums;              // [tiles][2^kEmbedDigit]; the pass's [tiles / kEmbedTiles][2^kEmbedDigit], 0 on entry
+  int2* range;                        // [V]: each id's sorted places, 0 on entry
+  float* part;                        // [2 * pieces][d]
+};
+int embed_fwd_ctas(const EmbedArgs& a, bool f32);
+cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st);
+// One pass of the sort, by the digit of `bits` bits at `shift`; a single tile's launch_embed_place is the whole sort and marks.
+cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st);
+cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st);
+cudaError_t launch_embed_mark(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st);
+cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st);
+cudaError_t launch_embed_join(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st);
+
+// ------------------------------------------------------------ beam search
+constexpr int kBeamPieces = 8;       // 16-byte pieces a lane of the rows' kernel takes
+constexpr int kBeamMost = 1024;      // beams, in and out
+constexpr int kBeamItems = 8192;     // candidates that the selection holds at once
+struct BeamPart { double s; float ref; int far; };  // sum of exponentials: s 2^ref (a whole number), far: s exp(ref)
+struct BeamArgs {
+  const void* logits; int64_t ld;    // [B K, ld]
+  const float* scores;               // [B, K]
+  const uint32_t* allowed; int words;  // [B K, words] or null
+  const uint8_t* done;               // [B, K] or null
+  int B, K, V, n, eos, over_allowed;
+  float* out_scores; int32_t* out_tokens; int32_t* out_parents; uint8_t* out_done;  // [B, n]; the last or null
+  BeamPart* part; int tasks;         // [B K][tasks]
+  float* top; int runs, lg;          // [B K][runs]: largest logits of runs of 2^lg pieces
+  int* err;
+};
+struct BeamState { void* dst; const void* src; int64_t row_bytes; int first, chunks, unit; };
+struct BeamTable { int n; BeamState t[64]; };
+struct BeamMove { const int32_t* parents; int B, K, n, cols; int* err; };
+constexpr int kBeamMoveUnits = 2048; // accesses of a CTA of launch_beam_move: cols * max(K, n) of them at most
+cudaError_t launch_beam_rows(const BeamArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_beam_pick(const BeamArgs& a, bool f32, cudaStream_t st);
+// ctas: of all the table's tensors; one more checks the parents.
+cudaError_t launch_beam_move(const BeamTable& t, const BeamMove& m, int ctas, cudaStream_t st);
+
 // Checks the sequence data (error word *err) and marks the rows that begin a packed sequence.
 // Also forms a.kd and clears `words` words and the tile counter.
 // SEQS: counts the chunks of each place of the order (level[.] is 0 on entry) and clears `parts` values of a.dlam_part.

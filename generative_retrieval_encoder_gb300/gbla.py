@@ -31,7 +31,8 @@ EXPORTS = ("gbla_workspace_size", "gbla_saved_size", "gbla_validate_shape", "gbl
            "bla_core_forward_noalloc", "bla_core_noalloc_check_device_status", "gbla_diag_bounded_wait",
            "gbla_set_kernel_policy", "bla_decay_core_forward", "sa_core_forward",
            "glr_forward", "glr_backward", "glr_saved_size", "gbla_adamw_workspace_size", "gbla_grad_norm",
-           "gbla_adamw_step")
+           "gbla_adamw_step", "embed_forward", "embed_backward", "embed_workspace_size", "layer_norm_forward",
+           "layer_norm_backward", "layer_norm_workspace_size", "beam_select", "beam_workspace_size", "beam_reorder")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 ADAMW_BLOCK = 256
 
@@ -61,6 +62,15 @@ class AdamWTensor(ctypes.Structure):
 class AdamWConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
                 ("max_norm", ctypes.c_double), ("seed", ctypes.c_uint32)]
+
+
+class Beam(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("K", ctypes.c_int), ("V", ctypes.c_int), ("n_out", ctypes.c_int), ("io_dtype", ctypes.c_int),
+                ("eos", ctypes.c_int), ("over_allowed", ctypes.c_int)]
+
+
+class BeamState(ctypes.Structure):
+    _fields_ = [("dst", ctypes.c_void_p), ("src", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -107,6 +117,26 @@ def lib() -> ctypes.CDLL:
         L.gbla_grad_norm.restype = ctypes.c_int
         L.gbla_adamw_step.argtypes = [tp, ctypes.c_int, ctypes.POINTER(AdamWConfig), vp, vp, vp, sz, vp]
         L.gbla_adamw_step.restype = ctypes.c_int
+        i64, i32, fl = ctypes.c_int64, ctypes.c_int, ctypes.c_float
+        L.embed_workspace_size.argtypes = [sp, i64, i32, i32]
+        L.embed_workspace_size.restype = sz
+        L.embed_forward.argtypes = [sp, vp, i32, i32, vp, i64, fl, vp, vp, sz, vp]
+        L.embed_forward.restype = i32
+        L.embed_backward.argtypes = [sp, vp, i32, i32, vp, i64, fl, vp, vp, sz, vp]
+        L.embed_backward.restype = i32
+        L.layer_norm_workspace_size.argtypes = [sp, i32]
+        L.layer_norm_workspace_size.restype = sz
+        L.layer_norm_forward.argtypes = [sp, vp, i64, vp, vp, vp, fl, vp, vp, vp, vp, sz, vp]
+        L.layer_norm_forward.restype = i32
+        L.layer_norm_backward.argtypes = [sp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.layer_norm_backward.restype = i32
+        bp = ctypes.POINTER(Beam)
+        L.beam_workspace_size.argtypes = [bp]
+        L.beam_workspace_size.restype = sz
+        L.beam_select.argtypes = [bp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_select.restype = i32
+        L.beam_reorder.argtypes = [bp, ctypes.POINTER(BeamState), i32, vp, vp, sz, vp]
+        L.beam_reorder.restype = i32
         L.bla_core_forward_noalloc.argtypes = [sp] + [vp] * 8
         L.bla_core_forward_noalloc.restype = ctypes.c_int
         L.bla_core_noalloc_check_device_status.argtypes = [vp]
@@ -553,6 +583,230 @@ def gbla_adamw_step(plan: AdamWPlan, lr: float, betas=(0.9, 0.999), eps: float =
     cfg = AdamWConfig(lr, betas[0], betas[1], eps, max_norm or 0.0, seed)
     _check(_call(plan.device, lib().gbla_adamw_step, plan.tensors, plan.n, ctypes.byref(cfg), plan.step.data_ptr(),
                  None if norm is None else norm.data_ptr(), plan.ws.data_ptr(), plan.ws.numel()), "gbla_adamw_step")
+
+
+def _arg(name, t, shape, dtype, device):
+    """t's address.  Raises unless t is a contiguous tensor of this shape, dtype and device."""
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: want contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} with strides "
+                         f"{t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _cuda(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: want a CUDA tensor, got {t.device}")
+    return t.device
+
+
+def _ws(ws, size, what, device):
+    """A workspace of `size` bytes (0: the arguments' error) and its address and bytes."""
+    if ws is None:
+        if size == 0:
+            _check(GBLA_ERR_INVALID_ARG, what)
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+    return _glr_bytes("ws", ws, 0, device), ws.numel() * ws.element_size()
+
+
+def embed_workspace_size(shape: Shape, vocab: int, k: int = 1, backward: bool = False) -> int:
+    return lib().embed_workspace_size(ctypes.byref(shape), vocab, k, int(backward))
+
+
+def embed_workspace(shape: Shape, vocab: int, k: int = 1, backward: bool = False, device="cuda") -> torch.Tensor:
+    n = embed_workspace_size(shape, vocab, k, backward)
+    if n == 0:
+        _check(GBLA_ERR_INVALID_ARG, "embed_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _embed_ids(shape, ids):
+    dev, T = _cuda("ids", ids), rows(shape)
+    k = ids.shape[1] if ids.dim() == 2 else 1
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() not in (1, 2) or ids.shape[0] != T or k < 1 or not ids.is_contiguous():
+        raise ValueError(f"ids: want contiguous int32 or int64 [{T}] or [{T}, k], got {ids.dtype} {list(ids.shape)}")
+    return dev, T, k, ids.data_ptr(), int(ids.dtype is torch.int64)
+
+
+def embed_forward(shape: Shape, ids, table, scale: float = 1.0, y=None, ws=None):
+    """Rows of table [V, d] by ids [rows] or [rows, k] (int32 or int64; below 0: none), times scale (see gbla.h): returns y
+    [rows, k d].  shape: glr_shape or make_shape, whose d is the width of a table row."""
+    dev, T, k, pi, wide = _embed_ids(shape, ids)
+    io = io_dtype(shape)
+    if table.dim() != 2:
+        raise ValueError(f"table: want [V, {shape.d}], got {list(table.shape)}")
+    pt = _arg("table", table, (table.shape[0], shape.d), io, dev)
+    if y is None:
+        y = torch.empty((T, k * shape.d), dtype=io, device=dev)
+    py = _arg("y", y, (T, k * shape.d), io, dev)
+    pw, nw = _ws(ws, 256, "embed_forward", dev)  # (the error word alone)
+    st = _call(dev, lib().embed_forward, ctypes.byref(shape), pi, wide, k, pt, table.shape[0], scale, py, pw, nw)
+    if st != GBLA_OK:
+        raise GblaError(st, "embed_forward")
+    return y
+
+
+def embed_backward(shape: Shape, ids, dy, vocab: int, scale: float = 1.0, dtable=None, ws=None):
+    """The table's gradient for <dy, y>: fp32 [vocab, d], rows without a token 0."""
+    dev, T, k, pi, wide = _embed_ids(shape, ids)
+    pd = _arg("dy", dy, (T, k * shape.d), io_dtype(shape), dev)
+    if dtable is None:
+        dtable = torch.empty((vocab, shape.d), dtype=torch.float32, device=dev)
+    pg = _arg("dtable", dtable, (vocab, shape.d), torch.float32, dev)
+    pw, nw = _ws(ws, 0 if ws is not None else embed_workspace_size(shape, vocab, k, True), "embed_backward", dev)
+    st = _call(dev, lib().embed_backward, ctypes.byref(shape), pi, wide, k, pd, vocab, scale, pg, pw, nw)
+    if st != GBLA_OK:
+        raise GblaError(st, "embed_backward")
+    return dtable
+
+
+def layer_norm_workspace_size(shape: Shape, backward: bool = False) -> int:
+    return lib().layer_norm_workspace_size(ctypes.byref(shape), int(backward))
+
+
+def layer_norm_workspace(shape: Shape, backward: bool = False, device="cuda") -> torch.Tensor:
+    n = layer_norm_workspace_size(shape, backward)
+    if n == 0:
+        _check(GBLA_ERR_INVALID_ARG, "layer_norm_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _norm_input(shape, x):
+    """(device, rows, d, io dtype, row stride, address) of what is normed: rows of any stride."""
+    dev, T, d, io = _cuda("x", x), rows(shape), shape.d, io_dtype(shape)
+    ld = x.stride(0) if T > 1 and x.dim() == 2 else d
+    return dev, T, d, io, ld, _glr_arg("x", x, T, d, io, dev, ld)
+
+
+def layer_norm_forward(shape: Shape, x, w=None, b=None, eps: float = 1e-5, res=None, total: torch.Tensor | bool | None = None, y=None,
+                       stats: torch.Tensor | bool | None = None, ws=None):
+    """Layer norm of x, or of x + res (see gbla.h): returns (y, total, stats).  total: x + res as it is normed, allocated
+    where there is a res (False: not wanted; res itself, or x, to update it in place); stats = True allocates what
+    layer_norm_backward needs."""
+    dev, T, d, io, ld, px = _norm_input(shape, x)
+    full = (T, d)
+    if y is None:
+        y = torch.empty(full, dtype=io, device=dev)
+    if total is None or total is True:
+        total = torch.empty(full, dtype=io, device=dev) if res is not None else None
+    if total is False:
+        total = None
+    if stats is True:
+        stats = torch.empty((T, 2), dtype=torch.float32, device=dev)
+    if stats is False:
+        stats = None
+    pw, nw = _ws(ws, 256, "layer_norm_forward", dev)  # (the error word alone)
+    st = _call(dev, lib().layer_norm_forward, ctypes.byref(shape), px, ld, None if res is None else _arg("res", res, full, io, dev),
+               None if w is None else _arg("w", w, (d,), io, dev), None if b is None else _arg("b", b, (d,), io, dev), eps,
+               None if total is None else _arg("total", total, full, io, dev), _arg("y", y, full, io, dev),
+               None if stats is None else _arg("stats", stats, (T, 2), torch.float32, dev), pw, nw)
+    if st != GBLA_OK:
+        raise GblaError(st, "layer_norm_forward")
+    return y, total, stats
+
+
+def layer_norm_backward(shape: Shape, x, w, stats, dy, ds=None, affine: bool = True, ws=None, out: dict | None = None) -> dict:
+    """Backward of layer_norm_forward for <dy, y> + <ds, total>: x is what was normed (total, where there was a res).  Returns
+    dx (the gradient of x and of res) and, with affine, dw and db fp32.  out: tensors to fill (dx may be ds)."""
+    dev, T, d, io, ld, px = _norm_input(shape, x)
+    full, f32 = (T, d), torch.float32
+    g = out
+    if g is None:
+        g = {"dx": torch.empty(full, dtype=io, device=dev)}
+        if affine:
+            g["dw"], g["db"] = torch.empty(d, dtype=f32, device=dev), torch.empty(d, dtype=f32, device=dev)
+    dw, db = g.get("dw"), g.get("db")
+    pw, nw = _ws(ws, 0 if ws is not None else layer_norm_workspace_size(shape, True), "layer_norm_backward", dev)
+    st = _call(dev, lib().layer_norm_backward, ctypes.byref(shape), px, ld, None if w is None else _arg("w", w, (d,), io, dev),
+               _arg("stats", stats, (T, 2), f32, dev), _arg("dy", dy, full, io, dev), None if ds is None else _arg("ds", ds, full, io, dev),
+               _arg("dx", g["dx"], full, io, dev), None if dw is None else _arg("dw", dw, (d,), f32, dev),
+               None if db is None else _arg("db", db, (d,), f32, dev), pw, nw)
+    if st != GBLA_OK:
+        raise GblaError(st, "layer_norm_backward")
+    return g
+
+
+def beam_shape(B: int, K: int, V: int, n_out: int | None = None, dtype: str = "bf16", eos: int = -1, over_allowed: bool = False) -> Beam:
+    """A step of beam search over B groups of K beams and V tokens, of which n_out (K) beams go on; dtype: of the logits."""
+    return Beam(B, K, V, K if n_out is None else n_out, GBLA_F32 if dtype in ("f32", "fp32", torch.float32) else GBLA_BF16, eos,
+                int(over_allowed))
+
+
+def beam_workspace_size(beam: Beam) -> int:
+    return lib().beam_workspace_size(ctypes.byref(beam))
+
+
+def beam_workspace(beam: Beam, device="cuda") -> torch.Tensor:
+    n = beam_workspace_size(beam)
+    if n == 0:
+        _check(GBLA_ERR_INVALID_ARG, "beam_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def beam_select(beam: Beam, logits, scores, allowed=None, done=None, out: tuple | None = None, ws=None):
+    """The n_out best of each group's K x V candidates (see gbla.h): returns (scores, tokens, parents, done), each [B, n_out],
+    done (bool) where beam has an eos.  logits [B K, V] of any row stride; scores fp32 [B, K]; allowed int32 [B K,
+    ceil(V / 32)], the bits of the tokens that may follow; done bool [B, K].  out: such a tuple to fill."""
+    B, K, V, n = beam.B, beam.K, beam.V, beam.n_out
+    dev, dt = _cuda("logits", logits), torch.float32 if beam.io_dtype == GBLA_F32 else torch.bfloat16
+    ld = logits.stride(0) if B * K > 1 and logits.dim() == 2 else V
+    pl = _glr_arg("logits", logits, B * K, V, dt, dev, ld)
+    if out is None:
+        out = (torch.empty((B, n), dtype=torch.float32, device=dev), torch.empty((B, n), dtype=torch.int32, device=dev),
+               torch.empty((B, n), dtype=torch.int32, device=dev), torch.empty((B, n), dtype=torch.bool, device=dev) if beam.eos >= 0 else None)
+    po = [_arg(name, t, (B, n), kind, dev) for name, t, kind in zip(("scores", "tokens", "parents"), out, (torch.float32, torch.int32, torch.int32))]
+    pw, nw = _ws(ws, 0 if ws is not None else beam_workspace_size(beam), "beam_select", dev)
+    st = _call(dev, lib().beam_select, ctypes.byref(beam), pl, ld, _arg("scores", scores, (B, K), torch.float32, dev),
+               None if allowed is None else _arg("allowed", allowed, (B * K, -(-V // 32)), torch.int32, dev),
+               None if done is None else _arg("done", done, (B, K), torch.bool, dev), *po,
+               None if out[3] is None else _arg("done", out[3], (B, n), torch.bool, dev), pw, nw)
+    if st != GBLA_OK:
+        raise GblaError(st, "beam_select")
+    return out
+
+
+class BeamReorderPlan:
+    """Which tensors follow their beams' parents (beam_reorder_plan); it keeps them alive."""
+
+    def __init__(self, beam: Beam, states, out=None):
+        S, D = list(states), list(states if out is None else out)
+        if len(S) != len(D):
+            raise ValueError(f"{len(D)} tensors to fill for {len(S)} states")
+        if out is None and beam.n_out != beam.K:
+            raise ValueError(f"in place needs as many beams out ({beam.n_out}) as in ({beam.K})")
+        self.beam, self.B, self.n = beam, beam.B, beam.n_out
+        self.device = _cuda("state", S[0]) if S else torch.device("cuda", torch.cuda.current_device())
+        self._keep = (S, D)
+        self.states = (BeamState * len(S))()
+        taken = []
+        for j, (a, b) in enumerate(zip(S, D)):
+            row = a.numel() // (beam.B * beam.K) * a.element_size()
+            for name, t, n in (("state", a, beam.B * beam.K), ("tensor to fill", b, beam.B * beam.n_out)):
+                if t.device != self.device or t.dtype is not a.dtype or not t.is_contiguous() or t.numel() * t.element_size() != n * row:
+                    raise ValueError(f"{name} {j}: want {n} contiguous rows of {row} bytes of {a.dtype} on {self.device}, got {t.dtype} "
+                                     f"{list(t.shape)} on {t.device}")
+            if row:
+                taken.append((a.data_ptr(), beam.B * beam.K * row, f"state {j}"))
+                if out is not None:
+                    taken.append((b.data_ptr(), beam.B * beam.n_out * row, f"tensor to fill {j}"))
+            self.states[j] = BeamState(b.data_ptr() if row else None, a.data_ptr() if row else None, row)
+        taken.sort()
+        for (at, size, who), (nxt, _, name) in zip(taken, taken[1:]):
+            if nxt < at + size:
+                raise ValueError(f"{who} and {name} overlap")
+        self.ws = torch.empty(256, dtype=torch.uint8, device=self.device)
+
+
+def beam_reorder_plan(beam: Beam, states, out=None) -> BeamReorderPlan:
+    """The plan of moving states (tensors of B K rows; the rows' shape and type are free) to where beam_select's parents send
+    them: in place (n_out = K), or into out (tensors of B n_out rows).  Its workspace orders its calls on one stream."""
+    return BeamReorderPlan(beam, states, out)
+
+
+def beam_reorder(plan: BeamReorderPlan, parents) -> None:
+    """Row [b, i] of each of the plan's tensors becomes the state's row [b, parents[b, i]] (see gbla.h)."""
+    _check(_call(plan.device, lib().beam_reorder, ctypes.byref(plan.beam), plan.states, len(plan.states),
+                 _arg("parents", parents, (plan.B, plan.n), torch.int32, plan.device), plan.ws.data_ptr(), plan.ws.numel()),
+           "beam_reorder")
 
 
 def bla_core_forward_noalloc(shape: Shape, q, k, v, g, o, den=None, state=None) -> int:

@@ -349,6 +349,148 @@ gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors,
                             void* stream);
 
 /*
+ * Token embedding: rows of a table by ids, k of them a token (items named by
+ * several hashes into one shared table; their rows stand side by side):
+ *   y[t, j d .. (j + 1) d - 1] = scale table[ids[t, j]].
+ *   shape   B, L, d (the width of a table row), io_dtype and the sequence
+ *           form; a token of a padded slot past its sequence has a row of
+ *           zeros and its ids count for nothing; cu_seqlens is not read
+ *   ids     [rows, k] int32 (wide_ids = 0) or int64 (1); an id below 0 is no
+ *           token: zeros.  An id >= vocab sets the error word
+ *           (GBLA_ERR_DEVICE_CHECK), and so does a seq_lens value outside
+ *           [0, L]: they count as no token and as an empty sequence
+ *   table   (io) [vocab, d];  y (io) [rows, k d], rounded once
+ * d, k and vocab are free: rows k <= 2^30, vocab <= 2^30, d <= 2^20,
+ * vocab d <= 2^38.  Pointers are aligned to their element (rows of a multiple of
+ * 16 bytes in 16-byte aligned tensors are read in wider pieces).  The shape's H,
+ * d_h, gate and rms_eps are ignored.  Workspace: embed_workspace_size(.., 0).
+ */
+gbla_status embed_forward(const gbla_shape* shape, const void* ids,
+                          int wide_ids, int k, const void* table,
+                          int64_t vocab, float scale, void* y, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * The table's gradient for the scalar <dy, y>: dtable fp32 [vocab, d],
+ *   dtable[v] = scale sum of dy[t, j d ..] over the (t, j) with ids[t, j] = v,
+ * all of it written (rows without a token: 0).  dy (io) [rows, k d].  The sums
+ * run over the tokens in their order, in pieces of fixed size: the same bits
+ * again for the same call.  Workspace: embed_workspace_size(.., 1).
+ */
+gbla_status embed_backward(const gbla_shape* shape, const void* ids,
+                           int wide_ids, int k, const void* dy, int64_t vocab,
+                           float scale, float* dtable, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of embed_forward (backward = 0) or embed_backward (1; it
+ * serves the forward too); 0 on an argument error. */
+size_t embed_workspace_size(const gbla_shape* shape, int64_t vocab, int k,
+                            int backward);
+
+/*
+ * Layer norm of each token, with the residual stream's addition before it:
+ *   s = x + res,  m = mean(s),  r = 1 / sqrt(mean((s - m)^2) + eps),
+ *   y = (s - m) r w + b.
+ *   shape   B, L, d, io_dtype and the sequence form; tokens of padded slots past
+ *           their sequence get zeros in every output (a seq_lens value outside
+ *           [0, L] sets the error word and counts as 0); cu_seqlens is not read
+ *   x       (io) [rows, d], row stride ldx >= d
+ *   res     (io) [rows, d] or NULL (s = x)
+ *   w, b    (io) [d] or NULL (ones, zeros)
+ *   sum     (io) [rows, d]: s, rounded once, which is what is normed; NULL without
+ *           res, and where s is not wanted.  It may be res, or x with ldx = d
+ *   y       (io) [rows, d]
+ *   stats   fp32 [rows, 2] (m, r) for the backward, 8-byte aligned, or NULL
+ * rows <= 2^30, d <= 2^20; pointers aligned to their element; tensors do not
+ * overlap (but sum as above).  The shape's H, d_h, gate and rms_eps are ignored.
+ * Workspace: layer_norm_workspace_size(shape, 0).
+ */
+gbla_status layer_norm_forward(const gbla_shape* shape, const void* x,
+                               int64_t ldx, const void* res, const void* w,
+                               const void* b, float eps, void* sum, void* y,
+                               float* stats, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * Backward for <dy, y> + <ds, s>: x, ldx are what was normed (sum, where there
+ * was a res), stats the forward's; with z = (s - m) r and g = dy w
+ *   dx = r (g - mean(g) - z mean(g z)) + ds   (the gradient of x and of res),
+ *   dw = sum over the tokens of dy z,  db = sum over the tokens of dy.
+ *   dy (io) [rows, d];  ds (io) [rows, d] or NULL;  dx (io) [rows, d], may be ds;
+ *   dw, db fp32 [d] or NULL.  Gradients overwrite; fixed order of sums.
+ * Workspace: layer_norm_workspace_size(shape, 1).
+ */
+gbla_status layer_norm_backward(const gbla_shape* shape, const void* x,
+                                int64_t ldx, const void* w, const float* stats,
+                                const void* dy, const void* ds, void* dx,
+                                float* dw, float* db, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* Bytes of workspace of layer_norm_forward (backward = 0) or
+ * layer_norm_backward (1; it serves the forward too); 0 on a shape error. */
+size_t layer_norm_workspace_size(const gbla_shape* shape, int backward);
+
+/*
+ * A step of beam search.  Of each of B groups' K beams x V tokens, the n_out of
+ * highest
+ *   score(b, t) = scores[b] + logits[b, t] - log sum_t' exp(logits[b, t']),
+ * in falling order, ties to the lowest beam and then the lowest token.
+ */
+typedef struct {
+  int B, K, V;       /* groups; beams of each, 1 .. 1024; tokens                  */
+  int n_out;         /* beams that go on, 1 .. 1024 (K = 1 starts a search)       */
+  int io_dtype;      /* gbla_dtype of the logits                                  */
+  int eos;           /* the token that ends a beam, or -1                         */
+  int over_allowed;  /* 1: the logarithm's sum runs over the allowed tokens alone */
+} gbla_beam;
+
+/*
+ *   logits   (io) [B K, V], row stride ld >= V, aligned to the element
+ *   scores   fp32 [B, K]; a beam of -inf or NaN has no candidates (the beams but
+ *            the first of a search that starts with K copies)
+ *   allowed  uint32 [B K, ceil(V / 32)] or NULL: bit t % 32 of word t / 32 lets
+ *            token t be a candidate (valid continuations of an item's code)
+ *   done     uint8 [B, K] or NULL (needs eos >= 0): an ended beam's only candidate
+ *            is (b, eos) with scores[b], whatever its logits and mask are
+ *   new_scores fp32, tokens, parents int32 [B, n_out]: parents in 0 .. K - 1;
+ *            new_done uint8 [B, n_out] or NULL: done[parent], or token = eos.
+ *            Where there are fewer candidates than n_out the last are (-inf, token
+ *            -1, parent 0, not done).
+ * Logits of -inf and rows with a NaN or +inf among those summed have no candidates.
+ * Exponentials are summed, and scores compared, in two fp32 words: which of two
+ * candidates is first is decided to 2^-26 (to 2^-30 on the mean), and a score is
+ * rounded once.
+ * K V <= 2^32, B K V / 1024 <= 2^31.  Outputs do not overlap inputs.  Workspace:
+ * beam_workspace_size().
+ */
+gbla_status beam_select(const gbla_beam* beam, const void* logits, int64_t ld,
+                        const float* scores, const uint32_t* allowed,
+                        const uint8_t* done, float* new_scores, int32_t* tokens,
+                        int32_t* parents, uint8_t* new_done, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of beam_select and beam_reorder; 0 on an argument error. */
+size_t beam_workspace_size(const gbla_beam* beam);
+
+/* What a beam keeps: rows of row_bytes bytes, [B K] in src, [B n_out] in dst. */
+typedef struct {
+  void* dst;         /* may be src, with n_out = K: moved in place               */
+  const void* src;
+  int64_t row_bytes; /* >= 0                                                     */
+} gbla_beam_state;
+
+/*
+ * The beams' states (of a recurrence: its h) follow their parents, any number of
+ * tensors: dst[b n_out + i] = src[b K + parents[b, i]].  A parent outside
+ * 0 .. K - 1 sets the error word (GBLA_ERR_DEVICE_CHECK) and leaves its row of dst as
+ * it was.  states: host array, read during the call; tensors do not overlap (but
+ * dst = src).  beam: B, K and n_out are read.
+ */
+gbla_status beam_reorder(const gbla_beam* beam, const gbla_beam_state* states,
+                         int n_states, const int32_t* parents, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
  * bla_core_forward without a caller workspace (the pages have no counterpart:
  * this is a deployment convenience).  Some callers cannot call cudaMalloc or
  * hand the library a scratch buffer: a plugin running inside a host framework

@@ -1,0 +1,456 @@
+"""beam_select and beam_reorder against their definition in 64 bits: both types,
+odd and unaligned rows, masks (also over a whole row), ended, dead and identical
+beams, ties, infinities and NaN, fewer candidates than beams, one to 1024 beams,
+streams and graphs, states of every width moved in place and into others, a
+decoding loop of embedding, norm, recurrence, selection and reordering, and a
+training step of the same parts.
+
+Order: the sum of a row's exponentials is off by 2^-27 at most (each by 2^-30; two
+words, 16 additions of at most 0.011 of them in the lower), and so is its
+logarithm.  So candidates of two beams may change places only where their scores
+differ by less than 2 * 2^-27 (and 2^-46 of their size: two fp32 words); within a beam
+never.  A score is rounded once: 2^-24 of its value beside that."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from generative_retrieval_encoder_gb300 import build, gbla
+
+pytestmark = pytest.mark.gpu
+E = 2.0 ** -24
+NEAR = 2.0 ** -26
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    gbla.lib()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def reference(logits, scores, V, n, allowed=None, done=None, eos=-1, over=False):
+    """(B, K V) scores in 64 bits (-inf: no candidate) and each group's order of candidates, ties by place."""
+    B, K = scores.shape
+    x = logits.double().numpy().reshape(B, K, -1)[:, :, :V]
+    ok = np.ones((B, K, V), bool) if allowed is None else allowed.reshape(B, K, V)
+    s = np.where(ok, x, -np.inf) if over else x
+    with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+        m = np.max(np.where(np.isnan(s), -np.inf, s), axis=2, keepdims=True)
+        base = np.where(np.isfinite(m), m, 0.0)
+        log = np.log(np.exp(s - base).sum(2, keepdims=True))
+        p = scores.double().numpy()[:, :, None] + ((x - base) - log)  # (of logits of 3e38 a sum with `base` would lose `log`)
+    p = np.where(ok & (x > -np.inf), p, -np.inf)
+    if done is not None:
+        e = done.numpy()
+        p[e] = -np.inf
+        p[e, eos] = scores.double().numpy()[e]
+    p = np.where(p > -np.inf, p, -np.inf).reshape(B, K * V)
+    order = np.argsort(-p, axis=1, kind="stable")[:, :n]
+    return p, order
+
+
+def pack(ok):
+    R, V = ok.shape
+    bits = np.zeros((R, -(-V // 32) * 32), np.uint8)
+    bits[:, :V] = ok
+    w = np.packbits(bits.reshape(R, -1, 32), axis=2, bitorder="little").view(np.uint32).reshape(R, -1)
+    return torch.from_numpy(w.astype(np.int64).astype(np.uint32).view(np.int32).copy())
+
+
+def check(got, p, order, V, n, done=None, eos=-1, strict=True):
+    sc, tok, par, dn = [None if t is None else t.cpu().numpy() for t in got]
+    B = p.shape[0]
+    for b in range(B):
+        live = min(n, int((p[b] > -np.inf).sum()))
+        assert (sc[b, live:] == -np.inf).all() and (tok[b, live:] == -1).all() and (par[b, live:] == 0).all()
+        at = par[b, :live].astype(np.int64) * V + tok[b, :live]
+        want = order[b, :live]
+        assert len(set(at.tolist())) == live
+        a, w = p[b, at], p[b, want]
+        with np.errstate(invalid="ignore"):
+            slack = NEAR + 2.0 ** -46 * np.abs(w)
+            assert ((np.abs(a - w) <= slack) | (a == w)).all(), b
+            assert ((np.abs(sc[b, :live] - a) <= NEAR + E * np.abs(a)) | (sc[b, :live] == a.astype(np.float32))).all()
+        if strict:
+            # (scores of -3e38, of logits of the type's lowest value: 64 bits hold no difference below 2^74 there, so -3e38 - 3 and
+            # -3e38 - 6 tie in the reference; the second fp32 word holds it, and such candidates come in their true order)
+            near = np.abs(w) < 2.0 ** 100
+            assert (at == want)[near].all(), (b, np.flatnonzero(at != want)[:5])
+        if dn is not None:
+            old = np.zeros(par.shape[1], bool) if done is None else done[b].numpy()[par[b]]
+            assert (dn[b, :live] == (old | (tok[b] == eos))[:live]).all() and not dn[b, live:].any()
+
+
+def make(B, K, V, dtype="bf16", pad=0, offset=0, seed=0, std=2.0):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = gen(seed)
+    x = (torch.randn(B * K, V + pad, generator=g) * std).to(dt)
+    buf = torch.full((offset + x.numel() + 64,), float("nan"), dtype=dt, device="cuda")
+    v = buf[offset:offset + x.numel()].view(B * K, V + pad)
+    v.copy_(x)
+    if pad:
+        v[:, V:] = float("nan")  # the padding's columns are nobody's tokens
+    scores = torch.sort(-5 * torch.rand(B, K, generator=g), dim=1, descending=True).values.contiguous()
+    return v[:, :V], x[:, :V], scores
+
+
+def run(B, K, V, n=None, dtype="bf16", mask=None, over=False, ends=0.0, eos=-1, strict=True, dead=(), **kw):
+    n = K if n is None else n
+    seed = B * 7 + K * 3 + V
+    v, x, scores = make(B, K, V, dtype, seed=seed, **kw)
+    for b, k in dead:
+        scores[b, k] = -math.inf
+    ok = None if mask is None else torch.rand(B * K, V, generator=gen(seed + 1)).numpy() < mask
+    done = torch.rand(B, K, generator=gen(seed + 2)) < ends if ends else None
+    beam = gbla.beam_shape(B, K, V, n, dtype=dtype, eos=eos, over_allowed=over)
+    ws = gbla.beam_workspace(beam)
+    ws.fill_(0xA5)
+    got = gbla.beam_select(beam, v, scores.cuda(), allowed=None if ok is None else pack(ok).cuda(), done=None if done is None else done.cuda(), ws=ws)
+    assert gbla.gbla_check_device_status(ws) == gbla.GBLA_OK
+    p, order = reference(x, scores, V, n, ok, done, eos, over)
+    check(got, p, order, V, n, done, eos, strict)
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,K,V,n", [(1, 1, 1, 1), (2, 1, 7, 3), (1, 8, 256, 8), (3, 5, 33, 5), (4, 1, 1000, 16), (2, 16, 2048, 16), (5, 7, 2049, 7), (2, 3, 40001, 20),
+                                     (1, 256, 300, 256), (2, 50, 5000, 50), (1, 1024, 64, 1024), (1, 700, 90, 1000), (3, 2, 100, 1024), (1, 4, 130000, 512), (7, 4, 16384, 1)])
+def test_beam_matches_definition(dtype, B, K, V, n):
+    run(B, K, V, n, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 0), (24, 7)])
+@pytest.mark.parametrize("V", [5, 100, 4000])
+def test_beam_rows_of_any_stride_and_alignment(dtype, pad, offset, V):
+    run(2, 6, V, 6, dtype, pad=pad, offset=offset)
+    run(2, 6, V, 6, dtype, pad=pad, offset=offset, mask=0.4, over=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("over", [False, True])
+@pytest.mark.parametrize("K,V,mask", [(4, 100, 0.5), (16, 5000, 0.01), (256, 512, 0.02), (3, 31, 0.05), (5, 65, 0.0), (2, 20000, 0.001)])
+def test_beam_masks(dtype, over, K, V, mask):
+    run(3, K, V, K, dtype, mask=mask, over=over)
+    run(3, K, V, K, dtype, mask=mask, over=over, ends=0.4, eos=V // 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_beam_ended_and_dead_beams(dtype):
+    run(4, 8, 500, 8, dtype, ends=0.5, eos=0)
+    run(4, 8, 500, 8, dtype, ends=1.0, eos=499)           # every beam has ended: each goes on as itself
+    run(4, 8, 500, 8, dtype, eos=3)                       # none has yet
+    run(2, 6, 50, 6, dtype, dead=[(0, k) for k in range(1, 6)])  # a search that starts with copies of one beam
+    run(2, 6, 50, 6, dtype, dead=[(1, k) for k in range(6)])     # a group without a live beam
+    run(2, 6, 3, 6, dtype, dead=[(1, k) for k in range(5)], ends=0.2, eos=1)
+
+
+def test_beam_ties_go_to_the_lowest_beam_and_token():
+    for V, n in ((40, 16), (5000, 16), (300, 200)):
+        beam = gbla.beam_shape(2, 16, V, n, dtype="f32")
+        x = torch.zeros(32, V, device="cuda")
+        sc, tok, par, _ = gbla.beam_select(beam, x, torch.zeros(2, 16, device="cuda"))
+        want = torch.arange(n).repeat(2, 1)
+        assert torch.equal(tok.cpu().long(), want % V) and torch.equal(par.cpu().long(), want // V)
+        # three values, spread so that the equal ones lie in many runs and rows
+        x = (torch.arange(32 * V).view(32, V) * 7919 % 3).float()
+        x = torch.sort(x, dim=1).values[:, torch.randperm(V, generator=gen(V))]  # every row the same values: the same logarithm
+        scores = torch.zeros(2, 16)
+        got = gbla.beam_select(beam, x.cuda(), scores.cuda())
+        p, order = reference(x, scores, V, n)
+        top = p.max()
+        flat = (got[2].long() * V + got[1]).cpu().numpy()
+        for b in range(2):
+            first = np.flatnonzero(np.abs(p[b] - top) < 1e-9)[:n]
+            assert (flat[b, :len(first)] == first).all()
+
+
+def test_beam_infinities_nan_and_far_logits():
+    inf, nan = math.inf, math.nan
+    V, K = 70, 6
+    for dtype in ("bf16", "f32"):
+        dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+        low = torch.finfo(dt).min
+        x = torch.randn(K, V, generator=gen(1)).to(dt)
+        x[0, 5:] = -inf
+        x[1] = -inf
+        x[2, 7] = nan
+        x[3, 9] = inf
+        x[4, ::2] = low       # masks of the type's lowest value
+        x[5] = low
+        x[5, 11] = 0
+        scores = torch.tensor([[-1.0, -0.5, 0.0, 0.0, -2.0, -3.0]])
+        beam = gbla.beam_shape(1, K, V, 60, dtype=dtype)
+        got = gbla.beam_select(beam, x.cuda(), scores.cuda())
+        p, order = reference(x, scores, V, 60)
+        assert set(got[2][0].tolist()) == {0, 4, 5}
+        check(got, p, order, V, 60)
+        # NaN and infinities where the mask lets nothing through: counted over all tokens, not counted over the allowed
+        ok = np.ones((K, V), bool)
+        ok[2, 7] = ok[3, 9] = False
+        for over in (False, True):
+            beam = gbla.beam_shape(1, K, V, 60, dtype=dtype, over_allowed=over)
+            got = gbla.beam_select(beam, x.cuda(), scores.cuda(), allowed=pack(ok).cuda())
+            p, order = reference(x, scores, V, 60, ok, over=over)
+            check(got, p, order, V, 60)
+            assert ({2, 3} <= set(got[2][0].tolist())) == over
+        # logits far from 0, of whole rows and of parts of them, and the largest there are
+        x = (torch.randn(K, 5000, generator=gen(2)) * 3).to(dt)
+        x[1] += 1e4
+        x[2] -= 1e5
+        x[3, :100] = 5e3
+        x[4] = torch.finfo(dt).max
+        x[5, 2000:] = -3e4
+        beam = gbla.beam_shape(1, K, 5000, 64, dtype=dtype)
+        got = gbla.beam_select(beam, x.cuda(), scores.cuda())
+        p, order = reference(x, scores, 5000, 64)
+        check(got, p, order, 5000, 64, strict=False)
+        # scores that are no numbers, infinite, and huge
+        x = torch.randn(K, V, generator=gen(3)).to(dt)
+        for s in ([nan, -1, -inf, -2, -3, -4], [inf, -1, -2, -3, nan, -5], [-1e30, -1e30, -2e30, -3e38, 1e30, 0]):
+            scores = torch.tensor([s], dtype=torch.float32)
+            got = gbla.beam_select(gbla.beam_shape(1, K, V, 20, dtype=dtype), x.cuda(), scores.cuda())
+            p, order = reference(x, scores, V, 20)
+            sc, tok, par, _ = got
+            if inf in s:  # all of beam 0's are infinitely good: by token
+                assert (par[0] == 0).all() and tok[0].tolist() == list(range(20)) and (sc[0] == inf).all()
+            else:
+                check(got, p, order, V, 20, strict=max(abs(v) for v in s if abs(v) < inf) < 100)
+
+
+def test_beam_order_of_close_candidates():
+    """Rows that differ in one far logit, so that their logarithms are some 2^-20 apart: fp32 would see ties."""
+    V, K = 3000, 32
+    x = (torch.randn(1, V, generator=gen(5)) * 2).repeat(K, 1)
+    for k in range(K):  # a different mass in one token, the same best ones
+        x[k, V - 1] = -9 + 0.01 * ((k * 11) % K)
+    scores = torch.zeros(1, K)
+    beam = gbla.beam_shape(1, K, V, K, dtype="f32")
+    got = gbla.beam_select(beam, x.cuda(), scores.cuda())
+    p, order = reference(x, scores, V, K)
+    best = p[0].max()
+    gaps = -np.diff(np.sort(-p[0])[:K] * -1)
+    assert gaps.max() < 2.0 ** -20 and best > -20  # what fp32 could not tell apart
+    check(got, p, order, V, K)
+
+
+def test_beam_a_large_call_by_spot_checks():
+    B, K, V = 64, 16, 32768
+    v, x, scores = make(B, K, V, "bf16", seed=3)
+    beam = gbla.beam_shape(B, K, V)
+    ws = gbla.beam_workspace(beam)
+    got = gbla.beam_select(beam, v, scores.cuda(), ws=ws)
+    for b in (0, 31, 63):
+        p, order = reference(x[b * K:(b + 1) * K], scores[b:b + 1], V, K)
+        check([None if t is None else t[b:b + 1] for t in got], p, order, V, K)
+
+
+def test_beam_offsets_beyond_32_bits():
+    B, K, V = 2, 40, 1 << 24
+    x = torch.full((B * K, V), -8.0, dtype=torch.bfloat16, device="cuda")
+    want = {}
+    for i, (b, k, t) in enumerate([(1, 39, V - 1), (1, 38, V - 2), (0, 39, 12345678), (1, 0, 0), (0, 0, V - 1)]):
+        x[b * K + k, t] = 30 - i
+        want.setdefault(b, []).append((k, t))
+    scores = torch.zeros(B, K, device="cuda")
+    sc, tok, par, _ = gbla.beam_select(gbla.beam_shape(B, K, V, 3), x, scores)
+    for b, pairs in want.items():
+        assert list(zip(par[b].tolist(), tok[b].tolist()))[:len(pairs)] == pairs or \
+            set(list(zip(par[b].tolist(), tok[b].tolist()))[:len(pairs)]) == set(pairs)
+
+
+# ------------------------------------------------------------------ reorder
+@pytest.mark.parametrize("dtype,width,offset", [(torch.float32, 512, 0), (torch.float32, 5, 0), (torch.float32, 64, 1), (torch.bfloat16, 33, 0), (torch.uint8, 1, 0),
+                                                (torch.bfloat16, 8, 4), (torch.uint8, 100, 3), (torch.float32, 5000, 0), (torch.float64, 3, 0)])
+@pytest.mark.parametrize("B,K", [(1, 1), (3, 8), (2, 100), (1, 1024), (70, 16)])
+def test_reorder_moves_rows(dtype, width, offset, B, K):
+    n = max(1, K // 2 + 1)
+    raw = torch.randint(0, 100, (B * K * width + offset + 16,), generator=gen(K), dtype=torch.uint8).to(dtype).cuda()
+    src = raw[offset:offset + B * K * width].view(B * K, width)
+    keep = raw.clone()
+    beam = gbla.beam_shape(B, K, 50, n)
+    parents = torch.randint(0, K, (B, n), generator=gen(7), dtype=torch.int32).cuda()
+    out = torch.full((B * n * width + offset + 16,), 7, dtype=torch.uint8).to(dtype).cuda()
+    dst = out[offset:offset + B * n * width].view(B * n, width)
+    plan = gbla.beam_reorder_plan(beam, [src], [dst])
+    gbla.beam_reorder(plan, parents)
+    assert gbla.gbla_check_device_status(plan.ws) == gbla.GBLA_OK
+    rows = (parents.long() + torch.arange(B, device="cuda")[:, None] * K).view(-1)
+    assert torch.equal(dst, src[rows]) and torch.equal(raw, keep)
+    assert (out[:offset].float() == 7).all() and (out[offset + dst.numel():].float() == 7).all()
+    # in place, with repeated, crossed and unmoved rows
+    inplace = gbla.beam_shape(B, K, 50)
+    parents = torch.randint(0, K, (B, K), generator=gen(8), dtype=torch.int32).cuda()
+    parents[0] = torch.arange(K - 1, -1, -1)
+    want = src[(parents.long() + torch.arange(B, device="cuda")[:, None] * K).view(-1)]
+    gbla.beam_reorder(gbla.beam_reorder_plan(inplace, [src]), parents)
+    assert torch.equal(src, want)
+    assert torch.equal(raw[:offset], keep[:offset]) and torch.equal(raw[offset + src.numel():], keep[offset + src.numel():])
+
+
+def test_reorder_many_tensors_and_bad_parents():
+    B, K = 3, 4
+    beam = gbla.beam_shape(B, K, 10)
+    states = [torch.randn(B * K, 1 + j % 7, generator=gen(j)).cuda() for j in range(150)] + [torch.empty(B * K, 0, device="cuda")]
+    before = [s.clone() for s in states]
+    parents = torch.tensor([[1, 0, 0, 3], [3, 3, 3, 3], [0, 1, 2, 3]], dtype=torch.int32, device="cuda")
+    plan = gbla.beam_reorder_plan(beam, states)
+    gbla.beam_reorder(plan, parents)
+    assert gbla.gbla_check_device_status(plan.ws) == gbla.GBLA_OK
+    rows = (parents.long() + torch.arange(B, device="cuda")[:, None] * K).view(-1)
+    for s, t in zip(states, before):
+        assert torch.equal(s, t[rows])
+    for bad in (-1, K, 2 ** 31 - 1):  # reported, and its row stays
+        t = [s.clone() for s in states]
+        parents[1, 2] = bad
+        gbla.beam_reorder(plan, parents)
+        assert gbla.gbla_check_device_status(plan.ws) == gbla.GBLA_ERR_DEVICE_CHECK
+        good = torch.where(parents < 0, 2, torch.where(parents >= K, 2, parents))
+        rows = (good.long() + torch.arange(B, device="cuda")[:, None] * K).view(-1)
+        for s, u in zip(states, t):
+            assert torch.equal(s, u[rows])
+    empty = gbla.beam_reorder_plan(beam, [])
+    gbla.beam_reorder(empty, parents.clamp(0, K - 1))
+    assert gbla.gbla_check_device_status(empty.ws) == gbla.GBLA_OK
+
+
+def test_beam_on_streams_and_in_graphs():
+    B, K, V = 4, 8, 1000
+    beam = gbla.beam_shape(B, K, V, eos=5)
+    data = [make(B, K, V, seed=s) for s in (1, 2)]
+    ws = gbla.beam_workspace(beam)
+    state0 = torch.randn(B * K, 24, generator=gen(0)).cuda()
+    want = []
+    for v, _, sc in data:
+        st = state0.clone()
+        out = gbla.beam_select(beam, v, sc.cuda(), ws=ws)
+        gbla.beam_reorder(gbla.beam_reorder_plan(beam, [st]), out[2])
+        want.append((*out, st))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = gbla.beam_select(beam, data[0][0], data[0][2].cuda(), ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(other, want[0]):
+        assert torch.equal(a, b)
+    x, sc, st = data[0][0].contiguous().clone(), data[0][2].cuda(), state0.clone()
+    out = tuple(torch.empty_like(t) for t in want[0][:4])
+    plan = gbla.beam_reorder_plan(beam, [st])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gbla.beam_select(beam, x, sc, out=out, ws=ws)
+        gbla.beam_reorder(plan, out[2])
+    for k in (1, 0):
+        x.copy_(data[k][0])
+        sc.copy_(data[k][2])
+        st.copy_(state0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*out, st), want[k]):
+            assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- together
+def sigmoid(x):
+    return 1 / (1 + np.exp(-x))
+
+
+def test_decoding_loop():
+    """Tokens in, best beams out, three steps: embedding, norm, one step of the recurrence with its state in place, norm, logits,
+    selection among the allowed, states after their parents; against the same in numpy in 64 bits.  Scores by a bound: each
+    step's logits are off by the roundings of fp32 (200 E of values up to 4, times the row sums of the products, below 60)."""
+    B, K, V, d = 2, 5, 61, 24
+    g = gen(11)
+    f = lambda *s, k=1.0: torch.randn(*s, generator=g) * k  # noqa: E731
+    table, W, head, lam = f(V, d), f(d, 3 * d, k=d ** -0.5), f(d, V, k=1.5 * d ** -0.5), f(d, k=0.5)
+    w1, b1, w2, b2 = 1 + f(d, k=0.1), f(d, k=0.1), 1 + f(d, k=0.1), f(d, k=0.1)
+    ok = torch.rand(B * K, V, generator=g).numpy() < 0.5
+    cu = lambda t: t.float().cuda()  # noqa: E731
+    shape, beam = gbla.glr_shape(B * K, 1, d, dtype="f32"), gbla.beam_shape(B, K, V, dtype="f32", eos=2)
+    h = torch.zeros(B * K, d, device="cuda")
+    tokens = torch.randint(0, V, (B, 1), generator=g, dtype=torch.int32).repeat(1, K).contiguous().cuda()
+    scores = torch.full((B, K), -math.inf)
+    scores[:, 0] = 0
+    scores, done = scores.cuda(), torch.zeros(B, K, dtype=torch.bool, device="cuda")
+    plan = gbla.beam_reorder_plan(beam, [h])
+    allowed = pack(ok).cuda()
+    # the same in 64 bits
+    h64, t64 = np.zeros((B * K, d)), tokens.cpu().numpy().reshape(-1)
+    s64, d64 = scores.cpu().double(), torch.zeros(B, K, dtype=torch.bool)
+    n64 = lambda t: t.double().numpy()  # noqa: E731
+
+    def norm(s, w, b):
+        c = s - s.mean(1, keepdims=True)
+        return c / np.sqrt((c ** 2).mean(1, keepdims=True) + 1e-5) * n64(w) + n64(b)
+    for step in range(3):
+        e = gbla.embed_forward(shape, tokens.view(-1), cu(table), scale=2.0)
+        y, _, _ = gbla.layer_norm_forward(shape, e, cu(w1), cu(b1))
+        xri = y @ cu(W)
+        z, _, _ = gbla.glr_forward(shape, xri[:, :d], xri[:, d:2 * d], xri[:, 2 * d:], cu(lam), h0=h, hT=h)
+        o, _, _ = gbla.layer_norm_forward(shape, z, cu(w2), cu(b2), res=e)
+        scores, tok, parents, done = gbla.beam_select(beam, o @ cu(head), scores, allowed=allowed, done=done)
+        gbla.beam_reorder(plan, parents)
+        tokens = tok
+        e6 = np.where(t64[:, None] >= 0, 2 * n64(table)[t64.clip(0)], 0)
+        q = norm(e6, w1, b1) @ n64(W)
+        a = np.exp(-8.0 * np.log1p(np.exp(n64(lam))) * sigmoid(q[:, d:2 * d]))
+        h64 = a * h64 + np.sqrt(1 - a * a) * sigmoid(q[:, 2 * d:]) * q[:, :d]
+        logits = norm(h64 + e6, w2, b2) @ n64(head)
+        p, order = reference(torch.from_numpy(logits), s64, V, K, ok, d64, 2)
+        live = np.sort(-p, axis=1)[:, :K + 1]
+        assert (np.diff(live[np.isfinite(live).all(1)], axis=1) > 1e-4).all()  # the best are far enough apart to compare
+        par, tk = order // V, order % V
+        assert np.array_equal(parents.cpu().numpy(), par) and np.array_equal(tok.cpu().numpy(), tk)
+        s64 = torch.from_numpy(np.take_along_axis(p, order, 1))
+        d64 = torch.gather(d64, 1, torch.from_numpy(par)) | torch.from_numpy(tk == 2)
+        assert torch.equal(done.cpu(), d64)
+        assert (scores.cpu().double() - s64).abs().max() <= 200 * E * 4 * 60 * (step + 1)
+        h64 = h64[(par + np.arange(B)[:, None] * K).reshape(-1)]
+        t64 = tk.reshape(-1)
+        assert np.abs(h.cpu().double().numpy() - h64).max() <= 200 * E * 4 * (step + 1) + 1e-4
+
+
+def test_training_step_with_the_update():
+    """ids -> embedding -> norm -> the layer -> norm with its residual, their gradients into one AdamW plan; the gradients of the
+    embedding and the norms against differences of the whole's loss in the directions that they give.  The loss is summed in 64
+    bits; the step of 2^-6 of each tensor's size leaves 0.05 of the derivative for the second differences and the layer's fp32."""
+    B, L, d, H, dh, V = 2, 48, 64, 2, 32, 40
+    n = H * dh
+    g = gen(21)
+    f = lambda *s, k=1.0: (torch.randn(*s, generator=g) * k).cuda()  # noqa: E731
+    P = {"conv_w": f(d, 4, k=0.5), "conv_b": f(d, k=0.1), **{k: f(d, n, k=d ** -0.5) for k in ("W_q", "W_k", "W_v", "W_r")},
+         "w_g": f(d, H, k=d ** -0.5), "b_g": f(H, k=0.1), "rms_w": 1 + f(dh, k=0.1),
+         "table": f(V, d, k=0.2), "n1_w": 1 + f(d, k=0.1), "n1_b": f(d, k=0.1), "n2_w": 1 + f(d, k=0.1), "n2_b": f(d, k=0.1)}
+    ids = torch.randint(0, V, (B * L,), generator=g, dtype=torch.int32).cuda()
+    lens = torch.tensor([48, 31], dtype=torch.int32, device="cuda")
+    shape = gbla.make_shape(B, L, d, H, dh, dtype="f32", seq_lens=lens)
+    target = f(B * L, d)
+
+    def forward(P):
+        e = gbla.embed_forward(shape, ids, P["table"], scale=8.0)
+        x, _, st1 = gbla.layer_norm_forward(shape, e, P["n1_w"], P["n1_b"], stats=True)
+        y, saved = gbla.gbla_forward(shape, x, P, saved=True)
+        o, s, st2 = gbla.layer_norm_forward(shape, y, P["n2_w"], P["n2_b"], res=e, stats=True)
+        return float((o.double() * target.double()).sum()), (e, x, st1, saved, s, st2)
+    loss, (e, x, st1, saved, s, st2) = forward(P)
+    g2 = gbla.layer_norm_backward(shape, s, P["n2_w"], st2, target)
+    grads = gbla.gbla_backward(shape, x, P, saved, g2["dx"])
+    g1 = gbla.layer_norm_backward(shape, e, P["n1_w"], st1, grads["dx"], ds=g2["dx"])  # e goes on as the residual too
+    grads.update(dtable=gbla.embed_backward(shape, ids, g1["dx"], V, scale=8.0), dn1_w=g1["dw"], dn1_b=g1["db"], dn2_w=g2["dw"], dn2_b=g2["db"])
+    for k in ("table", "n1_w", "n1_b", "n2_w", "n2_b"):
+        dirn = grads["d" + k] / grads["d" + k].norm()
+        h = 2.0 ** -6 * float(P[k].norm()) / math.sqrt(P[k].numel())
+        lo, hi = (forward({**P, k: P[k] + c * h * dirn})[0] for c in (-1, 1))
+        want = float(grads["d" + k].norm())
+        assert abs((hi - lo) / (2 * h) - want) <= 0.05 * want, k
+    state = gbla.gbla_adamw_state(P)
+    plan = gbla.gbla_adamw_plan(P, grads, state)
+    before = {k: v.clone() for k, v in P.items()}
+    gbla.gbla_adamw_step(plan, lr=1e-3, norm=gbla.gbla_grad_norm(plan), max_norm=1.0)
+    torch.cuda.synchronize()
+    assert int(state["step"]) == 1 and all(not torch.equal(before[k], P[k]) for k in P)
