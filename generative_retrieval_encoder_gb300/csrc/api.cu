@@ -651,7 +651,7 @@ gbla_status ws_status(const void* ws, size_t have, size_t need) {
   return !ws || !aligned(ws, kAlign) || have < need ? GBLA_ERR_WORKSPACE : GBLA_OK;
 }
 
-struct EmbedLayout { size_t sums, range, zero_bytes, keys[2], slots[2], count, part, total; int passes, bits; };
+struct EmbedLayout { size_t sums, range, zero_bytes, keys[2], slots[2], count, part, longs, total; int passes, bits; };
 gbla_status embed_plan(const gbla_shape* s, int64_t vocab, int k, RowPlan& p) {
   const gbla_status r = make_row_plan(s, p);
   if (r != GBLA_OK) return r;
@@ -679,6 +679,7 @@ EmbedLayout embed_layout(const RowPlan& p, int64_t vocab, int k, bool backward) 
     }
     l.count = c.take(tiles > 1 ? tiles * (4u << kEmbedDigit) : 0);
     l.part = c.take(2 * ((n + kEmbedCap - 1) / kEmbedCap) * p.d * 4);
+    l.longs = c.take((n / kEmbedCap + 1) * 8);
   }
   l.total = c.off;
   return l;
@@ -1344,7 +1345,7 @@ gbla_status embed_forward(const gbla_shape* shape, const void* ids, int wide_ids
   const RowCtx c{static_cast<cudaStream_t>(stream)};
   EmbedArgs a = embed_args(p, ids, wide_ids, k, vocab, scale, ws);
   a.table = table; a.y = y;
-  if (embed_fwd_ctas(a, p.f32) > 1) GBLA_CHECK(cudaMemsetAsync(a.err, 0, sizeof(int), c.st), "memset");
+  if (embed_fwd_ctas(a, p.f32) > 1) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
   GBLA_CHECK(launch_embed_fwd(a, p.f32, c.st), "embed fwd");
   return GBLA_OK;
 }
@@ -1372,7 +1373,9 @@ gbla_status embed_backward(const gbla_shape* shape, const void* ids, int wide_id
   s.count = at<int>(ws, l.count);
   s.range = at<int2>(ws, l.range);
   s.part = at<float>(ws, l.part);
-  GBLA_CHECK(cudaMemsetAsync(ws, 0, l.zero_bytes, c.st), "memset");
+  s.n_long = at<int>(ws, 4);
+  s.longs = at<int2>(ws, l.longs);
+  GBLA_CHECK(launch_zero(ws, l.zero_bytes, c.st), "clear");
   const int groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
   for (int i = 0; i < (s.tiles == 1 ? 1 : l.passes); ++i) {
     s.key_in = s.keys[(i + 1) & 1]; s.slot_in = s.slots[(i + 1) & 1];
@@ -1412,7 +1415,7 @@ gbla_status layer_norm_forward(const gbla_shape* shape, const void* x, int64_t l
   const RowCtx c{static_cast<cudaStream_t>(stream)};
   LnArgs a = ln_args(p, x, ldx, w, ws);
   a.res = res; a.b = b; a.eps = eps; a.sum = sum; a.y = y; a.stats = stats;
-  if (a.lens) GBLA_CHECK(cudaMemsetAsync(a.err, 0, sizeof(int), c.st), "memset");
+  if (a.lens) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
   GBLA_CHECK(launch_ln(a, p.f32, false, c.st), "layer norm fwd");
   return GBLA_OK;
 }
@@ -1432,7 +1435,7 @@ gbla_status layer_norm_backward(const gbla_shape* shape, const void* x, int64_t 
   LnArgs a = ln_args(p, x, ldx, w, ws);
   a.stats = const_cast<float*>(stats); a.dy = dy; a.ds = ds; a.dx = dx;
   a.part = dw || db ? at<float>(ws, kAlign) : nullptr;
-  if (a.lens) GBLA_CHECK(cudaMemsetAsync(a.err, 0, sizeof(int), c.st), "memset");
+  if (a.lens) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
   GBLA_CHECK(launch_ln(a, p.f32, true, c.st), "layer norm bwd");
   if (!a.part) return GBLA_OK;
   if (!ln_group(p.d)) GBLA_CHECK(launch_ln_cols_long(a, p.f32, c.st), "layer norm cols");

@@ -4,8 +4,7 @@
 //
 // The gradient goes by sorted slots, so that each row of the table is written once, in one fixed order of its slots: a stable
 // counting sort by the id's digits (no CTA waits for another: a tile's place among its digit's keys comes from the counts of
-// the tiles before it), each id's range in the sorted order, then a group of threads per table row.  An id of more than
-// kEmbedCap slots is summed in pieces of kEmbedCap sorted places, whose partial sums a last kernel adds in order.
+// the tiles before it), each id's range in the sorted order, then the sums, kEmbedCap sorted places a group of threads.
 #include <algorithm>
 
 #include "common.cuh"
@@ -126,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_count(const EmbedArgs a, con
 
 // Exclusive sums over `bins` values of smem by the CTA, `v` in place.
 __device__ __forceinline__ void scan_bins(int* v, int bins, int* red) {
-  constexpr int P = kMaxBins / kThreads;
+  constexpr int P = (kMaxBins + kThreads - 1) / kThreads;
   int own[P], sum = 0;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
@@ -199,9 +198,9 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
         sum += c;
       }
       if (!ALL) {
-        const int g0 = tile / kEmbedTiles, groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
+        const int groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
         sum = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int g = 0; g < groups; ++g) sum += s.sums[(int64_t)g * kMaxBins + i];
       }
       base[i] = sum;
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
         int sum = base[i];
 #pragma unroll 4
         for (int g = 0; g < g0; ++g) sum += s.sums[(int64_t)g * kMaxBins + i];
-#pragma unroll 8
+#pragma unroll 16
         for (int t = g0 * kEmbedTiles; t < tile; ++t) sum += s.count[(int64_t)t * kMaxBins + i];
         base[i] = sum;
       }
@@ -253,122 +252,161 @@ __global__ void __launch_bounds__(kThreads) k_embed_mark(const EmbedArgs a, cons
 }
 
 // ------------------------------------------------------------------ the sums
-// The sums of the thread's E columns from column c of the rows of slots [lo, hi), in order, eight rows in flight.
-template <typename T, int E, bool WIDE>
-__device__ __forceinline__ void sum_rows(float (&acc)[E], const EmbedArgs& a, const int* slot, int lo, int hi, int c, int step) {
+// A chunk is kEmbedCap places of the sorted order.  Runs (the places of one id) of up to kEmbedCap places are summed by the chunk
+// in which they begin, also past its end; each chunk sums its part of a longer run into a partial row: 2 c for the run that its
+// first place is in, 2 c + 1 for one that begins later.  So a group of threads goes through a chunk's rows of dy at a stretch,
+// eight of them in flight whatever ids they are of, and stores a sum where the id changes.
+template <typename T, bool WIDE>
+struct Sum {
+  static constexpr int E = 16 / sizeof(T);
+  float v[E];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int j = 0; j < E; ++j) acc[j] = 0.f;
-  const T* dy = static_cast<const T*>(a.dy);
-  constexpr int U = WIDE ? 8 : 2;
-  for (int i = lo; i < hi; i += U) {
-    int at[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) at[u] = i + u < hi ? slot[i + u] : -1;
+    for (int j = 0; j < E; ++j) v[j] = 0.f;
+  }
+  __device__ __forceinline__ void store(float scale, float* out, int c, int d, int step) const {
     if (WIDE) {
-      uint4 w[U];
+      if (c >= d) return;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        w[u] = make_uint4(0, 0, 0, 0);
-        if (at[u] >= 0 && c < a.d) w[u] = __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)at[u] * a.d + c));
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (at[u] < 0) continue;
-        const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          acc[j] += sizeof(T) == 2 ? (j & 1 ? bf_hi(q[(j / 2) & 3]) : bf_lo(q[(j / 2) & 3])) : __uint_as_float(q[j & 3]);
-      }
+      for (int j = 0; j < E; j += 4)
+        *reinterpret_cast<float4*>(out + c + j) = make_float4(v[j] * scale, v[j + 1] * scale, v[j + 2] * scale, v[j + 3] * scale);
     } else {
-      float w[U][E];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < E; ++j) w[u][j] = at[u] >= 0 && c + j * step < a.d ? to_f(dy[(int64_t)at[u] * a.d + c + j * step]) : 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < E; ++j) acc[j] += w[u][j];
+      for (int j = 0; j < E; ++j)
+        if (c + j * step < d) out[c + j * step] = v[j] * scale;
     }
   }
-}
-template <int E, bool WIDE>
-__device__ __forceinline__ void put(const float (&acc)[E], float scale, float* out, int c, int d, int step) {
-  if (WIDE) {
-    if (c >= d) return;
-#pragma unroll
-    for (int j = 0; j < E; j += 4)
-      *reinterpret_cast<float4*>(out + c + j) = make_float4(acc[j] * scale, acc[j + 1] * scale, acc[j + 2] * scale, acc[j + 3] * scale);
-  } else {
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (c + j * step < d) out[c + j * step] = acc[j] * scale;
-  }
-}
+};
 
-// Groups of G threads, G E columns each.  The first `piece_ctas` CTAs take pieces of the sorted places for ids of many slots
-// (at most the one that enters the piece and the one that leaves it), the others a table row's columns.
+// Groups of G threads, G E columns each.  The first `chunk_ctas` CTAs take chunks, the others the rows of ids without a slot: a
+// warp 32 table rows.
 template <typename T, int G, bool WIDE>
-__global__ void __launch_bounds__(kThreads) k_embed_rows(const EmbedArgs a, const int* key, const int* slot, const int2* range,
-                                                         float* part, int blocks, int piece_ctas) {
+__global__ void __launch_bounds__(kThreads) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
   pdl_enter();
-  constexpr int E = 16 / sizeof(T);
-  const int t = threadIdx.x % G;
-  const bool pieces = (int)blockIdx.x < piece_ctas;
-  const int64_t task = ((int64_t)blockIdx.x - (pieces ? 0 : piece_ctas)) * (kThreads / G) + threadIdx.x / G;
-  const int64_t item = task / blocks;
-  const int col = (int)(task - item * blocks) * G * E, c = col + (WIDE ? t * E : t);
-  float acc[E];
-  if (!pieces) {
-    if (item >= a.V) return;
-    const int2 r = range[item];
-    const int n = r.y - r.x;
-    if (n > kEmbedCap) return;
-    sum_rows<T, E, WIDE>(acc, a, slot, r.x, r.y, c, G);
-    put<E, WIDE>(acc, a.scale, a.dtable + item * a.d, c, a.d, G);
+  constexpr int E = 16 / sizeof(T), U = WIDE ? 8 : 2;
+  if ((int)blockIdx.x >= chunk_ctas) {
+    const int64_t v0 = (((int64_t)blockIdx.x - chunk_ctas) * (kThreads / 32) + (threadIdx.x >> 5)) * 32;
+    const int lane = threadIdx.x & 31;
+    bool none = false;
+    if (v0 + lane < a.V) {
+      const int2 r = s.range[v0 + lane];
+      none = r.x == r.y;
+    }
+    for (unsigned m = __ballot_sync(FULL, none); m; m &= m - 1) {
+      float* out = a.dtable + (v0 + __ffs(m) - 1) * a.d;
+      if (a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0)
+        for (int c = lane * 4; c < a.d; c += 128) *reinterpret_cast<float4*>(out + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      else
+        for (int c = lane; c < a.d; c += 32) out[c] = 0.f;
+    }
     return;
   }
-  const int64_t lo = item * kEmbedCap;
+  const int t = threadIdx.x % G;
+  const int64_t task = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
+  const int64_t chunk = task / blocks;
+  const int c = (int)(task - chunk * blocks) * G * E + (WIDE ? t * E : t);
+  const int64_t lo = chunk * kEmbedCap;
   if (lo >= a.n) return;
   const int64_t hi = min(a.n, lo + kEmbedCap);
+  const int *key = s.key_out, *slot = s.slot_out;
+  const T* dy = static_cast<const T*>(a.dy);
+  // the places to go through
   const int k0 = key[lo], k1 = key[hi - 1];
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int k = which ? k1 : k0;
-    if (k >= a.V || (which && k1 == k0)) continue;
-    const int2 r = range[k];
-    if (r.y - r.x <= kEmbedCap) continue;
-    sum_rows<T, E, WIDE>(acc, a, slot, (int)max((int64_t)r.x, lo), (int)min((int64_t)r.y, hi), c, G);
-    put<E, WIDE>(acc, 1.f, part + (2 * item + which) * a.d, c, a.d, G);
+  int from = (int)lo, to = (int)hi;
+  int l1 = (int)lo, m0 = 0x7fffffff;  // of long runs: places below l1 and from m0 on
+  const int2 none = make_int2(0, 0), r0 = k0 < a.V ? s.range[k0] : none, r1 = k1 < a.V ? s.range[k1] : none;
+  if (k0 >= a.V) return;  // sorted last: nothing but slots without an id
+  if (r0.y - r0.x > kEmbedCap) l1 = min(r0.y, (int)hi);
+  else if (r0.x < lo) from = r0.y;  // another chunk's
+  if (k1 >= a.V) {
+    // the ids end in this chunk: behind the last of them
+    int x = (int)lo, y = (int)hi - 1;  // key[x] < V <= key[y]
+    while (y - x > 1) {
+      const int mid = (x + y) >> 1;
+      if (key[mid] < a.V) x = mid; else y = mid;
+    }
+    to = y;
+  } else if (r1.y - r1.x <= kEmbedCap) {
+    to = r1.y;
+  } else if (k1 != k0) {
+    m0 = r1.x;
+    if (t == 0 && c < G * E) {  // a long run's first chunk lists it
+      const int at = atomicAdd(s.n_long, 1);
+      s.longs[at] = make_int2(k1, (int)(2 * chunk + 1));
+    }
   }
+  if (l1 > lo && r0.x == lo && t == 0 && c < G * E) {
+    const int at = atomicAdd(s.n_long, 1);
+    s.longs[at] = make_int2(k0, (int)(2 * chunk));
+  }
+  Sum<T, WIDE> acc;
+  acc.clear();
+  int now = -1;
+  auto flush = [&](int i) {  // the sum of the run whose last place is i - 1
+    if (now < 0) return;
+    if (i - 1 < l1) acc.store(1.f, s.part + 2 * chunk * a.d, c, a.d, G);
+    else if (i - 1 >= m0) acc.store(1.f, s.part + (2 * chunk + 1) * a.d, c, a.d, G);
+    else acc.store(a.scale, a.dtable + (int64_t)now * a.d, c, a.d, G);
+  };
+  for (int i = from; i < to; i += U) {
+    int k[U], at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      k[u] = i + u < to ? key[i + u] : -1;
+      at[u] = i + u < to ? slot[i + u] : -1;
+    }
+    uint4 w[U];
+    float f[U][WIDE ? 1 : E];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (WIDE) {
+        w[u] = make_uint4(0, 0, 0, 0);
+        if (at[u] >= 0 && c < a.d) w[u] = __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)at[u] * a.d + c));
+      } else {
+#pragma unroll
+        for (int j = 0; j < (WIDE ? 1 : E); ++j) f[u][j] = at[u] >= 0 && c + j * G < a.d ? to_f(dy[(int64_t)at[u] * a.d + c + j * G]) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k[u] < 0) continue;
+      if (k[u] != now) {
+        flush(i + u);
+        now = k[u];
+        acc.clear();
+      }
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        acc.v[j] += !WIDE ? f[u][WIDE ? 0 : j] : sizeof(T) == 2 ? (j & 1 ? bf_hi(q[(j / 2) & 3]) : bf_lo(q[(j / 2) & 3])) : __uint_as_float(q[j & 3]);
+      }
+    }
+  }
+  flush(to);
 }
 
-// The ids of many slots: the CTA of the piece in which one begins adds its pieces' sums of 32 columns, a warp every eighth
-// piece, in 64 bits.
-__global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, const int* key, const int2* range, const float* part) {
+// The ids of long runs: a CTA adds the partial rows of one, 32 columns, a warp every eighth of them, in 64 bits.
+__global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, const EmbedSort s) {
   pdl_enter();
   __shared__ double red[kThreads / 32][32];
-  const int64_t item = blockIdx.x, lo = item * kEmbedCap, hi = min(a.n, lo + kEmbedCap);
-  const int k0 = key[lo], k1 = key[hi - 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.y * 32 + lane;
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int k = which ? k1 : k0;
-    if (k >= a.V || (which && k1 == k0)) continue;
-    const int2 r = range[k];
-    if (r.y - r.x <= kEmbedCap || r.x < lo) continue;
-    const int64_t last = (r.y - 1) / kEmbedCap;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = (a.d + 31) / 32;
+  const int64_t tasks = (int64_t)*s.n_long * blocks;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int which = (int)(task / blocks), c = (int)(task - (int64_t)which * blocks) * 32 + lane;
+    const int2 run = s.longs[which];
+    const int64_t first = run.y, last = 2 * (int64_t)((s.range[run.x].y - 1) / kEmbedCap);
     double sum = 0.;
     if (c < a.d) {
-#pragma unroll 4
-      for (int64_t p = item + warp; p <= last; p += kThreads / 32) sum += part[(2 * p + (p == item ? which : 0)) * a.d + c];
+      if (warp == 0) sum = s.part[first * a.d + c];
+#pragma unroll 8
+      for (int64_t p = (first | 1) + 1 + 2 * warp; p <= last; p += 2 * (kThreads / 32)) sum += s.part[p * a.d + c];
     }
     __syncthreads();
     red[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && c < a.d) {
       for (int w = 1; w < kThreads / 32; ++w) sum += red[w][lane];
-      a.dtable[(int64_t)k * a.d + c] = (float)(sum * (double)a.scale);
+      a.dtable[(int64_t)run.x * a.d + c] = (float)(sum * (double)a.scale);
     }
   }
 }
@@ -376,16 +414,20 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, cons
 template <typename T, bool WIDE>
 cudaError_t rows(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st) {
   constexpr int E = 16 / sizeof(T);
-  const int pieces = (int)((a.n + kEmbedCap - 1) / kEmbedCap);
+  const int64_t chunks = (a.n + kEmbedCap - 1) / kEmbedCap, empty = ((int64_t)a.V + kThreads - 1) / kThreads;
   auto go = [&](auto kernel, int G) {
     const int blocks = (a.d + G * E - 1) / (G * E), per = kThreads / G;
-    const int64_t pc = ((int64_t)pieces * blocks + per - 1) / per, rc = ((int64_t)a.V * blocks + per - 1) / per;
-    return launch_pdl(kernel, dim3((unsigned)(pc + rc)), dim3(kThreads), 0, st, a, (const int*)s.key_out, (const int*)s.slot_out,
-                      (const int2*)s.range, s.part, blocks, (int)pc);
+    const int64_t ctas = (chunks * blocks + per - 1) / per;
+    return launch_pdl(kernel, dim3((unsigned)(ctas + empty)), dim3(kThreads), 0, st, a, s, blocks, (int)ctas);
   };
   const int v = (a.d + E - 1) / E;
   return v <= 4 ? go(k_embed_rows<T, 4, WIDE>, 4) : v <= 8 ? go(k_embed_rows<T, 8, WIDE>, 8)
          : v <= 16 ? go(k_embed_rows<T, 16, WIDE>, 16) : go(k_embed_rows<T, 32, WIDE>, 32);
+}
+
+__global__ void __launch_bounds__(kThreads) k_zero(uint4* p, int64_t n) {
+  pdl_enter();
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) p[i] = make_uint4(0, 0, 0, 0);
 }
 
 // Accesses a row of the forward takes: of 16 bytes where rows and tensors allow it, of one value else.
@@ -434,8 +476,13 @@ cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, 
   return wide ? rows<bf16, true>(a, s, st) : rows<bf16, false>(a, s, st);
 }
 cudaError_t launch_embed_join(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.n + kEmbedCap - 1) / kEmbedCap), (unsigned)((a.d + 31) / 32));
-  return launch_pdl(k_embed_join, grid, dim3(kThreads), 0, st, a, (const int*)s.key_out, (const int2*)s.range, (const float*)s.part);
+  return launch_pdl(k_embed_join, dim3((unsigned)std::min<int64_t>((a.n + kEmbedCap - 1) / kEmbedCap * ((a.d + 31) / 32), sm_count() * 8)),
+                    dim3(kThreads), 0, st, a, s);
+}
+cudaError_t launch_zero(void* p, size_t bytes, cudaStream_t st) {
+  const int64_t n = (int64_t)(bytes / 16);
+  return launch_pdl(k_zero, dim3((unsigned)std::min<int64_t>((n + kThreads - 1) / kThreads, sm_count() * 8)), dim3(kThreads), 0, st,
+                    static_cast<uint4*>(p), n);
 }
 
 }  // namespace gbla

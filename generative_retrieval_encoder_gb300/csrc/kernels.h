@@ -331,10 +331,10 @@ cudaError_t launch_ln_cols_long(const LnArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_ln_cols(const LnArgs& a, float* dw, float* db, cudaStream_t st);
 
 // ------------------------------------------------------------ token embedding
-constexpr int kEmbedTile = 2048;   // keys of a CTA of the sort
+constexpr int kEmbedTile = 1024;   // keys of a CTA of the sort
 constexpr int kEmbedTiles = 32;    // tiles whose counts are also kept summed
-constexpr int kEmbedDigit = 11;    // bits of a digit, at most
-constexpr int kEmbedCap = 64;      // slots of an id that one group of threads sums; more go in pieces
+constexpr int kEmbedDigit = 8;     // bits of a digit, at most
+constexpr int kEmbedCap = 32;      // sorted places that a group of threads sums
 struct EmbedArgs {
   const void* ids; int wide_ids;      // [n] int32 or int64
   int64_t n; int k;                   // slots = tokens * k
@@ -351,7 +351,8 @@ struct EmbedSort {
   int* keys[2]; int* slots[2];        // [n] each
   int* count; int* sums;              // [tiles][2^kEmbedDigit]; the pass's [tiles / kEmbedTiles][2^kEmbedDigit], 0 on entry
   int2* range;                        // [V]: each id's sorted places, 0 on entry
-  float* part;                        // [2 * pieces][d]
+  float* part;                        // [2 * chunks][d]
+  int* n_long; int2* longs;           // how many ids have more than kEmbedCap slots, 0 on entry; each and its first partial row
 };
 int embed_fwd_ctas(const EmbedArgs& a, bool f32);
 cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st);
@@ -361,6 +362,8 @@ cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, int bits,
 cudaError_t launch_embed_mark(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st);
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st);
 cudaError_t launch_embed_join(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st);
+// Clears a multiple of 16 bytes (a launch that follows its predecessor like the kernels do; a memset waits longer).
+cudaError_t launch_zero(void* p, size_t bytes, cudaStream_t st);
 
 // ------------------------------------------------------------ beam search
 constexpr int kBeamPieces = 8;       // 16-byte pieces a lane of the rows' kernel takes

@@ -37,53 +37,67 @@ __device__ __forceinline__ int col_of(int i, int t) {
   return WIDE ? ((i / E) * G + t) * E + i % E : i * G + t;
 }
 
-// The thread's N values of a row (0 past d).
+// The thread's N values of a row as they lie in memory (0 past d): bf16 values stay two to a register until they are used.
 template <typename T, int G, int N, bool WIDE>
-__device__ __forceinline__ void load_row(float (&v)[N], const T* p, int t, int d) {
-  constexpr int E = 16 / sizeof(T);
-  if (WIDE) {
+struct Row {
+  static constexpr int E = 16 / sizeof(T);
+  uint4 w[WIDE ? N / E : 1];
+  float v[WIDE ? 1 : N];
+  __device__ __forceinline__ void load(const T* p, int t, int d) {
+    if (WIDE) {
 #pragma unroll
-    for (int i = 0; i < N; i += E) {
-      const int c = col_of<T, G, true>(i, t);
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (c < d) w = *reinterpret_cast<const uint4*>(p + c);
-      if (sizeof(T) == 2) {
-        v[i] = bf_lo(w.x); v[i + 1] = bf_hi(w.x); v[i + 2] = bf_lo(w.y); v[i + 3] = bf_hi(w.y);
-        v[i + 4 < N ? i + 4 : 0] = bf_lo(w.z); v[i + 5 < N ? i + 5 : 0] = bf_hi(w.z);
-        v[i + 6 < N ? i + 6 : 0] = bf_lo(w.w); v[i + 7 < N ? i + 7 : 0] = bf_hi(w.w);
-      } else {
-        v[i] = __uint_as_float(w.x); v[i + 1] = __uint_as_float(w.y); v[i + 2] = __uint_as_float(w.z); v[i + 3] = __uint_as_float(w.w);
+      for (int i = 0; i < N / E; ++i) {
+        const int c = (i * G + t) * E;
+        w[i] = c < d ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
       }
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = col_of<T, G, false>(i, t);
-      v[i] = c < d ? to_f(p[c]) : 0.f;
+      for (int i = 0; i < N; ++i) v[WIDE ? 0 : i] = i * G + t < d ? to_f(p[i * G + t]) : 0.f;
     }
   }
-}
-template <typename T, int G, int N, bool WIDE>
-__device__ __forceinline__ void store_row(const float (&v)[N], T* p, int t, int d) {
+  // The same by way of the thread's own places in shared memory, kThreads apart: asked for now, read when it has come.
+  __device__ static __forceinline__ void ask(uint4* mine, const T* p, int t, int d) {
+#pragma unroll
+    for (int i = 0; i < N / E; ++i) {
+      const int c = (i * G + t) * E;
+      cp_async16(smem_u32(mine + i * kThreads), p + (c < d ? c : 0), c < d ? 16 : 0);
+    }
+  }
+  __device__ __forceinline__ void take(const uint4* mine) {
+#pragma unroll
+    for (int i = 0; i < N / E; ++i) w[WIDE ? i : 0] = mine[i * kThreads];
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (WIDE ? N / E : 1); ++i) w[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < (WIDE ? 1 : N); ++i) v[i] = 0.f;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if (!WIDE) return v[WIDE ? 0 : i];
+    const uint4& q = w[WIDE ? i / E : 0];
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+    if (sizeof(T) == 2) return i & 1 ? bf_hi(u[(i % E) / 2]) : bf_lo(u[(i % E) / 2]);
+    return __uint_as_float(u[i & 3]);
+  }
+};
+// Stores the values f(0) .. f(N - 1) of the thread.
+template <typename T, int G, int N, bool WIDE, typename F>
+__device__ __forceinline__ void store_row(T* p, int t, int d, F&& f) {
   constexpr int E = 16 / sizeof(T);
   if (WIDE) {
 #pragma unroll
     for (int i = 0; i < N; i += E) {
       const int c = col_of<T, G, true>(i, t);
-      uint4 w;
-      if (sizeof(T) == 2)
-        w = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4 < N ? i + 4 : 0], v[i + 5 < N ? i + 5 : 0]),
-                       pack_bf16(v[i + 6 < N ? i + 6 : 0], v[i + 7 < N ? i + 7 : 0]));
-      else
-        w = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
-      if (c < d) *reinterpret_cast<uint4*>(p + c) = w;
+      uint32_t u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = sizeof(T) == 2 ? pack_bf16(f(i + 2 * k), f(i + 2 * k + 1)) : __float_as_uint(f(i + k));
+      if (c < d) *reinterpret_cast<uint4*>(p + c) = make_uint4(u[0], u[1], u[2], u[3]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = col_of<T, G, false>(i, t);
-      if (c < d) p[c] = from_f<T>(v[i]);
-    }
+    for (int i = 0; i < N; ++i)
+      if (i * G + t < d) p[i * G + t] = from_f<T>(f(i));
   }
 }
 
@@ -114,111 +128,138 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*red)[M]) {
 }
 
 template <typename T, int G, int N, bool WIDE>
-__global__ void __launch_bounds__(kThreads) k_ln_fwd(const LnArgs a) {
+__global__ void __launch_bounds__(kThreads, N == 32 ? 2 : !WIDE ? 3 : N * sizeof(T) <= 32 ? 5 : 4) k_ln_fwd(const LnArgs a) {
   pdl_enter();
   __shared__ float red[kThreads / 32][1];
-  constexpr int R = kThreads / G;
+  using R = Row<T, G, N, WIDE>;
   const int t = threadIdx.x % G;
   const float inv = 1.f / (float)a.d;
   if (!a.lens && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
-  float w[N], b[N];
-  if (a.w) load_row<T, G, N, WIDE>(w, static_cast<const T*>(a.w), t, a.d);
-  if (a.b) load_row<T, G, N, WIDE>(b, static_cast<const T*>(a.b), t, a.d);
-  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += (int64_t)gridDim.x * R) {  // (as often in every thread of the CTA)
-    const int64_t row = r0 + threadIdx.x / G;
-    const bool in = row < a.rows, live = in && row_valid(a, row);
-    float s[N];
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
+  const bool in = row < a.rows, live = in && row_valid(a, row);
+  float s[N];
+  {
+    R x, q;
+    x.clear();
+    q.clear();
     if (live) {
-      load_row<T, G, N, WIDE>(s, static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
-      if (a.res) {
-        float q[N];
-        load_row<T, G, N, WIDE>(q, static_cast<const T*>(a.res) + row * a.d, t, a.d);
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = to_f(from_f<T>(s[i] + q[i]));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] = 0.f;
+      x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
+      if (a.res) q.load(static_cast<const T*>(a.res) + row * a.d, t, a.d);
     }
-    if (in && a.sum) store_row<T, G, N, WIDE>(s, static_cast<T*>(a.sum) + row * a.d, t, a.d);
-    float m[1] = {0.f}, v[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < N; ++i) m[0] += s[i];
-    group_sum<G, 1>(m, red);
-    const float mean = m[0] * inv;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float c = s[i] - mean;
-      v[0] += col_of<T, G, WIDE>(i, t) < a.d ? c * c : 0.f;
-    }
-    group_sum<G, 1>(v, red);
-    const float r = live ? 1.f / sqrtf(v[0] * inv + a.eps) : 0.f;
-    if (!in) continue;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float z = (s[i] - mean) * r;
-      if (a.w) z *= w[i];
-      if (a.b) z += b[i];
-      s[i] = live ? z : 0.f;
-    }
-    store_row<T, G, N, WIDE>(s, static_cast<T*>(a.y) + row * a.d, t, a.d);
-    if (a.stats && t == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(live ? mean : 0.f, r);
+    for (int i = 0; i < N; ++i) s[i] = a.res ? to_f(from_f<T>(x.get(i) + q.get(i))) : x.get(i);
   }
+  if (in && a.sum) store_row<T, G, N, WIDE>(static_cast<T*>(a.sum) + row * a.d, t, a.d, [&](int i) { return s[i]; });
+  float m[1] = {0.f}, v[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[0] += s[i];
+  group_sum<G, 1>(m, red);
+  const float mean = m[0] * inv;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float c = s[i] - mean;
+    v[0] += col_of<T, G, WIDE>(i, t) < a.d ? c * c : 0.f;
+  }
+  group_sum<G, 1>(v, red);
+  if (!in) return;
+  const float r = live ? 1.f / sqrtf(v[0] * inv + a.eps) : 0.f;
+  R w, b;
+  if (a.w) w.load(static_cast<const T*>(a.w), t, a.d);
+  if (a.b) b.load(static_cast<const T*>(a.b), t, a.d);
+  store_row<T, G, N, WIDE>(static_cast<T*>(a.y) + row * a.d, t, a.d, [&](int i) {
+    float z = (s[i] - mean) * r;
+    if (a.w) z *= w.get(i);
+    if (a.b) z += b.get(i);
+    return live ? z : 0.f;
+  });
+  if (a.stats && t == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(live ? mean : 0.f, r);
 }
 
+// Rows that the backward asks for ahead: what is in flight covers the memory's latency with the two CTAs an SM that the column
+// sums' registers allow.
+template <typename T, int N, bool WIDE>
+constexpr int kAhead = !WIDE || N == 32 ? 0 : 2;
+
 template <typename T, int G, int N, bool WIDE>
-__global__ void __launch_bounds__(kThreads) k_ln_bwd(const LnArgs a) {
+__global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_bwd(const LnArgs a) {
   pdl_enter();
   __shared__ float red[kThreads / 32][2];
-  extern __shared__ float acc[];  // [R][G N], the groups' column sums, where the CTA has several
-  constexpr int R = kThreads / G;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  float* acc = reinterpret_cast<float*>(dyn);  // at the end: [R][G N], the groups' column sums, where the CTA has several
+  uint4* ring = reinterpret_cast<uint4*>(dyn) + threadIdx.x;  // [kAhead][3 (N / E)][kThreads]
+  constexpr int R = kThreads / G, A = kAhead<T, N, WIDE>, P = N * (int)sizeof(T) / 16;
+  using Mine = Row<T, G, N, WIDE>;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const float inv = 1.f / (float)a.d;
   if (!a.lens && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
-  float w[N], dw[N], db[N];
+  Mine w, x, y, s;
+  float dw[N], db[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    w[i] = 1.f;
-    dw[i] = db[i] = 0.f;
+  for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.f;
+  if (a.w) w.load(static_cast<const T*>(a.w), t, a.d);
+  s.clear();
+  const int64_t step = (int64_t)gridDim.x * R;
+  auto ask = [&](int64_t row, int slot) {
+    if (row < a.rows && row_valid(a, row)) {
+      uint4* to = ring + slot * 3 * P * kThreads;
+      Mine::ask(to, static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
+      Mine::ask(to + P * kThreads, static_cast<const T*>(a.dy) + row * a.d, t, a.d);
+      if (a.ds) Mine::ask(to + 2 * P * kThreads, static_cast<const T*>(a.ds) + row * a.d, t, a.d);
+    }
+    cp_async_commit();
+  };
+  if (A > 0) {
+#pragma unroll
+    for (int k = 0; k < A; ++k) ask((int64_t)blockIdx.x * R + grp + k * step, k);
   }
-  if (a.w) load_row<T, G, N, WIDE>(w, static_cast<const T*>(a.w), t, a.d);
-  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += (int64_t)gridDim.x * R) {
+  int slot = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += step) {  // (as often in every thread of the CTA)
     const int64_t row = r0 + grp;
     const bool in = row < a.rows, live = in && row_valid(a, row);
-    float z[N], g[N];
     float mean = 0.f, r = 0.f;
+    if (A > 0) cp_async_wait<(A > 0 ? A - 1 : 0)>();
     if (live) {
-      load_row<T, G, N, WIDE>(z, static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
-      load_row<T, G, N, WIDE>(g, static_cast<const T*>(a.dy) + row * a.d, t, a.d);
       const float2 st = reinterpret_cast<const float2*>(a.stats)[row];
+      if (A > 0) {
+        const uint4* from = ring + slot * 3 * P * kThreads;
+        x.take(from);
+        y.take(from + P * kThreads);
+        if (a.ds) s.take(from + 2 * P * kThreads);
+      } else {
+        x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
+        y.load(static_cast<const T*>(a.dy) + row * a.d, t, a.d);
+        if (a.ds) s.load(static_cast<const T*>(a.ds) + row * a.d, t, a.d);
+      }
       mean = st.x;
       r = st.y;
     } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = g[i] = 0.f;
+      x.clear();
+      y.clear();
+      s.clear();
     }
     float c[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      z[i] = (z[i] - mean) * r;  // past d: dy and w are 0 there
-      dw[i] += g[i] * z[i];
-      db[i] += g[i];
-      g[i] *= w[i];
-      c[0] += g[i];
-      c[1] += g[i] * z[i];
+      const float z = (x.get(i) - mean) * r, q = y.get(i), g = a.w ? q * w.get(i) : q;  // past d: dy is 0 there
+      dw[i] += q * z;
+      db[i] += q;
+      c[0] += g;
+      c[1] += g * z;
     }
     group_sum<G, 2>(c, red);
     const float c0 = c[0] * inv, c1 = c[1] * inv;
-    if (!in) continue;
-#pragma unroll
-    for (int i = 0; i < N; ++i) g[i] = r * (g[i] - c0 - z[i] * c1);
-    if (a.ds && live) {
-      load_row<T, G, N, WIDE>(z, static_cast<const T*>(a.ds) + row * a.d, t, a.d);
-#pragma unroll
-      for (int i = 0; i < N; ++i) g[i] += z[i];
+    if (in)
+      store_row<T, G, N, WIDE>(static_cast<T*>(a.dx) + row * a.d, t, a.d, [&](int i) {
+        const float z = (x.get(i) - mean) * r, q = y.get(i);
+        const float g = r * ((a.w ? q * w.get(i) : q) - c0 - z * c1);
+        return a.ds ? g + s.get(i) : g;
+      });
+    if (A > 0) {  // into the places whose values are used by now
+      ask(row + A * step, slot);
+      slot = slot + 1 == A ? 0 : slot + 1;
     }
-    store_row<T, G, N, WIDE>(g, static_cast<T*>(a.dx) + row * a.d, t, a.d);
   }
+  if (A > 0) cp_async_wait<0>();
   if (!a.part) return;
   // [CTA][dw | db][d], the CTA's rows summed in the order of its groups
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
@@ -357,6 +398,7 @@ __global__ void __launch_bounds__(1024) k_ln_cols(const float* part, int n, int 
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < 2 * (int64_t)d)
+#pragma unroll 8
     for (int k = warp; k < n; k += 32) v += part[(int64_t)k * 2 * d + c];
   red[warp][lane] = v;
   __syncthreads();
@@ -374,8 +416,13 @@ __global__ void __launch_bounds__(1024) k_ln_cols(const float* part, int n, int 
 
 template <typename T, int G, int N, bool WIDE>
 cudaError_t run(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
-  if (!bwd) return launch_pdl(k_ln_fwd<T, G, N, WIDE>, dim3((unsigned)ctas), dim3(kThreads), 0, st, a);
-  const size_t smem = a.part && kThreads / G > 1 ? (size_t)kThreads * N * 4 : 0;
+  if (!bwd) return launch_pdl(k_ln_fwd<T, G, N, WIDE>, dim3((unsigned)((a.rows + kThreads / G - 1) / (kThreads / G))), dim3(kThreads), 0, st, a);
+  const size_t ring = (size_t)kAhead<T, N, WIDE> * 3 * N * sizeof(T) * kThreads;
+  const size_t smem = std::max(ring, a.part && kThreads / G > 1 ? (size_t)kThreads * N * 4 : 0);
+  if (smem > 32 << 10) {
+    const cudaError_t e = cudaFuncSetAttribute(k_ln_bwd<T, G, N, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_pdl(k_ln_bwd<T, G, N, WIDE>, dim3((unsigned)ctas), dim3(kThreads), smem, st, a);
 }
 template <typename T, bool WIDE>
@@ -406,7 +453,7 @@ int ln_group(int d) {
 }
 int ln_ctas(int64_t rows, int d) {
   const int g = ln_group(d), per = g ? kThreads / g : 1;
-  return (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * 4);
+  return (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * 2);
 }
 int ln_parts(int64_t rows, int d) { return ln_group(d) ? ln_ctas(rows, d) : (int)std::min<int64_t>(rows, 16); }
 
