@@ -651,7 +651,7 @@ gbla_status ws_status(const void* ws, size_t have, size_t need) {
   return !ws || !aligned(ws, kAlign) || have < need ? GBLA_ERR_WORKSPACE : GBLA_OK;
 }
 
-struct EmbedLayout { size_t sums, range, zero_bytes, keys[2], slots[2], count, part, longs, total; int passes, bits; };
+struct EmbedLayout { size_t sums, last, zero_bytes, keys[2], slots[2], count, part, longs, total; int passes, bits; };
 gbla_status embed_plan(const gbla_shape* s, int64_t vocab, int k, RowPlan& p) {
   const gbla_status r = make_row_plan(s, p);
   if (r != GBLA_OK) return r;
@@ -659,7 +659,7 @@ gbla_status embed_plan(const gbla_shape* s, int64_t vocab, int k, RowPlan& p) {
   if (vocab > (1LL << 30) || vocab * p.d > (1LL << 38) || k > (1 << 20) || p.rows * k > (1LL << 30)) return GBLA_ERR_UNSUPPORTED;
   return GBLA_OK;
 }
-// The workspace: the error word; of the backward also the sort's counts, two sets of keys and slots, the ids' ranges, partial sums.
+// The workspace: the error word; of the backward also the sort's counts, two sets of keys and slots, partial sums and whose they are.
 EmbedLayout embed_layout(const RowPlan& p, int64_t vocab, int k, bool backward) {
   EmbedLayout l{};
   Cursor c;
@@ -671,8 +671,8 @@ EmbedLayout embed_layout(const RowPlan& p, int64_t vocab, int k, bool backward) 
     l.passes = cdiv(bits, kEmbedDigit);
     l.bits = cdiv(bits, l.passes);
     l.sums = c.take(tiles > 1 ? l.passes * ((tiles + kEmbedTiles - 1) / kEmbedTiles) * (4u << kEmbedDigit) : 0);
-    l.range = c.take((size_t)vocab * 8);
     l.zero_bytes = c.off;
+    l.last = c.take((size_t)vocab * 4);
     for (int i = 0; i < 2; ++i) {
       l.keys[i] = c.take(n * 4);
       l.slots[i] = c.take(n * 4);
@@ -1371,7 +1371,7 @@ gbla_status embed_backward(const gbla_shape* shape, const void* ids, int wide_id
     s.slots[i] = at<int>(ws, l.slots[i]);
   }
   s.count = at<int>(ws, l.count);
-  s.range = at<int2>(ws, l.range);
+  s.last = at<int>(ws, l.last);
   s.part = at<float>(ws, l.part);
   s.n_long = at<int>(ws, 4);
   s.longs = at<int2>(ws, l.longs);
@@ -1384,9 +1384,7 @@ gbla_status embed_backward(const gbla_shape* shape, const void* ids, int wide_id
     if (s.tiles > 1) GBLA_CHECK(launch_embed_count(a, s, l.bits, i * l.bits, c.st), "embed count");
     GBLA_CHECK(launch_embed_place(a, s, l.bits, i * l.bits, c.st), "embed place");
   }
-  if (s.tiles > 1) {
-    GBLA_CHECK(launch_embed_mark(a, s, c.st), "embed mark");
-  } else {  // the one CTA went through every pass
+  if (s.tiles == 1) {  // the one CTA went through every pass
     s.key_out = s.keys[(l.passes - 1) & 1];
     s.slot_out = s.slots[(l.passes - 1) & 1];
   }

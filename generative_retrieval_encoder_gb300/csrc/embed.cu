@@ -4,7 +4,7 @@
 //
 // The gradient goes by sorted slots, so that each row of the table is written once, in one fixed order of its slots: a stable
 // counting sort by the id's digits (no CTA waits for another: a tile's place among its digit's keys comes from the counts of
-// the tiles before it), each id's range in the sorted order, then the sums, kEmbedCap sorted places a group of threads.
+// the tiles before it), then the sums, kEmbedCap sorted places a group of threads.
 #include <algorithm>
 
 #include "common.cuh"
@@ -16,7 +16,8 @@ namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kMaxBins = 1 << kEmbedDigit;
+constexpr int kMaxBins = 1 << kEmbedDigit;  // a thread's each, at most
+static_assert(kMaxBins <= kThreads, "");
 
 // The id of a slot, -1 for none.  An id past the table or a length outside [0, L] sets the error word and counts as none.
 __device__ __forceinline__ int id_of(const EmbedArgs& a, int64_t slot) {
@@ -123,44 +124,23 @@ __global__ void __launch_bounds__(kThreads) k_embed_count(const EmbedArgs a, con
   }
 }
 
-// Exclusive sums over `bins` values of smem by the CTA, `v` in place.
-__device__ __forceinline__ void scan_bins(int* v, int bins, int* red) {
-  constexpr int P = (kMaxBins + kThreads - 1) / kThreads;
-  int own[P], sum = 0;
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    const int i = threadIdx.x * P + j;
-    own[j] = i < bins ? v[i] : 0;
-    sum += own[j];
-  }
-  int inc = sum;
+// The sum of the values of the CTA's threads before this one.
+__device__ __forceinline__ int sum_before(int v, int* red) {
+  int inc = v;
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(FULL, inc, o);
     if ((threadIdx.x & 31) >= o) inc += x;
   }
   if ((threadIdx.x & 31) == 31) red[threadIdx.x >> 5] = inc;
   __syncthreads();
-  int at = inc - sum;
-  for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) at += red[w];
+  int at = inc - v;
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
-    const int i = threadIdx.x * P + j;
-    if (i < bins) v[i] = at;
-    at += own[j];
-  }
-  __syncthreads();
-}
-
-// The sorted places' boundaries: range[v] = (first place of v, the one behind its last).
-__device__ __forceinline__ void mark(const EmbedArgs& a, const int* key, int2* range, int64_t i) {
-  const int k = key[i], before = i > 0 ? key[i - 1] : -1;
-  if (k == before) return;
-  if (k < a.V) range[k].x = (int)i;
-  if (before >= 0) range[before].y = (int)i;
+  for (int w = 0; w < kThreads / 32; ++w) at += w < (int)(threadIdx.x >> 5) ? red[w] : 0;
+  return at;
 }
 
 // A tile's keys and slots to their places by the digit at `shift`.  ALL: a single tile, every pass in this one CTA, which also
-// counts, and marks the ranges.
+// counts.
 template <bool ALL>
 __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, EmbedSort s, int bits, int shift, bool first) {
   pdl_enter();
@@ -171,54 +151,52 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
   for (;;) {
     for (int i = lane; i < bins; i += 32) warp_count[warp][i] = 0;
     __syncwarp();
-    int key[kRounds], rank[kRounds];
+    int key[kRounds], rank[kRounds], own[kRounds];
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       const int64_t i = place_of(tile, r);
       key[r] = key_at(a, s, i, first);
+      own[r] = first || i >= a.n ? (int)i : s.slot_in[i];
+    }
+    // keys of the thread's digit (bins <= kThreads): of all tiles, and of the tiles before this one; on their way meanwhile
+    int all = 0, before = 0;
+    if (!ALL && threadIdx.x < bins) {
+      const int g0 = tile / kEmbedTiles, groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
+#pragma unroll 8
+      for (int g = 0; g < groups; ++g) {
+        const int c = s.sums[(int64_t)g * kMaxBins + threadIdx.x];
+        all += c;
+        before += g < g0 ? c : 0;
+      }
+#pragma unroll 16
+      for (int t = g0 * kEmbedTiles; t < tile; ++t) before += s.count[(int64_t)t * kMaxBins + threadIdx.x];
     }
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       const bool in = place_of(tile, r) < a.n;
       const int digit = (key[r] >> shift) & (bins - 1);
       const unsigned same = __match_any_sync(FULL, in ? digit : -1);
-      const int before = warp_count[warp][digit];
+      const int ahead = warp_count[warp][digit];
       __syncwarp();
-      rank[r] = before + __popc(same & ((1u << lane) - 1));
-      if (in && lane == __ffs(same) - 1) warp_count[warp][digit] = (uint16_t)(before + __popc(same));
+      rank[r] = ahead + __popc(same & ((1u << lane) - 1));
+      if (in && lane == __ffs(same) - 1) warp_count[warp][digit] = (uint16_t)(ahead + __popc(same));
       __syncwarp();
     }
     __syncthreads();
     // where each digit's keys of this tile begin: all smaller digits, then the tiles before this one
-    for (int i = threadIdx.x; i < bins; i += kThreads) {
+    if (threadIdx.x < bins) {
       int sum = 0;  // the warps' counts become each warp's start within the tile
+#pragma unroll
       for (int w = 0; w < kThreads / 32; ++w) {
-        const int c = warp_count[w][i];
-        warp_count[w][i] = (uint16_t)sum;
+        const int c = warp_count[w][threadIdx.x];
+        warp_count[w][threadIdx.x] = (uint16_t)sum;
         sum += c;
       }
-      if (!ALL) {
-        const int groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
-        sum = 0;
-#pragma unroll 8
-        for (int g = 0; g < groups; ++g) sum += s.sums[(int64_t)g * kMaxBins + i];
-      }
-      base[i] = sum;
+      if (ALL) all = sum;
     }
+    const int at = sum_before(all, red) + before;
+    if (threadIdx.x < bins) base[threadIdx.x] = at;
     __syncthreads();
-    scan_bins(base, bins, red);
-    if (!ALL) {
-      for (int i = threadIdx.x; i < bins; i += kThreads) {
-        const int g0 = tile / kEmbedTiles;
-        int sum = base[i];
-#pragma unroll 4
-        for (int g = 0; g < g0; ++g) sum += s.sums[(int64_t)g * kMaxBins + i];
-#pragma unroll 16
-        for (int t = g0 * kEmbedTiles; t < tile; ++t) sum += s.count[(int64_t)t * kMaxBins + i];
-        base[i] = sum;
-      }
-      __syncthreads();
-    }
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       const int64_t i = place_of(tile, r);
@@ -226,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
       const int digit = (key[r] >> shift) & (bins - 1);
       const int to = base[digit] + warp_count[warp][digit] + rank[r];
       s.key_out[to] = key[r];
-      s.slot_out[to] = first ? (int)i : s.slot_in[i];
+      s.slot_out[to] = own[r];
     }
     if (!ALL) return;
     __syncthreads();
@@ -238,17 +216,6 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
     s.key_out = s.key_in == s.keys[0] ? s.keys[1] : s.keys[0];
     s.slot_out = s.slot_in == s.slots[0] ? s.slots[1] : s.slots[0];
   }
-  for (int64_t i = threadIdx.x; i <= a.n; i += kThreads) {
-    if (i < a.n) mark(a, s.key_out, s.range, i);
-    else if (s.key_out[i - 1] < a.V) s.range[s.key_out[i - 1]].y = (int)i;
-  }
-}
-
-__global__ void __launch_bounds__(kThreads) k_embed_mark(const EmbedArgs a, const int* key, int2* range) {
-  pdl_enter();
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i < a.n) mark(a, key, range, i);
-  if (i == a.n - 1 && key[i] < a.V) range[key[i]].y = (int)a.n;
 }
 
 // ------------------------------------------------------------------ the sums
@@ -278,67 +245,124 @@ struct Sum {
   }
 };
 
-// Groups of G threads, G E columns each.  The first `chunk_ctas` CTAs take chunks, the others the rows of ids without a slot: a
-// warp 32 table rows.
+// The rows of the ids without a slot, kThreads of them a CTA: which of them occur is read from the sorted keys between the first
+// and the last of them.
+__device__ void clear_rows(const EmbedArgs& a, const int* key, int64_t v0) {
+  __shared__ int64_t bound[2];
+  __shared__ unsigned there[kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < kThreads / 32) there[threadIdx.x] = 0;
+  if (warp < 2) {  // the first place of a key >= v, 32 places looked at at a time
+    const int64_t v = min(v0 + warp * kThreads, (int64_t)a.V);
+    int64_t lo = 0, hi = a.n;  // it is in [lo, hi]
+    while (lo < hi) {
+      const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+      const unsigned m = __ballot_sync(FULL, i < hi && key[i] < v);  // a prefix of the lanes
+      const int k = __popc(m);
+      const int64_t l = lo;
+      lo = k ? l + (k - 1) * step + 1 : l;
+      hi = min(hi, l + k * step);
+    }
+    if (lane == 0) bound[warp] = lo;
+  }
+  __syncthreads();
+  // (a frequent id has many places: four keys a load, four loads on their way)
+  for (int64_t i0 = (bound[0] & ~3) + threadIdx.x * 4; i0 < bound[1]; i0 += kThreads * 16) {
+    int4 k[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = i0 + u * kThreads * 4;
+      k[u] = i < bound[1] ? *reinterpret_cast<const int4*>(key + i) : make_int4(-1, -1, -1, -1);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = i0 + u * kThreads * 4;
+      const int q[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = q[j] - (int)v0;
+        if (i + j < bound[0] || i + j >= bound[1]) continue;
+        if (!(reinterpret_cast<volatile unsigned*>(there)[r >> 5] >> (r & 31) & 1)) atomicOr(&there[r >> 5], 1u << (r & 31));
+      }
+    }
+  }
+  __syncthreads();
+  const int64_t w0 = v0 + warp * 32;
+  const bool wide = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0;
+  for (unsigned m = ~there[warp]; m; m &= m - 1) {
+    const int64_t v = w0 + __ffs(m) - 1;
+    if (v >= a.V) break;
+    float* out = a.dtable + v * a.d;
+    if (wide)
+      for (int c = lane * 4; c < a.d; c += 128) *reinterpret_cast<float4*>(out + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else
+      for (int c = lane; c < a.d; c += 32) out[c] = 0.f;
+  }
+}
+
+// Groups of G threads, G E columns each.  The first `chunk_ctas` CTAs take chunks, the others the rows of ids without a slot.
 template <typename T, int G, bool WIDE>
-__global__ void __launch_bounds__(kThreads) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
+__global__ void __launch_bounds__(kThreads, WIDE ? 4 : 3) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
   pdl_enter();
-  constexpr int E = 16 / sizeof(T), U = WIDE ? 8 : 2;
+  constexpr int E = 16 / sizeof(T), U = 32 / E, C = kEmbedCap;
   if ((int)blockIdx.x >= chunk_ctas) {
-    const int64_t v0 = (((int64_t)blockIdx.x - chunk_ctas) * (kThreads / 32) + (threadIdx.x >> 5)) * 32;
-    const int lane = threadIdx.x & 31;
-    bool none = false;
-    if (v0 + lane < a.V) {
-      const int2 r = s.range[v0 + lane];
-      none = r.x == r.y;
-    }
-    for (unsigned m = __ballot_sync(FULL, none); m; m &= m - 1) {
-      float* out = a.dtable + (v0 + __ffs(m) - 1) * a.d;
-      if (a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0)
-        for (int c = lane * 4; c < a.d; c += 128) *reinterpret_cast<float4*>(out + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-      else
-        for (int c = lane; c < a.d; c += 32) out[c] = 0.f;
-    }
+    clear_rows(a, s.key_out, ((int64_t)blockIdx.x - chunk_ctas) * kThreads);
     return;
   }
-  const int t = threadIdx.x % G;
-  const int64_t task = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
+  // the keys from C places before the chunk to C behind it, and the slots from its first place on
+  __shared__ __align__(16) int keys[kThreads / G][3 * C];
+  __shared__ __align__(16) int slots[kThreads / G][2 * C];
+  const int t = threadIdx.x % G, grp = threadIdx.x / G;
+  const unsigned team = G == 32 ? FULL : ((1u << (G & 31)) - 1) << (threadIdx.x & 31 & ~(G - 1));
+  const int64_t task = (int64_t)blockIdx.x * (kThreads / G) + grp;
   const int64_t chunk = task / blocks;
-  const int c = (int)(task - chunk * blocks) * G * E + (WIDE ? t * E : t);
-  const int64_t lo = chunk * kEmbedCap;
+  const int block = (int)(task - chunk * blocks), c = block * G * E + (WIDE ? t * E : t);
+  const int64_t lo = chunk * C;
   if (lo >= a.n) return;
-  const int64_t hi = min(a.n, lo + kEmbedCap);
-  const int *key = s.key_out, *slot = s.slot_out;
+  int *key = keys[grp] + C, *slot = slots[grp];  // by place - lo
+  const int len = (int)min((int64_t)C, a.n - lo);
+  // also: the places nearest to the chunk's first and last one that have another key than it, before and behind
+  const int k0 = s.key_out[lo], k1 = s.key_out[lo + len - 1];
+  if (k0 >= a.V) return;  // sorted last: slots without an id, nothing else
+  int b0 = -C - 1, f0 = 2 * C, b1 = -1, f1 = 2 * C;
+#pragma unroll
+  for (int j = t - C; j < 2 * C; j += G) {
+    const bool in = lo + j >= 0 && lo + j < a.n;
+    const int k = in ? s.key_out[lo + j] : -1;
+    key[j] = k;
+    if (j >= 0) slot[j] = in ? s.slot_out[lo + j] : -1;
+    if (j < 0 && k != k0) b0 = max(b0, j);
+    if (j > 0 && k != k0) f0 = min(f0, j);
+    if (j >= 0 && j < len && k != k1) b1 = max(b1, j);
+    if (j >= len && k != k1) f1 = min(f1, j);
+  }
+#pragma unroll
+  for (int o = G / 2; o; o >>= 1) {
+    b0 = max(b0, __shfl_xor_sync(team, b0, o));
+    f0 = min(f0, __shfl_xor_sync(team, f0, o));
+    b1 = max(b1, __shfl_xor_sync(team, b1, o));
+    f1 = min(f1, __shfl_xor_sync(team, f1, o));
+  }
+  __syncwarp(team);
+  // the first run is the places (b0, f0), the last one (b1, f1), as far as they are looked at: C before and behind
+  const bool long0 = f0 - b0 - 1 > C, same = b1 < 0, long1 = k1 < a.V && (same ? long0 : f1 - b1 - 1 > C);
+  int from = 0, to = len;
+  if (!long0 && b0 != -1) from = f0;  // another chunk's
+  if (!long1) {
+    if (k1 < a.V) {
+      to = f1;
+    } else {  // the ids end in this chunk
+      to = 0;
+      while (key[to] < a.V) ++to;
+    }
+  }
+  const int l1 = long0 ? min(f0, len) : 0, m0 = long1 && !same ? b1 + 1 : 0x7fffffff;  // of long runs: places below l1 and from m0 on
+  if (block == 0 && t == 0) {  // a long run's first chunk lists it, its last one says so
+    if (long0 && b0 == -1) s.longs[atomicAdd(s.n_long, 1)] = make_int2(k0, (int)(2 * chunk));
+    if (m0 < len) s.longs[atomicAdd(s.n_long, 1)] = make_int2(k1, (int)(2 * chunk + 1));
+    if (long0 && f0 <= len) s.last[k0] = (int)(2 * chunk);
+  }
   const T* dy = static_cast<const T*>(a.dy);
-  // the places to go through
-  const int k0 = key[lo], k1 = key[hi - 1];
-  int from = (int)lo, to = (int)hi;
-  int l1 = (int)lo, m0 = 0x7fffffff;  // of long runs: places below l1 and from m0 on
-  const int2 none = make_int2(0, 0), r0 = k0 < a.V ? s.range[k0] : none, r1 = k1 < a.V ? s.range[k1] : none;
-  if (k0 >= a.V) return;  // sorted last: nothing but slots without an id
-  if (r0.y - r0.x > kEmbedCap) l1 = min(r0.y, (int)hi);
-  else if (r0.x < lo) from = r0.y;  // another chunk's
-  if (k1 >= a.V) {
-    // the ids end in this chunk: behind the last of them
-    int x = (int)lo, y = (int)hi - 1;  // key[x] < V <= key[y]
-    while (y - x > 1) {
-      const int mid = (x + y) >> 1;
-      if (key[mid] < a.V) x = mid; else y = mid;
-    }
-    to = y;
-  } else if (r1.y - r1.x <= kEmbedCap) {
-    to = r1.y;
-  } else if (k1 != k0) {
-    m0 = r1.x;
-    if (t == 0 && c < G * E) {  // a long run's first chunk lists it
-      const int at = atomicAdd(s.n_long, 1);
-      s.longs[at] = make_int2(k1, (int)(2 * chunk + 1));
-    }
-  }
-  if (l1 > lo && r0.x == lo && t == 0 && c < G * E) {
-    const int at = atomicAdd(s.n_long, 1);
-    s.longs[at] = make_int2(k0, (int)(2 * chunk));
-  }
   Sum<T, WIDE> acc;
   acc.clear();
   int now = -1;
@@ -348,65 +372,147 @@ __global__ void __launch_bounds__(kThreads) k_embed_rows(const EmbedArgs a, cons
     else if (i - 1 >= m0) acc.store(1.f, s.part + (2 * chunk + 1) * a.d, c, a.d, G);
     else acc.store(a.scale, a.dtable + (int64_t)now * a.d, c, a.d, G);
   };
-  for (int i = from; i < to; i += U) {
-    int k[U], at[U];
+  auto begin = [&](int i) {  // the sum goes on with place i
+    const int k = key[i];
+    if (k == now) return;
+    flush(i);
+    now = k;
+    acc.clear();
+  };
+  if (WIDE) {
+    const bool in = c < a.d;
+    for (int i = from; i < to; i += 8) {
+      uint4 w[8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      k[u] = i + u < to ? key[i + u] : -1;
-      at[u] = i + u < to ? slot[i + u] : -1;
-    }
-    uint4 w[U];
-    float f[U][WIDE ? 1 : E];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (WIDE) {
+      for (int u = 0; u < 8; ++u) {
         w[u] = make_uint4(0, 0, 0, 0);
-        if (at[u] >= 0 && c < a.d) w[u] = __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)at[u] * a.d + c));
-      } else {
+        if (i + u < to && in) w[u] = __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)slot[i + u] * a.d + c));
+      }
 #pragma unroll
-        for (int j = 0; j < (WIDE ? 1 : E); ++j) f[u][j] = at[u] >= 0 && c + j * G < a.d ? to_f(dy[(int64_t)at[u] * a.d + c + j * G]) : 0.f;
+      for (int u = 0; u < 8; ++u) {
+        if (i + u >= to) continue;
+        begin(i + u);
+        const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          acc.v[j] += sizeof(T) == 2 ? (j & 1 ? bf_hi(q[(j / 2) & 3]) : bf_lo(q[(j / 2) & 3])) : __uint_as_float(q[j & 3]);
       }
     }
+  } else {
+    for (int i = from; i < to; i += U) {
+      float f[U][E];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k[u] < 0) continue;
-      if (k[u] != now) {
-        flush(i + u);
-        now = k[u];
-        acc.clear();
+      for (int u = 0; u < U; ++u) {
+        const T* at = dy + (i + u < to ? (int64_t)slot[i + u] * a.d : 0);
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[u][j] = i + u < to && c + j * G < a.d ? to_f(at[c + j * G]) : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-        acc.v[j] += !WIDE ? f[u][WIDE ? 0 : j] : sizeof(T) == 2 ? (j & 1 ? bf_hi(q[(j / 2) & 3]) : bf_lo(q[(j / 2) & 3])) : __uint_as_float(q[j & 3]);
+      for (int u = 0; u < U; ++u) {
+        if (i + u >= to) continue;
+        begin(i + u);
+#pragma unroll
+        for (int j = 0; j < E; ++j) acc.v[j] += f[u][j];
       }
     }
   }
   flush(to);
 }
 
-// The ids of long runs: a CTA adds the partial rows of one, 32 columns, a warp every eighth of them, in 64 bits.
+// hi + lo + v, in two words again (64-bit additions have a hundredth of fp32's rate: 35 us for what takes 6)
+__device__ __forceinline__ void add2(float& hi, float& lo, float v) {
+  const float s = __fadd_rn(hi, v), b = __fadd_rn(s, -hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -b)), __fadd_rn(v, -b)));
+  hi = s;
+}
+
+// The ids of long runs, 32 columns of one (128 where rows are whole pieces of 16 bytes) a task: their partial rows are added in two
+// words, by a warp in order, or, of more than kWarpRows, by the CTA's warps each every eighth row.
+constexpr int kWarpRows = 24;
+template <int C>
+struct Join {
+  float hi[C], lo[C];
+  // rows p, p + step .. of up to last, of those below `first` that one
+  __device__ __forceinline__ void add(const float* part, int d, int p, int step, int first, int last) {
+    constexpr int U = 8;  // in flight
+#pragma unroll
+    for (int j = 0; j < C; ++j) hi[j] = lo[j] = 0.f;
+    for (; p <= last; p += U * step) {
+      float v[U][C];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = max(p + u * step, first);
+        const float* at = part + (int64_t)r * d;
+        if (C == 4) {
+          const float4 q = r <= last ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[u][C > 3 ? 3 : 0] = q.w; v[u][C > 2 ? 2 : 0] = q.z; v[u][C > 1 ? 1 : 0] = q.y; v[u][0] = q.x;
+        } else {
+          v[u][0] = r <= last ? *at : 0.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (p + u * step > last) break;
+#pragma unroll
+        for (int j = 0; j < C; ++j) add2(hi[j], lo[j], v[u][j]);
+      }
+    }
+  }
+};
+template <int C>
 __global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, const EmbedSort s) {
   pdl_enter();
-  __shared__ double red[kThreads / 32][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = (a.d + 31) / 32;
-  const int64_t tasks = (int64_t)*s.n_long * blocks;
-  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int which = (int)(task / blocks), c = (int)(task - (int64_t)which * blocks) * 32 + lane;
-    const int2 run = s.longs[which];
-    const int64_t first = run.y, last = 2 * (int64_t)((s.range[run.x].y - 1) / kEmbedCap);
-    double sum = 0.;
-    if (c < a.d) {
-      if (warp == 0) sum = s.part[first * a.d + c];
-#pragma unroll 8
-      for (int64_t p = (first | 1) + 1 + 2 * warp; p <= last; p += 2 * (kThreads / 32)) sum += s.part[p * a.d + c];
+  constexpr int W = kThreads / 32;
+  __shared__ float2 red[W][32 * C];
+  __shared__ int2 big[W];  // the warps' tasks that are the CTA's: the run, its first column
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = (a.d + 32 * C - 1) / (32 * C);
+  const int n_long = *s.n_long;
+  const int64_t tasks = (int64_t)n_long * blocks;
+  for (int64_t t0 = (int64_t)blockIdx.x * W; t0 < tasks; t0 += (int64_t)gridDim.x * W) {
+    const int64_t task = t0 + warp;
+    Join<C> sum;
+    int n_rows = 0;
+    if (task < tasks) {
+      // (one id's columns go to different CTAs: a frequent one's are long tasks)
+      const int b = (int)(task / n_long), which = (int)(task - (int64_t)b * n_long), c0 = b * 32 * C, c = c0 + lane * C;
+      const int2 run = s.longs[which];  // the id, and its first partial row: maybe the odd one of its chunk, then each chunk's even one
+      const int last = s.last[run.x], first = (run.y | 1) - 1;
+      n_rows = (last - first) / 2 + 1;
+      if (n_rows > kWarpRows) {
+        if (lane == 0) big[warp] = make_int2(which, c0);
+      } else if (c < a.d) {
+        sum.add(s.part + c, a.d, first, 2, run.y, last);
+        float* out = a.dtable + (int64_t)run.x * a.d + c;
+#pragma unroll
+        for (int j = 0; j < C; ++j) out[j] = (sum.hi[j] + sum.lo[j]) * a.scale;
+      }
     }
+    if (!__syncthreads_or(n_rows > kWarpRows)) continue;
+    // (each warp's own answer, known to all)
+    if (lane == 0 && n_rows <= kWarpRows) big[warp] = make_int2(-1, 0);
     __syncthreads();
-    red[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && c < a.d) {
-      for (int w = 1; w < kThreads / 32; ++w) sum += red[w][lane];
-      a.dtable[(int64_t)run.x * a.d + c] = (float)(sum * (double)a.scale);
+    for (int k = 0; k < W; ++k) {
+      const int2 it = big[k];
+      if (it.x < 0) continue;
+      const int2 run = s.longs[it.x];
+      const int c = it.y + lane * C;
+      if (c < a.d) {
+        sum.add(s.part + c, a.d, (run.y | 1) - 1 + 2 * warp, 2 * W, run.y, s.last[run.x]);
+#pragma unroll
+        for (int j = 0; j < C; ++j) red[warp][lane * C + j] = make_float2(sum.hi[j], sum.lo[j]);
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 32 * C; i += kThreads) {
+        if (it.y + i >= a.d) continue;
+        float h = red[0][i].x, l = red[0][i].y;
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+          add2(h, l, red[w][i].x);
+          l += red[w][i].y;
+        }
+        a.dtable[(int64_t)run.x * a.d + it.y + i] = (h + l) * a.scale;
+      }
+      __syncthreads();
     }
   }
 }
@@ -465,10 +571,6 @@ cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, int bits,
   if (s.tiles == 1) return launch_pdl(k_embed_place<true>, dim3(1), dim3(kThreads), 0, st, a, s, bits, 0, true);
   return launch_pdl(k_embed_place<false>, dim3((unsigned)s.tiles), dim3(kThreads), 0, st, a, s, bits, shift, shift == 0);
 }
-cudaError_t launch_embed_mark(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st) {
-  return launch_pdl(k_embed_mark, dim3((unsigned)((a.n + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, a, (const int*)s.key_out,
-                    s.range);
-}
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st) {
   const size_t es = f32 ? 4 : 2;
   const bool wide = ((uintptr_t)(a.d * es) | (uintptr_t)a.d * 4 | reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.dtable)) % 16 == 0;
@@ -476,8 +578,11 @@ cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, 
   return wide ? rows<bf16, true>(a, s, st) : rows<bf16, false>(a, s, st);
 }
 cudaError_t launch_embed_join(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st) {
-  return launch_pdl(k_embed_join, dim3((unsigned)std::min<int64_t>((a.n + kEmbedCap - 1) / kEmbedCap * ((a.d + 31) / 32), sm_count() * 8)),
-                    dim3(kThreads), 0, st, a, s);
+  const int C = a.d % 4 == 0 ? 4 : 1;  // (the partial rows are in the workspace: aligned)
+  // at most one long run in more than kEmbedCap places
+  const int64_t most = (a.n / (kEmbedCap + 1) * ((a.d + 32 * C - 1) / (32 * C)) + 7) / 8;
+  return launch_pdl(C == 4 ? k_embed_join<4> : k_embed_join<1>, dim3((unsigned)std::min<int64_t>(most, sm_count() * 4)), dim3(kThreads), 0,
+                    st, a, s);
 }
 cudaError_t launch_zero(void* p, size_t bytes, cudaStream_t st) {
   const int64_t n = (int64_t)(bytes / 16);

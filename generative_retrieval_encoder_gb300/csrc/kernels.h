@@ -350,16 +350,15 @@ struct EmbedSort {
   const int* key_in; int* key_out; const int* slot_in; int* slot_out;  // of the pass; at last key_out, slot_out are the sorted ones
   int* keys[2]; int* slots[2];        // [n] each
   int* count; int* sums;              // [tiles][2^kEmbedDigit]; the pass's [tiles / kEmbedTiles][2^kEmbedDigit], 0 on entry
-  int2* range;                        // [V]: each id's sorted places, 0 on entry
   float* part;                        // [2 * chunks][d]
   int* n_long; int2* longs;           // how many ids have more than kEmbedCap slots, 0 on entry; each and its first partial row
+  int* last;                          // [V]: of such an id its last partial row
 };
 int embed_fwd_ctas(const EmbedArgs& a, bool f32);
 cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st);
-// One pass of the sort, by the digit of `bits` bits at `shift`; a single tile's launch_embed_place is the whole sort and marks.
+// One pass of the sort, by the digit of `bits` bits at `shift`; a single tile's launch_embed_place is the whole sort.
 cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st);
 cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st);
-cudaError_t launch_embed_mark(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st);
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st);
 cudaError_t launch_embed_join(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st);
 // Clears a multiple of 16 bytes (a launch that follows its predecessor like the kernels do; a memset waits longer).
