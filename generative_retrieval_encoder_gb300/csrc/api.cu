@@ -718,23 +718,26 @@ gbla_status beam_ok(const gbla_beam* g) {
   if (rows > (1LL << 30) || rows * (g->V / 1024 + 1) > (1LL << 31) || (int64_t)g->B * g->n_out > (1LL << 30)) return GBLA_ERR_UNSUPPORTED;
   return GBLA_OK;
 }
-// Sizes of beam_select: the rows' tasks, and runs of about sqrt(K V / n_out) tokens, so that the two selections (of K V / run and of
-// n_out * run) are alike.
+// Sizes of beam_select: the rows' tasks, and runs of about 1.5 sqrt(K V / n_out) tokens: of the two selections the first, of K V / run
+// runs, goes over its items several times, the second, of n_out runs' tokens, once.  aligned: rows begin at 16-byte boundaries (the
+// workspace has room for the other case).
 struct BeamLayout { int tasks, runs, lg; size_t part, top, total; };
-BeamLayout beam_layout(const gbla_beam& g) {
+BeamLayout beam_layout(const gbla_beam& g, bool aligned) {
   BeamLayout l{};
   const int E = g.io_dtype == GBLA_F32 ? 4 : 8;
-  const int64_t places = (int64_t)g.V + E - 1;  // a row may begin behind a 16-byte boundary
-  l.tasks = (int)((places + kBeamPieces * 32 * E - 1) / (kBeamPieces * 32 * E));
-  const double want = std::sqrt((double)g.K * g.V / g.n_out);
+  const double want = 1.5 * std::sqrt((double)g.K * g.V / g.n_out);
   while (l.lg < 5 && E * (1.5 * (1 << l.lg)) < want) ++l.lg;
-  const int run = E << l.lg;
-  l.runs = (int)((places + run - 1) / run);
+  const int run = E << l.lg, task = kBeamPieces * 32 * E;
+  auto tasks = [&](int64_t places) { return (int)((places + task - 1) / task); };
+  auto runs = [&](int64_t places) { return (int)((places + run - 1) / run); };
+  const int64_t most = (int64_t)g.V + E - 1, places = aligned ? g.V : most;
+  l.tasks = tasks(places);
+  l.runs = runs(places);
   Cursor c;
   c.take(16);
   const size_t rows = (size_t)g.B * g.K;
-  l.part = c.take(rows * l.tasks * sizeof(BeamPart));
-  l.top = c.take(rows * l.runs * 4);
+  l.part = c.take(rows * tasks(most) * sizeof(BeamPart));
+  l.top = c.take(rows * runs(most) * 4);
   l.total = c.off;
   return l;
 }
@@ -1441,7 +1444,7 @@ gbla_status layer_norm_backward(const gbla_shape* shape, const void* x, int64_t 
   return GBLA_OK;
 }
 
-size_t beam_workspace_size(const gbla_beam* beam) { return beam_ok(beam) == GBLA_OK ? beam_layout(*beam).total : 0; }
+size_t beam_workspace_size(const gbla_beam* beam) { return beam_ok(beam) == GBLA_OK ? beam_layout(*beam, false).total : 0; }
 
 gbla_status beam_select(const gbla_beam* beam, const void* logits, int64_t ld, const float* scores, const uint32_t* allowed,
                         const uint8_t* done, float* new_scores, int32_t* tokens, int32_t* parents, uint8_t* new_done, void* ws,
@@ -1454,7 +1457,7 @@ gbla_status beam_select(const gbla_beam* beam, const void* logits, int64_t ld, c
     if (!q || !aligned4(q)) return GBLA_ERR_INVALID_ARG;
   if (!logits || !aligned(logits, f32 ? 4 : 2) || ld < g.V || ld > (1LL << 40) || !aligned4(allowed) || (done && g.eos < 0))
     return GBLA_ERR_INVALID_ARG;
-  const BeamLayout l = beam_layout(g);
+  const BeamLayout l = beam_layout(g, aligned16(logits) && ld * (f32 ? 4 : 2) % 16 == 0);
   if ((r = ws_status(ws, ws_bytes, l.total)) != GBLA_OK) return r;
   const RowCtx c{static_cast<cudaStream_t>(stream)};
   BeamArgs a{};

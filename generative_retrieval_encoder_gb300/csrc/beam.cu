@@ -24,18 +24,18 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr float kInf = __builtin_huge_valf();
 constexpr double kLn2 = 0.6931471805599453;
 
-// 2^(j / 32) = hi + lo
+// 2^(j / 32) / (1 + j / 32) = hi + lo, hi of 18 bits: times (1 + j / 32) 2^q, which the rounded exponent's own bits make, it is exact
 __device__ const float kExpHi[32] = {
-    0x1.0p+0f, 0x1.059b0ep+0f, 0x1.0b5586p+0f, 0x1.11301ep+0f, 0x1.172b84p+0f, 0x1.1d4874p+0f, 0x1.2387a6p+0f, 0x1.29e9ep+0f,
-    0x1.306fep+0f, 0x1.371a74p+0f, 0x1.3dea64p+0f, 0x1.44e086p+0f, 0x1.4bfdaep+0f, 0x1.5342b6p+0f, 0x1.5ab07ep+0f, 0x1.6247ecp+0f,
-    0x1.6a09e6p+0f, 0x1.71f75ep+0f, 0x1.7a1148p+0f, 0x1.82589ap+0f, 0x1.8ace54p+0f, 0x1.93737cp+0f, 0x1.9c4918p+0f, 0x1.a5503cp+0f,
-    0x1.ae89fap+0f, 0x1.b7f77p+0f, 0x1.c199bep+0f, 0x1.cb720ep+0f, 0x1.d5818ep+0f, 0x1.dfc974p+0f, 0x1.ea4afap+0f, 0x1.f50766p+0f,
+    0x1p+0f, 0x1.fb5b8p-1f, 0x1.f7378p-1f, 0x1.f38bp-1f, 0x1.f04d8p-1f, 0x1.ed768p-1f, 0x1.eaff8p-1f, 0x1.e8e28p-1f,
+    0x1.e7198p-1f, 0x1.e5ap-1f, 0x1.e4718p-1f, 0x1.e3898p-1f, 0x1.e2e58p-1f, 0x1.e281p-1f, 0x1.e2598p-1f, 0x1.e26dp-1f,
+    0x1.e2b8p-1f, 0x1.e3388p-1f, 0x1.e3edp-1f, 0x1.e4d38p-1f, 0x1.e5ea8p-1f, 0x1.e72f8p-1f, 0x1.e8a28p-1f, 0x1.ea418p-1f,
+    0x1.ec0b8p-1f, 0x1.edff8p-1f, 0x1.f01c8p-1f, 0x1.f2618p-1f, 0x1.f4ce8p-1f, 0x1.f762p-1f, 0x1.fa1cp-1f, 0x1.fcfb8p-1f,
 };
 __device__ const float kExpLo[32] = {
-    0x0.0p+0f, -0x1.9d4f52p-25f, 0x1.9f3122p-25f, -0x1.fdb496p-25f, -0x1.c15742p-27f, -0x1.d2e8cap-25f, 0x1.ceac48p-25f, -0x1.5c0424p-25f,
-    0x1.4636e2p-25f, -0x1.18aac6p-25f, 0x1.824684p-25f, 0x1.8624b4p-30f, -0x1.593abcp-25f, -0x1.2c561p-25f, -0x1.5bd5ecp-27f, -0x1.f8b55p-25f,
-    0x1.9fcef4p-26f, 0x1.1d8beep-25f, -0x1.829fdp-25f, -0x1.accc7cp-26f, 0x1.15506ep-27f, -0x1.e64744p-25f, 0x1.51f848p-27f, -0x1.b83b54p-25f,
-    -0x1.a94b14p-26f, -0x1.a09438p-25f, -0x1.3d56b2p-27f, -0x1.8837ccp-27f, -0x1.822dbcp-27f, -0x1.908c94p-25f, 0x1.52486cp-27f, -0x1.246ebp-26f,
+    0x0p+0f, -0x1.fd0268p-20f, 0x1.45997ap-21f, 0x1.6dc7a4p-20f, -0x1.1f909cp-20f, -0x1.9cb2a4p-21f, -0x1.60e976p-21f, -0x1.fbcb98p-20f,
+    -0x1.894a0ep-21f, -0x1.3965fep-21f, -0x1.1b5fd8p-20f, 0x1.acef48p-20f, -0x1.36643ep-20f, 0x1.014d7ep-24f, 0x1.d1967ep-20f, -0x1.67559p-20f,
+    -0x1.110082p-20f, 0x1.2a661ep-20f, 0x1.3ff29p-20f, 0x1.38d8dap-21f, -0x1.feaabp-20f, 0x1.65eb56p-20f, -0x1.22e3d8p-23f, -0x1.14a9b8p-21f,
+    -0x1.99e158p-21f, -0x1.14c836p-20f, -0x1.872644p-21f, 0x1.7c2b28p-20f, -0x1.5bc508p-22f, 0x1.789ea6p-22f, -0x1.387142p-20f, -0x1.67e88p-20f,
 };
 constexpr float kL = 0x1.715476p+5f, kLlo = 0x1.4ae0cp-21f;  // 32 / ln 2 in two words
 // 2^(f / 32) - 1 = f (c1 + f (c2 + f (c3 + f c4))): c_k = (ln 2 / 32)^k / k!, the next term below 2^-39 at |f| = 1/2
@@ -67,11 +67,47 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* m, int words, int 
   return __funnelshift_r(lo, hi, t & 31) & ((1u << E) - 1);
 }
 
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+__device__ __forceinline__ double sum_of(const BeamPart& p) {
+  return p.far ? __hiloint2double(p.hi, __float_as_int(p.lo)) : (double)p.hi * (1. / 65536.) + (double)p.lo;
+}
+
 constexpr int kU = kBeamPieces;
 
-// A warp takes kU pieces a lane of one row.
+// The larger of two packed bf16 values each; of NaN and a number the number (of two NaN that), or NaN.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t o;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+  return o;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t o;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+  return o;
+}
+// The largest of a piece's values (no NaN).
 template <typename T>
-__global__ void __launch_bounds__(256) k_beam_rows(const BeamArgs a) {
+__device__ __forceinline__ float piece_max(const uint4& w) {
+  if (sizeof(T) == 2) {
+    const uint32_t m = max2(max2(w.x, w.y), max2(w.z, w.w));
+    return fmaxf(bf_lo(m), bf_hi(m));
+  }
+  return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+// A piece with -infinity in place of the values without a mask bit.
+template <typename T>
+__device__ __forceinline__ uint4 masked(uint4 w, uint32_t ok) {
+  auto pick = [&](uint32_t v, int j) {
+    if (sizeof(T) == 4) return ok >> j & 1 ? v : 0xff800000u;
+    const uint32_t keep = (ok >> 2 * j & 1 ? 0xffffu : 0u) | (ok >> (2 * j + 1) & 1 ? 0xffff0000u : 0u);
+    return (v & keep) | (0xff80ff80u & ~keep);
+  };
+  return make_uint4(pick(w.x, 0), pick(w.y, 1), pick(w.z, 2), pick(w.w, 3));
+}
+
+// A warp takes kU pieces a lane of one row.  Bound by instructions, some 16 a value (a plain exponential takes 6).
+template <typename T>
+__global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
   pdl_enter();
   constexpr int E = 16 / sizeof(T);
   __shared__ float hi_tab[32], lo_tab[32];
@@ -90,7 +126,6 @@ __global__ void __launch_bounds__(256) k_beam_rows(const BeamArgs a) {
   const uint32_t* mask = a.allowed ? a.allowed + row * a.words : nullptr;
   constexpr uint32_t LOWEST = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -infinity
   uint4 w[kU];
-  uint32_t ok[kU];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int t = t0 + u * 32 * E;
@@ -111,56 +146,73 @@ __global__ void __launch_bounds__(256) k_beam_rows(const BeamArgs a) {
         }
       w[u] = make_uint4(q[0], q[1], q[2], q[3]);
     }
-    ok[u] = mask ? mask_bits<E>(mask, a.words, t) : (1u << E) - 1;
   }
-  // the largest value of each run, and of all that are summed
+  // the largest value of each run, and of all that are summed; w: what is summed
   float top = -kInf;
   const int per = 32 >> a.lg;  // runs of the warp's 32 pieces
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
-    float all = -kInf, run = -kInf;
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float v = piece<T>(w[u], j);
-      all = fmaxf(all, v);
-      if (ok[u] >> j & 1) run = fmaxf(run, v);
+    float run = piece_max<T>(w[u]);
+    if (mask) {
+      const uint4 m = masked<T>(w[u], mask_bits<E>(mask, a.words, t0 + u * 32 * E));
+      top = fmaxf(top, run);
+      run = piece_max<T>(m);
+      if (a.over_allowed) w[u] = m;
     }
-    top = fmaxf(top, a.over_allowed ? run : all);
+    top = fmaxf(top, run);
     for (int o = 1; o < 1 << a.lg; o <<= 1) run = fmaxf(run, __shfl_xor_sync(FULL, run, o));
     const int g = (tile * kU + u) * per + (lane >> a.lg);
     if ((lane & ((1 << a.lg) - 1)) == 0 && g < a.runs) a.top[row * a.runs + g] = run;
+  }
+  if (mask && a.over_allowed) {
+    top = -kInf;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) top = fmaxf(top, piece_max<T>(w[u]));
   }
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
   BeamPart part;
   if (fabsf(top) <= 4096.f) {
     const float floor_ = top - 80.f;  // what is below counts as e^-80 of the largest: nothing
+    const uint32_t floor2 = pack_bf16(floor_, floor_);
     const int e = (int)floorf(top * 1.44269504f) + 1;
     const uint32_t bias = (uint32_t)(127 - e) << 23;
-    float sum = 192.f, lo = 0.f;  // sum: on the grid of 2^-16 that its start fixes; lo: what the grid cuts off, and the rest
+    // two values at a time.  sum: on the grid of 2^-16 that its start fixes; lo: what the grid cuts off, and the rest
+    float2 sum = two(192.f), lo = two(0.f);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      float rest = 0.f;  // of one piece first: 16 additions a value goes through, not 64
+      float2 rest = two(0.f);  // of one piece first: 8 additions a value goes through, not 32
+      const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        float v = piece<T>(w[u], j);
-        if (a.over_allowed && !(ok[u] >> j & 1)) v = -kInf;
-        v = max_nan(v, floor_);
-        const float k = __fmaf_rn(v, kL, 12582912.f);  // rounded to 32nds of an octave
-        const float n = __fadd_rn(k, -12582912.f);
-        const float f = __fmaf_rn(v, kLlo, __fmaf_rn(v, kL, -n));
-        const float p = f * __fmaf_rn(f, __fmaf_rn(f, __fmaf_rn(f, kC4, kC3), kC2), kC1);
-        const uint32_t b = __float_as_uint(k);
-        const float scale = __uint_as_float(((b & ~31u) << 18) + bias);  // 2^(floor(n / 32) - e)
-        const float h = hi_tab[b & 31], h2 = __fmul_rn(h, scale);
-        const float next = __fadd_rn(sum, h2);
-        rest += __fmaf_rn(__fmaf_rn(h, p, lo_tab[b & 31]), scale, __fadd_rn(h2, -__fadd_rn(next, -sum)));
+      for (int j = 0; j < E; j += 2) {
+        float2 v;
+        if (sizeof(T) == 2) {
+          const uint32_t c = max2_nan(q[j / 2], floor2);
+          v = make_float2(bf_lo(c), bf_hi(c));
+        } else {
+          v = make_float2(max_nan(__uint_as_float(q[j & 3]), floor_), max_nan(__uint_as_float(q[(j + 1) & 3]), floor_));
+        }
+        const float2 k = __ffma2_rn(v, two(kL), two(12582912.f));  // rounded to 32nds of an octave: n + 1.5 2^23
+        const float2 n = __ffma2_rn(k, two(-1.f), two(12582912.f));  // -n
+        const float2 f = __ffma2_rn(v, two(kLlo), __ffma2_rn(v, two(kL), n));
+        const float2 p = __fmul2_rn(f, __ffma2_rn(f, __ffma2_rn(f, __ffma2_rn(f, two(kC4), two(kC3)), two(kC2)), two(kC1)));
+        const uint32_t bx = __float_as_uint(k.x), by = __float_as_uint(k.y);
+        // n's lower 5 bits are j, the others the octave: (1 + j / 32) 2^(n / 32 - e)
+        const float2 scale = make_float2(__uint_as_float((bx << 18) + bias), __uint_as_float((by << 18) + bias));
+        const float2 h = make_float2(hi_tab[bx & 31], hi_tab[by & 31]), l = make_float2(lo_tab[bx & 31], lo_tab[by & 31]);
+        const float2 h2 = __fmul2_rn(h, scale), next = __fadd2_rn(sum, h2);
+        const float2 cut = __ffma2_rn(__ffma2_rn(sum, two(-1.f), next), two(-1.f), h2);  // h2 - (next - sum): exact
+        rest = __fadd2_rn(rest, __ffma2_rn(__ffma2_rn(h, p, l), scale, cut));
         sum = next;
       }
-      lo += rest;
+      lo = __fadd2_rn(lo, rest);
     }
-    double s = (double)__fadd_rn(sum, -192.f) + (double)lo;
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-    part = BeamPart{s, (float)e, 0};
+    // the grid's parts are whole numbers of 2^-16, at most 2^22 a lane: exact as integers
+    part.hi = __reduce_add_sync(FULL, (int)((sum.x - 192.f) * 65536.f) + (int)((sum.y - 192.f) * 65536.f));
+    float r = lo.x + lo.y;
+    for (int o = 16; o; o >>= 1) r += __shfl_xor_sync(FULL, r, o);
+    part.lo = r;
+    part.ref = (float)e;
+    part.far = 0;
   } else if (top > -kInf) {  // far from 0 (or infinite): in 64 bits
     double s = 0.;
     for (int u = 0; u < kU; ++u)
@@ -172,7 +224,7 @@ __global__ void __launch_bounds__(256) k_beam_rows(const BeamArgs a) {
         s += exp((double)v - (double)top);
       }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-    part = BeamPart{s, top, 1};
+    part = BeamPart{__double2hiint(s), __int_as_float(__double2loint(s)), top, 1};
   } else {  // nothing above -infinity; a NaN among them shows
     float q = 0.f;
 #pragma unroll
@@ -180,10 +232,10 @@ __global__ void __launch_bounds__(256) k_beam_rows(const BeamArgs a) {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const float v = piece<T>(w[u], j);
-        if (v != v && (!a.over_allowed || (ok[u] >> j & 1))) q = v;
+        if (v != v) q = v;
       }
     for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(FULL, q, o);
-    part = BeamPart{(double)q, -kInf, 0};
+    part = BeamPart{0, q, -kInf, 0};
   }
   if (lane == 0) a.part[task] = part;
 }
@@ -222,138 +274,124 @@ __device__ __forceinline__ float score_of(uint64_t key) {
 }
 
 constexpr int kPick = 1024;   // threads
-constexpr int kBins = 2048;
+constexpr int kBins = 2 * kPick;
 struct PickSmem {
-  uint64_t key[kBeamItems];      // the items at hand; the kept ones first
+  uint64_t key[kBeamItems];       // the items at hand; the kept ones first
   uint64_t kept[kBeamMost];
-  double total[kBeamMost];       // rows' sums of exponentials; then their base scores
-  double expo[kBeamMost];
+  double expo[kBeamMost];         // rows' references; then the kept runs
   uint32_t at[kBeamItems];
   uint32_t kept_at[kBeamMost];
-  float ref[kBeamMost];          // what a row's logits are taken relative to
+  double total[kBeamMost];        // rows' sums of exponentials; then their base scores
+  float ref[kBeamMost];           // what a row's logits are taken relative to
   int hist[kBins];
-  uint64_t red[32];
-  uint64_t red2[32];
+  uint32_t red[64];
   int n, digit, need, whole;
 };
+// An item is kept if its key is above `key`, or equal and its place at most `at`.
+struct Cut { uint64_t key; uint32_t at; };
 
-// Of items [0, cnt) the `want` best to the front, in any order; returns how many there are (fewer: no more candidates).
-__device__ int select_best(PickSmem& s, int cnt, int want) {
+// The number of the CTA's counts before this thread's.
+__device__ __forceinline__ int count_before(PickSmem& s, int v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(FULL, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) s.red[warp] = (uint32_t)inc;
+  __syncthreads();
+  const unsigned sum = __reduce_add_sync(FULL, lane < warp ? s.red[lane] : 0u);
+  return (int)sum + inc - v;
+}
+
+// Among items [0, cnt), more than `want` of them live (key > 0), the cut that keeps `want`: digits of 11 bits from the highest in
+// which the keys differ, then, where more keys are equal than are kept, of the place.  same(i): item i agrees in all digits so far.
+template <bool PLACE>
+__device__ __forceinline__ bool digits(PickSmem& s, int cnt, uint64_t eq, uint64_t& pre, int& shift, int& need) {
+  const int tid = threadIdx.x;
+  bool whole = false;
+  while (shift > 0 && !whole) {
+    const int bits = min(11, shift), to = shift - bits;
+    s.hist[tid] = 0;
+    s.hist[tid + kPick] = 0;
+    __syncthreads();
+    for (int i = tid; i < cnt; i += kPick) {
+      const uint64_t k = s.key[i];
+      if (PLACE ? k == eq : k != 0) {
+        const uint64_t v = PLACE ? (uint64_t)~s.at[i] & 0xffffffffu : k;  // the lowest place first
+        if (shift == 64 || v >> shift == pre) atomicAdd(&s.hist[(int)(v >> to) & ((1 << bits) - 1)], 1);
+      }
+    }
+    __syncthreads();
+    const int b1 = kBins - 1 - 2 * tid, c1 = s.hist[b1], c0 = s.hist[b1 - 1];  // from the top bin down, two a thread
+    const int above = count_before(s, c0 + c1);
+    if (above < need && need <= above + c0 + c1) {
+      const bool first = need <= above + c1;
+      const int left = first ? need - above : need - above - c1;
+      s.digit = first ? b1 : b1 - 1;
+      s.need = left;
+      s.whole = left == (first ? c1 : c0);
+    }
+    __syncthreads();
+    pre = (shift == 64 ? 0 : pre << bits) | (uint64_t)s.digit;
+    need = s.need;
+    whole = s.whole;
+    shift = to;
+  }
+  return whole;
+}
+
+// Of items [0, cnt) the `want` best to the front, in any order; returns how many there are (fewer: no more candidates).  low: a key
+// that none of the kept is below; 1 if they are fewer than `want`.
+__device__ int select_best(PickSmem& s, int cnt, int want, uint64_t& low) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the live ones, and the range of their keys
-  uint64_t top = 0, low = ~0ull;
+  uint32_t top = 0, bottom = 0xffffffffu;  // of the keys' upper words
   int live = 0;
   for (int i = tid; i < cnt; i += kPick) {
     const uint64_t k = s.key[i];
     if (k) {
-      top = max(top, k);
-      low = min(low, k);
+      top = max(top, (uint32_t)(k >> 32));
+      bottom = min(bottom, (uint32_t)(k >> 32));
       ++live;
     }
   }
-  for (int o = 16; o; o >>= 1) {
-    top = max(top, __shfl_xor_sync(FULL, top, o));
-    low = min(low, __shfl_xor_sync(FULL, low, o));
-  }
+  top = __reduce_max_sync(FULL, top);
+  bottom = __reduce_min_sync(FULL, bottom);
   live = __reduce_add_sync(FULL, live);
   __syncthreads();
+  if (lane == 0) s.red[warp] = top, s.red[32 + warp] = bottom, s.hist[warp] = live;
+  __syncthreads();
+  top = __reduce_max_sync(FULL, s.red[lane]);
+  bottom = __reduce_min_sync(FULL, s.red[32 + lane]);
+  live = __reduce_add_sync(FULL, s.hist[lane]);
   if (tid == 0) s.n = 0;
-  if (lane == 0) s.red[warp] = top, s.red2[warp] = low;
   __syncthreads();
-  if (lane == 0 && live) atomicAdd(&s.n, live);
-  for (int w = 0; w < 32; ++w) {
-    top = max(top, s.red[w]);
-    low = min(low, s.red2[w]);
-  }
-  __syncthreads();
-  live = s.n;
-  // the threshold: keys above `pre` in the bits above `shift` are kept, those equal there go on; at last by the place, whose
-  // lowest value is the best
-  uint64_t key_min = 1, key_eq = 0;  // kept: key >= key_min, or key == key_eq and place <= at_max
-  uint32_t at_max = 0;
+  Cut cut{0, 0};
+  low = live < want ? 1 : (uint64_t)bottom << 32;
   if (live > want) {
-    int need = want;
-    const uint64_t diff = top ^ low;
-    int shift = diff ? 64 - __clzll((long long)diff) : 0;  // bits [shift, 64) are common
-    uint64_t pre = shift < 64 ? top >> shift : 0;
-    bool whole = false;
-    while (shift > 0 && !whole) {
-      const int bits = min(11, shift), to = shift - bits;
-      for (int i = tid; i < kBins; i += kPick) s.hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < cnt; i += kPick) {
-        const uint64_t k = s.key[i];
-        if (k && (shift == 64 || k >> shift == pre)) atomicAdd(&s.hist[(int)(k >> to) & ((1 << bits) - 1)], 1);
-      }
-      __syncthreads();
-      // thread t: bins from the top, two each
-      const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
-      const int c1 = s.hist[b1], c0 = s.hist[b0];
-      int inc = c1 + c0;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(FULL, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (lane == 31) s.red[warp] = (uint64_t)inc;
-      __syncthreads();
-      int above = inc - c1 - c0;
-      for (int w = 0; w < warp; ++w) above += (int)s.red[w];
-      if (above < need && need <= above + c1) s.digit = b1, s.need = need - above, s.whole = need == above + c1;
-      if (above + c1 < need && need <= above + c1 + c0) s.digit = b0, s.need = need - above - c1, s.whole = need == above + c1 + c0;
-      __syncthreads();
-      pre = (shift == 64 ? 0 : pre << bits) | (uint64_t)s.digit;
-      need = s.need;
-      whole = s.whole;
-      shift = to;
-      __syncthreads();
-    }
-    key_min = pre << shift;  // everything from here up, if the last digit's items are all kept
-    if (!whole) {            // more equal keys than are kept: by place
-      key_eq = key_min;
-      key_min = key_eq + 1;
-      uint32_t apre = 0;
-      int ashift = 32;
-      bool all = false;
-      while (ashift > 0 && !all) {
-        const int bits = min(11, ashift), to = ashift - bits;
-        for (int i = tid; i < kBins; i += kPick) s.hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < cnt; i += kPick)
-          if (s.key[i] == key_eq && (ashift == 32 || s.at[i] >> ashift == apre)) atomicAdd(&s.hist[(s.at[i] >> to) & ((1u << bits) - 1)], 1);
-        __syncthreads();
-        const int b0 = 2 * tid, b1 = b0 + 1;  // from the lowest place
-        const int c0 = s.hist[b0], c1 = s.hist[b1];
-        int inc = c0 + c1;
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(FULL, inc, o);
-          if (lane >= o) inc += v;
-        }
-        if (lane == 31) s.red[warp] = (uint64_t)inc;
-        __syncthreads();
-        int before = inc - c0 - c1;
-        for (int w = 0; w < warp; ++w) before += (int)s.red[w];
-        if (before < need && need <= before + c0) s.digit = b0, s.need = need - before, s.whole = need == before + c0;
-        if (before + c0 < need && need <= before + c0 + c1) s.digit = b1, s.need = need - before - c0, s.whole = need == before + c0 + c1;
-        __syncthreads();
-        apre = (ashift == 32 ? 0 : apre << bits) | (uint32_t)s.digit;
-        need = s.need;
-        all = s.whole;
-        ashift = to;
-        __syncthreads();
-      }
-      at_max = ashift ? (apre << ashift) | ((1u << ashift) - 1) : apre;
+    int need = want, shift = 32 + (top == bottom ? 0 : 32 - __clz((int)(top ^ bottom)));
+    uint64_t pre = shift < 64 ? ((uint64_t)top << 32) >> shift : 0;
+    if (digits<false>(s, cnt, 0, pre, shift, need)) {
+      low = pre << shift;
+      cut.key = low - 1;  // everything from `low` up
+    } else {
+      low = cut.key = pre;
+      uint64_t at = 0;
+      int bits = 32;
+      digits<true>(s, cnt, cut.key, at, bits, need);
+      cut.at = ~(uint32_t)(at << bits);  // (places differ: the last digit's items are all kept)
     }
   }
   // the kept ones aside, then to the front
-  if (tid == 0) s.n = 0;
-  __syncthreads();
   for (int i0 = 0; i0 < cnt; i0 += kPick) {
     const int i = i0 + tid;
     const uint64_t k = i < cnt ? s.key[i] : 0;
-    const bool keep = k && (k >= key_min || (k == key_eq && s.at[i] <= at_max));
+    const bool keep = k && (k > cut.key || (k == cut.key && s.at[i] <= cut.at));
     const unsigned m = __ballot_sync(FULL, keep);
+    if (!m) continue;
     int first = 0;
-    if (lane == 0 && m) first = atomicAdd(&s.n, __popc(m));
+    if (lane == 0) first = atomicAdd(&s.n, __popc(m));
     first = __shfl_sync(FULL, first, 0);
     if (keep) {
       const int to = first + __popc(m & ((1u << lane) - 1));
@@ -363,26 +401,12 @@ __device__ int select_best(PickSmem& s, int cnt, int want) {
   }
   __syncthreads();
   const int n = s.n;
-  for (int i = tid; i < n; i += kPick) {
-    s.key[i] = s.kept[i];
-    s.at[i] = s.kept_at[i];
+  if (tid < n) {
+    s.key[tid] = s.kept[tid];
+    s.at[tid] = s.kept_at[tid];
   }
   __syncthreads();
   return n;
-}
-
-// The `want` best of `total` items, item(i) -> (key, place), kBeamItems at a time.
-template <typename F>
-__device__ int select_all(PickSmem& s, int64_t total, int want, F&& item) {
-  int have = 0;
-  for (int64_t i0 = 0; i0 < total;) {
-    const int more = (int)min((int64_t)(kBeamItems - have), total - i0);
-    for (int i = threadIdx.x; i < more; i += kPick) item(i0 + i, s.key[have + i], s.at[have + i]);
-    __syncthreads();
-    have = select_best(s, have + more, want);
-    i0 += more;
-  }
-  return have;
 }
 
 // A CTA a group: the rows' logarithms, the n best runs, the n best tokens of those, in order.
@@ -392,42 +416,39 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
   PickSmem& s = *reinterpret_cast<PickSmem*>(raw);
   constexpr int E = 16 / sizeof(T);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int64_t row0 = (int64_t)blockIdx.x * a.K;
   if (blockIdx.x == 0 && tid == 0) *a.err = 0;
   float2* base = reinterpret_cast<float2*>(s.total);  // [K], over the sums once they are used
-  for (int b = warp; b < a.K; b += kPick / 32) {
+  // the rows' sums from their parts, 1 to 32 threads a row
+  int team = 1;
+  while (team < a.tasks && team < 32) team <<= 1;
+  for (int b0 = 0; b0 < a.K; b0 += kPick / team) {
+    const int b = b0 + tid / team, t = tid % team;
     const BeamPart* p = a.part + (row0 + b) * a.tasks;
-    const bool done = a.done && a.done[row0 + b];
-    double e = 0., sum = 0.;  // the sum is sum exp(e)
-    float ref = 0.f;
-    if (!done) {
-      float best = -kInf;  // of the parts near 0: as powers of two, exactly
-      bool far = false;
-      for (int i = lane; i < a.tasks; i += 32) {
-        if (p[i].far) far = true;
-        else best = fmaxf(best, p[i].ref);
-      }
-      for (int o = 16; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(FULL, best, o));
-      far = __any_sync(FULL, far);
-      e = best > -kInf ? (double)best * kLn2 : -kInf;
-      if (far) {  // relative to the largest of all, a logit itself where it is far from 0
-        float most = -kInf;
-        for (int i = lane; i < a.tasks; i += 32)
-          if (p[i].far) most = fmaxf(most, p[i].ref);
-        for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, o));
-        if ((double)most > e) e = (double)most, ref = most;
-      }
-      for (int i = lane; i < a.tasks; i += 32) {
-        const BeamPart q = p[i];
-        double f = 1.;  // (a part without values has a sum of 0, or NaN)
-        if (q.ref > -kInf && far) f = exp((q.far ? (double)q.ref : (double)q.ref * kLn2) - e);
-        else if (q.ref > -kInf) f = q.ref > best - 1000.f ? __longlong_as_double((long long)(1023 + (int)(q.ref - best)) << 52) : 0.;
-        sum += q.s * f;
-      }
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    const bool mine = b < a.K && !(a.done && a.done[row0 + b]);
+    float best = -kInf, most = -kInf;  // of the parts near 0: as powers of two, exactly; of those far from it
+    for (int i = t; mine && i < a.tasks; i += team) {
+      if (p[i].far) most = fmaxf(most, p[i].ref);
+      else best = fmaxf(best, p[i].ref);
     }
-    if (lane == 0) s.total[b] = sum, s.expo[b] = ref != 0.f ? 0. : e, s.ref[b] = ref;
+    for (int o = team / 2; o; o >>= 1) {
+      best = fmaxf(best, __shfl_xor_sync(FULL, best, o));
+      most = fmaxf(most, __shfl_xor_sync(FULL, most, o));
+    }
+    const bool far = most > -kInf;
+    double e = best > -kInf ? (double)best * kLn2 : -kInf, sum = 0.;  // the sum is sum exp(e)
+    float ref = 0.f;
+    if (far && (double)most > e) e = (double)most, ref = most;  // relative to a logit itself where it is far from 0
+    for (int i = t; mine && i < a.tasks; i += team) {
+      const BeamPart q = p[i];
+      double f = 1.;  // (a part without values has a sum of 0, or NaN)
+      if (q.ref > -kInf && far) f = exp((q.far ? (double)q.ref : (double)q.ref * kLn2) - e);
+      else if (q.ref > -kInf) f = q.ref > best - 1000.f ? __hiloint2double((1023 + (int)(q.ref - best)) << 20, 0) : 0.;
+      sum += sum_of(q) * f;
+    }
+    for (int o = team / 2; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    if (b < a.K && t == 0) s.total[b] = sum, s.expo[b] = ref != 0.f ? 0. : e, s.ref[b] = ref;
   }
   __syncthreads();
   float2 mine = make_float2(-kInf, 0.f);
@@ -448,60 +469,110 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   __syncthreads();
   if (tid < a.K) base[tid] = mine;
   __syncthreads();
-  const int G = E << a.lg;
-  int have = select_all(s, (int64_t)a.K * a.runs, a.n, [&](int64_t i, uint64_t& key, uint32_t& at) {
-    const int b = (int)(i / a.runs), g = (int)(i - (int64_t)b * a.runs);
-    at = (uint32_t)i;
-    if (a.done && a.done[row0 + b]) key = g == 0 ? key_of(base[b], 0.f, 0.f) : 0;
-    else key = key_of(base[b], a.top[(row0 + b) * a.runs + g], s.ref[b]);
-  });
-  // the runs' places, out of the way of the tokens
-  uint32_t* run = reinterpret_cast<uint32_t*>(s.expo);
-  for (int i = tid; i < have; i += kPick) run[i] = s.at[i];
-  __syncthreads();
-  have = select_all(s, (int64_t)have * G, a.n, [&](int64_t i, uint64_t& key, uint32_t& at) {
-    const uint32_t r = run[i / G];
-    const int b = (int)(r / (uint32_t)a.runs), g = (int)(r - (uint32_t)b * a.runs), j = (int)(i % G);
-    const int64_t row = row0 + b;
-    key = 0;
-    at = 0;
-    if (a.done && a.done[row]) {
-      if (j == 0) key = key_of(base[b], 0.f, 0.f), at = (uint32_t)b * (uint32_t)a.V + (uint32_t)a.eos;
-      return;
+  // the n best runs, kBeamItems at a time
+  const uint32_t runs = (uint32_t)a.runs, all = (uint32_t)a.K * runs;
+  const float* tops = a.top + row0 * a.runs;
+  int have = 0;
+  uint64_t low = 1;
+  for (uint32_t i0 = 0; i0 < all;) {
+    const int more = (int)min((uint32_t)(kBeamItems - have), all - i0);
+    for (int j = tid; j < more; j += kPick) {
+      const uint32_t i = i0 + j, b = i / runs;
+      s.at[have + j] = i;
+      s.key[have + j] = a.done && a.done[row0 + b] ? (i == b * runs ? key_of(base[b], 0.f, 0.f) : 0) : key_of(base[b], tops[i], s.ref[b]);
     }
-    const int t = g * G + j - row_offset<T>(a, row);
-    if (t < 0 || t >= a.V) return;
-    if (a.allowed && !(a.allowed[row * a.words + (t >> 5)] >> (t & 31) & 1)) return;
-    key = key_of(base[b], to_f(static_cast<const T*>(a.logits)[row * a.ld + t]), s.ref[b]);
-    at = (uint32_t)b * (uint32_t)a.V + (uint32_t)t;
-  });
-  // in order: bitonic, by (key descending, place ascending)
-  int size = 1;
-  while (size < have) size <<= 1;
-  for (int i = have + tid; i < size; i += kPick) s.key[i] = 0, s.at[i] = 0xffffffffu;
+    __syncthreads();
+    have = select_best(s, have + more, a.n, low);
+    i0 += more;
+  }
+  uint32_t* run = reinterpret_cast<uint32_t*>(s.expo);  // out of the way of the tokens
+  if (tid < have) run[tid] = s.at[tid];
+  if (tid == 0) s.n = 0;
   __syncthreads();
-  for (int k = 2; k <= size; k <<= 1)
-    for (int j = k >> 1; j; j >>= 1) {
-      for (int i = tid; i < size; i += kPick) {
-        const int o = i ^ j;
-        if (o > i) {
-          const uint64_t x = s.key[i], y = s.key[o];
-          const uint32_t p = s.at[i], q = s.at[o];
-          const bool later = x < y || (x == y && p > q);  // i comes after o
-          if (later == ((i & k) == 0)) s.key[i] = y, s.key[o] = x, s.at[i] = q, s.at[o] = p;
+  // their tokens, a piece a thread: those not below `low`, which is n runs' largest at least
+  const int pieces = have << a.lg;
+  for (int i0 = 0; i0 < pieces; i0 += kPick) {
+    const int i = i0 + tid;
+    if (i < pieces) {
+      const uint32_t r = run[i >> a.lg], b = r / runs;
+      const int64_t row = row0 + b;
+      const float2 bs = base[b];
+      const float ref = s.ref[b];
+      auto put = [&](float x, float rf, uint32_t t) {
+        const uint64_t k = key_of(bs, x, rf);
+        if (k < low) return;
+        const int to = atomicAdd(&s.n, 1);
+        s.key[to] = k;
+        s.at[to] = b * (uint32_t)a.V + t;
+      };
+      if (a.done && a.done[row]) {
+        if ((i & ((1 << a.lg) - 1)) == 0) put(0.f, 0.f, (uint32_t)a.eos);
+      } else {
+        const int t0 = (int)(((r - b * runs) << a.lg) + (i & ((1 << a.lg) - 1))) * E - row_offset<T>(a, row);
+        const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+        // what is below this as one sum of fp32, off by 2^-23 of either number at most, is below `low` (NaN: nothing is)
+        const float lowest = score_of(low), least = lowest - 0x1p-21f * (fabsf(lowest) + fabsf(bs.x)) - 1e-30f;
+        const bool inside = t0 >= 0 && t0 + E <= a.V;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (inside) w = *reinterpret_cast<const uint4*>(x + t0);
+        uint32_t ok = (1u << E) - 1;
+        if (a.allowed) ok = mask_bits<E>(a.allowed + row * a.words, a.words, t0);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const int t = t0 + j;
+          if (!inside && (t < 0 || t >= a.V)) continue;
+          const float v = inside ? piece<T>(w, j) : to_f(x[t]);
+          if ((ok >> j & 1) && !(bs.x + (v - ref) < least)) put(v, ref, (uint32_t)t);
         }
       }
-      __syncthreads();
     }
-  const int64_t o0 = (int64_t)blockIdx.x * a.n;
-  for (int i = tid; i < a.n; i += kPick) {
-    const bool is = i < have;
-    const uint32_t at = is ? s.at[i] : 0;
-    const int b = (int)(at / (uint32_t)a.V), t = (int)(at - (uint32_t)b * (uint32_t)a.V);
-    a.out_scores[o0 + i] = is ? score_of(s.key[i]) : -kInf;
-    a.out_tokens[o0 + i] = is ? t : -1;
-    a.out_parents[o0 + i] = is ? b : 0;
-    if (a.out_done) a.out_done[o0 + i] = is && ((a.done && a.done[row0 + b]) || t == a.eos);
+    __syncthreads();
+    const int cnt = s.n;
+    __syncthreads();
+    if (cnt > kBeamItems - kPick * E) {  // room for as many again
+      uint64_t l;
+      select_best(s, cnt, a.n, l);
+      low = max(low, l);
+    }
+  }
+  int cnt = s.n;
+  __syncthreads();
+  if (cnt > kPick) {
+    uint64_t l;
+    cnt = select_best(s, cnt, a.n, l);
+  }
+  // in order, an item a thread: bitonic, by (key descending, place ascending)
+  int size = 1;
+  while (size < cnt) size <<= 1;
+  uint64_t key = tid < cnt ? s.key[tid] : 0;
+  uint32_t at = tid < cnt ? s.at[tid] : 0xffffffffu;
+  for (int k = 2; k <= size; k <<= 1)
+    for (int j = k >> 1; j; j >>= 1) {
+      uint64_t ok;
+      uint32_t oa;
+      if (j < 32) {
+        ok = __shfl_xor_sync(FULL, key, j);
+        oa = __shfl_xor_sync(FULL, at, j);
+      } else {
+        __syncthreads();
+        s.key[tid] = key;
+        s.at[tid] = at;
+        __syncthreads();
+        ok = s.key[tid ^ j];
+        oa = s.at[tid ^ j];
+      }
+      const bool better = key > ok || (key == ok && at < oa);
+      if (better != (((tid & j) == 0) == ((tid & k) == 0))) key = ok, at = oa;
+    }
+  const int have_n = min(cnt, a.n);
+  if (tid < a.n) {
+    const int64_t o = (int64_t)blockIdx.x * a.n + tid;
+    const bool is = tid < have_n;
+    const uint32_t b = is ? at / (uint32_t)a.V : 0, t = at - b * (uint32_t)a.V;
+    a.out_scores[o] = is ? score_of(key) : -kInf;
+    a.out_tokens[o] = is ? (int)t : -1;
+    a.out_parents[o] = (int)b;
+    if (a.out_done) a.out_done[o] = is && ((a.done && a.done[row0 + b]) || (int)t == a.eos);
   }
 }
 

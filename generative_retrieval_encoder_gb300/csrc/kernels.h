@@ -367,8 +367,9 @@ cudaError_t launch_zero(void* p, size_t bytes, cudaStream_t st);
 // ------------------------------------------------------------ beam search
 constexpr int kBeamPieces = 8;       // 16-byte pieces a lane of the rows' kernel takes
 constexpr int kBeamMost = 1024;      // beams, in and out
-constexpr int kBeamItems = 8192;     // candidates that the selection holds at once
-struct BeamPart { double s; float ref; int far; };  // sum of exponentials: s 2^ref (a whole number), far: s exp(ref)
+constexpr int kBeamItems = 12288;    // candidates that the selection holds at once
+// Sum of exponentials: (hi 2^-16 + lo) 2^ref (ref a whole number); far: the double of the words hi, lo, times exp(ref).
+struct __align__(16) BeamPart { int hi; float lo; float ref; int far; };
 struct BeamArgs {
   const void* logits; int64_t ld;    // [B K, ld]
   const float* scores;               // [B, K]

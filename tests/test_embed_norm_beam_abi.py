@@ -58,9 +58,10 @@ def test_embed_sizes(L):
     s, big = gbla.glr_shape(2, 100, 48), gbla.glr_shape(32, 4096, 512)
     assert gbla.embed_workspace_size(s, 500) == 256
     assert 0 < gbla.embed_workspace_size(s, 500, 1, True) < gbla.embed_workspace_size(s, 500, 4, True) < gbla.embed_workspace_size(big, 500, 4, True)
-    # keys and slots twice, ranges, two partial rows of 64 slots: about n (16 + d / 8) + 8 V bytes
+    # keys and slots twice, the digits' counts of tiles of 1024 keys, two partial rows of 32 slots, a word an id: about
+    # n (17 + d / 4) + 4 V bytes
     n, d, V = 32 * 4096, 512, 1 << 20
-    assert gbla.embed_workspace_size(big, V, 1, True) < n * (16 + d // 8) + 8 * V + (n // 2048 + 8) * 8192 + 4096
+    assert gbla.embed_workspace_size(big, V, 1, True) < n * (18 + d // 4) + 4 * V + (1 << 16)
 
 
 def _fwd(L, s, x=FAKE, ldx=48, res=OTHER, w=FAKE, b=FAKE, eps=1e-5, total=ctypes.c_void_p(3 << 20), y=ctypes.c_void_p(4 << 20),
