@@ -41,6 +41,39 @@ constexpr float kL = 0x1.715476p+5f, kLlo = 0x1.4ae0cp-21f;  // 32 / ln 2 in two
 // 2^(f / 32) - 1 = f (c1 + f (c2 + f (c3 + f c4))): c_k = (ln 2 / 32)^k / k!, the next term below 2^-39 at |f| = 1/2
 constexpr float kC1 = 0x1.62e43p-6f, kC2 = 0x1.ebfbep-13f, kC3 = 0x1.c6b08ep-20f, kC4 = 0x1.3b2ab6p-27f;
 
+// Logarithms: c_j of 8 bits next to 1 / (1 + (j + 1/2) / 64), and -ln c_j in two words
+__device__ const float kLogC[64] = {
+    0x1.fcp-1f, 0x1.f4p-1f, 0x1.ecp-1f, 0x1.e6p-1f, 0x1.dep-1f, 0x1.d8p-1f, 0x1.dp-1f, 0x1.cap-1f,
+    0x1.c4p-1f, 0x1.bep-1f, 0x1.b8p-1f, 0x1.b2p-1f, 0x1.acp-1f, 0x1.a6p-1f, 0x1.a2p-1f, 0x1.9cp-1f,
+    0x1.98p-1f, 0x1.92p-1f, 0x1.8ep-1f, 0x1.88p-1f, 0x1.84p-1f, 0x1.8p-1f, 0x1.7ap-1f, 0x1.76p-1f,
+    0x1.72p-1f, 0x1.6ep-1f, 0x1.6ap-1f, 0x1.66p-1f, 0x1.62p-1f, 0x1.5ep-1f, 0x1.5ap-1f, 0x1.58p-1f,
+    0x1.54p-1f, 0x1.5p-1f, 0x1.4cp-1f, 0x1.4ap-1f, 0x1.46p-1f, 0x1.42p-1f, 0x1.4p-1f, 0x1.3cp-1f,
+    0x1.3ap-1f, 0x1.36p-1f, 0x1.34p-1f, 0x1.3p-1f, 0x1.2ep-1f, 0x1.2cp-1f, 0x1.28p-1f, 0x1.26p-1f,
+    0x1.24p-1f, 0x1.2p-1f, 0x1.1ep-1f, 0x1.1cp-1f, 0x1.1ap-1f, 0x1.16p-1f, 0x1.14p-1f, 0x1.12p-1f,
+    0x1.1p-1f, 0x1.0ep-1f, 0x1.0cp-1f, 0x1.0ap-1f, 0x1.08p-1f, 0x1.06p-1f, 0x1.04p-1f, 0x1.02p-1f,
+};
+__device__ const float kLogHi[64] = {
+    0x1.010158p-7f, 0x1.849252p-6f, 0x1.466aeep-5f, 0x1.aaef2ep-5f, 0x1.1973bep-4f, 0x1.4d3116p-4f, 0x1.9335e6p-4f, 0x1.c8858p-4f,
+    0x1.fe8914p-4f, 0x1.1aa2b8p-3f, 0x1.365fccp-3f, 0x1.527e5ep-3f, 0x1.6f0128p-3f, 0x1.8beafep-3f, 0x1.9f6c4p-3f, 0x1.bd0874p-3f,
+    0x1.d1038p-3f, 0x1.ef5adep-3f, 0x1.01eae6p-2f, 0x1.1178e8p-2f, 0x1.1bf996p-2f, 0x1.269622p-2f, 0x1.36b678p-2f, 0x1.419b42p-2f,
+    0x1.4c9e0ap-2f, 0x1.57bf76p-2f, 0x1.63003p-2f, 0x1.6e60eep-2f, 0x1.79e266p-2f, 0x1.858558p-2f, 0x1.914a86p-2f, 0x1.973a34p-2f,
+    0x1.a3344p-2f, 0x1.af5296p-2f, 0x1.bb9612p-2f, 0x1.c1c606p-2f, 0x1.ce42f2p-2f, 0x1.dae754p-2f, 0x1.e148a2p-2f, 0x1.ee2a16p-2f,
+    0x1.f4aa7ep-2f, 0x1.00e5aep-1f, 0x1.04360cp-1f, 0x1.0ae76ep-1f, 0x1.0e4898p-1f, 0x1.11af82p-1f, 0x1.188ee4p-1f, 0x1.1c0784p-1f,
+    0x1.1f8636p-1f, 0x1.269622p-1f, 0x1.2a2786p-1f, 0x1.2dbf56p-1f, 0x1.315da4p-1f, 0x1.38ae22p-1f, 0x1.3c608p-1f, 0x1.4019c2p-1f,
+    0x1.43dap-1f, 0x1.47a152p-1f, 0x1.4b6fd6p-1f, 0x1.4f45a8p-1f, 0x1.5322e2p-1f, 0x1.5707a2p-1f, 0x1.5af406p-1f, 0x1.5ee82ap-1f,
+};
+__device__ const float kLogLo[64] = {
+    -0x1.4ee432p-32f, 0x1.191958p-31f, -0x1.7a4382p-30f, -0x1.e09dep-30f, -0x1.d73554p-29f, -0x1.6fc0aap-31f, -0x1.535b3cp-31f, 0x1.bc4b24p-32f,
+    -0x1.890aa6p-30f, -0x1.dc08d6p-31f, -0x1.fd4dfep-28f, 0x1.286d64p-29f, 0x1.6ead58p-28f, 0x1.671fd2p-28f, 0x1.c2259ap-29f, -0x1.f109d4p-29f,
+    -0x1.b3543p-28f, 0x1.373ffap-29f, -0x1.3b272ep-27f, 0x1.13f23ep-29f, 0x1.ad35cap-29f, -0x1.d9648ep-27f, -0x1.283ddep-27f, 0x1.eaf464p-29f,
+    -0x1.e8d3c4p-30f, -0x1.86e5cp-27f, 0x1.67558ap-27f, 0x1.abc65cp-28f, 0x1.0f9f68p-27f, -0x1.12468p-27f, 0x1.adfb44p-29f, 0x1.89ab56p-29f,
+    0x1.127d3cp-29f, -0x1.b6e646p-27f, -0x1.1fc742p-28f, 0x1.27f474p-27f, -0x1.fe6e3p-28f, 0x1.0992c2p-27f, -0x1.76364cp-28f, -0x1.297d84p-27f,
+    0x1.c06326p-27f, 0x1.6c81eap-27f, -0x1.89fc54p-29f, 0x1.682a7ep-28f, 0x1.847338p-27f, 0x1.e3ad54p-28f, 0x1.e4794cp-30f, 0x1.35ccp-26f,
+    -0x1.cf4d3ap-32f, -0x1.d9648ep-26f, 0x1.a1d82p-26f, -0x1.09e418p-26f, 0x1.0d01a2p-27f, -0x1.1cd124p-26f, 0x1.86d7f6p-26f, 0x1.25ca94p-29f,
+    -0x1.a0db88p-26f, 0x1.fa28b4p-27f, 0x1.f2e184p-26f, 0x1.ad270cp-28f, 0x1.a19e16p-27f, 0x1.aee31ap-27f, -0x1.e4db1p-28f, 0x1.448324p-26f,
+};
+constexpr float kLn2A = 0x1.63p-1f, kLn2B = -0x1.bdp-13f, kLn2C = -0x1.05c61p-29f;  // ln 2; A and B times 13 bits are exact
+
 // A logit's E values of a 16-byte piece.
 template <typename T>
 __device__ __forceinline__ float piece(const uint4& w, int j) {
@@ -274,21 +307,49 @@ __device__ __forceinline__ float score_of(uint64_t key) {
 }
 
 constexpr int kPick = 1024;   // threads
+struct One { static constexpr int value = 1; };
+struct Four { static constexpr int value = 4; };
 constexpr int kBins = 2 * kPick;
 struct PickSmem {
   uint64_t key[kBeamItems];       // the items at hand; the kept ones first
   uint64_t kept[kBeamMost];
-  double expo[kBeamMost];         // rows' references; then the kept runs
   uint32_t at[kBeamItems];
   uint32_t kept_at[kBeamMost];
-  double total[kBeamMost];        // rows' sums of exponentials; then their base scores
-  float ref[kBeamMost];           // what a row's logits are taken relative to
+  uint32_t run[kBeamMost];        // the kept runs
+  float2 base[kBeamMost];         // rows: the score of a logit at ref
+  float ref[kBeamMost];           // rows: what logits are taken relative to; kInf: ended
   int hist[kBins];
   uint32_t red[64];
   int n, digit, need, whole;
 };
 // An item is kept if its key is above `key`, or equal and its place at most `at`.
 struct Cut { uint64_t key; uint32_t at; };
+// Of the keys > 0 that a thread has seen: the largest and the smallest upper word, and how many.
+struct Seen {
+  uint32_t top = 0, bottom = 0xffffffffu;
+  int live = 0;
+  __device__ __forceinline__ void add(uint64_t k) {
+    if (!k) return;
+    top = max(top, (uint32_t)(k >> 32));
+    bottom = min(bottom, (uint32_t)(k >> 32));
+    ++live;
+  }
+};
+
+// ln((s + t) 2^q0), s > 0 and normal, t its rest, |q0| < 2^12, in two words (to 2^-35): table-driven (P. T. P. Tang), r = m c - 1 below 0.01.
+__device__ __forceinline__ float2 log2w(float s, float t, float q0) {
+  const uint32_t b = __float_as_uint(s);
+  const int q = (int)(b >> 23) - 127, j = b >> 17 & 63;
+  const float inv = __uint_as_float((uint32_t)(127 - q) << 23), mh = __fmul_rn(s, inv), ml = __fmul_rn(t, inv);
+  const float c = kLogC[j], ph = __fmul_rn(mh, c), r1 = __fadd_rn(ph, -1.f);
+  const float r0 = __fadd_rn(__fmaf_rn(mh, c, -ph), __fmul_rn(ml, c)), r = __fadd_rn(r1, r0), rl = __fadd_rn(r0, -__fadd_rn(r, -r1));
+  const float poly = r * r * __fmaf_rn(r, __fmaf_rn(r, __fmaf_rn(r, 0.2f, -0.25f), 1.f / 3.f), -0.5f);
+  const float n = (float)q + q0;
+  float hi, lo = two_sum(__fmul_rn(n, kLn2A), __fmul_rn(n, kLn2B), hi);
+  lo = __fadd_rn(lo, two_sum(hi, kLogHi[j], hi));
+  lo = __fadd_rn(lo, two_sum(hi, r, hi));
+  return make_float2(hi, __fadd_rn(lo, __fadd_rn(__fmaf_rn(n, kLn2C, kLogLo[j]), __fadd_rn(poly, rl))));
+}
 
 // The number of the CTA's counts before this thread's.
 __device__ __forceinline__ int count_before(PickSmem& s, int v) {
@@ -342,26 +403,14 @@ __device__ __forceinline__ bool digits(PickSmem& s, int cnt, uint64_t eq, uint64
   return whole;
 }
 
-// Of items [0, cnt) the `want` best to the front, in any order; returns how many there are (fewer: no more candidates).  low: a key
-// that none of the kept is below; 1 if they are fewer than `want`.
-__device__ int select_best(PickSmem& s, int cnt, int want, uint64_t& low) {
+// Of items [0, cnt) the `want` best to the front, in any order; returns how many there are (fewer: no more candidates).  seen: of the
+// threads' shares of the items.  low: a key that none of the kept is below; 1 if they are fewer than `want`.
+__device__ int select_best(PickSmem& s, int cnt, int want, Seen seen, uint64_t& low) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t top = 0, bottom = 0xffffffffu;  // of the keys' upper words
-  int live = 0;
-  for (int i = tid; i < cnt; i += kPick) {
-    const uint64_t k = s.key[i];
-    if (k) {
-      top = max(top, (uint32_t)(k >> 32));
-      bottom = min(bottom, (uint32_t)(k >> 32));
-      ++live;
-    }
-  }
-  top = __reduce_max_sync(FULL, top);
-  bottom = __reduce_min_sync(FULL, bottom);
-  live = __reduce_add_sync(FULL, live);
-  __syncthreads();
+  uint32_t top = __reduce_max_sync(FULL, seen.top), bottom = __reduce_min_sync(FULL, seen.bottom);
+  int live = __reduce_add_sync(FULL, seen.live);
   if (lane == 0) s.red[warp] = top, s.red[32 + warp] = bottom, s.hist[warp] = live;
-  __syncthreads();
+  __syncthreads();  // (the items are written, too)
   top = __reduce_max_sync(FULL, s.red[lane]);
   bottom = __reduce_min_sync(FULL, s.red[32 + lane]);
   live = __reduce_add_sync(FULL, s.hist[lane]);
@@ -408,8 +457,15 @@ __device__ int select_best(PickSmem& s, int cnt, int want, uint64_t& low) {
   __syncthreads();
   return n;
 }
+__device__ int select_best(PickSmem& s, int cnt, int want, uint64_t& low) {
+  Seen seen;
+  for (int i = threadIdx.x; i < cnt; i += kPick) seen.add(s.key[i]);
+  __syncthreads();
+  return select_best(s, cnt, want, seen, low);
+}
 
-// A CTA a group: the rows' logarithms, the n best runs, the n best tokens of those, in order.
+// A CTA a group: the rows' logarithms, the n best runs, the n best tokens of those, in order.  Bound by the latency of some
+// twenty steps that the CTA takes together.
 template <typename T>
 __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   pdl_enter();
@@ -419,55 +475,66 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   const int tid = threadIdx.x;
   const int64_t row0 = (int64_t)blockIdx.x * a.K;
   if (blockIdx.x == 0 && tid == 0) *a.err = 0;
-  float2* base = reinterpret_cast<float2*>(s.total);  // [K], over the sums once they are used
   // the rows' sums from their parts, 1 to 32 threads a row
   int team = 1;
   while (team < a.tasks && team < 32) team <<= 1;
   for (int b0 = 0; b0 < a.K; b0 += kPick / team) {
     const int b = b0 + tid / team, t = tid % team;
+    const bool is = b < a.K, ended = is && a.done && a.done[row0 + b], mine = is && !ended;
+    const float c = is ? a.scores[row0 + b] : 0.f;
     const BeamPart* p = a.part + (row0 + b) * a.tasks;
-    const bool mine = b < a.K && !(a.done && a.done[row0 + b]);
     float best = -kInf, most = -kInf;  // of the parts near 0: as powers of two, exactly; of those far from it
     for (int i = t; mine && i < a.tasks; i += team) {
-      if (p[i].far) most = fmaxf(most, p[i].ref);
-      else best = fmaxf(best, p[i].ref);
+      const BeamPart q = p[i];
+      if (q.far) most = fmaxf(most, q.ref);
+      else best = fmaxf(best, q.ref);
     }
     for (int o = team / 2; o; o >>= 1) {
       best = fmaxf(best, __shfl_xor_sync(FULL, best, o));
       most = fmaxf(most, __shfl_xor_sync(FULL, most, o));
     }
-    const bool far = most > -kInf;
-    double e = best > -kInf ? (double)best * kLn2 : -kInf, sum = 0.;  // the sum is sum exp(e)
+    float2 at0 = make_float2(-kInf, 0.f);  // no value above -infinity, or a NaN among them: no candidates
     float ref = 0.f;
-    if (far && (double)most > e) e = (double)most, ref = most;  // relative to a logit itself where it is far from 0
-    for (int i = t; mine && i < a.tasks; i += team) {
-      const BeamPart q = p[i];
-      double f = 1.;  // (a part without values has a sum of 0, or NaN)
-      if (q.ref > -kInf && far) f = exp((q.far ? (double)q.ref : (double)q.ref * kLn2) - e);
-      else if (q.ref > -kInf) f = q.ref > best - 1000.f ? __hiloint2double((1023 + (int)(q.ref - best)) << 20, 0) : 0.;
-      sum += sum_of(q) * f;
-    }
-    for (int o = team / 2; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-    if (b < a.K && t == 0) s.total[b] = sum, s.expo[b] = ref != 0.f ? 0. : e, s.ref[b] = ref;
-  }
-  __syncthreads();
-  float2 mine = make_float2(-kInf, 0.f);
-  if (tid < a.K) {
-    const float c = a.scores[row0 + tid];
-    if (a.done && a.done[row0 + tid]) {
-      mine = make_float2(c, 0.f);
-    } else {
-      const double sum = s.total[tid];
-      if (sum > 0.) {  // else no value above -infinity, or a NaN among them
-        const double v = (double)c - (s.expo[tid] + log(sum));
-        mine.x = (float)v;
-        if (fabsf(mine.x) < kInf) mine.y = (float)(v - (double)mine.x);
+    if (!__any_sync(FULL, most > -kInf)) {
+      float hi = 0.f, lo = 0.f;
+      for (int i = t; mine && i < a.tasks; i += team) {
+        const BeamPart q = p[i];
+        const float d = best - q.ref, f = d < 120.f ? __uint_as_float((uint32_t)(127 - (int)d) << 23) : 0.f;  // (a part without values is 0, or NaN)
+        lo += two_sum(hi, (float)(q.hi >> 12) * 0x1p-4f * f, hi);
+        lo += two_sum(hi, (float)(q.hi & 4095) * 0x1p-16f * f, hi);
+        lo += two_sum(hi, q.lo * f, hi);
+      }
+      for (int o = team / 2; o; o >>= 1) {
+        const float oh = __shfl_xor_sync(FULL, hi, o), ol = __shfl_xor_sync(FULL, lo, o);
+        lo = lo + ol + two_sum(hi, oh, hi);
+      }
+      lo = two_sum(hi, lo, hi);
+      if (hi > 0.f) {
+        const float2 l = log2w(hi, lo, best);
+        const float e = two_sum(c, -l.x, at0.x);
+        at0.y = fabsf(at0.x) < kInf ? two_sum(at0.x, e - l.y, at0.x) : 0.f;
+      }
+    } else {  // some row of the warp has logits far from 0: in 64 bits, relative to the largest part's, a logit itself if it is a far one
+      const bool far = most > -kInf;
+      double e = best > -kInf ? (double)best * kLn2 : -kInf, sum = 0.;
+      if (far && (double)most > e) e = (double)most, ref = most;
+      for (int i = t; mine && i < a.tasks; i += team) {
+        const BeamPart q = p[i];
+        sum += sum_of(q) * (q.ref > -kInf ? exp((q.far ? (double)q.ref : (double)q.ref * kLn2) - e) : 1.);
+      }
+      for (int o = team / 2; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+      if (sum > 0.) {
+        const double v = (double)c - ((ref != 0.f ? 0. : e) + log(sum));
+        at0.x = (float)v;
+        if (fabsf(at0.x) < kInf) at0.y = (float)(v - (double)at0.x);
       }
     }
-    if (!(mine.x > -kInf)) mine = make_float2(-kInf, 0.f);  // NaN: no candidates
+    if (ended) at0 = make_float2(c, 0.f), ref = kInf;
+    if (is && t == 0) {
+      s.base[b] = at0.x > -kInf ? at0 : make_float2(-kInf, 0.f);  // NaN: no candidates
+      s.ref[b] = ref;
+    }
   }
-  __syncthreads();
-  if (tid < a.K) base[tid] = mine;
   __syncthreads();
   // the n best runs, kBeamItems at a time
   const uint32_t runs = (uint32_t)a.runs, all = (uint32_t)a.K * runs;
@@ -476,103 +543,160 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   uint64_t low = 1;
   for (uint32_t i0 = 0; i0 < all;) {
     const int more = (int)min((uint32_t)(kBeamItems - have), all - i0);
-    for (int j = tid; j < more; j += kPick) {
-      const uint32_t i = i0 + j, b = i / runs;
-      s.at[have + j] = i;
-      s.key[have + j] = a.done && a.done[row0 + b] ? (i == b * runs ? key_of(base[b], 0.f, 0.f) : 0) : key_of(base[b], tops[i], s.ref[b]);
+    Seen seen;
+    if (tid < have) seen.add(s.key[tid]);
+    for (int j0 = tid; j0 < more; j0 += 4 * kPick) {
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = j0 + u * kPick < more ? tops[i0 + j0 + u * kPick] : 0.f;  // (an ended beam's: anything)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + u * kPick;
+        if (j >= more) continue;
+        const uint32_t i = i0 + j, b = i / runs;
+        const float ref = s.ref[b];
+        const bool ended = ref == kInf;
+        const uint64_t k = ended && i != b * runs ? 0 : key_of(s.base[b], ended ? 0.f : v[u], ended ? 0.f : ref);
+        s.at[have + j] = i;
+        s.key[have + j] = k;
+        seen.add(k);
+      }
     }
-    __syncthreads();
-    have = select_best(s, have + more, a.n, low);
+    have = select_best(s, have + more, a.n, seen, low);
     i0 += more;
   }
-  uint32_t* run = reinterpret_cast<uint32_t*>(s.expo);  // out of the way of the tokens
-  if (tid < have) run[tid] = s.at[tid];
+  if (tid < have) s.run[tid] = s.at[tid];
   if (tid == 0) s.n = 0;
   __syncthreads();
-  // their tokens, a piece a thread: those not below `low`, which is n runs' largest at least
+  // their tokens, a piece a thread: those not below `low`, which is n runs' largest at least: few more than n, unless many are alike
   const int pieces = have << a.lg;
-  for (int i0 = 0; i0 < pieces; i0 += kPick) {
-    const int i = i0 + tid;
-    if (i < pieces) {
-      const uint32_t r = run[i >> a.lg], b = r / runs;
-      const int64_t row = row0 + b;
-      const float2 bs = base[b];
+  const float lowest = score_of(low);
+  auto tokens = [&](int i0, auto many) {  // of pieces i0, i0 + kPick ..
+    constexpr int U = decltype(many)::value;
+    uint4 w[U];
+    uint32_t ok[U], row[U];
+    int t0[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kPick;
+      ok[u] = 0;
+      if (i >= pieces) continue;
+      const uint32_t r = s.run[i >> a.lg], b = r / runs;
+      row[u] = b;
+      const int64_t at = row0 + b;
+      const int j = i & ((1 << a.lg) - 1);
+      t0[u] = (int)(((r - b * runs) << a.lg) + j) * E - row_offset<T>(a, at);
+      if (s.ref[b] == kInf) {
+        ok[u] = j == 0 ? 1 : 0;
+        continue;
+      }
+      ok[u] = a.allowed ? mask_bits<E>(a.allowed + at * a.words, a.words, t0[u]) : (1u << E) - 1;
+      if (t0[u] >= 0 && t0[u] + E <= a.V) w[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits) + at * a.ld + t0[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!ok[u]) continue;
+      const uint32_t b = row[u];
+      const float2 bs = s.base[b];
       const float ref = s.ref[b];
       auto put = [&](float x, float rf, uint32_t t) {
         const uint64_t k = key_of(bs, x, rf);
         if (k < low) return;
         const int to = atomicAdd(&s.n, 1);
+        if (to >= kBeamItems) return;
         s.key[to] = k;
         s.at[to] = b * (uint32_t)a.V + t;
       };
-      if (a.done && a.done[row]) {
-        if ((i & ((1 << a.lg) - 1)) == 0) put(0.f, 0.f, (uint32_t)a.eos);
-      } else {
-        const int t0 = (int)(((r - b * runs) << a.lg) + (i & ((1 << a.lg) - 1))) * E - row_offset<T>(a, row);
-        const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-        // what is below this as one sum of fp32, off by 2^-23 of either number at most, is below `low` (NaN: nothing is)
-        const float lowest = score_of(low), least = lowest - 0x1p-21f * (fabsf(lowest) + fabsf(bs.x)) - 1e-30f;
-        const bool inside = t0 >= 0 && t0 + E <= a.V;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (inside) w = *reinterpret_cast<const uint4*>(x + t0);
-        uint32_t ok = (1u << E) - 1;
-        if (a.allowed) ok = mask_bits<E>(a.allowed + row * a.words, a.words, t0);
+      if (ref == kInf) {
+        put(0.f, 0.f, (uint32_t)a.eos);
+        continue;
+      }
+      // what is below this as one sum of fp32, off by 2^-23 of either number at most, is below `low` (NaN: nothing is)
+      const float least = lowest - 0x1p-21f * (fabsf(lowest) + fabsf(bs.x)) - 1e-30f;
+      const bool inside = t0[u] >= 0 && t0[u] + E <= a.V;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const int t = t0 + j;
-          if (!inside && (t < 0 || t >= a.V)) continue;
-          const float v = inside ? piece<T>(w, j) : to_f(x[t]);
-          if ((ok >> j & 1) && !(bs.x + (v - ref) < least)) put(v, ref, (uint32_t)t);
-        }
+      for (int j = 0; j < E; ++j) {
+        const int t = t0[u] + j;
+        if (!(ok[u] >> j & 1) || (!inside && (t < 0 || t >= a.V))) continue;
+        const float v = inside ? piece<T>(w[u], j) : to_f(static_cast<const T*>(a.logits)[(row0 + b) * a.ld + t]);
+        if (!(bs.x + (v - ref) < least)) put(v, ref, (uint32_t)t);
       }
     }
-    __syncthreads();
-    const int cnt = s.n;
-    __syncthreads();
-    if (cnt > kBeamItems - kPick * E) {  // room for as many again
-      uint64_t l;
-      select_best(s, cnt, a.n, l);
-      low = max(low, l);
-    }
-  }
+  };
+  for (int i0 = 0; i0 < pieces; i0 += 4 * kPick) tokens(i0 + tid, Four{});
+  __syncthreads();
   int cnt = s.n;
   __syncthreads();
+  if (cnt > kBeamItems) {  // many alike: again, as many at a time as there is room for
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    for (int i0 = 0; i0 < pieces; i0 += kPick) {
+      tokens(i0 + tid, One{});
+      __syncthreads();
+      cnt = s.n;
+      __syncthreads();
+      if (cnt > kBeamItems - kPick * E) {
+        uint64_t l;
+        select_best(s, cnt, a.n, l);
+        low = max(low, l);
+      }
+    }
+    cnt = s.n;
+    __syncthreads();
+  }
   if (cnt > kPick) {
     uint64_t l;
     cnt = select_best(s, cnt, a.n, l);
   }
-  // in order, an item a thread: bitonic, by (key descending, place ascending)
-  int size = 1;
-  while (size < cnt) size <<= 1;
+  // in order, by (key descending, place ascending), an item a thread: each warp sorts its 32, then an item's rank is how many of each
+  // warp's precede it, by halving (a bitonic sort of all takes twice as long at 256 items, five times at 1024)
   uint64_t key = tid < cnt ? s.key[tid] : 0;
   uint32_t at = tid < cnt ? s.at[tid] : 0xffffffffu;
-  for (int k = 2; k <= size; k <<= 1)
-    for (int j = k >> 1; j; j >>= 1) {
-      uint64_t ok;
-      uint32_t oa;
-      if (j < 32) {
-        ok = __shfl_xor_sync(FULL, key, j);
-        oa = __shfl_xor_sync(FULL, at, j);
-      } else {
-        __syncthreads();
-        s.key[tid] = key;
-        s.at[tid] = at;
-        __syncthreads();
-        ok = s.key[tid ^ j];
-        oa = s.at[tid ^ j];
+  const int warps = (cnt + 31) / 32, lane = tid & 31;
+  __syncthreads();
+  int rank = kBeamMost;
+  if (tid < warps * 32) {
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+      for (int j = k >> 1; j; j >>= 1) {
+        const uint64_t ok = __shfl_xor_sync(FULL, key, j);
+        const uint32_t oa = __shfl_xor_sync(FULL, at, j);
+        const bool better = key > ok || (key == ok && at < oa);
+        if (better != (((lane & j) == 0) == ((lane & k) == 0))) key = ok, at = oa;
       }
-      const bool better = key > ok || (key == ok && at < oa);
-      if (better != (((tid & j) == 0) == ((tid & k) == 0))) key = ok, at = oa;
+    s.key[tid] = key;
+    s.at[tid] = at;
+  }
+  __syncthreads();
+  if (tid < warps * 32 && key) {
+    rank = lane;
+    for (int w = 0; w < warps; ++w) {
+      if (w == tid >> 5) continue;
+      int pos = w * 32;
+#pragma unroll
+      for (int st = 16; st; st >>= 1) {
+        const uint64_t k = s.key[pos + st - 1];
+        if (k > key || (k == key && s.at[pos + st - 1] < at)) pos += st;
+      }
+      const uint64_t k = s.key[pos];
+      rank += pos - w * 32 + (k > key || (k == key && s.at[pos] < at));
     }
+  }
   const int have_n = min(cnt, a.n);
-  if (tid < a.n) {
-    const int64_t o = (int64_t)blockIdx.x * a.n + tid;
-    const bool is = tid < have_n;
-    const uint32_t b = is ? at / (uint32_t)a.V : 0, t = at - b * (uint32_t)a.V;
-    a.out_scores[o] = is ? score_of(key) : -kInf;
-    a.out_tokens[o] = is ? (int)t : -1;
-    a.out_parents[o] = (int)b;
-    if (a.out_done) a.out_done[o] = is && ((a.done && a.done[row0 + b]) || (int)t == a.eos);
+  const int64_t o = (int64_t)blockIdx.x * a.n;
+  if (rank < have_n) {
+    const uint32_t b = at / (uint32_t)a.V, t = at - b * (uint32_t)a.V;
+    a.out_scores[o + rank] = score_of(key);
+    a.out_tokens[o + rank] = (int)t;
+    a.out_parents[o + rank] = (int)b;
+    if (a.out_done) a.out_done[o + rank] = (a.done && a.done[row0 + b]) || (int)t == a.eos;
+  }
+  if (tid >= have_n && tid < a.n) {
+    a.out_scores[o + tid] = -kInf;
+    a.out_tokens[o + tid] = -1;
+    a.out_parents[o + tid] = 0;
+    if (a.out_done) a.out_done[o + tid] = 0;
   }
 }
 
