@@ -703,7 +703,7 @@ LnArgs ln_args(const RowPlan& p, const void* x, int64_t ldx, const void* w, void
   LnArgs a{};
   a.x = x; a.ldx = ldx; a.w = w;
   a.rows = p.rows; a.d = p.d;
-  a.lens = p.lens; a.L = p.L;
+  a.lens = p.lens; a.L = p.L; a.slots = p.lens ? (int)(p.rows / p.L) : 0;
   a.err = at<int>(ws, 0);
   return a;
 }
@@ -1348,7 +1348,7 @@ gbla_status embed_forward(const gbla_shape* shape, const void* ids, int wide_ids
   const RowCtx c{static_cast<cudaStream_t>(stream)};
   EmbedArgs a = embed_args(p, ids, wide_ids, k, vocab, scale, ws);
   a.table = table; a.y = y;
-  if (embed_fwd_ctas(a, p.f32) > 1) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
+  if (!embed_fwd_clears(a)) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
   GBLA_CHECK(launch_embed_fwd(a, p.f32, c.st), "embed fwd");
   return GBLA_OK;
 }
@@ -1378,7 +1378,7 @@ gbla_status embed_backward(const gbla_shape* shape, const void* ids, int wide_id
   s.part = at<float>(ws, l.part);
   s.n_long = at<int>(ws, 4);
   s.longs = at<int2>(ws, l.longs);
-  GBLA_CHECK(launch_zero(ws, l.zero_bytes, c.st), "clear");
+  if (s.tiles > 1) GBLA_CHECK(launch_zero(ws, l.zero_bytes, c.st), "clear");
   const int groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
   for (int i = 0; i < (s.tiles == 1 ? 1 : l.passes); ++i) {
     s.key_in = s.keys[(i + 1) & 1]; s.slot_in = s.slots[(i + 1) & 1];
@@ -1416,7 +1416,7 @@ gbla_status layer_norm_forward(const gbla_shape* shape, const void* x, int64_t l
   const RowCtx c{static_cast<cudaStream_t>(stream)};
   LnArgs a = ln_args(p, x, ldx, w, ws);
   a.res = res; a.b = b; a.eps = eps; a.sum = sum; a.y = y; a.stats = stats;
-  if (a.lens) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
+  if (!ln_clears(a)) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
   GBLA_CHECK(launch_ln(a, p.f32, false, c.st), "layer norm fwd");
   return GBLA_OK;
 }
@@ -1436,7 +1436,7 @@ gbla_status layer_norm_backward(const gbla_shape* shape, const void* x, int64_t 
   LnArgs a = ln_args(p, x, ldx, w, ws);
   a.stats = const_cast<float*>(stats); a.dy = dy; a.ds = ds; a.dx = dx;
   a.part = dw || db ? at<float>(ws, kAlign) : nullptr;
-  if (a.lens) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
+  if (!ln_clears(a)) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
   GBLA_CHECK(launch_ln(a, p.f32, true, c.st), "layer norm bwd");
   if (!a.part) return GBLA_OK;
   if (!ln_group(p.d)) GBLA_CHECK(launch_ln_cols_long(a, p.f32, c.st), "layer norm cols");

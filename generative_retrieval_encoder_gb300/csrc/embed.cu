@@ -19,22 +19,28 @@ constexpr int kThreads = 256;
 constexpr int kMaxBins = 1 << kEmbedDigit;  // a thread's each, at most
 static_assert(kMaxBins <= kThreads, "");
 
-// The id of a slot, -1 for none.  An id past the table or a length outside [0, L] sets the error word and counts as none.
-__device__ __forceinline__ int id_of(const EmbedArgs& a, int64_t slot) {
+// The id of a slot, -1 for none.  An id past the table or a length outside [0, L] counts as none and is `bad`.
+__device__ __forceinline__ int id_of(const EmbedArgs& a, int64_t slot, bool& bad) {
   const int64_t id = a.wide_ids ? static_cast<const int64_t*>(a.ids)[slot] : (int64_t)static_cast<const int32_t*>(a.ids)[slot];
   if (a.lens) {
     const int row = (int)slot / a.k, b = row / a.L, len = a.lens[b];
     if (len < 0 || len > a.L) {
-      atomicOr(a.err, 1);
+      bad = true;
       return -1;
     }
     if (row - b * a.L >= len) return -1;
   }
   if (id >= a.V) {
-    atomicOr(a.err, 1);
+    bad = true;
     return -1;
   }
   return id < 0 ? -1 : (int)id;
+}
+__device__ __forceinline__ int id_of(const EmbedArgs& a, int64_t slot) {  // and says so in the error word
+  bool bad = false;
+  const int id = id_of(a, slot, bad);
+  if (bad) atomicOr(a.err, 1);
+  return id;
 }
 
 template <typename T>
@@ -49,16 +55,23 @@ __device__ __forceinline__ uint4 scaled(uint4 w, float s) {
 // A CTA takes `per` slots: their ids once, then the rows as one run of `cols` accesses each (16 bytes where WIDE, one value
 // else), four in flight a thread.
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads) k_embed_fwd(const EmbedArgs a, int per, int cols, uint32_t by_cols) {
+__global__ void __launch_bounds__(kThreads) k_embed_fwd(const EmbedArgs a, int per, int cols, uint32_t by_cols, bool check) {
   pdl_enter();
   __shared__ int id[1024];
-  if (gridDim.x == 1) {  // nobody else has an error to report
-    if (threadIdx.x == 0) *a.err = 0;
-    __syncthreads();
+  if (check && blockIdx.x == gridDim.x - 1) {  // one CTA looks at every id and alone reports: no launch to clear the error word first
+    bool bad = false;
+    for (int64_t i = threadIdx.x; i < a.n; i += kThreads) id_of(a, i, bad);
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *a.err = any ? 1 : 0;
+    return;
   }
   const int64_t s0 = (int64_t)blockIdx.x * per;
   const int ns = (int)min((int64_t)per, a.n - s0);
-  for (int i = threadIdx.x; i < ns; i += kThreads) id[i] = id_of(a, s0 + i);
+  for (int i = threadIdx.x; i < ns; i += kThreads) {
+    bool bad = false;
+    id[i] = id_of(a, s0 + i, bad);
+    if (bad && !check) atomicOr(a.err, 1);
+  }
   __syncthreads();
   const T* tab = static_cast<const T*>(a.table);
   T* y = static_cast<T*>(a.y) + s0 * a.d;
@@ -148,6 +161,10 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
   __shared__ int base[kMaxBins];
   __shared__ int red[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tile = blockIdx.x, bins = 1 << bits;
+  if (ALL) {  // no launch before this one cleared the words that it and the next ones count in
+    if (threadIdx.x == 0) *a.err = *s.n_long = 0;
+    __syncthreads();
+  }
   for (;;) {
     for (int i = lane; i < bins; i += 32) warp_count[warp][i] = 0;
     __syncwarp();
@@ -545,23 +562,21 @@ int row_cols(const EmbedArgs& a, bool f32, bool& wide) {
 
 }  // namespace
 
-// Slots of a CTA of the forward, about four accesses a thread.
-int embed_fwd_ctas(const EmbedArgs& a, bool f32) {
-  bool wide;
-  const int per = std::max(1, 1024 / row_cols(a, f32, wide));
-  return (int)((a.n + per - 1) / per);
-}
+// Up to so many ids one more CTA of the forward checks them, 32 a thread, while the others copy (a launch that clears the error word
+// is 1 us on the device and 2 on the host); of more, each reports what it finds.
+constexpr int64_t kCheckIds = 8192;
+bool embed_fwd_clears(const EmbedArgs& a) { return a.n <= kCheckIds; }
 
 cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st) {
   bool wide;
-  const int cols = row_cols(a, f32, wide), per = std::max(1, 1024 / cols);
+  const int cols = row_cols(a, f32, wide), per = std::max(1, 1024 / cols);  // about four accesses a thread
   // i / cols = the high word of i ceil(2^32 / cols) for i cols < 2^32: here i < 1024 and cols <= 1024
   const uint32_t by = cols == 1 ? 0 : (uint32_t)((0x100000000ull + cols - 1) / cols);
-  const dim3 grid((unsigned)embed_fwd_ctas(a, f32));
-  if (f32) return wide ? launch_pdl(k_embed_fwd<float, true>, grid, dim3(kThreads), 0, st, a, per, cols, by)
-                       : launch_pdl(k_embed_fwd<float, false>, grid, dim3(kThreads), 0, st, a, per, cols, by);
-  return wide ? launch_pdl(k_embed_fwd<bf16, true>, grid, dim3(kThreads), 0, st, a, per, cols, by)
-              : launch_pdl(k_embed_fwd<bf16, false>, grid, dim3(kThreads), 0, st, a, per, cols, by);
+  const bool check = embed_fwd_clears(a);
+  const dim3 grid((unsigned)((a.n + per - 1) / per + (check ? 1 : 0)));
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kThreads), 0, st, a, per, cols, by, check); };
+  if (f32) return wide ? go(k_embed_fwd<float, true>) : go(k_embed_fwd<float, false>);
+  return wide ? go(k_embed_fwd<bf16, true>) : go(k_embed_fwd<bf16, false>);
 }
 
 cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st) {

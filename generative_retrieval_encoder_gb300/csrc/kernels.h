@@ -319,12 +319,14 @@ struct LnArgs {
   void* dx; float* part;              // [rows, d]; [ln_parts][2][d] or null
   int64_t rows; int d;
   const int32_t* lens; int L;         // padded slots: valid rows of each, or null
-  int* err;                           // the error word: 0 on entry with lens, cleared by the kernel without
+  int slots, first;                   // padded slots; the first CTA with rows (set by launch_ln)
+  int* err;                           // the error word, 0 on entry (but where ln_clears)
 };
+bool ln_clears(const LnArgs& a);      // whether launch_ln clears the error word itself
 int ln_group(int d);
 int ln_ctas(int64_t rows, int d);
 int ln_parts(int64_t rows, int d);    // partial rows of the gradients of w and b
-cudaError_t launch_ln(const LnArgs& a, bool f32, bool bwd, cudaStream_t st);
+cudaError_t launch_ln(LnArgs a, bool f32, bool bwd, cudaStream_t st);
 // Rows that no group of threads holds (ln_group = 0): their partial column sums, by a kernel of their own.
 cudaError_t launch_ln_cols_long(const LnArgs& a, bool f32, cudaStream_t st);
 // dw, db (either may be null) from the partial rows.
@@ -343,7 +345,7 @@ struct EmbedArgs {
   const void* table; void* y;         // [V, d]; [n, d]
   const void* dy; float* dtable;      // [n, d]; [V, d]
   const int32_t* lens; int L;         // padded slots: valid tokens of each, or null
-  int* err;                           // the error word, 0 on entry (the forward of one CTA clears it itself)
+  int* err;                           // the error word, 0 on entry (but where the kernel clears it itself)
 };
 struct EmbedSort {
   int tiles, key_bits;
@@ -354,9 +356,9 @@ struct EmbedSort {
   int* n_long; int2* longs;           // how many ids have more than kEmbedCap slots, 0 on entry; each and its first partial row
   int* last;                          // [V]: of such an id its last partial row
 };
-int embed_fwd_ctas(const EmbedArgs& a, bool f32);
+bool embed_fwd_clears(const EmbedArgs& a);  // whether launch_embed_fwd clears the error word itself
 cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st);
-// One pass of the sort, by the digit of `bits` bits at `shift`; a single tile's launch_embed_place is the whole sort.
+// One pass of the sort, by the digit of `bits` bits at `shift`; a single tile's launch_embed_place is the whole sort, and clears.
 cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st);
 cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st);
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st);

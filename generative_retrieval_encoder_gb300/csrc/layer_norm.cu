@@ -19,15 +19,30 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kThreads = 256;
 
+// Up to so many slots one CTA checks their lengths while the others work (a launch that clears the error word is 1 us on the device and
+// 2 on the host); of more, the first row of each reports what it finds.
+constexpr int kCheckSlots = 8192;
+
 // Whether row `row` belongs to its sequence; a length outside [0, L] sets the error word and counts as 0.
 __device__ __forceinline__ bool row_valid(const LnArgs& a, int64_t row) {
   if (!a.lens) return true;
   const int b = (int)row / a.L, len = a.lens[b];
   if (len < 0 || len > a.L) {
-    if (row == (int64_t)b * a.L) atomicOr(a.err, 1);
+    if (a.slots > kCheckSlots && row == (int64_t)b * a.L) atomicOr(a.err, 1);
     return false;
   }
   return row - (int64_t)b * a.L < len;
+}
+// The error word.  With lengths to check that is the first CTA's only work (a.first = 1): it alone reports, and returns true.
+__device__ __forceinline__ bool check_slots(const LnArgs& a) {
+  if (blockIdx.x > 0 || a.slots > kCheckSlots) return false;
+  int bad = 0;
+  if (a.first) {
+    for (int b = threadIdx.x; b < a.slots; b += kThreads) bad |= a.lens[b] < 0 || a.lens[b] > a.L;
+    bad = __syncthreads_or(bad);
+  }
+  if (threadIdx.x == 0) *a.err = bad ? 1 : 0;
+  return a.first;
 }
 
 // The column of value i of thread t in a row of G threads: 16-byte pieces dealt out in turn (WIDE), or single values.
@@ -134,8 +149,9 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 2 : !WIDE ? 3 : N * sizeof
   using R = Row<T, G, N, WIDE>;
   const int t = threadIdx.x % G;
   const float inv = 1.f / (float)a.d;
-  if (!a.lens && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
+  if (check_slots(a)) return;
+  const int64_t cta = blockIdx.x - a.first, ctas = gridDim.x - a.first;
+  const int64_t row = cta * (kThreads / G) + threadIdx.x / G;
   const bool in = row < a.rows, live = in && row_valid(a, row);
   float s[N];
   {
@@ -191,14 +207,15 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
   using Mine = Row<T, G, N, WIDE>;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const float inv = 1.f / (float)a.d;
-  if (!a.lens && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  if (check_slots(a)) return;
+  const int64_t cta = blockIdx.x - a.first, ctas = gridDim.x - a.first;
   Mine w, x, y, s;
   float dw[N], db[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.f;
   if (a.w) w.load(static_cast<const T*>(a.w), t, a.d);
   s.clear();
-  const int64_t step = (int64_t)gridDim.x * R;
+  const int64_t step = ctas * R;
   auto ask = [&](int64_t row, int slot) {
     if (row < a.rows && row_valid(a, row)) {
       uint4* to = ring + slot * 3 * P * kThreads;
@@ -210,10 +227,10 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
   };
   if (A > 0) {
 #pragma unroll
-    for (int k = 0; k < A; ++k) ask((int64_t)blockIdx.x * R + grp + k * step, k);
+    for (int k = 0; k < A; ++k) ask(cta * R + grp + k * step, k);
   }
   int slot = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += step) {  // (as often in every thread of the CTA)
+  for (int64_t r0 = cta * R; r0 < a.rows; r0 += step) {  // (as often in every thread of the CTA)
     const int64_t row = r0 + grp;
     const bool in = row < a.rows, live = in && row_valid(a, row);
     float mean = 0.f, r = 0.f;
@@ -262,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
   if (A > 0) cp_async_wait<0>();
   if (!a.part) return;
   // [CTA][dw | db][d], the CTA's rows summed in the order of its groups
-  float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
+  float* out = a.part + cta * 2 * a.d;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if (R == 1) {
@@ -301,9 +318,10 @@ __global__ void __launch_bounds__(kThreads) k_ln_fwd_long(const LnArgs a) {
   pdl_enter();
   __shared__ float red[kThreads / 32];
   const float inv = 1.f / (float)a.d;
-  if (!a.lens && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  if (check_slots(a)) return;
+  const int64_t cta = blockIdx.x - a.first, ctas = gridDim.x - a.first;
   const T *w = static_cast<const T*>(a.w), *b = static_cast<const T*>(a.b);
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  for (int64_t row = cta; row < a.rows; row += ctas) {
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
     const T* res = a.res ? static_cast<const T*>(a.res) + row * a.d : nullptr;
     T* sum = a.sum ? static_cast<T*>(a.sum) + row * a.d : nullptr;
@@ -345,9 +363,10 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd_long(const LnArgs a) {
   pdl_enter();
   __shared__ float red[kThreads / 32];
   const float inv = 1.f / (float)a.d;
-  if (!a.lens && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  if (check_slots(a)) return;
+  const int64_t cta = blockIdx.x - a.first, ctas = gridDim.x - a.first;
   const T* w = static_cast<const T*>(a.w);
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  for (int64_t row = cta; row < a.rows; row += ctas) {
     const T *x = static_cast<const T*>(a.x) + row * a.ldx, *dy = static_cast<const T*>(a.dy) + row * a.d;
     const T* ds = a.ds ? static_cast<const T*>(a.ds) + row * a.d : nullptr;
     T* dx = static_cast<T*>(a.dx) + row * a.d;
@@ -416,14 +435,14 @@ __global__ void __launch_bounds__(1024) k_ln_cols(const float* part, int n, int 
 
 template <typename T, int G, int N, bool WIDE>
 cudaError_t run(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
-  if (!bwd) return launch_pdl(k_ln_fwd<T, G, N, WIDE>, dim3((unsigned)((a.rows + kThreads / G - 1) / (kThreads / G))), dim3(kThreads), 0, st, a);
+  if (!bwd) return launch_pdl(k_ln_fwd<T, G, N, WIDE>, dim3((unsigned)((a.rows + kThreads / G - 1) / (kThreads / G)) + a.first), dim3(kThreads), 0, st, a);
   const size_t ring = (size_t)kAhead<T, N, WIDE> * 3 * N * sizeof(T) * kThreads;
   const size_t smem = std::max(ring, a.part && kThreads / G > 1 ? (size_t)kThreads * N * 4 : 0);
   if (smem > 32 << 10) {
     const cudaError_t e = cudaFuncSetAttribute(k_ln_bwd<T, G, N, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(k_ln_bwd<T, G, N, WIDE>, dim3((unsigned)ctas), dim3(kThreads), smem, st, a);
+  return launch_pdl(k_ln_bwd<T, G, N, WIDE>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), smem, st, a);
 }
 template <typename T, bool WIDE>
 cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
@@ -435,12 +454,13 @@ cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
     case 128: return run<T, 128, 16, WIDE>(a, bwd, ctas, st);
     case 256: return a.d <= 4096 ? run<T, 256, 16, WIDE>(a, bwd, ctas, st) : run<T, 256, 32, WIDE>(a, bwd, ctas, st);
   }
-  if (!bwd) return launch_pdl(k_ln_fwd_long<T>, dim3((unsigned)ctas), dim3(kThreads), 0, st, a);
-  return launch_pdl(k_ln_bwd_long<T>, dim3((unsigned)ctas), dim3(kThreads), 0, st, a);
+  if (!bwd) return launch_pdl(k_ln_fwd_long<T>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
+  return launch_pdl(k_ln_bwd_long<T>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace
 
+bool ln_clears(const LnArgs& a) { return a.slots <= kCheckSlots; }
 // Threads of a row: 8 values each up to 256 columns, 16 up to 4096, 32 up to 8192; 0: a CTA in passes.
 int ln_group(int d) {
   if (d <= 64) return 8;
@@ -457,7 +477,8 @@ int ln_ctas(int64_t rows, int d) {
 }
 int ln_parts(int64_t rows, int d) { return ln_group(d) ? ln_ctas(rows, d) : (int)std::min<int64_t>(rows, 16); }
 
-cudaError_t launch_ln(const LnArgs& a, bool f32, bool bwd, cudaStream_t st) {
+cudaError_t launch_ln(LnArgs a, bool f32, bool bwd, cudaStream_t st) {
+  a.first = a.slots > 0 && a.slots <= kCheckSlots;
   const size_t es = f32 ? 4 : 2;
   uintptr_t bits = (uintptr_t)(a.d * es) | (uintptr_t)(a.ldx * es);
   for (const void* q : {a.x, a.res, a.w, a.b, (const void*)a.sum, (const void*)a.y, a.dy, a.ds, (const void*)a.dx})

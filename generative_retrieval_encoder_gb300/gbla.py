@@ -586,11 +586,13 @@ def gbla_adamw_step(plan: AdamWPlan, lr: float, betas=(0.9, 0.999), eps: float =
 
 
 def _arg(name, t, shape, dtype, device):
-    """t's address.  Raises unless t is a contiguous tensor of this shape, dtype and device."""
-    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: want contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} with strides "
-                         f"{t.stride()} on {t.device}")
-    return t.data_ptr()
+    """t's address (None: of none).  Raises unless t is a contiguous tensor of this shape, dtype and device."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: want contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} with strides "
+                     f"{t.stride()} on {t.device}")
 
 
 def _cuda(name, t):
@@ -599,13 +601,17 @@ def _cuda(name, t):
     return t.device
 
 
-def _ws(ws, size, what, device):
-    """A workspace of `size` bytes (0: the arguments' error) and its address and bytes."""
-    if ws is None:
-        if size == 0:
-            _check(GBLA_ERR_INVALID_ARG, what)
-        ws = torch.empty(size, dtype=torch.uint8, device=device)
-    return _glr_bytes("ws", ws, 0, device), ws.numel() * ws.element_size()
+def _ws(ws, device):
+    """A workspace's address and bytes."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: want contiguous bytes on {device}, got strides {ws.stride()} on {ws.device}")
+    return ws.data_ptr(), ws.nbytes
+
+
+# Outputs that a call allocates need no check: (tensor, its address).
+def _new(shape, dtype, device):
+    t = torch.empty(shape, dtype=dtype, device=device)
+    return t, t.data_ptr()
 
 
 def embed_workspace_size(shape: Shape, vocab: int, k: int = 1, backward: bool = False) -> int:
@@ -631,15 +637,18 @@ def embed_forward(shape: Shape, ids, table, scale: float = 1.0, y=None, ws=None)
     """Rows of table [V, d] by ids [rows] or [rows, k] (int32 or int64; below 0: none), times scale (see gbla.h): returns y
     [rows, k d].  shape: glr_shape or make_shape, whose d is the width of a table row."""
     dev, T, k, pi, wide = _embed_ids(shape, ids)
-    io = io_dtype(shape)
+    io, d = io_dtype(shape), shape.d
     if table.dim() != 2:
-        raise ValueError(f"table: want [V, {shape.d}], got {list(table.shape)}")
-    pt = _arg("table", table, (table.shape[0], shape.d), io, dev)
+        raise ValueError(f"table: want [V, {d}], got {list(table.shape)}")
+    V = table.shape[0]
+    pt = _arg("table", table, (V, d), io, dev)
     if y is None:
-        y = torch.empty((T, k * shape.d), dtype=io, device=dev)
-    py = _arg("y", y, (T, k * shape.d), io, dev)
-    pw, nw = _ws(ws, 256, "embed_forward", dev)  # (the error word alone)
-    st = _call(dev, lib().embed_forward, ctypes.byref(shape), pi, wide, k, pt, table.shape[0], scale, py, pw, nw)
+        y, py = _new((T, k * d), io, dev)
+    else:
+        py = _arg("y", y, (T, k * d), io, dev)
+    if ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=dev)  # the error word alone
+    st = _call(dev, lib().embed_forward, ctypes.byref(shape), pi, wide, k, pt, V, scale, py, *_ws(ws, dev))
     if st != GBLA_OK:
         raise GblaError(st, "embed_forward")
     return y
@@ -648,12 +657,15 @@ def embed_forward(shape: Shape, ids, table, scale: float = 1.0, y=None, ws=None)
 def embed_backward(shape: Shape, ids, dy, vocab: int, scale: float = 1.0, dtable=None, ws=None):
     """The table's gradient for <dy, y>: fp32 [vocab, d], rows without a token 0."""
     dev, T, k, pi, wide = _embed_ids(shape, ids)
-    pd = _arg("dy", dy, (T, k * shape.d), io_dtype(shape), dev)
+    d = shape.d
+    pd = _arg("dy", dy, (T, k * d), io_dtype(shape), dev)
     if dtable is None:
-        dtable = torch.empty((vocab, shape.d), dtype=torch.float32, device=dev)
-    pg = _arg("dtable", dtable, (vocab, shape.d), torch.float32, dev)
-    pw, nw = _ws(ws, 0 if ws is not None else embed_workspace_size(shape, vocab, k, True), "embed_backward", dev)
-    st = _call(dev, lib().embed_backward, ctypes.byref(shape), pi, wide, k, pd, vocab, scale, pg, pw, nw)
+        dtable, pg = _new((vocab, d), torch.float32, dev)
+    else:
+        pg = _arg("dtable", dtable, (vocab, d), torch.float32, dev)
+    if ws is None:
+        ws = embed_workspace(shape, vocab, k, True, dev)
+    st = _call(dev, lib().embed_backward, ctypes.byref(shape), pi, wide, k, pd, vocab, scale, pg, *_ws(ws, dev))
     if st != GBLA_OK:
         raise GblaError(st, "embed_backward")
     return dtable
@@ -683,22 +695,25 @@ def layer_norm_forward(shape: Shape, x, w=None, b=None, eps: float = 1e-5, res=N
     where there is a res (False: not wanted; res itself, or x, to update it in place); stats = True allocates what
     layer_norm_backward needs."""
     dev, T, d, io, ld, px = _norm_input(shape, x)
-    full = (T, d)
+    full, f32 = (T, d), torch.float32
     if y is None:
-        y = torch.empty(full, dtype=io, device=dev)
-    if total is None or total is True:
-        total = torch.empty(full, dtype=io, device=dev) if res is not None else None
-    if total is False:
-        total = None
+        y, py = _new(full, io, dev)
+    else:
+        py = _arg("y", y, full, io, dev)
+    if total is True or (total is None and res is not None):
+        total, pt = _new(full, io, dev)
+    else:
+        total = None if total is False else total
+        pt = _arg("total", total, full, io, dev)
     if stats is True:
-        stats = torch.empty((T, 2), dtype=torch.float32, device=dev)
-    if stats is False:
-        stats = None
-    pw, nw = _ws(ws, 256, "layer_norm_forward", dev)  # (the error word alone)
-    st = _call(dev, lib().layer_norm_forward, ctypes.byref(shape), px, ld, None if res is None else _arg("res", res, full, io, dev),
-               None if w is None else _arg("w", w, (d,), io, dev), None if b is None else _arg("b", b, (d,), io, dev), eps,
-               None if total is None else _arg("total", total, full, io, dev), _arg("y", y, full, io, dev),
-               None if stats is None else _arg("stats", stats, (T, 2), torch.float32, dev), pw, nw)
+        stats, ps = _new((T, 2), f32, dev)
+    else:
+        stats = None if stats is False else stats
+        ps = _arg("stats", stats, (T, 2), f32, dev)
+    if ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=dev)  # the error word alone
+    st = _call(dev, lib().layer_norm_forward, ctypes.byref(shape), px, ld, _arg("res", res, full, io, dev), _arg("w", w, (d,), io, dev),
+               _arg("b", b, (d,), io, dev), eps, pt, py, ps, *_ws(ws, dev))
     if st != GBLA_OK:
         raise GblaError(st, "layer_norm_forward")
     return y, total, stats
@@ -709,17 +724,22 @@ def layer_norm_backward(shape: Shape, x, w, stats, dy, ds=None, affine: bool = T
     dx (the gradient of x and of res) and, with affine, dw and db fp32.  out: tensors to fill (dx may be ds)."""
     dev, T, d, io, ld, px = _norm_input(shape, x)
     full, f32 = (T, d), torch.float32
-    g = out
-    if g is None:
-        g = {"dx": torch.empty(full, dtype=io, device=dev)}
+    if out is None:
+        dx, pdx = _new(full, io, dev)
+        g = {"dx": dx}
+        pdw = pdb = None
         if affine:
-            g["dw"], g["db"] = torch.empty(d, dtype=f32, device=dev), torch.empty(d, dtype=f32, device=dev)
-    dw, db = g.get("dw"), g.get("db")
-    pw, nw = _ws(ws, 0 if ws is not None else layer_norm_workspace_size(shape, True), "layer_norm_backward", dev)
-    st = _call(dev, lib().layer_norm_backward, ctypes.byref(shape), px, ld, None if w is None else _arg("w", w, (d,), io, dev),
-               _arg("stats", stats, (T, 2), f32, dev), _arg("dy", dy, full, io, dev), None if ds is None else _arg("ds", ds, full, io, dev),
-               _arg("dx", g["dx"], full, io, dev), None if dw is None else _arg("dw", dw, (d,), f32, dev),
-               None if db is None else _arg("db", db, (d,), f32, dev), pw, nw)
+            g["dw"], pdw = _new(d, f32, dev)
+            g["db"], pdb = _new(d, f32, dev)
+    else:
+        g = out
+        pdx, pdw, pdb = (_arg("dx", g["dx"], full, io, dev), _arg("dw", g.get("dw"), (d,), f32, dev), _arg("db", g.get("db"), (d,), f32, dev))
+    if ws is None:
+        ws = layer_norm_workspace(shape, True, dev)
+    if stats is None:
+        raise ValueError("stats: layer_norm_forward's (stats = True)")
+    st = _call(dev, lib().layer_norm_backward, ctypes.byref(shape), px, ld, _arg("w", w, (d,), io, dev), _arg("stats", stats, (T, 2), f32, dev),
+               _arg("dy", dy, full, io, dev), _arg("ds", ds, full, io, dev), pdx, pdw, pdb, *_ws(ws, dev))
     if st != GBLA_OK:
         raise GblaError(st, "layer_norm_backward")
     return g
@@ -751,14 +771,20 @@ def beam_select(beam: Beam, logits, scores, allowed=None, done=None, out: tuple 
     ld = logits.stride(0) if B * K > 1 and logits.dim() == 2 else V
     pl = _glr_arg("logits", logits, B * K, V, dt, dev, ld)
     if out is None:
-        out = (torch.empty((B, n), dtype=torch.float32, device=dev), torch.empty((B, n), dtype=torch.int32, device=dev),
-               torch.empty((B, n), dtype=torch.int32, device=dev), torch.empty((B, n), dtype=torch.bool, device=dev) if beam.eos >= 0 else None)
-    po = [_arg(name, t, (B, n), kind, dev) for name, t, kind in zip(("scores", "tokens", "parents"), out, (torch.float32, torch.int32, torch.int32))]
-    pw, nw = _ws(ws, 0 if ws is not None else beam_workspace_size(beam), "beam_select", dev)
+        shape, i32 = (B, n), torch.int32
+        s, ps = _new(shape, torch.float32, dev)
+        t, pt = _new(shape, i32, dev)
+        p, pp = _new(shape, i32, dev)
+        e, pe = _new(shape, torch.bool, dev) if beam.eos >= 0 else (None, None)
+        out = (s, t, p, e)
+    else:
+        ps, pt, pp, pe = (_arg(name, t, (B, n), kind, dev) for name, t, kind in
+                          zip(("scores", "tokens", "parents", "done"), out, (torch.float32, torch.int32, torch.int32, torch.bool)))
+    if ws is None:
+        ws = beam_workspace(beam, dev)
     st = _call(dev, lib().beam_select, ctypes.byref(beam), pl, ld, _arg("scores", scores, (B, K), torch.float32, dev),
-               None if allowed is None else _arg("allowed", allowed, (B * K, -(-V // 32)), torch.int32, dev),
-               None if done is None else _arg("done", done, (B, K), torch.bool, dev), *po,
-               None if out[3] is None else _arg("done", out[3], (B, n), torch.bool, dev), pw, nw)
+               _arg("allowed", allowed, (B * K, -(-V // 32)), torch.int32, dev), _arg("done", done, (B, K), torch.bool, dev), ps, pt, pp, pe,
+               *_ws(ws, dev))
     if st != GBLA_OK:
         raise GblaError(st, "beam_select")
     return out
@@ -773,7 +799,7 @@ class BeamReorderPlan:
             raise ValueError(f"{len(D)} tensors to fill for {len(S)} states")
         if out is None and beam.n_out != beam.K:
             raise ValueError(f"in place needs as many beams out ({beam.n_out}) as in ({beam.K})")
-        self.beam, self.B, self.n = beam, beam.B, beam.n_out
+        self.beam, self.B, self.n = Beam.from_buffer_copy(beam), beam.B, beam.n_out  # a copy: the caller's may change
         self.device = _cuda("state", S[0]) if S else torch.device("cuda", torch.cuda.current_device())
         self._keep = (S, D)
         self.states = (BeamState * len(S))()
@@ -794,6 +820,7 @@ class BeamReorderPlan:
             if nxt < at + size:
                 raise ValueError(f"{who} and {name} overlap")
         self.ws = torch.empty(256, dtype=torch.uint8, device=self.device)
+        self._ws, self._beam = self.ws.data_ptr(), ctypes.byref(self.beam)
 
 
 def beam_reorder_plan(beam: Beam, states, out=None) -> BeamReorderPlan:
@@ -804,9 +831,10 @@ def beam_reorder_plan(beam: Beam, states, out=None) -> BeamReorderPlan:
 
 def beam_reorder(plan: BeamReorderPlan, parents) -> None:
     """Row [b, i] of each of the plan's tensors becomes the state's row [b, parents[b, i]] (see gbla.h)."""
-    _check(_call(plan.device, lib().beam_reorder, ctypes.byref(plan.beam), plan.states, len(plan.states),
-                 _arg("parents", parents, (plan.B, plan.n), torch.int32, plan.device), plan.ws.data_ptr(), plan.ws.numel()),
-           "beam_reorder")
+    st = _call(plan.device, lib().beam_reorder, plan._beam, plan.states, len(plan.states),
+               _arg("parents", parents, (plan.B, plan.n), torch.int32, plan.device), plan._ws, 256)
+    if st != GBLA_OK:
+        raise GblaError(st, "beam_reorder")
 
 
 def bla_core_forward_noalloc(shape: Shape, q, k, v, g, o, den=None, state=None) -> int:
