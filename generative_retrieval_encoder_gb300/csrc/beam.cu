@@ -138,8 +138,41 @@ __device__ __forceinline__ uint4 masked(uint4 w, uint32_t ok) {
   return make_uint4(pick(w.x, 0), pick(w.y, 1), pick(w.z, 2), pick(w.w, 3));
 }
 
-// A warp takes kU pieces a lane of one row.  Bound by instructions, some 16 a value (a plain exponential takes 6).
-template <typename T>
+// The largest of each run of 2^lg lanes' pieces: v[u] is the lane's of piece u, first the group of the warp's first run, stored at
+// out[u per + lane >> lg] below `end`.  From 8 lanes on the pieces are dealt out to the lanes while they are compared: 7 exchanges
+// and those of what is left of lg, in place of 8 lg.
+__device__ __forceinline__ void store_runs(float (&v)[kU], int lg, int per, float* out, int end) {
+  static_assert(kU == 8, "three halvings");
+  const int lane = threadIdx.x & 31;
+  if (lg < 3) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      for (int o = 1; o < 1 << lg; o <<= 1) v[u] = fmaxf(v[u], __shfl_xor_sync(FULL, v[u], o));
+      const int g = u * per + (lane >> lg);
+      if ((lane & ((1 << lg) - 1)) == 0 && g < end) out[g] = v[u];
+    }
+    return;
+  }
+  int o = 1 << (lg - 1), u = 0;
+#pragma unroll
+  for (int h = kU / 2; h; h >>= 1, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float other = __shfl_xor_sync(FULL, upper ? v[i] : v[i + h], o);
+      v[i] = fmaxf(upper ? v[i + h] : v[i], other);
+    }
+    u += upper ? h : 0;
+  }
+  const int mine = o ? 2 * o : 1;  // lanes that now hold the same
+  for (; o; o >>= 1) v[0] = fmaxf(v[0], __shfl_xor_sync(FULL, v[0], o));
+  const int g = u * per + (lane >> lg);
+  if ((lane & (mine - 1)) == 0 && g < end) out[g] = v[0];
+}
+
+enum BeamMask { MASK_NONE, MASK_CANDIDATES, MASK_SUM };  // no mask; of the candidates alone; of the sum, too
+// A warp takes kU pieces a lane of one row.  Bound by instructions, some 20 a value (a plain exponential takes 6).
+template <typename T, BeamMask MASK>
 __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
   pdl_enter();
   constexpr int E = 16 / sizeof(T);
@@ -155,53 +188,47 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
   const int tile = (int)(task - row * a.tasks);
   if (row >= (int64_t)a.B * a.K || (a.done && a.done[row])) return;
   const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-  const int t0 = tile * (kU * 32 * E) + lane * E - row_offset<T>(a, row);  // the token of the lane's first value
-  const uint32_t* mask = a.allowed ? a.allowed + row * a.words : nullptr;
+  const int first = tile * (kU * 32 * E) - row_offset<T>(a, row), t0 = first + lane * E;  // the tokens of the warp's, the lane's first value
+  const uint32_t* mask = MASK == MASK_NONE ? nullptr : a.allowed + row * a.words;
   constexpr uint32_t LOWEST = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -infinity
   uint4 w[kU];
+  if (first >= 0 && first + kU * 32 * E <= a.V) {
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const int t = t0 + u * 32 * E;
-    w[u] = make_uint4(LOWEST, LOWEST, LOWEST, LOWEST);
-    if (t >= 0 && t + E <= a.V) {
-      w[u] = __ldcs(reinterpret_cast<const uint4*>(x + t));
-    } else if (t > -E && t < a.V) {  // the row's edges, value by value
-      uint32_t q[4] = {LOWEST, LOWEST, LOWEST, LOWEST};
+    for (int u = 0; u < kU; ++u) w[u] = __ldcs(reinterpret_cast<const uint4*>(x + t0) + u * 32);
+  } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (t + j >= 0 && t + j < a.V) {
-          if (sizeof(T) == 2) {
-            const uint32_t v = reinterpret_cast<const uint16_t*>(x)[t + j];
-            q[j / 2] = j & 1 ? (q[j / 2] & 0xffffu) | v << 16 : (q[j / 2] & 0xffff0000u) | v;
-          } else {
-            q[j & 3] = reinterpret_cast<const uint32_t*>(x)[t + j];
+    for (int u = 0; u < kU; ++u) {
+      const int t = t0 + u * 32 * E;
+      w[u] = make_uint4(LOWEST, LOWEST, LOWEST, LOWEST);
+      if (t >= 0 && t + E <= a.V) {
+        w[u] = __ldcs(reinterpret_cast<const uint4*>(x + t));
+      } else if (t > -E && t < a.V) {  // the row's edges, value by value
+        uint32_t q[4] = {LOWEST, LOWEST, LOWEST, LOWEST};
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (t + j >= 0 && t + j < a.V) {
+            if (sizeof(T) == 2) {
+              const uint32_t v = reinterpret_cast<const uint16_t*>(x)[t + j];
+              q[j / 2] = j & 1 ? (q[j / 2] & 0xffffu) | v << 16 : (q[j / 2] & 0xffff0000u) | v;
+            } else {
+              q[j & 3] = reinterpret_cast<const uint32_t*>(x)[t + j];
+            }
           }
-        }
-      w[u] = make_uint4(q[0], q[1], q[2], q[3]);
+        w[u] = make_uint4(q[0], q[1], q[2], q[3]);
+      }
     }
   }
   // the largest value of each run, and of all that are summed; w: what is summed
-  float top = -kInf;
-  const int per = 32 >> a.lg;  // runs of the warp's 32 pieces
+  float top = -kInf, run[kU];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
-    float run = piece_max<T>(w[u]);
-    if (mask) {
-      const uint4 m = masked<T>(w[u], mask_bits<E>(mask, a.words, t0 + u * 32 * E));
-      top = fmaxf(top, run);
-      run = piece_max<T>(m);
-      if (a.over_allowed) w[u] = m;
-    }
-    top = fmaxf(top, run);
-    for (int o = 1; o < 1 << a.lg; o <<= 1) run = fmaxf(run, __shfl_xor_sync(FULL, run, o));
-    const int g = (tile * kU + u) * per + (lane >> a.lg);
-    if ((lane & ((1 << a.lg) - 1)) == 0 && g < a.runs) a.top[row * a.runs + g] = run;
+    if (MASK == MASK_SUM) w[u] = masked<T>(w[u], mask_bits<E>(mask, a.words, t0 + u * 32 * E));
+    run[u] = piece_max<T>(w[u]);
+    top = fmaxf(top, run[u]);
+    if (MASK == MASK_CANDIDATES) run[u] = piece_max<T>(masked<T>(w[u], mask_bits<E>(mask, a.words, t0 + u * 32 * E)));
   }
-  if (mask && a.over_allowed) {
-    top = -kInf;
-#pragma unroll
-    for (int u = 0; u < kU; ++u) top = fmaxf(top, piece_max<T>(w[u]));
-  }
+  const int per = 32 >> a.lg;  // runs of the warp's 32 pieces
+  store_runs(run, a.lg, per, a.top + row * a.runs + (int64_t)tile * kU * per, a.runs - tile * kU * per);
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
   BeamPart part;
   if (fabsf(top) <= 4096.f) {
@@ -253,7 +280,7 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
         float v = -kInf;
         const int t = t0 + u * 32 * E + j;
         if (t >= 0 && t < a.V) v = to_f(x[t]);
-        if (a.over_allowed && mask && !(t >= 0 && t < a.V && mask[t >> 5] >> (t & 31) & 1)) v = -kInf;
+        if (MASK == MASK_SUM && !(t >= 0 && t < a.V && mask[t >> 5] >> (t & 31) & 1)) v = -kInf;
         s += exp((double)v - (double)top);
       }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
@@ -753,8 +780,10 @@ __global__ void __launch_bounds__(256) k_beam_move(const __grid_constant__ BeamT
 
 cudaError_t launch_beam_rows(const BeamArgs& a, bool f32, cudaStream_t st) {
   const int64_t tasks = (int64_t)a.B * a.K * a.tasks;
-  const dim3 grid((unsigned)((tasks + 7) / 8));
-  return f32 ? launch_pdl(k_beam_rows<float>, grid, dim3(256), 0, st, a) : launch_pdl(k_beam_rows<bf16>, grid, dim3(256), 0, st, a);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)((tasks + 7) / 8)), dim3(256), 0, st, a); };
+  if (!a.allowed) return f32 ? go(k_beam_rows<float, MASK_NONE>) : go(k_beam_rows<bf16, MASK_NONE>);
+  if (!a.over_allowed) return f32 ? go(k_beam_rows<float, MASK_CANDIDATES>) : go(k_beam_rows<bf16, MASK_CANDIDATES>);
+  return f32 ? go(k_beam_rows<float, MASK_SUM>) : go(k_beam_rows<bf16, MASK_SUM>);
 }
 cudaError_t launch_beam_pick(const BeamArgs& a, bool f32, cudaStream_t st) {
   auto go = [&](auto kernel) {
