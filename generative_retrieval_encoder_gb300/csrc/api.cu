@@ -1380,12 +1380,14 @@ gbla_status embed_backward(const gbla_shape* shape, const void* ids, int wide_id
   s.longs = at<int2>(ws, l.longs);
   if (s.tiles > 1) GBLA_CHECK(launch_zero(ws, l.zero_bytes, c.st), "clear");
   const int groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
+  const int launches = s.tiles == 1 ? 1 : 2 * l.passes;  // each clears a share of the gradient
   for (int i = 0; i < (s.tiles == 1 ? 1 : l.passes); ++i) {
     s.key_in = s.keys[(i + 1) & 1]; s.slot_in = s.slots[(i + 1) & 1];
     s.key_out = s.keys[i & 1]; s.slot_out = s.slots[i & 1];
     s.sums = at<int>(ws, l.sums) + ((size_t)i * groups << kEmbedDigit);
-    if (s.tiles > 1) GBLA_CHECK(launch_embed_count(a, s, l.bits, i * l.bits, c.st), "embed count");
-    GBLA_CHECK(launch_embed_place(a, s, l.bits, i * l.bits, c.st), "embed place");
+    if (s.tiles > 1) GBLA_CHECK(launch_embed_count(a, s, embed_fill(a, 2 * i, launches), l.bits, i * l.bits, c.st), "embed count");
+    const EmbedFill f = s.tiles > 1 ? embed_fill(a, 2 * i + 1, launches) : embed_fill(a, 0, 1);
+    GBLA_CHECK(launch_embed_place(a, s, f, l.bits, i * l.bits, c.st), "embed place");
   }
   if (s.tiles == 1) {  // the one CTA went through every pass
     s.key_out = s.keys[(l.passes - 1) & 1];

@@ -116,9 +116,29 @@ __device__ __forceinline__ int key_at(const EmbedArgs& a, const EmbedSort& s, in
   return id < 0 ? a.V : id;
 }
 
+// The table's gradient is cleared meanwhile: the sort's CTAs are few and wait for latencies, so each of its launches has more CTAs that
+// clear a share of it, kFill values each (4 hashes into a million rows of 128: 512 MB, 122 us against 95; the rows that no id has need not
+// be found later).
+constexpr int kFill = 16384;
+__device__ __forceinline__ bool fill(const EmbedFill& f, int tiles) {
+  if ((int)blockIdx.x < tiles) return false;
+  const int64_t lo = f.lo + ((int64_t)blockIdx.x - tiles) * kFill, hi = min(f.hi, lo + kFill);
+  if (f.wide) {
+    for (int64_t i = lo + threadIdx.x * 4; i < hi; i += kThreads * 4) {
+      if (i + 4 <= hi) *reinterpret_cast<float4*>(f.p + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+      else
+        for (int64_t j = i; j < hi; ++j) f.p[j] = 0.f;
+    }
+  } else {
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) f.p[i] = 0.f;
+  }
+  return true;
+}
+
 // Each tile's keys by digit, and the sums of kEmbedTiles tiles.
-__global__ void __launch_bounds__(kThreads) k_embed_count(const EmbedArgs a, const EmbedSort s, int bins, int shift, bool first) {
+__global__ void __launch_bounds__(kThreads) k_embed_count(const EmbedArgs a, const EmbedSort s, const EmbedFill f, int bins, int shift, bool first) {
   pdl_enter();
+  if (fill(f, s.tiles)) return;
   __shared__ int count[kMaxBins];
   for (int i = threadIdx.x; i < bins; i += kThreads) count[i] = 0;
   __syncthreads();
@@ -155,8 +175,9 @@ __device__ __forceinline__ int sum_before(int v, int* red) {
 // A tile's keys and slots to their places by the digit at `shift`.  ALL: a single tile, every pass in this one CTA, which also
 // counts.
 template <bool ALL>
-__global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, EmbedSort s, int bits, int shift, bool first) {
+__global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, EmbedSort s, const EmbedFill f, int bits, int shift, bool first) {
   pdl_enter();
+  if (fill(f, s.tiles)) return;
   __shared__ uint16_t warp_count[kThreads / 32][kMaxBins];
   __shared__ int base[kMaxBins];
   __shared__ int red[kThreads / 32];
@@ -262,70 +283,11 @@ struct Sum {
   }
 };
 
-// The rows of the ids without a slot, kThreads of them a CTA: which of them occur is read from the sorted keys between the first
-// and the last of them.
-__device__ void clear_rows(const EmbedArgs& a, const int* key, int64_t v0) {
-  __shared__ int64_t bound[2];
-  __shared__ unsigned there[kThreads / 32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x < kThreads / 32) there[threadIdx.x] = 0;
-  if (warp < 2) {  // the first place of a key >= v, 32 places looked at at a time
-    const int64_t v = min(v0 + warp * kThreads, (int64_t)a.V);
-    int64_t lo = 0, hi = a.n;  // it is in [lo, hi]
-    while (lo < hi) {
-      const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
-      const unsigned m = __ballot_sync(FULL, i < hi && key[i] < v);  // a prefix of the lanes
-      const int k = __popc(m);
-      const int64_t l = lo;
-      lo = k ? l + (k - 1) * step + 1 : l;
-      hi = min(hi, l + k * step);
-    }
-    if (lane == 0) bound[warp] = lo;
-  }
-  __syncthreads();
-  // (a frequent id has many places: four keys a load, four loads on their way)
-  for (int64_t i0 = (bound[0] & ~3) + threadIdx.x * 4; i0 < bound[1]; i0 += kThreads * 16) {
-    int4 k[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + u * kThreads * 4;
-      k[u] = i < bound[1] ? *reinterpret_cast<const int4*>(key + i) : make_int4(-1, -1, -1, -1);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + u * kThreads * 4;
-      const int q[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = q[j] - (int)v0;
-        if (i + j < bound[0] || i + j >= bound[1]) continue;
-        if (!(reinterpret_cast<volatile unsigned*>(there)[r >> 5] >> (r & 31) & 1)) atomicOr(&there[r >> 5], 1u << (r & 31));
-      }
-    }
-  }
-  __syncthreads();
-  const int64_t w0 = v0 + warp * 32;
-  const bool wide = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0;
-  for (unsigned m = ~there[warp]; m; m &= m - 1) {
-    const int64_t v = w0 + __ffs(m) - 1;
-    if (v >= a.V) break;
-    float* out = a.dtable + v * a.d;
-    if (wide)
-      for (int c = lane * 4; c < a.d; c += 128) *reinterpret_cast<float4*>(out + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-    else
-      for (int c = lane; c < a.d; c += 32) out[c] = 0.f;
-  }
-}
-
-// Groups of G threads, G E columns each.  The first `chunk_ctas` CTAs take chunks, the others the rows of ids without a slot.
+// Groups of G threads, G E columns of a chunk each.
 template <typename T, int G, bool WIDE>
-__global__ void __launch_bounds__(kThreads, WIDE ? 4 : 3) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
+__global__ void __launch_bounds__(kThreads, WIDE ? 4 : 3) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks) {
   pdl_enter();
   constexpr int E = 16 / sizeof(T), U = 32 / E, C = kEmbedCap;
-  if ((int)blockIdx.x >= chunk_ctas) {
-    clear_rows(a, s.key_out, ((int64_t)blockIdx.x - chunk_ctas) * kThreads);
-    return;
-  }
   // the keys from C places before the chunk to C behind it, and the slots from its first place on
   __shared__ __align__(16) int keys[kThreads / G][3 * C];
   __shared__ __align__(16) int slots[kThreads / G][2 * C];
@@ -537,11 +499,11 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, cons
 template <typename T, bool WIDE>
 cudaError_t rows(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st) {
   constexpr int E = 16 / sizeof(T);
-  const int64_t chunks = (a.n + kEmbedCap - 1) / kEmbedCap, empty = ((int64_t)a.V + kThreads - 1) / kThreads;
+  const int64_t chunks = (a.n + kEmbedCap - 1) / kEmbedCap;
   auto go = [&](auto kernel, int G) {
     const int blocks = (a.d + G * E - 1) / (G * E), per = kThreads / G;
     const int64_t ctas = (chunks * blocks + per - 1) / per;
-    return launch_pdl(kernel, dim3((unsigned)(ctas + empty)), dim3(kThreads), 0, st, a, s, blocks, (int)ctas);
+    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), 0, st, a, s, blocks);
   };
   const int v = (a.d + E - 1) / E;
   return v <= 4 ? go(k_embed_rows<T, 4, WIDE>, 4) : v <= 8 ? go(k_embed_rows<T, 8, WIDE>, 8)
@@ -579,12 +541,21 @@ cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st) {
   return wide ? go(k_embed_fwd<bf16, true>) : go(k_embed_fwd<bf16, false>);
 }
 
-cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st) {
-  return launch_pdl(k_embed_count, dim3((unsigned)s.tiles), dim3(kThreads), 0, st, a, s, 1 << bits, shift, shift == 0);
+// Share `i` of `n` of the gradient's values, from a multiple of 4 on.
+EmbedFill embed_fill(const EmbedArgs& a, int i, int n) {
+  const int64_t all = (int64_t)a.V * a.d;
+  auto cut = [&](int k) { return k == n ? all : all / n * k / 4 * 4; };
+  return EmbedFill{a.dtable, cut(i), cut(i + 1), reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0};
 }
-cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st) {
-  if (s.tiles == 1) return launch_pdl(k_embed_place<true>, dim3(1), dim3(kThreads), 0, st, a, s, bits, 0, true);
-  return launch_pdl(k_embed_place<false>, dim3((unsigned)s.tiles), dim3(kThreads), 0, st, a, s, bits, shift, shift == 0);
+unsigned fill_ctas(const EmbedFill& f) { return (unsigned)((f.hi - f.lo + kFill - 1) / kFill); }
+
+cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st) {
+  return launch_pdl(k_embed_count, dim3((unsigned)s.tiles + fill_ctas(f)), dim3(kThreads), 0, st, a, s, f, 1 << bits, shift, shift == 0);
+}
+cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st) {
+  const dim3 grid((unsigned)s.tiles + fill_ctas(f));
+  if (s.tiles == 1) return launch_pdl(k_embed_place<true>, grid, dim3(kThreads), 0, st, a, s, f, bits, 0, true);
+  return launch_pdl(k_embed_place<false>, grid, dim3(kThreads), 0, st, a, s, f, bits, shift, shift == 0);
 }
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st) {
   const size_t es = f32 ? 4 : 2;

@@ -358,9 +358,12 @@ struct EmbedSort {
 };
 bool embed_fwd_clears(const EmbedArgs& a);  // whether launch_embed_fwd clears the error word itself
 cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st);
+// Values [lo, hi) of the gradient that a launch of the sort also clears; wide: p is aligned to 16 bytes.
+struct EmbedFill { float* p; int64_t lo, hi; bool wide; };
+EmbedFill embed_fill(const EmbedArgs& a, int i, int n);  // share i of n
 // One pass of the sort, by the digit of `bits` bits at `shift`; a single tile's launch_embed_place is the whole sort, and clears.
-cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st);
-cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, int bits, int shift, cudaStream_t st);
+cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st);
+cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st);
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st);
 cudaError_t launch_embed_join(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st);
 // Clears a multiple of 16 bytes (a launch that follows its predecessor like the kernels do; a memset waits longer).
