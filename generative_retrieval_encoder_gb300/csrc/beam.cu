@@ -342,7 +342,8 @@ struct PickSmem {
   uint64_t kept[kBeamMost];
   uint32_t at[kBeamItems];
   uint32_t kept_at[kBeamMost];
-  uint32_t run[kBeamMost];        // the kept runs
+  uint32_t run[kBeamMost];        // the kept runs: row,
+  int token[kBeamMost];           // first token
   float2 base[kBeamMost];         // rows: the score of a logit at ref
   float ref[kBeamMost];           // rows: what logits are taken relative to; kInf: ended
   int hist[kBins];
@@ -592,7 +593,11 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
     have = select_best(s, have + more, a.n, seen, low);
     i0 += more;
   }
-  if (tid < have) s.run[tid] = s.at[tid];
+  if (tid < have) {
+    const uint32_t i = s.at[tid], b = i / runs;
+    s.run[tid] = b;
+    s.token[tid] = (int)((i - b * runs) << a.lg) * E - row_offset<T>(a, row0 + b);
+  }
   if (tid == 0) s.n = 0;
   __syncthreads();
   // their tokens, a piece a thread: those not below `low`, which is n runs' largest at least: few more than n, unless many are alike
@@ -608,11 +613,11 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
       const int i = i0 + u * kPick;
       ok[u] = 0;
       if (i >= pieces) continue;
-      const uint32_t r = s.run[i >> a.lg], b = r / runs;
+      const uint32_t b = s.run[i >> a.lg];
       row[u] = b;
       const int64_t at = row0 + b;
       const int j = i & ((1 << a.lg) - 1);
-      t0[u] = (int)(((r - b * runs) << a.lg) + j) * E - row_offset<T>(a, at);
+      t0[u] = s.token[i >> a.lg] + j * E;
       if (s.ref[b] == kInf) {
         ok[u] = j == 0 ? 1 : 0;
         continue;
@@ -694,20 +699,34 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
       }
     s.key[tid] = key;
     s.at[tid] = at;
+    s.kept_at[tid] = (uint32_t)(key >> 32);
   }
   __syncthreads();
   if (tid < warps * 32 && key) {
+    const uint32_t hi = (uint32_t)(key >> 32);
+    const uint32_t* upper = s.kept_at;
     rank = lane;
-    for (int w = 0; w < warps; ++w) {
-      if (w == tid >> 5) continue;
-      int pos = w * 32;
+    for (int w0 = 0; w0 < warps; w0 += 4) {  // four warps' at a time, by the keys' upper words
+      int pos[4];
 #pragma unroll
-      for (int st = 16; st; st >>= 1) {
-        const uint64_t k = s.key[pos + st - 1];
-        if (k > key || (k == key && s.at[pos + st - 1] < at)) pos += st;
+      for (int u = 0; u < 4; ++u) pos[u] = min(w0 + u, warps - 1) * 32;
+#pragma unroll
+      for (int st = 16; st; st >>= 1)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (upper[pos[u] + st - 1] > hi) pos[u] += st;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int w = w0 + u, end = w * 32 + 32;
+        if (w >= warps || w == tid >> 5) continue;
+        if (upper[pos[u]] > hi) ++pos[u];
+        while (pos[u] < end && upper[pos[u]] == hi) {  // alike so far
+          const uint64_t k = s.key[pos[u]];
+          if (k < key || (k == key && s.at[pos[u]] > at)) break;
+          ++pos[u];
+        }
+        rank += pos[u] - w * 32;
       }
-      const uint64_t k = s.key[pos];
-      rank += pos - w * 32 + (k > key || (k == key && s.at[pos] < at));
     }
   }
   const int have_n = min(cnt, a.n);
