@@ -656,7 +656,8 @@ gbla_status embed_plan(const gbla_shape* s, int64_t vocab, int k, RowPlan& p) {
   const gbla_status r = make_row_plan(s, p);
   if (r != GBLA_OK) return r;
   if (vocab < 1 || k < 1) return GBLA_ERR_INVALID_ARG;
-  if (vocab > (1LL << 30) || vocab * p.d > (1LL << 38) || k > (1 << 20) || p.rows * k > (1LL << 30)) return GBLA_ERR_UNSUPPORTED;
+  if (vocab > (1LL << 30) || vocab * p.d > (1LL << 38) || k > (1 << 20) || p.rows * k > (1LL << 30) || p.rows * k * p.d > (1LL << 40))
+    return GBLA_ERR_UNSUPPORTED;
   return GBLA_OK;
 }
 // The workspace: the error word; of the backward also the sort's counts, two sets of keys and slots, partial sums and whose they are.
@@ -713,7 +714,7 @@ gbla_status beam_ok(const gbla_beam* g) {
   if (!g || g->B < 1 || g->K < 1 || g->V < 1 || g->n_out < 1) return GBLA_ERR_INVALID_ARG;
   if (g->io_dtype != GBLA_F32 && g->io_dtype != GBLA_BF16) return GBLA_ERR_INVALID_ARG;
   if (g->eos < -1 || g->eos >= g->V || (g->over_allowed != 0 && g->over_allowed != 1)) return GBLA_ERR_INVALID_ARG;
-  if (g->K > kBeamMost || g->n_out > kBeamMost || (int64_t)g->K * g->V > (1LL << 32)) return GBLA_ERR_UNSUPPORTED;
+  if (g->K > kBeamMost || g->n_out > kBeamMost || g->V > (1 << 30) || (int64_t)g->K * g->V > (1LL << 32)) return GBLA_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)g->B * g->K;
   if (rows > (1LL << 30) || rows * (g->V / 1024 + 1) > (1LL << 31) || (int64_t)g->B * g->n_out > (1LL << 30)) return GBLA_ERR_UNSUPPORTED;
   return GBLA_OK;

@@ -361,7 +361,7 @@ gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors,
  *           [0, L]: they count as no token and as an empty sequence
  *   table   (io) [vocab, d];  y (io) [rows, k d], rounded once
  * d, k and vocab are free: rows k <= 2^30, vocab <= 2^30, d <= 2^20,
- * vocab d <= 2^38.  Pointers are aligned to their element (rows of a multiple of
+ * vocab d <= 2^38, rows k d <= 2^40.  Pointers are aligned to their element (rows of a multiple of
  * 16 bytes in 16-byte aligned tensors are read in wider pieces).  The shape's H,
  * d_h, gate and rms_eps are ignored.  Workspace: embed_workspace_size(.., 0).
  */
@@ -460,7 +460,7 @@ typedef struct {
  * Exponentials are summed, and scores compared, in two fp32 words: which of two
  * candidates is first is decided to 2^-26 (to 2^-30 on the mean), and a score is
  * rounded once.
- * K V <= 2^32, B K V / 1024 <= 2^31.  Outputs do not overlap inputs.  Workspace:
+ * V <= 2^30, K V <= 2^32, B K V / 1024 <= 2^31.  Outputs do not overlap inputs.  Workspace:
  * beam_workspace_size().
  */
 gbla_status beam_select(const gbla_beam* beam, const void* logits, int64_t ld,

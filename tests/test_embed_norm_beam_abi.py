@@ -40,6 +40,7 @@ def test_embed_host_errors_launch_nothing(L, bwd, dtype):
     for bad in (dict(ids=None), dict(ids=ODD), dict(t=None), dict(t=ODD), dict(out=None), dict(out=ODD), dict(wide=2), dict(wide=-1),
                 dict(k=0), dict(V=0), dict(V=-1), dict(wide=1, ids=ctypes.c_void_p((1 << 20) + 4))):
         assert _embed(L, s, bwd, **bad) == I, bad
+    assert _embed(L, gbla.glr_shape(1 << 10, 1 << 18, 8192, dtype=dtype), bwd) == U  # rows k d
     for big in (dict(V=(1 << 30) + 1), dict(k=1 << 24), dict(k=(1 << 20) + 1)):
         assert _embed(L, s, bwd, **big) == U, big
     assert _embed(L, gbla.glr_shape(2, 100, 1 << 20, dtype=dtype), bwd, V=1 << 20) == U
@@ -107,7 +108,7 @@ def _wrong_beams():
     g = gbla.beam_shape(**ok)
     g.over_allowed = 2
     yield g, I
-    for bad in (dict(K=1025), dict(n_out=1025), dict(K=1024, V=(1 << 22) + 1), dict(B=1 << 30)):
+    for bad in (dict(K=1025), dict(n_out=1025), dict(K=1024, V=(1 << 22) + 1), dict(K=1, V=(1 << 30) + 1), dict(B=1 << 30)):
         yield gbla.beam_shape(**{**ok, **bad}), U
 
 

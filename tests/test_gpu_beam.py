@@ -293,6 +293,15 @@ def test_reorder_moves_rows(dtype, width, offset, B, K):
     assert torch.equal(raw[:offset], keep[:offset]) and torch.equal(raw[offset + src.numel():], keep[offset + src.numel():])
 
 
+def test_reorder_to_more_beams_than_there_were():
+    B, K, n = 5, 1, 700
+    src = torch.randn(B, 96, generator=gen(1)).cuda()
+    dst = torch.empty(B * n, 96, device="cuda")
+    plan = gbla.beam_reorder_plan(gbla.beam_shape(B, K, 10, n), [src], [dst])
+    gbla.beam_reorder(plan, torch.zeros(B, n, dtype=torch.int32, device="cuda"))
+    assert torch.equal(dst, src.repeat_interleave(n, 0)) and gbla.gbla_check_device_status(plan.ws) == gbla.GBLA_OK
+
+
 def test_reorder_many_tensors_and_bad_parents():
     B, K = 3, 4
     beam = gbla.beam_shape(B, K, 10)

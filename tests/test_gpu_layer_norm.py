@@ -236,6 +236,34 @@ def test_layer_norm_bad_lengths_are_reported():
             assert gbla.gbla_check_device_status(ws) == gbla.GBLA_OK
 
 
+def test_layer_norm_of_many_slots():
+    """More slots than one CTA checks: each reports its own length."""
+    B, L, d = 9000, 2, 40
+    ln = torch.randint(0, L + 1, (B,), generator=gen(4), dtype=torch.int32)
+    for bad in (False, True):
+        lens = ln.clone()
+        if bad:
+            lens[8999] = 3
+        shape = gbla.glr_shape(B, L, d, dtype="f32", seq_lens=lens.cuda())
+        x, dy = torch.randn(B * L, d, generator=gen(5)).cuda(), torch.randn(B * L, d, generator=gen(6)).cuda()
+        ws = gbla.layer_norm_workspace(shape, True)
+        ws.fill_(0xA5)
+        y, _, st = gbla.layer_norm_forward(shape, x, stats=True, ws=ws)
+        want = gbla.GBLA_ERR_DEVICE_CHECK if bad else gbla.GBLA_OK
+        assert gbla.gbla_check_device_status(ws) == want
+        g = gbla.layer_norm_backward(shape, x, None, st, dy, ws=ws)
+        assert gbla.gbla_check_device_status(ws) == want
+        valid = (torch.arange(L)[None] < torch.where(lens > L, 0, lens)[:, None]).view(-1)
+        dense = gbla.glr_shape(1, B * L, d, dtype="f32")
+        y2, _, st2 = gbla.layer_norm_forward(dense, x, stats=True)
+        dy2 = torch.where(valid.cuda()[:, None], dy, 0.0)
+        g2 = gbla.layer_norm_backward(dense, x, None, st2, dy2)
+        assert torch.equal(y[valid], y2[valid]) and (y[~valid] == 0).all()
+        assert torch.equal(g["dx"][valid], g2["dx"][valid]) and (g["dx"][~valid] == 0).all()
+        # a row that counts for nothing adds exact zeros
+        assert torch.equal(g["dw"], g2["dw"]) and torch.equal(g["db"], g2["db"])
+
+
 def test_layer_norm_gradients_by_differences():
     T, d = 6, 20
     shape = gbla.glr_shape(1, T, d, dtype="f32")
