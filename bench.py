@@ -19,6 +19,7 @@ from __future__ import annotations
 import argparse
 import hashlib
 import json
+import math
 import os
 import statistics
 import subprocess
@@ -374,7 +375,10 @@ def core_lines(wl, dev, timed, flush, peaks, steps: int = 10):
     8 d_h + 8: q, k, v, g, lambda in, o out); the SA blocks' softmax
     attention (sa_core_forward) with its tensor rate; and the gated linear
     recurrence on the same tokens and channels (per value: forward 8 bytes, x,
-    r, i in, y out; backward 14, x, r, i, dy in, dx, dr, di out)."""
+    r, i in, y out; backward 14, x, r, i, dy in, dx, dr, di out); the token
+    embedding (32768 rows) and the layer norm with its residual on the same
+    tokens, and a step of beam search over 64 groups of 16 beams and 32768
+    tokens (each input read and each output written once)."""
     import torch
     from generative_retrieval_encoder_gb300 import gbla
     B, L, H, dh = wl.B, wl.L, wl.H, wl.dh
@@ -429,7 +433,34 @@ def core_lines(wl, dev, timed, flush, peaks, steps: int = 10):
         out[name] = {"ms": round(ms, 4), "tokens_per_s": T / (ms * 1e-3), "algorithmic_bytes": T * d * per,
                      "achieved_GBps": round(T * d * per / (ms * 1e-3) / 1e9, 1),
                      "frac": round(T * d * per / (ms * 1e-3) / 1e9 / peaks["hbm_gbs"], 3)}
-    del q, k, v, d_o, g, lam, o, ws_f, ws_b, ws_d, ws_s, saved, dout
+    # what stands around the layers: token embedding over 32768 rows, layer norm with its residual, and a step of beam search
+    V, es = 32768, 2
+    ids = (torch.exp(torch.rand(T, generator=r) * math.log(V + 1)).long() - 1).clamp(0, V - 1).to(torch.int32).to(dev)  # a power law
+    table = torch.randn(V, d, generator=r).to(torch.bfloat16).to(dev)
+    dtable = torch.empty(V, d, dtype=torch.float32, device=dev)
+    ws_e = gbla.embed_workspace(rec, V, 1, True, dev)
+    w, ws_n = torch.ones(d, dtype=torch.bfloat16, device=dev), gbla.layer_norm_workspace(rec, True, dev)
+    total, st = torch.empty_like(q), torch.empty(T, 2, dtype=torch.float32, device=dev)
+    gbla.layer_norm_forward(rec, q, w, w, res=k, total=total, y=o, stats=st, ws=ws_n)
+    grads = {"dx": torch.empty_like(q), "dw": torch.empty(d, device=dev), "db": torch.empty(d, device=dev)}
+    beam = gbla.beam_shape(64, 16, V)
+    logits = (2 * torch.randn(64 * 16, V, generator=r)).to(torch.bfloat16).to(dev)
+    scores = torch.zeros(64, 16, device=dev)
+    picked = gbla.beam_select(beam, logits, scores)
+    ws_p = gbla.beam_workspace(beam, dev)
+    for name, fn, by in (("embed_forward", lambda: gbla.embed_forward(rec, ids, table, y=o, ws=ws_e), T * (4 + d * es) + V * d * es),
+                         ("embed_backward", lambda: gbla.embed_backward(rec, ids, d_o, V, dtable=dtable, ws=ws_e), T * (4 + d * es) + V * d * 4),
+                         ("layer_norm_forward", lambda: gbla.layer_norm_forward(rec, q, w, w, res=k, total=total, y=o, stats=st, ws=ws_n),
+                          4 * T * d * es + 8 * T),
+                         ("layer_norm_backward", lambda: gbla.layer_norm_backward(rec, total, w, st, d_o, ds=v, ws=ws_n, out=grads),
+                          4 * T * d * es + 8 * T),
+                         ("beam_select", lambda: gbla.beam_select(beam, logits, scores, out=picked, ws=ws_p), logits.numel() * es)):
+        for _ in range(3):
+            fn()
+        ms = timed(fn, steps)
+        out[name] = {"ms": round(ms, 4), "algorithmic_bytes": by, "achieved_GBps": round(by / (ms * 1e-3) / 1e9, 1),
+                     "frac": round(by / (ms * 1e-3) / 1e9 / peaks["hbm_gbs"], 3)}
+    del q, k, v, d_o, g, lam, o, ws_f, ws_b, ws_d, ws_s, saved, dout, ids, table, dtable, ws_e, w, ws_n, total, st, grads, logits, picked, ws_p
     torch.cuda.empty_cache()
     return out
 
