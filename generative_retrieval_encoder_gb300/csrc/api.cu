@@ -660,13 +660,14 @@ gbla_status embed_plan(const gbla_shape* s, int64_t vocab, int k, RowPlan& p) {
     return GBLA_ERR_UNSUPPORTED;
   return GBLA_OK;
 }
+size_t embed_tiles(size_t n) { return n <= kEmbedOne ? 1 : (n + kEmbedTile - 1) / kEmbedTile; }
 // The workspace: the error word; of the backward also the sort's counts, two sets of keys and slots, partial sums and whose they are.
 EmbedLayout embed_layout(const RowPlan& p, int64_t vocab, int k, bool backward) {
   EmbedLayout l{};
   Cursor c;
   c.take(16);
   if (backward) {
-    const size_t n = (size_t)p.rows * k, tiles = (n + kEmbedTile - 1) / kEmbedTile;
+    const size_t n = (size_t)p.rows * k, tiles = embed_tiles(n);
     int bits = 1;
     while ((vocab >> bits) > 0) ++bits;  // of the keys 0 .. vocab
     l.passes = cdiv(bits, kEmbedDigit);
@@ -1368,7 +1369,7 @@ gbla_status embed_backward(const gbla_shape* shape, const void* ids, int wide_id
   EmbedArgs a = embed_args(p, ids, wide_ids, k, vocab, scale, ws);
   a.dy = dy; a.dtable = dtable;
   EmbedSort s{};
-  s.tiles = (int)((a.n + kEmbedTile - 1) / kEmbedTile);
+  s.tiles = (int)embed_tiles((size_t)a.n);
   s.key_bits = l.passes * l.bits;
   for (int i = 0; i < 2; ++i) {
     s.keys[i] = at<int>(ws, l.keys[i]);

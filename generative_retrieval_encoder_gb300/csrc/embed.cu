@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(kThreads) k_embed_fwd(const EmbedArgs a, int p
   __syncthreads();
   const T* tab = static_cast<const T*>(a.table);
   T* y = static_cast<T*>(a.y) + s0 * a.d;
-  constexpr int E = WIDE ? 16 / sizeof(T) : 1;
   const int64_t total = (int64_t)ns * cols;  // more than 2^16 for one slot alone
   for (int64_t i0 = threadIdx.x; i0 < total; i0 += 4 * kThreads) {
     uint4 v[4];
@@ -103,10 +102,11 @@ __global__ void __launch_bounds__(kThreads) k_embed_fwd(const EmbedArgs a, int p
 }
 
 // ------------------------------------------------------------------ the sort
-// A tile's keys: a warp takes kEmbedTile / 8 consecutive ones, 32 a round.
+// A tile's keys: a warp takes an eighth of them, consecutive, 32 a round.
 constexpr int kRounds = kEmbedTile / kThreads;
+template <int R>
 __device__ __forceinline__ int64_t place_of(int tile, int round) {
-  return (int64_t)tile * kEmbedTile + (threadIdx.x >> 5) * (kRounds * 32) + round * 32 + (threadIdx.x & 31);
+  return (int64_t)tile * (R * kThreads) + (threadIdx.x >> 5) * (R * 32) + round * 32 + (threadIdx.x & 31);
 }
 // The key at a place of the pass's input: an id, V for none (last of all), V too past the end.
 __device__ __forceinline__ int key_at(const EmbedArgs& a, const EmbedSort& s, int64_t i, bool first) {
@@ -116,10 +116,12 @@ __device__ __forceinline__ int key_at(const EmbedArgs& a, const EmbedSort& s, in
   return id < 0 ? a.V : id;
 }
 
-// The table's gradient is cleared meanwhile: the sort's CTAs are few and wait for latencies, so each of its launches has more CTAs that
-// clear a share of it, kFill values each (4 hashes into a million rows of 128: 512 MB, 122 us against 95; the rows that no id has need not
-// be found later).
+// Of a table of more rows than there are slots the whole gradient is cleared meanwhile: the sort's CTAs are few and wait for latencies, so
+// each of its launches has more CTAs that clear a share, kFill values each.  Of a smaller one the rows that no id has are cleared beside
+// the sums, which write the others.  (4 hashes into a million rows of 128, 512 MB: 109 us against 122; 32768 rows of 512 and 131072 slots,
+// 67 MB: 79 against 71.)
 constexpr int kFill = 16384;
+bool embed_fills(const EmbedArgs& a) { return a.V > a.n; }
 __device__ __forceinline__ bool fill(const EmbedFill& f, int tiles) {
   if ((int)blockIdx.x < tiles) return false;
   const int64_t lo = f.lo + ((int64_t)blockIdx.x - tiles) * kFill, hi = min(f.hi, lo + kFill);
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_count(const EmbedArgs a, con
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = place_of(blockIdx.x, r);
+    const int64_t i = place_of<kRounds>(blockIdx.x, r);
     if (i < a.n) atomicAdd(&count[(key_at(a, s, i, first) >> shift) & (bins - 1)], 1);
   }
   __syncthreads();
@@ -174,7 +176,7 @@ __device__ __forceinline__ int sum_before(int v, int* red) {
 
 // A tile's keys and slots to their places by the digit at `shift`.  ALL: a single tile, every pass in this one CTA, which also
 // counts.
-template <bool ALL>
+template <bool ALL, int R>
 __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, EmbedSort s, const EmbedFill f, int bits, int shift, bool first) {
   pdl_enter();
   if (fill(f, s.tiles)) return;
@@ -189,10 +191,10 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
   for (;;) {
     for (int i = lane; i < bins; i += 32) warp_count[warp][i] = 0;
     __syncwarp();
-    int key[kRounds], rank[kRounds], own[kRounds];
+    int key[R], rank[R], own[R];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const int64_t i = place_of(tile, r);
+    for (int r = 0; r < R; ++r) {
+      const int64_t i = place_of<R>(tile, r);
       key[r] = key_at(a, s, i, first);
       own[r] = first || i >= a.n ? (int)i : s.slot_in[i];
     }
@@ -210,8 +212,8 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
       for (int t = g0 * kEmbedTiles; t < tile; ++t) before += s.count[(int64_t)t * kMaxBins + threadIdx.x];
     }
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const bool in = place_of(tile, r) < a.n;
+    for (int r = 0; r < R; ++r) {
+      const bool in = place_of<R>(tile, r) < a.n;
       const int digit = (key[r] >> shift) & (bins - 1);
       const unsigned same = __match_any_sync(FULL, in ? digit : -1);
       const int ahead = warp_count[warp][digit];
@@ -236,8 +238,8 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
     if (threadIdx.x < bins) base[threadIdx.x] = at;
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const int64_t i = place_of(tile, r);
+    for (int r = 0; r < R; ++r) {
+      const int64_t i = place_of<R>(tile, r);
       if (i >= a.n) continue;
       const int digit = (key[r] >> shift) & (bins - 1);
       const int to = base[digit] + warp_count[warp][digit] + rank[r];
@@ -283,11 +285,71 @@ struct Sum {
   }
 };
 
-// Groups of G threads, G E columns of a chunk each.
+// The rows of the ids without a slot, kThreads of them a CTA: which of them occur is read from the sorted keys between the first
+// and the last of them.
+__device__ void clear_rows(const EmbedArgs& a, const int* key, int64_t v0) {
+  __shared__ int64_t bound[2];
+  __shared__ unsigned there[kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < kThreads / 32) there[threadIdx.x] = 0;
+  if (warp < 2) {  // the first place of a key >= v, 32 places looked at at a time
+    const int64_t v = min(v0 + warp * kThreads, (int64_t)a.V);
+    int64_t lo = 0, hi = a.n;  // it is in [lo, hi]
+    while (lo < hi) {
+      const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+      const unsigned m = __ballot_sync(FULL, i < hi && key[i] < v);  // a prefix of the lanes
+      const int k = __popc(m);
+      const int64_t l = lo;
+      lo = k ? l + (k - 1) * step + 1 : l;
+      hi = min(hi, l + k * step);
+    }
+    if (lane == 0) bound[warp] = lo;
+  }
+  __syncthreads();
+  // (a frequent id has many places: four keys a load, four loads on their way)
+  for (int64_t i0 = (bound[0] & ~(int64_t)3) + threadIdx.x * 4; i0 < bound[1]; i0 += kThreads * 16) {
+    int4 k[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = i0 + u * kThreads * 4;
+      k[u] = i < bound[1] ? *reinterpret_cast<const int4*>(key + i) : make_int4(-1, -1, -1, -1);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = i0 + u * kThreads * 4;
+      const int q[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + j < bound[0] || i + j >= bound[1]) continue;
+        const int r = q[j] - (int)v0;
+        if (!(reinterpret_cast<volatile unsigned*>(there)[r >> 5] >> (r & 31) & 1)) atomicOr(&there[r >> 5], 1u << (r & 31));
+      }
+    }
+  }
+  __syncthreads();
+  const bool wide = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0;
+  for (unsigned m = ~there[warp]; m; m &= m - 1) {
+    const int64_t v = v0 + warp * 32 + __ffs(m) - 1;
+    if (v >= a.V) break;
+    float* out = a.dtable + v * a.d;
+    if (wide)
+      for (int c = lane * 4; c < a.d; c += 128) *reinterpret_cast<float4*>(out + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else
+      for (int c = lane; c < a.d; c += 32) out[c] = 0.f;
+  }
+}
+
+// Groups of G threads, G E columns of a chunk each: the first `chunk_ctas` CTAs; the others, if any, clear the rows of the ids without
+// a slot.
 template <typename T, int G, bool WIDE>
-__global__ void __launch_bounds__(kThreads, WIDE ? 4 : 3) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks) {
+__global__ void __launch_bounds__(kThreads, !WIDE ? 3 : G < 32 ? 2 : 4) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
   pdl_enter();
-  constexpr int E = 16 / sizeof(T), U = 32 / E, C = kEmbedCap;
+  if ((int)blockIdx.x >= chunk_ctas) {
+    clear_rows(a, s.key_out, ((int64_t)blockIdx.x - chunk_ctas) * kThreads);
+    return;
+  }
+  constexpr int E = 16 / sizeof(T), C = kEmbedCap;
+  constexpr int U = !WIDE ? 32 / E : G < 32 ? 16 : 8;  // rows in flight: short rows' groups are few
   // the keys from C places before the chunk to C behind it, and the slots from its first place on
   __shared__ __align__(16) int keys[kThreads / G][3 * C];
   __shared__ __align__(16) int slots[kThreads / G][2 * C];
@@ -300,16 +362,20 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 4 : 3) k_embed_rows(const Emb
   if (lo >= a.n) return;
   int *key = keys[grp] + C, *slot = slots[grp];  // by place - lo
   const int len = (int)min((int64_t)C, a.n - lo);
-  // also: the places nearest to the chunk's first and last one that have another key than it, before and behind
-  const int k0 = s.key_out[lo], k1 = s.key_out[lo + len - 1];
-  if (k0 >= a.V) return;  // sorted last: slots without an id, nothing else
-  int b0 = -C - 1, f0 = 2 * C, b1 = -1, f1 = 2 * C;
 #pragma unroll
   for (int j = t - C; j < 2 * C; j += G) {
     const bool in = lo + j >= 0 && lo + j < a.n;
-    const int k = in ? s.key_out[lo + j] : -1;
-    key[j] = k;
+    key[j] = in ? s.key_out[lo + j] : -1;
     if (j >= 0) slot[j] = in ? s.slot_out[lo + j] : -1;
+  }
+  __syncwarp(team);
+  const int k0 = key[0], k1 = key[len - 1];
+  if (k0 >= a.V) return;  // sorted last: slots without an id, nothing else
+  // the places nearest to the chunk's first and last one that have another key than it, before and behind
+  int b0 = -C - 1, f0 = 2 * C, b1 = -1, f1 = 2 * C;
+#pragma unroll
+  for (int j = t - C; j < 2 * C; j += G) {
+    const int k = key[j];
     if (j < 0 && k != k0) b0 = max(b0, j);
     if (j > 0 && k != k0) f0 = min(f0, j);
     if (j >= 0 && j < len && k != k1) b1 = max(b1, j);
@@ -322,7 +388,6 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 4 : 3) k_embed_rows(const Emb
     b1 = max(b1, __shfl_xor_sync(team, b1, o));
     f1 = min(f1, __shfl_xor_sync(team, f1, o));
   }
-  __syncwarp(team);
   // the first run is the places (b0, f0), the last one (b1, f1), as far as they are looked at: C before and behind
   const bool long0 = f0 - b0 - 1 > C, same = b1 < 0, long1 = k1 < a.V && (same ? long0 : f1 - b1 - 1 > C);
   int from = 0, to = len;
@@ -360,15 +425,15 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 4 : 3) k_embed_rows(const Emb
   };
   if (WIDE) {
     const bool in = c < a.d;
-    for (int i = from; i < to; i += 8) {
-      uint4 w[8];
+    for (int i = from; i < to; i += U) {
+      uint4 w[U];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < U; ++u) {
         w[u] = make_uint4(0, 0, 0, 0);
         if (i + u < to && in) w[u] = __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)slot[i + u] * a.d + c));
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < U; ++u) {
         if (i + u >= to) continue;
         begin(i + u);
         const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
@@ -499,11 +564,11 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, cons
 template <typename T, bool WIDE>
 cudaError_t rows(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st) {
   constexpr int E = 16 / sizeof(T);
-  const int64_t chunks = (a.n + kEmbedCap - 1) / kEmbedCap;
+  const int64_t chunks = (a.n + kEmbedCap - 1) / kEmbedCap, clear = embed_fills(a) ? 0 : ((int64_t)a.V + kThreads - 1) / kThreads;
   auto go = [&](auto kernel, int G) {
     const int blocks = (a.d + G * E - 1) / (G * E), per = kThreads / G;
     const int64_t ctas = (chunks * blocks + per - 1) / per;
-    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), 0, st, a, s, blocks);
+    return launch_pdl(kernel, dim3((unsigned)(ctas + clear)), dim3(kThreads), 0, st, a, s, blocks, (int)ctas);
   };
   const int v = (a.d + E - 1) / E;
   return v <= 4 ? go(k_embed_rows<T, 4, WIDE>, 4) : v <= 8 ? go(k_embed_rows<T, 8, WIDE>, 8)
@@ -543,7 +608,7 @@ cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st) {
 
 // Share `i` of `n` of the gradient's values, from a multiple of 4 on.
 EmbedFill embed_fill(const EmbedArgs& a, int i, int n) {
-  const int64_t all = (int64_t)a.V * a.d;
+  const int64_t all = embed_fills(a) ? (int64_t)a.V * a.d : 0;
   auto cut = [&](int k) { return k == n ? all : all / n * k / 4 * 4; };
   return EmbedFill{a.dtable, cut(i), cut(i + 1), reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0};
 }
@@ -554,8 +619,10 @@ cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, const Emb
 }
 cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st) {
   const dim3 grid((unsigned)s.tiles + fill_ctas(f));
-  if (s.tiles == 1) return launch_pdl(k_embed_place<true>, grid, dim3(kThreads), 0, st, a, s, f, bits, 0, true);
-  return launch_pdl(k_embed_place<false>, grid, dim3(kThreads), 0, st, a, s, f, bits, shift, shift == 0);
+  if (s.tiles == 1)  // (rounds without keys cost time, too: 1023 keys 14.0 us in 4 rounds a pass, 16.6 in 8)
+    return launch_pdl(a.n <= kEmbedOne / 2 ? k_embed_place<true, kEmbedOne / 2 / kThreads> : k_embed_place<true, kEmbedOne / kThreads>, grid,
+                      dim3(kThreads), 0, st, a, s, f, bits, 0, true);
+  return launch_pdl(k_embed_place<false, kRounds>, grid, dim3(kThreads), 0, st, a, s, f, bits, shift, shift == 0);
 }
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st) {
   const size_t es = f32 ? 4 : 2;

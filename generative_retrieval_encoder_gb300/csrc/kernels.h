@@ -333,7 +333,8 @@ cudaError_t launch_ln_cols_long(const LnArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_ln_cols(const LnArgs& a, float* dw, float* db, cudaStream_t st);
 
 // ------------------------------------------------------------ token embedding
-constexpr int kEmbedTile = 1024;   // keys of a CTA of the sort
+constexpr int kEmbedTile = 512;    // keys of a CTA of the sort
+constexpr int kEmbedOne = 2048;    // keys that one CTA sorts alone
 constexpr int kEmbedTiles = 32;    // tiles whose counts are also kept summed
 constexpr int kEmbedDigit = 8;     // bits of a digit, at most
 constexpr int kEmbedCap = 32;      // sorted places that a group of threads sums
@@ -348,7 +349,7 @@ struct EmbedArgs {
   int* err;                           // the error word, 0 on entry (but where the kernel clears it itself)
 };
 struct EmbedSort {
-  int tiles, key_bits;
+  int tiles, key_bits;               // tiles = 1: one CTA goes through every pass
   const int* key_in; int* key_out; const int* slot_in; int* slot_out;  // of the pass; at last key_out, slot_out are the sorted ones
   int* keys[2]; int* slots[2];        // [n] each
   int* count; int* sums;              // [tiles][2^kEmbedDigit]; the pass's [tiles / kEmbedTiles][2^kEmbedDigit], 0 on entry
