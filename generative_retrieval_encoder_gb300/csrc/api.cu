@@ -1502,8 +1502,9 @@ gbla_status beam_reorder(const gbla_beam* beam, const gbla_beam_state* states, i
       t.dst = states[k].dst; t.src = states[k].src; t.row_bytes = states[k].row_bytes;
       const uintptr_t bits = (uintptr_t)t.row_bytes | reinterpret_cast<uintptr_t>(t.dst) | reinterpret_cast<uintptr_t>(t.src);
       t.unit = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
-      t.chunks = (int)((t.row_bytes / t.unit + m.cols - 1) / m.cols);
-      more = (int64_t)t.chunks * g.B;
+      const int64_t units = t.row_bytes / t.unit;
+      more = t.dst == t.src ? (units + m.cols - 1) / m.cols * g.B : (units * g.B * g.n_out + kBeamMoveUnits - 1) / kBeamMoveUnits;
+      t.ctas = (int)more;
     }
     const bool full = tab.n == 64 || ctas + more > 0x7fffff00LL;
     if (full || k == n_states) {

@@ -747,49 +747,85 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
 }
 
 // ------------------------------------------------------------------ reorder
-// A CTA takes all K rows of one group over a few columns of one tensor: it reads every row that goes on before it writes one,
-// so the rows may be moved within their tensor.  U: the access's type.
+// i / d for i d < 2^32 as a multiplication: `by` is ceil(2^32 / d), or 0 for d = 1.
+__device__ __forceinline__ uint32_t recip(uint32_t d) { return d == 1 ? 0 : 0xffffffffu / d + 1; }
+__device__ __forceinline__ uint32_t quot(uint32_t i, uint32_t by) { return by ? __umulhi(i, by) : i; }
+
+constexpr int kMove = kBeamMoveUnits / 256;  // accesses of a thread, all on their way before the first is stored
+
+// Within one tensor a CTA takes all K rows of one group over a few columns: it reads every row that goes on before it writes one.
+// U: the access's type.
 template <typename U>
-__device__ __forceinline__ void move_rows(const BeamState& t, const BeamMove& m, int task) {
-  const int chunks = t.chunks, b = task / chunks, chunk = task - b * chunks;
-  const int units = (int)(t.row_bytes / sizeof(U)), cols = m.cols;
+__device__ __forceinline__ void move_within(const BeamState& t, const BeamMove& m, int task) {
+  const int units = (int)(t.row_bytes / sizeof(U)), cols = m.cols, chunks = t.ctas / m.B, b = task / chunks, chunk = task - b * chunks;
   const int c0 = chunk * cols, nc = min(cols, units - c0), total = nc * m.n;
-  const U* src = static_cast<const U*>(t.src) + (int64_t)b * m.K * units + c0;
-  U* dst = static_cast<U*>(t.dst) + (int64_t)b * m.n * units + c0;
-  U v[8];
-  bool is[8];
+  const uint32_t by = recip(nc);
+  U* rows = static_cast<U*>(t.dst) + (int64_t)b * m.n * units + c0;
+  U v[kMove];
+  int to[kMove];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
+  for (int u = 0; u < kMove; ++u) {
     const int i = threadIdx.x + u * 256;
-    is[u] = false;
+    to[u] = -1;
     if (i >= total) continue;
-    const int k = i / nc, c = i - k * nc, p = m.parents[(int64_t)b * m.n + k];
-    if ((unsigned)p >= (unsigned)m.K || (t.dst == t.src && p == k)) continue;
-    v[u] = src[(int64_t)p * units + c];
-    is[u] = true;
+    const int k = (int)quot(i, by), c = i - k * nc, p = m.parents[(int64_t)b * m.n + k];
+    if ((unsigned)p >= (unsigned)m.K || p == k) continue;
+    v[u] = rows[(int64_t)p * units + c];
+    to[u] = k;
   }
   __syncthreads();
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int i = threadIdx.x + u * 256;
-    if (!is[u]) continue;
-    const int k = i / nc, c = i - k * nc;
-    dst[(int64_t)k * units + c] = v[u];
+  for (int u = 0; u < kMove; ++u)
+    if (to[u] >= 0) rows[(int64_t)to[u] * units + (threadIdx.x + u * 256 - to[u] * nc)] = v[u];
+}
+// Between two, kBeamMoveUnits consecutive accesses of the destination, whatever rows they are in.
+template <typename U>
+__device__ __forceinline__ void move_between(const BeamState& t, const BeamMove& m, int task) {
+  const int64_t units = t.row_bytes / (int64_t)sizeof(U), all = units * m.B * m.n, i0 = (int64_t)task * kBeamMoveUnits;
+  const int64_t row0 = i0 / units;
+  const int off = (int)(i0 - row0 * units), b0 = (int)(row0 / m.n), k0 = (int)(row0 - (int64_t)b0 * m.n);
+  const bool wide = units >= kBeamMoveUnits;  // one row, or two
+  const uint32_t by = wide ? 0 : recip((uint32_t)units), by_n = recip(m.n);  // i < 2 kBeamMoveUnits
+  const U* src = static_cast<const U*>(t.src);
+  U* dst = static_cast<U*>(t.dst) + i0;
+  U v[kMove];
+  bool is[kMove];
+#pragma unroll
+  for (int u = 0; u < kMove; ++u) {
+    const int j = threadIdx.x + u * 256;
+    is[u] = false;
+    if (i0 + j >= all) continue;
+    const int64_t i = off + (int64_t)j;
+    const uint32_t r = wide ? i >= units : quot((uint32_t)i, by), g = quot(k0 + r, by_n);
+    const int p = m.parents[row0 + r];
+    if ((unsigned)p >= (unsigned)m.K) continue;
+    v[u] = src[((int64_t)(b0 + g) * m.K + p) * units + (i - (int64_t)r * units)];
+    is[u] = true;
   }
+#pragma unroll
+  for (int u = 0; u < kMove; ++u)
+    if (is[u]) dst[threadIdx.x + u * 256] = v[u];
+}
+template <typename U>
+__device__ __forceinline__ void move_rows(const BeamState& t, const BeamMove& m, int task) {
+  if (t.dst == t.src) move_within<U>(t, m, task);
+  else move_between<U>(t, m, task);
 }
 __global__ void __launch_bounds__(256) k_beam_move(const __grid_constant__ BeamTable tab, const BeamMove m) {
   pdl_enter();
-  if (blockIdx.x == gridDim.x - 1) {  // the last CTA looks at every parent and alone reports
+  if (blockIdx.x == 0) {  // one CTA looks at every parent and alone reports
     int bad = 0;
+#pragma unroll 8
     for (int64_t i = threadIdx.x; i < (int64_t)m.B * m.n; i += 256) bad |= (unsigned)m.parents[i] >= (unsigned)m.K;
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *m.err = bad ? 1 : 0;
     return;
   }
+  const int cta = (int)blockIdx.x - 1;
   int k = 0;
-  while (k + 1 < tab.n && tab.t[k + 1].first <= (int)blockIdx.x) ++k;
+  while (k + 1 < tab.n && tab.t[k + 1].first <= cta) ++k;
   const BeamState& t = tab.t[k];
-  const int task = (int)blockIdx.x - t.first;
+  const int task = cta - t.first;
   if (t.unit == 16) move_rows<uint4>(t, m, task);
   else if (t.unit == 4) move_rows<uint32_t>(t, m, task);
   else move_rows<uint8_t>(t, m, task);

@@ -387,10 +387,10 @@ struct BeamArgs {
   float* top; int runs, lg;          // [B K][runs]: largest logits of runs of 2^lg pieces
   int* err;
 };
-struct BeamState { void* dst; const void* src; int64_t row_bytes; int first, chunks, unit; };
+struct BeamState { void* dst; const void* src; int64_t row_bytes; int first, ctas, unit; };  // its first CTA, and how many
 struct BeamTable { int n; BeamState t[64]; };
-struct BeamMove { const int32_t* parents; int B, K, n, cols; int* err; };
-constexpr int kBeamMoveUnits = 2048; // accesses of a CTA of launch_beam_move: cols * max(K, n) of them at most
+struct BeamMove { const int32_t* parents; int B, K, n, cols; int* err; };  // cols: of a CTA that moves rows within a tensor, n cols <= kBeamMoveUnits
+constexpr int kBeamMoveUnits = 2048; // accesses of a CTA of launch_beam_move
 cudaError_t launch_beam_rows(const BeamArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_beam_pick(const BeamArgs& a, bool f32, cudaStream_t st);
 // ctas: of all the table's tensors; one more checks the parents.
