@@ -1414,7 +1414,7 @@ gbla_status layer_norm_forward(const gbla_shape* shape, const void* x, int64_t l
   const size_t es = p.f32 ? 4 : 2;
   for (const void* q : {x, res, w, b, (const void*)sum, (const void*)y})
     if (!aligned(q, es)) return GBLA_ERR_INVALID_ARG;
-  if (!x || !y || ldx < p.d || !aligned(stats, 8) || !(eps >= 0.f) || eps > 3e38f) return GBLA_ERR_INVALID_ARG;
+  if (!x || !y || ldx < p.d || ldx > (1LL << 40) || !aligned(stats, 8) || !(eps >= 0.f) || eps > 3e38f) return GBLA_ERR_INVALID_ARG;
   if (sum && (!res || (sum == x && ldx != p.d)) || y == x || y == res || (const void*)y == sum) return GBLA_ERR_INVALID_ARG;
   if ((r = ws_status(ws, ws_bytes, ln_bytes(p, false))) != GBLA_OK) return r;
   const RowCtx c{static_cast<cudaStream_t>(stream)};
@@ -1433,7 +1433,8 @@ gbla_status layer_norm_backward(const gbla_shape* shape, const void* x, int64_t 
   const size_t es = p.f32 ? 4 : 2;
   for (const void* q : {x, w, dy, ds, (const void*)dx})
     if (!aligned(q, es)) return GBLA_ERR_INVALID_ARG;
-  if (!x || !stats || !dy || !dx || ldx < p.d || !aligned(stats, 8) || !aligned4(dw) || !aligned4(db)) return GBLA_ERR_INVALID_ARG;
+  if (!x || !stats || !dy || !dx || ldx < p.d || ldx > (1LL << 40) || !aligned(stats, 8) || !aligned4(dw) || !aligned4(db))
+    return GBLA_ERR_INVALID_ARG;
   if (dx == x || dx == dy) return GBLA_ERR_INVALID_ARG;
   if ((r = ws_status(ws, ws_bytes, ln_bytes(p, true))) != GBLA_OK) return r;
   const RowCtx c{static_cast<cudaStream_t>(stream)};
@@ -1488,7 +1489,7 @@ gbla_status beam_reorder(const gbla_beam* beam, const gbla_beam_state* states, i
     const gbla_beam_state& t = states[k];
     if (t.row_bytes < 0 || (t.row_bytes > 0 && (!t.dst || !t.src)) || (t.dst == t.src && g.n_out != g.K && t.row_bytes > 0))
       return GBLA_ERR_INVALID_ARG;
-    if (t.row_bytes > (1LL << 30) || (double)t.row_bytes * g.B / m.cols > 1e9) return GBLA_ERR_UNSUPPORTED;  // tasks are counted in 31 bits
+    if (t.row_bytes > (1LL << 30) || t.row_bytes * g.B * g.n_out > (1LL << 39)) return GBLA_ERR_UNSUPPORTED;  // CTAs are counted in 31 bits
   }
   if ((r = ws_status(ws, ws_bytes, kAlign)) != GBLA_OK) return r;
   const RowCtx c{static_cast<cudaStream_t>(stream)};

@@ -360,10 +360,10 @@ gbla_status gbla_adamw_step(const gbla_adamw_tensor* tensors, int n_tensors,
  *           (GBLA_ERR_DEVICE_CHECK), and so does a seq_lens value outside
  *           [0, L]: they count as no token and as an empty sequence
  *   table   (io) [vocab, d];  y (io) [rows, k d], rounded once
- * d, k and vocab are free: rows k <= 2^30, vocab <= 2^30, d <= 2^20,
- * vocab d <= 2^38, rows k d <= 2^40.  Pointers are aligned to their element (rows of a multiple of
- * 16 bytes in 16-byte aligned tensors are read in wider pieces).  The shape's H,
- * d_h, gate and rms_eps are ignored.  Workspace: embed_workspace_size(.., 0).
+ * d, k and vocab are free: rows k <= 2^30, vocab <= 2^30, k <= 2^20, d <= 2^20,
+ * vocab d <= 2^38, rows k d <= 2^40.  Pointers are aligned to their element (rows
+ * of a multiple of 16 bytes in 16-byte aligned tensors are read in wider pieces).
+ * The shape's H, d_h, gate and rms_eps are ignored.  Workspace: embed_workspace_size(.., 0).
  */
 gbla_status embed_forward(const gbla_shape* shape, const void* ids,
                           int wide_ids, int k, const void* table,
@@ -394,7 +394,7 @@ size_t embed_workspace_size(const gbla_shape* shape, int64_t vocab, int k,
  *   shape   B, L, d, io_dtype and the sequence form; tokens of padded slots past
  *           their sequence get zeros in every output (a seq_lens value outside
  *           [0, L] sets the error word and counts as 0); cu_seqlens is not read
- *   x       (io) [rows, d], row stride ldx >= d
+ *   x       (io) [rows, d], row stride ldx, d .. 2^40
  *   res     (io) [rows, d] or NULL (s = x)
  *   w, b    (io) [d] or NULL (ones, zeros)
  *   sum     (io) [rows, d]: s, rounded once, which is what is normed; NULL without
@@ -445,7 +445,7 @@ typedef struct {
 } gbla_beam;
 
 /*
- *   logits   (io) [B K, V], row stride ld >= V, aligned to the element
+ *   logits   (io) [B K, V], row stride ld, V .. 2^40, aligned to the element
  *   scores   fp32 [B, K]; a beam of -inf or NaN has no candidates (the beams but
  *            the first of a search that starts with K copies)
  *   allowed  uint32 [B K, ceil(V / 32)] or NULL: bit t % 32 of word t / 32 lets
@@ -476,7 +476,7 @@ size_t beam_workspace_size(const gbla_beam* beam);
 typedef struct {
   void* dst;         /* may be src, with n_out = K: moved in place               */
   const void* src;
-  int64_t row_bytes; /* >= 0                                                     */
+  int64_t row_bytes; /* 0 .. 2^30; B n_out row_bytes <= 2^39                     */
 } gbla_beam_state;
 
 /*

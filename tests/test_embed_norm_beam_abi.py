@@ -94,6 +94,13 @@ def test_layer_norm_host_errors_launch_nothing(L, dtype):
     assert L.layer_norm_workspace_size(ctypes.byref(s), 2) == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_norm_refuses_strides_that_pass_64_bits(L, dtype):
+    s = gbla.glr_shape(2, 100, 48, dtype=dtype)
+    for ldx in ((1 << 40) + 1, 1 << 60):
+        assert _fwd(L, s, ldx=ldx) == I and _bwd(L, s, ldx=ldx) == I
+
+
 def _select(L, g, logits=FAKE, ld=1000, scores=FAKE, allowed=None, done=None, out=(FAKE, FAKE, FAKE), new_done=None, ws=FAKE, n=1 << 40):
     return L.beam_select(ctypes.byref(g), logits, ld, scores, allowed, done, *out, new_done, ws, n, None)
 
@@ -142,6 +149,16 @@ def test_reorder_host_errors_launch_nothing(L):
     assert L.beam_reorder(ctypes.byref(g), None, 1, FAKE, FAKE, 256, None) == I
     assert call(g, [ok], n=255) == W and call(g, [ok], ws=None) == W
     assert call(gbla.beam_shape(1 << 20, 4, 1000), [gbla.BeamState(1 << 20, 1 << 21, 1 << 30)]) == U
+
+
+def test_reorder_refuses_what_31_bits_of_tasks_cannot_count(L):
+    def call(B, n, row, dst):
+        table = (gbla.BeamState * 1)(gbla.BeamState(dst, 1 << 21, row))
+        return L.beam_reorder(ctypes.byref(gbla.beam_shape(B, 4, 1000, n_out=n)), table, 1, FAKE, FAKE, 256, None)
+    for dst in (1 << 20, 1 << 21):  # into another tensor, within one
+        assert call(1 << 20, 4, 1 << 18, dst) == U and call(1 << 9, 4, (1 << 28) + 1, dst) == U
+        assert call(1, 4, (1 << 30) + 1, dst) == U
+    assert call(1 << 9, 1024, (1 << 20) + 1, 1 << 20) == U
 
 
 def test_binding_refuses_wrong_tensors(L):
