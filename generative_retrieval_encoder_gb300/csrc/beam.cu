@@ -171,7 +171,9 @@ __device__ __forceinline__ void store_runs(float (&v)[kU], int lg, int per, floa
 }
 
 enum BeamMask { MASK_NONE, MASK_CANDIDATES, MASK_SUM };  // no mask; of the candidates alone; of the sum, too
-// A warp takes kU pieces a lane of one row.  Bound by instructions, some 20 a value (a plain exponential takes 6).
+// A warp takes kU pieces a lane of one row.  Bound by instructions, 19 a value, 16 of them in the fp32 pipe (a plain exponential takes
+// 6): 33.5 M bf16 logits in 29 us, 0.34 of a copy's rate, 16.8 M fp32 ones under a mask in 23, 0.43.  (Rows by way of shared memory
+// in persistent CTAs: 10 us more.)
 template <typename T, BeamMask MASK>
 __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
   pdl_enter();
@@ -493,7 +495,7 @@ __device__ int select_best(PickSmem& s, int cnt, int want, uint64_t& low) {
 }
 
 // A CTA a group: the rows' logarithms, the n best runs, the n best tokens of those, in order.  Bound by the latency of some
-// twenty steps that the CTA takes together.
+// twenty steps that the CTA takes together: K = 16 of V = 32768 in 12 us beside the rows' 29, K = n = 256 of V = 2048 in 18 beside 23.
 template <typename T>
 __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   pdl_enter();
@@ -754,7 +756,7 @@ __device__ __forceinline__ uint32_t quot(uint32_t i, uint32_t by) { return by ? 
 constexpr int kMove = kBeamMoveUnits / 256;  // accesses of a thread, all on their way before the first is stored
 
 // Within one tensor a CTA takes all K rows of one group over a few columns: it reads every row that goes on before it writes one.
-// U: the access's type.
+// U: the access's type.  (50 MB in and out of 16 beams each: 6.8 us, as a copy.)
 template <typename U>
 __device__ __forceinline__ void move_within(const BeamState& t, const BeamMove& m, int task) {
   const int units = (int)(t.row_bytes / sizeof(U)), cols = m.cols, chunks = t.ctas / m.B, b = task / chunks, chunk = task - b * chunks;
@@ -778,7 +780,8 @@ __device__ __forceinline__ void move_within(const BeamState& t, const BeamMove& 
   for (int u = 0; u < kMove; ++u)
     if (to[u] >= 0) rows[(int64_t)to[u] * units + (threadIdx.x + u * 256 - to[u] * nc)] = v[u];
 }
-// Between two, kBeamMoveUnits consecutive accesses of the destination, whatever rows they are in.
+// Between two, kBeamMoveUnits consecutive accesses of the destination, whatever rows they are in: 100 MB to 100 MB in 27 us, as a copy
+// (by columns of a group as above 38: the pieces of a row that a CTA takes are 128 bytes).
 template <typename U>
 __device__ __forceinline__ void move_between(const BeamState& t, const BeamMove& m, int task) {
   const int64_t units = t.row_bytes / (int64_t)sizeof(U), all = units * m.B * m.n, i0 = (int64_t)task * kBeamMoveUnits;
