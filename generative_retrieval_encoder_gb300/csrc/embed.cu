@@ -268,27 +268,23 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
 // eight of them in flight whatever ids they are of, and stores a sum where the id changes.  (131072 rows of 512 bf16, read from where the
 // sort sends it: 35 us with 67 MB of the table's gradient cleared beside, 0.85 of a copy's rate; chunks of 16 or 64 places 4 to 8 us more,
 // rows by way of shared memory 4 more.)
-template <typename T, bool WIDE>
-struct Sum {
-  static constexpr int E = 16 / sizeof(T);
-  float v[E];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int j = 0; j < E; ++j) v[j] = 0.f;
-  }
-  __device__ __forceinline__ void store(float scale, float* out, int c, int d, int step) const {
-    if (WIDE) {
-      if (c >= d) return;
-#pragma unroll
-      for (int j = 0; j < E; j += 4)
-        *reinterpret_cast<float4*>(out + c + j) = make_float4(v[j] * scale, v[j + 1] * scale, v[j + 2] * scale, v[j + 3] * scale);
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (c + j * step < d) out[c + j * step] = v[j] * scale;
-    }
-  }
-};
+// A thread takes P pieces of E columns each, G E columns apart: 16 bytes where rows are whole pieces of that, else pairs of bf16, or two
+// fp32, or a single bf16 where rows are odd.  (65536 slots of 511 columns, V = 32768: fp32 67 us, by one value 80; bf16 92, by two 98,
+// and 193 by eight, whose stores alone fill the instruction cache; 8192 of 201: 32, 39 and 79.  1000 of 100 bf16: 14 in pairs.)
+template <int BYTES> struct Bits;
+template <> struct Bits<16> { using type = uint4; };
+template <> struct Bits<4> { using type = uint32_t; };
+template <> struct Bits<2> { using type = uint16_t; };
+template <typename T, int E>
+using Piece = typename Bits<E * sizeof(T)>::type;
+template <typename T, int E>
+__device__ __forceinline__ float value(const Piece<T, E>& w, int j) {
+  uint32_t q;
+  if constexpr (sizeof(w) == 16) q = (&w.x)[sizeof(T) == 2 ? j / 2 : j];
+  else q = w;
+  if (sizeof(T) == 4) return __uint_as_float(q);
+  return j & 1 ? bf_hi(q) : bf_lo(q);
+}
 
 // The rows of the ids without a slot, kThreads of them a CTA: which of them occur is read from the sorted keys between the first
 // and the last of them.
@@ -344,17 +340,18 @@ __device__ void clear_rows(const EmbedArgs& a, const int* key, int64_t v0) {
   }
 }
 
-// Groups of G threads, G E columns of a chunk each: the first `chunk_ctas` CTAs; the others, if any, clear the rows of the ids without
+// Groups of G threads, G E P columns of a chunk each: the first `chunk_ctas` CTAs; the others, if any, clear the rows of the ids without
 // a slot.
-template <typename T, int G, bool WIDE>
-__global__ void __launch_bounds__(kThreads, !WIDE ? 3 : G < 32 ? 2 : 4) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
+template <typename T, int G, int E, int P>
+__global__ void __launch_bounds__(kThreads, G < 32 || P > 1 ? 2 : 4) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
   pdl_enter();
   if ((int)blockIdx.x >= chunk_ctas) {
     clear_rows(a, s.key_out, ((int64_t)blockIdx.x - chunk_ctas) * kThreads);
     return;
   }
-  constexpr int E = 16 / sizeof(T), C = kEmbedCap;
-  constexpr int U = !WIDE ? 32 / E : G < 32 ? 16 : 8;  // rows in flight: short rows' groups are few
+  using W = Piece<T, E>;
+  constexpr int C = kEmbedCap;
+  constexpr int U = G < 32 && sizeof(W) == 16 ? 16 : 8;  // rows in flight: short rows' groups are few
   // the keys from C places before the chunk to C behind it, and the slots from its first place on
   __shared__ __align__(16) int keys[kThreads / G][3 * C];
   __shared__ __align__(16) int slots[kThreads / G][2 * C];
@@ -362,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, !WIDE ? 3 : G < 32 ? 2 : 4) k_embed_
   const unsigned team = G == 32 ? FULL : ((1u << (G & 31)) - 1) << (threadIdx.x & 31 & ~(G - 1));
   const int64_t task = (int64_t)blockIdx.x * (kThreads / G) + grp;
   const int64_t chunk = task / blocks;
-  const int block = (int)(task - chunk * blocks), c = block * G * E + (WIDE ? t * E : t);
+  const int block = (int)(task - chunk * blocks), c = block * (G * E * P) + t * E;
   const int64_t lo = chunk * C;
   if (lo >= a.n) return;
   int *key = keys[grp] + C, *slot = slots[grp];  // by place - lo
@@ -411,61 +408,68 @@ __global__ void __launch_bounds__(kThreads, !WIDE ? 3 : G < 32 ? 2 : 4) k_embed_
     if (m0 < len) s.longs[atomicAdd(s.n_long, 1)] = make_int2(k1, (int)(2 * chunk + 1));
     if (long0 && f0 <= len) s.last[k0] = (int)(2 * chunk);
   }
+  // where the sum that ends at a place goes: -1 on to the next place, -2, -3 the chunk's partial rows, else the id's row.  In place of the
+  // keys, from the first of them on
+  int* dest = key - C;
+  int d[2 * C / G];
+#pragma unroll
+  for (int q = 0; q < 2 * C / G; ++q) {
+    const int j = t + q * G, k = key[j];
+    const bool ends = j >= from && j < to && (j == to - 1 || key[j + 1] != k);
+    d[q] = !ends ? -1 : j < l1 ? -2 : j >= m0 ? -3 : k;
+  }
+  __syncwarp(team);  // (all have read the keys)
+#pragma unroll
+  for (int q = 0; q < 2 * C / G; ++q) dest[t + q * G] = d[q];
+  __syncwarp(team);
   const T* dy = static_cast<const T*>(a.dy);
-  Sum<T, WIDE> acc;
-  acc.clear();
-  int now = -1;
-  auto flush = [&](int i) {  // the sum of the run whose last place is i - 1
-    if (now < 0) return;
-    if (i - 1 < l1) acc.store(1.f, s.part + 2 * chunk * a.d, c, a.d, G);
-    else if (i - 1 >= m0) acc.store(1.f, s.part + (2 * chunk + 1) * a.d, c, a.d, G);
-    else acc.store(a.scale, a.dtable + (int64_t)now * a.d, c, a.d, G);
+  float acc[P][E];
+  auto clear = [&] {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int j = 0; j < E; ++j) acc[p][j] = 0.f;
   };
-  auto begin = [&](int i) {  // the sum goes on with place i
-    const int k = key[i];
-    if (k == now) return;
-    flush(i);
-    now = k;
-    acc.clear();
-  };
-  if (WIDE) {
-    const bool in = c < a.d;
-    for (int i = from; i < to; i += U) {
-      uint4 w[U];
+  clear();
+  for (int i = from; i < to; i += U) {
+    W w[U][P];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        w[u] = make_uint4(0, 0, 0, 0);
-        if (i + u < to && in) w[u] = __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)slot[i + u] * a.d + c));
-      }
+    for (int u = 0; u < U; ++u) {
+      const T* at = dy + (i + u < to ? (int64_t)slot[i + u] * a.d : 0) + c;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + u >= to) continue;
-        begin(i + u);
-        const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          acc.v[j] += sizeof(T) == 2 ? (j & 1 ? bf_hi(q[(j / 2) & 3]) : bf_lo(q[(j / 2) & 3])) : __uint_as_float(q[j & 3]);
+      for (int p = 0; p < P; ++p) {
+        w[u][p] = W{};
+        if (i + u < to && c + p * G * E < a.d) w[u][p] = __ldcs(reinterpret_cast<const W*>(at + p * G * E));
       }
     }
-  } else {
-    for (int i = from; i < to; i += U) {
-      float f[U][E];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const T* at = dy + (i + u < to ? (int64_t)slot[i + u] * a.d : 0);
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= to) continue;
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[u][j] = i + u < to && c + j * G < a.d ? to_f(at[c + j * G]) : 0.f;
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < E; ++j) acc[p][j] += value<T, E>(w[u][p], j);
+      const int k = dest[i + u];
+      if (k == -1) continue;
+      const float scale = k < 0 ? 1.f : a.scale;
+      float* out = (k < 0 ? s.part + (2 * chunk - 2 - k) * a.d : a.dtable + (int64_t)k * a.d) + c;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (c + p * G * E >= a.d) continue;
+        float* o = out + p * G * E;
+        if constexpr (E % 4 == 0) {
+#pragma unroll
+          for (int j = 0; j < E; j += 4)
+            *reinterpret_cast<float4*>(o + j) = make_float4(acc[p][j] * scale, acc[p][j + 1] * scale, acc[p][j + 2] * scale, acc[p][j + 3] * scale);
+        } else if constexpr (E == 2) {
+          *reinterpret_cast<float2*>(o) = make_float2(acc[p][0] * scale, acc[p][1] * scale);
+        } else {
+          *o = acc[p][0] * scale;
+        }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + u >= to) continue;
-        begin(i + u);
-#pragma unroll
-        for (int j = 0; j < E; ++j) acc.v[j] += f[u][j];
-      }
+      clear();
     }
   }
-  flush(to);
 }
 
 // hi + lo + v, in two words again (64-bit additions have a hundredth of fp32's rate: 35 us for what takes 6)
@@ -567,18 +571,17 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, cons
   }
 }
 
-template <typename T, bool WIDE>
+template <typename T, int E, int P>
 cudaError_t rows(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st) {
-  constexpr int E = 16 / sizeof(T);
   const int64_t chunks = (a.n + kEmbedCap - 1) / kEmbedCap, clear = embed_fills(a) ? 0 : ((int64_t)a.V + kThreads - 1) / kThreads;
   auto go = [&](auto kernel, int G) {
-    const int blocks = (a.d + G * E - 1) / (G * E), per = kThreads / G;
+    const int blocks = (a.d + G * E * P - 1) / (G * E * P), per = kThreads / G;
     const int64_t ctas = (chunks * blocks + per - 1) / per;
     return launch_pdl(kernel, dim3((unsigned)(ctas + clear)), dim3(kThreads), 0, st, a, s, blocks, (int)ctas);
   };
-  const int v = (a.d + E - 1) / E;
-  return v <= 4 ? go(k_embed_rows<T, 4, WIDE>, 4) : v <= 8 ? go(k_embed_rows<T, 8, WIDE>, 8)
-         : v <= 16 ? go(k_embed_rows<T, 16, WIDE>, 16) : go(k_embed_rows<T, 32, WIDE>, 32);
+  const int v = (a.d + E * P - 1) / (E * P);
+  return v <= 4 ? go(k_embed_rows<T, 4, E, P>, 4) : v <= 8 ? go(k_embed_rows<T, 8, E, P>, 8)
+         : v <= 16 ? go(k_embed_rows<T, 16, E, P>, 16) : go(k_embed_rows<T, 32, E, P>, 32);
 }
 
 __global__ void __launch_bounds__(kThreads) k_zero(uint4* p, int64_t n) {
@@ -632,9 +635,11 @@ cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, const Emb
 }
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st) {
   const size_t es = f32 ? 4 : 2;
-  const bool wide = ((uintptr_t)(a.d * es) | (uintptr_t)a.d * 4 | reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.dtable)) % 16 == 0;
-  if (f32) return wide ? rows<float, true>(a, s, st) : rows<float, false>(a, s, st);
-  return wide ? rows<bf16, true>(a, s, st) : rows<bf16, false>(a, s, st);
+  const uintptr_t dy = reinterpret_cast<uintptr_t>(a.dy), out = reinterpret_cast<uintptr_t>(a.dtable);
+  const bool wide = ((uintptr_t)(a.d * es) | (uintptr_t)a.d * 4 | dy | out) % 16 == 0;
+  if (f32) return wide ? rows<float, 4, 1>(a, s, st) : rows<float, 1, 2>(a, s, st);
+  if (wide) return rows<bf16, 8, 1>(a, s, st);
+  return a.d % 2 == 0 && dy % 4 == 0 && out % 8 == 0 ? rows<bf16, 2, 1>(a, s, st) : rows<bf16, 1, 1>(a, s, st);
 }
 cudaError_t launch_embed_join(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st) {
   const int C = a.d % 4 == 0 ? 4 : 1;  // (the partial rows are in the workspace: aligned)
