@@ -699,7 +699,7 @@ EmbedArgs embed_args(const RowPlan& p, const void* ids, int wide_ids, int k, int
 struct RowCtx { cudaStream_t st; };
 
 size_t ln_bytes(const RowPlan& p, bool backward) {
-  return align_up(kAlign + (backward ? (size_t)ln_parts(p.rows, p.d) * 2 * p.d * 4 : 0));
+  return align_up(kAlign + (backward ? (size_t)ln_parts(p.rows, p.d, p.f32) * 2 * p.d * 4 : 0));
 }
 LnArgs ln_args(const RowPlan& p, const void* x, int64_t ldx, const void* w, void* ws) {
   LnArgs a{};
@@ -1444,8 +1444,8 @@ gbla_status layer_norm_backward(const gbla_shape* shape, const void* x, int64_t 
   if (!ln_clears(a)) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
   GBLA_CHECK(launch_ln(a, p.f32, true, c.st), "layer norm bwd");
   if (!a.part) return GBLA_OK;
-  if (!ln_group(p.d)) GBLA_CHECK(launch_ln_cols_long(a, p.f32, c.st), "layer norm cols");
-  GBLA_CHECK(launch_ln_cols(a, dw, db, c.st), "layer norm dw");
+  if (!ln_group(p.d, p.f32)) GBLA_CHECK(launch_ln_cols_long(a, p.f32, c.st), "layer norm cols");
+  GBLA_CHECK(launch_ln_cols(a, p.f32, dw, db, c.st), "layer norm dw");
   return GBLA_OK;
 }
 

@@ -52,10 +52,12 @@ __device__ __forceinline__ uint4 scaled(uint4 w, float s) {
                     __float_as_uint(__uint_as_float(w.z) * s), __float_as_uint(__uint_as_float(w.w) * s));
 }
 
-// A CTA takes `per` slots: their ids once, then the rows as one run of `cols` accesses each (16 bytes where WIDE, one value
-// else), four in flight a thread.  Bound by memory: 131072 rows of 512 bf16 from a table of 32768 in 27 us, 0.9 of a copy's rate with
-// the table read once (L2 holds it).
-template <typename T, bool WIDE>
+// A CTA takes `per` slots: their ids once, then the rows as one run of y.  ROWS: rows of `cols` accesses of 16 bytes each, four in flight a
+// thread.  Bound by memory: 131072 rows of 512 bf16 from a table of 32768 in 27 us, 0.9 of a copy's rate with the table read once (L2
+// holds it).  PAIRS, VALUES: y in pieces of 16 bytes of whatever rows, read from the table by two bf16 or by single values (`per` is a
+// multiple of a piece's values): FIGURES.  SINGLE: of a y that is not aligned, value by value, `cols` of them a row.
+enum EmbedRows { SINGLE, ROWS, PAIRS, VALUES };
+template <typename T, EmbedRows M>
 __global__ void __launch_bounds__(kThreads) k_embed_fwd(const EmbedArgs a, int per, int cols, uint32_t by_cols, bool check) {
   pdl_enter();
   __shared__ int id[1024];
@@ -76,28 +78,61 @@ __global__ void __launch_bounds__(kThreads) k_embed_fwd(const EmbedArgs a, int p
   __syncthreads();
   const T* tab = static_cast<const T*>(a.table);
   T* y = static_cast<T*>(a.y) + s0 * a.d;
-  const int64_t total = (int64_t)ns * cols;  // more than 2^16 for one slot alone
-  for (int64_t i0 = threadIdx.x; i0 < total; i0 += 4 * kThreads) {
-    uint4 v[4];
-    float f[4];
+  if constexpr (M == PAIRS || M == VALUES) {
+    constexpr int E = 16 / sizeof(T), V = M == PAIRS ? 2 : 1;
+    const int total = ns * a.d;  // (below 2^24: `per` is a piece's values, or total some 1024 pieces)
+    for (int e = threadIdx.x * E; e < total; e += kThreads * E) {
+      int k = by_cols ? (int)__umulhi((uint32_t)e, by_cols) : e / a.d, c = e - k * a.d;
+      uint32_t q[E / V];
+      int row = id[k];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + u * kThreads;
-      v[u] = make_uint4(0, 0, 0, 0);
-      f[u] = 0.f;
-      if (i >= total) continue;
-      const int s = per == 1 ? 0 : cols == 1 ? (int)i : (int)__umulhi((uint32_t)i, by_cols), c = (int)(i - (int64_t)s * cols);
-      const int k = id[s];
-      if (k < 0) continue;
-      if (WIDE) v[u] = __ldg(reinterpret_cast<const uint4*>(tab + (int64_t)k * a.d) + c);
-      else f[u] = to_f(tab[(int64_t)k * a.d + c]);
+      for (int j = 0; j < E; j += V) {
+        if (c == a.d && e + j < total) c = 0, row = id[++k];
+        q[j / V] = 0;
+        if (row >= 0 && e + j < total) {
+          const T* at = tab + (int64_t)row * a.d + c;
+          if constexpr (M == VALUES && sizeof(T) == 2) q[j / V] = *reinterpret_cast<const uint16_t*>(at);
+          else q[j / V] = *reinterpret_cast<const uint32_t*>(at);
+        }
+        c += V;
+      }
+      uint4 w;
+      if constexpr (M == VALUES && sizeof(T) == 2) w = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+      else w = make_uint4(q[0], q[1], q[2], q[3]);
+      w = scaled<T>(w, a.scale);
+      if (e + E <= total) {
+        *reinterpret_cast<uint4*>(y + e) = w;
+      } else {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (e + j < total) y[e + j] = from_f<T>(sizeof(T) == 2 ? (j & 1 ? bf_hi(u[j / 2 & 3]) : bf_lo(u[j / 2 & 3])) : __uint_as_float(u[j & 3]));
+      }
     }
+  } else {
+    const int64_t total = (int64_t)ns * cols;  // more than 2^16 for one slot alone
+    for (int64_t i0 = threadIdx.x; i0 < total; i0 += 4 * kThreads) {
+      uint4 v[4];
+      float f[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + u * kThreads;
-      if (i >= total) continue;
-      if (WIDE) reinterpret_cast<uint4*>(y)[i] = scaled<T>(v[u], a.scale);
-      else y[i] = from_f<T>(f[u] * a.scale);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = i0 + u * kThreads;
+        v[u] = make_uint4(0, 0, 0, 0);
+        f[u] = 0.f;
+        if (i >= total) continue;
+        const int s = per == 1 ? 0 : cols == 1 ? (int)i : (int)__umulhi((uint32_t)i, by_cols), c = (int)(i - (int64_t)s * cols);
+        const int k = id[s];
+        if (k < 0) continue;
+        if (M == ROWS) v[u] = __ldg(reinterpret_cast<const uint4*>(tab + (int64_t)k * a.d) + c);
+        else f[u] = to_f(tab[(int64_t)k * a.d + c]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = i0 + u * kThreads;
+        if (i >= total) continue;
+        if (M == ROWS) reinterpret_cast<uint4*>(y)[i] = scaled<T>(v[u], a.scale);
+        else y[i] = from_f<T>(f[u] * a.scale);
+      }
     }
   }
 }
@@ -589,13 +624,6 @@ __global__ void __launch_bounds__(kThreads) k_zero(uint4* p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Accesses a row of the forward takes: of 16 bytes where rows and tensors allow it, of one value else.
-int row_cols(const EmbedArgs& a, bool f32, bool& wide) {
-  const size_t es = f32 ? 4 : 2;
-  wide = ((uintptr_t)(a.d * es) | reinterpret_cast<uintptr_t>(a.table) | reinterpret_cast<uintptr_t>(a.y)) % 16 == 0;
-  return wide ? (int)(a.d * es / 16) : a.d;
-}
-
 }  // namespace
 
 // Up to so many ids one more CTA of the forward checks them, 32 a thread, while the others copy (a launch that clears the error word
@@ -604,15 +632,19 @@ constexpr int64_t kCheckIds = 8192;
 bool embed_fwd_clears(const EmbedArgs& a) { return a.n <= kCheckIds; }
 
 cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st) {
-  bool wide;
-  const int cols = row_cols(a, f32, wide), per = std::max(1, 1024 / cols);  // about four accesses a thread
-  // i / cols = the high word of i ceil(2^32 / cols) for i cols < 2^32: here i < 1024 and cols <= 1024
-  const uint32_t by = cols == 1 ? 0 : (uint32_t)((0x100000000ull + cols - 1) / cols);
+  const int es = f32 ? 4 : 2, E = 16 / es;
+  const uintptr_t tab = reinterpret_cast<uintptr_t>(a.table), y = reinterpret_cast<uintptr_t>(a.y);
+  const EmbedRows m = ((uintptr_t)a.d * es | tab | y) % 16 == 0 ? ROWS : y % 16 ? SINGLE : !f32 && a.d % 2 == 0 && tab % 4 == 0 ? PAIRS : VALUES;
+  const int cols = m == ROWS ? a.d / E : a.d;
+  // about four accesses a thread; of pieces also 16 slots' at least
+  const int per = m == ROWS || m == SINGLE ? std::max(1, 1024 / cols) : std::min(1024, std::max(1, 1024 / a.d) * E);
+  // i / cols = the high word of i ceil(2^32 / cols) for i cols < 2^32: here i < per cols
+  const uint32_t by = cols == 1 || (int64_t)per * cols * cols >> 32 ? 0 : (uint32_t)((0x100000000ull + cols - 1) / cols);
   const bool check = embed_fwd_clears(a);
   const dim3 grid((unsigned)((a.n + per - 1) / per + (check ? 1 : 0)));
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kThreads), 0, st, a, per, cols, by, check); };
-  if (f32) return wide ? go(k_embed_fwd<float, true>) : go(k_embed_fwd<float, false>);
-  return wide ? go(k_embed_fwd<bf16, true>) : go(k_embed_fwd<bf16, false>);
+  if (f32) return go(m == ROWS ? k_embed_fwd<float, ROWS> : m == VALUES ? k_embed_fwd<float, VALUES> : k_embed_fwd<float, SINGLE>);
+  return go(m == ROWS ? k_embed_fwd<bf16, ROWS> : m == PAIRS ? k_embed_fwd<bf16, PAIRS> : m == VALUES ? k_embed_fwd<bf16, VALUES> : k_embed_fwd<bf16, SINGLE>);
 }
 
 // Share `i` of `n` of the gradient's values, from a multiple of 4 on.

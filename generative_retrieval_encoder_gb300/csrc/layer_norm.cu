@@ -45,42 +45,92 @@ __device__ __forceinline__ bool check_slots(const LnArgs& a) {
   return a.first;
 }
 
-// The column of value i of thread t in a row of G threads: 16-byte pieces dealt out in turn (WIDE), or single values.
-template <typename T, int G, bool WIDE>
-__device__ __forceinline__ int col_of(int i, int t) {
+// How a row's values lie with its threads.  SINGLE: one value an access.  PIECES: 16 bytes an access, rows begin at 16-byte boundaries.
+// SHIFTED: the same of rows (bf16, of any number of values in 16-byte aligned tensors) that begin `off` values behind a boundary: the
+// pieces are those of memory, what they hold of other rows is masked, and the ends of a row are stored value by value.
+enum LnRows { SINGLE, PIECES, SHIFTED };
+// The values that row `row` begins behind a 16-byte boundary.
+template <typename T, LnRows M>
+__device__ __forceinline__ int row_off(int64_t row, int d) {
   constexpr int E = 16 / sizeof(T);
-  return WIDE ? ((i / E) * G + t) * E + i % E : i * G + t;
+  return M == SHIFTED ? ((int)row & (E - 1)) * (d & (E - 1)) & (E - 1) : 0;
+}
+// The column of value i of thread t in a row of G threads: pieces dealt out in turn, or single values.  Outside [0, d): none.
+template <typename T, int G, LnRows M>
+__device__ __forceinline__ int col_of(int i, int t, int off) {
+  constexpr int E = 16 / sizeof(T);
+  return M != SINGLE ? ((i / E) * G + t) * E + i % E - off : i * G + t;
 }
 
-// The thread's N values of a row as they lie in memory (0 past d): bf16 values stay two to a register until they are used.
-template <typename T, int G, int N, bool WIDE>
+// The thread's N values of a row as they lie in memory (0 outside the row): bf16 values stay two to a register until they are used.
+template <typename T, int G, int N, LnRows M>
 struct Row {
   static constexpr int E = 16 / sizeof(T);
+  static constexpr bool WIDE = M != SINGLE;
   uint4 w[WIDE ? N / E : 1];
   float v[WIDE ? 1 : N];
-  __device__ __forceinline__ void load(const T* p, int t, int d) {
+  // Zeros in place of a piece's values outside [0, d); c: the column of the first (SHIFTED: of 16-bit values).
+  __device__ static __forceinline__ uint4 masked(uint4 q, int c, int d) {
+    const uint32_t ok = (c < 0 ? 0xffu << -c : 0xffu) & (c + E > d ? (1u << (d - c)) - 1 : 0xffu);
+    auto keep = [&](uint32_t v, int j) { return v & ((ok >> 2 * j & 1 ? 0xffffu : 0u) | (ok >> (2 * j + 1) & 1 ? 0xffff0000u : 0u)); };
+    return make_uint4(keep(q.x, 0), keep(q.y, 1), keep(q.z, 2), keep(q.w, 3));
+  }
+  // The piece's values one by one, or by pairs.
+  __device__ static __forceinline__ uint4 singles(const T* p, int c, int d) {
+    uint32_t u[4] = {0, 0, 0, 0};
+    if (d % 2 == 0 && reinterpret_cast<uintptr_t>(p) % 4 == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((unsigned)(c + 2 * j) < (unsigned)d) u[j] = *reinterpret_cast<const uint32_t*>(p + c + 2 * j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((unsigned)(c + j) < (unsigned)d) u[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[c + j] << (j & 1 ? 16 : 0);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  // SHIFTED: `behind` values of the tensor lie behind the row at least.
+  __device__ __forceinline__ void load(const T* p, int t, int d, int off, int64_t behind) {
     if (WIDE) {
 #pragma unroll
       for (int i = 0; i < N / E; ++i) {
-        const int c = (i * G + t) * E;
-        w[i] = c < d ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
+        const int c = (i * G + t) * E - off;
+        const bool some = c > -E && c < d;
+        if (M == SHIFTED && some && c + E > d && behind < E) {
+          w[i] = singles(p, c, d);
+          continue;
+        }
+        w[i] = some ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
+        if (M == SHIFTED && some && (c < 0 || c + E > d)) w[i] = masked(w[i], c, d);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[WIDE ? 0 : i] = i * G + t < d ? to_f(p[i * G + t]) : 0.f;
     }
   }
-  // The same by way of the thread's own places in shared memory, kThreads apart: asked for now, read when it has come.
-  __device__ static __forceinline__ void ask(uint4* mine, const T* p, int t, int d) {
+  // Of a vector of d values that itself begins anywhere (w, b).
+  __device__ __forceinline__ void load_vec(const T* p, int t, int d, int off) {
+    if (M != SHIFTED) {
+      load(p, t, d, 0, 0);
+    } else {
 #pragma unroll
-    for (int i = 0; i < N / E; ++i) {
-      const int c = (i * G + t) * E;
-      cp_async16(smem_u32(mine + i * kThreads), p + (c < d ? c : 0), c < d ? 16 : 0);
+      for (int i = 0; i < N / E; ++i) w[WIDE ? i : 0] = singles(p, (i * G + t) * E - off, d);
     }
   }
-  __device__ __forceinline__ void take(const uint4* mine) {
+  // The same by way of the thread's own places in shared memory, kThreads apart: asked for now, read when it has come.  What is behind
+  // the row's end is not read (zeros).
+  __device__ static __forceinline__ void ask(uint4* mine, const T* p, int t, int d, int off) {
+#pragma unroll
+    for (int i = 0; i < N / E; ++i) {
+      const int c = (i * G + t) * E - off;
+      const bool some = c < d;
+      cp_async16(smem_u32(mine + i * kThreads), p + (some ? c : -off), !some ? 0 : M == SHIFTED ? min(E, d - c) * (int)sizeof(T) : 16);
+    }
+  }
+  __device__ __forceinline__ void take(const uint4* mine, int t, int d, int off) {
 #pragma unroll
     for (int i = 0; i < N / E; ++i) w[WIDE ? i : 0] = mine[i * kThreads];
+    if (M == SHIFTED && t == 0 && off) w[0] = masked(w[0], -off, d);  // (the row before's)
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -97,17 +147,29 @@ struct Row {
   }
 };
 // Stores the values f(0) .. f(N - 1) of the thread.
-template <typename T, int G, int N, bool WIDE, typename F>
-__device__ __forceinline__ void store_row(T* p, int t, int d, F&& f) {
+template <typename T, int G, int N, LnRows M, typename F>
+__device__ __forceinline__ void store_row(T* p, int t, int d, int off, F&& f) {
   constexpr int E = 16 / sizeof(T);
-  if (WIDE) {
+  if (M != SINGLE) {
 #pragma unroll
     for (int i = 0; i < N; i += E) {
-      const int c = col_of<T, G, true>(i, t);
+      const int c = col_of<T, G, M>(i, t, off);
       uint32_t u[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) u[k] = sizeof(T) == 2 ? pack_bf16(f(i + 2 * k), f(i + 2 * k + 1)) : __float_as_uint(f(i + k));
-      if (c < d) *reinterpret_cast<uint4*>(p + c) = make_uint4(u[0], u[1], u[2], u[3]);
+      if (M == SHIFTED && (c < 0 || c + E > d)) {  // an end of the row, or outside
+        if (d % 2 == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((unsigned)(c + 2 * j) < (unsigned)d) *reinterpret_cast<uint32_t*>(p + c + 2 * j) = u[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if ((unsigned)(c + j) < (unsigned)d) reinterpret_cast<uint16_t*>(p)[c + j] = (uint16_t)(u[j / 2] >> (j & 1 ? 16 : 0));
+        }
+      } else if (c < d) {
+        *reinterpret_cast<uint4*>(p + c) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
     }
   } else {
 #pragma unroll
@@ -145,71 +207,82 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*red)[M]) {
 // A row a group and no loop: bound by memory (two rows in, two out, 16 x 8192 rows of 512 bf16 in 80 us, 0.99 of a copy's rate; 5 CTAs
 // an SM ask for enough at a time, which rows unpacked to fp32 as they are loaded, in three CTAs, did not: 122 us).  One token of 16
 // sequences takes 2 us, a launch.
-template <typename T, int G, int N, bool WIDE>
-__global__ void __launch_bounds__(kThreads, N == 32 ? 2 : !WIDE ? 3 : N * sizeof(T) <= 32 ? 5 : 4) k_ln_fwd(const LnArgs a) {
+template <typename T, int G, int N, LnRows M>
+__global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE ? 3 : N * sizeof(T) <= 32 && M == PIECES ? 5 : 4) k_ln_fwd(const LnArgs a) {
   pdl_enter();
   __shared__ float red[kThreads / 32][1];
-  using R = Row<T, G, N, WIDE>;
+  using R = Row<T, G, N, M>;
   const int t = threadIdx.x % G;
   const float inv = 1.f / (float)a.d;
   if (check_slots(a)) return;
-  const int64_t cta = blockIdx.x - a.first, ctas = gridDim.x - a.first;
-  const int64_t row = cta * (kThreads / G) + threadIdx.x / G;
-  const bool in = row < a.rows, live = in && row_valid(a, row);
-  float s[N];
-  {
-    R x, q;
-    x.clear();
-    q.clear();
-    if (live) {
-      x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
-      if (a.res) q.load(static_cast<const T*>(a.res) + row * a.d, t, a.d);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = a.res ? to_f(from_f<T>(x.get(i) + q.get(i))) : x.get(i);
-  }
-  if (in && a.sum) store_row<T, G, N, WIDE>(static_cast<T*>(a.sum) + row * a.d, t, a.d, [&](int i) { return s[i]; });
-  float m[1] = {0.f}, v[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < N; ++i) m[0] += s[i];
-  group_sum<G, 1>(m, red);
-  const float mean = m[0] * inv;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float c = s[i] - mean;
-    v[0] += col_of<T, G, WIDE>(i, t) < a.d ? c * c : 0.f;
-  }
-  group_sum<G, 1>(v, red);
-  if (!in) return;
-  const float r = live ? 1.f / sqrtf(v[0] * inv + a.eps) : 0.f;
+  const int64_t r00 = (int64_t)(blockIdx.x - a.first) * (kThreads / G), step = (int64_t)(gridDim.x - a.first) * (kThreads / G);
+  const int off = row_off<T, M>(r00 + threadIdx.x / G, a.d);
   R w, b;
-  if (a.w) w.load(static_cast<const T*>(a.w), t, a.d);
-  if (a.b) b.load(static_cast<const T*>(a.b), t, a.d);
-  store_row<T, G, N, WIDE>(static_cast<T*>(a.y) + row * a.d, t, a.d, [&](int i) {
-    float z = (s[i] - mean) * r;
-    if (a.w) z *= w.get(i);
-    if (a.b) z += b.get(i);
-    return live ? z : 0.f;
-  });
-  if (a.stats && t == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(live ? mean : 0.f, r);
+  if (M == SHIFTED) {
+    if (a.w) w.load_vec(static_cast<const T*>(a.w), t, a.d, off);
+    if (a.b) b.load_vec(static_cast<const T*>(a.b), t, a.d, off);
+  }
+  for (int64_t r0 = r00; r0 < a.rows; r0 += step) {  // (as often in every thread of the CTA)
+    const int64_t row = r0 + threadIdx.x / G, behind = (a.rows - 1 - row) * a.d;
+    const bool in = row < a.rows, live = in && row_valid(a, row);
+    float s[N];
+    {
+      R x, q;
+      x.clear();
+      q.clear();
+      if (live) {
+        x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d, off, behind);
+        if (a.res) q.load(static_cast<const T*>(a.res) + row * a.d, t, a.d, off, behind);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = a.res ? to_f(from_f<T>(x.get(i) + q.get(i))) : x.get(i);
+    }
+    if (in && a.sum) store_row<T, G, N, M>(static_cast<T*>(a.sum) + row * a.d, t, a.d, off, [&](int i) { return s[i]; });
+    float m[1] = {0.f}, v[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) m[0] += s[i];
+    group_sum<G, 1>(m, red);
+    const float mean = m[0] * inv;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float c = s[i] - mean;
+      v[0] += (unsigned)col_of<T, G, M>(i, t, off) < (unsigned)a.d ? c * c : 0.f;
+    }
+    group_sum<G, 1>(v, red);
+    if (in) {
+      const float r = live ? 1.f / sqrtf(v[0] * inv + a.eps) : 0.f;
+      if (M != SHIFTED) {
+        if (a.w) w.load_vec(static_cast<const T*>(a.w), t, a.d, off);
+        if (a.b) b.load_vec(static_cast<const T*>(a.b), t, a.d, off);
+      }
+      store_row<T, G, N, M>(static_cast<T*>(a.y) + row * a.d, t, a.d, off, [&](int i) {
+        float z = (s[i] - mean) * r;
+        if (a.w) z *= w.get(i);
+        if (a.b) z += b.get(i);
+        return live ? z : 0.f;
+      });
+      if (a.stats && t == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(live ? mean : 0.f, r);
+    }
+    if (M != SHIFTED) break;
+  }
 }
 
 // Rows that the backward asks for ahead: what is in flight covers the memory's latency with the two CTAs an SM that the column
 // sums' registers allow.  Bound by memory, and by what is in flight at the turns of a row: three rows in, one out, 16 x 8192 rows of 512
 // bf16 in 89 us, 0.89 of a copy's rate (107 by registers alone, 90 with three rows ahead; 64 threads a row, 8 values each in three CTAs,
 // 115: the sums of a row then meet at CTA barriers).
-template <typename T, int N, bool WIDE>
-constexpr int kAhead = !WIDE || N == 32 ? 0 : 2;
+template <typename T, int N, LnRows M>
+constexpr int kAhead = M == SINGLE || N == 32 ? 0 : 2;
 
-template <typename T, int G, int N, bool WIDE>
+template <typename T, int G, int N, LnRows M>
 __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_bwd(const LnArgs a) {
   pdl_enter();
   __shared__ float red[kThreads / 32][2];
   extern __shared__ __align__(16) unsigned char dyn[];
   float* acc = reinterpret_cast<float*>(dyn);  // at the end: [R][G N], the groups' column sums, where the CTA has several
   uint4* ring = reinterpret_cast<uint4*>(dyn) + threadIdx.x;  // [kAhead][3 (N / E)][kThreads]
-  constexpr int R = kThreads / G, A = kAhead<T, N, WIDE>, P = N * (int)sizeof(T) / 16;
-  using Mine = Row<T, G, N, WIDE>;
+  constexpr int R = kThreads / G, A = kAhead<T, N, M>, P = N * (int)sizeof(T) / 16;
+  using Mine = Row<T, G, N, M>;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const float inv = 1.f / (float)a.d;
   if (check_slots(a)) return;
@@ -218,15 +291,16 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
   float dw[N], db[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.f;
-  if (a.w) w.load(static_cast<const T*>(a.w), t, a.d);
+  const int64_t step = ctas * R;  // a multiple of the values of a piece (ln_ctas): a group's rows all begin alike
+  const int off = row_off<T, M>(cta * R + grp, a.d);
+  if (a.w) w.load_vec(static_cast<const T*>(a.w), t, a.d, off);
   s.clear();
-  const int64_t step = ctas * R;
   auto ask = [&](int64_t row, int slot) {
     if (row < a.rows && row_valid(a, row)) {
       uint4* to = ring + slot * 3 * P * kThreads;
-      Mine::ask(to, static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
-      Mine::ask(to + P * kThreads, static_cast<const T*>(a.dy) + row * a.d, t, a.d);
-      if (a.ds) Mine::ask(to + 2 * P * kThreads, static_cast<const T*>(a.ds) + row * a.d, t, a.d);
+      Mine::ask(to, static_cast<const T*>(a.x) + row * a.ldx, t, a.d, off);
+      Mine::ask(to + P * kThreads, static_cast<const T*>(a.dy) + row * a.d, t, a.d, off);
+      if (a.ds) Mine::ask(to + 2 * P * kThreads, static_cast<const T*>(a.ds) + row * a.d, t, a.d, off);
     }
     cp_async_commit();
   };
@@ -244,13 +318,14 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
       const float2 st = reinterpret_cast<const float2*>(a.stats)[row];
       if (A > 0) {
         const uint4* from = ring + slot * 3 * P * kThreads;
-        x.take(from);
-        y.take(from + P * kThreads);
-        if (a.ds) s.take(from + 2 * P * kThreads);
+        x.take(from, t, a.d, off);
+        y.take(from + P * kThreads, t, a.d, off);
+        if (a.ds) s.take(from + 2 * P * kThreads, t, a.d, off);
       } else {
-        x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
-        y.load(static_cast<const T*>(a.dy) + row * a.d, t, a.d);
-        if (a.ds) s.load(static_cast<const T*>(a.ds) + row * a.d, t, a.d);
+        const int64_t behind = (a.rows - 1 - row) * a.d;
+        x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d, off, behind);
+        y.load(static_cast<const T*>(a.dy) + row * a.d, t, a.d, off, behind);
+        if (a.ds) s.load(static_cast<const T*>(a.ds) + row * a.d, t, a.d, off, behind);
       }
       mean = st.x;
       r = st.y;
@@ -262,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
     float c[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float z = (x.get(i) - mean) * r, q = y.get(i), g = a.w ? q * w.get(i) : q;  // past d: dy is 0 there
+      const float z = (x.get(i) - mean) * r, q = y.get(i), g = a.w ? q * w.get(i) : q;  // outside the row: dy is 0 there
       dw[i] += q * z;
       db[i] += q;
       c[0] += g;
@@ -271,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
     group_sum<G, 2>(c, red);
     const float c0 = c[0] * inv, c1 = c[1] * inv;
     if (in)
-      store_row<T, G, N, WIDE>(static_cast<T*>(a.dx) + row * a.d, t, a.d, [&](int i) {
+      store_row<T, G, N, M>(static_cast<T*>(a.dx) + row * a.d, t, a.d, off, [&](int i) {
         const float z = (x.get(i) - mean) * r, q = y.get(i);
         const float g = r * ((a.w ? q * w.get(i) : q) - c0 - z * c1);
         return a.ds ? g + s.get(i) : g;
@@ -290,13 +365,16 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
     if (R == 1) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int c = col_of<T, G, WIDE>(i, t);
-        if (c < a.d) out[which * a.d + c] = which ? db[i] : dw[i];
+        const int c = col_of<T, G, M>(i, t, off);
+        if ((unsigned)c < (unsigned)a.d) out[which * a.d + c] = which ? db[i] : dw[i];
       }
     } else {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[grp * (G * N) + col_of<T, G, WIDE>(i, t)] = which ? db[i] : dw[i];
+      for (int i = 0; i < N; ++i) {
+        const int c = col_of<T, G, M>(i, t, off);
+        if (c >= 0) acc[grp * (G * N) + c] = which ? db[i] : dw[i];
+      }
       __syncthreads();
       for (int c = threadIdx.x; c < a.d; c += kThreads) {
         float q = 0.f;
@@ -439,26 +517,33 @@ __global__ void __launch_bounds__(1024) k_ln_cols(const float* part, int n, int 
   }
 }
 
-template <typename T, int G, int N, bool WIDE>
+// CTAs of `per` rows at a time.  Shifted rows: the scale and the bias, which are read value by value, once for four rows of a group, which
+// begin alike, where four CTAs an SM are left.
+int64_t ln_fwd_ctas(int64_t rows, int per, bool shifted) {
+  const int64_t all = (rows + per - 1) / per, alike = per < 8 ? 8 / per : 1;
+  return !shifted || all < sm_count() * 16 ? all : ((all + 3) / 4 + alike - 1) / alike * alike;
+}
+template <typename T, int G, int N, LnRows M>
 cudaError_t run(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
-  if (!bwd) return launch_pdl(k_ln_fwd<T, G, N, WIDE>, dim3((unsigned)((a.rows + kThreads / G - 1) / (kThreads / G)) + a.first), dim3(kThreads), 0, st, a);
-  const size_t ring = (size_t)kAhead<T, N, WIDE> * 3 * N * sizeof(T) * kThreads;
+  if (!bwd) return launch_pdl(k_ln_fwd<T, G, N, M>, dim3((unsigned)(ln_fwd_ctas(a.rows, kThreads / G, M == SHIFTED) + a.first)), dim3(kThreads), 0, st, a);
+  const size_t ring = (size_t)kAhead<T, N, M> * 3 * N * sizeof(T) * kThreads;
   const size_t smem = std::max(ring, a.part && kThreads / G > 1 ? (size_t)kThreads * N * 4 : 0);
   if (smem > 32 << 10) {
-    const cudaError_t e = cudaFuncSetAttribute(k_ln_bwd<T, G, N, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(k_ln_bwd<T, G, N, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(k_ln_bwd<T, G, N, WIDE>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), smem, st, a);
+  return launch_pdl(k_ln_bwd<T, G, N, M>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), smem, st, a);
 }
-template <typename T, bool WIDE>
+template <typename T, LnRows M>
 cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
-  switch (ln_group(a.d)) {
-    case 8: return run<T, 8, 8, WIDE>(a, bwd, ctas, st);
-    case 16: return run<T, 16, 8, WIDE>(a, bwd, ctas, st);
-    case 32: return a.d <= 256 ? run<T, 32, 8, WIDE>(a, bwd, ctas, st) : run<T, 32, 16, WIDE>(a, bwd, ctas, st);
-    case 64: return run<T, 64, 16, WIDE>(a, bwd, ctas, st);
-    case 128: return run<T, 128, 16, WIDE>(a, bwd, ctas, st);
-    case 256: return a.d <= 4096 ? run<T, 256, 16, WIDE>(a, bwd, ctas, st) : run<T, 256, 32, WIDE>(a, bwd, ctas, st);
+  const int span = ln_span(a.d, sizeof(T) == 4);
+  switch (ln_group(a.d, sizeof(T) == 4)) {
+    case 8: return run<T, 8, 8, M>(a, bwd, ctas, st);
+    case 16: return run<T, 16, 8, M>(a, bwd, ctas, st);
+    case 32: return span <= 256 ? run<T, 32, 8, M>(a, bwd, ctas, st) : run<T, 32, 16, M>(a, bwd, ctas, st);
+    case 64: return run<T, 64, 16, M>(a, bwd, ctas, st);
+    case 128: return run<T, 128, 16, M>(a, bwd, ctas, st);
+    case 256: return span <= 4096 ? run<T, 256, 16, M>(a, bwd, ctas, st) : run<T, 256, 32, M>(a, bwd, ctas, st);
   }
   if (!bwd) return launch_pdl(k_ln_fwd_long<T>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
   return launch_pdl(k_ln_bwd_long<T>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
@@ -467,41 +552,45 @@ cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
 }  // namespace
 
 bool ln_clears(const LnArgs& a) { return a.slots <= kCheckSlots; }
+// Values that a row's pieces of 16 bytes hold: of bf16 rows that are not whole pieces more than d, as far from a boundary as they begin.
+int ln_span(int d, bool f32) { return d + (f32 || d % 8 == 0 ? 0 : d % 4 == 0 ? 4 : d % 2 == 0 ? 6 : 7); }
 // Threads of a row: 8 values each up to 256 columns, 16 up to 4096, 32 up to 8192; 0: a CTA in passes.
-int ln_group(int d) {
-  if (d <= 64) return 8;
-  if (d <= 128) return 16;
-  if (d <= 512) return 32;
-  if (d <= 1024) return 64;
-  if (d <= 2048) return 128;
-  if (d <= 8192) return 256;
+int ln_group(int d, bool f32) {
+  const int n = ln_span(d, f32);
+  if (n <= 64) return 8;
+  if (n <= 128) return 16;
+  if (n <= 512) return 32;
+  if (n <= 1024) return 64;
+  if (n <= 2048) return 128;
+  if (n <= 8192) return 256;
   return 0;
 }
-int ln_ctas(int64_t rows, int d) {
-  const int g = ln_group(d), per = g ? kThreads / g : 1;
-  return (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * 2);
+int ln_ctas(int64_t rows, int d, bool f32) {
+  const int g = ln_group(d, f32), per = g ? kThreads / g : 1, alike = per < 8 ? 8 / per : 1;  // CTAs whose rows are a multiple of 8
+  const int64_t most = std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * 2);
+  return (int)((most + alike - 1) / alike * alike);
 }
-int ln_parts(int64_t rows, int d) { return ln_group(d) ? ln_ctas(rows, d) : (int)std::min<int64_t>(rows, 16); }
+int ln_parts(int64_t rows, int d, bool f32) { return ln_group(d, f32) ? ln_ctas(rows, d, f32) : (int)std::min<int64_t>(rows, 16); }
 
 cudaError_t launch_ln(LnArgs a, bool f32, bool bwd, cudaStream_t st) {
   a.first = a.slots > 0 && a.slots <= kCheckSlots;
   const size_t es = f32 ? 4 : 2;
-  uintptr_t bits = (uintptr_t)(a.d * es) | (uintptr_t)(a.ldx * es);
-  for (const void* q : {a.x, a.res, a.w, a.b, (const void*)a.sum, (const void*)a.y, a.dy, a.ds, (const void*)a.dx})
-    bits |= reinterpret_cast<uintptr_t>(q);
-  const bool wide = bits % 16 == 0;
-  const int ctas = ln_ctas(a.rows, a.d);
-  if (f32) return wide ? pick<float, true>(a, bwd, ctas, st) : pick<float, false>(a, bwd, ctas, st);
-  return wide ? pick<bf16, true>(a, bwd, ctas, st) : pick<bf16, false>(a, bwd, ctas, st);
+  uintptr_t rows = 0;  // where the rows' tensors begin
+  for (const void* q : {a.x, a.res, (const void*)a.sum, (const void*)a.y, a.dy, a.ds, (const void*)a.dx}) rows |= reinterpret_cast<uintptr_t>(q);
+  const uintptr_t all = rows | reinterpret_cast<uintptr_t>(a.w) | reinterpret_cast<uintptr_t>(a.b) | (uintptr_t)(a.d * es) | (uintptr_t)(a.ldx * es);
+  const int ctas = ln_ctas(a.rows, a.d, f32);
+  if (f32) return all % 16 == 0 ? pick<float, PIECES>(a, bwd, ctas, st) : pick<float, SINGLE>(a, bwd, ctas, st);
+  if (all % 16 == 0) return pick<bf16, PIECES>(a, bwd, ctas, st);
+  return rows % 16 == 0 && (a.ldx - a.d) % 8 == 0 ? pick<bf16, SHIFTED>(a, bwd, ctas, st) : pick<bf16, SINGLE>(a, bwd, ctas, st);
 }
 cudaError_t launch_ln_cols_long(const LnArgs& a, bool f32, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.d + kThreads - 1) / kThreads), (unsigned)ln_parts(a.rows, a.d));
+  const dim3 grid((unsigned)((a.d + kThreads - 1) / kThreads), (unsigned)ln_parts(a.rows, a.d, f32));
   return f32 ? launch_pdl(k_ln_cols_long<float>, grid, dim3(kThreads), 0, st, a)
              : launch_pdl(k_ln_cols_long<bf16>, grid, dim3(kThreads), 0, st, a);
 }
-cudaError_t launch_ln_cols(const LnArgs& a, float* dw, float* db, cudaStream_t st) {
+cudaError_t launch_ln_cols(const LnArgs& a, bool f32, float* dw, float* db, cudaStream_t st) {
   return launch_pdl(k_ln_cols, dim3((unsigned)((2 * (int64_t)a.d + 31) / 32)), dim3(1024), 0, st, (const float*)a.part,
-                    ln_parts(a.rows, a.d), a.d, dw, db);
+                    ln_parts(a.rows, a.d, f32), a.d, dw, db);
 }
 
 }  // namespace gbla
