@@ -1444,7 +1444,7 @@ gbla_status layer_norm_backward(const gbla_shape* shape, const void* x, int64_t 
   if (!ln_clears(a)) GBLA_CHECK(launch_zero(a.err, 16, c.st), "clear");
   GBLA_CHECK(launch_ln(a, p.f32, true, c.st), "layer norm bwd");
   if (!a.part) return GBLA_OK;
-  if (!ln_group(p.d, p.f32)) GBLA_CHECK(launch_ln_cols_long(a, p.f32, c.st), "layer norm cols");
+  if (!ln_group(p.d, p.f32, true).threads) GBLA_CHECK(launch_ln_cols_long(a, p.f32, c.st), "layer norm cols");
   GBLA_CHECK(launch_ln_cols(a, p.f32, dw, db, c.st), "layer norm dw");
   return GBLA_OK;
 }

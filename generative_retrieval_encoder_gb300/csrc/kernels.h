@@ -323,12 +323,12 @@ struct LnArgs {
   int* err;                           // the error word, 0 on entry (but where ln_clears)
 };
 bool ln_clears(const LnArgs& a);      // whether launch_ln clears the error word itself
-int ln_span(int d, bool f32);
-int ln_group(int d, bool f32);
+struct LnGroup { int threads, values; };
+LnGroup ln_group(int d, bool f32, bool bwd);
 int ln_ctas(int64_t rows, int d, bool f32);
-int ln_parts(int64_t rows, int d, bool f32);    // partial rows of the gradients of w and b
+int ln_parts(int64_t rows, int d, bool f32);  // partial rows of the gradients of w and b
 cudaError_t launch_ln(LnArgs a, bool f32, bool bwd, cudaStream_t st);
-// Rows that no group of threads holds (ln_group = 0): their partial column sums, by a kernel of their own.
+// Rows that no group of threads holds (ln_group: 0): their partial column sums, by a kernel of their own.
 cudaError_t launch_ln_cols_long(const LnArgs& a, bool f32, cudaStream_t st);
 // dw, db (either may be null) from the partial rows.
 cudaError_t launch_ln_cols(const LnArgs& a, bool f32, float* dw, float* db, cudaStream_t st);

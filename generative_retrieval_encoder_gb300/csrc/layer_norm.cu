@@ -178,8 +178,8 @@ __device__ __forceinline__ void store_row(T* p, int t, int d, int off, F&& f) {
   }
 }
 
-// The sums of M values over the G threads of a row, in a fixed order, in every thread.  Rows of more than a warp meet at two CTA
-// barriers; `red` [kThreads / 32][M].
+// The sums of M values over the G threads of a row, in a fixed order, in every thread.  Rows of more than a warp meet at a barrier of
+// their own; `red` [kThreads / 32][M], another one than the last time.
 template <int G, int M>
 __device__ __forceinline__ void group_sum(float (&v)[M], float (*red)[M]) {
 #pragma unroll
@@ -192,7 +192,7 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*red)[M]) {
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
       for (int m = 0; m < M; ++m) red[warp][m] = v[m];
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / G), "n"(G) : "memory");
     const int w0 = warp / W * W;
 #pragma unroll
     for (int m = 0; m < M; ++m) v[m] = red[w0][m];
@@ -200,7 +200,6 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*red)[M]) {
     for (int w = 1; w < W; ++w)
 #pragma unroll
       for (int m = 0; m < M; ++m) v[m] += red[w0 + w][m];
-    __syncthreads();
   }
 }
 
@@ -208,9 +207,9 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*red)[M]) {
 // an SM ask for enough at a time, which rows unpacked to fp32 as they are loaded, in three CTAs, did not: 122 us).  One token of 16
 // sequences takes 2 us, a launch.
 template <typename T, int G, int N, LnRows M>
-__global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE ? 3 : N * sizeof(T) <= 32 && M == PIECES ? 5 : 4) k_ln_fwd(const LnArgs a) {
+__global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE || (N == 24 && M == SHIFTED) ? 3 : N * sizeof(T) <= 32 && M == PIECES ? 5 : 4) k_ln_fwd(const LnArgs a) {
   pdl_enter();
-  __shared__ float red[kThreads / 32][1];
+  __shared__ float red[2][kThreads / 32][1];
   using R = Row<T, G, N, M>;
   const int t = threadIdx.x % G;
   const float inv = 1.f / (float)a.d;
@@ -241,14 +240,14 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE ? 3 : N * 
     float m[1] = {0.f}, v[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) m[0] += s[i];
-    group_sum<G, 1>(m, red);
+    group_sum<G, 1>(m, red[0]);
     const float mean = m[0] * inv;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float c = s[i] - mean;
       v[0] += (unsigned)col_of<T, G, M>(i, t, off) < (unsigned)a.d ? c * c : 0.f;
     }
-    group_sum<G, 1>(v, red);
+    group_sum<G, 1>(v, red[1]);
     if (in) {
       const float r = live ? 1.f / sqrtf(v[0] * inv + a.eps) : 0.f;
       if (M != SHIFTED) {
@@ -277,7 +276,7 @@ constexpr int kAhead = M == SINGLE || N == 32 ? 0 : 2;
 template <typename T, int G, int N, LnRows M>
 __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_bwd(const LnArgs a) {
   pdl_enter();
-  __shared__ float red[kThreads / 32][2];
+  __shared__ float red[2][kThreads / 32][2];
   extern __shared__ __align__(16) unsigned char dyn[];
   float* acc = reinterpret_cast<float*>(dyn);  // at the end: [R][G N], the groups' column sums, where the CTA has several
   uint4* ring = reinterpret_cast<uint4*>(dyn) + threadIdx.x;  // [kAhead][3 (N / E)][kThreads]
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
 #pragma unroll
     for (int k = 0; k < A; ++k) ask(cta * R + grp + k * step, k);
   }
-  int slot = 0;
+  int slot = 0, turn = 0;
   for (int64_t r0 = cta * R; r0 < a.rows; r0 += step) {  // (as often in every thread of the CTA)
     const int64_t row = r0 + grp;
     const bool in = row < a.rows, live = in && row_valid(a, row);
@@ -343,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
       c[0] += g;
       c[1] += g * z;
     }
-    group_sum<G, 2>(c, red);
+    group_sum<G, 2>(c, red[turn]);
+    turn ^= 1;
     const float c0 = c[0] * inv, c1 = c[1] * inv;
     if (in)
       store_row<T, G, N, M>(static_cast<T*>(a.dx) + row * a.d, t, a.d, off, [&](int i) {
@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(1024) k_ln_cols(const float* part, int n, int 
   }
 }
 
+template <int V> struct Int { static constexpr int value = V; };
 // CTAs of `per` rows at a time.  Shifted rows: the scale and the bias, which are read value by value, once for four rows of a group, which
 // begin alike, where four CTAs an SM are left.
 int64_t ln_fwd_ctas(int64_t rows, int per, bool shifted) {
@@ -524,8 +525,12 @@ int64_t ln_fwd_ctas(int64_t rows, int per, bool shifted) {
   return !shifted || all < sm_count() * 16 ? all : ((all + 3) / 4 + alike - 1) / alike * alike;
 }
 template <typename T, int G, int N, LnRows M>
-cudaError_t run(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
-  if (!bwd) return launch_pdl(k_ln_fwd<T, G, N, M>, dim3((unsigned)(ln_fwd_ctas(a.rows, kThreads / G, M == SHIFTED) + a.first)), dim3(kThreads), 0, st, a);
+cudaError_t run_fwd(const LnArgs& a, cudaStream_t st) {
+  const unsigned ctas = (unsigned)(ln_fwd_ctas(a.rows, kThreads / G, M == SHIFTED) + a.first);
+  return launch_pdl(k_ln_fwd<T, G, N, M>, dim3(ctas), dim3(kThreads), 0, st, a);
+}
+template <typename T, int G, int N, LnRows M>
+cudaError_t run_bwd(const LnArgs& a, int ctas, cudaStream_t st) {
   const size_t ring = (size_t)kAhead<T, N, M> * 3 * N * sizeof(T) * kThreads;
   const size_t smem = std::max(ring, a.part && kThreads / G > 1 ? (size_t)kThreads * N * 4 : 0);
   if (smem > 32 << 10) {
@@ -536,15 +541,23 @@ cudaError_t run(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
 }
 template <typename T, LnRows M>
 cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
-  const int span = ln_span(a.d, sizeof(T) == 4);
-  switch (ln_group(a.d, sizeof(T) == 4)) {
-    case 8: return run<T, 8, 8, M>(a, bwd, ctas, st);
-    case 16: return run<T, 16, 8, M>(a, bwd, ctas, st);
-    case 32: return span <= 256 ? run<T, 32, 8, M>(a, bwd, ctas, st) : run<T, 32, 16, M>(a, bwd, ctas, st);
-    case 64: return run<T, 64, 16, M>(a, bwd, ctas, st);
-    case 128: return run<T, 128, 16, M>(a, bwd, ctas, st);
-    case 256: return span <= 4096 ? run<T, 256, 16, M>(a, bwd, ctas, st) : run<T, 256, 32, M>(a, bwd, ctas, st);
+  const LnGroup g = ln_group(a.d, sizeof(T) == 4, bwd);
+  auto is = [&](auto G, auto N) { return g.threads == G.value && g.values == N.value; };
+  cudaError_t e = cudaErrorNotSupported;
+  auto go = [&](auto G, auto N) {
+    if (is(G, N)) e = bwd ? run_bwd<T, G.value, N.value, M>(a, ctas, st) : run_fwd<T, G.value, N.value, M>(a, st);
+  };
+  auto all = [&](auto N, auto... G) { (go(G, N), ...); };
+  if constexpr (sizeof(T) == 4) {
+    all(Int<8>{}, Int<8>{}, Int<16>{}, Int<32>{});
+    all(Int<16>{}, Int<32>{}, Int<64>{}, Int<128>{}, Int<256>{});
+  } else {
+    all(Int<8>{}, Int<4>{});
+    all(Int<16>{}, Int<4>{}, Int<8>{}, Int<16>{}, Int<32>{}, Int<64>{}, Int<128>{}, Int<256>{});
+    all(Int<24>{}, Int<4>{}, Int<8>{}, Int<16>{}, Int<32>{}, Int<64>{}, Int<128>{}, Int<256>{});
   }
+  go(Int<256>{}, Int<32>{});
+  if (g.threads) return e;
   if (!bwd) return launch_pdl(k_ln_fwd_long<T>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
   return launch_pdl(k_ln_bwd_long<T>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
 }
@@ -552,25 +565,28 @@ cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
 }  // namespace
 
 bool ln_clears(const LnArgs& a) { return a.slots <= kCheckSlots; }
-// Values that a row's pieces of 16 bytes hold: of bf16 rows that are not whole pieces more than d, as far from a boundary as they begin.
-int ln_span(int d, bool f32) { return d + (f32 || d % 8 == 0 ? 0 : d % 4 == 0 ? 4 : d % 2 == 0 ? 6 : 7); }
-// Threads of a row: 8 values each up to 256 columns, 16 up to 4096, 32 up to 8192; 0: a CTA in passes.
-int ln_group(int d, bool f32) {
-  const int n = ln_span(d, f32);
-  if (n <= 64) return 8;
-  if (n <= 128) return 16;
-  if (n <= 512) return 32;
-  if (n <= 1024) return 64;
-  if (n <= 2048) return 128;
-  if (n <= 8192) return 256;
-  return 0;
+// Threads of a row and values of each; 0: a CTA in passes.  FIGURES
+LnGroup ln_group(int d, bool f32, bool bwd) {
+  if (f32) {
+    for (int g = 8; g <= 32; g *= 2)
+      if (d <= 8 * g) return {g, 8};
+    for (int g = 32; g <= 256; g *= 2)
+      if (d <= 16 * g) return {g, 16};
+  } else {
+    d += d % 8 == 0 ? 0 : d % 4 == 0 ? 4 : d % 2 == 0 ? 6 : 7;  // rows that are not whole pieces may begin so far behind a boundary
+    if (d <= 32) return {4, 8};
+    for (int g = 4; g <= 256; g *= 2)
+      for (int n = 16; n <= (bwd ? 16 : 24); n += 8)
+        if (d <= n * g) return {g, n};
+  }
+  return d <= 8192 ? LnGroup{256, 32} : LnGroup{0, 0};
 }
 int ln_ctas(int64_t rows, int d, bool f32) {
-  const int g = ln_group(d, f32), per = g ? kThreads / g : 1, alike = per < 8 ? 8 / per : 1;  // CTAs whose rows are a multiple of 8
+  const int g = ln_group(d, f32, true).threads, per = g ? kThreads / g : 1, alike = per < 8 ? 8 / per : 1;  // CTAs whose rows are a multiple of 8
   const int64_t most = std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * 2);
   return (int)((most + alike - 1) / alike * alike);
 }
-int ln_parts(int64_t rows, int d, bool f32) { return ln_group(d, f32) ? ln_ctas(rows, d, f32) : (int)std::min<int64_t>(rows, 16); }
+int ln_parts(int64_t rows, int d, bool f32) { return ln_group(d, f32, true).threads ? ln_ctas(rows, d, f32) : (int)std::min<int64_t>(rows, 16); }
 
 cudaError_t launch_ln(LnArgs a, bool f32, bool bwd, cudaStream_t st) {
   a.first = a.slots > 0 && a.slots <= kCheckSlots;
