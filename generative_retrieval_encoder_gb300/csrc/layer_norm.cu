@@ -138,15 +138,24 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < (WIDE ? 1 : N); ++i) v[i] = 0.f;
   }
-  __device__ __forceinline__ float get(int i) const {
-    if (!WIDE) return v[WIDE ? 0 : i];
-    const uint4& q = w[WIDE ? i / E : 0];
+  __device__ __forceinline__ void ones() {
+    const uint32_t o = sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
+#pragma unroll
+    for (int i = 0; i < (WIDE ? N / E : 1); ++i) w[i] = make_uint4(o, o, o, o);
+#pragma unroll
+    for (int i = 0; i < (WIDE ? 1 : N); ++i) v[i] = 1.f;
+  }
+  // Values 2 k and 2 k + 1.
+  __device__ __forceinline__ float2 get(int k) const {
+    if (!WIDE) return make_float2(v[WIDE ? 0 : 2 * k], v[WIDE ? 0 : 2 * k + 1]);
+    const uint4& q = w[WIDE ? 2 * k / E : 0];
     const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-    if (sizeof(T) == 2) return i & 1 ? bf_hi(u[(i % E) / 2]) : bf_lo(u[(i % E) / 2]);
-    return __uint_as_float(u[i & 3]);
+    if (sizeof(T) == 2) return make_float2(bf_lo(u[k & 3]), bf_hi(u[k & 3]));
+    return make_float2(__uint_as_float(u[2 * k & 3]), __uint_as_float(u[(2 * k + 1) & 3]));
   }
 };
-// Stores the values f(0) .. f(N - 1) of the thread.
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+// Stores the values of the thread, f(k) the pair 2 k, 2 k + 1.
 template <typename T, int G, int N, LnRows M, typename F>
 __device__ __forceinline__ void store_row(T* p, int t, int d, int off, F&& f) {
   constexpr int E = 16 / sizeof(T);
@@ -156,7 +165,11 @@ __device__ __forceinline__ void store_row(T* p, int t, int d, int off, F&& f) {
       const int c = col_of<T, G, M>(i, t, off);
       uint32_t u[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) u[k] = sizeof(T) == 2 ? pack_bf16(f(i + 2 * k), f(i + 2 * k + 1)) : __float_as_uint(f(i + k));
+      for (int k = 0; k < E / 2; ++k) {
+        const float2 q = f(i / 2 + k);
+        if (sizeof(T) == 2) u[k & 3] = pack_bf16(q.x, q.y);
+        else u[2 * k & 3] = __float_as_uint(q.x), u[(2 * k + 1) & 3] = __float_as_uint(q.y);
+      }
       if (M == SHIFTED && (c < 0 || c + E > d)) {  // an end of the row, or outside
         if (d % 2 == 0) {
 #pragma unroll
@@ -173,8 +186,11 @@ __device__ __forceinline__ void store_row(T* p, int t, int d, int off, F&& f) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i * G + t < d) p[i * G + t] = from_f<T>(f(i));
+    for (int i = 0; i < N; i += 2) {
+      const float2 q = f(i / 2);
+      if (i * G + t < d) p[i * G + t] = from_f<T>(q.x);
+      if ((i + 1) * G + t < d) p[(i + 1) * G + t] = from_f<T>(q.y);
+    }
   }
 }
 
@@ -192,7 +208,13 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*red)[M]) {
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
       for (int m = 0; m < M; ++m) red[warp][m] = v[m];
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / G), "n"(G) : "memory");
+    // (its number written out: a register's counts as all 16, of which an SM has few)
+    const int own = threadIdx.x / G;
+    if (G == kThreads) __syncthreads();
+    else if (own == 0) asm volatile("bar.sync 1, %0;" ::"n"(G) : "memory");
+    else if (own == 1) asm volatile("bar.sync 2, %0;" ::"n"(G) : "memory");
+    else if (own == 2) asm volatile("bar.sync 3, %0;" ::"n"(G) : "memory");
+    else asm volatile("bar.sync 4, %0;" ::"n"(G) : "memory");
     const int w0 = warp / W * W;
 #pragma unroll
     for (int m = 0; m < M; ++m) v[m] = red[w0][m];
@@ -217,14 +239,17 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE || (N == 2
   const int64_t r00 = (int64_t)(blockIdx.x - a.first) * (kThreads / G), step = (int64_t)(gridDim.x - a.first) * (kThreads / G);
   const int off = row_off<T, M>(r00 + threadIdx.x / G, a.d);
   R w, b;
-  if (M == SHIFTED) {
+  auto affine = [&] {
     if (a.w) w.load_vec(static_cast<const T*>(a.w), t, a.d, off);
+    else w.ones();
     if (a.b) b.load_vec(static_cast<const T*>(a.b), t, a.d, off);
-  }
+    else b.clear();
+  };
+  if (M == SHIFTED) affine();
   for (int64_t r0 = r00; r0 < a.rows; r0 += step) {  // (as often in every thread of the CTA)
     const int64_t row = r0 + threadIdx.x / G, behind = (a.rows - 1 - row) * a.d;
     const bool in = row < a.rows, live = in && row_valid(a, row);
-    float s[N];
+    float2 s[N / 2];  // two values at a time
     {
       R x, q;
       x.clear();
@@ -234,31 +259,41 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE || (N == 2
         if (a.res) q.load(static_cast<const T*>(a.res) + row * a.d, t, a.d, off, behind);
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) s[i] = a.res ? to_f(from_f<T>(x.get(i) + q.get(i))) : x.get(i);
+      for (int k = 0; k < N / 2; ++k) {
+        s[k] = x.get(k);
+        if (!a.res) continue;
+        s[k] = __fadd2_rn(s[k], q.get(k));
+        if (sizeof(T) == 2) {
+          const uint32_t u = pack_bf16(s[k].x, s[k].y);
+          s[k] = make_float2(bf_lo(u), bf_hi(u));
+        }
+      }
     }
-    if (in && a.sum) store_row<T, G, N, M>(static_cast<T*>(a.sum) + row * a.d, t, a.d, off, [&](int i) { return s[i]; });
-    float m[1] = {0.f}, v[1] = {0.f};
+    if (in && a.sum) store_row<T, G, N, M>(static_cast<T*>(a.sum) + row * a.d, t, a.d, off, [&](int k) { return s[k]; });
+    float2 q = two(0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) m[0] += s[i];
+    for (int k = 0; k < N / 2; ++k) q = __fadd2_rn(q, s[k]);
+    float m[1] = {q.x + q.y}, v[1];
     group_sum<G, 1>(m, red[0]);
     const float mean = m[0] * inv;
+    q = two(0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float c = s[i] - mean;
-      v[0] += (unsigned)col_of<T, G, M>(i, t, off) < (unsigned)a.d ? c * c : 0.f;
+    for (int k = 0; k < N / 2; ++k) {
+      s[k] = __fadd2_rn(s[k], two(-mean));
+      // (pieces are of one row or of none)
+      const int c0 = col_of<T, G, M>(M == PIECES ? 2 * k / R::E * R::E : 2 * k, t, off), c1 = M == PIECES ? c0 : col_of<T, G, M>(2 * k + 1, t, off);
+      if ((unsigned)c0 >= (unsigned)a.d) s[k].x = 0.f;
+      if ((unsigned)c1 >= (unsigned)a.d) s[k].y = 0.f;
+      q = __ffma2_rn(s[k], s[k], q);
     }
+    v[0] = q.x + q.y;
     group_sum<G, 1>(v, red[1]);
     if (in) {
       const float r = live ? 1.f / sqrtf(v[0] * inv + a.eps) : 0.f;
-      if (M != SHIFTED) {
-        if (a.w) w.load_vec(static_cast<const T*>(a.w), t, a.d, off);
-        if (a.b) b.load_vec(static_cast<const T*>(a.b), t, a.d, off);
-      }
-      store_row<T, G, N, M>(static_cast<T*>(a.y) + row * a.d, t, a.d, off, [&](int i) {
-        float z = (s[i] - mean) * r;
-        if (a.w) z *= w.get(i);
-        if (a.b) z += b.get(i);
-        return live ? z : 0.f;
+      if (M != SHIFTED) affine();
+      store_row<T, G, N, M>(static_cast<T*>(a.y) + row * a.d, t, a.d, off, [&](int k) {
+        const float2 y = __ffma2_rn(__fmul2_rn(s[k], two(r)), w.get(k), b.get(k));
+        return live ? y : two(0.f);
       });
       if (a.stats && t == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(live ? mean : 0.f, r);
     }
@@ -271,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE || (N == 2
 // bf16 in 89 us, 0.89 of a copy's rate (107 by registers alone, 90 with three rows ahead; 64 threads a row, 8 values each in three CTAs,
 // 115: the sums of a row then meet at CTA barriers).
 template <typename T, int N, LnRows M>
-constexpr int kAhead = M == SINGLE || N == 32 ? 0 : 2;
+constexpr int kAhead = M == SINGLE ? 0 : 2;
 
 template <typename T, int G, int N, LnRows M>
 __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_bwd(const LnArgs a) {
@@ -287,13 +322,18 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
   if (check_slots(a)) return;
   const int64_t cta = blockIdx.x - a.first, ctas = gridDim.x - a.first;
   Mine w, x, y, s;
-  float dw[N], db[N];
+  float2 dw[N / 2], db[N / 2];  // two values at a time
 #pragma unroll
-  for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.f;
+  for (int k = 0; k < N / 2; ++k) dw[k] = db[k] = two(0.f);
   const int64_t step = ctas * R;  // a multiple of the values of a piece (ln_ctas): a group's rows all begin alike
   const int off = row_off<T, M>(cta * R + grp, a.d);
   if (a.w) w.load_vec(static_cast<const T*>(a.w), t, a.d, off);
+  else w.ones();
   s.clear();
+  auto stats = [&](int64_t row) {
+    return row < a.rows ? reinterpret_cast<const float2*>(a.stats)[row] : make_float2(0.f, 0.f);
+  };
+  float2 next = stats(cta * R + grp);
   auto ask = [&](int64_t row, int slot) {
     if (row < a.rows && row_valid(a, row)) {
       uint4* to = ring + slot * 3 * P * kThreads;
@@ -311,10 +351,10 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
   for (int64_t r0 = cta * R; r0 < a.rows; r0 += step) {  // (as often in every thread of the CTA)
     const int64_t row = r0 + grp;
     const bool in = row < a.rows, live = in && row_valid(a, row);
-    float mean = 0.f, r = 0.f;
+    const float2 st = live ? next : make_float2(0.f, 0.f);
+    next = stats(row + step);
     if (A > 0) cp_async_wait<(A > 0 ? A - 1 : 0)>();
     if (live) {
-      const float2 st = reinterpret_cast<const float2*>(a.stats)[row];
       if (A > 0) {
         const uint4* from = ring + slot * 3 * P * kThreads;
         x.take(from, t, a.d, off);
@@ -326,30 +366,30 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
         y.load(static_cast<const T*>(a.dy) + row * a.d, t, a.d, off, behind);
         if (a.ds) s.load(static_cast<const T*>(a.ds) + row * a.d, t, a.d, off, behind);
       }
-      mean = st.x;
-      r = st.y;
     } else {
       x.clear();
       y.clear();
       s.clear();
     }
-    float c[2] = {0.f, 0.f};
+    const float2 mean = two(-st.x), r = two(st.y);
+    float2 c0 = two(0.f), c1 = two(0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float z = (x.get(i) - mean) * r, q = y.get(i), g = a.w ? q * w.get(i) : q;  // outside the row: dy is 0 there
-      dw[i] += q * z;
-      db[i] += q;
-      c[0] += g;
-      c[1] += g * z;
+    for (int k = 0; k < N / 2; ++k) {  // outside the row: dy is 0 there
+      const float2 z = __fmul2_rn(__fadd2_rn(x.get(k), mean), r), q = y.get(k), g = __fmul2_rn(q, w.get(k));
+      dw[k] = __ffma2_rn(q, z, dw[k]);
+      db[k] = __fadd2_rn(db[k], q);
+      c0 = __fadd2_rn(c0, g);
+      c1 = __ffma2_rn(g, z, c1);
     }
+    float c[2] = {c0.x + c0.y, c1.x + c1.y};
     group_sum<G, 2>(c, red[turn]);
     turn ^= 1;
-    const float c0 = c[0] * inv, c1 = c[1] * inv;
+    c0 = two(-c[0] * inv);
+    c1 = two(-c[1] * inv);
     if (in)
-      store_row<T, G, N, M>(static_cast<T*>(a.dx) + row * a.d, t, a.d, off, [&](int i) {
-        const float z = (x.get(i) - mean) * r, q = y.get(i);
-        const float g = r * ((a.w ? q * w.get(i) : q) - c0 - z * c1);
-        return a.ds ? g + s.get(i) : g;
+      store_row<T, G, N, M>(static_cast<T*>(a.dx) + row * a.d, t, a.d, off, [&](int k) {
+        const float2 z = __fmul2_rn(__fadd2_rn(x.get(k), mean), r), g = __fmul2_rn(y.get(k), w.get(k));
+        return __ffma2_rn(__ffma2_rn(z, c1, __fadd2_rn(g, c0)), r, s.get(k));
       });
     if (A > 0) {  // into the places whose values are used by now
       ask(row + A * step, slot);
@@ -366,14 +406,16 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = col_of<T, G, M>(i, t, off);
-        if ((unsigned)c < (unsigned)a.d) out[which * a.d + c] = which ? db[i] : dw[i];
+        const float2 q = which ? db[i / 2] : dw[i / 2];
+        if ((unsigned)c < (unsigned)a.d) out[which * a.d + c] = i & 1 ? q.y : q.x;
       }
     } else {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = col_of<T, G, M>(i, t, off);
-        if (c >= 0) acc[grp * (G * N) + c] = which ? db[i] : dw[i];
+        const float2 q = which ? db[i / 2] : dw[i / 2];
+        if (c >= 0) acc[grp * (G * N) + c] = i & 1 ? q.y : q.x;
       }
       __syncthreads();
       for (int c = threadIdx.x; c < a.d; c += kThreads) {
