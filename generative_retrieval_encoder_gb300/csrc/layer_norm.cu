@@ -7,6 +7,8 @@
 // A group of G threads holds a row, N values each, so mean and squares are taken
 // from registers (the squares about the mean itself: no cancellation) and every
 // tensor is read once.  Rows longer than 8192 values go by CTA in passes over L2.
+// Additions and products are of two values at a time: bf16 rows are otherwise bound
+// by instructions (backward 91 us against 80 at 16 x 8192 rows of 512).
 #include <algorithm>
 
 #include "common.cuh"
@@ -69,12 +71,6 @@ struct Row {
   static constexpr bool WIDE = M != SINGLE;
   uint4 w[WIDE ? N / E : 1];
   float v[WIDE ? 1 : N];
-  // Zeros in place of a piece's values outside [0, d); c: the column of the first (SHIFTED: of 16-bit values).
-  __device__ static __forceinline__ uint4 masked(uint4 q, int c, int d) {
-    const uint32_t ok = (c < 0 ? 0xffu << -c : 0xffu) & (c + E > d ? (1u << (d - c)) - 1 : 0xffu);
-    auto keep = [&](uint32_t v, int j) { return v & ((ok >> 2 * j & 1 ? 0xffffu : 0u) | (ok >> (2 * j + 1) & 1 ? 0xffff0000u : 0u)); };
-    return make_uint4(keep(q.x, 0), keep(q.y, 1), keep(q.z, 2), keep(q.w, 3));
-  }
   // The piece's values one by one, or by pairs.
   __device__ static __forceinline__ uint4 singles(const T* p, int c, int d) {
     uint32_t u[4] = {0, 0, 0, 0};
@@ -89,19 +85,12 @@ struct Row {
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
-  // SHIFTED: `behind` values of the tensor lie behind the row at least.
-  __device__ __forceinline__ void load(const T* p, int t, int d, int off, int64_t behind) {
+  __device__ __forceinline__ void load(const T* p, int t, int d) {  // (SHIFTED rows come by way of shared memory)
     if (WIDE) {
 #pragma unroll
       for (int i = 0; i < N / E; ++i) {
-        const int c = (i * G + t) * E - off;
-        const bool some = c > -E && c < d;
-        if (M == SHIFTED && some && c + E > d && behind < E) {
-          w[i] = singles(p, c, d);
-          continue;
-        }
-        w[i] = some ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
-        if (M == SHIFTED && some && (c < 0 || c + E > d)) w[i] = masked(w[i], c, d);
+        const int c = (i * G + t) * E;
+        w[i] = c < d ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
       }
     } else {
 #pragma unroll
@@ -111,7 +100,7 @@ struct Row {
   // Of a vector of d values that itself begins anywhere (w, b).
   __device__ __forceinline__ void load_vec(const T* p, int t, int d, int off) {
     if (M != SHIFTED) {
-      load(p, t, d, 0, 0);
+      load(p, t, d);
     } else {
 #pragma unroll
       for (int i = 0; i < N / E; ++i) w[WIDE ? i : 0] = singles(p, (i * G + t) * E - off, d);
@@ -127,10 +116,13 @@ struct Row {
       cp_async16(smem_u32(mine + i * kThreads), p + (some ? c : -off), !some ? 0 : M == SHIFTED ? min(E, d - c) * (int)sizeof(T) : 16);
     }
   }
-  __device__ __forceinline__ void take(const uint4* mine, int t, int d, int off) {
+  __device__ __forceinline__ void take(const uint4* mine, int t, int off) {
 #pragma unroll
     for (int i = 0; i < N / E; ++i) w[WIDE ? i : 0] = mine[i * kThreads];
-    if (M == SHIFTED && t == 0 && off) w[0] = masked(w[0], -off, d);  // (the row before's)
+    if (M == SHIFTED && t == 0 && off) {  // the row before's
+      auto keep = [&](uint32_t v, int k) { return v & ((2 * k >= off ? 0xffffu : 0u) | (2 * k + 1 >= off ? 0xffff0000u : 0u)); };
+      w[0] = make_uint4(keep(w[0].x, 0), keep(w[0].y, 1), keep(w[0].z, 2), keep(w[0].w, 3));
+    }
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -225,11 +217,17 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*red)[M]) {
   }
 }
 
-// A row a group and no loop: bound by memory (two rows in, two out, 16 x 8192 rows of 512 bf16 in 80 us, 0.99 of a copy's rate; 5 CTAs
-// an SM ask for enough at a time, which rows unpacked to fp32 as they are loaded, in three CTAs, did not: 122 us).  One token of 16
-// sequences takes 2 us, a launch.
+// The forward's CTAs an SM, and the rows that those of SHIFTED rows ask for ahead.
+template <typename T, int N, LnRows M>
+constexpr int kLnFwdCtas = N == 32 || (N == 24 && M == SHIFTED) ? 2 : M != PIECES ? 3 : N * sizeof(T) <= 32 ? 5 : 4;
+constexpr int kLnFwdAhead = 2;
+
+// A row a group and no loop: bound by memory (two rows in, two out, 16 x 8192 rows of 512 bf16 in 78 us, the rate of a copy; 5 CTAs an SM
+// ask for enough at a time, which rows unpacked to fp32 as they are loaded, in three CTAs, did not: 122 us).  One token of 16 sequences
+// takes 2 us, a launch.  SHIFTED rows in a loop, with w and b read once for a group: 65536 of 500 bf16 in 46 us, 0.84 of a copy's rate,
+// of 511 in 61 (value by value 135).
 template <typename T, int G, int N, LnRows M>
-__global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE || (N == 24 && M == SHIFTED) ? 3 : N * sizeof(T) <= 32 && M == PIECES ? 5 : 4) k_ln_fwd(const LnArgs a) {
+__global__ void __launch_bounds__(kThreads, kLnFwdCtas<T, N, M>) k_ln_fwd(const LnArgs a) {
   pdl_enter();
   __shared__ float red[2][kThreads / 32][1];
   using R = Row<T, G, N, M>;
@@ -245,18 +243,42 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE || (N == 2
     if (a.b) b.load_vec(static_cast<const T*>(a.b), t, a.d, off);
     else b.clear();
   };
-  if (M == SHIFTED) affine();
+  constexpr int A = kLnFwdAhead, P = N * (int)sizeof(T) / 16;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  uint4* ring = reinterpret_cast<uint4*>(dyn) + threadIdx.x;  // SHIFTED: [A][2 P][kThreads]
+  auto ask = [&](int64_t row, int slot) {
+    if (row < a.rows && row_valid(a, row)) {
+      uint4* to = ring + slot * 2 * P * kThreads;
+      R::ask(to, static_cast<const T*>(a.x) + row * a.ldx, t, a.d, off);
+      if (a.res) R::ask(to + P * kThreads, static_cast<const T*>(a.res) + row * a.d, t, a.d, off);
+    }
+    cp_async_commit();
+  };
+  if (M == SHIFTED) {
+#pragma unroll
+    for (int k = 0; k < A; ++k) ask(r00 + threadIdx.x / G + k * step, k);
+    affine();
+  }
+  int slot = 0;
   for (int64_t r0 = r00; r0 < a.rows; r0 += step) {  // (as often in every thread of the CTA)
-    const int64_t row = r0 + threadIdx.x / G, behind = (a.rows - 1 - row) * a.d;
+    const int64_t row = r0 + threadIdx.x / G;
     const bool in = row < a.rows, live = in && row_valid(a, row);
     float2 s[N / 2];  // two values at a time
     {
       R x, q;
       x.clear();
       q.clear();
-      if (live) {
-        x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d, off, behind);
-        if (a.res) q.load(static_cast<const T*>(a.res) + row * a.d, t, a.d, off, behind);
+      if (M == SHIFTED) {
+        cp_async_wait<A - 1>();
+        if (live) {
+          x.take(ring + slot * 2 * P * kThreads, t, off);
+          if (a.res) q.take(ring + (slot * 2 + 1) * P * kThreads, t, off);
+        }
+        ask(row + A * step, slot);
+        slot = slot + 1 == A ? 0 : slot + 1;
+      } else if (live) {
+        x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
+        if (a.res) q.load(static_cast<const T*>(a.res) + row * a.d, t, a.d);
       }
 #pragma unroll
       for (int k = 0; k < N / 2; ++k) {
@@ -299,12 +321,14 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 2 : M == SINGLE || (N == 2
     }
     if (M != SHIFTED) break;
   }
+  if (M == SHIFTED) cp_async_wait<0>();
 }
 
 // Rows that the backward asks for ahead: what is in flight covers the memory's latency with the two CTAs an SM that the column
-// sums' registers allow.  Bound by memory, and by what is in flight at the turns of a row: three rows in, one out, 16 x 8192 rows of 512
-// bf16 in 89 us, 0.89 of a copy's rate (107 by registers alone, 90 with three rows ahead; 64 threads a row, 8 values each in three CTAs,
-// 115: the sums of a row then meet at CTA barriers).
+// sums' registers allow.  Bound by memory: three rows in, one out, 16 x 8192 rows of 512 bf16 in 78 us, the rate of a copy (91 with the
+// statistics read when they are needed and one value at a time; before that, 107 by registers alone, 90 with three rows ahead).  Rows
+// of more than 2048 by the few that are at work at once, which wait for one another's sums: 4096 at 0.65, 5120 to 8192, in one CTA, at 0.57
+// (without rows ahead 0.45).
 template <typename T, int N, LnRows M>
 constexpr int kAhead = M == SINGLE ? 0 : 2;
 
@@ -357,14 +381,13 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
     if (live) {
       if (A > 0) {
         const uint4* from = ring + slot * 3 * P * kThreads;
-        x.take(from, t, a.d, off);
-        y.take(from + P * kThreads, t, a.d, off);
-        if (a.ds) s.take(from + 2 * P * kThreads, t, a.d, off);
+        x.take(from, t, off);
+        y.take(from + P * kThreads, t, off);
+        if (a.ds) s.take(from + 2 * P * kThreads, t, off);
       } else {
-        const int64_t behind = (a.rows - 1 - row) * a.d;
-        x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d, off, behind);
-        y.load(static_cast<const T*>(a.dy) + row * a.d, t, a.d, off, behind);
-        if (a.ds) s.load(static_cast<const T*>(a.ds) + row * a.d, t, a.d, off, behind);
+        x.load(static_cast<const T*>(a.x) + row * a.ldx, t, a.d);
+        y.load(static_cast<const T*>(a.dy) + row * a.d, t, a.d);
+        if (a.ds) s.load(static_cast<const T*>(a.ds) + row * a.d, t, a.d);
       }
     } else {
       x.clear();
@@ -560,16 +583,20 @@ __global__ void __launch_bounds__(1024) k_ln_cols(const float* part, int n, int 
 }
 
 template <int V> struct Int { static constexpr int value = V; };
-// CTAs of `per` rows at a time.  Shifted rows: the scale and the bias, which are read value by value, once for four rows of a group, which
-// begin alike, where four CTAs an SM are left.
-int64_t ln_fwd_ctas(int64_t rows, int per, bool shifted) {
-  const int64_t all = (rows + per - 1) / per, alike = per < 8 ? 8 / per : 1;
-  return !shifted || all < sm_count() * 16 ? all : ((all + 3) / 4 + alike - 1) / alike * alike;
-}
 template <typename T, int G, int N, LnRows M>
 cudaError_t run_fwd(const LnArgs& a, cudaStream_t st) {
-  const unsigned ctas = (unsigned)(ln_fwd_ctas(a.rows, kThreads / G, M == SHIFTED) + a.first);
-  return launch_pdl(k_ln_fwd<T, G, N, M>, dim3(ctas), dim3(kThreads), 0, st, a);
+  constexpr int per = kThreads / G, alike = per < 8 ? 8 / per : 1;
+  int64_t ctas = (a.rows + per - 1) / per;
+  if (M != SHIFTED) return launch_pdl(k_ln_fwd<T, G, N, M>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
+  // the scale and the bias are read value by value, once for all rows of a group, which begin alike: as many CTAs as there is room for
+  ctas = std::min<int64_t>(ctas, (int64_t)sm_count() * kLnFwdCtas<T, N, M>);
+  ctas = (ctas + alike - 1) / alike * alike;
+  const size_t smem = (size_t)kLnFwdAhead * 2 * N * sizeof(T) * kThreads;
+  if (smem > 32 << 10) {
+    const cudaError_t e = cudaFuncSetAttribute(k_ln_fwd<T, G, N, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(k_ln_fwd<T, G, N, M>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), smem, st, a);
 }
 template <typename T, int G, int N, LnRows M>
 cudaError_t run_bwd(const LnArgs& a, int ctas, cudaStream_t st) {
@@ -587,7 +614,9 @@ cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
   auto is = [&](auto G, auto N) { return g.threads == G.value && g.values == N.value; };
   cudaError_t e = cudaErrorNotSupported;
   auto go = [&](auto G, auto N) {
-    if (is(G, N)) e = bwd ? run_bwd<T, G.value, N.value, M>(a, ctas, st) : run_fwd<T, G.value, N.value, M>(a, st);
+    if (!is(G, N)) return;
+    if (!bwd) e = run_fwd<T, G.value, N.value, M>(a, st);
+    else if constexpr (N.value != 24) e = run_bwd<T, G.value, N.value, M>(a, ctas, st);
   };
   auto all = [&](auto N, auto... G) { (go(G, N), ...); };
   if constexpr (sizeof(T) == 4) {
@@ -607,7 +636,9 @@ cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
 }  // namespace
 
 bool ln_clears(const LnArgs& a) { return a.slots <= kCheckSlots; }
-// Threads of a row and values of each; 0: a CTA in passes.  FIGURES
+// Threads of a row and values of each; 0: a CTA in passes.  Of bf16 16 values or, where they fill the threads better, 24 (64 MB a tensor,
+// forward: 768 columns 41 us, in 64 threads of 16 51; 64 columns 42, in 8 threads of 8 50); the backward's column sums have no registers
+// for 24 (384 columns 60 us, by 24 65; 1536 64, 79).  Of fp32, whose values take twice the registers, 8 to 16.
 LnGroup ln_group(int d, bool f32, bool bwd) {
   if (f32) {
     for (int g = 8; g <= 32; g *= 2)

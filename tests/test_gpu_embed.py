@@ -122,6 +122,28 @@ def test_embed_rows_of_any_alignment(dtype, d, offset):
     check_case(ids_of("hot", 3000, 50, d), 50, d, dtype, offset=offset, seed=d)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,d", [(20001, 1), (20001, 2), (9001, 5), (9001, 6), (5003, 7), (5003, 10), (3001, 12), (3001, 60), (3001, 100), (2500, 201), (700, 453),
+                                 (2500, 510), (2500, 1001), (90, 8198), (40, 30001)])
+def test_embed_rows_that_are_not_whole_pieces(dtype, n, d):
+    """Pieces of y that hold the ends of rows, or several of them; sums by pairs and by single values."""
+    check_case(ids_of("hot", n, 300, d), 300, d, dtype, seed=d)
+    check_case(ids_of("hot", n, n // 2, d), n // 2, d, dtype, offset=8 if dtype == "bf16" else 4, seed=d + 1)
+
+
+@pytest.mark.parametrize("d,offset", [(10, 2), (100, 1), (7, 1), (510, 6)])
+def test_embed_tables_of_other_alignment_than_the_output(d, offset):
+    table, _ = place(torch.randn(70, d, generator=gen(d)).bfloat16(), offset)
+    ids = ids_of("hot", 4001, 70, d).int().cuda()
+    shape = gbla.glr_shape(1, 4001, d)
+    want = (table.float()[ids.clamp(min=0).long()] * 0.5).bfloat16()
+    want[ids < 0] = 0
+    for y_off in (0, 3):
+        y, buf = place(torch.zeros(4001, d).bfloat16(), y_off)
+        gbla.embed_forward(shape, ids, table, scale=0.5, y=y)
+        assert torch.equal(y, want) and (buf[:y_off] == 77).all() and (buf[y_off + y.numel():] == 77).all()
+
+
 @pytest.mark.parametrize("k,d", [(2, 64), (3, 5), (4, 128)])
 @pytest.mark.parametrize("form", ["dense", "padded", "varlen"])
 def test_embed_several_ids_and_forms(k, d, form):

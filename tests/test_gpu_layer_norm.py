@@ -195,6 +195,50 @@ def test_layer_norm_far_means_and_constant_rows(d):
     assert torch.isfinite(st[[0, 1, 3]]).all()
 
 
+@pytest.mark.parametrize("rows,d", [(60000, 1), (90000, 7), (60000, 30), (90000, 33), (45000, 57), (45000, 95), (45000, 100), (25000, 187), (12000, 250), (12000, 381),
+                                    (8000, 505), (6000, 511), (6000, 766), (3500, 1001), (2500, 1530), (2500, 2041), (1500, 2900), (1500, 4001), (1000, 6001),
+                                    (1000, 8001), (700, 8180), (3, 8185), (3, 8191)])
+def test_layer_norm_many_rows_that_begin_anywhere(rows, d):
+    """bf16 rows that are not whole pieces of 16 bytes, several to each of the groups of threads of a launch."""
+    run(1, rows, d, "bf16", seed=d)
+
+
+@pytest.mark.parametrize("d,cols", [(100, 8), (101, 16), (510, 24), (766, 8), (1001, 40), (2050, 8), (1001, 3)])
+def test_layer_norm_strided_rows_that_begin_anywhere(d, cols):
+    run(2, 700, d, "bf16", cols=cols, seed=d)
+    run(2, 700, d, "bf16", cols=cols, seed=d, seq_lens=[650, 333], res=False)
+    run(3, 450, d, "bf16", seed=d, seq_lens=[450, 0, 77], inplace="res")
+    run(3, 450, d, "bf16", seed=d, seq_lens=[1, 450, 449], inplace="x")
+
+
+@pytest.mark.parametrize("d", [1, 3, 101, 250, 511, 1530, 4001])
+def test_layer_norm_a_row_of_nan_beside_rows_that_begin_anywhere(d):
+    """What the pieces of a row hold of its neighbours counts for nothing, NaN and infinities among it."""
+    T = 700
+    shape = gbla.glr_shape(1, T, d)
+    x, dy, ds = (torch.randn(T, d, generator=gen(d + k)).bfloat16().cuda() for k in range(3))
+    w, b = torch.randn(d, generator=gen(9)).bfloat16().cuda(), torch.randn(d, generator=gen(8)).bfloat16().cuda()
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[1::3] = True
+    want = {}
+    for kind in (0.0, float("nan"), float("inf")):
+        for t in (x, dy, ds):
+            t[bad] = kind
+        y, total, st = gbla.layer_norm_forward(shape, x, w, b, res=ds, stats=True)
+        dx = gbla.layer_norm_backward(shape, total, w, st, dy, ds=ds)["dx"]
+        for k, t in (("y", y), ("total", total), ("stats", st), ("dx", dx)):
+            if kind == 0.0:
+                want[k] = t[~bad].clone()
+                assert torch.isfinite(want[k]).all(), k
+            assert torch.equal(t[~bad], want[k]), (k, kind)
+
+
+@pytest.mark.parametrize("d", [24, 32, 40, 88, 96, 104, 184, 192, 200, 320, 384, 392, 640, 768, 776, 1280, 1536, 1544, 2560, 4096, 4104, 5120, 6144, 6152, 8192])
+def test_layer_norm_widths_of_every_group(d):
+    run(1, 40 + 4000 // d, d, "bf16", seed=d)
+    run(2, 1600000 // d // 8, d, "bf16", seed=d, res=False)
+
+
 def test_layer_norm_padded_rows_may_hold_anything_and_nan_stays_in_its_row():
     B, L, d = 3, 16, 200
     lens = [16, 0, 5]
