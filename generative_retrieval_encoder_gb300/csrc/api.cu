@@ -722,13 +722,14 @@ gbla_status beam_ok(const gbla_beam* g) {
 }
 // Sizes of beam_select: the rows' tasks, and runs of about 1.5 sqrt(K V / n_out) tokens: of the two selections the first, of K V / run
 // runs, goes over its items several times, the second, of n_out runs' tokens, once.  aligned: rows begin at 16-byte boundaries (the
-// workspace has room for the other case).
+// workspace has room for the other case).  Up to a warp's share of a row, 1024 or 2048 tokens (2 groups of 105 beams of 111532, 2 of which
+// go on: 46 us in fp32, 108 with runs of 32 pieces at most; 256 beams of 100000: 123, 245).
 struct BeamLayout { int tasks, runs, lg; size_t part, top, total; };
 BeamLayout beam_layout(const gbla_beam& g, bool aligned) {
   BeamLayout l{};
   const int E = g.io_dtype == GBLA_F32 ? 4 : 8;
   const double want = 1.5 * std::sqrt((double)g.K * g.V / g.n_out);
-  while (l.lg < 5 && E * (1.5 * (1 << l.lg)) < want) ++l.lg;
+  while (l.lg < 8 && E * (1.5 * (1 << l.lg)) < want) ++l.lg;  // of a warp's pieces at most
   const int run = E << l.lg, task = kBeamPieces * 32 * E;
   auto tasks = [&](int64_t places) { return (int)((places + task - 1) / task); };
   auto runs = [&](int64_t places) { return (int)((places + run - 1) / run); };

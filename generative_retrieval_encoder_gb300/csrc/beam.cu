@@ -138,12 +138,29 @@ __device__ __forceinline__ uint4 masked(uint4 w, uint32_t ok) {
   return make_uint4(pick(w.x, 0), pick(w.y, 1), pick(w.z, 2), pick(w.w, 3));
 }
 
-// The largest of each run of 2^lg lanes' pieces: v[u] is the lane's of piece u, first the group of the warp's first run, stored at
-// out[u per + lane >> lg] below `end`.  From 8 lanes on the pieces are dealt out to the lanes while they are compared: 7 exchanges
-// and those of what is left of lg, in place of 8 lg.
-__device__ __forceinline__ void store_runs(float (&v)[kU], int lg, int per, float* out, int end) {
+// The largest of each run of 2^lg pieces: v[u] is the lane's of the u-th 32 of the warp's pieces; run g is stored at out[g] where it is
+// below `end`.  From 8 lanes on the pieces are dealt out to the lanes while they are compared: 7 exchanges and those of what is left of
+// lg, in place of 8 lg.
+__device__ __forceinline__ void store_runs(float (&v)[kU], int lg, float* out, int end) {
   static_assert(kU == 8, "three halvings");
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, per = 32 >> lg;  // runs of 32 pieces
+  if (lg > 5) {  // of 64, 128 or all 256 pieces
+    int n = kU;
+#pragma unroll
+    for (int h = 0; h < 3; ++h) {
+      if (h >= lg - 5) break;
+      n >>= 1;
+#pragma unroll
+      for (int u = 0; u < kU >> (h + 1); ++u) v[u] = fmaxf(v[2 * u], v[2 * u + 1]);
+    }
+#pragma unroll
+    for (int u = 0; u < kU / 2; ++u) {
+      if (u >= n) break;
+      for (int o = 16; o; o >>= 1) v[u] = fmaxf(v[u], __shfl_xor_sync(FULL, v[u], o));
+      if (lane == 0 && u < end) out[u] = v[u];
+    }
+    return;
+  }
   if (lg < 3) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -229,8 +246,8 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
     top = fmaxf(top, run[u]);
     if (MASK == MASK_CANDIDATES) run[u] = piece_max<T>(masked<T>(w[u], mask_bits<E>(mask, a.words, t0 + u * 32 * E)));
   }
-  const int per = 32 >> a.lg;  // runs of the warp's 32 pieces
-  store_runs(run, a.lg, per, a.top + row * a.runs + (int64_t)tile * kU * per, a.runs - tile * kU * per);
+  const int mine = kU * 32 >> a.lg;  // the warp's runs
+  store_runs(run, a.lg, a.top + row * a.runs + (int64_t)tile * mine, a.runs - tile * mine);
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
   BeamPart part;
   if (fabsf(top) <= 4096.f) {

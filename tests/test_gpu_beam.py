@@ -125,6 +125,15 @@ def test_beam_matches_definition(dtype, B, K, V, n):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,K,V,n,pad,offset", [(1, 1, 131072, 1, 0, 0), (2, 4, 131072, 3, 0, 0), (2, 100, 20001, 2, 0, 0), (1, 64, 70000, 5, 3, 1), (3, 8, 100003, 16, 1, 0),
+                                                (1, 300, 9000, 4, 8, 4), (1, 30, 65537, 60, 0, 3), (2, 2, 200000, 1, 7, 0)])
+def test_beam_few_of_many(dtype, B, K, V, n, pad, offset):
+    """Few beams of many candidates: runs of up to a warp's whole share of a row."""
+    run(B, K, V, n, dtype, pad=pad, offset=offset)
+    run(B, K, V, n, dtype, pad=pad, offset=offset, mask=0.01, over=K % 2 == 0, ends=0.2, eos=V - 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 0), (24, 7)])
 @pytest.mark.parametrize("V", [5, 100, 4000])
 def test_beam_rows_of_any_stride_and_alignment(dtype, pad, offset, V):
