@@ -17,7 +17,7 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kMaxBins = 1 << kEmbedDigit;  // a thread's each, at most
-static_assert(kMaxBins <= kThreads, "");
+static_assert(kMaxBins <= kThreads && kEmbedCap % 4 == 0 && kEmbedCap <= 32, "");
 
 // The id of a slot, -1 for none.  An id past the table or a length outside [0, L] counts as none and is `bad`.
 __device__ __forceinline__ int id_of(const EmbedArgs& a, int64_t slot, bool& bad) {
@@ -323,7 +323,9 @@ __device__ __forceinline__ float value(const Piece<T, E>& w, int j) {
 }
 
 // The rows of the ids without a slot, kThreads of them a CTA: which of them occur is read from the sorted keys between the first
-// and the last of them.
+// and the last of them, up to kScan places; among more each is looked for (500000 places of 1000
+// ids, a few of them most: the whole gradient 81 us, 197 by reading all).
+constexpr int kScan = 16384;
 __device__ void clear_rows(const EmbedArgs& a, const int* key, int64_t v0) {
   __shared__ int64_t bound[2];
   __shared__ unsigned there[kThreads / 32];
@@ -343,23 +345,37 @@ __device__ void clear_rows(const EmbedArgs& a, const int* key, int64_t v0) {
     if (lane == 0) bound[warp] = lo;
   }
   __syncthreads();
-  // (a frequent id has many places: four keys a load, four loads on their way)
-  for (int64_t i0 = (bound[0] & ~(int64_t)3) + threadIdx.x * 4; i0 < bound[1]; i0 += kThreads * 16) {
-    int4 k[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + u * kThreads * 4;
-      k[u] = i < bound[1] ? *reinterpret_cast<const int4*>(key + i) : make_int4(-1, -1, -1, -1);
+  if (bound[1] - bound[0] > kScan) {  // (frequent ids) a thread looks for its own, three places at a time
+    const int64_t v = v0 + threadIdx.x;
+    int64_t lo = bound[0], hi = bound[1];  // the first place of a key >= v is in [lo, hi]
+    while (lo < hi) {
+      const int64_t q = (hi - lo + 3) / 4, p0 = lo + q - 1, p1 = min(p0 + q, hi - 1), p2 = min(p0 + 2 * q, hi - 1);
+      const int k0 = key[p0], k1 = key[p1], k2 = key[p2];
+      if (k0 >= v) hi = p0;
+      else if (k1 >= v) lo = p0 + 1, hi = p1;
+      else if (k2 >= v) lo = p1 + 1, hi = p2;
+      else lo = p2 + 1;
     }
+    const unsigned m = __ballot_sync(FULL, lo < bound[1] && key[lo] == v);
+    if (lane == 0) there[warp] = m;
+  } else {  // four keys a load, four loads on their way
+    for (int64_t i0 = (bound[0] & ~(int64_t)3) + threadIdx.x * 4; i0 < bound[1]; i0 += kThreads * 16) {
+      int4 k[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + u * kThreads * 4;
-      const int q[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = i0 + u * kThreads * 4;
+        k[u] = i < bound[1] ? *reinterpret_cast<const int4*>(key + i) : make_int4(-1, -1, -1, -1);
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (i + j < bound[0] || i + j >= bound[1]) continue;
-        const int r = q[j] - (int)v0;
-        if (!(reinterpret_cast<volatile unsigned*>(there)[r >> 5] >> (r & 31) & 1)) atomicOr(&there[r >> 5], 1u << (r & 31));
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = i0 + u * kThreads * 4;
+        const int q[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (i + j < bound[0] || i + j >= bound[1]) continue;
+          const int r = q[j] - (int)v0;
+          if (!(reinterpret_cast<volatile unsigned*>(there)[r >> 5] >> (r & 31) & 1)) atomicOr(&there[r >> 5], 1u << (r & 31));
+        }
       }
     }
   }
@@ -379,7 +395,7 @@ __device__ void clear_rows(const EmbedArgs& a, const int* key, int64_t v0) {
 // Groups of G threads, G E P columns of a chunk each: the first `chunk_ctas` CTAs; the others, if any, clear the rows of the ids without
 // a slot.
 template <typename T, int G, int E, int P>
-__global__ void __launch_bounds__(kThreads, G < 32 || P > 1 ? 2 : 4) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
+__global__ void __launch_bounds__(kThreads, 4) k_embed_rows(const EmbedArgs a, const EmbedSort s, int blocks, int chunk_ctas) {
   pdl_enter();
   if ((int)blockIdx.x >= chunk_ctas) {
     clear_rows(a, s.key_out, ((int64_t)blockIdx.x - chunk_ctas) * kThreads);
@@ -387,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, G < 32 || P > 1 ? 2 : 4) k_embed_row
   }
   using W = Piece<T, E>;
   constexpr int C = kEmbedCap;
-  constexpr int U = G < 32 && sizeof(W) == 16 ? 16 : 8;  // rows in flight: short rows' groups are few
+  constexpr int U = 8;  // rows in flight (16 of short rows, in half as many CTAs: 168 us against 152 for 1000000 slots of 32 columns)
   // the keys from C places before the chunk to C behind it, and the slots from its first place on
   __shared__ __align__(16) int keys[kThreads / G][3 * C];
   __shared__ __align__(16) int slots[kThreads / G][2 * C];
@@ -400,31 +416,59 @@ __global__ void __launch_bounds__(kThreads, G < 32 || P > 1 ? 2 : 4) k_embed_row
   if (lo >= a.n) return;
   int *key = keys[grp] + C, *slot = slots[grp];  // by place - lo
   const int len = (int)min((int64_t)C, a.n - lo);
+  // four at a time (chunks begin at multiples of 4, the arrays' ends are padded); before the first place -1, behind the last one the most
 #pragma unroll
-  for (int j = t - C; j < 2 * C; j += G) {
-    const bool in = lo + j >= 0 && lo + j < a.n;
-    key[j] = in ? s.key_out[lo + j] : -1;
-    if (j >= 0) slot[j] = in ? s.slot_out[lo + j] : -1;
+  for (int q = t; q < 3 * C / 4; q += G) {
+    const int64_t i = lo - C + 4 * q;
+    int4 k = make_int4(-1, -1, -1, -1);
+    if (i >= 0) {
+      const int4 none = make_int4(0x7fffffff, 0x7fffffff, 0x7fffffff, 0x7fffffff);
+      k = i < a.n ? *reinterpret_cast<const int4*>(s.key_out + i) : none;
+      if (i + 1 >= a.n) k.y = none.y;
+      if (i + 2 >= a.n) k.z = none.z;
+      if (i + 3 >= a.n) k.w = none.w;
+    }
+    *reinterpret_cast<int4*>(keys[grp] + 4 * q) = k;
+    if (4 * q >= C && i < a.n) *reinterpret_cast<int4*>(slot + 4 * q - C) = *reinterpret_cast<const int4*>(s.slot_out + i);
   }
   __syncwarp(team);
   const int k0 = key[0], k1 = key[len - 1];
   if (k0 >= a.V) return;  // sorted last: slots without an id, nothing else
   // the places nearest to the chunk's first and last one that have another key than it, before and behind
   int b0 = -C - 1, f0 = 2 * C, b1 = -1, f1 = 2 * C;
+  if (G >= 16) {
 #pragma unroll
-  for (int j = t - C; j < 2 * C; j += G) {
-    const int k = key[j];
-    if (j < 0 && k != k0) b0 = max(b0, j);
-    if (j > 0 && k != k0) f0 = min(f0, j);
-    if (j >= 0 && j < len && k != k1) b1 = max(b1, j);
-    if (j >= len && k != k1) f1 = min(f1, j);
-  }
+    for (int j = t - C; j < 2 * C; j += G) {
+      const int k = key[j];
+      if (j < 0 && k != k0) b0 = max(b0, j);
+      if (j > 0 && k != k0) f0 = min(f0, j);
+      if (j >= 0 && j < len && k != k1) b1 = max(b1, j);
+      if (j >= len && k != k1) f1 = min(f1, j);
+    }
 #pragma unroll
-  for (int o = G / 2; o; o >>= 1) {
-    b0 = max(b0, __shfl_xor_sync(team, b0, o));
-    f0 = min(f0, __shfl_xor_sync(team, f0, o));
-    b1 = max(b1, __shfl_xor_sync(team, b1, o));
-    f1 = min(f1, __shfl_xor_sync(team, f1, o));
+    for (int o = G / 2; o; o >>= 1) {
+      b0 = max(b0, __shfl_xor_sync(team, b0, o));
+      f0 = min(f0, __shfl_xor_sync(team, f0, o));
+      b1 = max(b1, __shfl_xor_sync(team, b1, o));
+      f1 = min(f1, __shfl_xor_sync(team, f1, o));
+    }
+  } else {  // by halving, every thread the same: each is in [lower, upper] (1000000 slots of 32 columns:
+           // 116 us, 123 by reading all keys)
+    int l0 = -C, u0 = 0, l1 = 1, u1 = 2 * C, l2 = 0, u2 = len - 1, l3 = len, u3 = 2 * C;
+    auto halve = [&](int& l, int& u, int k) {  // the first place of a key >= k
+      if (l >= u) return;
+      const int m = (l + u) >> 1;
+      if (key[m] >= k) u = m;
+      else l = m + 1;
+    };
+#pragma unroll
+    for (int step = 0; step < 7; ++step) {  // (2 C <= 2^6)
+      halve(l0, u0, k0);
+      halve(l1, u1, k0 + 1);
+      halve(l2, u2, k1);
+      halve(l3, u3, k1 + 1);
+    }
+    b0 = l0 - 1, f0 = l1, b1 = l2 - 1, f1 = l3;
   }
   // the first run is the places (b0, f0), the last one (b1, f1), as far as they are looked at: C before and behind
   const bool long0 = f0 - b0 - 1 > C, same = b1 < 0, long1 = k1 < a.V && (same ? long0 : f1 - b1 - 1 > C);
