@@ -107,6 +107,10 @@ __device__ __forceinline__ double sum_of(const BeamPart& p) {
 
 constexpr int kU = kBeamPieces;
 
+// i / d for i d < 2^32 as a multiplication: `by` is ceil(2^32 / d), or 0 for d = 1.
+__device__ __forceinline__ uint32_t recip(uint32_t d) { return d == 1 ? 0 : 0xffffffffu / d + 1; }
+__device__ __forceinline__ uint32_t quot(uint32_t i, uint32_t by) { return by ? __umulhi(i, by) : i; }
+
 // The larger of two packed bf16 values each; of NaN and a number the number (of two NaN that), or NaN.
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   uint32_t o;
@@ -356,6 +360,7 @@ constexpr int kPick = 1024;   // threads
 struct One { static constexpr int value = 1; };
 struct Four { static constexpr int value = 4; };
 constexpr int kBins = 2 * kPick;
+constexpr int kBeamCount = 256; // items whose ranks are counted
 struct PickSmem {
   uint64_t key[kBeamItems];       // the items at hand; the kept ones first
   uint64_t kept[kBeamMost];
@@ -369,6 +374,10 @@ struct PickSmem {
   uint32_t red[64];
   int n, digit, need, whole;
 };
+__device__ __forceinline__ PickSmem& pick_smem() {
+  extern __shared__ __align__(16) unsigned char raw[];
+  return *reinterpret_cast<PickSmem*>(raw);
+}
 // An item is kept if its key is above `key`, or equal and its place at most `at`.
 struct Cut { uint64_t key; uint32_t at; };
 // Of the keys > 0 that a thread has seen: the largest and the smallest upper word, and how many.
@@ -452,7 +461,8 @@ __device__ __forceinline__ bool digits(PickSmem& s, int cnt, uint64_t eq, uint64
 
 // Of items [0, cnt) the `want` best to the front, in any order; returns how many there are (fewer: no more candidates).  seen: of the
 // threads' shares of the items.  low: a key that none of the kept is below; 1 if they are fewer than `want`.
-__device__ int select_best(PickSmem& s, int cnt, int want, Seen seen, uint64_t& low) {
+__device__ __forceinline__ int select_best(int cnt, int want, Seen seen, uint64_t& low) {
+  PickSmem& s = pick_smem();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t top = __reduce_max_sync(FULL, seen.top), bottom = __reduce_min_sync(FULL, seen.bottom);
   int live = __reduce_add_sync(FULL, seen.live);
@@ -504,11 +514,13 @@ __device__ int select_best(PickSmem& s, int cnt, int want, Seen seen, uint64_t& 
   __syncthreads();
   return n;
 }
-__device__ int select_best(PickSmem& s, int cnt, int want, uint64_t& low) {
+// The same of items that are there already.  Seldom called: not inlined, so that what is in the way of every call stays short.
+__device__ __noinline__ int select_again(int cnt, int want, uint64_t& low) {
+  PickSmem& s = pick_smem();
   Seen seen;
   for (int i = threadIdx.x; i < cnt; i += kPick) seen.add(s.key[i]);
   __syncthreads();
-  return select_best(s, cnt, want, seen, low);
+  return select_best(cnt, want, seen, low);
 }
 
 // A CTA a group: the rows' logarithms, the n best runs, the n best tokens of those, in order.  Bound by the latency of some
@@ -516,8 +528,7 @@ __device__ int select_best(PickSmem& s, int cnt, int want, uint64_t& low) {
 template <typename T>
 __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   pdl_enter();
-  extern __shared__ __align__(16) unsigned char raw[];
-  PickSmem& s = *reinterpret_cast<PickSmem*>(raw);
+  PickSmem& s = pick_smem();
   constexpr int E = 16 / sizeof(T);
   const int tid = threadIdx.x;
   const int64_t row0 = (int64_t)blockIdx.x * a.K;
@@ -586,6 +597,7 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   // the n best runs, kBeamItems at a time
   const uint32_t runs = (uint32_t)a.runs, all = (uint32_t)a.K * runs;
   const float* tops = a.top + row0 * a.runs;
+  const uint32_t by = (uint64_t)all * runs >> 32 ? 0 : recip(runs);  // i / runs as a multiplication where that is exact
   int have = 0;
   uint64_t low = 1;
   for (uint32_t i0 = 0; i0 < all;) {
@@ -600,7 +612,7 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
       for (int u = 0; u < 4; ++u) {
         const int j = j0 + u * kPick;
         if (j >= more) continue;
-        const uint32_t i = i0 + j, b = i / runs;
+        const uint32_t i = i0 + j, b = by ? __umulhi(i, by) : i / runs;
         const float ref = s.ref[b];
         const bool ended = ref == kInf;
         const uint64_t k = ended && i != b * runs ? 0 : key_of(s.base[b], ended ? 0.f : v[u], ended ? 0.f : ref);
@@ -609,7 +621,7 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
         seen.add(k);
       }
     }
-    have = select_best(s, have + more, a.n, seen, low);
+    have = select_best(have + more, a.n, seen, low);
     i0 += more;
   }
   if (tid < have) {
@@ -625,53 +637,56 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   auto tokens = [&](int i0, auto many) {  // of pieces i0, i0 + kPick ..
     constexpr int U = decltype(many)::value;
     uint4 w[U];
-    uint32_t ok[U], row[U];
-    int t0[U];
+    uint32_t ok[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kPick;
       ok[u] = 0;
       if (i >= pieces) continue;
       const uint32_t b = s.run[i >> a.lg];
-      row[u] = b;
-      const int64_t at = row0 + b;
-      const int j = i & ((1 << a.lg) - 1);
-      t0[u] = s.token[i >> a.lg] + j * E;
+      const int j = i & ((1 << a.lg) - 1), t0 = s.token[i >> a.lg] + j * E;
       if (s.ref[b] == kInf) {
         ok[u] = j == 0 ? 1 : 0;
         continue;
       }
-      ok[u] = a.allowed ? mask_bits<E>(a.allowed + at * a.words, a.words, t0[u]) : (1u << E) - 1;
-      if (t0[u] >= 0 && t0[u] + E <= a.V) w[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits) + at * a.ld + t0[u]);
+      const int64_t at = row0 + b;
+      ok[u] = a.allowed ? mask_bits<E>(a.allowed + at * a.words, a.words, t0) : (1u << E) - 1;
+      if (t0 >= 0 && t0 + E <= a.V) {
+        w[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits) + at * a.ld + t0);
+      } else {  // an end of the row: its tokens are all looked at below
+        w[u] = make_uint4(0, 0, 0, 0);
+        ok[u] &= (t0 < 0 ? ~0u << -t0 : ~0u) & (t0 + E > a.V ? (t0 < a.V ? (1u << (a.V - t0)) - 1 : 0u) : ~0u);
+        ok[u] |= ok[u] << 16;
+      }
     }
+    uint32_t found = 0;  // E bits a piece
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!ok[u]) continue;
-      const uint32_t b = row[u];
-      const float2 bs = s.base[b];
-      const float ref = s.ref[b];
-      auto put = [&](float x, float rf, uint32_t t) {
-        const uint64_t k = key_of(bs, x, rf);
-        if (k < low) return;
-        const int to = atomicAdd(&s.n, 1);
-        if (to >= kBeamItems) return;
-        s.key[to] = k;
-        s.at[to] = b * (uint32_t)a.V + t;
-      };
-      if (ref == kInf) {
-        put(0.f, 0.f, (uint32_t)a.eos);
-        continue;
-      }
+      const uint32_t b = s.run[(i0 + u * kPick) >> a.lg];
       // what is below this as one sum of fp32, off by 2^-23 of either number at most, is below `low` (NaN: nothing is)
-      const float least = lowest - 0x1p-21f * (fabsf(lowest) + fabsf(bs.x)) - 1e-30f;
-      const bool inside = t0[u] >= 0 && t0[u] + E <= a.V;
+      const float bx = s.base[b].x, ref = s.ref[b], least = lowest - 0x1p-21f * (fabsf(lowest) + fabsf(bx)) - 1e-30f;
+      uint32_t bits = ok[u] >> 16;
+      if (ref == kInf) bits = 1;
+      if (!bits) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int t = t0[u] + j;
-        if (!(ok[u] >> j & 1) || (!inside && (t < 0 || t >= a.V))) continue;
-        const float v = inside ? piece<T>(w[u], j) : to_f(static_cast<const T*>(a.logits)[(row0 + b) * a.ld + t]);
-        if (!(bs.x + (v - ref) < least)) put(v, ref, (uint32_t)t);
+        for (int j = 0; j < E; ++j) bits |= bx + (piece<T>(w[u], j) - ref) < least ? 0u : 1u << j;
+        bits &= ok[u];
       }
+      found |= bits << (u * E);
+    }
+    for (; found; found &= found - 1) {  // few
+      const int q = __ffs((int)found) - 1, i = i0 + q / E * kPick;
+      const uint32_t b = s.run[i >> a.lg];
+      const bool ended = s.ref[b] == kInf;
+      const int t = ended ? a.eos : s.token[i >> a.lg] + (i & ((1 << a.lg) - 1)) * E + q % E;
+      const float x = ended ? 0.f : to_f(static_cast<const T*>(a.logits)[(row0 + b) * a.ld + t]);
+      const uint64_t k = key_of(s.base[b], x, ended ? 0.f : s.ref[b]);
+      if (k < low) continue;
+      const int to = atomicAdd(&s.n, 1);
+      if (to >= kBeamItems) continue;
+      s.key[to] = k;
+      s.at[to] = b * (uint32_t)a.V + (uint32_t)t;
     }
   };
   for (int i0 = 0; i0 < pieces; i0 += 4 * kPick) tokens(i0 + tid, Four{});
@@ -688,7 +703,7 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
       __syncthreads();
       if (cnt > kBeamItems - kPick * E) {
         uint64_t l;
-        select_best(s, cnt, a.n, l);
+        select_again(cnt, a.n, l);
         low = max(low, l);
       }
     }
@@ -697,54 +712,86 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   }
   if (cnt > kPick) {
     uint64_t l;
-    cnt = select_best(s, cnt, a.n, l);
+    cnt = select_again(cnt, a.n, l);
   }
-  // in order, by (key descending, place ascending), an item a thread: each warp sorts its 32, then an item's rank is how many of each
-  // warp's precede it, by halving (a bitonic sort of all takes twice as long at 256 items, five times at 1024)
-  uint64_t key = tid < cnt ? s.key[tid] : 0;
-  uint32_t at = tid < cnt ? s.at[tid] : 0xffffffffu;
-  const int warps = (cnt + 31) / 32, lane = tid & 31;
-  __syncthreads();
+  // in order, by (key descending, place ascending): an item's rank is how many precede it
   int rank = kBeamMost;
-  if (tid < warps * 32) {
-#pragma unroll
-    for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-      for (int j = k >> 1; j; j >>= 1) {
-        const uint64_t ok = __shfl_xor_sync(FULL, key, j);
-        const uint32_t oa = __shfl_xor_sync(FULL, at, j);
-        const bool better = key > ok || (key == ok && at < oa);
-        if (better != (((lane & j) == 0) == ((lane & k) == 0))) key = ok, at = oa;
+  uint64_t key = 0;
+  uint32_t at = 0xffffffffu;
+  if (cnt <= kBeamCount) {  // counted among all, by the keys' upper words, `team` threads an item
+    int team = 32;
+    while (team > 1 && team * cnt > kPick) team >>= 1;
+    const int quads = (cnt + 3) / 4;
+    for (int i = tid; i < quads * 4; i += kPick) s.kept_at[i] = i < cnt ? (uint32_t)(s.key[i] >> 32) : 0;
+    __syncthreads();
+    const int item = tid / team, part = tid % team;
+    int above = 0, alike = 0;
+    if (item < cnt) {
+      key = s.key[item];
+      at = s.at[item];
+      const uint32_t hi = (uint32_t)(key >> 32);
+      for (int q = part; q < quads; q += team) {
+        const uint4 o = *reinterpret_cast<const uint4*>(s.kept_at + 4 * q);
+        above += (o.x > hi) + (o.y > hi) + (o.z > hi) + (o.w > hi);
+        alike += (o.x == hi) + (o.y == hi) + (o.z == hi) + (o.w == hi);
       }
-    s.key[tid] = key;
-    s.at[tid] = at;
-    s.kept_at[tid] = (uint32_t)(key >> 32);
-  }
-  __syncthreads();
-  if (tid < warps * 32 && key) {
-    const uint32_t hi = (uint32_t)(key >> 32);
-    const uint32_t* upper = s.kept_at;
-    rank = lane;
-    for (int w0 = 0; w0 < warps; w0 += 4) {  // four warps' at a time, by the keys' upper words
-      int pos[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) pos[u] = min(w0 + u, warps - 1) * 32;
-#pragma unroll
-      for (int st = 16; st; st >>= 1)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (upper[pos[u] + st - 1] > hi) pos[u] += st;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int w = w0 + u, end = w * 32 + 32;
-        if (w >= warps || w == tid >> 5) continue;
-        if (upper[pos[u]] > hi) ++pos[u];
-        while (pos[u] < end && upper[pos[u]] == hi) {  // alike so far
-          const uint64_t k = s.key[pos[u]];
-          if (k < key || (k == key && s.at[pos[u]] > at)) break;
-          ++pos[u];
+    }
+    for (int o = team / 2; o; o >>= 1) {
+      above += __shfl_xor_sync(FULL, above, o);
+      alike += __shfl_xor_sync(FULL, alike, o);
+    }
+    if (item < cnt && part == 0) {
+      if (alike > 1)  // (itself among them)
+        for (int q = 0; q < cnt; ++q) {
+          const uint64_t k = s.key[q];
+          above += k >> 32 == key >> 32 && (k > key || (k == key && s.at[q] < at));
         }
-        rank += pos[u] - w * 32;
+      rank = above;
+    }
+  } else {  // an item a thread: each warp sorts its 32, then how many of each warp's precede an item is found by halving
+    if (tid < cnt) key = s.key[tid], at = s.at[tid];
+    const int warps = (cnt + 31) / 32, lane = tid & 31;
+    __syncthreads();
+    if (tid < warps * 32) {
+#pragma unroll
+      for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j; j >>= 1) {
+          const uint64_t ok = __shfl_xor_sync(FULL, key, j);
+          const uint32_t oa = __shfl_xor_sync(FULL, at, j);
+          const bool better = key > ok || (key == ok && at < oa);
+          if (better != (((lane & j) == 0) == ((lane & k) == 0))) key = ok, at = oa;
+        }
+      s.key[tid] = key;
+      s.at[tid] = at;
+      s.kept_at[tid] = (uint32_t)(key >> 32);
+    }
+    __syncthreads();
+    if (tid < warps * 32 && key) {
+      const uint32_t hi = (uint32_t)(key >> 32);
+      const uint32_t* upper = s.kept_at;
+      rank = lane;
+      for (int w0 = 0; w0 < warps; w0 += 4) {  // four warps' at a time, by the keys' upper words
+        int pos[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pos[u] = min(w0 + u, warps - 1) * 32;
+#pragma unroll
+        for (int st = 16; st; st >>= 1)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (upper[pos[u] + st - 1] > hi) pos[u] += st;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int w = w0 + u, end = w * 32 + 32;
+          if (w >= warps || w == tid >> 5) continue;
+          if (upper[pos[u]] > hi) ++pos[u];
+          while (pos[u] < end && upper[pos[u]] == hi) {  // alike so far
+            const uint64_t k = s.key[pos[u]];
+            if (k < key || (k == key && s.at[pos[u]] > at)) break;
+            ++pos[u];
+          }
+          rank += pos[u] - w * 32;
+        }
       }
     }
   }
@@ -766,10 +813,6 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
 }
 
 // ------------------------------------------------------------------ reorder
-// i / d for i d < 2^32 as a multiplication: `by` is ceil(2^32 / d), or 0 for d = 1.
-__device__ __forceinline__ uint32_t recip(uint32_t d) { return d == 1 ? 0 : 0xffffffffu / d + 1; }
-__device__ __forceinline__ uint32_t quot(uint32_t i, uint32_t by) { return by ? __umulhi(i, by) : i; }
-
 constexpr int kMove = kBeamMoveUnits / 256;  // accesses of a thread, all on their way before the first is stored
 
 // Within one tensor a CTA takes all K rows of one group over a few columns: it reads every row that goes on before it writes one.
