@@ -360,7 +360,7 @@ constexpr int kPick = 1024;   // threads
 struct One { static constexpr int value = 1; };
 struct Four { static constexpr int value = 4; };
 constexpr int kBins = 2 * kPick;
-constexpr int kBeamCount = 256; // items whose ranks are counted
+constexpr int kBeamCount = 256; // items whose ranks are counted (256: 2.5 us, sorted by warps 4; the counts grow with their square)
 struct PickSmem {
   uint64_t key[kBeamItems];       // the items at hand; the kept ones first
   uint64_t kept[kBeamMost];
@@ -524,7 +524,7 @@ __device__ __noinline__ int select_again(int cnt, int want, uint64_t& low) {
 }
 
 // A CTA a group: the rows' logarithms, the n best runs, the n best tokens of those, in order.  Bound by the latency of some
-// twenty steps that the CTA takes together: K = 16 of V = 32768 in 12 us beside the rows' 29, K = n = 256 of V = 2048 in 18 beside 23.
+// twenty steps that the CTA takes together: K = 16 of V = 32768 in 11 us beside the rows' 29, K = n = 256 of V = 2048 in 16 beside 23.
 template <typename T>
 __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   pdl_enter();
