@@ -451,7 +451,8 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 1 : N == 8 ? 3 : 2) k_ln_b
   }
 }
 
-// Rows of any length, a CTA each: three passes over the row, from L2 after the first.
+// Rows of any length, a CTA each: three passes over the row, from L2 after the first, six CTAs an SM (3355 rows of 10000 bf16: forward
+// 69 us, 0.57 of a copy's rate, backward 85, 0.46; in two CTAs an SM 94 and 132, value by value 318 of both).
 __device__ __forceinline__ float cta_sum(float v, float* red) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
   __syncthreads();
@@ -461,10 +462,21 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   for (int w = 1; w < kThreads / 32; ++w) v += red[w];
   return v;
 }
+// The row's values a piece (or as many single ones) a thread at a time.
+template <typename T, LnRows M>
+using Part = Row<T, kThreads, 16 / (int)sizeof(T), M>;
 template <typename T>
+constexpr int kPart = kThreads * 16 / (int)sizeof(T);
+template <typename T, LnRows M, typename F>
+__device__ __forceinline__ void store_part(T* p, int d, F&& f) {
+  store_row<T, kThreads, 16 / (int)sizeof(T), M>(p, threadIdx.x, d, 0, f);
+}
+template <typename T, LnRows M>
 __global__ void __launch_bounds__(kThreads) k_ln_fwd_long(const LnArgs a) {
   pdl_enter();
   __shared__ float red[kThreads / 32];
+  constexpr int E = 16 / (int)sizeof(T);
+  const int t = threadIdx.x;
   const float inv = 1.f / (float)a.d;
   if (check_slots(a)) return;
   const int64_t cta = blockIdx.x - a.first, ctas = gridDim.x - a.first;
@@ -475,41 +487,67 @@ __global__ void __launch_bounds__(kThreads) k_ln_fwd_long(const LnArgs a) {
     T* sum = a.sum ? static_cast<T*>(a.sum) + row * a.d : nullptr;
     T* y = static_cast<T*>(a.y) + row * a.d;
     if (!row_valid(a, row)) {
-      for (int c = threadIdx.x; c < a.d; c += kThreads) {
-        if (sum) sum[c] = from_f<T>(0.f);
-        y[c] = from_f<T>(0.f);
+      for (int c = 0; c < a.d; c += kPart<T>) {
+        if (sum) store_part<T, M>(sum + c, a.d - c, [](int) { return two(0.f); });
+        store_part<T, M>(y + c, a.d - c, [](int) { return two(0.f); });
       }
-      if (a.stats && threadIdx.x == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(0.f, 0.f);
+      if (a.stats && t == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(0.f, 0.f);
       continue;
     }
-    // a thread's own columns in every pass, so what it stored (sum may be x or res) is what it reads again
-    const T *p = res && sum ? sum : x, *q = res && !sum ? res : nullptr;
-    auto at = [&](int c) { return q ? to_f(from_f<T>(to_f(p[c]) + to_f(q[c]))) : to_f(p[c]); };
-    float m = 0.f, v = 0.f;
-    for (int c = threadIdx.x; c < a.d; c += kThreads) {
-      const T s = res ? from_f<T>(to_f(x[c]) + to_f(res[c])) : x[c];
-      if (sum) sum[c] = s;
-      m += to_f(s);
+    // s of the thread's values from column c on; a thread's own columns in every pass, so what it stored (sum may be x or res) is what it
+    // reads again
+    float2 s[E / 2];
+    auto load = [&](const T* p, const T* q, int c) {
+      Part<T, M> v, u;
+      v.load(p + c, t, a.d - c);
+      if (q) u.load(q + c, t, a.d - c);
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        s[k] = v.get(k);
+        if (!q) continue;
+        s[k] = __fadd2_rn(s[k], u.get(k));
+        s[k] = make_float2(to_f(from_f<T>(s[k].x)), to_f(from_f<T>(s[k].y)));
+      }
+    };
+    float2 q = two(0.f);
+    for (int c = 0; c < a.d; c += kPart<T>) {
+      load(x, res, c);
+      if (sum) store_part<T, M>(sum + c, a.d - c, [&](int k) { return s[k]; });
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) q = __fadd2_rn(q, s[k]);
     }
-    m = cta_sum(m, red) * inv;
-    for (int c = threadIdx.x; c < a.d; c += kThreads) {
-      const float e = at(c) - m;
-      v += e * e;
+    const float mean = cta_sum(q.x + q.y, red) * inv;
+    const T *p1 = res && sum ? sum : x, *p2 = res && !sum ? res : nullptr;
+    q = two(0.f);
+    for (int c = 0; c < a.d; c += kPart<T>) {
+      load(p1, p2, c);
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        float2 e = __fadd2_rn(s[k], two(-mean));
+        if (c + col_of<T, kThreads, M>(2 * k, t, 0) >= a.d) e.x = 0.f;
+        if (c + col_of<T, kThreads, M>(2 * k + 1, t, 0) >= a.d) e.y = 0.f;
+        q = __ffma2_rn(e, e, q);
+      }
     }
-    const float r = 1.f / sqrtf(cta_sum(v, red) * inv + a.eps);
-    for (int c = threadIdx.x; c < a.d; c += kThreads) {
-      float z = (at(c) - m) * r;
-      if (w) z *= to_f(w[c]);
-      if (b) z += to_f(b[c]);
-      y[c] = from_f<T>(z);
+    const float r = 1.f / sqrtf(cta_sum(q.x + q.y, red) * inv + a.eps);
+    for (int c = 0; c < a.d; c += kPart<T>) {
+      load(p1, p2, c);
+      Part<T, M> wp, bp;
+      if (w) wp.load(w + c, t, a.d - c);
+      else wp.ones();
+      if (b) bp.load(b + c, t, a.d - c);
+      else bp.clear();
+      store_part<T, M>(y + c, a.d - c, [&](int k) { return __ffma2_rn(__fmul2_rn(__fadd2_rn(s[k], two(-mean)), two(r)), wp.get(k), bp.get(k)); });
     }
-    if (a.stats && threadIdx.x == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(m, r);
+    if (a.stats && t == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(mean, r);
   }
 }
-template <typename T>
+template <typename T, LnRows M>
 __global__ void __launch_bounds__(kThreads) k_ln_bwd_long(const LnArgs a) {
   pdl_enter();
   __shared__ float red[kThreads / 32];
+  constexpr int E = 16 / (int)sizeof(T);
+  const int t = threadIdx.x;
   const float inv = 1.f / (float)a.d;
   if (check_slots(a)) return;
   const int64_t cta = blockIdx.x - a.first, ctas = gridDim.x - a.first;
@@ -519,42 +557,73 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd_long(const LnArgs a) {
     const T* ds = a.ds ? static_cast<const T*>(a.ds) + row * a.d : nullptr;
     T* dx = static_cast<T*>(a.dx) + row * a.d;
     if (!row_valid(a, row)) {
-      for (int c = threadIdx.x; c < a.d; c += kThreads) dx[c] = from_f<T>(0.f);
+      for (int c = 0; c < a.d; c += kPart<T>) store_part<T, M>(dx + c, a.d - c, [](int) { return two(0.f); });
       continue;
     }
     const float2 st = reinterpret_cast<const float2*>(a.stats)[row];
-    float c0 = 0.f, c1 = 0.f;
-    for (int c = threadIdx.x; c < a.d; c += kThreads) {
-      const float g = to_f(dy[c]) * (w ? to_f(w[c]) : 1.f);
-      c0 += g;
-      c1 += g * ((to_f(x[c]) - st.x) * st.y);
+    float2 g[E / 2], z[E / 2];
+    auto load = [&](int c) {  // g and z of the thread's values from column c on; past the row's end g is 0
+      Part<T, M> xp, yp, wp;
+      xp.load(x + c, t, a.d - c);
+      yp.load(dy + c, t, a.d - c);
+      if (w) wp.load(w + c, t, a.d - c);
+      else wp.ones();
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        g[k] = __fmul2_rn(yp.get(k), wp.get(k));
+        z[k] = __fmul2_rn(__fadd2_rn(xp.get(k), two(-st.x)), two(st.y));
+      }
+    };
+    float2 q0 = two(0.f), q1 = two(0.f);
+    for (int c = 0; c < a.d; c += kPart<T>) {
+      load(c);
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        q0 = __fadd2_rn(q0, g[k]);
+        q1 = __ffma2_rn(g[k], z[k], q1);
+      }
     }
-    c0 = cta_sum(c0, red) * inv;
-    c1 = cta_sum(c1, red) * inv;
-    for (int c = threadIdx.x; c < a.d; c += kThreads) {
-      const float g = to_f(dy[c]) * (w ? to_f(w[c]) : 1.f), z = (to_f(x[c]) - st.x) * st.y;
-      dx[c] = from_f<T>(st.y * (g - c0 - z * c1) + (ds ? to_f(ds[c]) : 0.f));
+    const float c0 = -cta_sum(q0.x + q0.y, red) * inv, c1 = -cta_sum(q1.x + q1.y, red) * inv;
+    for (int c = 0; c < a.d; c += kPart<T>) {
+      load(c);
+      Part<T, M> sp;
+      if (ds) sp.load(ds + c, t, a.d - c);
+      else sp.clear();
+      store_part<T, M>(dx + c, a.d - c, [&](int k) { return __ffma2_rn(__ffma2_rn(z[k], two(c1), __fadd2_rn(g[k], two(c0))), two(st.y), sp.get(k)); });
     }
   }
 }
-// The long rows' column sums: CTA (x, y) 256 columns of the y-th range of rows.
-template <typename T>
+// The long rows' column sums: CTA (x, y) kPart columns of the y-th range of rows.
+template <typename T, LnRows M>
 __global__ void __launch_bounds__(kThreads) k_ln_cols_long(const LnArgs a) {
   pdl_enter();
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= a.d) return;
+  constexpr int E = 16 / (int)sizeof(T);
+  const int c = blockIdx.x * kPart<T>, t = threadIdx.x;
   const int64_t lo = a.rows * blockIdx.y / gridDim.y, hi = a.rows * (blockIdx.y + 1) / gridDim.y;
-  float dw = 0.f, db = 0.f;
+  float2 dw[E / 2], db[E / 2];
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) dw[k] = db[k] = two(0.f);
+#pragma unroll 2
   for (int64_t row = lo; row < hi; ++row) {
     if (!row_valid(a, row)) continue;
     const float2 st = reinterpret_cast<const float2*>(a.stats)[row];
-    const float g = to_f(static_cast<const T*>(a.dy)[row * a.d + c]);
-    dw += g * ((to_f(static_cast<const T*>(a.x)[row * a.ldx + c]) - st.x) * st.y);
-    db += g;
+    Part<T, M> x, y;
+    x.load(static_cast<const T*>(a.x) + row * a.ldx + c, t, a.d - c);
+    y.load(static_cast<const T*>(a.dy) + row * a.d + c, t, a.d - c);
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+      dw[k] = __ffma2_rn(y.get(k), __fmul2_rn(__fadd2_rn(x.get(k), two(-st.x)), two(st.y)), dw[k]);
+      db[k] = __fadd2_rn(db[k], y.get(k));
+    }
   }
   float* out = a.part + (int64_t)blockIdx.y * 2 * a.d;
-  out[c] = dw;
-  out[a.d + c] = db;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int at = c + col_of<T, kThreads, M>(i, t, 0);
+    if (at >= a.d) continue;
+    out[at] = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+    out[a.d + at] = i & 1 ? db[i / 2].y : db[i / 2].x;
+  }
 }
 
 // dw | db from `n` partial rows of 2 d sums: 32 columns a CTA, its 32 warps take every 32nd partial, then their sums in order (304 rows
@@ -629,8 +698,8 @@ cudaError_t pick(const LnArgs& a, bool bwd, int ctas, cudaStream_t st) {
   }
   go(Int<256>{}, Int<32>{});
   if (g.threads) return e;
-  if (!bwd) return launch_pdl(k_ln_fwd_long<T>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
-  return launch_pdl(k_ln_bwd_long<T>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
+  constexpr LnRows L = M == PIECES ? PIECES : SINGLE;
+  return launch_pdl(bwd ? k_ln_bwd_long<T, L> : k_ln_fwd_long<T, L>, dim3((unsigned)(ctas + a.first)), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace
@@ -656,26 +725,32 @@ LnGroup ln_group(int d, bool f32, bool bwd) {
 }
 int ln_ctas(int64_t rows, int d, bool f32) {
   const int g = ln_group(d, f32, true).threads, per = g ? kThreads / g : 1, alike = per < 8 ? 8 / per : 1;  // CTAs whose rows are a multiple of 8
-  const int64_t most = std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * 2);
+  const int64_t most = std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * (g ? 2 : 6));  // (as many as there is room for)
   return (int)((most + alike - 1) / alike * alike);
 }
-int ln_parts(int64_t rows, int d, bool f32) { return ln_group(d, f32, true).threads ? ln_ctas(rows, d, f32) : (int)std::min<int64_t>(rows, 16); }
+int ln_parts(int64_t rows, int d, bool f32) { return ln_group(d, f32, true).threads ? ln_ctas(rows, d, f32) : (int)std::min<int64_t>(rows, 64); }
 
-cudaError_t launch_ln(LnArgs a, bool f32, bool bwd, cudaStream_t st) {
-  a.first = a.slots > 0 && a.slots <= kCheckSlots;
+static LnRows ln_rows(const LnArgs& a, bool f32) {
   const size_t es = f32 ? 4 : 2;
   uintptr_t rows = 0;  // where the rows' tensors begin
   for (const void* q : {a.x, a.res, (const void*)a.sum, (const void*)a.y, a.dy, a.ds, (const void*)a.dx}) rows |= reinterpret_cast<uintptr_t>(q);
   const uintptr_t all = rows | reinterpret_cast<uintptr_t>(a.w) | reinterpret_cast<uintptr_t>(a.b) | (uintptr_t)(a.d * es) | (uintptr_t)(a.ldx * es);
+  return all % 16 == 0 ? PIECES : !f32 && rows % 16 == 0 && (a.ldx - a.d) % 8 == 0 ? SHIFTED : SINGLE;
+}
+cudaError_t launch_ln(LnArgs a, bool f32, bool bwd, cudaStream_t st) {
+  a.first = a.slots > 0 && a.slots <= kCheckSlots;
   const int ctas = ln_ctas(a.rows, a.d, f32);
-  if (f32) return all % 16 == 0 ? pick<float, PIECES>(a, bwd, ctas, st) : pick<float, SINGLE>(a, bwd, ctas, st);
-  if (all % 16 == 0) return pick<bf16, PIECES>(a, bwd, ctas, st);
-  return rows % 16 == 0 && (a.ldx - a.d) % 8 == 0 ? pick<bf16, SHIFTED>(a, bwd, ctas, st) : pick<bf16, SINGLE>(a, bwd, ctas, st);
+  const LnRows m = ln_rows(a, f32);
+  if (f32) return m == PIECES ? pick<float, PIECES>(a, bwd, ctas, st) : pick<float, SINGLE>(a, bwd, ctas, st);
+  return m == PIECES ? pick<bf16, PIECES>(a, bwd, ctas, st) : m == SHIFTED ? pick<bf16, SHIFTED>(a, bwd, ctas, st) : pick<bf16, SINGLE>(a, bwd, ctas, st);
 }
 cudaError_t launch_ln_cols_long(const LnArgs& a, bool f32, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.d + kThreads - 1) / kThreads), (unsigned)ln_parts(a.rows, a.d, f32));
-  return f32 ? launch_pdl(k_ln_cols_long<float>, grid, dim3(kThreads), 0, st, a)
-             : launch_pdl(k_ln_cols_long<bf16>, grid, dim3(kThreads), 0, st, a);
+  const int part = f32 ? kPart<float> : kPart<bf16>;
+  const dim3 grid((unsigned)((a.d + part - 1) / part), (unsigned)ln_parts(a.rows, a.d, f32));
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kThreads), 0, st, a); };
+  const bool pieces = ln_rows(a, f32) == PIECES;
+  if (f32) return pieces ? go(k_ln_cols_long<float, PIECES>) : go(k_ln_cols_long<float, SINGLE>);
+  return pieces ? go(k_ln_cols_long<bf16, PIECES>) : go(k_ln_cols_long<bf16, SINGLE>);
 }
 cudaError_t launch_ln_cols(const LnArgs& a, bool f32, float* dw, float* db, cudaStream_t st) {
   return launch_pdl(k_ln_cols, dim3((unsigned)((2 * (int64_t)a.d + 31) / 32)), dim3(1024), 0, st, (const float*)a.part,

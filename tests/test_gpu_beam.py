@@ -179,6 +179,15 @@ def test_beam_ties_go_to_the_lowest_beam_and_token():
             assert (flat[b, :len(first)] == first).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_beam_ties_of_few_of_many(dtype):
+    """Equal logits all over: more tokens of the best runs than the selection holds at once."""
+    beam = gbla.beam_shape(1, 128, 131072, 8, dtype=dtype)
+    sc, tok, par, _ = gbla.beam_select(beam, torch.ones(128, 131072, device="cuda", dtype=dtype), torch.zeros(1, 128, device="cuda"))
+    assert torch.equal(tok.cpu().long(), torch.arange(8)[None]) and not par.any()
+    assert ((sc.cpu().double() + math.log(131072)).abs() <= NEAR + E * math.log(131072)).all()
+
+
 def test_beam_infinities_nan_and_far_logits():
     inf, nan = math.inf, math.nan
     V, K = 70, 6
