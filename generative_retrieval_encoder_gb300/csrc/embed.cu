@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, cons
       }
       __syncthreads();
     }
+    __syncthreads();  // all have read `big` to its end (entries of -1 pass no barrier) before the next turn writes it
   }
 }
 

@@ -296,3 +296,30 @@ def test_embed_on_streams_in_graphs_and_with_shared_workspaces():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, want[k][0]) and torch.equal(g, want[k][1])
+
+
+def torch_gradient(ids, dy, V, scale):
+    """(dtable, sum of magnitudes) in 64 bits, on the GPU."""
+    keep = ids >= 0
+    at, rows = ids[keep].long(), dy[keep].double()
+    zero = torch.zeros(V, dy.shape[1], dtype=torch.float64, device="cuda")
+    return zero.index_add(0, at, rows) * scale, zero.index_add(0, at, rows.abs()) * abs(scale)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 2048), ("f32", 2044), ("bf16", 515)])
+def test_embed_frequent_ids_in_every_turn_of_the_join(dtype, d):
+    """More columns of repeated ids than the join's CTAs take at once (32 tasks an SM), every tenth id so frequent that a whole CTA
+    sums it.  Bound: up to 31 additions in fp32, two words after that, their sum and the scale: 34 E of the magnitudes."""
+    V, rare, often = 900, 40, 1000
+    blocks = -(-d // (128 if d % 4 == 0 else 32))
+    assert V * blocks > 2 * 32 * torch.cuda.get_device_properties(0).multi_processor_count
+    ids = torch.cat([torch.arange(V).repeat_interleave(rare), torch.arange(0, V, 10).repeat_interleave(often)])
+    ids = ids[torch.randperm(len(ids), generator=gen(1))].to(torch.int32).cuda()
+    dy = torch.randn(len(ids), d, generator=gen(2)).to(torch.bfloat16 if dtype == "bf16" else torch.float32).cuda()
+    shape = gbla.glr_shape(1, len(ids), d, dtype=dtype)
+    ws = gbla.embed_workspace(shape, V, 1, True)
+    got = gbla.embed_backward(shape, ids, dy, V, scale=1.5, ws=ws)
+    want, size = torch_gradient(ids, dy, V, 1.5)
+    assert ((got.double() - want).abs() <= 34 * E * size).all()
+    for _ in range(5):
+        assert torch.equal(gbla.embed_backward(shape, ids, dy, V, scale=1.5, ws=ws), got)
