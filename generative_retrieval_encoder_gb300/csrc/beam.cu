@@ -8,9 +8,9 @@
 // is to select n of K V / G runs, then n of their n G tokens.
 //
 // Which of two beams' candidates is the better one depends on the difference of two such logarithms, and among thousands of
-// candidates some lie closer than fp32's rounding.  So each exponential is formed to 2^-30 (2^(j/32) from a table in two
-// words, P. T. P. Tang's reduction, and a polynomial of degree 4), added into two words (the sum is off by 2^-27 at most, by
-// 2^-31 on the mean), and scores are compared in two fp32 words.  Equal logits of one row stay equal.
+// candidates some lie closer than fp32's rounding.  So each exponential is formed to 2^-28.8 (2^-31.4 on the mean; 2^(j/32) from
+// a table in two words, P. T. P. Tang's reduction, and a polynomial of degree 3), added into two words (the sum is off by 2^-27
+// at most, by 2^-31 on the mean), and scores are compared in two fp32 words.  Equal logits of one row stay equal.
 #include <algorithm>
 
 #include "common.cuh"
@@ -38,8 +38,9 @@ __device__ const float kExpLo[32] = {
     -0x1.99e158p-21f, -0x1.14c836p-20f, -0x1.872644p-21f, 0x1.7c2b28p-20f, -0x1.5bc508p-22f, 0x1.789ea6p-22f, -0x1.387142p-20f, -0x1.67e88p-20f,
 };
 constexpr float kL = 0x1.715476p+5f, kLlo = 0x1.4ae0cp-21f;  // 32 / ln 2 in two words
-// 2^(f / 32) - 1 = f (c1 + f (c2 + f (c3 + f c4))): c_k = (ln 2 / 32)^k / k!, the next term below 2^-39 at |f| = 1/2
-constexpr float kC1 = 0x1.62e43p-6f, kC2 = 0x1.ebfbep-13f, kC3 = 0x1.c6b08ep-20f, kC4 = 0x1.3b2ab6p-27f;
+// 2^(f / 32) - 1 = f (c1 + f (c2 + f c3)): c_k = (ln 2 / 32)^k / k!, and in c2 the next term too: for f^4 the multiple of f^2 that is
+// nearest on |f| <= 1/2, (sqrt 2 - 1) / 2, which leaves 2^-33
+constexpr float kC1 = 0x1.62e43p-6f, kC2 = 0x1.ebfce6p-13f, kC3 = 0x1.c6b08ep-20f;
 
 // Logarithms: c_j of 8 bits next to 1 / (1 + (j + 1/2) / 64), and -ln c_j in two words
 __device__ const float kLogC[64] = {
@@ -277,21 +278,24 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
         const float2 k = __ffma2_rn(v, two(kL), two(12582912.f));  // rounded to 32nds of an octave: n + 1.5 2^23
         const float2 n = __ffma2_rn(k, two(-1.f), two(12582912.f));  // -n
         const float2 f = __ffma2_rn(v, two(kLlo), __ffma2_rn(v, two(kL), n));
-        const float2 p = __fmul2_rn(f, __ffma2_rn(f, __ffma2_rn(f, __ffma2_rn(f, two(kC4), two(kC3)), two(kC2)), two(kC1)));
+        const float2 p = __fmul2_rn(f, __ffma2_rn(f, __ffma2_rn(f, two(kC3), two(kC2)), two(kC1)));
         const uint32_t bx = __float_as_uint(k.x), by = __float_as_uint(k.y);
         // n's lower 5 bits are j, the others the octave: (1 + j / 32) 2^(n / 32 - e)
         const float2 scale = make_float2(__uint_as_float((bx << 18) + bias), __uint_as_float((by << 18) + bias));
         const float2 h = make_float2(hi_tab[bx & 31], hi_tab[by & 31]), l = make_float2(lo_tab[bx & 31], lo_tab[by & 31]);
         const float2 h2 = __fmul2_rn(h, scale), next = __fadd2_rn(sum, h2);
         const float2 cut = __ffma2_rn(__ffma2_rn(sum, two(-1.f), next), two(-1.f), h2);  // h2 - (next - sum): exact
-        rest = __fadd2_rn(rest, __ffma2_rn(__ffma2_rn(h, p, l), scale, cut));
+        rest = __fadd2_rn(rest, __ffma2_rn(__ffma2_rn(h, p, __ffma2_rn(l, p, l)), scale, cut));  // (h + l) (1 + p) - h: l p counts
         sum = next;
       }
       lo = __fadd2_rn(lo, rest);
     }
-    // the grid's parts are whole numbers of 2^-16, at most 2^22 a lane: exact as integers
-    part.hi = __reduce_add_sync(FULL, (int)((sum.x - 192.f) * 65536.f) + (int)((sum.y - 192.f) * 65536.f));
+    // the grid's parts are whole numbers of 2^-16, at most 2^22 a lane: exact as integers.  What of lo is on the grid joins them, so the
+    // exchanges round values below 2^-12 (a value's rest, 0.011 of it at most, has gone through 7 additions on the mean by then)
     float r = lo.x + lo.y;
+    const int more = __float2int_rn(r * 65536.f);
+    r = __fmaf_rn((float)more, -0x1p-16f, r);
+    part.hi = __reduce_add_sync(FULL, (int)((sum.x - 192.f) * 65536.f) + (int)((sum.y - 192.f) * 65536.f) + more);
     for (int o = 16; o; o >>= 1) r += __shfl_xor_sync(FULL, r, o);
     part.lo = r;
     part.ref = (float)e;

@@ -257,6 +257,27 @@ def test_beam_order_of_close_candidates():
     check(got, p, order, V, K)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("std", [8.0, 300.0])
+def test_beam_order_of_rows_that_one_logit_dominates(dtype, std):
+    """1024 beams, in each one logit (another value each) so far above the rest that it has all the mass: score + logit - logarithm is
+    the score, whatever the logit.  Scores are 2^-26 apart, the bound of two rows' logarithms: their order is the beams'."""
+    K, V = 1024, 24
+    x = torch.full((K, V), -math.inf)
+    at = torch.randint(0, V, (K,), generator=gen(1))
+    top = torch.randn(K, generator=gen(2)) * std
+    x[torch.arange(K), (at + 3) % V] = top - 60
+    x[torch.arange(K), at] = top
+    x = x.bfloat16() if dtype == "bf16" else x
+    for spread in (1, -1):
+        scores = -(torch.arange(K)[None] * 2.0 ** -26).float()
+        order = torch.arange(K) if spread > 0 else torch.arange(K).flip(0)
+        scores = scores[:, order].contiguous()
+        sc, tok, par, _ = gbla.beam_select(gbla.beam_shape(1, K, V, K, dtype=dtype), x.cuda(), scores.cuda())
+        assert torch.equal(par[0].cpu().long(), order) and torch.equal(tok[0].cpu().long(), at[order])
+        assert ((sc.cpu().double() - torch.sort(scores.double(), descending=True).values).abs() <= NEAR / 2).all()
+
+
 def test_beam_a_large_call_by_spot_checks():
     B, K, V = 64, 16, 32768
     v, x, scores = make(B, K, V, "bf16", seed=3)
