@@ -256,8 +256,9 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
   BeamPart part;
   if (fabsf(top) <= 4096.f) {
-    const float floor_ = top - 80.f;  // what is below counts as e^-80 of the largest: nothing
-    const uint32_t floor2 = pack_bf16(floor_, floor_);
+    const float floor_ = top - 80.f;  // what is below counts as e^-80 (bf16: e^-64 to e^-80) of the largest: nothing
+    // rounded up: further down (96 below -4064 to nearest) the exponent of 2^(n / 32 - e) leaves its field
+    const uint32_t floor1 = (__float_as_uint(floor_) + (floor_ > 0.f ? 0xffffu : 0u)) >> 16, floor2 = floor1 | floor1 << 16;
     const int e = (int)floorf(top * 1.44269504f) + 1;
     const uint32_t bias = (uint32_t)(127 - e) << 23;
     // two values at a time.  sum: on the grid of 2^-16 that its start fixes; lo: what the grid cuts off, and the rest

@@ -278,6 +278,23 @@ def test_beam_order_of_rows_that_one_logit_dominates(dtype, std):
         assert ((sc.cpu().double() - torch.sort(scores.double(), descending=True).values).abs() <= NEAR / 2).all()
 
 
+def test_beam_every_bf16_top():
+    """Rows whose largest logit is each bf16 value up to 4096 of either sign, with logits just below and far below it, -inf, and places
+    past the row's end: none of them loses its row."""
+    v = (torch.arange(65536, dtype=torch.int32) << 16).view(torch.float32)
+    top = v[torch.isfinite(v) & (v.abs() <= 4096)]
+    B, V = len(top), 300
+    x = torch.full((B, V), -math.inf)
+    x[:, 100:200] = top[:, None] - 2000
+    x[:, 250] = top - 1
+    x[:, 7] = top
+    x = x.bfloat16()
+    scores = torch.zeros(B, 1)
+    got = gbla.beam_select(gbla.beam_shape(B, 1, V, 3), x.cuda(), scores.cuda())
+    p, order = reference(x, scores, V, 3)
+    check(got, p, order, V, 3, strict=False)
+
+
 def test_beam_a_large_call_by_spot_checks():
     B, K, V = 64, 16, 32768
     v, x, scores = make(B, K, V, "bf16", seed=3)
