@@ -721,26 +721,22 @@ gbla_status beam_ok(const gbla_beam* g) {
   return GBLA_OK;
 }
 // Sizes of beam_select: the rows' tasks, and runs of about 1.5 sqrt(K V / n_out) tokens: of the two selections the first, of K V / run
-// runs, goes over its items several times, the second, of n_out runs' tokens, once.  aligned: rows begin at 16-byte boundaries (the
-// workspace has room for the other case).  Up to a warp's share of a row, 1024 or 2048 tokens (2 groups of 105 beams of 111532, 2 of which
-// go on: 46 us in fp32, 108 with runs of 32 pieces at most; 256 beams of 100000: 123, 245).
+// runs, goes over its items several times, the second, of n_out runs' tokens, once.  Up to a warp's share of a row, 1024 or 2048 tokens
+// (2 groups of 105 beams of 111532, 2 of which go on: 46 us in fp32, 108 with runs of 32 pieces at most; 256 beams of 100000: 123, 245).
 struct BeamLayout { int tasks, runs, lg; size_t part, top, total; };
-BeamLayout beam_layout(const gbla_beam& g, bool aligned) {
+BeamLayout beam_layout(const gbla_beam& g) {
   BeamLayout l{};
   const int E = g.io_dtype == GBLA_F32 ? 4 : 8;
   const double want = 1.5 * std::sqrt((double)g.K * g.V / g.n_out);
   while (l.lg < 8 && E * (1.5 * (1 << l.lg)) < want) ++l.lg;  // of a warp's pieces at most
   const int run = E << l.lg, task = kBeamPieces * 32 * E;
-  auto tasks = [&](int64_t places) { return (int)((places + task - 1) / task); };
-  auto runs = [&](int64_t places) { return (int)((places + run - 1) / run); };
-  const int64_t most = (int64_t)g.V + E - 1, places = aligned ? g.V : most;
-  l.tasks = tasks(places);
-  l.runs = runs(places);
+  l.tasks = (g.V + task - 1) / task;
+  l.runs = (g.V + run - 1) / run;
   Cursor c;
   c.take(16);
   const size_t rows = (size_t)g.B * g.K;
-  l.part = c.take(rows * tasks(most) * sizeof(BeamPart));
-  l.top = c.take(rows * runs(most) * 4);
+  l.part = c.take(rows * l.tasks * sizeof(BeamPart));
+  l.top = c.take(rows * l.runs * 4);
   l.total = c.off;
   return l;
 }
@@ -1450,7 +1446,7 @@ gbla_status layer_norm_backward(const gbla_shape* shape, const void* x, int64_t 
   return GBLA_OK;
 }
 
-size_t beam_workspace_size(const gbla_beam* beam) { return beam_ok(beam) == GBLA_OK ? beam_layout(*beam, false).total : 0; }
+size_t beam_workspace_size(const gbla_beam* beam) { return beam_ok(beam) == GBLA_OK ? beam_layout(*beam).total : 0; }
 
 gbla_status beam_select(const gbla_beam* beam, const void* logits, int64_t ld, const float* scores, const uint32_t* allowed,
                         const uint8_t* done, float* new_scores, int32_t* tokens, int32_t* parents, uint8_t* new_done, void* ws,
@@ -1463,7 +1459,7 @@ gbla_status beam_select(const gbla_beam* beam, const void* logits, int64_t ld, c
     if (!q || !aligned4(q)) return GBLA_ERR_INVALID_ARG;
   if (!logits || !aligned(logits, f32 ? 4 : 2) || ld < g.V || ld > (1LL << 40) || !aligned4(allowed) || (done && g.eos < 0))
     return GBLA_ERR_INVALID_ARG;
-  const BeamLayout l = beam_layout(g, aligned16(logits) && ld * (f32 ? 4 : 2) % 16 == 0);
+  const BeamLayout l = beam_layout(g);
   if ((r = ws_status(ws, ws_bytes, l.total)) != GBLA_OK) return r;
   const RowCtx c{static_cast<cudaStream_t>(stream)};
   BeamArgs a{};

@@ -10,7 +10,8 @@
 // Which of two beams' candidates is the better one depends on the difference of two such logarithms, and among thousands of
 // candidates some lie closer than fp32's rounding.  So each exponential is formed to 2^-28.8 (2^-31.4 on the mean; 2^(j/32) from
 // a table in two words, P. T. P. Tang's reduction, and a polynomial of degree 3), added into two words (the sum is off by 2^-27
-// at most, by 2^-31 on the mean), and scores are compared in two fp32 words.  Equal logits of one row stay equal.
+// at most, by 2^-31 on the mean), and scores are compared in two fp32 words.  Equal logits of one row stay equal, and so do equal
+// rows: which values are added to which goes by their tokens, wherever a row begins in memory.
 #include <algorithm>
 
 #include "common.cuh"
@@ -88,17 +89,35 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return o;
 }
 
-// The row's tokens begin `off` values behind a 16-byte boundary; places are counted from that boundary.
+// The row's tokens begin so many values behind a 16-byte boundary.
 template <typename T>
 __device__ __forceinline__ int row_offset(const BeamArgs& a, int64_t row) {
   return (int)((reinterpret_cast<uintptr_t>(a.logits) + row * a.ld * sizeof(T)) % 16 / sizeof(T));
 }
-// E mask bits from token t (below 0: bits of no token) of a row.
+// E mask bits from token t, a multiple of E, of a row.
 template <int E>
 __device__ __forceinline__ uint32_t mask_bits(const uint32_t* m, int words, int t) {
-  const int w = t >> 5;  // -1 for t < 0
-  const uint32_t lo = w >= 0 && w < words ? m[w] : 0u, hi = w + 1 < words && (t & 31) + E > 32 ? m[w + 1] : 0u;
-  return __funnelshift_r(lo, hi, t & 31) & ((1u << E) - 1);
+  const int w = t >> 5;
+  return (w < words ? m[w] : 0u) >> (t & 31) & ((1u << E) - 1);
+}
+// Of the values of two pieces those from the off-th on, a piece of them.
+template <typename T>
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int off) {
+  uint32_t q[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int words = off * (int)sizeof(T) / 4;
+  if (words & 2) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) q[i] = q[i + 2];
+  }
+  if (words & 1) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) q[i] = q[i + 1];
+  }
+  if (sizeof(T) == 2 && off & 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = __funnelshift_r(q[i], q[i + 1], 16);
+  }
+  return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
@@ -107,6 +126,7 @@ __device__ __forceinline__ double sum_of(const BeamPart& p) {
 }
 
 constexpr int kU = kBeamPieces;
+template <int V> struct Int { static constexpr int value = V; };
 
 // i / d for i d < 2^32 as a multiplication: `by` is ceil(2^32 / d), or 0 for d = 1.
 __device__ __forceinline__ uint32_t recip(uint32_t d) { return d == 1 ? 0 : 0xffffffffu / d + 1; }
@@ -195,8 +215,10 @@ __device__ __forceinline__ void store_runs(float (&v)[kU], int lg, float* out, i
 enum BeamMask { MASK_NONE, MASK_CANDIDATES, MASK_SUM };  // no mask; of the candidates alone; of the sum, too
 // A warp takes kU pieces a lane of one row.  Bound by instructions, 19 a value, 16 of them in the fp32 pipe (a plain exponential takes
 // 6): 33.5 M bf16 logits in 29 us, 0.34 of a copy's rate, 16.8 M fp32 ones under a mask in 23, 0.43.  (Rows by way of shared memory
-// in persistent CTAs: 10 us more.)
-template <typename T, BeamMask MASK>
+// in persistent CTAs: 10 us more.)  SHIFT: rows do not all begin at 16-byte boundaries, and are moved to them in registers, as
+// which values are added to which must not depend on it (64 x 16 beams, the whole selection: 43.2 us for rows of 32767 tokens, 45.1 for rows
+// of 32768 at a stride of 32769, 39.4 for whole pieces, 40.4 with the shifts compiled in; words picked by selects: 44.3, 46.1).
+template <typename T, BeamMask MASK, bool SHIFT>
 __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
   pdl_enter();
   constexpr int E = 16 / sizeof(T);
@@ -212,22 +234,19 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
   const int tile = (int)(task - row * a.tasks);
   if (row >= (int64_t)a.B * a.K || (a.done && a.done[row])) return;
   const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-  const int first = tile * (kU * 32 * E) - row_offset<T>(a, row), t0 = first + lane * E;  // the tokens of the warp's, the lane's first value
+  const int first = tile * (kU * 32 * E), t0 = first + lane * E, off = SHIFT ? row_offset<T>(a, row) : 0;  // the tokens of the warp's, the lane's first value
   const uint32_t* mask = MASK == MASK_NONE ? nullptr : a.allowed + row * a.words;
   constexpr uint32_t LOWEST = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -infinity
-  uint4 w[kU];
-  if (first >= 0 && first + kU * 32 * E <= a.V) {
+  uint4 w[kU], tail;  // tail: of a row that does not begin at a boundary, the piece after the warp's
+  if (first >= off && first - off + (kU * 32 + (off ? 1 : 0)) * E <= a.V) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) w[u] = __ldcs(reinterpret_cast<const uint4*>(x + t0) + u * 32);
+    for (int u = 0; u < kU; ++u) w[u] = __ldcs(reinterpret_cast<const uint4*>(x + t0 - off) + u * 32);
+    if (off) tail = __ldcs(reinterpret_cast<const uint4*>(x + first - off) + kU * 32);
   } else {
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int t = t0 + u * 32 * E;
-      w[u] = make_uint4(LOWEST, LOWEST, LOWEST, LOWEST);
-      if (t >= 0 && t + E <= a.V) {
-        w[u] = __ldcs(reinterpret_cast<const uint4*>(x + t));
-      } else if (t > -E && t < a.V) {  // the row's edges, value by value
-        uint32_t q[4] = {LOWEST, LOWEST, LOWEST, LOWEST};
+    auto piece_at = [&](int t) {  // of tokens t ..
+      uint32_t q[4] = {LOWEST, LOWEST, LOWEST, LOWEST};
+      if (t >= 0 && t + E <= a.V) return __ldcs(reinterpret_cast<const uint4*>(x + t));
+      if (t > -E && t < a.V) {  // the row's edges, value by value
 #pragma unroll
         for (int j = 0; j < E; ++j)
           if (t + j >= 0 && t + j < a.V) {
@@ -238,7 +257,30 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
               q[j & 3] = reinterpret_cast<const uint32_t*>(x)[t + j];
             }
           }
-        w[u] = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+      return make_uint4(q[0], q[1], q[2], q[3]);
+    };
+#pragma unroll
+    for (int u = 0; u < kU; ++u) w[u] = piece_at(t0 - off + u * 32 * E);
+    if (off) tail = piece_at(first - off + kU * 32 * E);
+  }
+  if (SHIFT && off) {  // pieces of memory to pieces of tokens: what a lane's token piece lacks is in the piece that follows, the next lane's
+    auto following = [&](int u) {  // of lane 31, the first lane's next piece
+      return __shfl_sync(FULL, lane ? w[u].x : u + 1 < kU ? w[u + 1 < kU ? u + 1 : 0].x : tail.x, (lane + 1) & 31);
+    };
+    for (int k = off * (int)sizeof(T) / 4; k; --k) {  // a word at a time, the first of the piece that follows after the last
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t got = following(u);
+        w[u] = make_uint4(w[u].y, w[u].z, w[u].w, got);
+      }
+      tail = make_uint4(tail.y, tail.z, tail.w, tail.x);
+    }
+    if (sizeof(T) == 2 && off & 1) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t got = following(u);
+        w[u] = make_uint4(__funnelshift_r(w[u].x, w[u].y, 16), __funnelshift_r(w[u].y, w[u].z, 16), __funnelshift_r(w[u].z, w[u].w, 16), __funnelshift_r(w[u].w, got, 16));
       }
     }
   }
@@ -362,8 +404,6 @@ __device__ __forceinline__ float score_of(uint64_t key) {
 }
 
 constexpr int kPick = 1024;   // threads
-struct One { static constexpr int value = 1; };
-struct Four { static constexpr int value = 4; };
 constexpr int kBins = 2 * kPick;
 constexpr int kBeamCount = 256; // items whose ranks are counted (256: 2.5 us, sorted by warps 4; the counts grow with their square)
 struct PickSmem {
@@ -530,7 +570,7 @@ __device__ __noinline__ int select_again(int cnt, int want, uint64_t& low) {
 
 // A CTA a group: the rows' logarithms, the n best runs, the n best tokens of those, in order.  Bound by the latency of some
 // twenty steps that the CTA takes together: K = 16 of V = 32768 in 11 us beside the rows' 29, K = n = 256 of V = 2048 in 16 beside 23.
-template <typename T>
+template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   pdl_enter();
   PickSmem& s = pick_smem();
@@ -558,9 +598,10 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
     }
     float2 at0 = make_float2(-kInf, 0.f);  // no value above -infinity, or a NaN among them: no candidates
     float ref = 0.f;
-    if (!__any_sync(FULL, most > -kInf)) {
+    const bool far = most > -kInf;  // (known to the row's threads) the row has logits far from 0: in 64 bits, below
+    {
       float hi = 0.f, lo = 0.f;
-      for (int i = t; mine && i < a.tasks; i += team) {
+      for (int i = t; mine && !far && i < a.tasks; i += team) {
         const BeamPart q = p[i];
         const float d = best - q.ref, f = d < 120.f ? __uint_as_float((uint32_t)(127 - (int)d) << 23) : 0.f;  // (a part without values is 0, or NaN)
         lo += two_sum(hi, (float)(q.hi >> 12) * 0x1p-4f * f, hi);
@@ -577,11 +618,11 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
         const float e = two_sum(c, -l.x, at0.x);
         at0.y = fabsf(at0.x) < kInf ? two_sum(at0.x, e - l.y, at0.x) : 0.f;
       }
-    } else {  // some row of the warp has logits far from 0: in 64 bits, relative to the largest part's, a logit itself if it is a far one
-      const bool far = most > -kInf;
+    }
+    if (__any_sync(FULL, far)) {  // relative to the largest part's, a logit itself if it is a far one.  The warp's other rows keep theirs
       double e = best > -kInf ? (double)best * kLn2 : -kInf, sum = 0.;
       if (far && (double)most > e) e = (double)most, ref = most;
-      for (int i = t; mine && i < a.tasks; i += team) {
+      for (int i = t; mine && far && i < a.tasks; i += team) {
         const BeamPart q = p[i];
         sum += sum_of(q) * (q.ref > -kInf ? exp((q.far ? (double)q.ref : (double)q.ref * kLn2) - e) : 1.);
       }
@@ -632,7 +673,7 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
   if (tid < have) {
     const uint32_t i = s.at[tid], b = i / runs;
     s.run[tid] = b;
-    s.token[tid] = (int)((i - b * runs) << a.lg) * E - row_offset<T>(a, row0 + b);
+    s.token[tid] = (int)((i - b * runs) << a.lg) * E;
   }
   if (tid == 0) s.n = 0;
   __syncthreads();
@@ -656,11 +697,14 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
       }
       const int64_t at = row0 + b;
       ok[u] = a.allowed ? mask_bits<E>(a.allowed + at * a.words, a.words, t0) : (1u << E) - 1;
-      if (t0 >= 0 && t0 + E <= a.V) {
-        w[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits) + at * a.ld + t0);
+      const int off = SHIFT ? row_offset<T>(a, at) : 0;
+      const T* x = static_cast<const T*>(a.logits) + at * a.ld + t0 - off;  // where that is a 16-byte boundary
+      if (t0 >= off && t0 - off + (off ? 2 : 1) * E <= a.V) {
+        w[u] = *reinterpret_cast<const uint4*>(x);
+        if (off) w[u] = shifted<T>(w[u], *reinterpret_cast<const uint4*>(x + E), off);
       } else {  // an end of the row: its tokens are all looked at below
         w[u] = make_uint4(0, 0, 0, 0);
-        ok[u] &= (t0 < 0 ? ~0u << -t0 : ~0u) & (t0 + E > a.V ? (t0 < a.V ? (1u << (a.V - t0)) - 1 : 0u) : ~0u);
+        ok[u] &= t0 + E > a.V ? (t0 < a.V ? (1u << (a.V - t0)) - 1 : 0u) : ~0u;
         ok[u] |= ok[u] << 16;
       }
     }
@@ -694,7 +738,7 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
       s.at[to] = b * (uint32_t)a.V + (uint32_t)t;
     }
   };
-  for (int i0 = 0; i0 < pieces; i0 += 4 * kPick) tokens(i0 + tid, Four{});
+  for (int i0 = 0; i0 < pieces; i0 += 4 * kPick) tokens(i0 + tid, Int<4>{});
   __syncthreads();
   int cnt = s.n;
   __syncthreads();
@@ -702,7 +746,7 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
     if (tid == 0) s.n = 0;
     __syncthreads();
     for (int i0 = 0; i0 < pieces; i0 += kPick) {
-      tokens(i0 + tid, One{});
+      tokens(i0 + tid, Int<1>{});
       __syncthreads();
       cnt = s.n;
       __syncthreads();
@@ -901,19 +945,27 @@ __global__ void __launch_bounds__(256) k_beam_move(const __grid_constant__ BeamT
 
 }  // namespace
 
-cudaError_t launch_beam_rows(const BeamArgs& a, bool f32, cudaStream_t st) {
+// Whether some row does not begin at a 16-byte boundary.
+static bool shifts(const BeamArgs& a, bool f32) {
+  return (reinterpret_cast<uintptr_t>(a.logits) | (uintptr_t)a.ld * (f32 ? 4 : 2)) % 16 != 0;
+}
+template <typename T, bool SHIFT>
+static cudaError_t rows(const BeamArgs& a, cudaStream_t st) {
   const int64_t tasks = (int64_t)a.B * a.K * a.tasks;
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)((tasks + 7) / 8)), dim3(256), 0, st, a); };
-  if (!a.allowed) return f32 ? go(k_beam_rows<float, MASK_NONE>) : go(k_beam_rows<bf16, MASK_NONE>);
-  if (!a.over_allowed) return f32 ? go(k_beam_rows<float, MASK_CANDIDATES>) : go(k_beam_rows<bf16, MASK_CANDIDATES>);
-  return f32 ? go(k_beam_rows<float, MASK_SUM>) : go(k_beam_rows<bf16, MASK_SUM>);
+  return !a.allowed ? go(k_beam_rows<T, MASK_NONE, SHIFT>) : a.over_allowed ? go(k_beam_rows<T, MASK_SUM, SHIFT>) : go(k_beam_rows<T, MASK_CANDIDATES, SHIFT>);
+}
+cudaError_t launch_beam_rows(const BeamArgs& a, bool f32, cudaStream_t st) {
+  if (shifts(a, f32)) return f32 ? rows<float, true>(a, st) : rows<bf16, true>(a, st);
+  return f32 ? rows<float, false>(a, st) : rows<bf16, false>(a, st);
 }
 cudaError_t launch_beam_pick(const BeamArgs& a, bool f32, cudaStream_t st) {
   auto go = [&](auto kernel) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PickSmem));
     return e != cudaSuccess ? e : launch_pdl(kernel, dim3((unsigned)a.B), dim3(kPick), sizeof(PickSmem), st, a);
   };
-  return f32 ? go(k_beam_pick<float>) : go(k_beam_pick<bf16>);
+  if (shifts(a, f32)) return f32 ? go(k_beam_pick<float, true>) : go(k_beam_pick<bf16, true>);
+  return f32 ? go(k_beam_pick<float, false>) : go(k_beam_pick<bf16, false>);
 }
 cudaError_t launch_beam_move(const BeamTable& t, const BeamMove& m, int ctas, cudaStream_t st) {
   return launch_pdl(k_beam_move, dim3((unsigned)ctas + 1), dim3(256), 0, st, t, m);

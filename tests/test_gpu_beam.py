@@ -179,6 +179,44 @@ def test_beam_ties_go_to_the_lowest_beam_and_token():
             assert (flat[b, :len(first)] == first).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,pad,offset", [(101, 0, 0), (255, 0, 0), (333, 1, 3), (1001, 0, 1), (2048, 1, 0), (5003, 0, 0), (5000, 3, 5), (40001, 0, 2)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_beam_identical_beams_tie_wherever_their_rows_begin(dtype, V, pad, offset, masked):
+    """Copies of one row with equal scores: the candidates of a token are exactly alike in all beams, and go by beam."""
+    K, n = 24, 96
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for seed, std in ((1, 2.0), (2, 6.0), (3, 0.05)):
+        row = (torch.randn(1, V, generator=gen(seed)) * std).to(dt)
+        x = row.repeat(K, 1)
+        buf = torch.full((offset + K * (V + pad) + 64,), float("nan"), dtype=dt, device="cuda")
+        v = buf[offset:offset + K * (V + pad)].view(K, V + pad)[:, :V]
+        v.copy_(x)
+        ok = (torch.rand(1, V, generator=gen(seed + 9)).numpy() < 0.5).repeat(K, 0) if masked else None
+        scores = torch.full((1, K), -1.25)
+        for over in (False, True) if masked else (False,):
+            beam = gbla.beam_shape(1, K, V, n, dtype=dtype, over_allowed=over)
+            got = gbla.beam_select(beam, v, scores.cuda(), allowed=None if ok is None else pack(ok).cuda())
+            p, _ = reference(x[:1], scores[:, :1], V, n, None if ok is None else ok[:1], over=over)
+            p = np.tile(p, (1, K))  # exactly alike
+            check(got, p, np.argsort(-p, axis=1, kind="stable")[:, :n], V, n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_beam_identical_beams_tie_beside_a_beam_far_from_zero(dtype):
+    """Equal rows of which some share a warp with rows whose logits are far from 0."""
+    V, K = 777, 48
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for seed in range(8):
+        row = (torch.randn(1, V, generator=gen(seed)) * 2).to(dt)
+        x = torch.cat([row.repeat(40, 1), (torch.randn(8, V, generator=gen(seed + 50)) * 2 - 2e4).to(dt)])
+        scores = torch.cat([torch.full((1, 40), -0.75), torch.full((1, 8), -9.0)], 1)
+        got = gbla.beam_select(gbla.beam_shape(1, K, V, K, dtype=dtype), x.cuda(), scores.cuda())
+        p, _ = reference(x, scores, V, K)
+        p = np.concatenate([np.tile(p[:, :V], (1, 40)), p[:, 40 * V:]], 1)  # exactly alike
+        check(got, p, np.argsort(-p, axis=1, kind="stable")[:, :K], V, K)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_beam_ties_of_few_of_many(dtype):
     """Equal logits all over: more tokens of the best runs than the selection holds at once."""
