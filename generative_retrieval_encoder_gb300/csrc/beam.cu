@@ -437,7 +437,9 @@ struct Seen {
   }
 };
 
-// ln((s + t) 2^q0), s > 0 and normal, t its rest, |q0| < 2^12, in two words (to 2^-35): table-driven (P. T. P. Tang), r = m c - 1 below 0.01.
+// ln((s + t) 2^q0), s > 0 and normal, t its rest, in two words: table-driven (P. T. P. Tang), r = m c - 1 below 0.01.  q0 and the exponent
+// of s together below 2^13 (logits up to 4096 give 5941 at most): n times kLn2A and kLn2B is exact; to 2^-33, as the lower word is rounded
+// at 2^-36 three times there (below 2^10 to 2^-36).
 __device__ __forceinline__ float2 log2w(float s, float t, float q0) {
   const uint32_t b = __float_as_uint(s);
   const int q = (int)(b >> 23) - 127, j = b >> 17 & 63;

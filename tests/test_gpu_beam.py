@@ -333,6 +333,24 @@ def test_beam_every_bf16_top():
     check(got, p, order, V, 3, strict=False)
 
 
+@pytest.mark.parametrize("far", [4090.0, -4090.0])
+def test_beam_order_of_close_candidates_near_the_ends_of_the_fast_range(far):
+    """Logits near +-4096, where the logarithm's power of two takes 13 bits; rows whose sums differ by some 2^-20."""
+    V, K = 3000, 32
+    x = (torch.randn(1, V, generator=gen(5)).clamp(-4, 4) + far).repeat(K, 1)
+    for k in range(K):
+        x[k, V - 1] = far - 4 + 0.25 * ((k * 11) % K) / K
+        x[k] = x[k] + (k % 3) * 0.5  # the same row, moved: its candidates' scores stay
+    x = torch.round(x * 1024) / 1024   # (moving a row is exact)
+    scores = torch.zeros(1, K)
+    got = gbla.beam_select(gbla.beam_shape(1, K, V, K, dtype="f32"), x.cuda(), scores.cuda())
+    p, order = reference(x, scores, V, K)
+    w = np.take_along_axis(p[0], order[0], 0)
+    assert 0 < (-np.diff(w))[np.diff(w) != 0].min() < 2.0 ** -19
+    check(got, p, order, V, K, strict=False)
+    assert np.abs(got[0].cpu().double().numpy()[0] - w).max() <= NEAR + E * np.abs(w).max()
+
+
 def test_beam_a_large_call_by_spot_checks():
     B, K, V = 64, 16, 32768
     v, x, scores = make(B, K, V, "bf16", seed=3)
