@@ -376,6 +376,23 @@ def test_beam_offsets_beyond_32_bits():
             set(list(zip(par[b].tolist(), tok[b].tolist()))[:len(pairs)]) == set(pairs)
 
 
+def test_beam_logits_and_places_beyond_32_bits():
+    """Logits of more than 2^32 values, and a group of more than 2^31 candidates whose best are in its last rows."""
+    for B, K, V in ((2, 130, (1 << 24) + 1), (1, 150, 1 << 24)):
+        assert K * V > 1 << 31 and (B == 1 or B * K * V > 1 << 32)
+        x = torch.full((B * K, V), -8.0, dtype=torch.bfloat16, device="cuda")
+        scores = torch.zeros(B, K)
+        want = [[(K - 1, V - 1), (K - 2, 0), (0, 12345678), (K - 1, 3)], [(K - 1, V - 2), (K // 2, 5), (K - 3, V - 1), (1, 1)]][:B]
+        for b, pairs in enumerate(want):
+            for i, (k, t) in enumerate(pairs):
+                x[b * K + k, t] = 30 - i / 4 if (k, t) != (K - 1, 3) else 24
+                scores[b, k] -= i if k != K - 1 else 0
+        sc, tok, par, _ = gbla.beam_select(gbla.beam_shape(B, K, V, 4), x, scores.cuda())
+        for b, pairs in enumerate(want):
+            assert list(zip(par[b].tolist(), tok[b].tolist())) == pairs, (K, b)
+        del x
+
+
 # ------------------------------------------------------------------ reorder
 @pytest.mark.parametrize("dtype,width,offset", [(torch.float32, 512, 0), (torch.float32, 5, 0), (torch.float32, 64, 1), (torch.bfloat16, 33, 0), (torch.uint8, 1, 0),
                                                 (torch.bfloat16, 8, 4), (torch.uint8, 100, 3), (torch.float32, 5000, 0), (torch.float64, 3, 0)])
