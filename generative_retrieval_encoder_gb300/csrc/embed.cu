@@ -558,6 +558,8 @@ __device__ __forceinline__ void add2(float& hi, float& lo, float v) {
   lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -b)), __fadd_rn(v, -b)));
   hi = s;
 }
+// The value of two words: of an infinite (or no) number the upper one, as lo is NaN then.
+__device__ __forceinline__ float sum2(float hi, float lo) { return fabsf(hi) <= 3.402823466e38f ? hi + lo : hi; }
 
 // The ids of long runs, 32 columns of one (128 where rows are whole pieces of 16 bytes) a task: their partial rows are added in two
 // words, by a warp in order, or, of more than kWarpRows, by the CTA's warps each every eighth row.  Bound by
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, cons
         sum.add(s.part + c, a.d, first, 2, run.y, last);
         float* out = a.dtable + (int64_t)run.x * a.d + c;
 #pragma unroll
-        for (int j = 0; j < C; ++j) out[j] = (sum.hi[j] + sum.lo[j]) * a.scale;
+        for (int j = 0; j < C; ++j) out[j] = sum2(sum.hi[j], sum.lo[j]) * a.scale;
       }
     }
     if (!__syncthreads_or(n_rows > kWarpRows)) continue;
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const EmbedArgs a, cons
           add2(h, l, red[w][i].x);
           l += red[w][i].y;
         }
-        a.dtable[(int64_t)run.x * a.d + it.y + i] = (h + l) * a.scale;
+        a.dtable[(int64_t)run.x * a.d + it.y + i] = sum2(h, l) * a.scale;
       }
       __syncthreads();
     }

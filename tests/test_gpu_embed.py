@@ -218,6 +218,28 @@ def test_embed_nonfinite_rows_stay_theirs():
     assert g[7].isnan().all() and g[[v for v in range(V) if v != 7]].isfinite().all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("count", [33, 100, 3000])
+def test_embed_infinite_gradients_of_frequent_ids(dtype, count):
+    """An infinity among an id's gradients makes its sum infinite, two of different sign NaN; an fp32 sum past the range is infinite."""
+    V, d, inf = 5, 16, float("inf")
+    ids = torch.arange(V).repeat_interleave(count).to(torch.int32)
+    dy = torch.randn(V * count, d, generator=gen(1)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    dy[count // 2, 3] = inf                # id 0
+    dy[2 * count - 1, 4] = -inf            # id 1
+    dy[2 * count, 5], dy[3 * count - 1, 5] = inf, -inf
+    dy[3 * count:4 * count, 6] = 3e38      # id 3: every partial sum of two and more is past the range
+    dy[3 * count:4 * count, 7] = 1e37      # one of 32 is in it, the whole is not, or only the whole of many
+    shape = gbla.glr_shape(1, V * count, d, dtype=dtype)
+    g = gbla.embed_backward(shape, ids.cuda(), dy.cuda(), V).cpu()
+    want = dy.double().view(V, count, d).sum(1)
+    want = torch.where(want.abs() > torch.finfo(torch.float32).max, torch.sign(want) * inf, want)
+    size = dy.double().abs().view(V, count, d).sum(1)
+    assert want[0, 3] == inf and want[1, 4] == -inf and want[2, 5].isnan() and want[3, 6] == inf
+    same = (g.double() == want) | (g.isnan() & want.isnan()) | ((g.double() - want).abs() <= 34 * E * size)
+    assert same.all(), (~same).nonzero()
+
+
 def test_embed_gradient_by_differences():
     V, d, n = 7, 5, 300
     shape = gbla.glr_shape(1, n, d, dtype="f32")
