@@ -6,6 +6,7 @@
 // counting sort by the id's digits (no CTA waits for another: a tile's place among its digit's keys comes from the counts of
 // the tiles before it), then the sums, kEmbedCap sorted places a group of threads.
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -56,7 +57,7 @@ __device__ __forceinline__ uint4 scaled(uint4 w, float s) {
 // thread.  Bound by memory: 131072 rows of 512 bf16 from a table of 32768 in 27 us, 0.9 of a copy's rate with the table read once (L2
 // holds it).  PAIRS, VALUES: y in pieces of 16 bytes of whatever rows, read from the table by two bf16 or by single values (`per` is a
 // multiple of a piece's values): 65536 rows of 510 in 19 us, of 511 in 29, of 512 by ROWS in 14; value by value 62.  SINGLE: of a y that
-// is not aligned, value by value, `cols` of them a row.
+// is not aligned, value by value, `cols` of them a row; of a scale that is not finite, too, as the others multiply the zeros of no token.
 enum EmbedRows { SINGLE, ROWS, PAIRS, VALUES };
 template <typename T, EmbedRows M>
 __global__ void __launch_bounds__(kThreads) k_embed_fwd(const EmbedArgs a, int per, int cols, uint32_t by_cols, bool check) {
@@ -125,14 +126,14 @@ __global__ void __launch_bounds__(kThreads) k_embed_fwd(const EmbedArgs a, int p
         const int k = id[s];
         if (k < 0) continue;
         if (M == ROWS) v[u] = __ldg(reinterpret_cast<const uint4*>(tab + (int64_t)k * a.d) + c);
-        else f[u] = to_f(tab[(int64_t)k * a.d + c]);
+        else f[u] = to_f(tab[(int64_t)k * a.d + c]) * a.scale;
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t i = i0 + u * kThreads;
         if (i >= total) continue;
         if (M == ROWS) reinterpret_cast<uint4*>(y)[i] = scaled<T>(v[u], a.scale);
-        else y[i] = from_f<T>(f[u] * a.scale);
+        else y[i] = from_f<T>(f[u]);
       }
     }
   }
@@ -682,7 +683,8 @@ bool embed_fwd_clears(const EmbedArgs& a) { return a.n <= kCheckIds; }
 cudaError_t launch_embed_fwd(const EmbedArgs& a, bool f32, cudaStream_t st) {
   const int es = f32 ? 4 : 2, E = 16 / es;
   const uintptr_t tab = reinterpret_cast<uintptr_t>(a.table), y = reinterpret_cast<uintptr_t>(a.y);
-  const EmbedRows m = ((uintptr_t)a.d * es | tab | y) % 16 == 0 ? ROWS : y % 16 ? SINGLE : !f32 && a.d % 2 == 0 && tab % 4 == 0 ? PAIRS : VALUES;
+  const bool finite = std::fabs(a.scale) <= 3.402823466e38f;
+  const EmbedRows m = !finite ? SINGLE : ((uintptr_t)a.d * es | tab | y) % 16 == 0 ? ROWS : y % 16 ? SINGLE : !f32 && a.d % 2 == 0 && tab % 4 == 0 ? PAIRS : VALUES;
   const int cols = m == ROWS ? a.d / E : a.d;
   // about four accesses a thread; of pieces also 16 slots' at least
   const int per = m == ROWS || m == SINGLE ? std::max(1, 1024 / cols) : std::min(1024, std::max(1, 1024 / a.d) * E);

@@ -240,6 +240,23 @@ def test_embed_infinite_gradients_of_frequent_ids(dtype, count):
     assert same.all(), (~same).nonzero()
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 10), ("bf16", 7), ("f32", 64), ("f32", 7)])
+@pytest.mark.parametrize("scale", [float("inf"), -float("inf"), float("nan")])
+def test_embed_rows_of_no_token_are_zeros_whatever_the_scale(dtype, d, scale):
+    V, n = 9, 300
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    ids = torch.randint(-1, V, (n,), generator=gen(1), dtype=torch.int32).cuda()
+    table, dy = torch.randn(V, d, generator=gen(2)).to(dt).cuda(), torch.randn(n, d, generator=gen(3)).to(dt).cuda()
+    lens = torch.tensor([90, 0, 100], dtype=torch.int32, device="cuda")
+    shape = gbla.glr_shape(3, 100, d, dtype=dtype, seq_lens=lens)
+    has = (ids >= 0) & torch.as_tensor(valid_rows(3, 100, lens.tolist())).cuda()
+    y = gbla.embed_forward(shape, ids, table, scale=scale)
+    assert torch.equal(y[~has], torch.zeros_like(y[~has]))
+    assert torch.equal(y[has].nan_to_num(nan=7.0), (table[ids[has].long()].float() * scale).to(dt).nan_to_num(nan=7.0))
+    g = gbla.embed_backward(shape, torch.where(ids == 5, -1, ids), dy, V, scale=scale)
+    assert (g[5] == 0).all() and not g[4].isfinite().any()
+
+
 def test_embed_gradient_by_differences():
     V, d, n = 7, 5, 300
     shape = gbla.glr_shape(1, n, d, dtype="f32")
