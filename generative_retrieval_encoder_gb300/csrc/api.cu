@@ -672,7 +672,7 @@ EmbedLayout embed_layout(const RowPlan& p, int64_t vocab, int k, bool backward) 
     while ((vocab >> bits) > 0) ++bits;  // of the keys 0 .. vocab
     l.passes = cdiv(bits, kEmbedDigit);
     l.bits = cdiv(bits, l.passes);
-    l.sums = c.take(tiles > 1 ? l.passes * ((tiles + kEmbedTiles - 1) / kEmbedTiles) * (4u << kEmbedDigit) : 0);
+    l.sums = c.take(tiles > 1 ? l.passes * ((tiles + kEmbedTiles - 1) / kEmbedTiles + 1) * (4u << kEmbedDigit) : 0);
     l.zero_bytes = c.off;
     l.last = c.take((size_t)vocab * 4);
     for (int i = 0; i < 2; ++i) {
@@ -1383,8 +1383,9 @@ gbla_status embed_backward(const gbla_shape* shape, const void* ids, int wide_id
   for (int i = 0; i < (s.tiles == 1 ? 1 : l.passes); ++i) {
     s.key_in = s.keys[(i + 1) & 1]; s.slot_in = s.slots[(i + 1) & 1];
     s.key_out = s.keys[i & 1]; s.slot_out = s.slots[i & 1];
-    s.sums = at<int>(ws, l.sums) + ((size_t)i * groups << kEmbedDigit);
+    s.sums = at<int>(ws, l.sums) + ((size_t)i * (groups + 1) << kEmbedDigit);
     if (s.tiles > 1) GBLA_CHECK(launch_embed_count(a, s, embed_fill(a, 2 * i, launches), l.bits, i * l.bits, c.st), "embed count");
+    if (groups > kEmbedGroups) GBLA_CHECK(launch_embed_scan(s, c.st), "embed scan");
     const EmbedFill f = s.tiles > 1 ? embed_fill(a, 2 * i + 1, launches) : embed_fill(a, 0, 1);
     GBLA_CHECK(launch_embed_place(a, s, f, l.bits, i * l.bits, c.st), "embed place");
   }

@@ -199,6 +199,42 @@ __global__ void __launch_bounds__(kThreads) k_embed_count(const EmbedArgs a, con
   }
 }
 
+// Of more than kEmbedGroups groups of tiles: their sums become the sums of the groups before each, the digits' totals behind them, so that
+// a tile reads two rows of them, not all, which would take the square of the slots.  (8 columns, 32768 rows; with this launch and
+// without: 524288 slots 68 us and 67, 786432 83 and 87, 4194304 302 and 492, 16777216 1102 and 4284.)  A thread a digit and 32nd of the
+// groups.
+__global__ void __launch_bounds__(1024) k_embed_scan(int* sums, int groups) {
+  pdl_enter();
+  __shared__ int red[32][32];
+  constexpr int U = 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* col = sums + blockIdx.x * 32 + lane;
+  const int per = (groups + 31) / 32, lo = min(groups, warp * per), hi = min(groups, lo + per);
+  int sum = 0;
+#pragma unroll 8
+  for (int g = lo; g < hi; ++g) sum += col[(int64_t)g * kMaxBins];
+  red[warp][lane] = sum;
+  __syncthreads();
+  int at = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) {
+    const int c = red[w][lane];
+    at += w < warp ? c : 0;
+    all += c;
+  }
+  if (warp == 0) col[(int64_t)groups * kMaxBins] = all;
+  for (int g = lo; g < hi; g += U) {
+    int c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) c[u] = g + u < hi ? col[(int64_t)(g + u) * kMaxBins] : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (g + u < hi) col[(int64_t)(g + u) * kMaxBins] = at;
+      at += c[u];
+    }
+  }
+}
+
 // The sum of the values of the CTA's threads before this one.
 __device__ __forceinline__ int sum_before(int v, int* red) {
   int inc = v;
@@ -242,11 +278,16 @@ __global__ void __launch_bounds__(kThreads) k_embed_place(const EmbedArgs a, Emb
     int all = 0, before = 0;
     if (!ALL && threadIdx.x < bins) {
       const int g0 = tile / kEmbedTiles, groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
+      if (groups > kEmbedGroups) {
+        all = s.sums[(int64_t)groups * kMaxBins + threadIdx.x];
+        before = s.sums[(int64_t)g0 * kMaxBins + threadIdx.x];
+      } else {
 #pragma unroll 8
-      for (int g = 0; g < groups; ++g) {
-        const int c = s.sums[(int64_t)g * kMaxBins + threadIdx.x];
-        all += c;
-        before += g < g0 ? c : 0;
+        for (int g = 0; g < groups; ++g) {
+          const int c = s.sums[(int64_t)g * kMaxBins + threadIdx.x];
+          all += c;
+          before += g < g0 ? c : 0;
+        }
       }
 #pragma unroll 16
       for (int t = g0 * kEmbedTiles; t < tile; ++t) before += s.count[(int64_t)t * kMaxBins + threadIdx.x];
@@ -707,6 +748,10 @@ unsigned fill_ctas(const EmbedFill& f) { return (unsigned)((f.hi - f.lo + kFill 
 
 cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st) {
   return launch_pdl(k_embed_count, dim3((unsigned)s.tiles + fill_ctas(f)), dim3(kThreads), 0, st, a, s, f, 1 << bits, shift, shift == 0);
+}
+cudaError_t launch_embed_scan(const EmbedSort& s, cudaStream_t st) {
+  const int groups = (s.tiles + kEmbedTiles - 1) / kEmbedTiles;
+  return launch_pdl(k_embed_scan, dim3(kMaxBins / 32), dim3(1024), 0, st, s.sums, groups);
 }
 cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st) {
   const dim3 grid((unsigned)s.tiles + fill_ctas(f));

@@ -337,6 +337,7 @@ cudaError_t launch_ln_cols(const LnArgs& a, bool f32, float* dw, float* db, cuda
 constexpr int kEmbedTile = 512;    // keys of a CTA of the sort
 constexpr int kEmbedOne = 2048;    // keys that one CTA sorts alone
 constexpr int kEmbedTiles = 32;    // tiles whose counts are also kept summed
+constexpr int kEmbedGroups = 40;   // groups of kEmbedTiles tiles whose counts a tile reads itself
 constexpr int kEmbedDigit = 8;     // bits of a digit, at most
 constexpr int kEmbedCap = 32;      // sorted places that a group of threads sums
 struct EmbedArgs {
@@ -353,7 +354,7 @@ struct EmbedSort {
   int tiles, key_bits;               // tiles = 1: one CTA goes through every pass
   const int* key_in; int* key_out; const int* slot_in; int* slot_out;  // of the pass; at last key_out, slot_out are the sorted ones
   int* keys[2]; int* slots[2];        // [n] each
-  int* count; int* sums;              // [tiles][2^kEmbedDigit]; the pass's [tiles / kEmbedTiles][2^kEmbedDigit], 0 on entry
+  int* count; int* sums;              // [tiles][2^kEmbedDigit]; the pass's [tiles / kEmbedTiles + 1][2^kEmbedDigit], 0 on entry
   float* part;                        // [2 * chunks][d]
   int* n_long; int2* longs;           // how many ids have more than kEmbedCap slots, 0 on entry; each and its first partial row
   int* last;                          // [V]: of such an id its last partial row
@@ -365,6 +366,7 @@ struct EmbedFill { float* p; int64_t lo, hi; bool wide; };
 EmbedFill embed_fill(const EmbedArgs& a, int i, int n);  // share i of n
 // One pass of the sort, by the digit of `bits` bits at `shift`; a single tile's launch_embed_place is the whole sort, and clears.
 cudaError_t launch_embed_count(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st);
+cudaError_t launch_embed_scan(const EmbedSort& s, cudaStream_t st);  // between the two, of more than kEmbedGroups groups
 cudaError_t launch_embed_place(const EmbedArgs& a, const EmbedSort& s, const EmbedFill& f, int bits, int shift, cudaStream_t st);
 cudaError_t launch_embed_rows(const EmbedArgs& a, const EmbedSort& s, bool f32, cudaStream_t st);
 cudaError_t launch_embed_join(const EmbedArgs& a, const EmbedSort& s, cudaStream_t st);
