@@ -263,6 +263,36 @@ def test_layer_norm_padded_rows_may_hold_anything_and_nan_stays_in_its_row():
     assert c[0][3].isnan().all() and c[3][3].isnan().all() and torch.equal(a[5], c[5])
 
 
+@pytest.mark.parametrize("dtype,T,d", [("bf16", 200000, 16), ("bf16", 90000, 33), ("bf16", 100001, 64), ("bf16", 60000, 512), ("bf16", 30000, 1000), ("bf16", 9000, 2048),
+                                       ("bf16", 5000, 4095), ("bf16", 3001, 8192), ("bf16", 6000, 8190), ("bf16", 9001, 9000), ("f32", 100001, 24), ("f32", 60000, 200),
+                                       ("f32", 30000, 511), ("f32", 9000, 2048), ("f32", 3000, 8192), ("f32", 4001, 8193)])
+def test_layer_norm_column_sums_of_many_rows(dtype, T, d):
+    """dw and db by the additions that a value goes through: a group's rows (of two CTAs an SM, 256 threads each), its CTA's groups,
+    every 32nd CTA, a tree of 32; of rows that no group holds a 64th of the rows, two more partials, the tree."""
+    f32 = dtype == "f32"
+    wide = d if f32 else d + (0 if d % 8 == 0 else 4 if d % 4 == 0 else 6 if d % 2 == 0 else 7)
+    if wide > 8192:
+        chain = -(-T // 64) + 2 + 5
+    else:
+        threads = next(g for g in (4, 8, 16, 32, 64, 128, 256) if wide <= (32 if g == 256 else 8 if (f32 or wide <= 32) and g <= 32 else 16) * g)
+        groups, sms = 256 // threads, torch.cuda.get_device_properties(0).multi_processor_count
+        chain = -(-T // (2 * sms * groups)) + groups + -(-(2 * sms + 8) // 32) + 5
+    dt = torch.float32 if f32 else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x, dy = ((torch.randn(T, d, generator=g, device="cuda") + 0.2).to(dt) for _ in range(2))
+    shape = gbla.glr_shape(1, T, d, dtype=dtype)
+    _, _, st = gbla.layer_norm_forward(shape, x, stats=True)
+    got = gbla.layer_norm_backward(shape, x, None, st, dy)
+    m, r = st[:, :1].double(), st[:, 1:].double()
+    c = x.double() - m
+    z, q = c * r, dy.double()
+    bz = 4 * E * z.abs() + 2 * E * c.abs() * r
+    for name, want, bound in (("dw", (q * z).sum(0), (chain + 2) * E * (q * z).abs().sum(0) + (q.abs() * bz).sum(0)),
+                              ("db", q.sum(0), (chain + 2) * E * q.abs().sum(0))):
+        err = (got[name].double() - want).abs()
+        assert (err <= bound).all(), (name, (err / bound).max())
+
+
 def test_layer_norm_bad_lengths_are_reported():
     for d in (64, 8300):
         for lens, bad in (([5, 9], 1), ([-1, 8], 0)):
