@@ -366,7 +366,7 @@ __device__ __forceinline__ float value(const Piece<T, E>& w, int j) {
 
 // The rows of the ids without a slot, kThreads of them a CTA: which of them occur is read from the sorted keys between the first
 // and the last of them, up to kScan places; among more each is looked for (500000 places of 1000
-// ids, a few of them most: the whole gradient 81 us, 197 by reading all).
+// ids, a few of them most: the whole gradient 74 us, 203 by reading all).
 constexpr int kScan = 16384;
 __device__ void clear_rows(const EmbedArgs& a, const int* key, int64_t v0) {
   __shared__ int64_t bound[2];

@@ -765,7 +765,8 @@ def beam_workspace(beam: Beam, device="cuda") -> torch.Tensor:
 def beam_select(beam: Beam, logits, scores, allowed=None, done=None, out: tuple | None = None, ws=None):
     """The n_out best of each group's K x V candidates (see gbla.h): returns (scores, tokens, parents, done), each [B, n_out],
     done (bool) where beam has an eos.  logits [B K, V] of any row stride; scores fp32 [B, K]; allowed int32 [B K,
-    ceil(V / 32)], the bits of the tokens that may follow; done bool [B, K].  out: such a tuple to fill."""
+    ceil(V / 32)], the bits of the tokens that may follow; done bool [B, K].  out: such a tuple to fill, of other tensors than
+    the inputs."""
     B, K, V, n = beam.B, beam.K, beam.V, beam.n_out
     dev, dt = _cuda("logits", logits), torch.float32 if beam.io_dtype == GBLA_F32 else torch.bfloat16
     ld = logits.stride(0) if B * K > 1 and logits.dim() == 2 else V

@@ -484,7 +484,7 @@ typedef struct {
  * tensors: dst[b n_out + i] = src[b K + parents[b, i]].  A parent outside
  * 0 .. K - 1 sets the error word (GBLA_ERR_DEVICE_CHECK) and leaves its row of dst as
  * it was.  states: host array, read during the call; tensors do not overlap (but
- * dst = src).  beam: B, K and n_out are read.
+ * dst = src).  beam: checked as a whole, as beam_select does; B, K and n_out are what counts.
  */
 gbla_status beam_reorder(const gbla_beam* beam, const gbla_beam_state* states,
                          int n_states, const int32_t* parents, void* ws,

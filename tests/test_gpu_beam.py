@@ -5,8 +5,8 @@ streams and graphs, states of every width moved in place and into others, a
 decoding loop of embedding, norm, recurrence, selection and reordering, and a
 training step of the same parts.
 
-Order: the sum of a row's exponentials is off by 2^-27 at most (each by 2^-30; two
-words, 16 additions of at most 0.011 of them in the lower), and so is its
+Order: the sum of a row's exponentials is off by 2^-27 at most (each by 2^-28.8; two
+words, the lower of at most 0.011 of them through 7 additions on the mean), and so is its
 logarithm.  So candidates of two beams may change places only where their scores
 differ by less than 2 * 2^-27 (and 2^-46 of their size: two fp32 words); within a beam
 never.  A score is rounded once: 2^-24 of its value beside that."""

@@ -4,9 +4,10 @@ tokens, sizes around the sort's tiles and digits, offsets beyond 32 bits, bad
 ids, streams and graphs.
 
 Bounds: y is one fp32 product and one rounding, so it equals the same operations
-in torch bit for bit.  A gradient sums at most 64 rows in fp32 in a row (63
+in torch bit for bit.  A gradient sums at most 32 rows in fp32 in a row (31
 additions, each off by 2^-24 of at most the sum of magnitudes S), such sums in
-64 bits, and is multiplied and rounded once: 66 * 2^-24 scale S."""
+two fp32 words, and is multiplied and rounded: 34 * 2^-24 scale S.  Tests that say
+66 were written for chains of 64 rows and allow more than that."""
 import numpy as np
 import pytest
 import torch
