@@ -11,7 +11,8 @@
 // candidates some lie closer than fp32's rounding.  So each exponential is formed to 2^-28.8 (2^-31.4 on the mean; 2^(j/32) from
 // a table in two words, P. T. P. Tang's reduction, and a polynomial of degree 3), added into two words (the sum is off by 2^-27
 // at most, by 2^-31 on the mean), and scores are compared in two fp32 words.  Equal logits of one row stay equal, and so do equal
-// rows: which values are added to which goes by their tokens, wherever a row begins in memory.
+// rows: which values are added to which goes by their tokens, wherever a row begins in memory.  A token with all of its row's sum has
+// the logarithm 0.
 #include <algorithm>
 
 #include "common.cuh"
@@ -121,6 +122,8 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int off
 }
 
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+// The power of two that exponentials of logits up to `top` are summed relative to: e^top is at most it, and above a quarter of it.
+__device__ __forceinline__ int octave(float top) { return (int)floorf(top * 1.44269504f) + 1; }
 __device__ __forceinline__ double sum_of(const BeamPart& p) {
   return p.far ? __hiloint2double(p.hi, __float_as_int(p.lo)) : (double)p.hi * (1. / 65536.) + (double)p.lo;
 }
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
     const float floor_ = top - 80.f;  // what is below counts as e^-80 (bf16: e^-64 to e^-80) of the largest: nothing
     // rounded up: further down (96 below -4064 to nearest) the exponent of 2^(n / 32 - e) leaves its field
     const uint32_t floor1 = (__float_as_uint(floor_) + (floor_ > 0.f ? 0xffffu : 0u)) >> 16, floor2 = floor1 | floor1 << 16;
-    const int e = (int)floorf(top * 1.44269504f) + 1;
+    const int e = octave(top);
     const uint32_t bias = (uint32_t)(127 - e) << 23;
     // two values at a time.  sum: on the grid of 2^-16 that its start fixes; lo: what the grid cuts off, and the rest
     float2 sum = two(192.f), lo = two(0.f);
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(256, 4) k_beam_rows(const BeamArgs a) {
     part.hi = __reduce_add_sync(FULL, (int)((sum.x - 192.f) * 65536.f) + (int)((sum.y - 192.f) * 65536.f) + more);
     for (int o = 16; o; o >>= 1) r += __shfl_xor_sync(FULL, r, o);
     part.lo = r;
-    part.ref = (float)e;
+    part.top = top;
     part.far = 0;
   } else if (top > -kInf) {  // far from 0 (or infinite): in 64 bits
     double s = 0.;
@@ -437,6 +440,18 @@ struct Seen {
   }
 };
 
+// The term of a row's largest logit as the pass over the logits formed it, relative to 2^e, in two words.
+__device__ __forceinline__ float2 own_term(float v, int e) {
+  const float k = __fmaf_rn(v, kL, 12582912.f), n = __fadd_rn(12582912.f, -k), f = __fmaf_rn(v, kLlo, __fmaf_rn(v, kL, n));
+  const float p = __fmul_rn(f, __fmaf_rn(f, __fmaf_rn(f, kC3, kC2), kC1));
+  const uint32_t b = __float_as_uint(k);
+  const float scale = __uint_as_float((b << 18) + ((uint32_t)(127 - e) << 23)), h = kExpHi[b & 31], l = kExpLo[b & 31];
+  const float h2 = __fmul_rn(h, scale), grid = __fadd_rn(__fadd_rn(192.f, h2), -192.f);
+  const float rest = __fmaf_rn(__fmaf_rn(h, p, __fmaf_rn(l, p, l)), scale, __fadd_rn(h2, -grid));
+  float hi;
+  const float lo = two_sum(grid, rest, hi);
+  return make_float2(hi, lo);
+}
 // ln((s + t) 2^q0), s > 0 and normal, t its rest, in two words: table-driven (P. T. P. Tang), r = m c - 1 below 0.01.  q0 and the exponent
 // of s together below 2^13 (logits up to 4096 give 5941 at most): n times kLn2A and kLn2B is exact; to 2^-33, as the lower word is rounded
 // at 2^-36 three times there (below 2^10 to 2^-36).
@@ -588,11 +603,11 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
     const bool is = b < a.K, ended = is && a.done && a.done[row0 + b], mine = is && !ended;
     const float c = is ? a.scores[row0 + b] : 0.f;
     const BeamPart* p = a.part + (row0 + b) * a.tasks;
-    float best = -kInf, most = -kInf;  // of the parts near 0: as powers of two, exactly; of those far from it
+    float best = -kInf, most = -kInf;  // the largest logit of the parts near 0; of those far from it
     for (int i = t; mine && i < a.tasks; i += team) {
       const BeamPart q = p[i];
-      if (q.far) most = fmaxf(most, q.ref);
-      else best = fmaxf(best, q.ref);
+      if (q.far) most = fmaxf(most, q.top);
+      else best = fmaxf(best, q.top);
     }
     for (int o = team / 2; o; o >>= 1) {
       best = fmaxf(best, __shfl_xor_sync(FULL, best, o));
@@ -600,12 +615,21 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
     }
     float2 at0 = make_float2(-kInf, 0.f);  // no value above -infinity, or a NaN among them: no candidates
     float ref = 0.f;
-    const bool far = most > -kInf;  // (known to the row's threads) the row has logits far from 0: in 64 bits, below
+    // (known to the row's threads) the row has logits far from 0, and not so far below the others that they count for nothing: in 64 bits,
+    // below
+    const bool far = most > -kInf && !(most < best - 200.f);
     {
+      const int e = best > -kInf ? octave(best) : 0;
+      const float2 own = own_term(best > -kInf ? best : 0.f, e);
       float hi = 0.f, lo = 0.f;
       for (int i = t; mine && !far && i < a.tasks; i += team) {
         const BeamPart q = p[i];
-        const float d = best - q.ref, f = d < 120.f ? __uint_as_float((uint32_t)(127 - (int)d) << 23) : 0.f;  // (a part without values is 0, or NaN)
+        if (q.far) {  // 0, or NaN
+          if (sum_of(q) != sum_of(q)) hi = __int_as_float(0x7fffffff);
+          continue;
+        }
+        const int d = q.top > -kInf ? e - octave(q.top) : 120;
+        const float f = d < 120 ? __uint_as_float((uint32_t)(127 - d) << 23) : 0.f;  // (a part without values is 0, or NaN)
         lo += two_sum(hi, (float)(q.hi >> 12) * 0x1p-4f * f, hi);
         lo += two_sum(hi, (float)(q.hi & 4095) * 0x1p-16f * f, hi);
         lo += two_sum(hi, q.lo * f, hi);
@@ -616,17 +640,28 @@ __global__ void __launch_bounds__(kPick) k_beam_pick(const BeamArgs a) {
       }
       lo = two_sum(hi, lo, hi);
       if (hi > 0.f) {
-        const float2 l = log2w(hi, lo, best);
-        const float e = two_sum(c, -l.x, at0.x);
-        at0.y = fabsf(at0.x) < kInf ? two_sum(at0.x, e - l.y, at0.x) : 0.f;
+        // where the largest logit has more than half the mass: relative to it, by its own term, so that the term's error counts for the
+        // other half alone, and a logit that has all of it has the logarithm 0 exactly (a beam whose next token is given keeps its score)
+        const bool half = own.x > 0.5f * hi;
+        float2 l = log2w(hi, lo, half ? 0.f : (float)e);
+        float from = c, rest = 0.f;
+        if (half) {
+          const float2 m = log2w(own.x, own.y, 0.f);
+          const bool all = (hi - own.x) + (lo - own.y) < 0x1p-40f * hi;
+          l.y = all ? 0.f : l.y - m.y;
+          l.y += two_sum(all ? 0.f : l.x, all ? 0.f : -m.x, l.x);
+          rest = two_sum(c, -best, from);
+        }
+        const float more = two_sum(from, -l.x, at0.x);
+        at0.y = fabsf(at0.x) < kInf ? two_sum(at0.x, more + (rest - l.y), at0.x) : 0.f;
       }
     }
     if (__any_sync(FULL, far)) {  // relative to the largest part's, a logit itself if it is a far one.  The warp's other rows keep theirs
-      double e = best > -kInf ? (double)best * kLn2 : -kInf, sum = 0.;
+      double e = best > -kInf ? (double)best : -kInf, sum = 0.;
       if (far && (double)most > e) e = (double)most, ref = most;
       for (int i = t; mine && far && i < a.tasks; i += team) {
         const BeamPart q = p[i];
-        sum += sum_of(q) * (q.ref > -kInf ? exp((q.far ? (double)q.ref : (double)q.ref * kLn2) - e) : 1.);
+        sum += sum_of(q) * (q.top > -kInf ? exp((q.far ? (double)q.top : (double)octave(q.top) * kLn2) - e) : 1.);
       }
       for (int o = team / 2; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
       if (sum > 0.) {

@@ -377,8 +377,8 @@ cudaError_t launch_zero(void* p, size_t bytes, cudaStream_t st);
 constexpr int kBeamPieces = 8;       // 16-byte pieces a lane of the rows' kernel takes
 constexpr int kBeamMost = 1024;      // beams, in and out
 constexpr int kBeamItems = 12288;    // candidates that the selection holds at once
-// Sum of exponentials: (hi 2^-16 + lo) 2^ref (ref a whole number); far: the double of the words hi, lo, times exp(ref).
-struct __align__(16) BeamPart { int hi; float lo; float ref; int far; };
+// Sum of exponentials of logits up to `top`: (hi 2^-16 + lo) 2^octave(top); far: the double of the words hi, lo, times exp(top).
+struct __align__(16) BeamPart { int hi; float lo; float top; int far; };
 struct BeamArgs {
   const void* logits; int64_t ld;    // [B K, ld]
   const float* scores;               // [B, K]

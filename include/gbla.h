@@ -457,6 +457,8 @@ typedef struct {
  *            Where there are fewer candidates than n_out the last are (-inf, token
  *            -1, parent 0, not done).
  * Logits of -inf and rows with a NaN or +inf among those summed have no candidates.
+ * A token that has all of its beam's sum (the only one that may follow) has the
+ * logarithm 0: the beam keeps its score exactly.
  * Exponentials are summed, and scores compared, in two fp32 words: which of two
  * candidates is first is decided to 2^-26 (to 2^-30 on the mean), and a score is
  * rounded once.

@@ -217,6 +217,33 @@ def test_beam_identical_beams_tie_beside_a_beam_far_from_zero(dtype):
         check(got, p, np.argsort(-p, axis=1, kind="stable")[:, :K], V, K)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1, 7, 300, 5001])
+@pytest.mark.parametrize("kind", ["allowed", "inf", "lowest"])
+def test_beam_given_tokens_keep_their_scores(dtype, V, kind):
+    """A beam with one token that may follow has log softmax 0, whatever the logit: its score stays, and beams of equal score, ended ones
+    among them, go by number."""
+    B, K = 3, 40
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for seed in range(6):
+        g = gen(seed)
+        x = (torch.randn(B * K, V, generator=g) * 9).to(dt)
+        at = torch.randint(0, V, (B * K,), generator=g)
+        ok = torch.zeros(B * K, V, dtype=torch.bool)
+        ok[torch.arange(B * K), at] = True
+        if kind != "allowed":
+            x = torch.where(ok, x, torch.full_like(x, -math.inf if kind == "inf" else torch.finfo(dt).min))
+        scores = (-torch.randint(0, 4, (B, K), generator=g) * 0.37 - (0.01 if seed % 2 else 0.0)).float()
+        done = torch.rand(B, K, generator=g) < 0.3
+        beam = gbla.beam_shape(B, K, V, dtype=dtype, eos=V // 2, over_allowed=True)
+        sc, tok, par, dn = gbla.beam_select(beam, x.cuda(), scores.cuda(), allowed=pack(ok.numpy()).cuda() if kind == "allowed" else None, done=done.cuda())
+        order = torch.sort(-scores, dim=1, stable=True).indices
+        live = torch.gather(scores, 1, order)
+        want = torch.gather(torch.where(done, V // 2, at.view(B, K)), 1, order)
+        assert torch.equal(par.cpu().long(), order) and torch.equal(tok.cpu().long(), want) and torch.equal(sc.cpu(), live)
+        assert torch.equal(dn.cpu(), torch.gather(done, 1, order) | (want == V // 2))
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_beam_ties_of_few_of_many(dtype):
     """Equal logits all over: more tokens of the best runs than the selection holds at once."""
